@@ -17,6 +17,9 @@
  *   wf_lmhead_draft_topk  the target and draft heads in one weight sweep
  *   wf_round          all of the above as one stream-ordered round
  *   wf_catchup        KV-only catch-up of the EAGLE-3 drafter after a switch
+ *   wf_paged_*        a round's rows over a paged key-value cache: keys and
+ *                     values in, attention, accepted rows compacted
+ *   wf_pages_*        the pages' own life: reserve (copy on write), fork, trim
  *
  * Conventions shared by every call
  * - Pointers named as device buffers must be device (or managed) memory
@@ -463,6 +466,158 @@ WF_API wf_status wf_catchup_kv(const wf_catchup_args* args, void* ws, size_t ws_
 
 /* The whole catch-up: wf_catchup_kv, then the final token's attention sublayer. */
 WF_API wf_status wf_catchup(const wf_catchup_args* args, void* ws, size_t ws_bytes, wf_stream_t stream);
+
+/* ------------------------------------------------------------------ paged cache
+ * A key-value cache whose rows live in pages of page_size positions.  Position
+ * t of sequence b is row t % page_size of page table[b][t / page_size], the
+ * same page in every layer.  The pages describe the drafters' and the target's
+ * caches as dense tensors; paging them is this library's own layout, and no
+ * passage corresponds to it.  One layer of a bf16 pool under an identity table
+ * is the [B, cap, G*D] cache of wf_catchup (cap = max_pages * page_size).
+ *
+ * A page is free when its reference count is 0.  Pages are only written
+ * through sequences that hold them alone: call wf_pages_reserve for a round's
+ * rows before wf_paged_append writes them.
+ */
+#define WF_KV_BF16 0
+#define WF_KV_E4M3 1   /* 8-bit values (4 exponent, 3 mantissa bits, largest 448) times an fp32 scale */
+/* Most sequences of one paged cache. */
+#define WF_PAGED_MAX_SEQS 4096
+
+typedef struct wf_paged_cache {
+    void* K;                   /* [layers, num_pages, page_size, G, D] bf16 bits or e4m3 bytes, 16-byte aligned */
+    void* V;                   /* same */
+    const float* k_scale;      /* [layers, G] fp32 > 0: key = stored value * scale (WF_KV_E4M3; NULL = 1) */
+    const float* v_scale;      /* same, for the values */
+    int32_t* table;            /* [B, max_pages] page of each block of positions, -1 = none */
+    int32_t* ref;              /* [num_pages] sequences that hold each page (wf_pages_*; else may be NULL) */
+    int kv_type;               /* WF_KV_BF16 or WF_KV_E4M3 */
+    int layers, num_pages;     /* num_pages * page_size < 2^31 - 4096 */
+    int page_size;             /* a power of two, 8 .. 1024 */
+    int G, D;                  /* KV heads, head size (D % 16 == 0, 16 <= D <= 128, G * D <= 16384) */
+    int B, max_pages;          /* sequences (1 .. WF_PAGED_MAX_SEQS), blocks a sequence may hold;
+                                  max_pages * page_size <= 2^30 */
+} wf_paged_cache;
+
+/*
+ * Workspace (bytes) of the wf_paged_* and wf_pages_* calls on a cache of B
+ * sequences, G KV heads of size D, with H query heads and at most max_rows
+ * rows a sequence (both only matter to wf_paged_attention).  0 if the shapes
+ * are out of range.  Zero it once with wf_workspace_init.
+ */
+WF_API size_t wf_paged_workspace_bytes(int B, int H, int G, int D, int max_rows);
+
+/*
+ * A round's new keys and values enter the cache: row pos_off[b] + i of k and v
+ * becomes position cache_len[b] + i of sequence b in `layer`.
+ * k, v device, P rows of [G, D] bf16 bits, k_stride / v_stride elements from
+ * row to row (a multiple of 8, at least G * D: slices of one projection's
+ * output are fine); pos_off [B+1], cache_len [B] device int32.  WF_KV_E4M3
+ * stores x / scale, saturated to +-448 and rounded to the nearest value (ties
+ * to even; NaN stays NaN).  Rows outside [pos_off[0], pos_off[B]) are not read
+ * and no other position is written.  A position without a page (or past
+ * max_pages) sets WF_ERR_BAD_DATA (info = b) and its row is dropped.
+ */
+WF_API wf_status wf_paged_append(const wf_paged_cache* cache, int layer, const uint16_t* k, int64_t k_stride,
+                                 const uint16_t* v, int64_t v_stride, int P, const int32_t* pos_off,
+                                 const int32_t* cache_len, void* ws, size_t ws_bytes, wf_stream_t stream);
+
+/*
+ * Attention of a round's rows over the paged cache (paper Sec. 3.2: all
+ * candidates of a block or tree are verified by the target in one parallel
+ * pass).  Sequence b's rows pos_off[b] .. pos_off[b+1]-1 are laid out as for
+ * wf_verify_*: the first holds the last committed token, row 1 + i drafted
+ * node i.  Their keys and values are positions cache_len[b] + row of the cache
+ * (wf_paged_append).  Row i sees every position below cache_len[b], itself,
+ * and in a chain all rows before it, in a tree the first row and its
+ * ancestors.  A single new token is a sequence of one row; a sequence may have
+ * no row.  Per head h, g = h / (H / G):
+ *   s_t    = scale <q[row, h], key_t[g]>,  t the positions the row sees
+ *   out[row, h] = sum_t softmax(s)_t value_t[g]                      (bf16)
+ *   lse[row, h] = log sum_t e^(s_t)                                  (fp32, natural log)
+ * A masked position never reaches a row, whatever it holds; positions from
+ * cache_len[b] + rows on are not read.  fp32 softmax statistics and sums; the
+ * probabilities enter the product with V rounded to the 16-bit type of the
+ * matrix instruction (bf16; fp16 for WF_KV_E4M3).  The result does not depend
+ * on timing (splits of a long cache are joined in order).
+ * A sequence with a parent outside [-1, i), more than max_rows rows, a
+ * negative length, or a position without a page sets WF_ERR_BAD_DATA
+ * (info = b) and its rows are NaN; rows outside [pos_off[0], pos_off[B]) are
+ * left as they are.
+ */
+typedef struct wf_paged_attn_args {
+    const uint16_t* q;         /* P rows of [H, D] bf16 bits, 16-byte aligned */
+    int64_t q_stride;          /* elements from row to row: a multiple of 8, at least H * D */
+    int P, H;                  /* rows; query heads (H % G == 0, H / G <= 128, H * D <= 65536) */
+    const int32_t* pos_off;    /* [B+1] */
+    const int32_t* cache_len;  /* [B] positions before this round's rows */
+    const int32_t* node_off;   /* [B+1] as for wf_verify_tree, or NULL: every sequence is a chain */
+    const int32_t* kind;       /* [B] 0 = chain, 1 = tree; NULL = all trees (all chains if parent is NULL) */
+    const int32_t* parent;     /* [N] sequence-local parents, or NULL: every sequence is a chain */
+    int max_rows;              /* most rows of a sequence, 1 .. WF_MAX_SEQ_NODES + 1 */
+    int layer;
+    float scale;               /* > 0 and finite, e.g. 1 / sqrt(D) */
+    uint16_t* out;             /* [P, H, D] bf16 bits */
+    float* lse;                /* [P, H] or NULL */
+} wf_paged_attn_args;
+WF_API wf_status wf_paged_attention(const wf_paged_cache* cache, const wf_paged_attn_args* args, void* ws,
+                                    size_t ws_bytes, wf_stream_t stream);
+
+/*
+ * Keep the committed rows of a round (paper Sec. 3.2: decoding continues from
+ * the last accepted token): in every layer the accepted path's keys and values
+ * move up behind the first row,
+ *   position cache_len[b] + 1 + j  <-  cache_len[b] + 1 + path[b*path_stride + j],  j < n_accept[b]
+ *   new_len[b] = cache_len[b] + n_accept[b] + 1
+ * n_accept, path as returned by wf_verify_* / wf_round with the same
+ * path_stride (0 .. WF_MAX_SEQ_NODES; an n_accept past it is taken as
+ * path_stride; -1 keeps no row: new_len = cache_len).  new_len [B] device
+ * int32 out, may be cache_len itself.  A path that does not increase or a
+ * position without a page sets WF_ERR_BAD_DATA (info = b), moves nothing and
+ * writes new_len[b] = -1.
+ */
+WF_API wf_status wf_paged_compact(const wf_paged_cache* cache, const int32_t* n_accept, const int32_t* path,
+                                  int path_stride, const int32_t* cache_len, int32_t* new_len, void* ws,
+                                  size_t ws_bytes, wf_stream_t stream);
+
+/*
+ * Room for a round's rows: after the call positions cache_len[b] ..
+ * cache_len[b] + (pos_off[b+1] - pos_off[b]) - 1 of every sequence lie in
+ * pages that it holds alone.  In the order of the sequences (and of the blocks
+ * within one), a block without a page takes the lowest-numbered free page, and
+ * so does a block whose page another sequence holds too (copy on write: the
+ * old page's count drops by one, and if it holds positions below cache_len[b]
+ * its contents are copied, in every layer); the last holder keeps the page.
+ * added [B] device int32 out (or NULL): pages taken.  If the free pages do not
+ * suffice, the first sequence that does not fit and all after it get none:
+ * added = -1, their blocks stay as they were.  Negative or too long lengths,
+ * negative row counts and page ids out of range set WF_ERR_BAD_DATA
+ * (info = b), added = -1, and leave that sequence as it was.
+ */
+WF_API wf_status wf_pages_reserve(const wf_paged_cache* cache, const int32_t* pos_off, const int32_t* cache_len,
+                                  int32_t* added, void* ws, size_t ws_bytes, wf_stream_t stream);
+
+/*
+ * Sequence dst[i] becomes a copy of sequence src[i] (i < n) that shares its
+ * pages: table entries of the blocks below cache_len[src], their counts, and
+ * cache_len[dst] = cache_len[src] (in place).  No page is copied; the first
+ * write to a shared one does that (wf_pages_reserve).  Refused with
+ * WF_ERR_BAD_DATA (info = i), leaving both as they were: an index outside
+ * [0, B), a dst that still holds a page, that is listed twice, or that is also
+ * a src, a length without its pages.
+ */
+WF_API wf_status wf_pages_fork(const wf_paged_cache* cache, const int32_t* src, const int32_t* dst, int n,
+                               int32_t* cache_len, void* ws, size_t ws_bytes, wf_stream_t stream);
+
+/*
+ * Give back the pages past each sequence's length: entries from
+ * ceil(cache_len[b] / page_size) on drop one reference and become -1 (a length
+ * of 0 frees the sequence).  A negative length (WF_ERR_BAD_DATA, info = b)
+ * leaves the sequence as it was; a page id out of range or without a
+ * reference sets the same error and the entry becomes -1.
+ */
+WF_API wf_status wf_pages_trim(const wf_paged_cache* cache, const int32_t* cache_len, void* ws, size_t ws_bytes,
+                               wf_stream_t stream);
 
 #ifdef __cplusplus
 }

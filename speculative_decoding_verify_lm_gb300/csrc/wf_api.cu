@@ -1,6 +1,8 @@
 // C ABI entry points: host-side validation, workspace layout and the
 // stream-ordered composition of one verify-and-route round.
 #include <atomic>
+#include <math.h>
+
 #include <initializer_list>
 #include <mutex>
 
@@ -46,6 +48,19 @@ size_t catchup_attend_smem(int H, int G, int D);
 wf_status noalloc_lmhead_argmax(const uint16_t* hidden, const uint16_t* W, int P, int d, int V, int32_t* ids,
                                 float* maxlogit, cudaStream_t s);
 wf_status noalloc_read_device_error(int* code, int* info, int clear, cudaStream_t s);
+
+size_t paged_workspace_bytes(int B, int H, int G, int D, int max_rows);
+wf_status launch_paged_append(const wf_paged_cache* c, int layer, const uint16_t* k, int64_t k_stride,
+                              const uint16_t* v, int64_t v_stride, int P, const int32_t* pos_off,
+                              const int32_t* cache_len, void* ws, cudaStream_t s);
+wf_status launch_paged_compact(const wf_paged_cache* c, const int32_t* n_accept, const int32_t* path,
+                               int path_stride, const int32_t* cache_len, int32_t* new_len, void* ws, cudaStream_t s);
+wf_status launch_pages_reserve(const wf_paged_cache* c, const int32_t* pos_off, const int32_t* cache_len,
+                               int32_t* added, void* ws, cudaStream_t s);
+wf_status launch_pages_fork(const wf_paged_cache* c, const int32_t* src, const int32_t* dst, int n,
+                            int32_t* cache_len, void* ws, cudaStream_t s);
+wf_status launch_pages_trim(const wf_paged_cache* c, const int32_t* cache_len, void* ws, cudaStream_t s);
+wf_status launch_paged_attention(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s);
 
 static std::atomic<uint64_t> g_timeout_ns{2000000000ull};
 uint64_t wait_timeout_ns() { return g_timeout_ns.load(std::memory_order_relaxed); }
@@ -458,6 +473,89 @@ wf_status wf_round(const wf_round_args* a, void* ws, size_t ws_bytes, wf_stream_
         WF_TRY(launch_draft_topk(a->x, a->Wd, a->d2t, a->B, a->d, a->Vd, a->k, a->draft_ids, a->tids, a->vals,
                                  a->lse, ws, L.cand, L.lsep, stream));
     return WF_OK;
+}
+
+// ------------------------------------------------------------------ paged cache
+static bool bad_paged_heads(int B, int H, int G, int D, int max_rows) {
+    if (B < 1 || B > WF_PAGED_MAX_SEQS || max_rows < 1 || max_rows > WF_MAX_SEQ_NODES + 1) return true;
+    if (G < 1 || D < 16 || D > 128 || D % 16 || (long)G * D > 16384) return true;
+    return H < G || H % G || H / G > 128 || (long)H * D > 65536;
+}
+
+size_t wf_paged_workspace_bytes(int B, int H, int G, int D, int max_rows) {
+    return bad_paged_heads(B, H, G, D, max_rows) ? 0 : paged_workspace_bytes(B, H, G, D, max_rows);
+}
+
+// The cache's description and the workspace; `pages` = the call counts references.
+static wf_status check_paged(const wf_paged_cache* c, int H, int max_rows, bool pages, void* ws, size_t ws_bytes) {
+    if (!c || bad_paged_heads(c->B, H, c->G, c->D, max_rows)) return WF_ERR_INVALID_ARG;
+    if (!c->K || !c->V || !aligned16(c->K) || !aligned16(c->V) || !c->table) return WF_ERR_INVALID_ARG;
+    if (c->kv_type != WF_KV_BF16 && c->kv_type != WF_KV_E4M3) return WF_ERR_INVALID_ARG;
+    if (c->kv_type == WF_KV_BF16 && (c->k_scale || c->v_scale)) return WF_ERR_INVALID_ARG;
+    if (c->layers < 1 || c->num_pages < 1 || c->max_pages < 1) return WF_ERR_INVALID_ARG;
+    if (c->page_size < 8 || c->page_size > 1024 || (c->page_size & (c->page_size - 1))) return WF_ERR_INVALID_ARG;
+    if ((long long)c->num_pages * c->page_size >= 0x7FFFFFFFll - 4096) return WF_ERR_INVALID_ARG;
+    if ((long long)c->max_pages * c->page_size > (1ll << 30)) return WF_ERR_INVALID_ARG;
+    // grids and column counts stay 32-bit: 16-byte columns of all layers' rows
+    if ((long long)c->layers * 2 * c->G * c->D / 8 > 0x3FFFFFFFll) return WF_ERR_INVALID_ARG;
+    if (pages && !c->ref) return WF_ERR_INVALID_ARG;
+    WF_TRY(check_ws(ws, ws_bytes, paged_workspace_bytes(c->B, H, c->G, c->D, max_rows)));
+    WF_TRY(check_device());
+    return check_local({c->K, c->V, c->table, pages ? c->ref : nullptr, ws});
+}
+
+wf_status wf_paged_append(const wf_paged_cache* c, int layer, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                          int64_t v_stride, int P, const int32_t* pos_off, const int32_t* cache_len, void* ws,
+                          size_t ws_bytes, wf_stream_t stream) {
+    if (!c || layer < 0 || layer >= c->layers || P < 0 || !k || !v || !pos_off || !cache_len) return WF_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)c->G * c->D;
+    if (k_stride < row || k_stride % 8 || v_stride < row || v_stride % 8 || !aligned16(k) || !aligned16(v))
+        return WF_ERR_INVALID_ARG;
+    WF_TRY(check_paged(c, c->G, 1, false, ws, ws_bytes));
+    WF_TRY(check_local({k, v}));
+    return launch_paged_append(c, layer, k, k_stride, v, v_stride, P, pos_off, cache_len, ws, stream);
+}
+
+wf_status wf_paged_attention(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, size_t ws_bytes,
+                             wf_stream_t stream) {
+    if (!c || !a || a->layer < 0 || a->layer >= c->layers || a->P < 0) return WF_ERR_INVALID_ARG;
+    if (!a->q || !a->out || !a->pos_off || !a->cache_len || (a->parent && !a->node_off)) return WF_ERR_INVALID_ARG;
+    if (!(a->scale > 0.f) || !(a->scale < INFINITY)) return WF_ERR_INVALID_ARG;
+    if (!aligned16(a->q) || !aligned16(a->out) || a->q_stride % 8 || a->q_stride < (int64_t)a->H * c->D)
+        return WF_ERR_INVALID_ARG;
+    WF_TRY(check_paged(c, a->H, a->max_rows, false, ws, ws_bytes));
+    WF_TRY(check_local({a->q, a->out}));
+    return launch_paged_attention(c, a, ws, stream);
+}
+
+wf_status wf_paged_compact(const wf_paged_cache* c, const int32_t* n_accept, const int32_t* path, int path_stride,
+                           const int32_t* cache_len, int32_t* new_len, void* ws, size_t ws_bytes, wf_stream_t stream) {
+    if (!c || !n_accept || !cache_len || !new_len || path_stride < 0 || path_stride > WF_MAX_SEQ_NODES ||
+        (path_stride > 0 && !path))
+        return WF_ERR_INVALID_ARG;
+    WF_TRY(check_paged(c, c->G, 1, false, ws, ws_bytes));
+    return launch_paged_compact(c, n_accept, path, path_stride, cache_len, new_len, ws, stream);
+}
+
+wf_status wf_pages_reserve(const wf_paged_cache* c, const int32_t* pos_off, const int32_t* cache_len, int32_t* added,
+                           void* ws, size_t ws_bytes, wf_stream_t stream) {
+    if (!c || !pos_off || !cache_len) return WF_ERR_INVALID_ARG;
+    WF_TRY(check_paged(c, c->G, 1, true, ws, ws_bytes));
+    return launch_pages_reserve(c, pos_off, cache_len, added, ws, stream);
+}
+
+wf_status wf_pages_fork(const wf_paged_cache* c, const int32_t* src, const int32_t* dst, int n, int32_t* cache_len,
+                        void* ws, size_t ws_bytes, wf_stream_t stream) {
+    if (!c || !src || !dst || !cache_len || n < 0 || n > c->B) return WF_ERR_INVALID_ARG;
+    WF_TRY(check_paged(c, c->G, 1, true, ws, ws_bytes));
+    return launch_pages_fork(c, src, dst, n, cache_len, ws, stream);
+}
+
+wf_status wf_pages_trim(const wf_paged_cache* c, const int32_t* cache_len, void* ws, size_t ws_bytes,
+                        wf_stream_t stream) {
+    if (!c || !cache_len) return WF_ERR_INVALID_ARG;
+    WF_TRY(check_paged(c, c->G, 1, true, ws, ws_bytes));
+    return launch_pages_trim(c, cache_len, ws, stream);
 }
 
 }  // extern "C"

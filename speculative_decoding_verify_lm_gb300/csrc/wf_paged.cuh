@@ -1,0 +1,132 @@
+// Definitions shared by the paged cache's translation units: the workspace,
+// row addresses, the e4m3 conversions and the small matrix instructions.
+#pragma once
+
+#include "wf_internal.cuh"
+
+namespace wf {
+
+// ----------------------------------------------------------------- workspace
+// control block | arrival counters (zero at rest) | page bookkeeping of a
+// reserve call | partial results of the attention's splits
+constexpr int PA_TILE_M = 16;       // (row, head) pairs of a small-tile item
+constexpr int PA_MAX_CTAS = 640;    // most CTAs of an attention launch
+
+struct PagedLayout {
+    size_t cnt, off, need, copies, stat, part, total;
+};
+
+// rows of the attention's partial area: two partials of a tile for each CTA
+inline size_t paged_part_rows(int H, int G, int max_rows) {
+    (void)H;
+    (void)G;
+    (void)max_rows;
+    return (size_t)PA_MAX_CTAS * 2 * PA_TILE_M;
+}
+
+inline PagedLayout paged_layout(int B, int H, int G, int D, int max_rows) {
+    PagedLayout L;
+    const size_t rows = paged_part_rows(H, G, max_rows);
+    size_t o = sizeof(Control);
+    L.cnt = o;
+    o = align_up(o + 4 * (size_t)(B > PA_MAX_CTAS ? B : PA_MAX_CTAS), 256);
+    L.off = o;
+    o = align_up(o + 4 * (size_t)B, 256);
+    L.need = o;
+    o = align_up(o + 4 * (size_t)B, 256);
+    L.copies = o;
+    o = align_up(o + 8 * (size_t)B, 256);
+    L.stat = o;
+    o = align_up(o + 8 * rows, 256);
+    L.part = o;
+    o = align_up(o + 4 * rows * (size_t)D, 256);
+    L.total = o;
+    return L;
+}
+
+// ----------------------------------------------------------------- conversions
+__device__ __forceinline__ uint16_t pg_f32_to_bf16(float f) {   // nearest even; NaN stays NaN
+    uint32_t u = __float_as_uint(f);
+    if ((u & 0x7F800000u) == 0x7F800000u && (u & 0x007FFFFFu)) return (uint16_t)((u >> 16) | 0x40u);
+    u += 0x7FFFu + ((u >> 16) & 1u);
+    return (uint16_t)(u >> 16);
+}
+__device__ __forceinline__ float pg_bf16_to_f32(uint32_t b) { return __uint_as_float(b << 16); }
+// (lo, hi) -> two bf16 / fp16 in one word, round to nearest even
+__device__ __forceinline__ uint32_t cvt_bf16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ uint32_t cvt_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// (lo, hi) -> two e4m3 bytes, saturating, round to nearest even
+__device__ __forceinline__ uint32_t cvt_e4m3x2(float lo, float hi) {
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// two e4m3 bytes (the low half of w) -> two fp16, exact
+__device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
+    return r;
+}
+
+// ----------------------------------------------------------------- matrix instructions
+__device__ __forceinline__ void pg_mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void pg_mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void pg_ldsm_x4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void pg_ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+// 16 bytes global -> shared; `bytes` = 0 writes zeros and reads nothing
+__device__ __forceinline__ void pg_cp16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void pg_cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void pg_cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Last sequence whose first row is at or before row p: the largest b with
+// off[b] <= p, or -1 (warp-collective, the same answer in every lane).  Each
+// step loads 32 samples, so 1,024 sequences take two dependent loads.
+__device__ __forceinline__ int warp_seq_of(const int32_t* off, int B, int p, int lane) {
+    int lo = 0, n = B;   // candidates [lo, lo + n)
+    if (off[0] > p) return -1;
+    while (n > 1) {
+        const int step = (n + 31) / 32;
+        const int i = lane * step;
+        const bool le = i < n && off[lo + i] <= p;
+        const unsigned m = __ballot_sync(0xffffffffu, le);
+        const int s = m ? 31 - __clz(m) : 0;
+        lo += s * step;
+        n = min(step, n - s * step);
+    }
+    return lo;
+}
+
+}  // namespace wf

@@ -22,6 +22,8 @@ _lib = None
 
 WF_MAX_SEQ_NODES = 256
 WF_MAX_TOPK = 16
+WF_KV_BF16, WF_KV_E4M3 = 0, 1
+WF_PAGED_MAX_SEQS = 4096
 STATUS = {0: "WF_OK", 1: "WF_ERR_INVALID_ARG", 2: "WF_ERR_WORKSPACE", 3: "WF_ERR_CUDA", 4: "WF_ERR_UNSUPPORTED",
           5: "WF_ERR_BAD_DATA", 6: "WF_ERR_TIMEOUT"}
 
@@ -68,6 +70,24 @@ class CatchupArgs(ctypes.Structure):
     ]
 
 
+class PagedCacheArgs(ctypes.Structure):
+    """Mirror of ``wf_paged_cache``."""
+    _fields_ = [
+        ("K", _c_void_p), ("V", _c_void_p), ("k_scale", _c_void_p), ("v_scale", _c_void_p), ("table", _c_void_p),
+        ("ref", _c_void_p), ("kv_type", _i32), ("layers", _i32), ("num_pages", _i32), ("page_size", _i32),
+        ("G", _i32), ("D", _i32), ("B", _i32), ("max_pages", _i32),
+    ]
+
+
+class PagedAttnArgs(ctypes.Structure):
+    """Mirror of ``wf_paged_attn_args``."""
+    _fields_ = [
+        ("q", _c_void_p), ("q_stride", ctypes.c_int64), ("P", _i32), ("H", _i32), ("pos_off", _c_void_p),
+        ("cache_len", _c_void_p), ("node_off", _c_void_p), ("kind", _c_void_p), ("parent", _c_void_p),
+        ("max_rows", _i32), ("layer", _i32), ("scale", _f32), ("out", _c_void_p), ("lse", _c_void_p),
+    ]
+
+
 _SIGS = {
     "wf_status_string": (ctypes.c_char_p, [_i32]),
     "wf_version": (_i32, []),
@@ -101,6 +121,18 @@ _SIGS = {
     "wf_catchup_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32, _i32]),
     "wf_catchup_kv": (_i32, [ctypes.POINTER(CatchupArgs), _c_void_p, _sz, _c_void_p]),
     "wf_catchup": (_i32, [ctypes.POINTER(CatchupArgs), _c_void_p, _sz, _c_void_p]),
+    "wf_paged_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "wf_paged_append": (_i32, [ctypes.POINTER(PagedCacheArgs), _i32, _c_void_p, ctypes.c_int64, _c_void_p,
+                               ctypes.c_int64, _i32, _c_void_p, _c_void_p, _c_void_p, _sz, _c_void_p]),
+    "wf_paged_attention": (_i32, [ctypes.POINTER(PagedCacheArgs), ctypes.POINTER(PagedAttnArgs), _c_void_p, _sz,
+                                  _c_void_p]),
+    "wf_paged_compact": (_i32, [ctypes.POINTER(PagedCacheArgs), _c_void_p, _c_void_p, _i32, _c_void_p, _c_void_p,
+                                _c_void_p, _sz, _c_void_p]),
+    "wf_pages_reserve": (_i32, [ctypes.POINTER(PagedCacheArgs), _c_void_p, _c_void_p, _c_void_p, _c_void_p, _sz,
+                                _c_void_p]),
+    "wf_pages_fork": (_i32, [ctypes.POINTER(PagedCacheArgs), _c_void_p, _c_void_p, _i32, _c_void_p, _c_void_p, _sz,
+                             _c_void_p]),
+    "wf_pages_trim": (_i32, [ctypes.POINTER(PagedCacheArgs), _c_void_p, _c_void_p, _sz, _c_void_p]),
 }
 
 
@@ -456,6 +488,166 @@ class Catchup:
         st = fn(ctypes.byref(self.args), self.ws.ptr, self.ws.nbytes, _stream(stream))
         _raise(st, "wf_catchup_kv" if self.kv_only else "wf_catchup")
         return self.out, self.attn
+
+
+class PagedCache:
+    """A paged key-value cache over caller-owned device tensors (``wf_paged_cache``).
+
+    K, V [layers, num_pages, page_size, G, D] (or without the layers: one layer),
+    bf16 or float8_e4m3fn; table [B, max_pages] int32 (-1 = no page); ref
+    [num_pages] int32 reference counts (wf_pages_*); k_scale / v_scale [layers, G]
+    fp32 scales of an e4m3 cache.  The object keeps the tensors alive; the calls
+    read and write them in place."""
+
+    def __init__(self, K, V, table, ref=None, k_scale=None, v_scale=None):
+        if K.dim() == 4 and V.dim() == 4:
+            K, V = K[None], V[None]
+        if K.dim() != 5 or K.shape != V.shape or K.dtype != V.dtype:
+            raise ValueError("K and V must be [layers, num_pages, page_size, G, D] of one type")
+        if table.dim() != 2:
+            raise ValueError("table must be [B, max_pages]")
+        e4m3 = K.dtype == torch.float8_e4m3fn
+        types = (torch.float8_e4m3fn,) if e4m3 else _BF16
+        layers, num_pages, page_size, G, D = K.shape
+        for name, t_ in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t_ is not None and (not e4m3 or t_.numel() != layers * G):
+                raise ValueError(f"{name}: [layers, G] fp32, of an e4m3 cache only")
+        if ref is not None and ref.numel() != num_pages:
+            raise ValueError("ref must be [num_pages]")
+        self.K, self.V, self.table, self.ref, self.k_scale, self.v_scale = K, V, table, ref, k_scale, v_scale
+        a = PagedCacheArgs()
+        a.K, a.V = _check(K, "K", types), _check(V, "V", types)
+        a.k_scale = _check(k_scale, "k_scale", _F32, True)
+        a.v_scale = _check(v_scale, "v_scale", _F32, True)
+        a.table = _check(table, "table", _I32)
+        a.ref = _check(ref, "ref", _I32, True)
+        a.kv_type = WF_KV_E4M3 if e4m3 else WF_KV_BF16
+        a.layers, a.num_pages, a.page_size, a.G, a.D = layers, num_pages, page_size, G, D
+        a.B, a.max_pages = table.shape
+        self.args = a
+        self._ref = ctypes.byref(a)
+
+    @property
+    def B(self) -> int:
+        return self.args.B
+
+
+class PagedWorkspace(Workspace):
+    """Workspace of the wf_paged_* / wf_pages_* calls on a cache of B sequences; H query heads and max_rows rows
+    a sequence as for wf_paged_attention (the other calls take any workspace of their B, G and D)."""
+
+    def __init__(self, B: int, H: int, G: int, D: int, max_rows: int = 1, device=None, stream=None):
+        self.nbytes = int(lib().wf_paged_workspace_bytes(B, H, G, D, max_rows))
+        if self.nbytes == 0:
+            raise ValueError("paged cache shapes outside the library's range")
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device or "cuda")
+        _raise(lib().wf_workspace_init(self.buf.data_ptr(), self.nbytes, _stream(stream)), "wf_workspace_init")
+
+
+def _rows(t, name, heads, D):
+    """Address and row stride of [P, heads, D] bf16 rows; the rows may lie apart (a slice of a wider projection)."""
+    if not t.is_cuda or t.dtype not in _BF16:
+        raise ValueError(f"{name} must be a bf16 CUDA tensor")
+    if t.dim() != 3 or t.shape[2] != D or (heads and t.shape[1] != heads):
+        raise ValueError(f"{name} must be [P, {heads or 'H'}, {D}]")
+    if t.numel() == 0:
+        return _placeholder(t.device), t.shape[1] * D
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+        raise ValueError(f"{name}: each row's heads must lie densely")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+
+
+def _lens(t, name, n, optional=False):
+    p = _check(t, name, _I32, optional)
+    if t is not None and t.numel() != n:
+        raise ValueError(f"{name} needs {n} elements")
+    return p
+
+
+def wf_paged_append(cache: PagedCache, k, v, pos_off, cache_len, ws: Workspace, layer: int = 0, stream=None):
+    """Store the round's keys and values (rows pos_off[b] + i of k, v [P, G, D] bf16, strided rows allowed) at
+    positions cache_len[b] + i of each sequence."""
+    a = cache.args
+    kp, ks = _rows(k, "k", a.G, a.D)
+    vp, vs = _rows(v, "v", a.G, a.D)
+    if k.shape[0] != v.shape[0]:
+        raise ValueError("k and v must have the same rows")
+    _raise(lib().wf_paged_append(cache._ref, layer, kp, ks, vp, vs, k.shape[0], _lens(pos_off, "pos_off", a.B + 1),
+                                 _lens(cache_len, "cache_len", a.B), ws.ptr, ws.nbytes, _stream(stream)),
+           "wf_paged_append")
+
+
+def wf_paged_attention(cache: PagedCache, q, pos_off, cache_len, ws: Workspace, node_off=None, kind=None, parent=None,
+                       max_rows: int = 1, layer: int = 0, scale=None, out=None, lse=None, with_lse: bool = False,
+                       stream=None):
+    """Attention of the round's rows over the paged cache -> (out [P, H, D] bf16, lse [P, H] fp32 or None).
+
+    q [P, H, D] bf16 (strided rows allowed), rows pos_off[b] .. pos_off[b+1]-1 of sequence b at positions
+    cache_len[b] ..; single new tokens: one row each.  Chains unless parent (with node_off, and kind to mix) gives
+    trees.  max_rows: most rows of a sequence.  scale: 1 / sqrt(D) if None."""
+    c = cache.args
+    a = PagedAttnArgs()
+    a.q, a.q_stride = _rows(q, "q", 0, c.D)
+    a.P, a.H, D = q.shape
+    a.pos_off = _lens(pos_off, "pos_off", c.B + 1)
+    a.cache_len = _lens(cache_len, "cache_len", c.B)
+    a.node_off = _lens(node_off, "node_off", c.B + 1, True)
+    a.kind = _lens(kind, "kind", c.B, True)
+    a.parent = _check(parent, "parent", _I32, True)
+    a.max_rows, a.layer = max_rows, layer
+    a.scale = D ** -0.5 if scale is None else scale
+    if out is None:
+        out = torch.empty((a.P, a.H, D), dtype=q.dtype, device=q.device)
+    elif out.numel() != q.numel():
+        raise ValueError("out must be [P, H, D]")
+    if lse is None and with_lse:
+        lse = torch.empty((a.P, a.H), dtype=torch.float32, device=q.device)
+    elif lse is not None and lse.numel() != a.P * a.H:
+        raise ValueError("lse must be [P, H]")
+    a.out = _check(out, "out", _BF16)
+    a.lse = _check(lse, "lse", _F32, True)
+    _raise(lib().wf_paged_attention(cache._ref, ctypes.byref(a), ws.ptr, ws.nbytes, _stream(stream)),
+           "wf_paged_attention")
+    return out, lse
+
+
+def wf_paged_compact(cache: PagedCache, n_accept, path, cache_len, ws: Workspace, new_len=None, stream=None):
+    """Move the accepted path's keys and values up behind the round's first row, in every layer -> new_len [B]
+    (pass cache_len as new_len to update it in place)."""
+    B = cache.args.B
+    if path is not None and (path.dim() != 2 or path.shape[0] != B):
+        raise ValueError("path must be [B, path_stride]")
+    if new_len is None:
+        new_len = torch.empty(B, dtype=torch.int32, device=cache.K.device)
+    ps = path.shape[1] if path is not None else 0
+    _raise(lib().wf_paged_compact(cache._ref, _lens(n_accept, "n_accept", B), _check(path, "path", _I32, True), ps,
+                                  _lens(cache_len, "cache_len", B), _lens(new_len, "new_len", B), ws.ptr, ws.nbytes,
+                                  _stream(stream)), "wf_paged_compact")
+    return new_len
+
+
+def wf_pages_reserve(cache: PagedCache, pos_off, cache_len, ws: Workspace, added=None, stream=None):
+    """Pages for the round's rows, shared ones replaced by copies -> added [B] (pages taken, -1 = did not fit)."""
+    B = cache.args.B
+    if added is None:
+        added = torch.empty(B, dtype=torch.int32, device=cache.K.device)
+    _raise(lib().wf_pages_reserve(cache._ref, _lens(pos_off, "pos_off", B + 1), _lens(cache_len, "cache_len", B),
+                                  _lens(added, "added", B), ws.ptr, ws.nbytes, _stream(stream)), "wf_pages_reserve")
+    return added
+
+
+def wf_pages_fork(cache: PagedCache, src, dst, cache_len, ws: Workspace, stream=None):
+    """Sequences dst become copies of sequences src that share their pages; cache_len[dst] follows, in place."""
+    n = src.numel()
+    _raise(lib().wf_pages_fork(cache._ref, _check(src, "src", _I32), _lens(dst, "dst", n), n,
+                               _lens(cache_len, "cache_len", cache.args.B), ws.ptr, ws.nbytes, _stream(stream)),
+           "wf_pages_fork")
+
+
+def wf_pages_trim(cache: PagedCache, cache_len, ws: Workspace, stream=None):
+    """Give back the pages past each sequence's length (0 frees the sequence)."""
+    _raise(lib().wf_pages_trim(cache._ref, _lens(cache_len, "cache_len", cache.args.B), ws.ptr, ws.nbytes,
+                               _stream(stream)), "wf_pages_trim")
 
 
 def _packed(spec, device):

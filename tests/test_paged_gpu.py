@@ -1,0 +1,449 @@
+"""The paged cache on the GPU against plain 64-bit references (paged_ref):
+attention of single tokens, chains and trees, appended and compacted rows, and
+the pages' bookkeeping.  Positions that no sequence owns hold NaN throughout."""
+import numpy as np
+import pytest
+import torch
+
+import paged_ref as ref
+from gpu_util import DEV, dev, host
+from speculative_decoding_verify_lm_gb300 import wf
+
+pytestmark = pytest.mark.gpu
+
+BAD = 5
+
+
+def cache_of(c, **kw):
+    return wf.PagedCache(c.K.to(DEV), c.V.to(DEV), dev(c.table), k_scale=dev(c.k_scale) if c.kv == "e4m3" else None,
+                         v_scale=dev(c.v_scale) if c.kv == "e4m3" else None, **kw)
+
+
+def run_attention(c, cache=None, scale=None, max_rows=None, q=None, ws=None, trees=None):
+    cache = cache or cache_of(c)
+    mr = max(max(c.rows), 1) if max_rows is None else max_rows
+    ws = ws or wf.PagedWorkspace(c.B, c.H, c.G, c.D, mr)
+    trees = any(c.kinds) if trees is None else trees
+    out = torch.full((c.P, c.H, c.D), 7.0, dtype=torch.bfloat16, device=DEV)
+    lse = torch.full((c.P, c.H), 7.0, dtype=torch.float32, device=DEV)
+    wf.wf_paged_attention(cache, c.q.to(DEV) if q is None else q, dev(c.pos_off), dev(np.array(c.lens, np.int32)), ws,
+                          node_off=dev(c.node_off) if trees else None,
+                          kind=dev(np.array(c.kinds, np.int32)) if trees else None,
+                          parent=dev(c.parent) if trees else None, max_rows=mr, layer=c.layer, scale=scale, out=out,
+                          lse=lse)
+    torch.cuda.synchronize()
+    return host(out.float()).astype(np.float64), host(lse).astype(np.float64), ws
+
+
+def check(c, scale=None, **kw):
+    out, lse, ws = run_attention(c, scale=scale, **kw)
+    assert ws.device_error() == (0, 0)
+    ro, rl, to, tl = ref.attention(c, c.D ** -0.5 if scale is None else scale)
+    mine = ~np.isnan(rl)
+    assert np.all(np.abs(out - ro)[mine] <= to[mine]), np.max((np.abs(out - ro) - to)[mine])
+    assert np.all(np.abs(lse - rl)[mine] <= tl[mine]), np.max((np.abs(lse - rl) - tl)[mine])
+    # rows of no sequence are left as they were
+    assert np.all(out[~mine] == 7.0) and np.all(lse[~mine] == 7.0)
+    return out, lse
+
+
+# lens, rows, H, G, D, ps
+ONE = [
+    ((0,), (1,), 4, 2, 64, 16),                             # the first token: it sees itself alone
+    ((1, 62, 63, 64, 65, 127), (1,) * 6, 8, 2, 128, 16),    # around a tile's end
+    ((200, 0, 7), (1, 0, 1), 8, 8, 64, 8),                  # a sequence without a row, one head a group
+    ((500,), (1,), 32, 8, 80, 16),                          # the drafter's geometry
+    ((1000, 3), (1, 1), 20, 1, 96, 32),                     # 20 heads over one: two tiles of pairs
+    ((333,), (1,), 4, 4, 16, 8),                            # the smallest head
+    ((90, 91), (1, 1), 12, 4, 48, 64),
+    ((300,), (1,), 7, 1, 112, 128),
+    ((5000,), (1,), 2, 1, 64, 1024),                        # split over many CTAs, one large page size
+    (tuple(range(40, 240)), (1,) * 200, 2, 1, 32, 16),      # more sequences than threads
+]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,rows,H,G,D,ps", ONE)
+def test_single_tokens(lens, rows, H, G, D, ps, kv):
+    check(ref.Case(1, lens, rows, H, G, D, ps, kv))
+
+
+# lens, rows, kinds, H, G, D, ps
+ROUNDS = [
+    ((0,), (2,), (0,), 2, 1, 32, 8),
+    ((50,), (17,), (0,), 8, 2, 128, 16),                    # a chain of 16
+    ((130,), (61,), (1,), 8, 2, 64, 16),                    # a tree of 60
+    ((63, 64, 0, 10), (17, 61, 5, 0), (0, 1, 1, 0), 8, 2, 128, 16),   # mixed, one without a row
+    ((300,), (257,), (1,), 2, 1, 16, 32),                   # the largest round
+    ((100, 700), (61, 17), (1, 0), 10, 2, 80, 16),          # five heads a group
+    ((20, 31), (33, 32), (1, 1), 16, 1, 96, 8),
+    ((1500,), (4,), (0,), 4, 2, 112, 64),
+    ((9, 8, 7), (3, 2, 1), (1, 1, 1), 1, 1, 128, 8),
+    ((129, 255), (128, 129), (0, 1), 3, 1, 48, 16),
+]
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,rows,kinds,H,G,D,ps", ROUNDS)
+def test_rounds(lens, rows, kinds, H, G, D, ps, kv):
+    check(ref.Case(2, lens, rows, H, G, D, ps, kv, kinds=kinds))
+
+
+def test_all_chains_without_a_tree_description():
+    c = ref.Case(3, (40, 5), (9, 17), 4, 2, 64, 16)
+    check(c, trees=False)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_layers_strided_queries_and_rows_outside(kv):
+    """Layer 2 of 3, queries inside a wider projection's rows, rows before the first and behind the last sequence."""
+    c = ref.Case(4, (70, 33), (5, 1), 8, 2, 64, 16, kv, kinds=(1, 0), layers=3, layer=2, extra_rows=3, first_row=2)
+    wide = torch.randn((c.P, 12, 64), device=DEV).to(torch.bfloat16)
+    wide[:, :8] = c.q.to(DEV)
+    check(c, q=wide[:, :8])
+
+
+@pytest.mark.parametrize("scale", [1e-3, 1.0, 8.0])
+def test_scales(scale):
+    """Nearly uniform weights, and scores far apart (the running maximum moves often)."""
+    check(ref.Case(5, (900, 70), (1, 20), 4, 2, 64, 16, kinds=(0, 1), spread=2.0), scale=scale)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_masked_values_that_are_not_finite(kv):
+    """A drafted row whose key and value are not finite reaches only the rows that see it."""
+    c = ref.Case(6, (45,), (40,), 8, 2, 64, 16, kv, kinds=(1,))
+    c.parent[:] = [-1 if i < 4 else int(c.rng.integers(0, i)) for i in range(39)]
+    see = c.sees(0)
+    j = 1 + 3                                                # node 3, a child of the root
+    t = c.lens[0] + j
+    clean_k, clean_v = c.K.clone(), c.V.clone()
+    spots = ("V", "K")
+    for which in spots:
+        c.K, c.V = clean_k.clone(), clean_v.clone()
+        pool = c.V if which == "V" else c.K
+        bad = float("inf") if kv == "bf16" and which == "V" else float("nan")
+        pool[0, c.table[0, t // c.ps], t % c.ps, 1, 5] = bad
+        out, lse, ws = run_attention(c)
+        assert ws.device_error() == (0, 0)
+        c.K, c.V = clean_k, clean_v
+        ro, rl, to, tl = ref.attention(c, c.D ** -0.5)
+        hit = see[:, j]
+        assert hit.any() and not hit.all()
+        for i in range(c.rows[0]):
+            good = np.abs(out[i] - ro[i]) <= to[i]
+            if not hit[i]:
+                assert good.all(), (which, i)
+            elif which == "V":
+                assert good[:4].all() and good[4:, [d for d in range(64) if d != 5]].all()
+                assert not np.isfinite(out[i, 4:, 5]).any()
+            else:
+                assert good[:4].all() and np.isnan(out[i, 4:]).all()
+
+
+def test_repeated_calls_give_the_same_bits():
+    c = ref.Case(7, (3000, 10, 1200), (1, 1, 1), 8, 2, 128, 16)
+    cache, ws = cache_of(c), wf.PagedWorkspace(3, 8, 2, 128)
+    a = run_attention(c, cache, ws=ws)
+    for _ in range(3):
+        b = run_attention(c, cache, ws=ws)
+        assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("what", ["parent", "rows", "length", "page", "long", "nodes"])
+def test_bad_sequences_are_nan_and_alone(what):
+    c = ref.Case(8, (100, 64, 30), (9, 9, 9), 4, 2, 64, 16, kinds=(1, 1, 1))
+    cache = cache_of(c)
+    ws = wf.PagedWorkspace(3, 4, 2, 64, 9)
+    good = run_attention(c, cache, ws=ws)
+    assert ws.device_error() == (0, 0)
+    keep_lens, mr = list(c.lens), 9
+    if what == "parent":
+        c.parent = c.parent.copy()
+        c.parent[8 + 4] = 4                                  # its own index
+    elif what == "rows":
+        mr = 8
+    elif what == "length":
+        c.lens[1] = -1
+    elif what == "long":
+        c.lens[1] = c.max_pages * c.ps - 8
+    elif what == "page":
+        t = c.table.copy()
+        t[1, 2] = c.num_pages
+        cache = wf.PagedCache(cache.K, cache.V, dev(t))
+    elif what == "nodes":
+        c.node_off = c.node_off.copy()
+        c.node_off[2:] += 1
+        c.parent = np.concatenate([c.parent, [0]]).astype(np.int32)
+    out, lse, _ = run_attention(c, cache, ws=ws, max_rows=mr)
+    code, info = ws.device_error()
+    assert code == BAD and info in ((0, 1, 2) if what == "rows" else (1,))
+    hit = slice(0, 27) if what == "rows" else slice(9, 18)
+    assert np.isnan(out[hit]).all() and np.isnan(lse[hit]).all()
+    if what not in ("rows", "nodes"):
+        for s in (slice(0, 9), slice(18, 27)):
+            assert np.array_equal(out[s], good[0][s]) and np.array_equal(lse[s], good[1][s])
+    elif what == "nodes":
+        assert np.array_equal(out[:9], good[0][:9])
+    c.lens = keep_lens
+    # the workspace is as good as before
+    assert ws.device_error() == (0, 0)
+
+
+def test_identity_table_reads_the_catch_up_cache():
+    """The catch-up's cache as a one-layer pool: its attention over the final token, again through the pages."""
+    import pins
+    case = pins.catchup_case(31, din=256, H=8, G=2, D=64, n=(5, 9), L=(40, 100), cap=128)
+    Kc, Vc = dev(case["Kc"]), dev(case["Vc"])
+    cu = wf.Catchup(dev(case["u"]), dev(case["bl_off"]), dev(case["cache_len"]), dev(case["gamma"]), dev(case["Wk"]),
+                    dev(case["Wv"]), Kc, Vc, 2, Wq=dev(case["Wq"]), Wo=dev(case["Wo"]), eps=case["eps"],
+                    theta=case["theta"])
+    cu()
+    torch.cuda.synchronize()
+    B, cap, G, D, H, ps = 2, 128, 2, 64, 8, 16
+    c = ref.Case(32, (44, 108), (1, 1), H, G, D, ps)
+    c.num_pages, c.max_pages = B * cap // ps, cap // ps
+    c.table = np.arange(B * cap // ps, dtype=np.int32).reshape(B, cap // ps)
+    c.K = Kc.view(torch.bfloat16).cpu().view(1, -1, ps, G, D)
+    c.V = Vc.view(torch.bfloat16).cpu().view(1, -1, ps, G, D)
+    check(c)
+
+
+# ------------------------------------------------------------------ append
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,rows,G,D,ps", [
+    ((0,), (1,), 1, 16, 8),
+    ((5, 0, 31, 7), (17, 0, 61, 1), 2, 80, 16),
+    ((100,) * 70, (3,) * 70, 4, 64, 32),
+    ((15, 16), (1, 257), 8, 128, 8),
+])
+def test_append(lens, rows, G, D, ps, kv):
+    c = ref.Case(11, lens, rows, G, G, D, ps, kv, layers=2, layer=1, extra_rows=2, first_row=1)
+    cache = cache_of(c)
+    x = torch.randn((c.P, 2, G, D), device=DEV).mul_(40).to(torch.bfloat16)
+    if kv == "e4m3":
+        x[0, :, 0, 0] = float("inf")
+    ws = wf.PagedWorkspace(c.B, G, G, D)
+    wf.wf_paged_append(cache, x[:, 0], x[:, 1], dev(c.pos_off), dev(np.array(lens, np.int32)), ws, layer=1)
+    torch.cuda.synchronize()
+    assert ws.device_error() == (0, 0)
+    for i, (pool, was, sc) in enumerate(((cache.K, c.K, c.k_scale), (cache.V, c.V, c.v_scale))):
+        want = was.float().numpy().astype(np.float64)
+        src = x[:, i].float().cpu().numpy().astype(np.float64)
+        for b in range(c.B):
+            for r in range(rows[b]):
+                t = lens[b] + r
+                y = src[c.pos_off[b] + r]
+                if sc is not None:
+                    # the quotient is a 32-bit number before it is rounded to 8 bits
+                    y = (y.astype(np.float32) / sc[1][:, None]).astype(np.float64)
+                    y = ref.nearest_e4m3(y)
+                want[1, c.table[b, t // ps], t % ps] = y
+        got = pool.float().cpu().numpy()
+        assert np.array_equal(got, want, equal_nan=True)
+
+
+def test_append_saturates_and_keeps_nan():
+    c = ref.Case(12, (0,), (1,), 1, 1, 16, 8, "e4m3")
+    cache = cache_of(c)
+    k = torch.zeros((1, 1, 16), dtype=torch.bfloat16, device=DEV)
+    k[0, 0, :4] = torch.tensor([float("inf"), -float("inf"), float("nan"), 1e30])
+    ws = wf.PagedWorkspace(1, 1, 1, 16)
+    wf.wf_paged_append(cache, k, k, dev(c.pos_off), dev(np.array([0], np.int32)), ws)
+    got = cache.K[0, c.table[0, 0], 0, 0].float().cpu().numpy()
+    assert got[0] == 448 and got[1] == -448 and np.isnan(got[2]) and got[3] == 448 and (got[4:] == 0).all()
+
+
+def test_append_without_a_page():
+    c = ref.Case(13, (14, 3), (4, 4), 2, 2, 32, 16)
+    t = c.table.copy()
+    t[0, 1] = -1                                             # positions 16, 17 of sequence 0
+    cache = wf.PagedCache(c.K.to(DEV), c.V.to(DEV), dev(t))
+    x = torch.randn((8, 2, 32), device=DEV).to(torch.bfloat16)
+    ws = wf.PagedWorkspace(2, 2, 2, 32)
+    wf.wf_paged_append(cache, x, x, dev(c.pos_off), dev(np.array([14, 3], np.int32)), ws)
+    torch.cuda.synchronize()
+    assert ws.device_error() == (BAD, 0)
+    want = c.K.clone()
+    xc = x.cpu()
+    want[0, c.table[0, 0], 14:16] = xc[:2]
+    want[0, c.table[1, 0], 3:7] = xc[4:]
+    assert torch.equal(torch.nan_to_num(cache.K.cpu()), torch.nan_to_num(want))
+
+
+# ------------------------------------------------------------------ compact
+@pytest.mark.parametrize("kv,in_place", [("bf16", False), ("e4m3", False), ("bf16", True)])
+def test_compact(kv, in_place):
+    lens, rows = (14, 0, 33, 7, 40, 5), (61, 9, 17, 3, 1, 257)
+    c = ref.Case(14, lens, rows, 2, 2, 48, 16, kv, kinds=(1, 1, 0, 1, 1, 1), layers=3)
+    S = 40
+    path = np.full((6, S), -1, np.int32)
+    n = np.array([8, 3, 5, -1, 0, 40], np.int32)
+    path[0, :8] = [0, 1, 5, 6, 20, 33, 40, 59]
+    path[1, :3] = [2, 3, 7]
+    path[2, :5] = range(5)                                   # a chain: nothing moves
+    path[5, :40] = np.sort(c.rng.permutation(256)[:40])
+    n_call = n.copy()
+    n_call[5] = 200                                          # past the columns: taken as the columns
+    cache = cache_of(c)
+    ws = wf.PagedWorkspace(6, 2, 2, 48)
+    ln = dev(np.array(lens, np.int32))
+    new = wf.wf_paged_compact(cache, dev(n_call), dev(path), ln, ws, new_len=ln if in_place else None)
+    torch.cuda.synchronize()
+    assert ws.device_error() == (0, 0)
+    assert np.array_equal(host(new), [23, 4, 39, 7, 41, 46])
+    for pool, was in ((cache.K, c.K), (cache.V, c.V)):
+        raw = torch.int16 if kv == "bf16" else torch.uint8
+        want = was.view(raw).clone()
+        src = want.clone()
+        for b in range(6):
+            for j in range(max(n[b], 0)):
+                f, t = lens[b] + 1 + path[b, j], lens[b] + 1 + j
+                want[:, c.table[b, t // 16], t % 16] = src[:, c.table[b, f // 16], f % 16]
+        assert torch.equal(pool.cpu().view(raw), want)
+
+
+def test_compact_refuses_bad_paths():
+    lens, rows = (14, 3, 9, 2), (9, 9, 9, 9)
+    c = ref.Case(15, lens, rows, 1, 1, 16, 8, layers=2)
+    path = np.array([[0, 2, 2], [1, 0, 3], [-1, 4, 5], [1, 3, 7]], np.int32)
+    n = np.array([3, 3, 3, 3], np.int32)
+    t = c.table.copy()
+    t[3, 1] = -1                                             # position 2 + 1 + 7 = 10 has no page
+    cache = wf.PagedCache(c.K.to(DEV), c.V.to(DEV), dev(t))
+    ws = wf.PagedWorkspace(4, 1, 1, 16)
+    new = wf.wf_paged_compact(cache, dev(n), dev(path), dev(np.array(lens, np.int32)), ws)
+    torch.cuda.synchronize()
+    assert ws.device_error()[0] == BAD
+    assert np.array_equal(host(new), [-1] * 4)
+    assert torch.equal(cache.K.cpu().view(torch.int16), c.K.view(torch.int16))
+
+
+# ------------------------------------------------------------------ pages
+def random_pages(rng, B, width, ps, num_pages, share):
+    """Sequences with pages of their own, then some that share another's."""
+    table = np.full((B, width), -1, np.int32)
+    refs = np.zeros(num_pages, np.int32)
+    lens = np.zeros(B, np.int32)
+    order = list(rng.permutation(num_pages))
+    for b in range(B):
+        if b and rng.random() < share:
+            a = int(rng.integers(0, b))
+            lens[b] = lens[a]
+            table[b] = table[a]
+            refs[table[b][table[b] >= 0]] += 1
+            continue
+        lens[b] = rng.integers(0, (width - 2) * ps)
+        n = min(-(-int(lens[b]) // ps), len(order))
+        lens[b] = min(lens[b], n * ps)
+        for j in range(n):
+            table[b, j] = order.pop()
+            refs[table[b, j]] = 1
+    return table, refs, lens
+
+
+def pages_cache(table, refs, ps, layers=2, G=1, D=16):
+    n = len(refs)
+    K = torch.arange(layers * n * ps * G * D, device=DEV).remainder_(251).view(layers, n, ps, G, D).to(torch.bfloat16)
+    V = (K.float() + 0.5).to(torch.bfloat16)
+    cache = wf.PagedCache(K, V, dev(table), ref=dev(refs))
+    return cache, wf.PagedWorkspace(table.shape[0], G, G, D), K.clone(), V.clone()
+
+
+@pytest.mark.parametrize("seed,B,width,num_pages,share,most", [
+    (1, 1, 4, 8, 0.0, 3),
+    (2, 20, 8, 300, 0.5, 40),
+    (3, 70, 6, 500, 0.8, 2),
+    (4, 40, 8, 220, 0.3, 60),                                # the pages run out
+    (5, 1500, 5, 9000, 0.6, 9),                              # more sequences than threads
+    (6, 30, 40, 40000, 0.2, 100),                            # free pages in several chunks
+    (7, 10, 5, 31, 1.0, 30),
+])
+def test_reserve(seed, B, width, num_pages, share, most):
+    ps = 8
+    rng = np.random.default_rng(seed)
+    table, refs, lens = random_pages(rng, B, width, ps, num_pages, share)
+    if seed == 6:                                            # the first 30,000 pages are held by others
+        refs[:30000] += 1
+    rows = rng.integers(0, most + 1, B).astype(np.int32)
+    rows = np.minimum(rows, width * ps - lens).astype(np.int32)
+    cache, ws, K, V = pages_cache(table, refs, ps)
+    pos = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    added = wf.wf_pages_reserve(cache, dev(pos), dev(lens), ws)
+    torch.cuda.synchronize()
+    assert ws.device_error() == (0, 0)
+    t2, r2, a2, copies = ref.reserve(table, refs, lens, rows, ps)
+    if seed == 4:
+        assert (a2 < 0).any() and (a2 > 0).any()
+    assert np.array_equal(host(added), a2)
+    assert np.array_equal(host(cache.table), t2)
+    assert np.array_equal(host(cache.ref), r2)
+    for a, b in copies:
+        K[:, b], V[:, b] = K[:, a], V[:, a]
+    assert torch.equal(cache.K, K) and torch.equal(cache.V, V)
+
+
+def test_reserve_leaves_bad_sequences():
+    ps = 8
+    table = np.array([[0, -1, -1], [1, -1, -1], [-1, -1, -1], [99, -1, -1], [2, -1, -1]], np.int32)
+    refs = np.zeros(16, np.int32)
+    refs[:3] = 1
+    lens = np.array([4, -3, 5, 4, 4], np.int32)              # negative; a position without a page; a page id past the pool
+    pos = np.array([0, 8, 9, 10, 11, 12], np.int32)
+    cache, ws, K, _ = pages_cache(table, refs, ps)
+    added = wf.wf_pages_reserve(cache, dev(pos), dev(lens), ws)
+    torch.cuda.synchronize()
+    code, info = ws.device_error()
+    assert code == BAD and info in (1, 2, 3)
+    assert np.array_equal(host(added), [1, -1, -1, -1, 0])
+    t = table.copy()
+    t[0, 1] = 3
+    assert np.array_equal(host(cache.table), t)
+    assert np.array_equal(host(cache.ref), [1, 1, 1, 1] + [0] * 12) and torch.equal(cache.K, K)
+
+
+@pytest.mark.parametrize("seed", [1, 2])
+def test_fork_and_trim(seed):
+    ps, B, width = 8, 12, 6
+    rng = np.random.default_rng(seed)
+    table, refs, lens = random_pages(rng, 6, width, ps, 60, 0.3)
+    table = np.concatenate([table, np.full((6, width), -1, np.int32)])
+    lens = np.concatenate([lens, np.zeros(6, np.int32)]).astype(np.int32)
+    cache, ws, K, V = pages_cache(table, refs, ps)
+    # good forks; then: twice the same destination, an index out of range, a
+    # destination in use, a destination that is a source
+    src = np.array([0, 0, 3, 1, 1, 2, 4, 12, 5], np.int32)
+    dst = np.array([6, 7, 8, 9, 9, 13, 1, 10, 3], np.int32)
+    ln = dev(lens)
+    wf.wf_pages_fork(cache, dev(src), dev(dst), ln, ws)
+    torch.cuda.synchronize()
+    t2, r2, l2, bad = ref.fork(table, refs, lens, src, dst, ps)
+    assert bad == [3, 4, 5, 6, 7, 8]
+    code, info = ws.device_error()
+    assert code == BAD and info in bad
+    assert np.array_equal(host(cache.table), t2) and np.array_equal(host(cache.ref), r2)
+    assert np.array_equal(host(ln), l2)
+    keep = l2.copy()
+    keep[[0, 7]] = 0
+    keep[3] = keep[3] // 2
+    keep[4] = -1                                             # left as it is
+    wf.wf_pages_trim(cache, dev(keep), ws)
+    torch.cuda.synchronize()
+    assert ws.device_error() == (BAD, 4)
+    t3, r3 = ref.trim(t2, r2, keep, ps)
+    assert np.array_equal(host(cache.table), t3) and np.array_equal(host(cache.ref), r3)
+    wf.wf_pages_trim(cache, dev(np.zeros(B, np.int32)), ws)  # everything back
+    torch.cuda.synchronize()
+    assert (host(cache.ref) == 0).all() and (host(cache.table) == -1).all()
+    assert torch.equal(cache.K, K) and torch.equal(cache.V, V)
+
+
+def test_trim_of_malformed_entries():
+    table = np.array([[0, 1, 77, -5], [2, 3, -1, -1]], np.int32)
+    refs = np.array([1, 0, 1, 1, 0], np.int32)               # page 1 is held by nobody
+    cache, ws, _, _ = pages_cache(table, refs, 8)
+    wf.wf_pages_trim(cache, dev(np.array([0, 8], np.int32)), ws)
+    torch.cuda.synchronize()
+    assert ws.device_error() == (BAD, 0)
+    assert np.array_equal(host(cache.table), [[-1] * 4, [2, -1, -1, -1]])
+    assert np.array_equal(host(cache.ref), [0, 0, 1, 0, 0])
