@@ -230,22 +230,31 @@ __global__ void __launch_bounds__(PA_THREADS) paged_attend_kernel(const PagedAtt
     // goes to s_off[n & 1] one barrier before the copies are issued.
     const int cpiece = tid % CPR, crow = tid / CPR;
     const bool cactive = cpiece * 16 < p.D * EB;
-    auto look_up = [&](int n) {
-        if (tid < PA_KT) {
-            int64_t off = -1;
+    // The page number is loaded before a tile is computed and used after it.
+    int up_page = 0, up_t = -1, up_g = 0;
+    auto look_up = [&]() {
+        up_t = -1;
+        if (pc.left > 0) {
             const int t = pc.kt * PA_KT + tid;
-            if (pc.left > 0 && !pc.w.bad && t < pc.w.T) {
-                const int page = p.table[(int64_t)pc.b * p.max_pages + (t >> p.page_shift)];
-                if (page < 0 || page >= p.num_pages) {
-                    s_badpage[n & 7] = n;
-                } else {
-                    const int64_t row = ((int64_t)page << p.page_shift) + (t & ((1 << p.page_shift) - 1));
-                    off = (row * p.G + pc.item % p.G) * p.D;
-                }
+            if (tid < PA_KT && !pc.w.bad && t < pc.w.T) {
+                up_t = t;
+                up_g = pc.item % p.G;
+                up_page = p.table[(int64_t)pc.b * p.max_pages + (t >> p.page_shift)];
             }
-            s_off[n & 1][tid] = off;
+            cursor_next(p, pc);
         }
-        if (pc.left > 0) cursor_next(p, pc);
+    };
+    auto put_off = [&](int n) {
+        int64_t off = -1;
+        if (up_t >= 0) {
+            if (up_page < 0 || up_page >= p.num_pages) {
+                s_badpage[n & 7] = n;
+            } else {
+                const int64_t row = ((int64_t)up_page << p.page_shift) + (up_t & ((1 << p.page_shift) - 1));
+                off = (row * p.G + up_g) * p.D;
+            }
+        }
+        if (tid < PA_KT) s_off[n & 1][tid] = off;
     };
     // Copies of tile n (cursor ic); positions past the end are written as zeros.
     // A stretch's first tile and every item's first tile bring the pairs' queries.
@@ -282,11 +291,13 @@ __global__ void __launch_bounds__(PA_THREADS) paged_attend_kernel(const PagedAtt
         pg_cp_commit();
     };
     for (int n = 0; n < PRE; ++n) {
-        look_up(n);
+        look_up();
+        put_off(n);
         __syncthreads();
         issue(n);
     }
-    look_up(PRE);
+    look_up();
+    put_off(PRE);
 
     // ------------------------------------------------ compute
     uint32_t qa[NKS][4];
@@ -299,7 +310,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_attend_kernel(const PagedAtt
         pg_cp_wait<PRE - 1>();
         __syncthreads();   // tile n has landed; its predecessor is consumed; the next offsets are there
         issue(n + PRE);
-        look_up(n + PRE + 1);
+        look_up();
 
         const int stage = n % S::STAGES;
         const uint8_t* st = smem + stage * S::STAGE;
@@ -521,6 +532,7 @@ __global__ void __launch_bounds__(PA_THREADS) paged_attend_kernel(const PagedAtt
             }
             if (odd_value) s_odd = n;
         }
+        put_off(n + PRE + 1);
         const bool item_end = cc.kt + 1 == cc.w.nt;
         if (item_end || cc.left == 1) {
             // -------------------------------------------- the piece's result
@@ -691,8 +703,11 @@ static PaVariant pa_variant(int D, bool e4m3) {
                 : PaVariant{paged_attend_kernel<128, false>, PaShape<128, false>::SMEM};
 }
 
+wf_status launch_paged_token(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s);
+
 wf_status launch_paged_attention(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s) {
     if (a->P == 0) return WF_OK;
+    if (a->max_rows == 1) return launch_paged_token(c, a, ws, s);
     static std::mutex mu;
     static bool attr_set[64] = {false};
     static int ctas[64][6];   // CTAs an SM holds, per variant
