@@ -501,7 +501,7 @@ static wf_status check_paged(const wf_paged_cache* c, int H, int max_rows, bool 
     if (pages && !c->ref) return WF_ERR_INVALID_ARG;
     WF_TRY(check_ws(ws, ws_bytes, paged_workspace_bytes(c->B, H, c->G, c->D, max_rows)));
     WF_TRY(check_device());
-    return check_local({c->K, c->V, c->table, pages ? c->ref : nullptr, ws});
+    return check_local({c->K, c->V});
 }
 
 wf_status wf_paged_append(const wf_paged_cache* c, int layer, const uint16_t* k, int64_t k_stride, const uint16_t* v,
@@ -512,7 +512,6 @@ wf_status wf_paged_append(const wf_paged_cache* c, int layer, const uint16_t* k,
     if (k_stride < row || k_stride % 8 || v_stride < row || v_stride % 8 || !aligned16(k) || !aligned16(v))
         return WF_ERR_INVALID_ARG;
     WF_TRY(check_paged(c, c->G, 1, false, ws, ws_bytes));
-    WF_TRY(check_local({k, v}));
     return launch_paged_append(c, layer, k, k_stride, v, v_stride, P, pos_off, cache_len, ws, stream);
 }
 
@@ -524,7 +523,6 @@ wf_status wf_paged_attention(const wf_paged_cache* c, const wf_paged_attn_args* 
     if (!aligned16(a->q) || !aligned16(a->out) || a->q_stride % 8 || a->q_stride < (int64_t)a->H * c->D)
         return WF_ERR_INVALID_ARG;
     WF_TRY(check_paged(c, a->H, a->max_rows, false, ws, ws_bytes));
-    WF_TRY(check_local({a->q, a->out}));
     return launch_paged_attention(c, a, ws, stream);
 }
 

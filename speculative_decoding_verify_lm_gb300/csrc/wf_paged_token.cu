@@ -118,6 +118,14 @@ __device__ __forceinline__ void cp_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
+// Counts an arrival: what the CTA wrote before its last barrier is visible to
+// whoever counts later, and what others wrote before theirs to this CTA's
+// threads behind its next barrier.
+__device__ __forceinline__ uint32_t arrive_acq_rel(uint32_t* cnt) {
+    uint32_t old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(cnt) : "memory");
+    return old;
+}
 // b16 8 x 8 transpose between the lanes of a warp
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     uint32_t r;
@@ -138,7 +146,6 @@ struct TokenShape {
     static constexpr int PER_SM = DP > 64 && NH == 2 ? 1 : 2;
     static constexpr int STAGES = PER_SM == 2 ? 3 : 6;
     static constexpr int SMEM = 128 + STAGES * STAGE;
-    static constexpr int STATS = STAGE / (16 * 8);   // pieces whose statistics fit a stage
     static_assert(2 * HEADS * DP * 4 <= STAGE, "two warps' outputs fit a stage");
 };
 
@@ -591,64 +598,49 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
             if (tid < heads) p.stat[slot * 16 + tid] = row_stat(tid);
             const int64_t ts = begin + (count - left) - kt_first;   // the item's first tile in the flat sequence
             const int c0 = (int)(ts / per), pieces = (int)((ts + c.w.nt - 1) / per) - c0 + 1;
-            __threadfence();
             consumer_sync();
-            if (tid == 0) s_last = atomicAdd(p.cnt + c0, 1u) == (uint32_t)(pieces - 1);
+            if (tid == 0) s_last = arrive_acq_rel(p.cnt + c0) == (uint32_t)(pieces - 1);
             consumer_sync();
             if (s_last) {
-                __threadfence();
-                // piece i is CTA c0 + i's: its second slot for the item's first, else its first
-                float2* st = reinterpret_cast<float2*>(red);   // statistics of up to STATS pieces, then their weights
-                float run_M[4], run_L[4];                      // of this thread's pairs
-                float2 acc[4];
-                // at most 16 heads x 64 pairs of dims = 8 per thread: two rounds of four
-                for (int base = 0; base < heads * half; base += 4 * PT_CONSUMERS) {
+                // piece k is CTA c0 + k's: its second slot for the item's first, else its
+                // first.  A thread takes four dims of a head; sixteen pieces' statistics
+                // and outputs are in flight together and added in order.
+                constexpr int BATCH = 16;
+                const int quarter = p.D / 4;
+                for (int i = tid; i < heads * quarter; i += PT_CONSUMERS) {
+                    const int h = i / quarter, d = (i - h * quarter) * 4;
+                    float M = -INFINITY, L = 0.f;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                    for (int q0 = 0; q0 < pieces; q0 += BATCH) {
+                        float2 s2[BATCH];
+                        float4 x[BATCH];
 #pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        run_M[u] = -INFINITY;
-                        run_L[u] = 0.f;
-                        acc[u] = make_float2(0.f, 0.f);
-                    }
-                    for (int q0 = 0; q0 < pieces; q0 += S::STATS) {
-                        const int nq = min(S::STATS, pieces - q0);
-                        consumer_sync();
-                        for (int i = tid; i < nq * heads; i += PT_CONSUMERS) {
-                            const int k = q0 + i / heads, h = i % heads;
-                            st[(i / heads) * 16 + h] = __ldcg(&p.stat[((c0 + k) * 2 + (k == 0)) * 16 + h]);
+                        for (int k = 0; k < BATCH; ++k) {
+                            const int at = ((c0 + q0 + k) * 2 + (q0 + k == 0)) * 16 + h;
+                            const bool in = q0 + k < pieces;
+                            s2[k] = in ? __ldcg(&p.stat[at]) : make_float2(-INFINITY, 0.f);
+                            x[k] = in ? __ldcg(reinterpret_cast<const float4*>(p.part + (int64_t)at * p.D + d))
+                                      : make_float4(0.f, 0.f, 0.f, 0.f);
                         }
-                        consumer_sync();
+                        float top = M;
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) {
-                            const int i = base + u * PT_CONSUMERS + tid;
-                            if (i >= heads * half) continue;
-                            const int h = i / half, d = (i - h * half) * 2;
-                            float M = run_M[u];
-                            for (int k = 0; k < nq; ++k) M = fmaxf(M, st[k * 16 + h].x);
-                            const float a = run_M[u] == -INFINITY ? 0.f : ex2_approx(run_M[u] - M);
-                            run_L[u] *= a;
-                            acc[u].x *= a;
-                            acc[u].y *= a;
-                            run_M[u] = M;
-                            const float* src = p.part + ((int64_t)(c0 + q0) * 2 * 16 + h) * p.D + d;
-#pragma unroll 8
-                            for (int k = 0; k < nq; ++k) {
-                                const float2 x = __ldcg(reinterpret_cast<const float2*>(
-                                    src + ((int64_t)k * 2 + (q0 + k == 0)) * 16 * p.D));
-                                const float2 s2 = st[k * 16 + h];
-                                const float w = s2.x == -INFINITY ? 0.f : ex2_approx(s2.x - M);
-                                run_L[u] = fmaf(s2.y, w, run_L[u]);
-                                acc[u].x = fmaf(x.x, w, acc[u].x);
-                                acc[u].y = fmaf(x.y, w, acc[u].y);
-                            }
+                        for (int k = 0; k < BATCH; ++k) top = fmaxf(top, s2[k].x);
+                        const float a = M == -INFINITY ? 0.f : ex2_approx(M - top);
+                        M = top;
+                        L *= a;
+                        v = make_float4(v.x * a, v.y * a, v.z * a, v.w * a);
+#pragma unroll
+                        for (int k = 0; k < BATCH; ++k) {
+                            const float w = s2[k].x == -INFINITY ? 0.f : ex2_approx(s2[k].x - top);
+                            L = fmaf(s2[k].y, w, L);
+                            v.x = fmaf(x[k].x, w, v.x);
+                            v.y = fmaf(x[k].y, w, v.y);
+                            v.z = fmaf(x[k].z, w, v.z);
+                            v.w = fmaf(x[k].w, w, v.w);
                         }
                     }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        const int i = base + u * PT_CONSUMERS + tid;
-                        if (i >= heads * half) continue;
-                        const int h = i / half, d = (i - h * half) * 2;
-                        write(h, d, acc[u], make_float2(run_M[u], run_L[u]));
-                    }
+                    write(h, d, make_float2(v.x, v.y), make_float2(M, L));
+                    write(h, d + 2, make_float2(v.z, v.w), make_float2(M, L));
                 }
                 if (tid == 0) p.cnt[c0] = 0;
             }
@@ -737,7 +729,7 @@ wf_status launch_paged_token(const wf_paged_cache* c, const wf_paged_attn_args* 
     while ((1 << p.page_shift) < c->page_size) ++p.page_shift;
     p.num_pages = c->num_pages;
     p.max_pages = c->max_pages;
-    p.min_tiles = 2;
+    p.min_tiles = 3;
     p.ctrl = static_cast<Control*>(ws);
     p.timeout_ns = wait_timeout_ns();
     const int vi = (e4m3 ? 1 : 0) | (p.hq > 8 ? 2 : 0) | (c->D > 64 ? 4 : 0);

@@ -190,9 +190,14 @@ _I32 = (torch.int32,)
 _F32 = (torch.float32,)
 
 
+_raw_stream = torch._C._cuda_getCurrentRawStream if hasattr(torch._C, "_cuda_getCurrentRawStream") else \
+    (lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+_device = torch.cuda.current_device
+
+
 def _stream(stream) -> int:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        return _raw_stream(_device())   # torch.cuda.current_stream().cuda_stream, without building the object
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
