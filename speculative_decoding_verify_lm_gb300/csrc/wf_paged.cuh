@@ -10,7 +10,9 @@ namespace wf {
 // control block | arrival counters (zero at rest) | page bookkeeping of a
 // reserve call | partial results of the attention's splits
 constexpr int PA_TILE_M = 16;       // (row, head) pairs of a small-tile item
-constexpr int PA_MAX_CTAS = 640;    // most CTAs of an attention launch
+constexpr int PA_MAX_CTAS = 640;    // most CTAs of a single-token launch
+constexpr int PA_MAX_ROUND_CTAS = 160;   // and of a launch over drafted rows
+constexpr int PA_ROUND_M = 256;     // pairs of an item there
 
 struct PagedLayout {
     size_t cnt, off, need, copies, stat, part, total;
@@ -20,8 +22,8 @@ struct PagedLayout {
 inline size_t paged_part_rows(int H, int G, int max_rows) {
     (void)H;
     (void)G;
-    (void)max_rows;
-    return (size_t)PA_MAX_CTAS * 2 * PA_TILE_M;
+    const size_t token = (size_t)PA_MAX_CTAS * 2 * PA_TILE_M, rounds = (size_t)PA_MAX_ROUND_CTAS * 2 * PA_ROUND_M;
+    return max_rows > 1 ? (rounds > token ? rounds : token) : token;
 }
 
 inline PagedLayout paged_layout(int B, int H, int G, int D, int max_rows) {

@@ -704,10 +704,12 @@ static PaVariant pa_variant(int D, bool e4m3) {
 }
 
 wf_status launch_paged_token(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s);
+wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s);
 
 wf_status launch_paged_attention(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s) {
     if (a->P == 0) return WF_OK;
     if (a->max_rows == 1) return launch_paged_token(c, a, ws, s);
+    if (c->kv_type == WF_KV_BF16) return launch_paged_rounds(c, a, ws, s);
     static std::mutex mu;
     static bool attr_set[64] = {false};
     static int ctas[64][6];   // CTAs an SM holds, per variant

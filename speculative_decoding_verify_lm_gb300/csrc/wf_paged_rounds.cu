@@ -1,0 +1,840 @@
+// Attention of a round's rows (drafted chains and trees) over a paged
+// key-value cache, on the tensor cores.
+//
+//   S = Q K^T,  P = e^(scale S - m) under the row's mask,  O = P V / sum P
+//
+// The (row, head) pairs of one KV head are the 128 rows of a product, so the
+// cache is read once for up to 256 pairs (a 60-node tree with four heads a
+// group).  Reading the cache and the products take about the same time on a
+// full batch: both have to run without a pause.
+//
+// The work is the flat sequence of 128-position tiles of every (sequence, 256
+// pairs, KV head), in equal stretches for one CTA an SM; pieces of an item that
+// several CTAs share are joined in order by the last of them to finish.
+//
+// Inside a CTA two streams of softmax warps (four each, a thread a row) work
+// in turn, so that the tensor cores compute one stream's products while the
+// other takes its exponentials:
+//   more than 128 pairs   stream w has pairs 128 w .., both see every tile
+//   128 pairs or fewer    both have the same pairs, stream w every second tile;
+//                         their results meet in shared memory
+// S and O live in tensor memory; P overwrites its S as the left operand of the
+// second product.  One warp copies pages (tensor copies of a page's rows into
+// the 128-byte swizzle), one issues the products.
+//
+// Tiles that reach the round's own rows take a mask of 128 bits per row.  There
+// a stored value that is not finite is set to zero before the product (0 * inf
+// would reach rows that do not see it) and added at the end to the rows that
+// do; rows past the sequence are zeroed as well.
+#include "wf_paged.cuh"
+
+#define PR_TRY(x)                      \
+    do {                               \
+        const wf_status _st = (x);     \
+        if (_st != WF_OK) return _st;  \
+    } while (0)
+
+namespace wf {
+
+constexpr int PR_THREADS = 320;    // two streams of four softmax warps, the copying and the issuing warp
+constexpr int PR_KT = 128;         // positions of a tile
+constexpr int PR_RING = 4;         // tiles of keys or values in flight
+constexpr int PR_ROWS = 128;       // pairs of a product
+constexpr float PR_LAG = 8.f;      // the running maximum may lag by 2^8
+
+struct RoundsParams {
+    const uint16_t* q;
+    int64_t q_stride;
+    const int32_t* pos_off;
+    const int32_t* cache_len;
+    const int32_t* node_off;
+    const int32_t* kind;
+    const int32_t* parent;
+    const int32_t* table;
+    const uint8_t* V;        // this layer's rows
+    uint16_t* out;
+    float* lse;
+    float* part;             // [CTA][2][256][D] unnormalised outputs
+    float2* stat;            // [CTA][2][256] (maximum, sum)
+    uint32_t* cnt;           // [CTA] arrivals of the item that begins in it, zero at rest
+    float qk;                // scale * log2(e)
+    int P, H, G, D, hq, B, page_shift, num_pages, max_pages, max_rows, min_tiles;
+    int box_rows;            // rows of a copy: min(page_size, 128)
+    uint32_t idesc_s, idesc_o;
+    Control* ctrl;
+    uint64_t timeout_ns;
+};
+
+struct RoundSeq {
+    int r0, rows, len, T, mp, nt;   // first row, rows, cached positions, all positions, 256s of pairs, tiles
+    bool bad;
+};
+
+__device__ __forceinline__ RoundSeq round_seq(const RoundsParams& p, int b) {
+    RoundSeq w;
+    w.r0 = p.pos_off[b];
+    const int r1 = p.pos_off[b + 1];
+    w.len = p.cache_len[b];
+    w.rows = r1 - w.r0;
+    w.T = w.mp = w.nt = 0;
+    w.bad = false;
+    if (w.r0 < 0 || r1 > p.P || r1 <= w.r0) {   // no row (or offsets that name no rows)
+        w.bad = w.r0 < 0 || r1 > p.P || r1 < w.r0;
+        w.rows = 0;
+        return w;
+    }
+    const int64_t T = (int64_t)w.len + w.rows;
+    w.bad = w.len < 0 || w.rows > p.max_rows || T > ((int64_t)p.max_pages << p.page_shift);
+    w.mp = (int)(((int64_t)w.rows * p.hq + 2 * PR_ROWS - 1) / (2 * PR_ROWS));
+    w.T = w.bad ? 0 : (int)T;
+    w.nt = w.bad ? 1 : (w.T + PR_KT - 1) / PR_KT;   // a bad sequence: one tile that writes NaN
+    return w;
+}
+
+// One piece of the CTA's stretch: tiles [kt, kt + tiles) of (sequence b, pairs 256 mp .., KV head g).
+struct Piece {
+    RoundSeq w;
+    int b, mp, g, kt, tiles, pairs;
+    bool solo;   // at most 128 pairs: the streams share them and take every second tile
+};
+
+__device__ __forceinline__ void piece_shape(const RoundsParams& p, Piece& x, int left) {
+    x.tiles = min(left, x.w.nt - x.kt);
+    x.pairs = min(2 * PR_ROWS, x.w.rows * p.hq - x.mp * 2 * PR_ROWS);
+    x.solo = x.pairs <= PR_ROWS;
+}
+
+// The piece behind this one; `left` tiles of the stretch remain (> 0).
+__device__ __forceinline__ void piece_next(const RoundsParams& p, Piece& x, int left) {
+    x.kt = 0;   // a piece ends at its item's end unless the stretch ends
+    if (++x.g == p.G) {
+        x.g = 0;
+        if (++x.mp == x.w.mp) {
+            x.mp = 0;
+            do {
+                ++x.b;
+                x.w = round_seq(p, x.b);
+            } while (x.w.mp == 0);
+        }
+    }
+    piece_shape(p, x, left);
+}
+
+// ----------------------------------------------------------------- tensor memory and barriers
+__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld_x16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// D (+)= A[tensor memory] B[shared memory]
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t b_desc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
+        : "memory");
+}
+// Operand whose contiguous dimension is the product's N (the values: rows of
+// 64 dims, 128 bytes, swizzled).  64-dim blocks lie 16 KB apart, groups of 8
+// positions 1,024 bytes.
+__device__ __forceinline__ uint64_t umma_desc_n_major(uint32_t smem_addr) {
+    uint64_t d = 0;
+    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
+    d |= (uint64_t)((PR_KT * 128) >> 4) << 16;   // from one 64-dim block to the next
+    d |= (uint64_t)(1024 >> 4) << 32;            // from 8 positions to the next
+    d |= (uint64_t)1 << 46;
+    d |= (uint64_t)2 << 61;
+    return d;
+}
+__device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void named_sync(int id, int threads) {
+    asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+__device__ __forceinline__ uint32_t round_arrive(uint32_t* cnt) {   // as for the single-token kernel
+    uint32_t old;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(cnt) : "memory");
+    return old;
+}
+
+// Shared memory: queries [2][blocks][128 rows][128 B], ring [4][blocks][128 positions][128 B];
+// blocks = 64-dim blocks of a head.
+__host__ __device__ constexpr int rounds_smem(int blocks) { return 1024 + (2 + PR_RING) * blocks * PR_KT * 128; }
+
+// BLK: 64-dim blocks of a head (1 or 2)
+template <int BLK>
+__global__ void __launch_bounds__(PR_THREADS, 1)
+    paged_rounds_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                        const RoundsParams p) {
+    constexpr int TILE = BLK * PR_KT * 128;    // bytes of a tile of queries, keys or values
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* sQ = smem;
+    uint8_t* sR = smem + 2 * TILE;
+    __shared__ uint64_t kv_full[PR_RING], kv_empty[PR_RING], q_full[2], s_full[2], p_full[2], o_full[2], told[4];
+    __shared__ uint32_t tmem_slot;
+    __shared__ int abort_word, s_bad[4], s_odd[2][2], s_last, s_pb;
+    __shared__ int16_t s_par[2][WF_MAX_SEQ_NODES];
+    __shared__ float2 s_xst[PR_ROWS];
+    __shared__ int64_t s_plan, s_scan[PR_THREADS / 32];
+    volatile int* abort_flag = &abort_word;
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (tid == 0) {
+        for (int i = 0; i < PR_RING; ++i) {
+            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], PR_ROWS);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_full[i], PR_ROWS);
+            mbar_init(&o_full[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) mbar_init(&told[i], 1);
+        abort_word = 0;
+        s_odd[0][0] = s_odd[0][1] = s_odd[1][0] = s_odd[1][1] = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&tmK);
+        tma_prefetch_desc(&tmV);
+    }
+    if (warp == 8) {
+        tmem_alloc(&tmem_slot, 512);
+        tmem_relinquish();
+    }
+    pdl_wait();
+    pdl_trigger();
+
+    // ------------------------------------------------ this CTA's stretch (as in the single-token kernel)
+    const int run = (p.B + PR_THREADS - 1) / PR_THREADS;
+    int64_t mine = 0;
+    for (int i = 0; i < run; ++i) {
+        const int b = tid * run + i;
+        if (b < p.B) {
+            const RoundSeq w = round_seq(p, b);
+            mine += (int64_t)w.mp * p.G * w.nt;
+            if (w.bad && blockIdx.x == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)b);
+        }
+    }
+    int64_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+    }
+    if (lane == 31) s_scan[warp] = inc;
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_slot;
+    int64_t total = 0, before = inc - mine;
+#pragma unroll
+    for (int w = 0; w < PR_THREADS / 32; ++w) {
+        if (w < warp) before += s_scan[w];
+        total += s_scan[w];
+    }
+    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    if (per < p.min_tiles) per = p.min_tiles;
+    const int64_t begin = (int64_t)blockIdx.x * per;
+    const int64_t end = begin + per < total ? begin + per : total;
+    const int count = begin < end ? (int)(end - begin) : 0;
+    if (count > 0 && mine > 0 && before <= begin && begin < before + mine) {
+        int64_t at = before;
+        int b = tid * run;
+        for (;; ++b) {
+            const RoundSeq w = round_seq(p, b);
+            const int64_t n = (int64_t)w.mp * p.G * w.nt;
+            if (begin < at + n) break;
+            at += n;
+        }
+        s_plan = begin - at;
+        s_pb = b;
+    }
+    __syncthreads();
+    Piece x;
+    if (count > 0) {
+        x.b = s_pb;
+        x.w = round_seq(p, x.b);
+        const int item = (int)(s_plan / x.w.nt);
+        x.kt = (int)(s_plan - (int64_t)item * x.w.nt);
+        x.mp = item / p.G;
+        x.g = item - x.mp * p.G;
+        piece_shape(p, x, count);
+    }
+
+    if (warp >= 8) {
+        if (warp == 8) {
+            // ---------------------------------------- copies: tile n's keys to ring place 2 n, its values to 2 n + 1
+            const uint64_t pol = policy_evict_first();
+            const int per_tile = PR_KT / p.box_rows;   // boxes of a tile: at most 16
+            int n = 0, k = 0;                          // tiles, pieces that have any
+            for (int left = count; left > 0;) {
+                bool bad = false;
+                if (!x.w.bad) {
+                    int page = 0;
+                    auto look_up = [&](int kt) {
+                        const int t = kt * PR_KT + lane * p.box_rows;
+                        page = lane < per_tile && t < x.w.T
+                                   ? p.table[(int64_t)x.b * p.max_pages + (t >> p.page_shift)]
+                                   : -2;
+                    };
+                    look_up(x.kt);
+                    for (int i = 0; i < x.tiles; ++i, ++n) {
+                        const int t = (x.kt + i) * PR_KT + lane * p.box_rows;
+                        const bool ok = page >= 0 && page < p.num_pages;
+                        bad |= page != -2 && !ok;
+                        const int y = ok ? (page << p.page_shift) + (t & ((1 << p.page_shift) - 1)) : 0;
+                        const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xffffffffu, ok));
+                        if (i + 1 < x.tiles) look_up(x.kt + i + 1);
+                        bool alive = true;
+#pragma unroll
+                        for (int kv = 0; kv < 2; ++kv) {
+                            const int at = 2 * n + kv, slot = at % PR_RING;
+                            alive = alive && (at < PR_RING || mbar_wait(&kv_empty[slot], ((at / PR_RING) & 1) ^ 1,
+                                                                       p.timeout_ns, abort_flag));
+                            if (!alive) break;
+                            if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], boxes * BLK * p.box_rows * 128);
+                            __syncwarp();
+                            if (ok) {
+                                uint8_t* dst = sR + slot * TILE + lane * p.box_rows * 128;
+#pragma unroll
+                                for (int blk = 0; blk < BLK; ++blk)
+                                    tma_load_2d(dst + blk * PR_KT * 128, kv ? &tmV : &tmK, &kv_full[slot],
+                                                x.g * p.D + blk * 64, y, pol);
+                            }
+                        }
+                        if (!alive) {
+                            *abort_flag = 1;
+                            if (lane == 0) record_error(p.ctrl, WF_ERR_TIMEOUT, 0x800u);
+                            break;
+                        }
+                    }
+                }
+                if (!x.w.bad) {   // whether the piece had a position without a page
+                    bad = __any_sync(0xffffffffu, bad);
+                    if (lane == 0) {
+                        s_bad[k & 3] = bad;
+                        mbar_arrive(&told[k & 3]);
+                    }
+                    ++k;
+                }
+                if (*abort_flag) break;
+                left -= x.tiles;
+                if (left > 0) piece_next(p, x, left);
+            }
+            // let every copy issued land before the shared memory goes
+            for (int at = max(0, 2 * n - PR_RING); at < 2 * n; ++at)
+                mbar_wait(&kv_full[at % PR_RING], (at / PR_RING) & 1, p.timeout_ns, nullptr);
+        } else if (warp == 9 && lane == 0) {
+            // ---------------------------------------- products
+            int n = 0;                                 // tiles before this piece
+            uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};   // queries and probabilities taken, by stream
+            bool ok = true;
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                ok = ok && mbar_wait(bar, parity, p.timeout_ns, abort_flag);
+            };
+            for (int left = count; left > 0 && ok;) {
+                if (!x.w.bad) {
+                    const int steps = x.solo ? (x.tiles + 1) / 2 : x.tiles;
+                    auto tile_of = [&](int i, int w) { return x.solo ? 2 * i + w : i; };
+                    auto scores = [&](int i, int w) {   // S of stream w's step i
+                        const int at = 2 * (n + tile_of(i, w)), slot = at % PR_RING;
+                        wait(&kv_full[slot], (at / PR_RING) & 1);
+                        if (!ok) return;
+                        tc_fence_after();
+                        const uint32_t a = smem_u32(sQ + (x.solo ? 0 : w) * TILE), b = smem_u32(sR + slot * TILE);
+                        for (int ks = 0; ks < p.D / 16; ++ks) {
+                            const uint32_t off = (uint32_t)((ks >> 2) * PR_KT * 128 + (ks & 3) * 32);
+                            umma_bf16(tmem + w * 128, umma_desc_sw128(a + off), umma_desc_sw128(b + off), p.idesc_s,
+                                      ks != 0);
+                        }
+                        umma_commit(&s_full[w]);
+                        if (x.solo || w == 1) umma_commit(&kv_empty[slot]);
+                    };
+                    for (int w = 0; w < (x.solo ? 1 : 2); ++w) wait(&q_full[w], qn[w]++ & 1);
+                    for (int w = 0; w < 2 && ok; ++w)
+                        if (tile_of(0, w) < x.tiles) scores(0, w);
+                    for (int i = 0; i < steps && ok; ++i)
+                        for (int w = 0; w < 2 && ok; ++w) {
+                            const int j = tile_of(i, w);
+                            if (j >= x.tiles) continue;
+                            const int at = 2 * (n + j) + 1, slot = at % PR_RING;
+                            wait(&kv_full[slot], (at / PR_RING) & 1);
+                            wait(&p_full[w], pn[w]++ & 1);
+                            if (!ok) break;
+                            tc_fence_after();
+                            const uint32_t b = smem_u32(sR + slot * TILE);
+                            for (int ks = 0; ks < PR_KT / 16; ++ks)
+                                umma_ts(tmem + 256 + w * 128, tmem + w * 128 + ks * 8, umma_desc_n_major(b + ks * 2048),
+                                        p.idesc_o, (i | ks) != 0);
+                            if (x.solo || w == 1) umma_commit(&kv_empty[slot]);
+                            if (tile_of(i + 1, w) >= x.tiles) umma_commit(&o_full[w]);   // the stream's last
+                            else scores(i + 1, w);
+                        }
+                    n += x.tiles;
+                }
+                left -= x.tiles;
+                if (left > 0) piece_next(p, x, left);
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                record_error(p.ctrl, WF_ERR_TIMEOUT, 0x810u);
+            }
+        }
+    } else {
+        // -------------------------------------------- softmax: stream w, thread = row of the product
+        const int w = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tmem + lanes + w * 128, tO = tmem + lanes + 256 + w * 128;
+        uint32_t sn = 0, on = 0;   // scores, outputs taken
+        int n = 0, k = 0;          // tiles before this piece, pieces that have any
+        int turn = 0;              // pieces
+        bool ok = true;
+        auto wait = [&](uint64_t* bar, uint32_t parity) {
+            if (ok && !mbar_wait(bar, parity, p.timeout_ns, abort_flag)) {
+                ok = false;
+                *abort_flag = 1;
+                record_error(p.ctrl, WF_ERR_TIMEOUT, 0x820u);
+            }
+        };
+        for (int left = count; left > 0; ++turn) {
+            const int m0 = x.mp * 2 * PR_ROWS + (x.solo ? 0 : w * PR_ROWS);   // first pair of this stream
+            const int pair = m0 + row;
+            const int r = pair / p.hq, h = pair - r * p.hq;
+            const bool live = r < x.w.rows;
+            const bool warp_live = (m0 + (row & ~31)) / p.hq < x.w.rows;
+            float m = -INFINITY, l = 0.f;
+            int* odd_word = &s_odd[turn & 1][w];
+            bool bad = x.w.bad, tree = false;
+            const int mine_tiles = x.solo ? (x.tiles - w + 1) / 2 : x.tiles;   // tiles of this stream
+            if (!x.w.bad) {
+                // queries into the 128-byte swizzle; rows past the pairs are zero
+                if (w == 0 || !x.solo) {
+                    const int per_row = p.D / 8;
+                    uint8_t* dst = sQ + w * TILE;
+                    for (int base = 0; base < PR_ROWS * per_row; base += 8 * 128) {
+                        uint4 v[8];
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const int i = base + u * 128 + row;
+                            const int mr = i / per_row, c = i - mr * per_row;
+                            const int qr = (m0 + mr) / p.hq, qh = (m0 + mr) - qr * p.hq;
+                            v[u] = make_uint4(0, 0, 0, 0);
+                            if (mr < PR_ROWS && qr < x.w.rows)
+                                v[u] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(x.w.r0 + qr) * p.q_stride +
+                                                                       (x.g * p.hq + qh) * p.D + c * 8);
+                        }
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            const int i = base + u * 128 + row;
+                            const int mr = i / per_row, c = i - mr * per_row;
+                            if (mr < PR_ROWS)
+                                *reinterpret_cast<uint4*>(dst + (c >> 3) * PR_KT * 128 + mr * 128 +
+                                                          (((c & 7) ^ (mr & 7)) << 4)) = v[u];
+                        }
+                    }
+                    fence_async_smem();
+                    mbar_arrive(&q_full[w]);
+                }
+                // what the streams learn of the piece: bit 0, a value under a mask is not
+                // finite; bit 1, the tree is malformed
+                if ((x.kt + x.tiles) * PR_KT > x.w.len) {
+                    const int kd = p.kind ? p.kind[x.b] : 1;
+                    tree = p.parent != nullptr && kd != 0;
+                    if (tree) {
+                        const int n0 = p.node_off[x.b], nn = p.node_off[x.b + 1] - n0;
+                        bool off = n0 < 0 || nn != x.w.rows - 1;
+                        if (off) tree = false;
+                        else
+                            for (int a = row; a < nn; a += 128) {
+                                const int pi = p.parent[n0 + a];
+                                const bool wrong = pi < -1 || pi >= a;
+                                s_par[w][a] = (int16_t)(wrong ? -1 : pi);
+                                off |= wrong;
+                            }
+                        if (off) atomicOr(odd_word, 2);
+                    }
+                    named_sync(1 + w, 128);
+                }
+                for (int i = 0; i < mine_tiles; ++i) {
+                    const int j = x.solo ? 2 * i + w : i;
+                    const int t0 = (x.kt + j) * PR_KT;
+                    const bool masked = t0 + PR_KT > x.w.len;
+                    const bool clean = masked && (x.solo || w == 0);
+                    if (clean && t0 + row >= x.w.len) {
+                        // one position's values a thread: zero past the end, and where not finite
+                        const int at = 2 * (n + j) + 1, slot = at % PR_RING;
+                        wait(&kv_full[slot], (at / PR_RING) & 1);
+                        const bool past = t0 + row >= x.w.T;
+                        bool odd = false;
+                        for (int c = 0; c < p.D / 8; ++c) {
+                            uint4* v = reinterpret_cast<uint4*>(sR + slot * TILE + (c >> 3) * PR_KT * 128 + row * 128 +
+                                                                (((c & 7) ^ (row & 7)) << 4));
+                            if (past) {
+                                *v = make_uint4(0, 0, 0, 0);
+                                continue;
+                            }
+                            uint4 y = *v;
+                            uint32_t* e = &y.x;
+                            bool hit = false;
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                if ((e[u] & 0x7F80u) == 0x7F80u) e[u] &= 0xFFFF0000u, hit = true;
+                                if ((e[u] & 0x7F800000u) == 0x7F800000u) e[u] &= 0x0000FFFFu, hit = true;
+                            }
+                            if (hit) *v = y;
+                            odd |= hit;
+                        }
+                        if (odd) atomicOr(odd_word, 1);
+                        fence_async_smem();
+                    }
+                    wait(&s_full[w], sn++ & 1);
+                    tc_fence_after();
+                    if (warp_live && __all_sync(0xffffffffu, ok)) {
+                        uint32_t see[4];   // the positions that the row sees
+                        if (masked) {
+                            // all below `upto`, then the row's ancestors
+                            const int upto = (tree ? x.w.len : x.w.len + r + 1) - t0;
+#pragma unroll
+                            for (int c = 0; c < 4; ++c) {
+                                const int u = upto - 32 * c;
+                                see[c] = u <= 0 ? 0u : (u >= 32 ? 0xFFFFFFFFu : (1u << u) - 1u);
+                            }
+                            if (tree && live) {
+                                int a = r;
+                                while (true) {
+                                    const int t = x.w.len + a - t0;
+#pragma unroll
+                                    for (int c = 0; c < 4; ++c)
+                                        if (t >= 32 * c && t < 32 * c + 32) see[c] |= 1u << (t & 31);
+                                    if (a == 0) break;
+                                    a = 1 + s_par[w][a - 1];
+                                }
+                            }
+                            __syncwarp();
+                        }
+                        // 64 scores in registers at a time: the upper half first, for its
+                        // maximum alone; the lower half stays for its exponentials (whose
+                        // place in tensor memory is the lower half's), then the upper again
+                        uint32_t s[2][32];
+                        auto fetch = [&](int c0) {
+                            tmem_ld_32x32b_x32(tS + c0 * 32, s[0]);
+                            tmem_ld_32x32b_x32(tS + c0 * 32 + 32, s[1]);
+                            tmem_ld_wait();
+                            if (masked) {
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                    for (int e = 0; e < 32; ++e)
+                                        if (!(see[c0 + c] >> e & 1u)) s[c][e] = 0xFF800000u;
+                            }
+                        };
+                        auto largest = [&]() {
+                            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                for (int e = 0; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[c][e]));
+                            return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+                        };
+                        fetch(2);
+                        const float upper = largest();
+                        fetch(0);
+                        const float mx = fmaxf(upper, largest()) * p.qk;
+                        if (__any_sync(0xffffffffu, mx > m + PR_LAG)) {
+                            const float mn = fmaxf(m, mx);
+                            const float a = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+                            m = mn;
+                            l *= a;
+                            if (i > 0)   // every earlier product into O has completed before this tile's scores
+                                for (int c = 0; c < p.D; c += 16) {
+                                    uint32_t y[16];
+                                    tmem_ld_x16(tO + c, y);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * a);
+                                    tmem_st_x16(tO + c, y);
+                                }
+                        }
+                        const float base = m == -INFINITY ? 0.f : -m;
+                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+                        auto weigh = [&](int c0) {
+#pragma unroll
+                            for (int c = 0; c < 2; ++c) {
+                                uint32_t pk[16];
+#pragma unroll
+                                for (int e = 0; e < 16; ++e) {
+                                    const float p0 = ex2_approx(fmaf(__uint_as_float(s[c][2 * e]), p.qk, base));
+                                    const float p1 = ex2_approx(fmaf(__uint_as_float(s[c][2 * e + 1]), p.qk, base));
+                                    sum[e & 3] += p0 + p1;
+                                    pk[e] = cvt_bf16x2(p0, p1);
+                                }
+                                tmem_st_x16(tS + (c0 + c) * 16, pk);
+                            }
+                        };
+                        weigh(0);
+                        fetch(2);
+                        weigh(2);
+                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        tmem_st_wait();
+                    }
+                    tc_fence_before();
+                    mbar_arrive(&p_full[w]);
+                }
+                if (mine_tiles > 0) {
+                    wait(&o_full[w], on++ & 1);
+                    tc_fence_after();
+                }
+            }
+            // ---------------------------------------- the piece's result
+            if (!x.w.bad) {
+                wait(&told[k & 3], (k >> 2) & 1);
+                bad |= s_bad[k & 3] != 0;
+                ++k;
+            }
+            const bool merge = x.solo && x.tiles > 1 && !x.w.bad;   // both streams hold parts of the same pairs
+            named_sync(3, 256);                                     // s_odd of both streams
+            const int learnt = s_odd[turn & 1][0] | s_odd[turn & 1][1];
+            if (row == 0) s_odd[(turn + 1) & 1][w] = 0;             // read last before the previous piece's end
+            const bool odd = learnt & 1;
+            bad |= (learnt & 2) != 0;
+            const bool whole = x.tiles == x.w.nt;
+            const int slot = (int)blockIdx.x * 2 + (x.kt == 0 ? 1 : 0);
+            const int prow = (x.solo ? 0 : w * PR_ROWS) + row;      // row of the partial area
+            const bool writer = !(x.solo && w == 1) && live;
+            float w0 = 1.f, w1 = 0.f, M = m, L = l;
+            if (merge) {
+                if (w == 1) s_xst[row] = make_float2(m, l);
+                named_sync(3, 256);
+                if (w == 0) {
+                    const float2 o1 = s_xst[row];
+                    M = fmaxf(m, o1.x);
+                    w0 = m == -INFINITY ? 0.f : ex2_approx(m - M);
+                    w1 = o1.x == -INFINITY ? 0.f : ex2_approx(o1.x - M);
+                    L = l * w0 + o1.y * w1;
+                }
+            }
+            if (bad) M = L = NAN;
+            const float inv = 1.f / L;
+            const int64_t out_pair = (int64_t)(x.w.r0 + r) * p.H + x.g * p.hq + h;
+            // values left out above, at the positions of this piece that the row sees
+            auto left_out = [&](int d) {
+                float sum = 0.f;
+                for (int j = 0; j <= r; ++j) {
+                    const int t = x.w.len + j;
+                    if (t < x.kt * PR_KT || t >= (x.kt + x.tiles) * PR_KT) continue;
+                    bool sees = !tree || j == 0 || j == r;
+                    for (int a = r; a > j && !sees;) {
+                        a = 1 + s_par[w][a - 1];
+                        sees = a == j;
+                    }
+                    const int page = p.table[(int64_t)x.b * p.max_pages + (t >> p.page_shift)];
+                    if (!sees || page < 0 || page >= p.num_pages) continue;
+                    const int64_t at = (((int64_t)page << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * p.G + x.g;
+                    const float v = pg_bf16_to_f32(reinterpret_cast<const uint16_t*>(p.V)[at * p.D + d]);
+                    if (!(fabsf(v) < INFINITY)) sum += v;
+                }
+                return sum;
+            };
+            constexpr int XC = BLK * 32;   // dims exchanged together: a row of the second stream's queries' place
+            for (int c0 = 0; c0 < p.D; c0 += XC) {
+                float* xb = reinterpret_cast<float*>(sQ + TILE);   // [128][XC]
+                if (merge) {
+                    if (c0 > 0) named_sync(3, 256);
+                    if (w == 1)
+                        for (int c = 0; c < XC && c0 + c < p.D; c += 16) {
+                            uint32_t y[16];
+                            tmem_ld_x16(tO + c0 + c, y);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                *reinterpret_cast<uint4*>(xb + row * XC + ((((c >> 2) + e) ^ (row & 7)) << 2)) =
+                                    make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                        }
+                    named_sync(3, 256);
+                }
+                for (int c = 0; c < XC && c0 + c < p.D; c += 16) {
+                    float v[16];
+                    if (!x.w.bad && mine_tiles > 0) {   // warp-uniform
+                        uint32_t y[16];
+                        tmem_ld_x16(tO + c0 + c, y);
+                        tmem_ld_wait();
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(y[e]) * w0;
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+                    }
+                    if (writer) {
+                        if (merge) {
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float4 y =
+                                    *reinterpret_cast<const float4*>(xb + row * XC + ((((c >> 2) + e) ^ (row & 7)) << 2));
+                                v[4 * e] = fmaf(y.x, w1, v[4 * e]);
+                                v[4 * e + 1] = fmaf(y.y, w1, v[4 * e + 1]);
+                                v[4 * e + 2] = fmaf(y.z, w1, v[4 * e + 2]);
+                                v[4 * e + 3] = fmaf(y.w, w1, v[4 * e + 3]);
+                            }
+                        }
+                        if (odd && !bad)
+                            for (int e = 0; e < 16; ++e) v[e] += left_out(c0 + c + e);
+                        if (whole) {
+                            uint32_t o[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) o[e] = cvt_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
+                            uint4* dst = reinterpret_cast<uint4*>(p.out + out_pair * p.D + c0 + c);
+                            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                        } else {
+                            float4* dst = reinterpret_cast<float4*>(
+                                p.part + ((int64_t)slot * 2 * PR_ROWS + prow) * p.D + c0 + c);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                        }
+                    }
+                    __syncwarp();
+                }
+            }
+            if (bad && row == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)x.b);
+            if (whole) {
+                if (writer && p.lse) p.lse[out_pair] = (M + __log2f(L)) * LN2;
+            } else {
+                if (writer) p.stat[slot * 2 * PR_ROWS + prow] = make_float2(M, L);
+                const int64_t ts = begin + (count - left) - x.kt;   // the item's first tile in the flat sequence
+                const int c0 = (int)(ts / per), pieces = (int)((ts + x.w.nt - 1) / per) - c0 + 1;
+                named_sync(3, 256);
+                if (tid == 0) s_last = round_arrive(p.cnt + c0) == (uint32_t)(pieces - 1);
+                named_sync(3, 256);
+                if (s_last) {
+                    // piece i is CTA c0 + i's: its second slot for the item's first, else its
+                    // first; four pieces' values in flight together, added in order
+                    const int quarter = p.D / 4;
+                    for (int i = tid; i < x.pairs * quarter; i += 256) {
+                        const int pr = i / quarter, d = (i - pr * quarter) * 4;
+                        float tM = -INFINITY, tL = 0.f;
+                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                        for (int q0 = 0; q0 < pieces; q0 += 4) {
+                            float2 st[4];
+                            float4 y[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const bool in = q0 + u < pieces;
+                                const int at = ((c0 + q0 + u) * 2 + (q0 + u == 0)) * 2 * PR_ROWS + pr;
+                                st[u] = in ? __ldcg(&p.stat[at]) : make_float2(-INFINITY, 0.f);
+                                y[u] = in ? __ldcg(reinterpret_cast<const float4*>(p.part + (int64_t)at * p.D + d))
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
+                            }
+                            float topm = tM;
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) topm = fmaxf(topm, st[u].x);
+                            const float a = tM == -INFINITY ? 0.f : ex2_approx(tM - topm);
+                            tM = topm;
+                            tL *= a;
+                            v = make_float4(v.x * a, v.y * a, v.z * a, v.w * a);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const float wt = st[u].x == -INFINITY ? 0.f : ex2_approx(st[u].x - topm);
+                                tL = fmaf(st[u].y, wt, tL);
+                                v.x = fmaf(y[u].x, wt, v.x);
+                                v.y = fmaf(y[u].y, wt, v.y);
+                                v.z = fmaf(y[u].z, wt, v.z);
+                                v.w = fmaf(y[u].w, wt, v.w);
+                            }
+                        }
+                        const int fp = x.mp * 2 * PR_ROWS + pr, fr = fp / p.hq, fh = fp - fr * p.hq;
+                        const int64_t o = (int64_t)(x.w.r0 + fr) * p.H + x.g * p.hq + fh;
+                        const float ti = 1.f / tL;
+                        *reinterpret_cast<uint2*>(p.out + o * p.D + d) =
+                            make_uint2(cvt_bf16x2(v.x * ti, v.y * ti), cvt_bf16x2(v.z * ti, v.w * ti));
+                        if (p.lse && d == 0) p.lse[o] = (tM + __log2f(tL)) * LN2;
+                    }
+                    if (tid == 0) p.cnt[c0] = 0;
+                }
+            }
+            if (!x.w.bad) n += x.tiles;
+            left -= x.tiles;
+            if (left > 0) {
+                named_sync(3, 256);   // s_odd, s_last and the exchanged rows are read to their end
+                piece_next(p, x, left);
+            }
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------ host side
+wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s) {
+    static std::mutex mu;
+    static bool attr_set[64] = {false};
+    PR_TRY(configure_once(mu, attr_set, [] {
+        return cudaFuncSetAttribute(paged_rounds_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    rounds_smem(1)) == cudaSuccess &&
+               cudaFuncSetAttribute(paged_rounds_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    rounds_smem(2)) == cudaSuccess;
+    }));
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    const PagedLayout L = paged_layout(c->B, a->H, c->G, c->D, a->max_rows);
+    const int64_t layer_bytes = (int64_t)c->num_pages * c->page_size * c->G * c->D * 2;
+    const uint8_t* K = static_cast<const uint8_t*>(c->K) + a->layer * layer_bytes;
+    RoundsParams p = {};
+    p.q = a->q;
+    p.q_stride = a->q_stride;
+    p.pos_off = a->pos_off;
+    p.cache_len = a->cache_len;
+    p.node_off = a->node_off;
+    p.kind = a->kind;
+    p.parent = a->parent;
+    p.table = c->table;
+    p.V = static_cast<const uint8_t*>(c->V) + a->layer * layer_bytes;
+    p.out = a->out;
+    p.lse = a->lse;
+    p.part = reinterpret_cast<float*>(w + L.part);
+    p.stat = reinterpret_cast<float2*>(w + L.stat);
+    p.cnt = reinterpret_cast<uint32_t*>(w + L.cnt);
+    p.qk = a->scale * LOG2E;
+    p.P = a->P;
+    p.H = a->H;
+    p.G = c->G;
+    p.D = c->D;
+    p.hq = a->H / c->G;
+    p.B = c->B;
+    while ((1 << p.page_shift) < c->page_size) ++p.page_shift;
+    p.num_pages = c->num_pages;
+    p.max_pages = c->max_pages;
+    p.max_rows = a->max_rows;
+    p.min_tiles = 1;
+    p.box_rows = c->page_size < PR_KT ? c->page_size : PR_KT;
+    p.idesc_s = umma_idesc_bf16(PR_ROWS, PR_KT);
+    p.idesc_o = umma_idesc_bf16(PR_ROWS, c->D) | (1u << 16);   // the values' contiguous dimension is N
+    p.ctrl = static_cast<Control*>(ws);
+    p.timeout_ns = wait_timeout_ns();
+    CUtensorMap tmK, tmV;
+    const uint64_t rows = (uint64_t)c->num_pages * c->page_size, cols = (uint64_t)c->G * c->D;
+    if (!make_map(&tmK, K, rows, cols, (uint32_t)p.box_rows) || !make_map(&tmV, p.V, rows, cols, (uint32_t)p.box_rows))
+        return WF_ERR_CUDA;
+    int grid = num_sms() < PA_MAX_ROUND_CTAS ? num_sms() : PA_MAX_ROUND_CTAS;
+    // no more CTAs than tiles that the bounds allow
+    const int64_t tiles = (int64_t)c->B * c->G * cdiv((int64_t)a->max_rows * p.hq, 2 * PR_ROWS) *
+                          cdiv((int64_t)c->max_pages * c->page_size, PR_KT);
+    if (tiles < grid) grid = (int)tiles;
+    if (c->D <= 64) return launch(paged_rounds_kernel<1>, dim3(grid), dim3(PR_THREADS), (size_t)rounds_smem(1), s, tmK, tmV, p);
+    return launch(paged_rounds_kernel<2>, dim3(grid), dim3(PR_THREADS), (size_t)rounds_smem(2), s, tmK, tmV, p);
+}
+
+}  // namespace wf
