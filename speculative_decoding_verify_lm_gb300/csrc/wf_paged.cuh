@@ -8,14 +8,14 @@ namespace wf {
 
 // ----------------------------------------------------------------- workspace
 // control block | arrival counters (zero at rest) | page bookkeeping of a
-// reserve call | partial results of the attention's splits
+// reserve call | shared items and partial results of the attention's splits
 constexpr int PA_TILE_M = 16;       // (row, head) pairs of a small-tile item
 constexpr int PA_MAX_CTAS = 640;    // most CTAs of a single-token launch
 constexpr int PA_MAX_ROUND_CTAS = 160;   // and of a launch over drafted rows
 constexpr int PA_ROUND_M = 256;     // pairs of an item there
 
 struct PagedLayout {
-    size_t cnt, off, need, copies, stat, part, total;
+    size_t cnt, off, need, copies, join, stat, part, total;
 };
 
 // rows of the attention's partial area: two partials of a tile for each CTA
@@ -38,6 +38,8 @@ inline PagedLayout paged_layout(int B, int H, int G, int D, int max_rows) {
     o = align_up(o + 4 * (size_t)B, 256);
     L.copies = o;
     o = align_up(o + 8 * (size_t)B, 256);
+    L.join = o;
+    o = align_up(o + 16 * (size_t)PA_MAX_ROUND_CTAS, 256);
     L.stat = o;
     o = align_up(o + 8 * rows, 256);
     L.part = o;

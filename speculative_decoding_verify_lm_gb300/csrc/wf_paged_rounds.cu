@@ -8,24 +8,28 @@
 // group).  Reading the cache and the products take about the same time on a
 // full batch: both have to run without a pause.
 //
-// The work is the flat sequence of 128-position tiles of every (sequence, 256
-// pairs, KV head), in equal stretches for one CTA an SM; pieces of an item that
-// several CTAs share are joined in order by the last of them to finish.
+// The work is the flat sequence of 128-position tiles of every (sequence, up to
+// 256 pairs, KV head), in equal stretches for one CTA an SM; the pieces of an
+// item that several CTAs share go to the workspace and a second, small kernel
+// joins them in order.
 //
 // Inside a CTA two streams of softmax warps (four each, a thread a row) work
 // in turn, so that the tensor cores compute one stream's products while the
 // other takes its exponentials:
-//   more than 128 pairs   stream w has pairs 128 w .., both see every tile
-//   128 pairs or fewer    both have the same pairs, stream w every second tile;
-//                         their results meet in shared memory
+//   two products of rows   each stream has one, both see every tile
+//   one                    both have it, stream w every second tile; their
+//                          results meet in shared memory
+// A product holds whole query rows: 128 / (heads a group) of them.
 // S and O live in tensor memory; P overwrites its S as the left operand of the
-// second product.  One warp copies pages (tensor copies of a page's rows into
-// the 128-byte swizzle), one issues the products.
+// second product.  One warp copies queries and pages (tensor copies into the
+// 128-byte swizzle), one issues the products.
 //
 // Tiles that reach the round's own rows take a mask of 128 bits per row.  There
 // a stored value that is not finite is set to zero before the product (0 * inf
 // would reach rows that do not see it) and added at the end to the rows that
 // do; rows past the sequence are zeroed as well.
+#include <cudaTypedefs.h>
+
 #include "wf_paged.cuh"
 
 #define PR_TRY(x)                      \
@@ -41,10 +45,10 @@ constexpr int PR_KT = 128;         // positions of a tile
 constexpr int PR_RING = 4;         // tiles of keys or values in flight
 constexpr int PR_ROWS = 128;       // pairs of a product
 constexpr float PR_LAG = 8.f;      // the running maximum may lag by 2^8
+constexpr int PR_XC = 32;          // dims that pass through shared memory together
+constexpr int PR_XBYTES = PR_ROWS * PR_XC * 4;
 
 struct RoundsParams {
-    const uint16_t* q;
-    int64_t q_stride;
     const int32_t* pos_off;
     const int32_t* cache_len;
     const int32_t* node_off;
@@ -54,11 +58,12 @@ struct RoundsParams {
     const uint8_t* V;        // this layer's rows
     uint16_t* out;
     float* lse;
-    float* part;             // [CTA][2][256][D] unnormalised outputs
+    float4* part;            // [CTA][2][D / 4][256] unnormalised outputs, four dims of a row together
     float2* stat;            // [CTA][2][256] (maximum, sum)
-    uint32_t* cnt;           // [CTA] arrivals of the item that begins in it, zero at rest
+    int4* join;              // [CTA] the shared item that begins in it: pieces, first row, pairs, KV head
     float qk;                // scale * log2(e)
     int P, H, G, D, hq, B, page_shift, num_pages, max_pages, max_rows, min_tiles;
+    int rpt;                 // query rows of a product: 128 / hq
     int box_rows;            // rows of a copy: min(page_size, 128)
     uint32_t idesc_s, idesc_o;
     Control* ctrl;
@@ -66,7 +71,7 @@ struct RoundsParams {
 };
 
 struct RoundSeq {
-    int r0, rows, len, T, mp, nt;   // first row, rows, cached positions, all positions, 256s of pairs, tiles
+    int r0, rows, len, T, mp, nt;   // first row, rows, cached positions, all positions, pairs of products, tiles
     bool bad;
 };
 
@@ -85,23 +90,23 @@ __device__ __forceinline__ RoundSeq round_seq(const RoundsParams& p, int b) {
     }
     const int64_t T = (int64_t)w.len + w.rows;
     w.bad = w.len < 0 || w.rows > p.max_rows || T > ((int64_t)p.max_pages << p.page_shift);
-    w.mp = (int)(((int64_t)w.rows * p.hq + 2 * PR_ROWS - 1) / (2 * PR_ROWS));
+    w.mp = (w.rows + 2 * p.rpt - 1) / (2 * p.rpt);
     w.T = w.bad ? 0 : (int)T;
     w.nt = w.bad ? 1 : (w.T + PR_KT - 1) / PR_KT;   // a bad sequence: one tile that writes NaN
     return w;
 }
 
-// One piece of the CTA's stretch: tiles [kt, kt + tiles) of (sequence b, pairs 256 mp .., KV head g).
+// One piece of the CTA's stretch: tiles [kt, kt + tiles) of (sequence b, query rows 2 rpt mp .., KV head g).
 struct Piece {
     RoundSeq w;
-    int b, mp, g, kt, tiles, pairs;
-    bool solo;   // at most 128 pairs: the streams share them and take every second tile
+    int b, mp, g, kt, tiles, rows;   // rows: query rows of the item
+    bool solo;   // one product: the streams share it and take every second tile
 };
 
 __device__ __forceinline__ void piece_shape(const RoundsParams& p, Piece& x, int left) {
     x.tiles = min(left, x.w.nt - x.kt);
-    x.pairs = min(2 * PR_ROWS, x.w.rows * p.hq - x.mp * 2 * PR_ROWS);
-    x.solo = x.pairs <= PR_ROWS;
+    x.rows = min(2 * p.rpt, x.w.rows - x.mp * 2 * p.rpt);
+    x.solo = x.rows <= p.rpt;
 }
 
 // The piece behind this one; `left` tiles of the stretch remain (> 0).
@@ -146,46 +151,52 @@ __device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a_tmem, uint64_t b_
         "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(acc)
         : "memory");
 }
-// Operand whose contiguous dimension is the product's N (the values: rows of
-// 64 dims, 128 bytes, swizzled).  64-dim blocks lie 16 KB apart, groups of 8
-// positions 1,024 bytes.
-__device__ __forceinline__ uint64_t umma_desc_n_major(uint32_t smem_addr) {
-    uint64_t d = 0;
-    d |= (uint64_t)((smem_addr >> 4) & 0x3FFFu);
-    d |= (uint64_t)((PR_KT * 128) >> 4) << 16;   // from one 64-dim block to the next
-    d |= (uint64_t)(1024 >> 4) << 32;            // from 8 positions to the next
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)2 << 61;
-    return d;
+// Matrix descriptors (128-byte swizzle): the low word, which holds the address
+// in 16-byte units, and the high word, the same for every operand.  The issuing
+// thread advances an operand by adding to the low word.
+// Queries, keys: rows of 64 dims (128 bytes), groups of 8 rows 1,024 bytes apart.
+__device__ __forceinline__ uint32_t desc_lo_rows(uint32_t smem_addr) { return (smem_addr >> 4) | (1u << 16); }
+// Values, whose contiguous dimension is the product's N: 64-dim blocks 16 KB
+// apart, groups of 8 positions 1,024 bytes.
+__device__ __forceinline__ uint32_t desc_lo_values(uint32_t smem_addr) {
+    return (smem_addr >> 4) | ((uint32_t)((PR_KT * 128) >> 4) << 16);
+}
+__device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
+    constexpr uint32_t HI = (1024u >> 4) | (1u << 14) | (2u << 29);
+    return ((uint64_t)HI << 32) | lo;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
-__device__ __forceinline__ uint32_t round_arrive(uint32_t* cnt) {   // as for the single-token kernel
-    uint32_t old;
-    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(cnt) : "memory");
-    return old;
+__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(smem_u32(smem_dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
+        : "memory");
 }
 
 // Shared memory: queries [2][blocks][128 rows][128 B], ring [4][blocks][128 positions][128 B];
-// blocks = 64-dim blocks of a head.
-__host__ __device__ constexpr int rounds_smem(int blocks) { return 1024 + (2 + PR_RING) * blocks * PR_KT * 128; }
+// exchanged rows [128][32] fp32; blocks = 64-dim blocks of a head.
+__host__ __device__ constexpr int rounds_smem(int blocks) {
+    return 1024 + (2 + PR_RING) * blocks * PR_KT * 128 + PR_XBYTES;
+}
 
 // BLK: 64-dim blocks of a head (1 or 2)
 template <int BLK>
 __global__ void __launch_bounds__(PR_THREADS, 1)
-    paged_rounds_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
-                        const RoundsParams p) {
+    paged_rounds_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
+                        const __grid_constant__ CUtensorMap tmV, const RoundsParams p) {
     constexpr int TILE = BLK * PR_KT * 128;    // bytes of a tile of queries, keys or values
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;
     uint8_t* sR = smem + 2 * TILE;
-    __shared__ uint64_t kv_full[PR_RING], kv_empty[PR_RING], q_full[2], s_full[2], p_full[2], o_full[2], told[4];
+    uint8_t* sX = sR + PR_RING * TILE;
+    __shared__ uint64_t kv_full[PR_RING], kv_empty[PR_RING], q_full, q_empty, s_full[2], p_full[2], o_full[2], told[4];
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_word, s_bad[4], s_odd[2][2], s_last, s_pb;
-    __shared__ int16_t s_par[2][WF_MAX_SEQ_NODES];
+    __shared__ int abort_word, s_bad[4], s_odd[2][2], s_pb;
+    __shared__ uint8_t s_par[2][WF_MAX_SEQ_NODES + 1];   // row of each row's parent, by stream (a row's own copy)
     __shared__ float2 s_xst[PR_ROWS];
     __shared__ int64_t s_plan, s_scan[PR_THREADS / 32];
     volatile int* abort_flag = &abort_word;
@@ -196,8 +207,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
         }
+        mbar_init(&q_full, 1);
+        mbar_init(&q_empty, 1);
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], PR_ROWS);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], PR_ROWS);
             mbar_init(&o_full[i], 1);
@@ -206,6 +218,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         abort_word = 0;
         s_odd[0][0] = s_odd[0][1] = s_odd[1][0] = s_odd[1][1] = 0;
         fence_barrier_init();
+        tma_prefetch_desc(&tmQ);
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
@@ -300,6 +313,19 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         bool alive = true;
 #pragma unroll
                         for (int kv = 0; kv < 2; ++kv) {
+                            if (kv == 1 && i == 0) {   // the piece's queries, behind its first keys
+                                alive = alive && (k == 0 || mbar_wait(&q_empty, (k & 1) ^ 1, p.timeout_ns, abort_flag));
+                                if (!alive) break;
+                                const int nq = x.solo ? 1 : 2;
+                                if (lane == 0) {
+                                    mbar_arrive_expect_tx(&q_full, (uint32_t)(nq * BLK * p.rpt * p.hq * 128));
+                                    for (int w = 0; w < nq; ++w)
+                                        for (int blk = 0; blk < BLK; ++blk)
+                                            tma_load_3d(sQ + w * TILE + blk * PR_KT * 128, &tmQ, &q_full, blk * 64,
+                                                        x.g * p.hq, x.w.r0 + (2 * x.mp + w) * p.rpt);
+                                }
+                                __syncwarp();
+                            }
                             const int at = 2 * n + kv, slot = at % PR_RING;
                             alive = alive && (at < PR_RING || mbar_wait(&kv_empty[slot], ((at / PR_RING) & 1) ^ 1,
                                                                        p.timeout_ns, abort_flag));
@@ -336,11 +362,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             // let every copy issued land before the shared memory goes
             for (int at = max(0, 2 * n - PR_RING); at < 2 * n; ++at)
                 mbar_wait(&kv_full[at % PR_RING], (at / PR_RING) & 1, p.timeout_ns, nullptr);
+            if (k > 0) mbar_wait(&q_full, (k & 1) ^ 1, p.timeout_ns, nullptr);
         } else if (warp == 9 && lane == 0) {
             // ---------------------------------------- products
             int n = 0;                                 // tiles before this piece
-            uint32_t qn[2] = {0, 0}, pn[2] = {0, 0};   // queries and probabilities taken, by stream
+            uint32_t qn = 0, pn[2] = {0, 0};           // queries, probabilities (by stream) taken
             bool ok = true;
+            const int nks = p.D / 16;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 ok = ok && mbar_wait(bar, parity, p.timeout_ns, abort_flag);
             };
@@ -353,16 +381,20 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         wait(&kv_full[slot], (at / PR_RING) & 1);
                         if (!ok) return;
                         tc_fence_after();
-                        const uint32_t a = smem_u32(sQ + (x.solo ? 0 : w) * TILE), b = smem_u32(sR + slot * TILE);
-                        for (int ks = 0; ks < p.D / 16; ++ks) {
-                            const uint32_t off = (uint32_t)((ks >> 2) * PR_KT * 128 + (ks & 3) * 32);
-                            umma_bf16(tmem + w * 128, umma_desc_sw128(a + off), umma_desc_sw128(b + off), p.idesc_s,
-                                      ks != 0);
-                        }
+                        const uint32_t a = desc_lo_rows(smem_u32(sQ + (x.solo ? 0 : w) * TILE));
+                        const uint32_t b = desc_lo_rows(smem_u32(sR + slot * TILE));
+#pragma unroll
+                        for (int ks = 0; ks < 4 * BLK; ++ks)
+                            if (ks < nks) {
+                                const uint32_t off = (uint32_t)((ks >> 2) * PR_KT * 8 + (ks & 3) * 2);
+                                umma_bf16(tmem + w * 128, desc_of(a + off), desc_of(b + off), p.idesc_s, ks != 0);
+                            }
                         umma_commit(&s_full[w]);
                         if (x.solo || w == 1) umma_commit(&kv_empty[slot]);
+                        // the piece's last scores: its queries may go
+                        if (tile_of(i, w) == x.tiles - 1 && (x.solo || w == 1)) umma_commit(&q_empty);
                     };
-                    for (int w = 0; w < (x.solo ? 1 : 2); ++w) wait(&q_full[w], qn[w]++ & 1);
+                    wait(&q_full, qn++ & 1);
                     for (int w = 0; w < 2 && ok; ++w)
                         if (tile_of(0, w) < x.tiles) scores(0, w);
                     for (int i = 0; i < steps && ok; ++i)
@@ -374,10 +406,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                             wait(&p_full[w], pn[w]++ & 1);
                             if (!ok) break;
                             tc_fence_after();
-                            const uint32_t b = smem_u32(sR + slot * TILE);
+                            const uint32_t b = desc_lo_values(smem_u32(sR + slot * TILE));
+#pragma unroll
                             for (int ks = 0; ks < PR_KT / 16; ++ks)
-                                umma_ts(tmem + 256 + w * 128, tmem + w * 128 + ks * 8, umma_desc_n_major(b + ks * 2048),
-                                        p.idesc_o, (i | ks) != 0);
+                                umma_ts(tmem + 256 + w * 128, tmem + w * 128 + ks * 8, desc_of(b + ks * 128), p.idesc_o,
+                                        (i | ks) != 0);
                             if (x.solo || w == 1) umma_commit(&kv_empty[slot]);
                             if (tile_of(i + 1, w) >= x.tiles) umma_commit(&o_full[w]);   // the stream's last
                             else scores(i + 1, w);
@@ -400,6 +433,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         uint32_t sn = 0, on = 0;   // scores, outputs taken
         int n = 0, k = 0;          // tiles before this piece, pieces that have any
         int turn = 0;              // pieces
+        bool shared_item = false;  // an item begins here and ends elsewhere
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
             if (ok && !mbar_wait(bar, parity, p.timeout_ns, abort_flag)) {
@@ -409,44 +443,15 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             }
         };
         for (int left = count; left > 0; ++turn) {
-            const int m0 = x.mp * 2 * PR_ROWS + (x.solo ? 0 : w * PR_ROWS);   // first pair of this stream
-            const int pair = m0 + row;
-            const int r = pair / p.hq, h = pair - r * p.hq;
-            const bool live = r < x.w.rows;
-            const bool warp_live = (m0 + (row & ~31)) / p.hq < x.w.rows;
+            const int first = (2 * x.mp + (x.solo ? 0 : w)) * p.rpt;   // first query row of this stream's product
+            const int r = first + row / p.hq;
+            const bool live = row < p.rpt * p.hq && r < x.w.rows;
+            const bool warp_live = (row & ~31) < p.rpt * p.hq && first + (row & ~31) / p.hq < x.w.rows;
             float m = -INFINITY, l = 0.f;
             int* odd_word = &s_odd[turn & 1][w];
             bool bad = x.w.bad, tree = false;
             const int mine_tiles = x.solo ? (x.tiles - w + 1) / 2 : x.tiles;   // tiles of this stream
             if (!x.w.bad) {
-                // queries into the 128-byte swizzle; rows past the pairs are zero
-                if (w == 0 || !x.solo) {
-                    const int per_row = p.D / 8;
-                    uint8_t* dst = sQ + w * TILE;
-                    for (int base = 0; base < PR_ROWS * per_row; base += 8 * 128) {
-                        uint4 v[8];
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const int i = base + u * 128 + row;
-                            const int mr = i / per_row, c = i - mr * per_row;
-                            const int qr = (m0 + mr) / p.hq, qh = (m0 + mr) - qr * p.hq;
-                            v[u] = make_uint4(0, 0, 0, 0);
-                            if (mr < PR_ROWS && qr < x.w.rows)
-                                v[u] = *reinterpret_cast<const uint4*>(p.q + (int64_t)(x.w.r0 + qr) * p.q_stride +
-                                                                       (x.g * p.hq + qh) * p.D + c * 8);
-                        }
-#pragma unroll
-                        for (int u = 0; u < 8; ++u) {
-                            const int i = base + u * 128 + row;
-                            const int mr = i / per_row, c = i - mr * per_row;
-                            if (mr < PR_ROWS)
-                                *reinterpret_cast<uint4*>(dst + (c >> 3) * PR_KT * 128 + mr * 128 +
-                                                          (((c & 7) ^ (mr & 7)) << 4)) = v[u];
-                        }
-                    }
-                    fence_async_smem();
-                    mbar_arrive(&q_full[w]);
-                }
                 // what the streams learn of the piece: bit 0, a value under a mask is not
                 // finite; bit 1, the tree is malformed
                 if ((x.kt + x.tiles) * PR_KT > x.w.len) {
@@ -460,7 +465,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                             for (int a = row; a < nn; a += 128) {
                                 const int pi = p.parent[n0 + a];
                                 const bool wrong = pi < -1 || pi >= a;
-                                s_par[w][a] = (int16_t)(wrong ? -1 : pi);
+                                s_par[w][1 + a] = (uint8_t)(wrong ? 0 : 1 + pi);
                                 off |= wrong;
                             }
                         if (off) atomicOr(odd_word, 2);
@@ -519,7 +524,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                                     for (int c = 0; c < 4; ++c)
                                         if (t >= 32 * c && t < 32 * c + 32) see[c] |= 1u << (t & 31);
                                     if (a == 0) break;
-                                    a = 1 + s_par[w][a - 1];
+                                    a = s_par[w][a];
                                 }
                             }
                             __syncwarp();
@@ -611,7 +616,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             bad |= (learnt & 2) != 0;
             const bool whole = x.tiles == x.w.nt;
             const int slot = (int)blockIdx.x * 2 + (x.kt == 0 ? 1 : 0);
-            const int prow = (x.solo ? 0 : w * PR_ROWS) + row;      // row of the partial area
+            const int prow = (x.solo ? 0 : w * p.rpt * p.hq) + row;   // pair within the item
             const bool writer = !(x.solo && w == 1) && live;
             float w0 = 1.f, w1 = 0.f, M = m, L = l;
             if (merge) {
@@ -627,7 +632,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             }
             if (bad) M = L = NAN;
             const float inv = 1.f / L;
-            const int64_t out_pair = (int64_t)(x.w.r0 + r) * p.H + x.g * p.hq + h;
             // values left out above, at the positions of this piece that the row sees
             auto left_out = [&](int d) {
                 float sum = 0.f;
@@ -636,7 +640,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     if (t < x.kt * PR_KT || t >= (x.kt + x.tiles) * PR_KT) continue;
                     bool sees = !tree || j == 0 || j == r;
                     for (int a = r; a > j && !sees;) {
-                        a = 1 + s_par[w][a - 1];
+                        a = s_par[w][a];
                         sees = a == j;
                     }
                     const int page = p.table[(int64_t)x.b * p.max_pages + (t >> p.page_shift)];
@@ -647,24 +651,23 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 }
                 return sum;
             };
-            constexpr int XC = BLK * 32;   // dims exchanged together: a row of the second stream's queries' place
-            for (int c0 = 0; c0 < p.D; c0 += XC) {
-                float* xb = reinterpret_cast<float*>(sQ + TILE);   // [128][XC]
+            float* xb = reinterpret_cast<float*>(sX);   // [128][32]: the second stream's rows, pieces of 16 bytes swizzled
+            for (int c0 = 0; c0 < p.D; c0 += PR_XC) {
                 if (merge) {
                     if (c0 > 0) named_sync(3, 256);
                     if (w == 1)
-                        for (int c = 0; c < XC && c0 + c < p.D; c += 16) {
+                        for (int c = 0; c < PR_XC && c0 + c < p.D; c += 16) {
                             uint32_t y[16];
                             tmem_ld_x16(tO + c0 + c, y);
                             tmem_ld_wait();
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                *reinterpret_cast<uint4*>(xb + row * XC + ((((c >> 2) + e) ^ (row & 7)) << 2)) =
+                                *reinterpret_cast<uint4*>(xb + row * PR_XC + ((((c >> 2) + e) ^ (row & 7)) << 2)) =
                                     make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
                         }
                     named_sync(3, 256);
                 }
-                for (int c = 0; c < XC && c0 + c < p.D; c += 16) {
+                for (int c = 0; c < PR_XC && c0 + c < p.D; c += 16) {
                     float v[16];
                     if (!x.w.bad && mine_tiles > 0) {   // warp-uniform
                         uint32_t y[16];
@@ -680,8 +683,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         if (merge) {
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const float4 y =
-                                    *reinterpret_cast<const float4*>(xb + row * XC + ((((c >> 2) + e) ^ (row & 7)) << 2));
+                                const float4 y = *reinterpret_cast<const float4*>(
+                                    xb + row * PR_XC + ((((c >> 2) + e) ^ (row & 7)) << 2));
                                 v[4 * e] = fmaf(y.x, w1, v[4 * e]);
                                 v[4 * e + 1] = fmaf(y.y, w1, v[4 * e + 1]);
                                 v[4 * e + 2] = fmaf(y.z, w1, v[4 * e + 2]);
@@ -691,86 +694,40 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         if (odd && !bad)
                             for (int e = 0; e < 16; ++e) v[e] += left_out(c0 + c + e);
                         if (whole) {
-                            uint32_t o[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) o[e] = cvt_bf16x2(v[2 * e] * inv, v[2 * e + 1] * inv);
-                            uint4* dst = reinterpret_cast<uint4*>(p.out + out_pair * p.D + c0 + c);
-                            dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                            dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                            const int64_t o = (int64_t)(x.w.r0 + r) * p.H + x.g * p.hq + (row - row / p.hq * p.hq);
+                            uint4* dst = reinterpret_cast<uint4*>(p.out + o * p.D + c0 + c);
+                            dst[0] = make_uint4(cvt_bf16x2(v[0] * inv, v[1] * inv), cvt_bf16x2(v[2] * inv, v[3] * inv),
+                                                cvt_bf16x2(v[4] * inv, v[5] * inv), cvt_bf16x2(v[6] * inv, v[7] * inv));
+                            dst[1] = make_uint4(cvt_bf16x2(v[8] * inv, v[9] * inv), cvt_bf16x2(v[10] * inv, v[11] * inv),
+                                                cvt_bf16x2(v[12] * inv, v[13] * inv), cvt_bf16x2(v[14] * inv, v[15] * inv));
                         } else {
-                            float4* dst = reinterpret_cast<float4*>(
-                                p.part + ((int64_t)slot * 2 * PR_ROWS + prow) * p.D + c0 + c);
+                            float4* dst = p.part + ((int64_t)slot * (p.D / 4) + (c0 + c) / 4) * 2 * PR_ROWS + prow;
 #pragma unroll
                             for (int e = 0; e < 4; ++e)
-                                dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                                dst[e * 2 * PR_ROWS] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                         }
                     }
                     __syncwarp();
                 }
             }
             if (bad && row == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)x.b);
-            if (whole) {
-                if (writer && p.lse) p.lse[out_pair] = (M + __log2f(L)) * LN2;
-            } else {
-                if (writer) p.stat[slot * 2 * PR_ROWS + prow] = make_float2(M, L);
-                const int64_t ts = begin + (count - left) - x.kt;   // the item's first tile in the flat sequence
-                const int c0 = (int)(ts / per), pieces = (int)((ts + x.w.nt - 1) / per) - c0 + 1;
-                named_sync(3, 256);
-                if (tid == 0) s_last = round_arrive(p.cnt + c0) == (uint32_t)(pieces - 1);
-                named_sync(3, 256);
-                if (s_last) {
-                    // piece i is CTA c0 + i's: its second slot for the item's first, else its
-                    // first; four pieces' values in flight together, added in order
-                    const int quarter = p.D / 4;
-                    for (int i = tid; i < x.pairs * quarter; i += 256) {
-                        const int pr = i / quarter, d = (i - pr * quarter) * 4;
-                        float tM = -INFINITY, tL = 0.f;
-                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                        for (int q0 = 0; q0 < pieces; q0 += 4) {
-                            float2 st[4];
-                            float4 y[4];
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const bool in = q0 + u < pieces;
-                                const int at = ((c0 + q0 + u) * 2 + (q0 + u == 0)) * 2 * PR_ROWS + pr;
-                                st[u] = in ? __ldcg(&p.stat[at]) : make_float2(-INFINITY, 0.f);
-                                y[u] = in ? __ldcg(reinterpret_cast<const float4*>(p.part + (int64_t)at * p.D + d))
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-                            }
-                            float topm = tM;
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) topm = fmaxf(topm, st[u].x);
-                            const float a = tM == -INFINITY ? 0.f : ex2_approx(tM - topm);
-                            tM = topm;
-                            tL *= a;
-                            v = make_float4(v.x * a, v.y * a, v.z * a, v.w * a);
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                const float wt = st[u].x == -INFINITY ? 0.f : ex2_approx(st[u].x - topm);
-                                tL = fmaf(st[u].y, wt, tL);
-                                v.x = fmaf(y[u].x, wt, v.x);
-                                v.y = fmaf(y[u].y, wt, v.y);
-                                v.z = fmaf(y[u].z, wt, v.z);
-                                v.w = fmaf(y[u].w, wt, v.w);
-                            }
-                        }
-                        const int fp = x.mp * 2 * PR_ROWS + pr, fr = fp / p.hq, fh = fp - fr * p.hq;
-                        const int64_t o = (int64_t)(x.w.r0 + fr) * p.H + x.g * p.hq + fh;
-                        const float ti = 1.f / tL;
-                        *reinterpret_cast<uint2*>(p.out + o * p.D + d) =
-                            make_uint2(cvt_bf16x2(v.x * ti, v.y * ti), cvt_bf16x2(v.z * ti, v.w * ti));
-                        if (p.lse && d == 0) p.lse[o] = (tM + __log2f(tL)) * LN2;
-                    }
-                    if (tid == 0) p.cnt[c0] = 0;
-                }
+            if (writer && !whole) p.stat[slot * 2 * PR_ROWS + prow] = make_float2(M, L);
+            if (writer && whole && p.lse)
+                p.lse[(int64_t)(x.w.r0 + r) * p.H + x.g * p.hq + (row - row / p.hq * p.hq)] = (M + __log2f(L)) * LN2;
+            if (tid == 0 && !whole && x.kt == 0) {
+                const int64_t ts = begin + (count - left);   // the item's first tile in the flat sequence
+                const int pieces = (int)((ts + x.w.nt - 1) / per) - (int)blockIdx.x + 1;
+                p.join[blockIdx.x] = make_int4(pieces, x.w.r0 + 2 * x.mp * p.rpt, x.rows * p.hq, x.g);
+                shared_item = true;
             }
             if (!x.w.bad) n += x.tiles;
             left -= x.tiles;
             if (left > 0) {
-                named_sync(3, 256);   // s_odd, s_last and the exchanged rows are read to their end
+                named_sync(3, 256);   // s_odd and the exchanged rows are read to their end
                 piece_next(p, x, left);
             }
         }
+        if (tid == 0 && !shared_item) p.join[blockIdx.x] = make_int4(0, 0, 0, 0);
         tc_fence_before();
     }
     __syncthreads();
@@ -778,7 +735,93 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
+// ------------------------------------------------------------------ join
+// The pieces of a shared item, added in order: piece k is CTA c + k's, its
+// second slot for the item's first piece, else its first.  Block (c, y): pairs
+// 32 y .. of the item that begins in CTA c; lanes are pairs, warps take a
+// quarter of the dims' groups of four; results leave by way of shared memory in
+// whole rows.
+constexpr int RJ_WARPS = 4;
+
+__global__ void __launch_bounds__(RJ_WARPS * 32)
+    rounds_join_kernel(const int4* __restrict__ join, const float4* __restrict__ part, const float2* __restrict__ stat,
+                       uint16_t* out, float* lse, int H, int D, int hq) {
+    __shared__ uint2 s_row[32][128 / 4 + 1];
+    pdl_wait();
+    pdl_trigger();
+    const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int4 j = __ldcg(&join[c]);   // pieces, first row, pairs, KV head
+    const int first = blockIdx.y * 32;
+    if (first >= j.z) return;
+    const int pr = first + lane;
+    const bool in = pr < j.z;
+    const int quads = D / 4;
+    const float2* st = stat + (in ? pr : first);
+    const float4* src = part + (in ? pr : first);
+    auto slot = [&](int k) { return (int64_t)(c + k) * 2 + (k == 0); };
+    float M = -INFINITY;
+#pragma unroll 8
+    for (int k = 0; k < j.x; ++k) M = fmaxf(M, __ldcg(st + slot(k) * 2 * PR_ROWS).x);
+    constexpr int MQ = 128 / 4 / RJ_WARPS;   // groups of four dims a warp takes at most
+    float4 v[MQ];
+    float L = 0.f;
+#pragma unroll
+    for (int u = 0; u < MQ; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+    for (int k = 0; k < j.x; ++k) {
+        const float2 s2 = __ldcg(st + slot(k) * 2 * PR_ROWS);
+        float4 y[MQ];
+#pragma unroll
+        for (int u = 0; u < MQ; ++u)
+            if (warp + u * RJ_WARPS < quads) y[u] = __ldcg(src + (slot(k) * quads + warp + u * RJ_WARPS) * 2 * PR_ROWS);
+        const float w = s2.x == -INFINITY ? 0.f : ex2_approx(s2.x - M);
+        L = fmaf(s2.y, w, L);
+#pragma unroll
+        for (int u = 0; u < MQ; ++u) {
+            if (warp + u * RJ_WARPS >= quads) continue;
+            v[u].x = fmaf(y[u].x, w, v[u].x);
+            v[u].y = fmaf(y[u].y, w, v[u].y);
+            v[u].z = fmaf(y[u].z, w, v[u].z);
+            v[u].w = fmaf(y[u].w, w, v[u].w);
+        }
+    }
+    const float inv = 1.f / L;
+#pragma unroll
+    for (int u = 0; u < MQ; ++u)
+        if (warp + u * RJ_WARPS < quads)
+            s_row[lane][warp + u * RJ_WARPS] =
+                make_uint2(cvt_bf16x2(v[u].x * inv, v[u].y * inv), cvt_bf16x2(v[u].z * inv, v[u].w * inv));
+    auto pair_row = [&](int q) { return (int64_t)(j.y + q / hq) * H + j.w * hq + q % hq; };
+    if (warp == 0 && in && lse) lse[pair_row(pr)] = (M + __log2f(L)) * LN2;
+    __syncthreads();
+    for (int r = warp; r < 32 && first + r < j.z; r += RJ_WARPS)
+        if (lane < quads) reinterpret_cast<uint2*>(out + pair_row(first + r) * D)[lane] = s_row[r][lane];
+}
+
 // ------------------------------------------------------------------ host side
+// The queries as [P, H, D] in boxes of 64 dims x hq heads x rpt rows: a box is
+// the 128-byte rows of a product's operand, row by row.
+static bool query_map(CUtensorMap* map, const wf_paged_attn_args* a, int D, int hq, int rpt) {
+    static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    if (!enc) return false;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a->H, (cuuint64_t)a->P};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a->q_stride * 2};
+    cuuint32_t box[3] = {64, (cuuint32_t)hq, (cuuint32_t)rpt};
+    cuuint32_t estr[3] = {1, 1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<uint16_t*>(a->q), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s) {
     static std::mutex mu;
     static bool attr_set[64] = {false};
@@ -793,8 +836,6 @@ wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args*
     const int64_t layer_bytes = (int64_t)c->num_pages * c->page_size * c->G * c->D * 2;
     const uint8_t* K = static_cast<const uint8_t*>(c->K) + a->layer * layer_bytes;
     RoundsParams p = {};
-    p.q = a->q;
-    p.q_stride = a->q_stride;
     p.pos_off = a->pos_off;
     p.cache_len = a->cache_len;
     p.node_off = a->node_off;
@@ -804,9 +845,9 @@ wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args*
     p.V = static_cast<const uint8_t*>(c->V) + a->layer * layer_bytes;
     p.out = a->out;
     p.lse = a->lse;
-    p.part = reinterpret_cast<float*>(w + L.part);
+    p.part = reinterpret_cast<float4*>(w + L.part);
     p.stat = reinterpret_cast<float2*>(w + L.stat);
-    p.cnt = reinterpret_cast<uint32_t*>(w + L.cnt);
+    p.join = reinterpret_cast<int4*>(w + L.join);
     p.qk = a->scale * LOG2E;
     p.P = a->P;
     p.H = a->H;
@@ -819,22 +860,27 @@ wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args*
     p.max_pages = c->max_pages;
     p.max_rows = a->max_rows;
     p.min_tiles = 1;
+    p.rpt = PR_ROWS / p.hq;
     p.box_rows = c->page_size < PR_KT ? c->page_size : PR_KT;
     p.idesc_s = umma_idesc_bf16(PR_ROWS, PR_KT);
     p.idesc_o = umma_idesc_bf16(PR_ROWS, c->D) | (1u << 16);   // the values' contiguous dimension is N
     p.ctrl = static_cast<Control*>(ws);
     p.timeout_ns = wait_timeout_ns();
-    CUtensorMap tmK, tmV;
+    CUtensorMap tmQ, tmK, tmV;
+    if (!query_map(&tmQ, a, c->D, p.hq, p.rpt)) return WF_ERR_CUDA;
     const uint64_t rows = (uint64_t)c->num_pages * c->page_size, cols = (uint64_t)c->G * c->D;
     if (!make_map(&tmK, K, rows, cols, (uint32_t)p.box_rows) || !make_map(&tmV, p.V, rows, cols, (uint32_t)p.box_rows))
         return WF_ERR_CUDA;
     int grid = num_sms() < PA_MAX_ROUND_CTAS ? num_sms() : PA_MAX_ROUND_CTAS;
     // no more CTAs than tiles that the bounds allow
-    const int64_t tiles = (int64_t)c->B * c->G * cdiv((int64_t)a->max_rows * p.hq, 2 * PR_ROWS) *
+    const int64_t tiles = (int64_t)c->B * c->G * cdiv(a->max_rows, 2 * p.rpt) *
                           cdiv((int64_t)c->max_pages * c->page_size, PR_KT);
     if (tiles < grid) grid = (int)tiles;
-    if (c->D <= 64) return launch(paged_rounds_kernel<1>, dim3(grid), dim3(PR_THREADS), (size_t)rounds_smem(1), s, tmK, tmV, p);
-    return launch(paged_rounds_kernel<2>, dim3(grid), dim3(PR_THREADS), (size_t)rounds_smem(2), s, tmK, tmV, p);
+    PR_TRY(launch(c->D <= 64 ? paged_rounds_kernel<1> : paged_rounds_kernel<2>, dim3(grid), dim3(PR_THREADS),
+                  (size_t)rounds_smem(c->D <= 64 ? 1 : 2), s, tmQ, tmK, tmV, p));
+    const int most = a->max_rows < 2 * p.rpt ? a->max_rows : 2 * p.rpt;   // query rows of an item
+    return launch(rounds_join_kernel, dim3(grid, cdiv(most * p.hq, 32)), dim3(RJ_WARPS * 32), 0, s, (const int4*)p.join,
+                  (const float4*)p.part, (const float2*)p.stat, a->out, a->lse, a->H, c->D, p.hq);
 }
 
 }  // namespace wf
