@@ -22,7 +22,8 @@
 // A product holds whole query rows: 128 / (heads a group) of them.
 // S and O live in tensor memory; P overwrites its S as the left operand of the
 // second product.  One warp copies queries and pages (tensor copies into the
-// 128-byte swizzle), one issues the products.
+// 128-byte swizzle); each stream has a warp of its own that issues its products
+// (one for both spent most of its time on barriers: 139 us for the batch of 32).
 //
 // Tiles that reach the round's own rows take a mask of 128 bits per row.  There
 // a stored value that is not finite is set to zero before the product (0 * inf
@@ -40,7 +41,7 @@
 
 namespace wf {
 
-constexpr int PR_THREADS = 320;    // two streams of four softmax warps, the copying and the issuing warp
+constexpr int PR_THREADS = 352;    // two streams of four softmax warps, the copying warp, an issuing warp a stream
 constexpr int PR_KT = 128;         // positions of a tile
 constexpr int PR_RING = 4;         // tiles of keys or values in flight
 constexpr int PR_ROWS = 128;       // pairs of a product
@@ -166,6 +167,12 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
     return ((uint64_t)HI << 32) | lo;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// one lane of a converged warp
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
 __device__ __forceinline__ void named_sync(int id, int threads) {
     asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -195,7 +202,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     uint8_t* sX = sR + PR_RING * TILE;
     __shared__ uint64_t kv_full[PR_RING], kv_empty[PR_RING], q_full, q_empty, s_full[2], p_full[2], o_full[2], told[4];
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_word, s_bad[4], s_odd[2][2], s_pb;
+    __shared__ int abort_word, s_bad[4], s_odd[2][2], s_pb, s_turn;
     __shared__ uint8_t s_par[2][WF_MAX_SEQ_NODES + 1];   // row of each row's parent, by stream (a row's own copy)
     __shared__ float2 s_xst[PR_ROWS];
     __shared__ int64_t s_plan, s_scan[PR_THREADS / 32];
@@ -205,17 +212,17 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     if (tid == 0) {
         for (int i = 0; i < PR_RING; ++i) {
             mbar_init(&kv_full[i], 1);
-            mbar_init(&kv_empty[i], 1);
+            mbar_init(&kv_empty[i], 2);   // both streams, or one twice
         }
         mbar_init(&q_full, 1);
-        mbar_init(&q_empty, 1);
+        mbar_init(&q_empty, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], PR_ROWS);
             mbar_init(&o_full[i], 1);
         }
         for (int i = 0; i < 4; ++i) mbar_init(&told[i], 1);
-        abort_word = 0;
+        abort_word = s_turn = 0;
         s_odd[0][0] = s_odd[0][1] = s_odd[1][0] = s_odd[1][1] = 0;
         fence_barrier_init();
         tma_prefetch_desc(&tmQ);
@@ -363,58 +370,93 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             for (int at = max(0, 2 * n - PR_RING); at < 2 * n; ++at)
                 mbar_wait(&kv_full[at % PR_RING], (at / PR_RING) & 1, p.timeout_ns, nullptr);
             if (k > 0) mbar_wait(&q_full, (k & 1) ^ 1, p.timeout_ns, nullptr);
-        } else if (warp == 9 && lane == 0) {
-            // ---------------------------------------- products
-            int n = 0;                                 // tiles before this piece
-            uint32_t qn = 0, pn[2] = {0, 0};           // queries, probabilities (by stream) taken
+        } else {
+            // ---------------------------------------- products of stream w
+            // The whole warp runs this with the same values and one elected lane
+            // issues: the operands' descriptors stay in uniform registers (issued
+            // from a single thread's own, a product took 107 cycles instead of its 64).
+            const int w = __shfl_sync(0xffffffffu, warp - 9, 0);
+            const uint32_t tS = __shfl_sync(0xffffffffu, tmem, 0) + w * 128, tO = tS + 256;
+            const uint32_t qdesc = __shfl_sync(0xffffffffu, desc_lo_rows(smem_u32(sQ)), 0);
+            const uint32_t kdesc = __shfl_sync(0xffffffffu, desc_lo_rows(smem_u32(sR)), 0);
+            const uint32_t vdesc = __shfl_sync(0xffffffffu, desc_lo_values(smem_u32(sR)), 0);
+            int n = 0;                  // tiles before this piece
+            uint32_t qn = 0, pn = 0;    // queries, probabilities taken
             bool ok = true;
             const int nks = p.D / 16;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 ok = ok && mbar_wait(bar, parity, p.timeout_ns, abort_flag);
             };
+            // One stream's products are issued without the other's between them: the
+            // tensor cores finish one stream early and the streams fall out of step
+            // (interleaved, both finish late and then both wait for exponentials).
+            auto take_turn = [&]() {
+                ok = __all_sync(0xffffffffu, ok);
+                if (ok && lane == 0 && atomicCAS(&s_turn, 0, 1) != 0) {
+                    const uint64_t start = globaltimer_ns();
+                    while (ok && atomicCAS(&s_turn, 0, 1) != 0)
+                        ok = !*abort_flag && globaltimer_ns() - start <= p.timeout_ns;
+                }
+                ok = __all_sync(0xffffffffu, ok);
+            };
+            auto give_turn = [&]() {
+                __syncwarp();
+                if (lane == 0) atomicExch(&s_turn, 0);
+            };
             for (int left = count; left > 0 && ok;) {
                 if (!x.w.bad) {
-                    const int steps = x.solo ? (x.tiles + 1) / 2 : x.tiles;
-                    auto tile_of = [&](int i, int w) { return x.solo ? 2 * i + w : i; };
-                    auto scores = [&](int i, int w) {   // S of stream w's step i
-                        const int at = 2 * (n + tile_of(i, w)), slot = at % PR_RING;
-                        wait(&kv_full[slot], (at / PR_RING) & 1);
-                        if (!ok) return;
-                        tc_fence_after();
-                        const uint32_t a = desc_lo_rows(smem_u32(sQ + (x.solo ? 0 : w) * TILE));
-                        const uint32_t b = desc_lo_rows(smem_u32(sR + slot * TILE));
+                    const int steps = __shfl_sync(0xffffffffu, x.solo ? (x.tiles - w + 1) / 2 : x.tiles, 0);
+                    const bool solo = __shfl_sync(0xffffffffu, (int)x.solo, 0) != 0;
+                    const int n0 = __shfl_sync(0xffffffffu, n, 0);
+                    auto place_of = [&](int i) { return 2 * (n0 + (solo ? 2 * i + w : i)); };   // of step i's keys
+                    auto release = [&](int slot) {
+                        umma_commit(&kv_empty[slot]);
+                        if (solo) umma_commit(&kv_empty[slot]);
+                    };
+                    auto arrived = [&](int at) { wait(&kv_full[at % PR_RING], (at / PR_RING) & 1); };
+                    auto scores = [&](int i) {   // S of step i
+                        const int slot = place_of(i) % PR_RING;
+                        const uint32_t a = qdesc + (solo ? 0 : w) * (TILE >> 4), b = kdesc + slot * (TILE >> 4);
 #pragma unroll
                         for (int ks = 0; ks < 4 * BLK; ++ks)
                             if (ks < nks) {
                                 const uint32_t off = (uint32_t)((ks >> 2) * PR_KT * 8 + (ks & 3) * 2);
-                                umma_bf16(tmem + w * 128, desc_of(a + off), desc_of(b + off), p.idesc_s, ks != 0);
+                                umma_bf16(tS, desc_of(a + off), desc_of(b + off), p.idesc_s, ks != 0);
                             }
                         umma_commit(&s_full[w]);
-                        if (x.solo || w == 1) umma_commit(&kv_empty[slot]);
-                        // the piece's last scores: its queries may go
-                        if (tile_of(i, w) == x.tiles - 1 && (x.solo || w == 1)) umma_commit(&q_empty);
+                        release(slot);
+                        if (i + 1 == steps) umma_commit(&q_empty);   // the stream is done with the queries
                     };
                     wait(&q_full, qn++ & 1);
-                    for (int w = 0; w < 2 && ok; ++w)
-                        if (tile_of(0, w) < x.tiles) scores(0, w);
-                    for (int i = 0; i < steps && ok; ++i)
-                        for (int w = 0; w < 2 && ok; ++w) {
-                            const int j = tile_of(i, w);
-                            if (j >= x.tiles) continue;
-                            const int at = 2 * (n + j) + 1, slot = at % PR_RING;
-                            wait(&kv_full[slot], (at / PR_RING) & 1);
-                            wait(&p_full[w], pn[w]++ & 1);
-                            if (!ok) break;
-                            tc_fence_after();
-                            const uint32_t b = desc_lo_values(smem_u32(sR + slot * TILE));
+                    if (steps == 0) {
+                        if (lane == 0) mbar_arrive(&q_empty);
+                    } else {
+                        arrived(place_of(0));
+                        take_turn();
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) scores(0);
+                        give_turn();
+                    }
+                    for (int i = 0; i < steps; ++i) {
+                        const int at = place_of(i) + 1, slot = at % PR_RING;
+                        arrived(at);
+                        if (i + 1 < steps) arrived(place_of(i + 1));
+                        wait(&p_full[w], pn++ & 1);
+                        take_turn();
+                        if (!ok) break;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            const uint32_t b = vdesc + slot * (TILE >> 4);
 #pragma unroll
                             for (int ks = 0; ks < PR_KT / 16; ++ks)
-                                umma_ts(tmem + 256 + w * 128, tmem + w * 128 + ks * 8, desc_of(b + ks * 128), p.idesc_o,
-                                        (i | ks) != 0);
-                            if (x.solo || w == 1) umma_commit(&kv_empty[slot]);
-                            if (tile_of(i + 1, w) >= x.tiles) umma_commit(&o_full[w]);   // the stream's last
-                            else scores(i + 1, w);
+                                umma_ts(tO, tS + ks * 8, desc_of(b + ks * 128), p.idesc_o, (i | ks) != 0);
+                            release(slot);
+                            if (i + 1 == steps) umma_commit(&o_full[w]);
+                            else scores(i + 1);
                         }
+                        give_turn();
+                    }
                     n += x.tiles;
                 }
                 left -= x.tiles;
@@ -422,7 +464,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             }
             if (!ok) {
                 *abort_flag = 1;
-                record_error(p.ctrl, WF_ERR_TIMEOUT, 0x810u);
+                if (lane == 0) record_error(p.ctrl, WF_ERR_TIMEOUT, 0x810u);
             }
         }
     } else {
@@ -456,9 +498,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 // finite; bit 1, the tree is malformed
                 if ((x.kt + x.tiles) * PR_KT > x.w.len) {
                     const int kd = p.kind ? p.kind[x.b] : 1;
+                    const int n0 = p.parent ? p.node_off[x.b] : 0, n1 = p.parent ? p.node_off[x.b + 1] : 0;
                     tree = p.parent != nullptr && kd != 0;
                     if (tree) {
-                        const int n0 = p.node_off[x.b], nn = p.node_off[x.b + 1] - n0;
+                        const int nn = n1 - n0;
                         bool off = n0 < 0 || nn != x.w.rows - 1;
                         if (off) tree = false;
                         else
@@ -476,34 +519,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     const int j = x.solo ? 2 * i + w : i;
                     const int t0 = (x.kt + j) * PR_KT;
                     const bool masked = t0 + PR_KT > x.w.len;
-                    const bool clean = masked && (x.solo || w == 0);
-                    if (clean && t0 + row >= x.w.len) {
-                        // one position's values a thread: zero past the end, and where not finite
-                        const int at = 2 * (n + j) + 1, slot = at % PR_RING;
-                        wait(&kv_full[slot], (at / PR_RING) & 1);
-                        const bool past = t0 + row >= x.w.T;
-                        bool odd = false;
-                        for (int c = 0; c < p.D / 8; ++c) {
-                            uint4* v = reinterpret_cast<uint4*>(sR + slot * TILE + (c >> 3) * PR_KT * 128 + row * 128 +
-                                                                (((c & 7) ^ (row & 7)) << 4));
-                            if (past) {
-                                *v = make_uint4(0, 0, 0, 0);
-                                continue;
-                            }
-                            uint4 y = *v;
-                            uint32_t* e = &y.x;
-                            bool hit = false;
-#pragma unroll
-                            for (int u = 0; u < 4; ++u) {
-                                if ((e[u] & 0x7F80u) == 0x7F80u) e[u] &= 0xFFFF0000u, hit = true;
-                                if ((e[u] & 0x7F800000u) == 0x7F800000u) e[u] &= 0x0000FFFFu, hit = true;
-                            }
-                            if (hit) *v = y;
-                            odd |= hit;
-                        }
-                        if (odd) atomicOr(odd_word, 1);
-                        fence_async_smem();
-                    }
                     wait(&s_full[w], sn++ & 1);
                     tc_fence_after();
                     if (warp_live && __all_sync(0xffffffffu, ok)) {
@@ -540,9 +555,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                             if (masked) {
 #pragma unroll
                                 for (int c = 0; c < 2; ++c)
+                                    if (!__all_sync(0xffffffffu, see[c0 + c] == 0xFFFFFFFFu))
 #pragma unroll
-                                    for (int e = 0; e < 32; ++e)
-                                        if (!(see[c0 + c] >> e & 1u)) s[c][e] = 0xFF800000u;
+                                        for (int e = 0; e < 32; ++e)
+                                            if (!(see[c0 + c] >> e & 1u)) s[c][e] = 0xFF800000u;
                             }
                         };
                         auto largest = [&]() {
@@ -592,8 +608,39 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         fetch(2);
                         weigh(2);
                         l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                        tmem_st_wait();
                     }
+                    if (masked && t0 + row >= x.w.len) {
+                        // one position's values a thread: zero past the end, and where not
+                        // finite (by both streams where both see the tile: the same bytes)
+                        const int at = 2 * (n + j) + 1, slot = at % PR_RING;
+                        wait(&kv_full[slot], (at / PR_RING) & 1);
+                        const bool past = t0 + row >= x.w.T;
+                        bool odd = false;
+#pragma unroll
+                        for (int blk = 0; blk < BLK; ++blk) {
+                            uint8_t* base = sR + slot * TILE + blk * PR_KT * 128 + row * 128;
+                            uint4 y[8];
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) y[c] = *reinterpret_cast<const uint4*>(base + ((c ^ (row & 7)) << 4));
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                uint32_t* e = &y[c].x;
+                                bool hit = past;
+#pragma unroll
+                                for (int u = 0; u < 4; ++u) {
+                                    if (past) e[u] = 0;
+                                    if ((e[u] & 0x7F80u) == 0x7F80u) e[u] &= 0xFFFF0000u, hit = true;
+                                    if ((e[u] & 0x7F800000u) == 0x7F800000u) e[u] &= 0x0000FFFFu, hit = true;
+                                }
+                                if (hit) *reinterpret_cast<uint4*>(base + ((c ^ (row & 7)) << 4)) = y[c];
+                                odd |= hit;
+                            }
+                        }
+                        if (odd && !past) atomicOr(odd_word, 1);
+                        fence_async_smem();
+                    }
+                    __syncwarp();
+                    tmem_st_wait();
                     tc_fence_before();
                     mbar_arrive(&p_full[w]);
                 }
@@ -655,60 +702,64 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             for (int c0 = 0; c0 < p.D; c0 += PR_XC) {
                 if (merge) {
                     if (c0 > 0) named_sync(3, 256);
-                    if (w == 1)
-                        for (int c = 0; c < PR_XC && c0 + c < p.D; c += 16) {
-                            uint32_t y[16];
-                            tmem_ld_x16(tO + c0 + c, y);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                *reinterpret_cast<uint4*>(xb + row * PR_XC + ((((c >> 2) + e) ^ (row & 7)) << 2)) =
-                                    make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
-                        }
-                    named_sync(3, 256);
-                }
-                for (int c = 0; c < PR_XC && c0 + c < p.D; c += 16) {
-                    float v[16];
-                    if (!x.w.bad && mine_tiles > 0) {   // warp-uniform
-                        uint32_t y[16];
-                        tmem_ld_x16(tO + c0 + c, y);
+                    if (w == 1) {
+                        uint32_t y[32];
+                        tmem_ld_32x32b_x32(tO + c0, y);
                         tmem_ld_wait();
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = __uint_as_float(y[e]) * w0;
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 16; ++e) v[e] = 0.f;
+                        for (int e = 0; e < 8; ++e)
+                            *reinterpret_cast<uint4*>(xb + row * PR_XC + ((e ^ (row & 7)) << 2)) =
+                                make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
                     }
-                    if (writer) {
-                        if (merge) {
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float4 y = *reinterpret_cast<const float4*>(
-                                    xb + row * PR_XC + ((((c >> 2) + e) ^ (row & 7)) << 2));
-                                v[4 * e] = fmaf(y.x, w1, v[4 * e]);
-                                v[4 * e + 1] = fmaf(y.y, w1, v[4 * e + 1]);
-                                v[4 * e + 2] = fmaf(y.z, w1, v[4 * e + 2]);
-                                v[4 * e + 3] = fmaf(y.w, w1, v[4 * e + 3]);
-                            }
-                        }
-                        if (odd && !bad)
-                            for (int e = 0; e < 16; ++e) v[e] += left_out(c0 + c + e);
-                        if (whole) {
-                            const int64_t o = (int64_t)(x.w.r0 + r) * p.H + x.g * p.hq + (row - row / p.hq * p.hq);
-                            uint4* dst = reinterpret_cast<uint4*>(p.out + o * p.D + c0 + c);
-                            dst[0] = make_uint4(cvt_bf16x2(v[0] * inv, v[1] * inv), cvt_bf16x2(v[2] * inv, v[3] * inv),
-                                                cvt_bf16x2(v[4] * inv, v[5] * inv), cvt_bf16x2(v[6] * inv, v[7] * inv));
-                            dst[1] = make_uint4(cvt_bf16x2(v[8] * inv, v[9] * inv), cvt_bf16x2(v[10] * inv, v[11] * inv),
-                                                cvt_bf16x2(v[12] * inv, v[13] * inv), cvt_bf16x2(v[14] * inv, v[15] * inv));
-                        } else {
-                            float4* dst = p.part + ((int64_t)slot * (p.D / 4) + (c0 + c) / 4) * 2 * PR_ROWS + prow;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e)
-                                dst[e * 2 * PR_ROWS] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-                        }
-                    }
-                    __syncwarp();
+                    named_sync(3, 256);
                 }
+                float v[PR_XC];
+                if (!x.w.bad && mine_tiles > 0) {   // warp-uniform
+                    uint32_t y[32];
+                    tmem_ld_32x32b_x32(tO + c0, y);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(y[e]) * w0;
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                }
+                if (writer) {
+                    if (merge) {
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            const float4 y = *reinterpret_cast<const float4*>(xb + row * PR_XC + ((e ^ (row & 7)) << 2));
+                            v[4 * e] = fmaf(y.x, w1, v[4 * e]);
+                            v[4 * e + 1] = fmaf(y.y, w1, v[4 * e + 1]);
+                            v[4 * e + 2] = fmaf(y.z, w1, v[4 * e + 2]);
+                            v[4 * e + 3] = fmaf(y.w, w1, v[4 * e + 3]);
+                        }
+                    }
+                    if (odd && !bad) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (c0 + e < p.D) v[e] += left_out(c0 + e);
+                    }
+                    // groups of 16 dims: the head size is a multiple of that
+                    if (whole) {
+                        const int64_t o = (int64_t)(x.w.r0 + r) * p.H + x.g * p.hq + (row - row / p.hq * p.hq);
+                        uint4* dst = reinterpret_cast<uint4*>(p.out + o * p.D + c0);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (c0 + (e >> 1) * 16 < p.D)
+                                dst[e] = make_uint4(cvt_bf16x2(v[8 * e] * inv, v[8 * e + 1] * inv),
+                                                    cvt_bf16x2(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
+                                                    cvt_bf16x2(v[8 * e + 4] * inv, v[8 * e + 5] * inv),
+                                                    cvt_bf16x2(v[8 * e + 6] * inv, v[8 * e + 7] * inv));
+                    } else {
+                        float4* dst = p.part + ((int64_t)slot * (p.D / 4) + c0 / 4) * 2 * PR_ROWS + prow;
+#pragma unroll
+                        for (int e = 0; e < 8; ++e)
+                            if (c0 + (e >> 2) * 16 < p.D)
+                                dst[e * 2 * PR_ROWS] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+                    }
+                }
+                __syncwarp();
             }
             if (bad && row == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)x.b);
             if (writer && !whole) p.stat[slot * 2 * PR_ROWS + prow] = make_float2(M, L);
@@ -829,7 +880,10 @@ wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args*
         return cudaFuncSetAttribute(paged_rounds_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     rounds_smem(1)) == cudaSuccess &&
                cudaFuncSetAttribute(paged_rounds_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    rounds_smem(2)) == cudaSuccess;
+                                    rounds_smem(2)) == cudaSuccess &&
+               // as for the catch-up's kernels: no change of the carveout between launches
+               cudaFuncSetAttribute(rounds_join_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) ==
+                   cudaSuccess;
     }));
     uint8_t* w = static_cast<uint8_t*>(ws);
     const PagedLayout L = paged_layout(c->B, a->H, c->G, c->D, a->max_rows);
