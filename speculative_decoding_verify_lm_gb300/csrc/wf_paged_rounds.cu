@@ -167,6 +167,41 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
     return ((uint64_t)HI << 32) | lo;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// whether `pred` holds in all of the named barrier's threads
+__device__ __forceinline__ bool named_all(int id, int threads, bool pred) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\tbar.red.and.pred q, %1, %2, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(id), "r"(threads), "r"((uint32_t)pred)
+        : "memory");
+    return r != 0;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// two fp32 operations in one instruction
+__device__ __forceinline__ uint64_t pair_of(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 // one lane of a converged warp
 __device__ __forceinline__ bool elect_one() {
     uint32_t e;
@@ -183,10 +218,10 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
         : "memory");
 }
 
-// Shared memory: queries [2][blocks][128 rows][128 B], ring [4][blocks][128 positions][128 B];
+// Shared memory: queries [2][blocks][128 rows][128 B], ring [4][blocks][128 positions][128 B],
 // exchanged rows [128][32] fp32; blocks = 64-dim blocks of a head.
 __host__ __device__ constexpr int rounds_smem(int blocks) {
-    return 1024 + (2 + PR_RING) * blocks * PR_KT * 128 + PR_XBYTES;
+    return 1024 + (2 * PR_ROWS + PR_RING * PR_KT) * blocks * 128 + PR_XBYTES;
 }
 
 // BLK: 64-dim blocks of a head (1 or 2)
@@ -194,15 +229,19 @@ template <int BLK>
 __global__ void __launch_bounds__(PR_THREADS, 1)
     paged_rounds_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const RoundsParams p) {
-    constexpr int TILE = BLK * PR_KT * 128;    // bytes of a tile of queries, keys or values
+    constexpr int QTILE = BLK * PR_ROWS * 128; // bytes of a product's queries
+    constexpr int TILE = BLK * PR_KT * 128;    // and of a tile of keys or values
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;
-    uint8_t* sR = smem + 2 * TILE;
+    uint8_t* sR = smem + 2 * QTILE;
     uint8_t* sX = sR + PR_RING * TILE;
-    __shared__ uint64_t kv_full[PR_RING], kv_empty[PR_RING], q_full, q_empty, s_full[2], p_full[2], o_full[2], told[4];
+    __shared__ uint64_t kv_full[PR_RING], kv_empty[PR_RING], q_full, q_empty, told[8];
+    __shared__ uint64_t piece_ready[8], piece_free[8];
+    __shared__ Piece s_piece[8];   // the copying warp's next pieces, for the others
+    __shared__ uint64_t s_full[2], p_full[2], o_full[2];   // by stream
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_word, s_bad[4], s_odd[2][2], s_pb, s_turn;
+    __shared__ int abort_word, s_bad[8], s_odd[2][2], s_pb, s_turn;
     __shared__ uint8_t s_par[2][WF_MAX_SEQ_NODES + 1];   // row of each row's parent, by stream (a row's own copy)
     __shared__ float2 s_xst[PR_ROWS];
     __shared__ int64_t s_plan, s_scan[PR_THREADS / 32];
@@ -221,7 +260,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             mbar_init(&p_full[i], PR_ROWS);
             mbar_init(&o_full[i], 1);
         }
-        for (int i = 0; i < 4; ++i) mbar_init(&told[i], 1);
+        for (int i = 0; i < 8; ++i) {
+            mbar_init(&told[i], 1);
+            mbar_init(&piece_ready[i], 1);
+            mbar_init(&piece_free[i], 4);   // two streams, two issuing warps
+        }
         abort_word = s_turn = 0;
         s_odd[0][0] = s_odd[0][1] = s_odd[1][0] = s_odd[1][1] = 0;
         fence_barrier_init();
@@ -282,24 +325,32 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         s_pb = b;
     }
     __syncthreads();
-    Piece x;
-    if (count > 0) {
-        x.b = s_pb;
-        x.w = round_seq(p, x.b);
-        const int item = (int)(s_plan / x.w.nt);
-        x.kt = (int)(s_plan - (int64_t)item * x.w.nt);
-        x.mp = item / p.G;
-        x.g = item - x.mp * p.G;
-        piece_shape(p, x, count);
-    }
-
     if (warp >= 8) {
         if (warp == 8) {
             // ---------------------------------------- copies: tile n's keys to ring place 2 n, its values to 2 n + 1
             const uint64_t pol = policy_evict_first();
             const int per_tile = PR_KT / p.box_rows;   // boxes of a tile: at most 16
+            Piece x;
+            if (count > 0) {
+                x.b = s_pb;
+                x.w = round_seq(p, x.b);
+                const int item = (int)(s_plan / x.w.nt);
+                x.kt = (int)(s_plan - (int64_t)item * x.w.nt);
+                x.mp = item / p.G;
+                x.g = item - x.mp * p.G;
+                piece_shape(p, x, count);
+            }
             int n = 0, k = 0;                          // tiles, pieces that have any
-            for (int left = count; left > 0;) {
+            for (int left = count, turn = 0; left > 0; ++turn) {
+                if (turn >= 8 && !mbar_wait(&piece_free[turn & 7], ((turn >> 3) & 1) ^ 1, p.timeout_ns, abort_flag)) {
+                    *abort_flag = 1;
+                    if (lane == 0) record_error(p.ctrl, WF_ERR_TIMEOUT, 0x801u);
+                    break;
+                }
+                if (lane == 0) {
+                    s_piece[turn & 7] = x;
+                    mbar_arrive(&piece_ready[turn & 7]);
+                }
                 bool bad = false;
                 if (!x.w.bad) {
                     int page = 0;
@@ -328,7 +379,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                                     mbar_arrive_expect_tx(&q_full, (uint32_t)(nq * BLK * p.rpt * p.hq * 128));
                                     for (int w = 0; w < nq; ++w)
                                         for (int blk = 0; blk < BLK; ++blk)
-                                            tma_load_3d(sQ + w * TILE + blk * PR_KT * 128, &tmQ, &q_full, blk * 64,
+                                            tma_load_3d(sQ + w * QTILE + blk * PR_ROWS * 128, &tmQ, &q_full, blk * 64,
                                                         x.g * p.hq, x.w.r0 + (2 * x.mp + w) * p.rpt);
                                 }
                                 __syncwarp();
@@ -357,8 +408,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 if (!x.w.bad) {   // whether the piece had a position without a page
                     bad = __any_sync(0xffffffffu, bad);
                     if (lane == 0) {
-                        s_bad[k & 3] = bad;
-                        mbar_arrive(&told[k & 3]);
+                        s_bad[k & 7] = bad;
+                        mbar_arrive(&told[k & 7]);
                     }
                     ++k;
                 }
@@ -403,7 +454,12 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) atomicExch(&s_turn, 0);
             };
-            for (int left = count; left > 0 && ok;) {
+            for (int left = count, turn = 0; left > 0 && ok; ++turn) {
+                wait(&piece_ready[turn & 7], (turn >> 3) & 1);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                const Piece& x = s_piece[turn & 7];
+                const int tiles = x.tiles;
                 if (!x.w.bad) {
                     const int steps = __shfl_sync(0xffffffffu, x.solo ? (x.tiles - w + 1) / 2 : x.tiles, 0);
                     const bool solo = __shfl_sync(0xffffffffu, (int)x.solo, 0) != 0;
@@ -416,7 +472,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     auto arrived = [&](int at) { wait(&kv_full[at % PR_RING], (at / PR_RING) & 1); };
                     auto scores = [&](int i) {   // S of step i
                         const int slot = place_of(i) % PR_RING;
-                        const uint32_t a = qdesc + (solo ? 0 : w) * (TILE >> 4), b = kdesc + slot * (TILE >> 4);
+                        const uint32_t a = qdesc + (solo ? 0 : w) * (QTILE >> 4), b = kdesc + slot * (TILE >> 4);
 #pragma unroll
                         for (int ks = 0; ks < 4 * BLK; ++ks)
                             if (ks < nks) {
@@ -457,10 +513,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         }
                         give_turn();
                     }
-                    n += x.tiles;
+                    n += tiles;
                 }
-                left -= x.tiles;
-                if (left > 0) piece_next(p, x, left);
+                left -= tiles;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&piece_free[turn & 7]);
             }
             if (!ok) {
                 *abort_flag = 1;
@@ -485,6 +542,11 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             }
         };
         for (int left = count; left > 0; ++turn) {
+            wait(&piece_ready[turn & 7], (turn >> 3) & 1);
+            // all of both streams go on, or none (also: s_odd and the exchanged rows of
+            // the piece before are read to their end)
+            if (!named_all(3, 256, ok)) break;
+            const Piece& x = s_piece[turn & 7];
             const int first = (2 * x.mp + (x.solo ? 0 : w)) * p.rpt;   // first query row of this stream's product
             const int r = first + row / p.hq;
             const bool live = row < p.rpt * p.hq && r < x.w.rows;
@@ -493,61 +555,64 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             int* odd_word = &s_odd[turn & 1][w];
             bool bad = x.w.bad, tree = false;
             const int mine_tiles = x.solo ? (x.tiles - w + 1) / 2 : x.tiles;   // tiles of this stream
-            if (!x.w.bad) {
-                // what the streams learn of the piece: bit 0, a value under a mask is not
-                // finite; bit 1, the tree is malformed
-                if ((x.kt + x.tiles) * PR_KT > x.w.len) {
-                    const int kd = p.kind ? p.kind[x.b] : 1;
-                    const int n0 = p.parent ? p.node_off[x.b] : 0, n1 = p.parent ? p.node_off[x.b + 1] : 0;
-                    tree = p.parent != nullptr && kd != 0;
-                    if (tree) {
-                        const int nn = n1 - n0;
-                        bool off = n0 < 0 || nn != x.w.rows - 1;
-                        if (off) tree = false;
-                        else
-                            for (int a = row; a < nn; a += 128) {
-                                const int pi = p.parent[n0 + a];
-                                const bool wrong = pi < -1 || pi >= a;
-                                s_par[w][1 + a] = (uint8_t)(wrong ? 0 : 1 + pi);
-                                off |= wrong;
-                            }
-                        if (off) atomicOr(odd_word, 2);
-                    }
-                    named_sync(1 + w, 128);
+            const bool piece_masked = (x.kt + x.tiles) * PR_KT > x.w.len;
+            // what the streams learn of the piece: bit 0, a value under a mask is not
+            // finite; bit 1, the tree is malformed
+            bool learned = false;
+            auto learn_tree = [&]() {   // the parents' rows into shared memory, once a piece
+                if (learned) return;
+                learned = true;
+                const int kd = p.kind ? p.kind[x.b] : 1;
+                const int n0 = p.parent ? p.node_off[x.b] : 0, n1 = p.parent ? p.node_off[x.b + 1] : 0;
+                tree = p.parent != nullptr && kd != 0;
+                if (tree) {
+                    const int nn = n1 - n0;
+                    bool off = n0 < 0 || nn != x.w.rows - 1;
+                    if (off) tree = false;
+                    else
+                        for (int a = row; a < nn; a += 128) {
+                            const int pi = p.parent[n0 + a];
+                            const bool wrong = pi < -1 || pi >= a;
+                            s_par[w][1 + a] = (uint8_t)(wrong ? 0 : 1 + pi);
+                            off |= wrong;
+                        }
+                    if (off) atomicOr(odd_word, 2);
                 }
+                named_sync(1 + w, 128);
+            };
+            if (!x.w.bad) {
                 for (int i = 0; i < mine_tiles; ++i) {
                     const int j = x.solo ? 2 * i + w : i;
                     const int t0 = (x.kt + j) * PR_KT;
                     const bool masked = t0 + PR_KT > x.w.len;
                     wait(&s_full[w], sn++ & 1);
                     tc_fence_after();
-                    if (warp_live && __all_sync(0xffffffffu, ok)) {
-                        uint32_t see[4];   // the positions that the row sees
-                        if (masked) {
-                            // all below `upto`, then the row's ancestors
-                            const int upto = (tree ? x.w.len : x.w.len + r + 1) - t0;
+                    const bool go = warp_live && __all_sync(0xffffffffu, ok);
+                    uint32_t see[4];   // the positions that the row sees
+                    if (masked) {
+                        learn_tree();
+                        // all below `upto`, then the row's ancestors
+                        const int upto = (tree ? x.w.len : x.w.len + r + 1) - t0;
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const int u = upto - 32 * c;
-                                see[c] = u <= 0 ? 0u : (u >= 32 ? 0xFFFFFFFFu : (1u << u) - 1u);
-                            }
-                            if (tree && live) {
-                                int a = r;
-                                while (true) {
-                                    const int t = x.w.len + a - t0;
-#pragma unroll
-                                    for (int c = 0; c < 4; ++c)
-                                        if (t >= 32 * c && t < 32 * c + 32) see[c] |= 1u << (t & 31);
-                                    if (a == 0) break;
-                                    a = s_par[w][a];
-                                }
-                            }
-                            __syncwarp();
+                        for (int c = 0; c < 4; ++c) {
+                            const int u = upto - 32 * c;
+                            see[c] = u <= 0 ? 0u : (u >= 32 ? 0xFFFFFFFFu : (1u << u) - 1u);
                         }
-                        // 64 scores in registers at a time: the upper half first, for its
-                        // maximum alone; the lower half stays for its exponentials (whose
-                        // place in tensor memory is the lower half's), then the upper again
-                        uint32_t s[2][32];
+                        if (tree && live) {
+                            int a = r;
+                            while (true) {
+                                const int t = x.w.len + a - t0;
+#pragma unroll
+                                for (int c = 0; c < 4; ++c)
+                                    if (t >= 32 * c && t < 32 * c + 32) see[c] |= 1u << (t & 31);
+                                if (a == 0) break;
+                                a = s_par[w][a];
+                            }
+                        }
+                        __syncwarp();
+                    }
+                    if (go) {
+                        uint32_t s[2][32];   // 64 scores at a time
                         auto fetch = [&](int c0) {
                             tmem_ld_32x32b_x32(tS + c0 * 32, s[0]);
                             tmem_ld_32x32b_x32(tS + c0 * 32 + 32, s[1]);
@@ -561,53 +626,70 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                                             if (!(see[c0 + c] >> e & 1u)) s[c][e] = 0xFF800000u;
                             }
                         };
-                        auto largest = [&]() {
-                            float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                        auto at = [&](int c, int e) { return __uint_as_float(s[c][e]); };
+                        auto largest = [&](float big) {
+                            float top[4] = {big, big, big, big};
 #pragma unroll
                             for (int c = 0; c < 2; ++c)
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) top[e & 3] = fmaxf(top[e & 3], __uint_as_float(s[c][e]));
+                                for (int e = 0; e < 32; e += 2) top[(e >> 1) & 3] = max3(top[(e >> 1) & 3], at(c, e), at(c, e + 1));
                             return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                         };
-                        fetch(2);
-                        const float upper = largest();
-                        fetch(0);
-                        const float mx = fmaxf(upper, largest()) * p.qk;
-                        if (__any_sync(0xffffffffu, mx > m + PR_LAG)) {
-                            const float mn = fmaxf(m, mx);
-                            const float a = m == -INFINITY ? 0.f : ex2_approx(m - mn);
-                            m = mn;
-                            l *= a;
-                            if (i > 0)   // every earlier product into O has completed before this tile's scores
-                                for (int c = 0; c < p.D; c += 16) {
-                                    uint32_t y[16];
-                                    tmem_ld_x16(tO + c, y);
-                                    tmem_ld_wait();
+                        // The weights are taken against the running maximum as it is; only
+                        // when a score has outgrown it by 2^LAG (or nothing has been seen
+                        // yet) is the tile's maximum taken first.
+                        uint32_t pk[4][16];
+                        float sum = 0.f;
+                        bool again = !__all_sync(0xffffffffu, m > -INFINITY);
+                        while (true) {
+                            if (again) {
+                                fetch(0);
+                                const float low = largest(-INFINITY);
+                                fetch(2);
+                                const float mn = fmaxf(m, largest(low) * p.qk);
+                                const float a = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+                                m = mn;
+                                l *= a;
+                                if (i > 0)   // every earlier product into O has completed before this tile's scores
+                                    for (int c = 0; c < p.D; c += 16) {
+                                        uint32_t y[16];
+                                        tmem_ld_x16(tO + c, y);
+                                        tmem_ld_wait();
 #pragma unroll
-                                    for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * a);
-                                    tmem_st_x16(tO + c, y);
-                                }
-                        }
-                        const float base = m == -INFINITY ? 0.f : -m;
-                        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-                        auto weigh = [&](int c0) {
-#pragma unroll
-                            for (int c = 0; c < 2; ++c) {
-                                uint32_t pk[16];
-#pragma unroll
-                                for (int e = 0; e < 16; ++e) {
-                                    const float p0 = ex2_approx(fmaf(__uint_as_float(s[c][2 * e]), p.qk, base));
-                                    const float p1 = ex2_approx(fmaf(__uint_as_float(s[c][2 * e + 1]), p.qk, base));
-                                    sum[e & 3] += p0 + p1;
-                                    pk[e] = cvt_bf16x2(p0, p1);
-                                }
-                                tmem_st_x16(tS + (c0 + c) * 16, pk);
+                                        for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * a);
+                                        tmem_st_x16(tO + c, y);
+                                    }
                             }
-                        };
-                        weigh(0);
-                        fetch(2);
-                        weigh(2);
-                        l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                            const float base = m == -INFINITY ? 0.f : -m;
+                            const uint64_t qk2 = pair_of(p.qk, p.qk), base2 = pair_of(base, base);
+                            uint64_t sum2[2] = {0, 0};
+                            float big = -INFINITY;
+#pragma unroll
+                            for (int c0 = 0; c0 < 4; c0 += 2) {
+                                fetch(c0);
+                                if (!again) big = largest(big);
+#pragma unroll
+                                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                    for (int e = 0; e < 16; ++e) {
+                                        float z0, z1;
+                                        unpair(fma2(pair_of(at(c, 2 * e), at(c, 2 * e + 1)), qk2, base2), z0, z1);
+                                        const float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
+                                        sum2[e & 1] = add2(sum2[e & 1], pair_of(p0, p1));
+                                        pk[c0 + c][e] = cvt_bf16x2(p0, p1);
+                                    }
+                            }
+                            if (again || !__any_sync(0xffffffffu, big * p.qk > m + PR_LAG)) {
+                                float a0, a1;
+                                unpair(add2(sum2[0], sum2[1]), a0, a1);
+                                sum = a0 + a1;
+                                break;
+                            }
+                            again = true;
+                        }
+                        l += sum;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_st_x16(tS + c * 16, pk[c]);
                     }
                     if (masked && t0 + row >= x.w.len) {
                         // one position's values a thread: zero past the end, and where not
@@ -643,6 +725,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     tmem_st_wait();
                     tc_fence_before();
                     mbar_arrive(&p_full[w]);
+                    if (i == 0 && piece_masked) learn_tree();   // while the products run
                 }
                 if (mine_tiles > 0) {
                     wait(&o_full[w], on++ & 1);
@@ -651,8 +734,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             }
             // ---------------------------------------- the piece's result
             if (!x.w.bad) {
-                wait(&told[k & 3], (k >> 2) & 1);
-                bad |= s_bad[k & 3] != 0;
+                wait(&told[k & 7], (k >> 3) & 1);
+                bad |= s_bad[k & 7] != 0;
                 ++k;
             }
             const bool merge = x.solo && x.tiles > 1 && !x.w.bad;   // both streams hold parts of the same pairs
@@ -679,25 +762,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             }
             if (bad) M = L = NAN;
             const float inv = 1.f / L;
-            // values left out above, at the positions of this piece that the row sees
-            auto left_out = [&](int d) {
-                float sum = 0.f;
-                for (int j = 0; j <= r; ++j) {
-                    const int t = x.w.len + j;
-                    if (t < x.kt * PR_KT || t >= (x.kt + x.tiles) * PR_KT) continue;
-                    bool sees = !tree || j == 0 || j == r;
-                    for (int a = r; a > j && !sees;) {
-                        a = s_par[w][a];
-                        sees = a == j;
-                    }
-                    const int page = p.table[(int64_t)x.b * p.max_pages + (t >> p.page_shift)];
-                    if (!sees || page < 0 || page >= p.num_pages) continue;
-                    const int64_t at = (((int64_t)page << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * p.G + x.g;
-                    const float v = pg_bf16_to_f32(reinterpret_cast<const uint16_t*>(p.V)[at * p.D + d]);
-                    if (!(fabsf(v) < INFINITY)) sum += v;
-                }
-                return sum;
-            };
+            const int64_t out_pair = (int64_t)(x.w.r0 + r) * p.H + x.g * p.hq + (row - row / p.hq * p.hq);
             float* xb = reinterpret_cast<float*>(sX);   // [128][32]: the second stream's rows, pieces of 16 bytes swizzled
             for (int c0 = 0; c0 < p.D; c0 += PR_XC) {
                 if (merge) {
@@ -735,15 +800,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                             v[4 * e + 3] = fmaf(y.w, w1, v[4 * e + 3]);
                         }
                     }
-                    if (odd && !bad) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (c0 + e < p.D) v[e] += left_out(c0 + e);
-                    }
                     // groups of 16 dims: the head size is a multiple of that
                     if (whole) {
-                        const int64_t o = (int64_t)(x.w.r0 + r) * p.H + x.g * p.hq + (row - row / p.hq * p.hq);
-                        uint4* dst = reinterpret_cast<uint4*>(p.out + o * p.D + c0);
+                        uint4* dst = reinterpret_cast<uint4*>(p.out + out_pair * p.D + c0);
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
                             if (c0 + (e >> 1) * 16 < p.D)
@@ -764,19 +823,48 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             if (bad && row == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)x.b);
             if (writer && !whole) p.stat[slot * 2 * PR_ROWS + prow] = make_float2(M, L);
             if (writer && whole && p.lse)
-                p.lse[(int64_t)(x.w.r0 + r) * p.H + x.g * p.hq + (row - row / p.hq * p.hq)] = (M + __log2f(L)) * LN2;
+                p.lse[out_pair] = (M + __log2f(L)) * LN2;
             if (tid == 0 && !whole && x.kt == 0) {
                 const int64_t ts = begin + (count - left);   // the item's first tile in the flat sequence
                 const int pieces = (int)((ts + x.w.nt - 1) / per) - (int)blockIdx.x + 1;
                 p.join[blockIdx.x] = make_int4(pieces, x.w.r0 + 2 * x.mp * p.rpt, x.rows * p.hq, x.g);
                 shared_item = true;
             }
+            if (odd && !bad) {
+                // rare: the values left out above, added behind the results to the rows
+                // that see them (inf or NaN whatever is there)
+                learn_tree();
+                for (int j = 0; j <= r && writer; ++j) {
+                    const int t = x.w.len + j;
+                    if (t < x.kt * PR_KT || t >= (x.kt + x.tiles) * PR_KT) continue;
+                    bool sees = !tree || j == 0 || j == r;
+                    for (int a = r; a > j && !sees;) {
+                        a = s_par[w][a];
+                        sees = a == j;
+                    }
+                    const int page = p.table[(int64_t)x.b * p.max_pages + (t >> p.page_shift)];
+                    if (!sees || page < 0 || page >= p.num_pages) continue;
+                    const int64_t at = (((int64_t)page << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * p.G + x.g;
+                    const uint16_t* v = reinterpret_cast<const uint16_t*>(p.V) + at * p.D;
+#pragma unroll 1
+                    for (int d = 0; d < p.D; ++d) {
+                        const float y = pg_bf16_to_f32(v[d]);
+                        if (fabsf(y) < INFINITY) continue;
+                        if (whole) {
+                            uint16_t* o = p.out + out_pair * p.D + d;
+                            *o = pg_f32_to_bf16(pg_bf16_to_f32(*o) + y);
+                        } else {
+                            float* o = reinterpret_cast<float*>(
+                                p.part + ((int64_t)slot * (p.D / 4) + d / 4) * 2 * PR_ROWS + prow) + d % 4;
+                            *o += y;
+                        }
+                    }
+                }
+            }
             if (!x.w.bad) n += x.tiles;
             left -= x.tiles;
-            if (left > 0) {
-                named_sync(3, 256);   // s_odd and the exchanged rows are read to their end
-                piece_next(p, x, left);
-            }
+            named_sync(1 + w, 128);   // the stream has read the piece
+            if (row == 0) mbar_arrive(&piece_free[turn & 7]);
         }
         if (tid == 0 && !shared_item) p.join[blockIdx.x] = make_int4(0, 0, 0, 0);
         tc_fence_before();

@@ -41,10 +41,10 @@ class Case:
             self.v_scale = rng.uniform(0.3, 3.0, (layers, G)).astype(np.float32)
         self.dtype = torch.float8_e4m3fn if kv == "e4m3" else torch.bfloat16
         for b in range(B):
-            for t in range(self.lens[b] + self.rows[b]):
-                pg = self.table[b, t // ps]
-                K[:, pg, t % ps] = torch.from_numpy(rng.standard_normal((layers, G, D)) * spread).float()
-                V[:, pg, t % ps] = torch.from_numpy(rng.standard_normal((layers, G, D))).float()
+            T = self.lens[b] + self.rows[b]
+            pg, at = self.table[b, np.arange(T) // ps], np.arange(T) % ps
+            K[:, pg, at] = torch.from_numpy(rng.standard_normal((layers, T, G, D)) * spread).float()
+            V[:, pg, at] = torch.from_numpy(rng.standard_normal((layers, T, G, D))).float()
         self.K, self.V = K.to(self.dtype), V.to(self.dtype)
         self.pos_off = np.cumsum([first_row] + self.rows).astype(np.int32)
         self.P = int(self.pos_off[-1]) + extra_rows
@@ -74,10 +74,8 @@ class Case:
     def dense(self, b, g, which):
         """[T, D] float64 keys or values of a sequence, scaled."""
         pool = (self.K if which == "K" else self.V)[self.layer]
-        T = self.lens[b] + self.rows[b]
-        x = np.empty((T, self.D))
-        for t in range(T):
-            x[t] = pool[self.table[b, t // self.ps], t % self.ps, g].float().numpy()
+        t = np.arange(self.lens[b] + self.rows[b])
+        x = pool.float()[self.table[b, t // self.ps], t % self.ps, g].numpy().astype(np.float64)
         sc = self.k_scale if which == "K" else self.v_scale
         return x if sc is None else x * float(sc[self.layer, g])
 

@@ -89,6 +89,22 @@ def test_rounds(lens, rows, kinds, H, G, D, ps, kv):
     check(ref.Case(2, lens, rows, H, G, D, ps, kv, kinds=kinds))
 
 
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,rows,kinds,H,G,D,ps", [
+    # a dozen tiles and several pieces a CTA: one product of rows and two, changing within a stretch
+    ((2500, 1900, 2222, 700, 2600, 1), (150, 17, 200, 1, 61, 130), (1, 0, 1, 0, 1, 1), 8, 8, 64, 16),
+    ((3000,) * 9, (140, 5) * 4 + (129,), (1,) * 9, 8, 8, 32, 64),
+    # pieces of one tile next to each other
+    (tuple(range(20, 140, 2)), (3,) * 60, (1,) * 60, 8, 8, 16, 8),
+])
+def test_many_tiles(lens, rows, kinds, H, G, D, ps, kv):
+    check(ref.Case(9, lens, rows, H, G, D, ps, kv, kinds=kinds))
+
+
+def test_many_tiles_of_single_tokens():
+    check(ref.Case(10, (9000, 100, 5000, 7000), (1,) * 4, 16, 8, 32, 32))
+
+
 def test_all_chains_without_a_tree_description():
     c = ref.Case(3, (40, 5), (9, 17), 4, 2, 64, 16)
     check(c, trees=False)
