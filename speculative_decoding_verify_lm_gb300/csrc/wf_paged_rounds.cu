@@ -167,6 +167,12 @@ __device__ __forceinline__ uint64_t desc_of(uint32_t lo) {
     return ((uint64_t)HI << 32) | lo;
 }
 __device__ __forceinline__ void fence_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// acc stays 0 while no bf16 of w is infinite or NaN, and is NaN from then on
+__device__ __forceinline__ uint32_t bf16x2_probe(uint32_t w, uint32_t acc) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "r"(acc));
+    return r;
+}
 // whether `pred` holds in all of the named barrier's threads
 __device__ __forceinline__ bool named_all(int id, int threads, bool pred) {
     uint32_t r;
@@ -497,7 +503,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     for (int i = 0; i < steps; ++i) {
                         const int at = place_of(i) + 1, slot = at % PR_RING;
                         arrived(at);
-                        if (i + 1 < steps) arrived(place_of(i + 1));
+                        // Two products share every tile: the next keys are here by now, and
+                        // both products go in one turn.  One product: its next keys are two
+                        // tiles ahead and may be waiting for the place of the values that
+                        // go now.
+                        const int next = place_of(i + 1);
+                        const bool both = !solo && i + 1 < steps;
+                        if (both) arrived(next);
                         wait(&p_full[w], pn++ & 1);
                         take_turn();
                         if (!ok) break;
@@ -509,9 +521,17 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                                 umma_ts(tO, tS + ks * 8, desc_of(b + ks * 128), p.idesc_o, (i | ks) != 0);
                             release(slot);
                             if (i + 1 == steps) umma_commit(&o_full[w]);
-                            else scores(i + 1);
+                            else if (both) scores(i + 1);
                         }
                         give_turn();
+                        if (i + 1 < steps && !both) {
+                            arrived(next);
+                            take_turn();
+                            if (!ok) break;
+                            tc_fence_after();
+                            if (elect_one()) scores(i + 1);
+                            give_turn();
+                        }
                     }
                     n += tiles;
                 }
@@ -701,24 +721,33 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
 #pragma unroll
                         for (int blk = 0; blk < BLK; ++blk) {
                             uint8_t* base = sR + slot * TILE + blk * PR_KT * 128 + row * 128;
-                            uint4 y[8];
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) y[c] = *reinterpret_cast<const uint4*>(base + ((c ^ (row & 7)) << 4));
+                            auto piece = [&](int c) { return reinterpret_cast<uint4*>(base + ((c ^ (row & 7)) << 4)); };
+                            uint32_t probe[2] = {0, 0};
 #pragma unroll
                             for (int c = 0; c < 8; ++c) {
-                                uint32_t* e = &y[c].x;
-                                bool hit = past;
+                                if (past) {
+                                    *piece(c) = make_uint4(0, 0, 0, 0);
+                                } else {
+                                    const uint4 y = *piece(c);
+                                    probe[0] = bf16x2_probe(y.y, bf16x2_probe(y.x, probe[0]));
+                                    probe[1] = bf16x2_probe(y.w, bf16x2_probe(y.z, probe[1]));
+                                }
+                            }
+                            if (((probe[0] | probe[1]) & 0x7FFF7FFFu) == 0) continue;
+                            odd = true;
+#pragma unroll 1
+                            for (int c = 0; c < 8; ++c) {
+                                uint4 y = *piece(c);
+                                uint32_t* e = &y.x;
 #pragma unroll
                                 for (int u = 0; u < 4; ++u) {
-                                    if (past) e[u] = 0;
-                                    if ((e[u] & 0x7F80u) == 0x7F80u) e[u] &= 0xFFFF0000u, hit = true;
-                                    if ((e[u] & 0x7F800000u) == 0x7F800000u) e[u] &= 0x0000FFFFu, hit = true;
+                                    if ((e[u] & 0x7F80u) == 0x7F80u) e[u] &= 0xFFFF0000u;
+                                    if ((e[u] & 0x7F800000u) == 0x7F800000u) e[u] &= 0x0000FFFFu;
                                 }
-                                if (hit) *reinterpret_cast<uint4*>(base + ((c ^ (row & 7)) << 4)) = y[c];
-                                odd |= hit;
+                                *piece(c) = y;
                             }
                         }
-                        if (odd && !past) atomicOr(odd_word, 1);
+                        if (odd) atomicOr(odd_word, 1);
                         fence_async_smem();
                     }
                     __syncwarp();
