@@ -9,9 +9,10 @@
 // full batch: both have to run without a pause.
 //
 // The work is the flat sequence of 128-position tiles of every (sequence, up to
-// 256 pairs, KV head), in equal stretches for one CTA an SM; the pieces of an
-// item that several CTAs share go to the workspace and a second, small kernel
-// joins them in order.
+// 256 pairs, KV head), a tile weighing 3 with two products of rows and 2 with
+// one (3,500 and 2,300 cycles), in equal stretches for one CTA an SM; the
+// pieces of an item that several CTAs share go to the workspace and a second,
+// small kernel joins them in order.
 //
 // Inside a CTA two streams of softmax warps (four each, a thread a row) work
 // in turn, so that the tensor cores compute one stream's products while the
@@ -63,7 +64,7 @@ struct RoundsParams {
     float2* stat;            // [CTA][2][256] (maximum, sum)
     int4* join;              // [CTA] the shared item that begins in it: pieces, first row, pairs, KV head
     float qk;                // scale * log2(e)
-    int P, H, G, D, hq, B, page_shift, num_pages, max_pages, max_rows, min_tiles;
+    int P, H, G, D, hq, B, page_shift, num_pages, max_pages, max_rows;
     int rpt;                 // query rows of a product: 128 / hq
     int box_rows;            // rows of a copy: min(page_size, 128)
     uint32_t idesc_s, idesc_o;
@@ -97,34 +98,22 @@ __device__ __forceinline__ RoundSeq round_seq(const RoundsParams& p, int b) {
     return w;
 }
 
+// Weight of a tile of the query rows 2 rpt mp ..
+__device__ __forceinline__ int tile_weight(const RoundsParams& p, const RoundSeq& w, int mp) {
+    return w.rows - mp * 2 * p.rpt > p.rpt ? 3 : 2;
+}
+// Weight of a whole sequence: every tile of its products is weighed alike but the last rows'.
+__device__ __forceinline__ int64_t seq_weight(const RoundsParams& p, const RoundSeq& w) {
+    return w.mp == 0 ? 0 : (int64_t)p.G * w.nt * (3 * (w.mp - 1) + tile_weight(p, w, w.mp - 1));
+}
+
 // One piece of the CTA's stretch: tiles [kt, kt + tiles) of (sequence b, query rows 2 rpt mp .., KV head g).
 struct Piece {
     RoundSeq w;
-    int b, mp, g, kt, tiles, rows;   // rows: query rows of the item
-    bool solo;   // one product: the streams share it and take every second tile
+    int b, mp, g, kt, tiles, rows;   // rows: query rows of the item; tiles: 0 ends the stretch
+    int pieces;                      // of the item, if it begins here and ends elsewhere; else 0
+    bool solo;                       // one product: the streams share it and take every second tile
 };
-
-__device__ __forceinline__ void piece_shape(const RoundsParams& p, Piece& x, int left) {
-    x.tiles = min(left, x.w.nt - x.kt);
-    x.rows = min(2 * p.rpt, x.w.rows - x.mp * 2 * p.rpt);
-    x.solo = x.rows <= p.rpt;
-}
-
-// The piece behind this one; `left` tiles of the stretch remain (> 0).
-__device__ __forceinline__ void piece_next(const RoundsParams& p, Piece& x, int left) {
-    x.kt = 0;   // a piece ends at its item's end unless the stretch ends
-    if (++x.g == p.G) {
-        x.g = 0;
-        if (++x.mp == x.w.mp) {
-            x.mp = 0;
-            do {
-                ++x.b;
-                x.w = round_seq(p, x.b);
-            } while (x.w.mp == 0);
-        }
-    }
-    piece_shape(p, x, left);
-}
 
 // ----------------------------------------------------------------- tensor memory and barriers
 __device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -288,11 +277,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     // ------------------------------------------------ this CTA's stretch (as in the single-token kernel)
     const int run = (p.B + PR_THREADS - 1) / PR_THREADS;
     int64_t mine = 0;
+    bool heavy = false;   // a tile of weight 3
     for (int i = 0; i < run; ++i) {
         const int b = tid * run + i;
         if (b < p.B) {
             const RoundSeq w = round_seq(p, b);
-            mine += (int64_t)w.mp * p.G * w.nt;
+            mine += seq_weight(p, w);
+            heavy |= w.mp > 0 && tile_weight(p, w, 0) == 3;
             if (w.bad && blockIdx.x == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)b);
         }
     }
@@ -304,7 +295,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     }
     if (lane == 31) s_scan[warp] = inc;
     tc_fence_before();
-    __syncthreads();
+    heavy = __syncthreads_or(heavy);
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     int64_t total = 0, before = inc - mine;
@@ -314,16 +305,16 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         total += s_scan[w];
     }
     int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    if (per < p.min_tiles) per = p.min_tiles;
+    // every stretch between an item's first and its last holds one of its tiles
+    if (per < (heavy ? 3 : 2)) per = heavy ? 3 : 2;
     const int64_t begin = (int64_t)blockIdx.x * per;
     const int64_t end = begin + per < total ? begin + per : total;
-    const int count = begin < end ? (int)(end - begin) : 0;
-    if (count > 0 && mine > 0 && before <= begin && begin < before + mine) {
+    if (begin < end && mine > 0 && before <= begin && begin < before + mine) {
         int64_t at = before;
         int b = tid * run;
         for (;; ++b) {
             const RoundSeq w = round_seq(p, b);
-            const int64_t n = (int64_t)w.mp * p.G * w.nt;
+            const int64_t n = seq_weight(p, w);
             if (begin < at + n) break;
             at += n;
         }
@@ -336,27 +327,65 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             // ---------------------------------------- copies: tile n's keys to ring place 2 n, its values to 2 n + 1
             const uint64_t pol = policy_evict_first();
             const int per_tile = PR_KT / p.box_rows;   // boxes of a tile: at most 16
-            Piece x;
-            if (count > 0) {
+            // the stretch's first item: `start`, the weight before it; its tile kt is
+            // the first that starts in the stretch
+            Piece x = {};
+            int64_t start = begin;
+            int weight = 2;
+            auto next_item = [&]() {
+                start += (int64_t)x.w.nt * weight;
+                x.kt = 0;
+                if (++x.g == p.G) {
+                    x.g = 0;
+                    if (++x.mp == x.w.mp) {
+                        x.mp = 0;
+                        do {
+                            if (++x.b >= p.B) {
+                                start = end;   // nothing is left
+                                return;
+                            }
+                            x.w = round_seq(p, x.b);
+                        } while (x.w.mp == 0);
+                    }
+                }
+                weight = tile_weight(p, x.w, x.mp);
+            };
+            if (begin < end) {
                 x.b = s_pb;
                 x.w = round_seq(p, x.b);
-                const int item = (int)(s_plan / x.w.nt);
-                x.kt = (int)(s_plan - (int64_t)item * x.w.nt);
-                x.mp = item / p.G;
-                x.g = item - x.mp * p.G;
-                piece_shape(p, x, count);
+                const int64_t full = (int64_t)p.G * x.w.nt * 3;
+                x.mp = (int)(s_plan / full);
+                if (x.mp > x.w.mp - 1) x.mp = x.w.mp - 1;
+                weight = tile_weight(p, x.w, x.mp);
+                const int64_t in_rows = s_plan - x.mp * full;
+                x.g = (int)(in_rows / ((int64_t)x.w.nt * weight));
+                const int64_t in_item = in_rows - (int64_t)x.g * x.w.nt * weight;
+                start = begin - in_item;
+                x.kt = (int)((in_item + weight - 1) / weight);
+                if (x.kt == x.w.nt) next_item();
             }
             int n = 0, k = 0;                          // tiles, pieces that have any
-            for (int left = count, turn = 0; left > 0; ++turn) {
+            for (int turn = 0;; ++turn) {
                 if (turn >= 8 && !mbar_wait(&piece_free[turn & 7], ((turn >> 3) & 1) ^ 1, p.timeout_ns, abort_flag)) {
                     *abort_flag = 1;
                     if (lane == 0) record_error(p.ctrl, WF_ERR_TIMEOUT, 0x801u);
                     break;
                 }
+                x.tiles = 0;
+                if (begin < end && start + (int64_t)x.kt * weight < end) {
+                    const int64_t upto = (end - start + weight - 1) / weight;
+                    x.tiles = (int)(upto < x.w.nt ? upto : x.w.nt) - x.kt;
+                    x.rows = min(2 * p.rpt, x.w.rows - x.mp * 2 * p.rpt);
+                    x.solo = x.rows <= p.rpt;
+                    x.pieces = 0;
+                    if (x.kt == 0 && x.tiles < x.w.nt)
+                        x.pieces = (int)((start + (int64_t)(x.w.nt - 1) * weight) / per) - (int)blockIdx.x + 1;
+                }
                 if (lane == 0) {
                     s_piece[turn & 7] = x;
                     mbar_arrive(&piece_ready[turn & 7]);
                 }
+                if (x.tiles == 0) break;
                 bool bad = false;
                 if (!x.w.bad) {
                     int page = 0;
@@ -420,8 +449,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     ++k;
                 }
                 if (*abort_flag) break;
-                left -= x.tiles;
-                if (left > 0) piece_next(p, x, left);
+                next_item();
             }
             // let every copy issued land before the shared memory goes
             for (int at = max(0, 2 * n - PR_RING); at < 2 * n; ++at)
@@ -460,12 +488,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) atomicExch(&s_turn, 0);
             };
-            for (int left = count, turn = 0; left > 0 && ok; ++turn) {
+            for (int turn = 0; ok; ++turn) {
                 wait(&piece_ready[turn & 7], (turn >> 3) & 1);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 const Piece& x = s_piece[turn & 7];
                 const int tiles = x.tiles;
+                if (tiles == 0) break;
                 if (!x.w.bad) {
                     const int steps = __shfl_sync(0xffffffffu, x.solo ? (x.tiles - w + 1) / 2 : x.tiles, 0);
                     const bool solo = __shfl_sync(0xffffffffu, (int)x.solo, 0) != 0;
@@ -535,7 +564,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     }
                     n += tiles;
                 }
-                left -= tiles;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&piece_free[turn & 7]);
             }
@@ -551,7 +579,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         const uint32_t tS = tmem + lanes + w * 128, tO = tmem + lanes + 256 + w * 128;
         uint32_t sn = 0, on = 0;   // scores, outputs taken
         int n = 0, k = 0;          // tiles before this piece, pieces that have any
-        int turn = 0;              // pieces
         bool shared_item = false;  // an item begins here and ends elsewhere
         bool ok = true;
         auto wait = [&](uint64_t* bar, uint32_t parity) {
@@ -561,12 +588,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 record_error(p.ctrl, WF_ERR_TIMEOUT, 0x820u);
             }
         };
-        for (int left = count; left > 0; ++turn) {
+        for (int turn = 0;; ++turn) {
             wait(&piece_ready[turn & 7], (turn >> 3) & 1);
             // all of both streams go on, or none (also: s_odd and the exchanged rows of
             // the piece before are read to their end)
             if (!named_all(3, 256, ok)) break;
             const Piece& x = s_piece[turn & 7];
+            if (x.tiles == 0) break;
             const int first = (2 * x.mp + (x.solo ? 0 : w)) * p.rpt;   // first query row of this stream's product
             const int r = first + row / p.hq;
             const bool live = row < p.rpt * p.hq && r < x.w.rows;
@@ -853,10 +881,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             if (writer && !whole) p.stat[slot * 2 * PR_ROWS + prow] = make_float2(M, L);
             if (writer && whole && p.lse)
                 p.lse[out_pair] = (M + __log2f(L)) * LN2;
-            if (tid == 0 && !whole && x.kt == 0) {
-                const int64_t ts = begin + (count - left);   // the item's first tile in the flat sequence
-                const int pieces = (int)((ts + x.w.nt - 1) / per) - (int)blockIdx.x + 1;
-                p.join[blockIdx.x] = make_int4(pieces, x.w.r0 + 2 * x.mp * p.rpt, x.rows * p.hq, x.g);
+            if (tid == 0 && x.pieces > 0) {
+                p.join[blockIdx.x] = make_int4(x.pieces, x.w.r0 + 2 * x.mp * p.rpt, x.rows * p.hq, x.g);
                 shared_item = true;
             }
             if (odd && !bad) {
@@ -891,7 +917,6 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 }
             }
             if (!x.w.bad) n += x.tiles;
-            left -= x.tiles;
             named_sync(1 + w, 128);   // the stream has read the piece
             if (row == 0) mbar_arrive(&piece_free[turn & 7]);
         }
@@ -1030,7 +1055,6 @@ wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args*
     p.num_pages = c->num_pages;
     p.max_pages = c->max_pages;
     p.max_rows = a->max_rows;
-    p.min_tiles = 1;
     p.rpt = PR_ROWS / p.hq;
     p.box_rows = c->page_size < PR_KT ? c->page_size : PR_KT;
     p.idesc_s = umma_idesc_bf16(PR_ROWS, PR_KT);
