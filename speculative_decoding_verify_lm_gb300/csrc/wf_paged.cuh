@@ -115,6 +115,12 @@ __device__ __forceinline__ void pg_cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// a / b of numbers that are seldom past 32 bits, b > 0
+__device__ __forceinline__ int64_t pg_quotient(int64_t a, int64_t b) {
+    if (((uint64_t)a | (uint64_t)b) >> 32 == 0) return (int64_t)((uint32_t)a / (uint32_t)b);
+    return a / b;
+}
+
 // Last sequence whose first row is at or before row p: the largest b with
 // off[b] <= p, or -1 (warp-collective, the same answer in every lane).  Each
 // step loads 32 samples, so 1,024 sequences take two dependent loads.

@@ -304,7 +304,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
     }
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    int64_t per = pg_quotient(total + gridDim.x - 1, gridDim.x);
     // every stretch between an item's first and its last holds one of its tiles
     if (per < (heavy ? 3 : 2)) per = heavy ? 3 : 2;
     const int64_t begin = (int64_t)blockIdx.x * per;
@@ -354,14 +354,14 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 x.b = s_pb;
                 x.w = round_seq(p, x.b);
                 const int64_t full = (int64_t)p.G * x.w.nt * 3;
-                x.mp = (int)(s_plan / full);
+                x.mp = (int)pg_quotient(s_plan, full);
                 if (x.mp > x.w.mp - 1) x.mp = x.w.mp - 1;
                 weight = tile_weight(p, x.w, x.mp);
                 const int64_t in_rows = s_plan - x.mp * full;
-                x.g = (int)(in_rows / ((int64_t)x.w.nt * weight));
+                x.g = (int)pg_quotient(in_rows, (int64_t)x.w.nt * weight);
                 const int64_t in_item = in_rows - (int64_t)x.g * x.w.nt * weight;
                 start = begin - in_item;
-                x.kt = (int)((in_item + weight - 1) / weight);
+                x.kt = ((int)in_item + weight - 1) / weight;
                 if (x.kt == x.w.nt) next_item();
             }
             int n = 0, k = 0;                          // tiles, pieces that have any
@@ -373,13 +373,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 }
                 x.tiles = 0;
                 if (begin < end && start + (int64_t)x.kt * weight < end) {
-                    const int64_t upto = (end - start + weight - 1) / weight;
+                    const int64_t upto = pg_quotient(end - start + weight - 1, weight);
                     x.tiles = (int)(upto < x.w.nt ? upto : x.w.nt) - x.kt;
                     x.rows = min(2 * p.rpt, x.w.rows - x.mp * 2 * p.rpt);
                     x.solo = x.rows <= p.rpt;
                     x.pieces = 0;
                     if (x.kt == 0 && x.tiles < x.w.nt)
-                        x.pieces = (int)((start + (int64_t)(x.w.nt - 1) * weight) / per) - (int)blockIdx.x + 1;
+                        x.pieces = (int)pg_quotient(start + (int64_t)(x.w.nt - 1) * weight, per) - (int)blockIdx.x + 1;
                 }
                 if (lane == 0) {
                     s_piece[turn & 7] = x;
@@ -931,10 +931,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
 // ------------------------------------------------------------------ join
 // The pieces of a shared item, added in order: piece k is CTA c + k's, its
 // second slot for the item's first piece, else its first.  Block (c, y): pairs
-// 32 y .. of the item that begins in CTA c; lanes are pairs, warps take a
-// quarter of the dims' groups of four; results leave by way of shared memory in
-// whole rows.
-constexpr int RJ_WARPS = 4;
+// 32 y .. of the item that begins in CTA c; lanes are pairs, warps share out the
+// dims' groups of four; results leave by way of shared memory in whole rows.
+constexpr int RJ_WARPS = 8;
+constexpr int RJ_BATCH = 8;   // pieces whose statistics and values are in flight together
 
 __global__ void __launch_bounds__(RJ_WARPS * 32)
     rounds_join_kernel(const int4* __restrict__ join, const float4* __restrict__ part, const float2* __restrict__ stat,
@@ -951,31 +951,44 @@ __global__ void __launch_bounds__(RJ_WARPS * 32)
     const int quads = D / 4;
     const float2* st = stat + (in ? pr : first);
     const float4* src = part + (in ? pr : first);
-    auto slot = [&](int k) { return (int64_t)(c + k) * 2 + (k == 0); };
-    float M = -INFINITY;
-#pragma unroll 8
-    for (int k = 0; k < j.x; ++k) M = fmaxf(M, __ldcg(st + slot(k) * 2 * PR_ROWS).x);
     constexpr int MQ = 128 / 4 / RJ_WARPS;   // groups of four dims a warp takes at most
     float4 v[MQ];
-    float L = 0.f;
+    float M = -INFINITY, L = 0.f;
 #pragma unroll
     for (int u = 0; u < MQ; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-    for (int k = 0; k < j.x; ++k) {
-        const float2 s2 = __ldcg(st + slot(k) * 2 * PR_ROWS);
-        float4 y[MQ];
+    for (int k0 = 0; k0 < j.x; k0 += RJ_BATCH) {
+        float2 s2[RJ_BATCH];
+        float4 y[RJ_BATCH][MQ];
 #pragma unroll
-        for (int u = 0; u < MQ; ++u)
-            if (warp + u * RJ_WARPS < quads) y[u] = __ldcg(src + (slot(k) * quads + warp + u * RJ_WARPS) * 2 * PR_ROWS);
-        const float w = s2.x == -INFINITY ? 0.f : ex2_approx(s2.x - M);
-        L = fmaf(s2.y, w, L);
+        for (int k = 0; k < RJ_BATCH; ++k) {
+            const bool is = k0 + k < j.x;
+            const int64_t slot = (int64_t)(c + k0 + k) * 2 + (k0 + k == 0);
+            s2[k] = is ? __ldcg(st + slot * 2 * PR_ROWS) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-        for (int u = 0; u < MQ; ++u) {
-            if (warp + u * RJ_WARPS >= quads) continue;
-            v[u].x = fmaf(y[u].x, w, v[u].x);
-            v[u].y = fmaf(y[u].y, w, v[u].y);
-            v[u].z = fmaf(y[u].z, w, v[u].z);
-            v[u].w = fmaf(y[u].w, w, v[u].w);
+            for (int u = 0; u < MQ; ++u)
+                y[k][u] = is && warp + u * RJ_WARPS < quads
+                              ? __ldcg(src + (slot * quads + warp + u * RJ_WARPS) * 2 * PR_ROWS)
+                              : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        float top = M;
+#pragma unroll
+        for (int k = 0; k < RJ_BATCH; ++k) top = fmaxf(top, s2[k].x);
+        const float a = M == -INFINITY ? 0.f : ex2_approx(M - top);
+        M = top;
+        L *= a;
+#pragma unroll
+        for (int u = 0; u < MQ; ++u) v[u] = make_float4(v[u].x * a, v[u].y * a, v[u].z * a, v[u].w * a);
+#pragma unroll
+        for (int k = 0; k < RJ_BATCH; ++k) {
+            const float w = s2[k].x == -INFINITY ? 0.f : ex2_approx(s2[k].x - top);
+            L = fmaf(s2[k].y, w, L);
+#pragma unroll
+            for (int u = 0; u < MQ; ++u) {
+                v[u].x = fmaf(y[k][u].x, w, v[u].x);
+                v[u].y = fmaf(y[k][u].y, w, v[u].y);
+                v[u].z = fmaf(y[k][u].z, w, v[u].z);
+                v[u].w = fmaf(y[k][u].w, w, v[u].w);
+            }
         }
     }
     const float inv = 1.f / L;

@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
     }
-    int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    int64_t per = pg_quotient(total + gridDim.x - 1, gridDim.x);
     if (per < p.min_tiles) per = p.min_tiles;
     const int64_t begin = (int64_t)blockIdx.x * per;
     const int64_t end = begin + per < total ? begin + per : total;
@@ -229,7 +229,7 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
     c.b = s_pb;
     c.w = token_seq<KT>(p, c.b);
     {
-        const int item = (int)(s_plan / c.w.nt);
+        const int item = (int)pg_quotient(s_plan, c.w.nt);
         c.kt = (int)(s_plan - (int64_t)item * c.w.nt);
         c.g = item / p.mt;
         c.m = item - c.g * p.mt;
@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
             }
             if (tid < heads) p.stat[slot * 16 + tid] = row_stat(tid);
             const int64_t ts = begin + (count - left) - kt_first;   // the item's first tile in the flat sequence
-            const int c0 = (int)(ts / per), pieces = (int)((ts + c.w.nt - 1) / per) - c0 + 1;
+            const int c0 = (int)pg_quotient(ts, per), pieces = (int)pg_quotient(ts + c.w.nt - 1, per) - c0 + 1;
             consumer_sync();
             if (tid == 0) s_last = arrive_acq_rel(p.cnt + c0) == (uint32_t)(pieces - 1);
             consumer_sync();
