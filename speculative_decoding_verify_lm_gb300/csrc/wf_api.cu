@@ -60,7 +60,8 @@ wf_status launch_pages_reserve(const wf_paged_cache* c, const int32_t* pos_off, 
 wf_status launch_pages_fork(const wf_paged_cache* c, const int32_t* src, const int32_t* dst, int n,
                             int32_t* cache_len, void* ws, cudaStream_t s);
 wf_status launch_pages_trim(const wf_paged_cache* c, const int32_t* cache_len, void* ws, cudaStream_t s);
-wf_status launch_paged_attention(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s);
+wf_status launch_paged_token(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s);
+wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s);
 
 static std::atomic<uint64_t> g_timeout_ns{2000000000ull};
 uint64_t wait_timeout_ns() { return g_timeout_ns.load(std::memory_order_relaxed); }
@@ -523,7 +524,10 @@ wf_status wf_paged_attention(const wf_paged_cache* c, const wf_paged_attn_args* 
     if (!aligned16(a->q) || !aligned16(a->out) || a->q_stride % 8 || a->q_stride < (int64_t)a->H * c->D)
         return WF_ERR_INVALID_ARG;
     WF_TRY(check_paged(c, a->H, a->max_rows, false, ws, ws_bytes));
-    return launch_paged_attention(c, a, ws, stream);
+    if (a->P == 0) return WF_OK;
+    // one row a sequence: the kernel for single tokens, bound by the cache's bytes;
+    // drafted rows: the tensor-core one, which shares a read of the cache among them
+    return a->max_rows == 1 ? launch_paged_token(c, a, ws, stream) : launch_paged_rounds(c, a, ws, stream);
 }
 
 wf_status wf_paged_compact(const wf_paged_cache* c, const int32_t* n_accept, const int32_t* path, int path_stride,

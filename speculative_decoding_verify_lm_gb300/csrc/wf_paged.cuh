@@ -9,7 +9,7 @@ namespace wf {
 // ----------------------------------------------------------------- workspace
 // control block | arrival counters (zero at rest) | page bookkeeping of a
 // reserve call | shared items and partial results of the attention's splits
-constexpr int PA_TILE_M = 16;       // (row, head) pairs of a small-tile item
+constexpr int PA_TILE_M = 16;       // query heads of a single-token item at most
 constexpr int PA_MAX_CTAS = 640;    // most CTAs of a single-token launch
 constexpr int PA_MAX_ROUND_CTAS = 160;   // and of a launch over drafted rows
 constexpr int PA_ROUND_M = 256;     // pairs of an item there

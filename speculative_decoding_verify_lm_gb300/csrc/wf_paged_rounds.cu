@@ -26,6 +26,11 @@
 // 128-byte swizzle); each stream has a warp of its own that issues its products
 // (one for both spent most of its time on barriers: 139 us for the batch of 32).
 //
+// An 8-bit cache goes through fp16 operands (the products take no mixed types):
+// its rows are copied raw and one more warp widens them into the ring, exactly;
+// the queries are brought to fp16 in place, each row scaled by a power of two
+// that puts its largest element in [1, 2).
+//
 // Tiles that reach the round's own rows take a mask of 128 bits per row.  There
 // a stored value that is not finite is set to zero before the product (0 * inf
 // would reach rows that do not see it) and added at the end to the rows that
@@ -42,11 +47,10 @@
 
 namespace wf {
 
-constexpr int PR_THREADS = 352;    // two streams of four softmax warps, the copying warp, an issuing warp a stream
+constexpr int PR_THREADS = 384;    // two streams of four softmax warps, the copying warp, an issuing warp a stream,
+                                   // the widening warp (8-bit caches)
 constexpr int PR_KT = 128;         // positions of a tile
-constexpr int PR_RING = 4;         // tiles of keys or values in flight
 constexpr int PR_ROWS = 128;       // pairs of a product
-constexpr float PR_LAG = 8.f;      // the running maximum may lag by 2^8
 constexpr int PR_XC = 32;          // dims that pass through shared memory together
 constexpr int PR_XBYTES = PR_ROWS * PR_XC * 4;
 
@@ -58,6 +62,8 @@ struct RoundsParams {
     const int32_t* parent;
     const int32_t* table;
     const uint8_t* V;        // this layer's rows
+    const float* k_scale;    // this layer's [G] scales, or null
+    const float* v_scale;
     uint16_t* out;
     float* lse;
     float4* part;            // [CTA][2][D / 4][256] unnormalised outputs, four dims of a row together
@@ -213,40 +219,65 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
         : "memory");
 }
 
-// Shared memory: queries [2][blocks][128 rows][128 B], ring [4][blocks][128 positions][128 B],
-// exchanged rows [128][32] fp32; blocks = 64-dim blocks of a head.
-__host__ __device__ constexpr int rounds_smem(int blocks) {
-    return 1024 + (2 * PR_ROWS + PR_RING * PR_KT) * blocks * 128 + PR_XBYTES;
+// Shared memory: queries [2][blocks][128 rows][128 B], a ring of tiles of keys or
+// values [blocks][128 positions][128 B], exchanged rows [128][32] fp32, and for an
+// 8-bit cache two raw tiles [128][D <= 64 blocks]; blocks = 64-dim blocks of a head.
+template <int BLK, bool E4M3>
+struct RoundsShape {
+    static constexpr int RING = E4M3 ? 3 : 4;        // tiles of keys or values ready or in flight
+    static constexpr int RAW = E4M3 ? 2 : 0;
+    static constexpr int QTILE = BLK * PR_ROWS * 128;
+    static constexpr int TILE = BLK * PR_KT * 128;
+    static constexpr int RAW_TILE = BLK * PR_KT * 64;
+    static constexpr int SMEM = 1024 + 2 * QTILE + RING * TILE + PR_XBYTES + RAW * RAW_TILE;
+    // the running maximum may lag by 2^LAG; fp16 probabilities use the range from 2^-24 up to 2^(BIAS + LAG)
+    static constexpr float LAG = E4M3 ? 4.f : 8.f;
+    static constexpr float BIAS = E4M3 ? 8.f : 0.f;
+};
+
+// acc stays 0 while no fp16 of w is infinite or NaN, and is NaN from then on
+__device__ __forceinline__ uint32_t f16x2_probe(uint32_t w, uint32_t acc) {
+    uint32_t r;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(w), "r"(0u), "r"(acc));
+    return r;
 }
 
-// BLK: 64-dim blocks of a head (1 or 2)
-template <int BLK>
+// BLK: 64-dim blocks of a head (1 or 2); E4M3: the cache's type
+template <int BLK, bool E4M3>
 __global__ void __launch_bounds__(PR_THREADS, 1)
     paged_rounds_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const RoundsParams p) {
-    constexpr int QTILE = BLK * PR_ROWS * 128; // bytes of a product's queries
-    constexpr int TILE = BLK * PR_KT * 128;    // and of a tile of keys or values
+    using S = RoundsShape<BLK, E4M3>;
+    constexpr int RING = S::RING, QTILE = S::QTILE, TILE = S::TILE;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;
     uint8_t* sR = smem + 2 * QTILE;
-    uint8_t* sX = sR + PR_RING * TILE;
-    __shared__ uint64_t kv_full[PR_RING], kv_empty[PR_RING], q_full, q_empty, told[8];
+    uint8_t* sX = sR + RING * TILE;
+    uint8_t* sW = sX + PR_XBYTES;              // raw tiles
+    __shared__ uint64_t kv_full[RING], kv_empty[RING], raw_full[2], raw_empty[2], q_full, q_empty, told[8];
     __shared__ uint64_t piece_ready[8], piece_free[8];
     __shared__ Piece s_piece[8];   // the copying warp's next pieces, for the others
     __shared__ uint64_t s_full[2], p_full[2], o_full[2];   // by stream
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word, s_bad[8], s_odd[2][2], s_pb, s_turn;
     __shared__ uint8_t s_par[2][WF_MAX_SEQ_NODES + 1];   // row of each row's parent, by stream (a row's own copy)
+    __shared__ uint64_t q_ready[2];                        // queries brought to fp16, by stream
     __shared__ float2 s_xst[PR_ROWS];
+    __shared__ float s_factor[PR_ROWS];                    // and their scores' factors, for the other stream
     __shared__ int64_t s_plan, s_scan[PR_THREADS / 32];
     volatile int* abort_flag = &abort_word;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
-        for (int i = 0; i < PR_RING; ++i) {
+        for (int i = 0; i < RING; ++i) {
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 2);   // both streams, or one twice
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&raw_full[i], 1);
+            mbar_init(&raw_empty[i], 1);
+            mbar_init(&q_ready[i], PR_ROWS);
         }
         mbar_init(&q_full, 1);
         mbar_init(&q_empty, 2);
@@ -258,7 +289,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         for (int i = 0; i < 8; ++i) {
             mbar_init(&told[i], 1);
             mbar_init(&piece_ready[i], 1);
-            mbar_init(&piece_free[i], 4);   // two streams, two issuing warps
+            mbar_init(&piece_free[i], E4M3 ? 5 : 4);   // two streams, two issuing warps (and the widening one)
         }
         abort_word = s_turn = 0;
         s_odd[0][0] = s_odd[0][1] = s_odd[1][0] = s_odd[1][1] = 0;
@@ -419,18 +450,27 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                                 }
                                 __syncwarp();
                             }
-                            const int at = 2 * n + kv, slot = at % PR_RING;
-                            alive = alive && (at < PR_RING || mbar_wait(&kv_empty[slot], ((at / PR_RING) & 1) ^ 1,
-                                                                       p.timeout_ns, abort_flag));
+                            const int at = 2 * n + kv;
+                            // the raw tiles' turn for an 8-bit cache, else the ring's
+                            constexpr int PLACES = E4M3 ? 2 : RING;
+                            const int place = at % PLACES;
+                            uint64_t* full = E4M3 ? &raw_full[place] : &kv_full[place];
+                            uint64_t* empty = E4M3 ? &raw_empty[place] : &kv_empty[place];
+                            alive = alive && (at < PLACES || mbar_wait(empty, ((at / PLACES) & 1) ^ 1, p.timeout_ns,
+                                                                       abort_flag));
                             if (!alive) break;
-                            if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], boxes * BLK * p.box_rows * 128);
+                            const int row_bytes = E4M3 ? p.D : BLK * 128;
+                            if (lane == 0) mbar_arrive_expect_tx(full, boxes * p.box_rows * row_bytes);
                             __syncwarp();
-                            if (ok) {
-                                uint8_t* dst = sR + slot * TILE + lane * p.box_rows * 128;
+                            if (ok && E4M3) {
+                                tma_load_2d(sW + place * S::RAW_TILE + lane * p.box_rows * p.D, kv ? &tmV : &tmK, full,
+                                            x.g * p.D, y, pol);
+                            } else if (ok) {
+                                uint8_t* dst = sR + place * TILE + lane * p.box_rows * 128;
 #pragma unroll
                                 for (int blk = 0; blk < BLK; ++blk)
-                                    tma_load_2d(dst + blk * PR_KT * 128, kv ? &tmV : &tmK, &kv_full[slot],
-                                                x.g * p.D + blk * 64, y, pol);
+                                    tma_load_2d(dst + blk * PR_KT * 128, kv ? &tmV : &tmK, full, x.g * p.D + blk * 64, y,
+                                                pol);
                             }
                         }
                         if (!alive) {
@@ -452,9 +492,68 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 next_item();
             }
             // let every copy issued land before the shared memory goes
-            for (int at = max(0, 2 * n - PR_RING); at < 2 * n; ++at)
-                mbar_wait(&kv_full[at % PR_RING], (at / PR_RING) & 1, p.timeout_ns, nullptr);
+            constexpr int PLACES = E4M3 ? 2 : RING;
+            for (int at = max(0, 2 * n - PLACES); at < 2 * n; ++at)
+                mbar_wait(E4M3 ? &raw_full[at % PLACES] : &kv_full[at % PLACES], (at / PLACES) & 1, p.timeout_ns, nullptr);
             if (k > 0) mbar_wait(&q_full, (k & 1) ^ 1, p.timeout_ns, nullptr);
+        } else if (warp == 11) {
+            // ---------------------------------------- 8-bit rows widened to fp16 in the ring
+            if (E4M3) {
+                int n = 0;
+                bool ok = true;
+                auto wait = [&](uint64_t* bar, uint32_t parity) {
+                    ok = ok && mbar_wait(bar, parity, p.timeout_ns, abort_flag);
+                };
+                const int per_row = p.D / 16;   // 16-byte pieces of a raw row
+                for (int turn = 0; ok; ++turn) {
+                    wait(&piece_ready[turn & 7], (turn >> 3) & 1);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const int tiles = s_piece[turn & 7].tiles;
+                    if (tiles == 0) break;
+                    const int loads = s_piece[turn & 7].w.bad ? 0 : 2 * tiles;
+                    for (int i = 0; i < loads && ok; ++i) {
+                        const int at = 2 * n + i, raw = at & 1, slot = at % RING;
+                        wait(&raw_full[raw], (at >> 1) & 1);
+                        if (at >= RING) wait(&kv_empty[slot], ((at / RING) & 1) ^ 1);
+                        ok = __all_sync(0xffffffffu, ok);
+                        if (!ok) break;
+                        const uint8_t* src = sW + raw * S::RAW_TILE;
+                        uint8_t* dst = sR + slot * TILE;
+                        for (int j = lane; j < PR_KT * per_row; j += 4 * 32) {
+                            uint4 v[4];
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)   // 128 rows of pieces: a multiple of 128
+                                v[u] = *reinterpret_cast<const uint4*>(src + (j + 32 * u) * 16);
+#pragma unroll
+                            for (int u = 0; u < 4; ++u) {
+                                const int r = (j + 32 * u) / per_row, c = 2 * ((j + 32 * u) - r * per_row);
+                                const uint4 lo = make_uint4(e4m3x2_f16x2(v[u].x), e4m3x2_f16x2(v[u].x >> 16),
+                                                            e4m3x2_f16x2(v[u].y), e4m3x2_f16x2(v[u].y >> 16));
+                                const uint4 hi = make_uint4(e4m3x2_f16x2(v[u].z), e4m3x2_f16x2(v[u].z >> 16),
+                                                            e4m3x2_f16x2(v[u].w), e4m3x2_f16x2(v[u].w >> 16));
+                                uint8_t* row = dst + (c >> 3) * PR_KT * 128 + r * 128;
+                                *reinterpret_cast<uint4*>(row + (((c & 7) ^ (r & 7)) << 4)) = lo;
+                                *reinterpret_cast<uint4*>(row + ((((c & 7) + 1) ^ (r & 7)) << 4)) = hi;
+                            }
+                        }
+                        fence_async_smem();
+                        __syncwarp();
+                        if (lane == 0) {
+                            mbar_arrive(&kv_full[slot]);
+                            mbar_arrive(&raw_empty[raw]);
+                        }
+                    }
+                    if (!ok) break;
+                    n += loads / 2;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&piece_free[turn & 7]);
+                }
+                if (!ok) {
+                    *abort_flag = 1;
+                    if (lane == 0) record_error(p.ctrl, WF_ERR_TIMEOUT, 0x830u);
+                }
+            }
         } else {
             // ---------------------------------------- products of stream w
             // The whole warp runs this with the same values and one elected lane
@@ -504,9 +603,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         umma_commit(&kv_empty[slot]);
                         if (solo) umma_commit(&kv_empty[slot]);
                     };
-                    auto arrived = [&](int at) { wait(&kv_full[at % PR_RING], (at / PR_RING) & 1); };
+                    auto arrived = [&](int at) { wait(&kv_full[at % RING], (at / RING) & 1); };
                     auto scores = [&](int i) {   // S of step i
-                        const int slot = place_of(i) % PR_RING;
+                        const int slot = place_of(i) % RING;
                         const uint32_t a = qdesc + (solo ? 0 : w) * (QTILE >> 4), b = kdesc + slot * (TILE >> 4);
 #pragma unroll
                         for (int ks = 0; ks < 4 * BLK; ++ks)
@@ -518,7 +617,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         release(slot);
                         if (i + 1 == steps) umma_commit(&q_empty);   // the stream is done with the queries
                     };
-                    wait(&q_full, qn++ & 1);
+                    wait(E4M3 ? &q_ready[w] : &q_full, qn++ & 1);
                     if (steps == 0) {
                         if (lane == 0) mbar_arrive(&q_empty);
                     } else {
@@ -530,7 +629,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         give_turn();
                     }
                     for (int i = 0; i < steps; ++i) {
-                        const int at = place_of(i) + 1, slot = at % PR_RING;
+                        const int at = place_of(i) + 1, slot = at % RING;
                         arrived(at);
                         // Two products share every tile: the next keys are here by now, and
                         // both products go in one turn.  One product: its next keys are two
@@ -578,6 +677,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + w * 128, tO = tmem + lanes + 256 + w * 128;
         uint32_t sn = 0, on = 0;   // scores, outputs taken
+        uint32_t qn = 0;           // queries (8-bit caches)
         int n = 0, k = 0;          // tiles before this piece, pieces that have any
         bool shared_item = false;  // an item begins here and ends elsewhere
         bool ok = true;
@@ -628,6 +728,46 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 }
                 named_sync(1 + w, 128);
             };
+            float f = p.qk;   // the row's scores times this are base-2 exponents
+            if (E4M3 && !x.w.bad) {
+                if (w == 0 || !x.solo) {
+                    // this row's queries to fp16 in place
+                    wait(&q_full, qn & 1);
+                    uint8_t* q = sQ + (x.solo ? 0 : w) * QTILE + row * 128;
+                    auto piece = [&](int c) {
+                        return reinterpret_cast<uint4*>(q + (c >> 3) * PR_ROWS * 128 + (((c & 7) ^ (row & 7)) << 4));
+                    };
+                    auto lo = [](uint32_t y) { return pg_bf16_to_f32(y & 0xFFFFu); };
+                    auto hi = [](uint32_t y) { return pg_bf16_to_f32(y >> 16); };
+                    float big = 0.f;
+#pragma unroll 4
+                    for (int c = 0; c < p.D / 8; ++c) {
+                        const uint4 y = *piece(c);
+                        big = max3(big, fabsf(lo(y.x)), fabsf(hi(y.x)));
+                        big = max3(big, fabsf(lo(y.y)), fabsf(hi(y.y)));
+                        big = max3(big, fabsf(lo(y.z)), fabsf(hi(y.z)));
+                        big = max3(big, fabsf(lo(y.w)), fabsf(hi(y.w)));
+                    }
+                    // exponents within +-100 of 1 keep both the scaling and its inverse normal
+                    const int e = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 100);
+                    const float down = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll 4
+                    for (int c = 0; c < p.D / 8; ++c) {
+                        const uint4 y = *piece(c);
+                        *piece(c) = make_uint4(cvt_f16x2(lo(y.x) * down, hi(y.x) * down), cvt_f16x2(lo(y.y) * down, hi(y.y) * down),
+                                               cvt_f16x2(lo(y.z) * down, hi(y.z) * down), cvt_f16x2(lo(y.w) * down, hi(y.w) * down));
+                    }
+                    f = p.qk * (p.k_scale ? __ldg(p.k_scale + x.g) : 1.f) * __uint_as_float((uint32_t)(127 + e) << 23);
+                    if (x.solo) s_factor[row] = f;
+                    fence_async_smem();
+                    mbar_arrive(&q_ready[w]);
+                    if (x.solo) mbar_arrive(&q_ready[1]);
+                } else {
+                    wait(&q_ready[1], qn & 1);
+                    f = s_factor[row];
+                }
+                ++qn;
+            }
             if (!x.w.bad) {
                 for (int i = 0; i < mine_tiles; ++i) {
                     const int j = x.solo ? 2 * i + w : i;
@@ -694,7 +834,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                                 fetch(0);
                                 const float low = largest(-INFINITY);
                                 fetch(2);
-                                const float mn = fmaxf(m, largest(low) * p.qk);
+                                const float mn = fmaxf(m, largest(low) * f);
                                 const float a = m == -INFINITY ? 0.f : ex2_approx(m - mn);
                                 m = mn;
                                 l *= a;
@@ -708,8 +848,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                                         tmem_st_x16(tO + c, y);
                                     }
                             }
-                            const float base = m == -INFINITY ? 0.f : -m;
-                            const uint64_t qk2 = pair_of(p.qk, p.qk), base2 = pair_of(base, base);
+                            const float base = (m == -INFINITY ? 0.f : -m) + S::BIAS;
+                            const uint64_t qk2 = pair_of(f, f), base2 = pair_of(base, base);
                             uint64_t sum2[2] = {0, 0};
                             float big = -INFINITY;
 #pragma unroll
@@ -724,10 +864,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                                         unpair(fma2(pair_of(at(c, 2 * e), at(c, 2 * e + 1)), qk2, base2), z0, z1);
                                         const float p0 = ex2_approx(z0), p1 = ex2_approx(z1);
                                         sum2[e & 1] = add2(sum2[e & 1], pair_of(p0, p1));
-                                        pk[c0 + c][e] = cvt_bf16x2(p0, p1);
+                                        pk[c0 + c][e] = E4M3 ? cvt_f16x2(p0, p1) : cvt_bf16x2(p0, p1);
                                     }
                             }
-                            if (again || !__any_sync(0xffffffffu, big * p.qk > m + PR_LAG)) {
+                            if (again || !__any_sync(0xffffffffu, big * f > m + S::LAG)) {
                                 float a0, a1;
                                 unpair(add2(sum2[0], sum2[1]), a0, a1);
                                 sum = a0 + a1;
@@ -742,8 +882,8 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     if (masked && t0 + row >= x.w.len) {
                         // one position's values a thread: zero past the end, and where not
                         // finite (by both streams where both see the tile: the same bytes)
-                        const int at = 2 * (n + j) + 1, slot = at % PR_RING;
-                        wait(&kv_full[slot], (at / PR_RING) & 1);
+                        const int at = 2 * (n + j) + 1, slot = at % RING;
+                        wait(&kv_full[slot], (at / RING) & 1);
                         const bool past = t0 + row >= x.w.T;
                         bool odd = false;
 #pragma unroll
@@ -757,8 +897,13 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                                     *piece(c) = make_uint4(0, 0, 0, 0);
                                 } else {
                                     const uint4 y = *piece(c);
-                                    probe[0] = bf16x2_probe(y.y, bf16x2_probe(y.x, probe[0]));
-                                    probe[1] = bf16x2_probe(y.w, bf16x2_probe(y.z, probe[1]));
+                                    if (E4M3) {
+                                        probe[0] = f16x2_probe(y.y, f16x2_probe(y.x, probe[0]));
+                                        probe[1] = f16x2_probe(y.w, f16x2_probe(y.z, probe[1]));
+                                    } else {
+                                        probe[0] = bf16x2_probe(y.y, bf16x2_probe(y.x, probe[0]));
+                                        probe[1] = bf16x2_probe(y.w, bf16x2_probe(y.z, probe[1]));
+                                    }
                                 }
                             }
                             if (((probe[0] | probe[1]) & 0x7FFF7FFFu) == 0) continue;
@@ -769,8 +914,9 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                                 uint32_t* e = &y.x;
 #pragma unroll
                                 for (int u = 0; u < 4; ++u) {
-                                    if ((e[u] & 0x7F80u) == 0x7F80u) e[u] &= 0xFFFF0000u;
-                                    if ((e[u] & 0x7F800000u) == 0x7F800000u) e[u] &= 0x0000FFFFu;
+                                    constexpr uint32_t EXP = E4M3 ? 0x7C00u : 0x7F80u;
+                                    if ((e[u] & EXP) == EXP) e[u] &= 0xFFFF0000u;
+                                    if ((e[u] & EXP << 16) == EXP << 16) e[u] &= 0x0000FFFFu;
                                 }
                                 *piece(c) = y;
                             }
@@ -818,7 +964,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                 }
             }
             if (bad) M = L = NAN;
-            const float inv = 1.f / L;
+            const float inv = (E4M3 && p.v_scale ? __ldg(p.v_scale + x.g) : 1.f) / L;
             const int64_t out_pair = (int64_t)(x.w.r0 + r) * p.H + x.g * p.hq + (row - row / p.hq * p.hq);
             float* xb = reinterpret_cast<float*>(sX);   // [128][32]: the second stream's rows, pieces of 16 bytes swizzled
             for (int c0 = 0; c0 < p.D; c0 += PR_XC) {
@@ -880,7 +1026,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             if (bad && row == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)x.b);
             if (writer && !whole) p.stat[slot * 2 * PR_ROWS + prow] = make_float2(M, L);
             if (writer && whole && p.lse)
-                p.lse[out_pair] = (M + __log2f(L)) * LN2;
+                p.lse[out_pair] = (M + __log2f(L) - S::BIAS) * LN2;
             if (tid == 0 && x.pieces > 0) {
                 p.join[blockIdx.x] = make_int4(x.pieces, x.w.r0 + 2 * x.mp * p.rpt, x.rows * p.hq, x.g);
                 shared_item = true;
@@ -900,10 +1046,10 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                     const int page = p.table[(int64_t)x.b * p.max_pages + (t >> p.page_shift)];
                     if (!sees || page < 0 || page >= p.num_pages) continue;
                     const int64_t at = (((int64_t)page << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * p.G + x.g;
-                    const uint16_t* v = reinterpret_cast<const uint16_t*>(p.V) + at * p.D;
 #pragma unroll 1
                     for (int d = 0; d < p.D; ++d) {
-                        const float y = pg_bf16_to_f32(v[d]);
+                        const float y = E4M3 ? ((p.V[at * p.D + d] & 0x7F) == 0x7F ? NAN : 0.f)
+                                             : pg_bf16_to_f32(reinterpret_cast<const uint16_t*>(p.V)[at * p.D + d]);
                         if (fabsf(y) < INFINITY) continue;
                         if (whole) {
                             uint16_t* o = p.out + out_pair * p.D + d;
@@ -938,7 +1084,7 @@ constexpr int RJ_BATCH = 8;   // pieces whose statistics and values are in fligh
 
 __global__ void __launch_bounds__(RJ_WARPS * 32)
     rounds_join_kernel(const int4* __restrict__ join, const float4* __restrict__ part, const float2* __restrict__ stat,
-                       uint16_t* out, float* lse, int H, int D, int hq) {
+                       uint16_t* out, float* lse, const float* v_scale, float bias, int H, int D, int hq) {
     __shared__ uint2 s_row[32][128 / 4 + 1];
     pdl_wait();
     pdl_trigger();
@@ -991,23 +1137,21 @@ __global__ void __launch_bounds__(RJ_WARPS * 32)
             }
         }
     }
-    const float inv = 1.f / L;
+    const float inv = (v_scale ? __ldg(v_scale + j.w) : 1.f) / L;
 #pragma unroll
     for (int u = 0; u < MQ; ++u)
         if (warp + u * RJ_WARPS < quads)
             s_row[lane][warp + u * RJ_WARPS] =
                 make_uint2(cvt_bf16x2(v[u].x * inv, v[u].y * inv), cvt_bf16x2(v[u].z * inv, v[u].w * inv));
     auto pair_row = [&](int q) { return (int64_t)(j.y + q / hq) * H + j.w * hq + q % hq; };
-    if (warp == 0 && in && lse) lse[pair_row(pr)] = (M + __log2f(L)) * LN2;
+    if (warp == 0 && in && lse) lse[pair_row(pr)] = (M + __log2f(L) - bias) * LN2;
     __syncthreads();
     for (int r = warp; r < 32 && first + r < j.z; r += RJ_WARPS)
         if (lane < quads) reinterpret_cast<uint2*>(out + pair_row(first + r) * D)[lane] = s_row[r][lane];
 }
 
 // ------------------------------------------------------------------ host side
-// The queries as [P, H, D] in boxes of 64 dims x hq heads x rpt rows: a box is
-// the 128-byte rows of a product's operand, row by row.
-static bool query_map(CUtensorMap* map, const wf_paged_attn_args* a, int D, int hq, int rpt) {
+static PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     static PFN_cuTensorMapEncodeTiled_v12000 enc = nullptr;
     static std::once_flag once;
     std::call_once(once, [] {
@@ -1018,6 +1162,13 @@ static bool query_map(CUtensorMap* map, const wf_paged_attn_args* a, int D, int 
             q == cudaDriverEntryPointSuccess)
             enc = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
     });
+    return enc;
+}
+
+// The queries as [P, H, D] in boxes of 64 dims x hq heads x rpt rows: a box is
+// the 128-byte rows of a product's operand, row by row.
+static bool query_map(CUtensorMap* map, const wf_paged_attn_args* a, int D, int hq, int rpt) {
+    const auto enc = encoder();
     if (!enc) return false;
     cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)a->H, (cuuint64_t)a->P};
     cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)a->q_stride * 2};
@@ -1028,21 +1179,53 @@ static bool query_map(CUtensorMap* map, const wf_paged_attn_args* a, int D, int 
                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// An 8-bit pool's layer as [rows, G * D] bytes in boxes of a head's row by `box_rows`.
+static bool raw_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, int D, int box_rows) {
+    const auto enc = encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {cols};
+    cuuint32_t box[2] = {(cuuint32_t)D, (cuuint32_t)box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_128B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+using RoundsFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, RoundsParams);
+
+struct RoundsVariant {
+    RoundsFn fn;
+    int smem;
+};
+
+// bit 0: an 8-bit cache; bit 1: heads wider than 64
+static RoundsVariant rounds_variant(int i) {
+    switch (i) {
+        case 0: return {paged_rounds_kernel<1, false>, RoundsShape<1, false>::SMEM};
+        case 1: return {paged_rounds_kernel<1, true>, RoundsShape<1, true>::SMEM};
+        case 2: return {paged_rounds_kernel<2, false>, RoundsShape<2, false>::SMEM};
+        default: return {paged_rounds_kernel<2, true>, RoundsShape<2, true>::SMEM};
+    }
+}
+
 wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s) {
     static std::mutex mu;
     static bool attr_set[64] = {false};
     PR_TRY(configure_once(mu, attr_set, [] {
-        return cudaFuncSetAttribute(paged_rounds_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    rounds_smem(1)) == cudaSuccess &&
-               cudaFuncSetAttribute(paged_rounds_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    rounds_smem(2)) == cudaSuccess &&
-               // as for the catch-up's kernels: no change of the carveout between launches
-               cudaFuncSetAttribute(rounds_join_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) ==
-                   cudaSuccess;
+        for (int i = 0; i < 4; ++i) {
+            const RoundsVariant v = rounds_variant(i);
+            if (cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) != cudaSuccess)
+                return false;
+        }
+        // as for the catch-up's kernels: no change of the carveout between launches
+        return cudaFuncSetAttribute(rounds_join_kernel, cudaFuncAttributePreferredSharedMemoryCarveout, 100) ==
+               cudaSuccess;
     }));
+    const bool e4m3 = c->kv_type == WF_KV_E4M3;
     uint8_t* w = static_cast<uint8_t*>(ws);
     const PagedLayout L = paged_layout(c->B, a->H, c->G, c->D, a->max_rows);
-    const int64_t layer_bytes = (int64_t)c->num_pages * c->page_size * c->G * c->D * 2;
+    const int64_t layer_bytes = (int64_t)c->num_pages * c->page_size * c->G * c->D * (e4m3 ? 1 : 2);
     const uint8_t* K = static_cast<const uint8_t*>(c->K) + a->layer * layer_bytes;
     RoundsParams p = {};
     p.pos_off = a->pos_off;
@@ -1052,6 +1235,8 @@ wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args*
     p.parent = a->parent;
     p.table = c->table;
     p.V = static_cast<const uint8_t*>(c->V) + a->layer * layer_bytes;
+    p.k_scale = c->k_scale ? c->k_scale + (int64_t)a->layer * c->G : nullptr;
+    p.v_scale = c->v_scale ? c->v_scale + (int64_t)a->layer * c->G : nullptr;
     p.out = a->out;
     p.lse = a->lse;
     p.part = reinterpret_cast<float4*>(w + L.part);
@@ -1070,25 +1255,30 @@ wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args*
     p.max_rows = a->max_rows;
     p.rpt = PR_ROWS / p.hq;
     p.box_rows = c->page_size < PR_KT ? c->page_size : PR_KT;
-    p.idesc_s = umma_idesc_bf16(PR_ROWS, PR_KT);
-    p.idesc_o = umma_idesc_bf16(PR_ROWS, c->D) | (1u << 16);   // the values' contiguous dimension is N
+    // fp16 operands are format 0 where bf16 are 1; the values' contiguous dimension is N
+    const uint32_t formats = e4m3 ? (1u << 7) | (1u << 10) : 0u;
+    p.idesc_s = umma_idesc_bf16(PR_ROWS, PR_KT) & ~formats;
+    p.idesc_o = (umma_idesc_bf16(PR_ROWS, c->D) & ~formats) | (1u << 16);
     p.ctrl = static_cast<Control*>(ws);
     p.timeout_ns = wait_timeout_ns();
     CUtensorMap tmQ, tmK, tmV;
     if (!query_map(&tmQ, a, c->D, p.hq, p.rpt)) return WF_ERR_CUDA;
     const uint64_t rows = (uint64_t)c->num_pages * c->page_size, cols = (uint64_t)c->G * c->D;
-    if (!make_map(&tmK, K, rows, cols, (uint32_t)p.box_rows) || !make_map(&tmV, p.V, rows, cols, (uint32_t)p.box_rows))
+    if (e4m3 ? !raw_map(&tmK, K, rows, cols, c->D, p.box_rows) || !raw_map(&tmV, p.V, rows, cols, c->D, p.box_rows)
+             : !make_map(&tmK, K, rows, cols, (uint32_t)p.box_rows) ||
+                   !make_map(&tmV, p.V, rows, cols, (uint32_t)p.box_rows))
         return WF_ERR_CUDA;
     int grid = num_sms() < PA_MAX_ROUND_CTAS ? num_sms() : PA_MAX_ROUND_CTAS;
     // no more CTAs than tiles that the bounds allow
     const int64_t tiles = (int64_t)c->B * c->G * cdiv(a->max_rows, 2 * p.rpt) *
                           cdiv((int64_t)c->max_pages * c->page_size, PR_KT);
     if (tiles < grid) grid = (int)tiles;
-    PR_TRY(launch(c->D <= 64 ? paged_rounds_kernel<1> : paged_rounds_kernel<2>, dim3(grid), dim3(PR_THREADS),
-                  (size_t)rounds_smem(c->D <= 64 ? 1 : 2), s, tmQ, tmK, tmV, p));
+    const RoundsVariant v = rounds_variant((e4m3 ? 1 : 0) | (c->D > 64 ? 2 : 0));
+    PR_TRY(launch(v.fn, dim3(grid), dim3(PR_THREADS), (size_t)v.smem, s, tmQ, tmK, tmV, p));
     const int most = a->max_rows < 2 * p.rpt ? a->max_rows : 2 * p.rpt;   // query rows of an item
     return launch(rounds_join_kernel, dim3(grid, cdiv(most * p.hq, 32)), dim3(RJ_WARPS * 32), 0, s, (const int4*)p.join,
-                  (const float4*)p.part, (const float2*)p.stat, a->out, a->lse, a->H, c->D, p.hq);
+                  (const float4*)p.part, (const float2*)p.stat, a->out, a->lse, p.v_scale,
+                  e4m3 ? RoundsShape<1, true>::BIAS : RoundsShape<1, false>::BIAS, a->H, c->D, p.hq);
 }
 
 }  // namespace wf
