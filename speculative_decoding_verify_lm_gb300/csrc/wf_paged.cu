@@ -309,6 +309,7 @@ __global__ void __launch_bounds__(RS_THREADS) reserve_kernel(const ReserveParams
     extern __shared__ int32_t list[];   // [RS_CHUNK]
     __shared__ int s_warp[32];
     pdl_wait();
+    pdl_trigger();   // the copies' CTAs may take their places and wait there
     const int tid = threadIdx.x;
     const int64_t cap = (int64_t)p.max_pages << p.page_shift;
     if (tid == 0) *p.n_copies = 0;
@@ -437,7 +438,6 @@ __global__ void __launch_bounds__(RS_THREADS) reserve_kernel(const ReserveParams
         }
         if (p.added) p.added[b] = fits ? need : -1;
     }
-    pdl_trigger();
 }
 
 // The pages that reserve_kernel listed, copied in every layer: 16 KB units

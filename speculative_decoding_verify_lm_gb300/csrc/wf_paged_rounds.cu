@@ -27,7 +27,8 @@
 // (one for both spent most of its time on barriers: 139 us for the batch of 32).
 //
 // An 8-bit cache goes through fp16 operands (the products take no mixed types):
-// its rows are copied raw and one more warp widens them into the ring, exactly;
+// its rows are copied raw and five more warps widen them into the ring, exactly
+// (one warp took 268 us for the batch of 32);
 // the queries are brought to fp16 in place, each row scaled by a power of two
 // that puts its largest element in [1, 2).
 //
@@ -47,8 +48,6 @@
 
 namespace wf {
 
-constexpr int PR_THREADS = 384;    // two streams of four softmax warps, the copying warp, an issuing warp a stream,
-                                   // the widening warp (8-bit caches)
 constexpr int PR_KT = 128;         // positions of a tile
 constexpr int PR_ROWS = 128;       // pairs of a product
 constexpr int PR_XC = 32;          // dims that pass through shared memory together
@@ -226,6 +225,13 @@ template <int BLK, bool E4M3>
 struct RoundsShape {
     static constexpr int RING = E4M3 ? 3 : 4;        // tiles of keys or values ready or in flight
     static constexpr int RAW = E4M3 ? 2 : 0;
+    // two streams of four softmax warps, the copying warp, an issuing warp a stream,
+    // and for an 8-bit cache the widening warps
+    static constexpr int WIDEN = E4M3 ? 5 : 0;
+    static constexpr int THREADS = (11 + WIDEN) * 32;
+    // registers: 512 threads start with 128 each (65,536); the softmax warps take 176,
+    // the other eight give down to 72 (63,488 in all)
+    static constexpr bool SPLIT_REGISTERS = E4M3;
     static constexpr int QTILE = BLK * PR_ROWS * 128;
     static constexpr int TILE = BLK * PR_KT * 128;
     static constexpr int RAW_TILE = BLK * PR_KT * 64;
@@ -244,11 +250,11 @@ __device__ __forceinline__ uint32_t f16x2_probe(uint32_t w, uint32_t acc) {
 
 // BLK: 64-dim blocks of a head (1 or 2); E4M3: the cache's type
 template <int BLK, bool E4M3>
-__global__ void __launch_bounds__(PR_THREADS, 1)
+__global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
     paged_rounds_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const RoundsParams p) {
     using S = RoundsShape<BLK, E4M3>;
-    constexpr int RING = S::RING, QTILE = S::QTILE, TILE = S::TILE;
+    constexpr int RING = S::RING, QTILE = S::QTILE, TILE = S::TILE, THREADS = S::THREADS, WIDEN = S::WIDEN;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;
@@ -265,18 +271,18 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     __shared__ uint64_t q_ready[2];                        // queries brought to fp16, by stream
     __shared__ float2 s_xst[PR_ROWS];
     __shared__ float s_factor[PR_ROWS];                    // and their scores' factors, for the other stream
-    __shared__ int64_t s_plan, s_scan[PR_THREADS / 32];
+    __shared__ int64_t s_plan, s_scan[THREADS / 32];
     volatile int* abort_flag = &abort_word;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     if (tid == 0) {
         for (int i = 0; i < RING; ++i) {
-            mbar_init(&kv_full[i], 1);
+            mbar_init(&kv_full[i], E4M3 ? WIDEN : 1);
             mbar_init(&kv_empty[i], 2);   // both streams, or one twice
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&raw_full[i], 1);
-            mbar_init(&raw_empty[i], 1);
+            mbar_init(&raw_empty[i], E4M3 ? WIDEN : 1);
             mbar_init(&q_ready[i], PR_ROWS);
         }
         mbar_init(&q_full, 1);
@@ -289,7 +295,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         for (int i = 0; i < 8; ++i) {
             mbar_init(&told[i], 1);
             mbar_init(&piece_ready[i], 1);
-            mbar_init(&piece_free[i], E4M3 ? 5 : 4);   // two streams, two issuing warps (and the widening one)
+            mbar_init(&piece_free[i], 4 + WIDEN);   // two streams, two issuing warps, the widening ones
         }
         abort_word = s_turn = 0;
         s_odd[0][0] = s_odd[0][1] = s_odd[1][0] = s_odd[1][1] = 0;
@@ -306,7 +312,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     pdl_trigger();
 
     // ------------------------------------------------ this CTA's stretch (as in the single-token kernel)
-    const int run = (p.B + PR_THREADS - 1) / PR_THREADS;
+    const int run = (p.B + THREADS - 1) / THREADS;
     int64_t mine = 0;
     bool heavy = false;   // a tile of weight 3
     for (int i = 0; i < run; ++i) {
@@ -331,7 +337,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     const uint32_t tmem = tmem_slot;
     int64_t total = 0, before = inc - mine;
 #pragma unroll
-    for (int w = 0; w < PR_THREADS / 32; ++w) {
+    for (int w = 0; w < THREADS / 32; ++w) {
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
     }
@@ -354,6 +360,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
     }
     __syncthreads();
     if (warp >= 8) {
+        if (S::SPLIT_REGISTERS) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 8) {
             // ---------------------------------------- copies: tile n's keys to ring place 2 n, its values to 2 n + 1
             const uint64_t pol = policy_evict_first();
@@ -496,7 +503,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
             for (int at = max(0, 2 * n - PLACES); at < 2 * n; ++at)
                 mbar_wait(E4M3 ? &raw_full[at % PLACES] : &kv_full[at % PLACES], (at / PLACES) & 1, p.timeout_ns, nullptr);
             if (k > 0) mbar_wait(&q_full, (k & 1) ^ 1, p.timeout_ns, nullptr);
-        } else if (warp == 11) {
+        } else if (warp >= 11) {
             // ---------------------------------------- 8-bit rows widened to fp16 in the ring
             if (E4M3) {
                 int n = 0;
@@ -520,13 +527,14 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
                         if (!ok) break;
                         const uint8_t* src = sW + raw * S::RAW_TILE;
                         uint8_t* dst = sR + slot * TILE;
-                        for (int j = lane; j < PR_KT * per_row; j += 4 * 32) {
-                            uint4 v[4];
+                        // 64 pieces a step, warp after warp
+                        for (int j = (warp - 11) * 64 + lane; j < PR_KT * per_row; j += WIDEN * 64) {
+                            uint4 v[2];
 #pragma unroll
-                            for (int u = 0; u < 4; ++u)   // 128 rows of pieces: a multiple of 128
+                            for (int u = 0; u < 2; ++u)   // 128 rows of pieces: a multiple of 64
                                 v[u] = *reinterpret_cast<const uint4*>(src + (j + 32 * u) * 16);
 #pragma unroll
-                            for (int u = 0; u < 4; ++u) {
+                            for (int u = 0; u < 2; ++u) {
                                 const int r = (j + 32 * u) / per_row, c = 2 * ((j + 32 * u) - r * per_row);
                                 const uint4 lo = make_uint4(e4m3x2_f16x2(v[u].x), e4m3x2_f16x2(v[u].x >> 16),
                                                             e4m3x2_f16x2(v[u].y), e4m3x2_f16x2(v[u].y >> 16));
@@ -673,6 +681,7 @@ __global__ void __launch_bounds__(PR_THREADS, 1)
         }
     } else {
         // -------------------------------------------- softmax: stream w, thread = row of the product
+        if (S::SPLIT_REGISTERS) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + w * 128, tO = tmem + lanes + 256 + w * 128;
@@ -1196,16 +1205,20 @@ using RoundsFn = void (*)(CUtensorMap, CUtensorMap, CUtensorMap, RoundsParams);
 
 struct RoundsVariant {
     RoundsFn fn;
-    int smem;
+    int smem, threads;
 };
 
 // bit 0: an 8-bit cache; bit 1: heads wider than 64
 static RoundsVariant rounds_variant(int i) {
     switch (i) {
-        case 0: return {paged_rounds_kernel<1, false>, RoundsShape<1, false>::SMEM};
-        case 1: return {paged_rounds_kernel<1, true>, RoundsShape<1, true>::SMEM};
-        case 2: return {paged_rounds_kernel<2, false>, RoundsShape<2, false>::SMEM};
-        default: return {paged_rounds_kernel<2, true>, RoundsShape<2, true>::SMEM};
+        case 0: return {paged_rounds_kernel<1, false>, RoundsShape<1, false>::SMEM,
+                         RoundsShape<1, false>::THREADS};
+        case 1: return {paged_rounds_kernel<1, true>, RoundsShape<1, true>::SMEM,
+                         RoundsShape<1, true>::THREADS};
+        case 2: return {paged_rounds_kernel<2, false>, RoundsShape<2, false>::SMEM,
+                         RoundsShape<2, false>::THREADS};
+        default: return {paged_rounds_kernel<2, true>, RoundsShape<2, true>::SMEM,
+                         RoundsShape<2, true>::THREADS};
     }
 }
 
@@ -1274,7 +1287,7 @@ wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args*
                           cdiv((int64_t)c->max_pages * c->page_size, PR_KT);
     if (tiles < grid) grid = (int)tiles;
     const RoundsVariant v = rounds_variant((e4m3 ? 1 : 0) | (c->D > 64 ? 2 : 0));
-    PR_TRY(launch(v.fn, dim3(grid), dim3(PR_THREADS), (size_t)v.smem, s, tmQ, tmK, tmV, p));
+    PR_TRY(launch(v.fn, dim3(grid), dim3(v.threads), (size_t)v.smem, s, tmQ, tmK, tmV, p));
     const int most = a->max_rows < 2 * p.rpt ? a->max_rows : 2 * p.rpt;   // query rows of an item
     return launch(rounds_join_kernel, dim3(grid, cdiv(most * p.hq, 32)), dim3(RJ_WARPS * 32), 0, s, (const int4*)p.join,
                   (const float4*)p.part, (const float2*)p.stat, a->out, a->lse, p.v_scale,

@@ -551,22 +551,25 @@ class PagedWorkspace(Workspace):
 
 def _rows(t, name, heads, D):
     """Address and row stride of [P, heads, D] bf16 rows; the rows may lie apart (a slice of a wider projection)."""
+    shape, strides = t.shape, t.stride()
     if not t.is_cuda or t.dtype not in _BF16:
         raise ValueError(f"{name} must be a bf16 CUDA tensor")
-    if t.dim() != 3 or t.shape[2] != D or (heads and t.shape[1] != heads):
+    if len(shape) != 3 or shape[2] != D or (heads and shape[1] != heads):
         raise ValueError(f"{name} must be [P, {heads or 'H'}, {D}]")
-    if t.numel() == 0:
-        return _placeholder(t.device), t.shape[1] * D
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != D):
+    if shape[0] * shape[1] == 0:
+        return _placeholder(t.device), shape[1] * D
+    if strides[2] != 1 or (strides[1] != D and shape[1] > 1):
         raise ValueError(f"{name}: each row's heads must lie densely")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else t.shape[1] * D
+    return t.data_ptr(), strides[0] if shape[0] > 1 else shape[1] * D
 
 
 def _lens(t, name, n, optional=False):
-    p = _check(t, name, _I32, optional)
-    if t is not None and t.numel() != n:
-        raise ValueError(f"{name} needs {n} elements")
-    return p
+    """Address of n int32 numbers (None if optional and not given)."""
+    if t is None and optional:
+        return None
+    if t is None or not t.is_cuda or t.dtype != torch.int32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {n} int32 numbers")
+    return t.data_ptr() if n else _placeholder(t.device)
 
 
 def wf_paged_append(cache: PagedCache, k, v, pos_off, cache_len, ws: Workspace, layer: int = 0, stream=None):
@@ -602,15 +605,18 @@ def wf_paged_attention(cache: PagedCache, q, pos_off, cache_len, ws: Workspace, 
     a.max_rows, a.layer = max_rows, layer
     a.scale = D ** -0.5 if scale is None else scale
     if out is None:
-        out = torch.empty((a.P, a.H, D), dtype=q.dtype, device=q.device)
+        out = q.new_empty(q.shape)
+        a.out = out.data_ptr() if a.P else _placeholder(q.device)
     elif out.numel() != q.numel():
         raise ValueError("out must be [P, H, D]")
+    else:
+        a.out = _check(out, "out", _BF16)
     if lse is None and with_lse:
-        lse = torch.empty((a.P, a.H), dtype=torch.float32, device=q.device)
+        lse = q.new_empty((a.P, a.H), dtype=torch.float32)
     elif lse is not None and lse.numel() != a.P * a.H:
         raise ValueError("lse must be [P, H]")
-    a.out = _check(out, "out", _BF16)
-    a.lse = _check(lse, "lse", _F32, True)
+    if lse is not None:
+        a.lse = _check(lse, "lse", _F32)
     _raise(lib().wf_paged_attention(cache._ref, ctypes.byref(a), ws.ptr, ws.nbytes, _stream(stream)),
            "wf_paged_attention")
     return out, lse
@@ -623,7 +629,7 @@ def wf_paged_compact(cache: PagedCache, n_accept, path, cache_len, ws: Workspace
     if path is not None and (path.dim() != 2 or path.shape[0] != B):
         raise ValueError("path must be [B, path_stride]")
     if new_len is None:
-        new_len = torch.empty(B, dtype=torch.int32, device=cache.K.device)
+        new_len = cache_len.new_empty(B)
     ps = path.shape[1] if path is not None else 0
     _raise(lib().wf_paged_compact(cache._ref, _lens(n_accept, "n_accept", B), _check(path, "path", _I32, True), ps,
                                   _lens(cache_len, "cache_len", B), _lens(new_len, "new_len", B), ws.ptr, ws.nbytes,
@@ -635,7 +641,7 @@ def wf_pages_reserve(cache: PagedCache, pos_off, cache_len, ws: Workspace, added
     """Pages for the round's rows, shared ones replaced by copies -> added [B] (pages taken, -1 = did not fit)."""
     B = cache.args.B
     if added is None:
-        added = torch.empty(B, dtype=torch.int32, device=cache.K.device)
+        added = cache_len.new_empty(B)
     _raise(lib().wf_pages_reserve(cache._ref, _lens(pos_off, "pos_off", B + 1), _lens(cache_len, "cache_len", B),
                                   _lens(added, "added", B), ws.ptr, ws.nbytes, _stream(stream)), "wf_pages_reserve")
     return added
