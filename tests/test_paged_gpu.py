@@ -465,3 +465,234 @@ def test_trim_of_malformed_entries():
     assert ws.device_error() == (BAD, 0)
     assert np.array_equal(host(cache.table), [[-1] * 4, [2, -1, -1, -1]])
     assert np.array_equal(host(cache.ref), [0, 0, 1, 0, 0])
+
+
+# ------------------------------------------------------------------ how a program uses them
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("lens,rows,H,G,D", [
+    ((70, 300), (5, 9), 20, 1, 96),        # 20 heads a group: six query rows a product
+    ((40,), (3,), 128, 1, 16),             # 128: one
+    ((200, 10), (1, 1), 16, 2, 64),        # single tokens through the kernel of drafted rows
+])
+def test_wide_groups_and_single_rows_among_rounds(lens, rows, H, G, D, kv):
+    check(ref.Case(41, lens, rows, H, G, D, 16, kv), max_rows=max(rows) + 2)
+
+
+def test_no_rows_at_all():
+    c = ref.Case(42, (5, 6), (0, 0), 4, 2, 32, 16)
+    cache, ws = cache_of(c), wf.PagedWorkspace(2, 4, 2, 32, 5)
+    for mr in (1, 5):
+        out, lse = wf.wf_paged_attention(cache, torch.empty((0, 4, 32), dtype=torch.bfloat16, device=DEV),
+                                         dev(np.zeros(3, np.int32)), dev(np.array([5, 6], np.int32)), ws, max_rows=mr,
+                                         with_lse=True)
+        assert out.shape == (0, 4, 32) and lse.shape == (0, 4)
+        q = torch.zeros((3, 4, 32), dtype=torch.bfloat16, device=DEV)   # rows that no sequence has
+        out = torch.full((3, 4, 32), 7.0, dtype=torch.bfloat16, device=DEV)
+        wf.wf_paged_attention(cache, q, dev(np.zeros(3, np.int32)), dev(np.array([5, 6], np.int32)), ws, max_rows=mr,
+                              out=out)
+        torch.cuda.synchronize()
+        assert (out == 7.0).all() and ws.device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("rows", [1, 9])
+def test_pools_past_32_bit_offsets(rows):
+    """Pages whose elements lie past 2^31 (and bytes past 2^32), with the rest of the pool never written."""
+    H, G, D, ps, num = 8, 8, 128, 64, 33100          # 33,100 x 64 x 1,024 elements
+    c = ref.Case(43, (150,), (rows,), H, G, D, ps)
+    used = [int(p) for p in c.table[0] if p >= 0]
+    K = torch.empty((1, num, ps, G, D), dtype=torch.bfloat16, device=DEV)
+    V = torch.empty_like(K)
+    table = c.table.copy()
+    for i, p in enumerate(used):
+        table[0, i] = num - 1 - i
+        K[0, num - 1 - i], V[0, num - 1 - i] = c.K[0, p].to(DEV), c.V[0, p].to(DEV)
+    cache = wf.PagedCache(K, V, dev(table))
+    check(c, cache=cache)
+    ws = wf.PagedWorkspace(1, H, G, D)
+    x = torch.randn((rows, G, D), device=DEV).to(torch.bfloat16)
+    wf.wf_paged_append(cache, x, x, dev(c.pos_off), dev(np.array([150], np.int32)), ws)
+    torch.cuda.synchronize()
+    t = 150 + rows - 1
+    assert torch.equal(K[0, table[0, t // ps], t % ps], x[-1]) and ws.device_error() == (0, 0)
+
+
+def test_captured_and_replayed_with_new_lengths():
+    """One graph of append, attention and compaction; the lengths and pages change between its replays."""
+    c = ref.Case(44, (90, 20), (9, 9), 8, 2, 64, 16, kinds=(1, 1), slack=8)
+    cache = cache_of(c)
+    ws = wf.PagedWorkspace(2, 8, 2, 64, 9)
+    q, pos, node = c.q.to(DEV), dev(c.pos_off), dev(c.node_off)
+    par, kind = dev(c.parent), dev(np.ones(2, np.int32))
+    ln = dev(np.array(c.lens, np.int32))
+    kv = torch.randn((18, 2, 2, 64), device=DEV).to(torch.bfloat16)
+    n_acc = dev(np.array([2, 1], np.int32))
+    path = dev(np.array([[0, 4, -1], [3, -1, -1]], np.int32))
+    new = torch.zeros(2, dtype=torch.int32, device=DEV)
+
+    def step():
+        wf.wf_paged_append(cache, kv[:, 0], kv[:, 1], pos, ln, ws)
+        out, lse = wf.wf_paged_attention(cache, q, pos, ln, ws, node_off=node, kind=kind, parent=par, max_rows=9,
+                                         with_lse=True)
+        wf.wf_paged_compact(cache, n_acc, path, ln, ws, new_len=new)
+        return out, lse
+
+    step()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out, lse = step()
+    for lens in ((90, 20), (3, 23), (60, 0)):   # within the two sequences' pages
+        K0, V0 = cache.K.clone(), cache.V.clone()
+        ln.copy_(dev(np.array(lens, np.int32)))
+        g.replay()
+        torch.cuda.synchronize()
+        assert ws.device_error() == (0, 0)
+        assert np.array_equal(host(new), [lens[0] + 3, lens[1] + 2])
+        c.lens = list(lens)
+        c.K, c.V = K0.cpu(), V0.cpu()
+        for b in range(2):
+            for r in range(9):
+                pg, at = c.table[b, (lens[b] + r) // 16], (lens[b] + r) % 16
+                c.K[0, pg, at], c.V[0, pg, at] = kv[9 * b + r, 0].cpu(), kv[9 * b + r, 1].cpu()
+        ro, rl, to, tl = ref.attention(c, 0.125)
+        assert np.all(np.abs(host(out.float()).astype(np.float64) - ro) <= to)
+        assert np.all(np.abs(host(lse).astype(np.float64) - rl) <= tl)
+
+
+def test_two_streams_with_a_workspace_each():
+    cs = [ref.Case(45 + i, (2000 - 700 * i, 300), (1, 1) if i else (20, 17), 8, 2, 64, 16, kinds=(1, 0) if not i else None)
+          for i in range(2)]
+    caches = [cache_of(c) for c in cs]
+    want = [run_attention(c, k) for c, k in zip(cs, caches)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    wss = [wf.PagedWorkspace(2, 8, 2, 64, 20) for _ in range(2)]
+    args = [(c.q.to(DEV), dev(c.pos_off), dev(np.array(c.lens, np.int32)), dev(c.node_off),
+             dev(np.array(c.kinds, np.int32)), dev(c.parent)) for c in cs]
+    outs = [[torch.empty((c.P, 8, 64), dtype=torch.bfloat16, device=DEV) for _ in range(6)] for c in cs]
+    torch.cuda.synchronize()
+    for r in range(6):
+        for i in range(2):
+            q, pos, ln, node, kind, par = args[i]
+            wf.wf_paged_attention(caches[i], q, pos, ln, wss[i], node_off=None if i else node, kind=None if i else kind,
+                                  parent=None if i else par, max_rows=1 if i else 20, out=outs[i][r], stream=streams[i])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert wss[i].device_error() == (0, 0)
+        for o in outs[i]:
+            assert np.array_equal(host(o.float()).astype(np.float64), want[i][0])
+
+
+def test_rounds_of_speculation_over_a_paged_cache():
+    """Reserve, append, attend, verify, compact, trim over several rounds of forked sequences, against lists of rows."""
+    rng = np.random.default_rng(50)
+    H, G, D, ps, B, layers, R = 4, 2, 32, 8, 4, 2, 13
+    num, width = 40, 12
+    K = torch.full((layers, num, ps, G, D), float("nan"), dtype=torch.bfloat16, device=DEV)
+    V = K.clone()
+    table = torch.full((B, width), -1, dtype=torch.int32, device=DEV)
+    refs = torch.zeros(num, dtype=torch.int32, device=DEV)
+    cache = wf.PagedCache(K, V, table, ref=refs)
+    ws = wf.PagedWorkspace(B, H, G, D, R)
+    vws = wf.Workspace(B * R, B)
+    ln = torch.zeros(B, dtype=torch.int32, device=DEV)
+    rows_of = [[] for _ in range(B)]                         # per sequence: (layers' keys, layers' values) of its positions
+
+    def append(rows, kv):
+        pos = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+        added = wf.wf_pages_reserve(cache, dev(pos), ln, ws)
+        for layer in range(layers):
+            wf.wf_paged_append(cache, kv[:, layer, 0], kv[:, layer, 1], dev(pos), ln, ws, layer=layer)
+        assert (host(added) >= 0).all()
+        return pos
+
+    def new_rows(n):
+        return torch.from_numpy(rng.standard_normal((n, layers, 2, G, D))).to(torch.bfloat16).to(DEV)
+
+    # two prompts, each forked once
+    rows = [11, 0, 16, 0]
+    kv = new_rows(sum(rows))
+    pos = append(rows, kv)
+    for b in range(B):
+        rows_of[b] = [kv[pos[b] + i] for i in range(rows[b])]
+    ln += dev(np.array(rows, np.int32))
+    wf.wf_pages_fork(cache, dev(np.array([0, 2], np.int32)), dev(np.array([1, 3], np.int32)), ln, ws)
+    rows_of[1], rows_of[3] = list(rows_of[0]), list(rows_of[2])
+    assert host(ln).tolist() == [11, 11, 16, 16]
+    for step in range(4):
+        rows = [R, 1, 7, R] if step % 2 else [5, R, R, 2]
+        kinds = np.array([1, 0, 1, 1], np.int32)
+        P = sum(rows)
+        kv, q = new_rows(P), torch.from_numpy(rng.standard_normal((P, H, D))).to(torch.bfloat16).to(DEV)
+        node = np.concatenate([[0], np.cumsum([r - 1 for r in rows])]).astype(np.int32)
+        par = np.array([int(rng.integers(max(-1, i - 4), i)) if kinds[b] else i - 1
+                        for b in range(B) for i in range(rows[b] - 1)] or [0], np.int32)
+        tok = rng.integers(0, 2, len(par)).astype(np.int32)  # two tokens: paths are accepted a few deep
+        target = rng.integers(0, 2, P).astype(np.int32)
+        pos = append(rows, kv)
+        before = host(ln).copy()
+        for layer in range(layers):
+            out, lse = wf.wf_paged_attention(cache, q, dev(pos), ln, ws, node_off=dev(node), kind=dev(kinds),
+                                             parent=dev(par), max_rows=R, layer=layer, with_lse=True)
+            # the same through the plain reference on the rows as the lists have them
+            c = ref.Case.__new__(ref.Case)
+            c.H, c.G, c.D, c.ps, c.kv, c.layer, c.B = H, G, D, ps, "bf16", 0, B
+            c.lens, c.rows, c.kinds, c.P = [int(x) for x in before], rows, list(kinds), P
+            c.q, c.pos_off, c.node_off, c.parent = q.cpu(), pos, node, par
+            c.k_scale = c.v_scale = None
+            c.dense = lambda b, g, which: torch.stack(  # noqa: E731
+                [r[layer, 0 if which == "K" else 1, g] for r in rows_of[b]] +
+                [kv[pos[b] + i, layer, 0 if which == "K" else 1, g] for i in range(rows[b])]).float().cpu().numpy().astype(np.float64)
+            ro, rl, to, tl = ref.attention(c, D ** -0.5)
+            assert np.all(np.abs(host(out.float()) - ro) <= to) and np.all(np.abs(host(lse) - rl) <= tl)
+        S = R - 1
+        # chains and trees as one verification of trees: a chain's parents are its predecessors
+        n_t, _, _, path_t = wf.wf_verify_tree(dev(target), dev(tok), dev(par), dev(node), dev(pos), vws, path_stride=S)
+        new = wf.wf_paged_compact(cache, n_t, path_t, ln, ws, new_len=ln)
+        assert new is ln
+        n_acc, path = host(n_t), host(path_t)
+        wf.wf_pages_trim(cache, ln, ws)
+        torch.cuda.synchronize()
+        assert ws.device_error() == (0, 0) and vws.device_error() == (0, 0)
+        for b in range(B):
+            rows_of[b].append(kv[pos[b]])
+            rows_of[b] += [kv[pos[b] + 1 + int(path[b, j])] for j in range(int(n_acc[b]))]
+            assert int(ln[b]) == len(rows_of[b]) == before[b] + n_acc[b] + 1
+        # every position of every sequence is the row it should be, in every layer
+        t = host(table)
+        for b in range(B):
+            for i, r in enumerate(rows_of[b]):
+                for layer in range(layers):
+                    assert torch.equal(K[layer, t[b, i // ps], i % ps], r[layer, 0])
+                    assert torch.equal(V[layer, t[b, i // ps], i % ps], r[layer, 1])
+            assert (t[b, -(-len(rows_of[b]) // ps):] == -1).all()
+        count = np.zeros(num, np.int32)
+        for p in t[t >= 0]:
+            count[p] += 1
+        assert np.array_equal(host(refs), count)
+    wf.wf_pages_trim(cache, torch.zeros_like(ln), ws)
+    assert (host(refs) == 0).all()
+
+
+def test_binding_refuses_wrong_tensors():
+    c = ref.Case(51, (20, 20), (3, 3), 4, 2, 32, 16)
+    cache, ws = cache_of(c), wf.PagedWorkspace(2, 4, 2, 32, 3)
+    pos, ln, q = dev(c.pos_off), dev(np.array(c.lens, np.int32)), c.q.to(DEV)
+    for bad in (dict(q=q.float()), dict(q=q[:, :, :16]), dict(q=q.transpose(0, 1)), dict(pos_off=pos[:2]),
+                dict(cache_len=ln.long()), dict(cache_len=ln.cpu()), dict(out=torch.empty(3, device=DEV))):
+        kw = dict(q=q, pos_off=pos, cache_len=ln, out=None)
+        kw.update(bad)
+        with pytest.raises(ValueError):
+            wf.wf_paged_attention(cache, kw["q"], kw["pos_off"], kw["cache_len"], ws, max_rows=3, out=kw["out"])
+    with pytest.raises(wf.WfError):
+        wf.wf_paged_attention(cache, q, pos, ln, ws, max_rows=3, layer=1)
+    with pytest.raises(wf.WfError):
+        wf.wf_pages_trim(cache, ln, ws)                      # no reference counts
+    with pytest.raises(ValueError):
+        wf.PagedCache(cache.K, cache.V[:, :1], cache.table)
+    with pytest.raises(ValueError):
+        wf.PagedCache(cache.K, cache.V, cache.table, k_scale=torch.ones(2, device=DEV))
+    with pytest.raises(ValueError):
+        wf.PagedWorkspace(2, 5, 2, 32)
+    small = wf.PagedWorkspace(2, 4, 2, 32, 1)                # made for single tokens
+    with pytest.raises(wf.WfError):
+        wf.wf_paged_attention(cache, q, pos, ln, small, max_rows=3)
