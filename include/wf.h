@@ -26,9 +26,9 @@
  *   allocated by the caller; the library allocates nothing and keeps no
  *   per-call state outside the caller's workspace.  Operands the kernels copy
  *   with the tensor-memory accelerator or bulk copies (weight matrices,
- *   hidden states, backlog rows, the key / value caches) must be memory of
- *   the current device: a host pointer or another GPU's memory there returns
- *   WF_ERR_INVALID_ARG.
+ *   hidden states, backlog rows, the key / value caches, the queries of drafted
+ *   rows) must be memory of the current device: a host pointer or another
+ *   GPU's memory there returns WF_ERR_INVALID_ARG.
  * - bf16 tensors are passed as raw uint16 bit patterns, row-major, densely
  *   packed (row stride = number of columns), 16-byte aligned.
  * - Every call is asynchronous on `stream`: it validates its arguments on the
@@ -503,7 +503,9 @@ typedef struct wf_paged_cache {
  * Workspace (bytes) of the wf_paged_* and wf_pages_* calls on a cache of B
  * sequences, G KV heads of size D, with H query heads and at most max_rows
  * rows a sequence (both only matter to wf_paged_attention).  0 if the shapes
- * are out of range.  Zero it once with wf_workspace_init.
+ * are out of range.  Zero it once with wf_workspace_init, and keep it for these
+ * calls (of any shapes it is large enough for): the other calls' scratch lies
+ * where these keep counters.
  */
 WF_API size_t wf_paged_workspace_bytes(int B, int H, int G, int D, int max_rows);
 
@@ -511,7 +513,7 @@ WF_API size_t wf_paged_workspace_bytes(int B, int H, int G, int D, int max_rows)
  * A round's new keys and values enter the cache: row pos_off[b] + i of k and v
  * becomes position cache_len[b] + i of sequence b in `layer`.
  * k, v device, P rows of [G, D] bf16 bits, k_stride / v_stride elements from
- * row to row (a multiple of 8, at least G * D: slices of one projection's
+ * row to row (a multiple of 8, from G * D to 2^30: slices of one projection's
  * output are fine); pos_off [B+1], cache_len [B] device int32.  WF_KV_E4M3
  * stores x / scale, saturated to +-448 and rounded to the nearest value (ties
  * to even; NaN stays NaN).  Rows outside [pos_off[0], pos_off[B]) are not read
@@ -547,7 +549,7 @@ WF_API wf_status wf_paged_append(const wf_paged_cache* cache, int layer, const u
  */
 typedef struct wf_paged_attn_args {
     const uint16_t* q;         /* P rows of [H, D] bf16 bits, 16-byte aligned */
-    int64_t q_stride;          /* elements from row to row: a multiple of 8, at least H * D */
+    int64_t q_stride;          /* elements from row to row: a multiple of 8, from H * D to 2^30 */
     int P, H;                  /* rows; query heads (H % G == 0, H / G <= 128, H * D <= 65536) */
     const int32_t* pos_off;    /* [B+1] */
     const int32_t* cache_len;  /* [B] positions before this round's rows */

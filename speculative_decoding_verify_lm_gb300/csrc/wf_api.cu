@@ -49,7 +49,7 @@ wf_status noalloc_lmhead_argmax(const uint16_t* hidden, const uint16_t* W, int P
                                 float* maxlogit, cudaStream_t s);
 wf_status noalloc_read_device_error(int* code, int* info, int clear, cudaStream_t s);
 
-size_t paged_workspace_bytes(int B, int H, int G, int D, int max_rows);
+size_t paged_workspace_bytes(int D, int max_rows);
 wf_status launch_paged_append(const wf_paged_cache* c, int layer, const uint16_t* k, int64_t k_stride,
                               const uint16_t* v, int64_t v_stride, int P, const int32_t* pos_off,
                               const int32_t* cache_len, void* ws, cudaStream_t s);
@@ -483,8 +483,11 @@ static bool bad_paged_heads(int B, int H, int G, int D, int max_rows) {
     return H < G || H % G || H / G > 128 || (long)H * D > 65536;
 }
 
+// elements from row to row of queries, keys or values
+static bool bad_paged_stride(int64_t stride, int64_t row) { return stride < row || stride > (1ll << 30) || stride % 8; }
+
 size_t wf_paged_workspace_bytes(int B, int H, int G, int D, int max_rows) {
-    return bad_paged_heads(B, H, G, D, max_rows) ? 0 : paged_workspace_bytes(B, H, G, D, max_rows);
+    return bad_paged_heads(B, H, G, D, max_rows) ? 0 : paged_workspace_bytes(D, max_rows);
 }
 
 // The cache's description and the workspace; `pages` = the call counts references.
@@ -500,7 +503,7 @@ static wf_status check_paged(const wf_paged_cache* c, int H, int max_rows, bool 
     // grids and column counts stay 32-bit: 16-byte columns of all layers' rows
     if ((long long)c->layers * 2 * c->G * c->D / 8 > 0x3FFFFFFFll) return WF_ERR_INVALID_ARG;
     if (pages && !c->ref) return WF_ERR_INVALID_ARG;
-    WF_TRY(check_ws(ws, ws_bytes, paged_workspace_bytes(c->B, H, c->G, c->D, max_rows)));
+    WF_TRY(check_ws(ws, ws_bytes, paged_workspace_bytes(c->D, max_rows)));
     WF_TRY(check_device());
     return check_local({c->K, c->V});
 }
@@ -510,7 +513,7 @@ wf_status wf_paged_append(const wf_paged_cache* c, int layer, const uint16_t* k,
                           size_t ws_bytes, wf_stream_t stream) {
     if (!c || layer < 0 || layer >= c->layers || P < 0 || !k || !v || !pos_off || !cache_len) return WF_ERR_INVALID_ARG;
     const int64_t row = (int64_t)c->G * c->D;
-    if (k_stride < row || k_stride % 8 || v_stride < row || v_stride % 8 || !aligned16(k) || !aligned16(v))
+    if (bad_paged_stride(k_stride, row) || bad_paged_stride(v_stride, row) || !aligned16(k) || !aligned16(v))
         return WF_ERR_INVALID_ARG;
     WF_TRY(check_paged(c, c->G, 1, false, ws, ws_bytes));
     return launch_paged_append(c, layer, k, k_stride, v, v_stride, P, pos_off, cache_len, ws, stream);
@@ -521,9 +524,10 @@ wf_status wf_paged_attention(const wf_paged_cache* c, const wf_paged_attn_args* 
     if (!c || !a || a->layer < 0 || a->layer >= c->layers || a->P < 0) return WF_ERR_INVALID_ARG;
     if (!a->q || !a->out || !a->pos_off || !a->cache_len || (a->parent && !a->node_off)) return WF_ERR_INVALID_ARG;
     if (!(a->scale > 0.f) || !(a->scale < INFINITY)) return WF_ERR_INVALID_ARG;
-    if (!aligned16(a->q) || !aligned16(a->out) || a->q_stride % 8 || a->q_stride < (int64_t)a->H * c->D)
+    if (!aligned16(a->q) || !aligned16(a->out) || bad_paged_stride(a->q_stride, (int64_t)a->H * c->D))
         return WF_ERR_INVALID_ARG;
     WF_TRY(check_paged(c, a->H, a->max_rows, false, ws, ws_bytes));
+    if (a->max_rows > 1) WF_TRY(check_local({a->q}));   // read by tensor copies
     if (a->P == 0) return WF_OK;
     // one row a sequence: the kernel for single tokens, bound by the cache's bytes;
     // drafted rows: the tensor-core one, which shares a read of the cache among them

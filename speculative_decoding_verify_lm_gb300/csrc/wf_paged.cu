@@ -544,8 +544,8 @@ __global__ void __launch_bounds__(FK_THREADS)
 }
 
 // ------------------------------------------------------------------ host side
-size_t paged_workspace_bytes(int B, int H, int G, int D, int max_rows) {
-    return paged_layout(B, H, G, D, max_rows).total;
+size_t paged_workspace_bytes(int D, int max_rows) {
+    return paged_layout(D, max_rows).total;
 }
 
 static int64_t kv_bytes(const wf_paged_cache* c) { return c->kv_type == WF_KV_E4M3 ? 1 : 2; }
@@ -590,7 +590,7 @@ wf_status launch_paged_compact(const wf_paged_cache* c, const int32_t* n_accept,
     p.path = path;
     p.cache_len = cache_len;
     p.new_len = new_len;
-    p.cnt = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + paged_layout(c->B, c->G, c->G, c->D, 1).cnt);
+    p.cnt = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(ws) + paged_layout(c->D, 1).cnt);
     p.row_bytes = (int)(c->G * c->D * kv_bytes(c));
     p.layer_bytes = (int64_t)c->num_pages * c->page_size * p.row_bytes;
     p.path_stride = path_stride;
@@ -613,7 +613,7 @@ wf_status launch_pages_reserve(const wf_paged_cache* c, const int32_t* pos_off, 
                cudaSuccess;
     }));
     uint8_t* w = static_cast<uint8_t*>(ws);
-    const PagedLayout L = paged_layout(c->B, c->G, c->G, c->D, 1);
+    const PagedLayout L = paged_layout(c->D, 1);
     ReserveParams p = {};
     p.table = c->table;
     p.ref = c->ref;

@@ -18,26 +18,24 @@ struct PagedLayout {
     size_t cnt, off, need, copies, join, stat, part, total;
 };
 
-// rows of the attention's partial area: two partials of a tile for each CTA
-inline size_t paged_part_rows(int H, int G, int max_rows) {
-    (void)H;
-    (void)G;
+// The counters have a fixed place, sized for the most sequences: calls of
+// different shapes share a workspace and none writes where another counts.
+// Partial results: two partials of a tile for each CTA.
+inline PagedLayout paged_layout(int D, int max_rows) {
+    constexpr size_t SEQS = WF_PAGED_MAX_SEQS;
+    static_assert(SEQS >= PA_MAX_CTAS, "a counter for each CTA");
     const size_t token = (size_t)PA_MAX_CTAS * 2 * PA_TILE_M, rounds = (size_t)PA_MAX_ROUND_CTAS * 2 * PA_ROUND_M;
-    return max_rows > 1 ? (rounds > token ? rounds : token) : token;
-}
-
-inline PagedLayout paged_layout(int B, int H, int G, int D, int max_rows) {
+    const size_t rows = max_rows > 1 && rounds > token ? rounds : token;
     PagedLayout L;
-    const size_t rows = paged_part_rows(H, G, max_rows);
     size_t o = sizeof(Control);
     L.cnt = o;
-    o = align_up(o + 4 * (size_t)(B > PA_MAX_CTAS ? B : PA_MAX_CTAS), 256);
+    o = align_up(o + 4 * SEQS, 256);
     L.off = o;
-    o = align_up(o + 4 * (size_t)B, 256);
+    o = align_up(o + 4 * SEQS, 256);
     L.need = o;
-    o = align_up(o + 4 * (size_t)B, 256);
+    o = align_up(o + 4 * SEQS, 256);
     L.copies = o;
-    o = align_up(o + 8 * (size_t)B, 256);
+    o = align_up(o + 8 * SEQS, 256);
     L.join = o;
     o = align_up(o + 16 * (size_t)PA_MAX_ROUND_CTAS, 256);
     L.stat = o;
@@ -79,6 +77,22 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t w) {
     asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)w));
     return r;
 }
+
+// fp16 queries: a row whose largest element is `big` is divided by 2^e, which
+// puts it in [1, 2) (a row of zeros or subnormals lower).  Within +-126 both 2^e
+// and 2^-e are normal numbers; bf16's largest exponent, 127, leaves [2, 4).
+__device__ __forceinline__ int pg_scale_exponent(float big) {
+    return min(max((int)(__float_as_uint(big) >> 23) - 127, -126), 126);
+}
+// The factor that turns such a row's products into base-2 exponents.  Never 0,
+// which would make NaN of a masked score (-inf); products below it are nothing.
+__device__ __forceinline__ float pg_factor(float s, int e) {
+    const float f = s * __uint_as_float((uint32_t)(127 + e) << 23);
+    return f < 1e-37f ? 1e-37f : f;
+}
+
+// largest base-2 exponent that stands for itself in fp32: rounded by 1/32 at most
+constexpr float PG_FAR = 1048576.f;
 
 // ----------------------------------------------------------------- matrix instructions
 __device__ __forceinline__ void pg_mma_bf16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {

@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
     if (warp >= 8) {
         if (S::SPLIT_REGISTERS) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         if (warp == 8) {
-            // ---------------------------------------- copies: tile n's keys to ring place 2 n, its values to 2 n + 1
+            // ---------------------------------------- copies: a tile's keys, then its values, to the ring's next places
             const uint64_t pol = policy_evict_first();
             const int per_tile = PR_KT / p.box_rows;   // boxes of a tile: at most 16
             // the stretch's first item: `start`, the weight before it; its tile kt is
@@ -402,7 +402,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                 x.kt = ((int)in_item + weight - 1) / weight;
                 if (x.kt == x.w.nt) next_item();
             }
-            int n = 0, k = 0;                          // tiles, pieces that have any
+            int sent = 0, k = 0;   // tiles of keys or values, pieces' queries copied or being copied
             for (int turn = 0;; ++turn) {
                 if (turn >= 8 && !mbar_wait(&piece_free[turn & 7], ((turn >> 3) & 1) ^ 1, p.timeout_ns, abort_flag)) {
                     *abort_flag = 1;
@@ -434,7 +434,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                                    : -2;
                     };
                     look_up(x.kt);
-                    for (int i = 0; i < x.tiles; ++i, ++n) {
+                    for (int i = 0; i < x.tiles; ++i) {
                         const int t = (x.kt + i) * PR_KT + lane * p.box_rows;
                         const bool ok = page >= 0 && page < p.num_pages;
                         bad |= page != -2 && !ok;
@@ -455,9 +455,10 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                                             tma_load_3d(sQ + w * QTILE + blk * PR_ROWS * 128, &tmQ, &q_full, blk * 64,
                                                         x.g * p.hq, x.w.r0 + (2 * x.mp + w) * p.rpt);
                                 }
+                                ++k;
                                 __syncwarp();
                             }
-                            const int at = 2 * n + kv;
+                            const int at = sent;
                             // the raw tiles' turn for an 8-bit cache, else the ring's
                             constexpr int PLACES = E4M3 ? 2 : RING;
                             const int place = at % PLACES;
@@ -468,6 +469,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                             if (!alive) break;
                             const int row_bytes = E4M3 ? p.D : BLK * 128;
                             if (lane == 0) mbar_arrive_expect_tx(full, boxes * p.box_rows * row_bytes);
+                            ++sent;
                             __syncwarp();
                             if (ok && E4M3) {
                                 tma_load_2d(sW + place * S::RAW_TILE + lane * p.box_rows * p.D, kv ? &tmV : &tmK, full,
@@ -490,17 +492,16 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                 if (!x.w.bad) {   // whether the piece had a position without a page
                     bad = __any_sync(0xffffffffu, bad);
                     if (lane == 0) {
-                        s_bad[k & 7] = bad;
-                        mbar_arrive(&told[k & 7]);
+                        s_bad[(k - 1) & 7] = bad;
+                        mbar_arrive(&told[(k - 1) & 7]);
                     }
-                    ++k;
                 }
                 if (*abort_flag) break;
                 next_item();
             }
             // let every copy issued land before the shared memory goes
             constexpr int PLACES = E4M3 ? 2 : RING;
-            for (int at = max(0, 2 * n - PLACES); at < 2 * n; ++at)
+            for (int at = max(0, sent - PLACES); at < sent; ++at)
                 mbar_wait(E4M3 ? &raw_full[at % PLACES] : &kv_full[at % PLACES], (at / PLACES) & 1, p.timeout_ns, nullptr);
             if (k > 0) mbar_wait(&q_full, (k & 1) ^ 1, p.timeout_ns, nullptr);
         } else if (warp >= 11) {
@@ -708,7 +709,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             const int r = first + row / p.hq;
             const bool live = row < p.rpt * p.hq && r < x.w.rows;
             const bool warp_live = (row & ~31) < p.rpt * p.hq && first + (row & ~31) / p.hq < x.w.rows;
-            float m = -INFINITY, l = 0.f;
+            float m = -INFINITY, l = 0.f;   // running maximum of the scores as they are, sum
             int* odd_word = &s_odd[turn & 1][w];
             bool bad = x.w.bad, tree = false;
             const int mine_tiles = x.solo ? (x.tiles - w + 1) / 2 : x.tiles;   // tiles of this stream
@@ -757,8 +758,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                         big = max3(big, fabsf(lo(y.z)), fabsf(hi(y.z)));
                         big = max3(big, fabsf(lo(y.w)), fabsf(hi(y.w)));
                     }
-                    // exponents within +-100 of 1 keep both the scaling and its inverse normal
-                    const int e = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 100);
+                    const int e = pg_scale_exponent(big);
                     const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll 4
                     for (int c = 0; c < p.D / 8; ++c) {
@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                         *piece(c) = make_uint4(cvt_f16x2(lo(y.x) * down, hi(y.x) * down), cvt_f16x2(lo(y.y) * down, hi(y.y) * down),
                                                cvt_f16x2(lo(y.z) * down, hi(y.z) * down), cvt_f16x2(lo(y.w) * down, hi(y.w) * down));
                     }
-                    f = p.qk * (p.k_scale ? __ldg(p.k_scale + x.g) : 1.f) * __uint_as_float((uint32_t)(127 + e) << 23);
+                    f = pg_factor(p.qk * (p.k_scale ? __ldg(p.k_scale + x.g) : 1.f), e);
                     if (x.solo) s_factor[row] = f;
                     fence_async_smem();
                     mbar_arrive(&q_ready[w]);
@@ -843,8 +843,8 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                                 fetch(0);
                                 const float low = largest(-INFINITY);
                                 fetch(2);
-                                const float mn = fmaxf(m, largest(low) * f);
-                                const float a = m == -INFINITY ? 0.f : ex2_approx(m - mn);
+                                const float mn = fmaxf(m, largest(low));
+                                const float a = m == -INFINITY ? 0.f : ex2_approx((m - mn) * f);
                                 m = mn;
                                 l *= a;
                                 if (i > 0)   // every earlier product into O has completed before this tile's scores
@@ -857,13 +857,24 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                                         tmem_st_x16(tO + c, y);
                                     }
                             }
-                            const float base = (m == -INFINITY ? 0.f : -m) + S::BIAS;
+                            // exponents relative to the maximum's rounded product with f,
+                            // or past PG_FAR to the maximum itself (as for single tokens)
+                            float base = S::BIAS - (m == -INFINITY ? 0.f : m * f);
+                            const bool far = __any_sync(0xffffffffu, fabsf(base) > PG_FAR);
+                            if (far) base = S::BIAS;
                             const uint64_t qk2 = pair_of(f, f), base2 = pair_of(base, base);
                             uint64_t sum2[2] = {0, 0};
                             float big = -INFINITY;
 #pragma unroll
                             for (int c0 = 0; c0 < 4; c0 += 2) {
                                 fetch(c0);
+                                if (far) {
+#pragma unroll
+                                    for (int c = 0; c < 2; ++c)
+#pragma unroll
+                                        for (int e = 0; e < 32; ++e)
+                                            s[c][e] = __float_as_uint(at(c, e) - (m == -INFINITY ? 0.f : m));
+                                }
                                 if (!again) big = largest(big);
 #pragma unroll
                                 for (int c = 0; c < 2; ++c)
@@ -876,7 +887,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                                         pk[c0 + c][e] = E4M3 ? cvt_f16x2(p0, p1) : cvt_bf16x2(p0, p1);
                                     }
                             }
-                            if (again || !__any_sync(0xffffffffu, big * f > m + S::LAG)) {
+                            if (again || !__any_sync(0xffffffffu, (far ? big : big - m) * f > S::LAG)) {
                                 float a0, a1;
                                 unpair(add2(sum2[0], sum2[1]), a0, a1);
                                 sum = a0 + a1;
@@ -960,6 +971,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             const int slot = (int)blockIdx.x * 2 + (x.kt == 0 ? 1 : 0);
             const int prow = (x.solo ? 0 : w * p.rpt * p.hq) + row;   // pair within the item
             const bool writer = !(x.solo && w == 1) && live;
+            m *= f;   // as exponents from here on
             float w0 = 1.f, w1 = 0.f, M = m, L = l;
             if (merge) {
                 if (w == 1) s_xst[row] = make_float2(m, l);
@@ -1237,7 +1249,7 @@ wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args*
     }));
     const bool e4m3 = c->kv_type == WF_KV_E4M3;
     uint8_t* w = static_cast<uint8_t*>(ws);
-    const PagedLayout L = paged_layout(c->B, a->H, c->G, c->D, a->max_rows);
+    const PagedLayout L = paged_layout(c->D, a->max_rows);
     const int64_t layer_bytes = (int64_t)c->num_pages * c->page_size * c->G * c->D * (e4m3 ? 1 : 2);
     const uint8_t* K = static_cast<const uint8_t*>(c->K) + a->layer * layer_bytes;
     RoundsParams p = {};

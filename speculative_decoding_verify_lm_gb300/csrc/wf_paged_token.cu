@@ -326,9 +326,15 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
         const int tiles = min(left, c.w.nt - c.kt);
         const int kt_first = c.kt;
         bool bad = c.w.bad;
-        // of heads 2 cq, 2 cq + 1 of each tile: running maximum, this lane's
-        // share of the sum, the scores' factor
+        // of heads 2 cq, 2 cq + 1 of each tile: running maximum of the scores as
+        // they are, this lane's share of the sum, the scores' factor
         float m[NH][2], l[NH][2], f[NH][2];
+        // Exponents are taken relative to the maximum's rounded product with f: its
+        // rounding is one factor for the whole row.  A product past PG_FAR rounds
+        // by too much for that (keys of the type's lowest value); there the
+        // maximum is taken off the scores themselves.
+        float base[NH][2];
+        bool far = false;
 #pragma unroll
         for (int h = 0; h < NH; ++h) {
 #pragma unroll
@@ -336,6 +342,7 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
                 m[h][u] = -INFINITY;
                 l[h][u] = 0.f;
                 f[h][u] = p.qk;
+                base[h][u] = PBIAS;   // no score above -inf yet: weights of 0
             }
 #pragma unroll
             for (int i = 0; i < NKS; ++i) o[h][i][0] = o[h][i][1] = o[h][i][2] = o[h][i][3] = 0.f;
@@ -381,8 +388,7 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
                         }
 #pragma unroll
                         for (int w = 1; w <= 2; w <<= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, w));
-                        // exponents within +-100 of 1 keep both the scaling and its inverse normal
-                        const int e = min(max((int)(__float_as_uint(big) >> 23) - 127, -100), 100);
+                        const int e = pg_scale_exponent(big);
                         const float down = __uint_as_float((uint32_t)(127 - e) << 23);
 #pragma unroll
                         for (int ks = 0; ks < NKS; ++ks)
@@ -390,7 +396,7 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
                             for (int u = 0; u < 2; ++u)
                                 qb[h][ks][u] = cvt_f16x2(lo(qb[h][ks][u]) * down, hi(qb[h][ks][u]) * down);
                         const float ksc = p.qk * (p.k_scale ? __ldg(p.k_scale + c.g) : 1.f);
-                        const float mine_f = ksc * __uint_as_float((uint32_t)(127 + e) << 23);   // of head gq
+                        const float mine_f = pg_factor(ksc, e);   // of head gq
 #pragma unroll
                         for (int u = 0; u < 2; ++u) f[h][u] = __shfl_sync(0xffffffffu, mine_f, (2 * cq + u) * 4);
                     }
@@ -452,8 +458,8 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
                         float x = fmaxf(sc[0][h][u], sc[0][h][2 + u]);
 #pragma unroll
                         for (int b = 1; b < NB; ++b) x = fmaxf(x, fmaxf(sc[b][h][u], sc[b][h][2 + u]));
-                        mx[h][u] = x * (E4M3 ? f[h][u] : p.qk);
-                        grown |= mx[h][u] > m[h][u] + LAG;
+                        mx[h][u] = x;
+                        grown |= (x - m[h][u]) * (E4M3 ? f[h][u] : p.qk) > LAG;
                     }
                 if (__any_sync(0xffffffffu, grown)) {
 #pragma unroll
@@ -464,7 +470,7 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
 #pragma unroll
                             for (int w = 4; w <= 16; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
                             x = fmaxf(x, m[h][u]);
-                            const float a = m[h][u] == -INFINITY ? 0.f : ex2_approx(m[h][u] - x);
+                            const float a = m[h][u] == -INFINITY ? 0.f : ex2_approx((m[h][u] - x) * (E4M3 ? f[h][u] : p.qk));
                             m[h][u] = x;
                             l[h][u] *= a;
 #pragma unroll
@@ -473,6 +479,29 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
                                 o[h][t][2 + u] *= a;
                             }
                         }
+                    far = false;
+#pragma unroll
+                    for (int h = 0; h < NH; ++h)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            base[h][u] = PBIAS - (m[h][u] == -INFINITY ? 0.f : m[h][u] * (E4M3 ? f[h][u] : p.qk));
+                            far |= fabsf(base[h][u]) > PG_FAR;
+                        }
+                    far = __any_sync(0xffffffffu, far);
+                    if (far)
+#pragma unroll
+                        for (int h = 0; h < NH; ++h) base[h][0] = base[h][1] = PBIAS;
+                }
+                if (far) {
+#pragma unroll
+                    for (int h = 0; h < NH; ++h)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u)
+#pragma unroll
+                            for (int b = 0; b < NB; ++b) {
+                                sc[b][h][u] -= m[h][u] == -INFINITY ? 0.f : m[h][u];
+                                sc[b][h][2 + u] -= m[h][u] == -INFINITY ? 0.f : m[h][u];
+                            }
                 }
 #pragma unroll
                 for (int b = 0; b < NB; ++b) {
@@ -481,8 +510,8 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
                     for (int h = 0; h < NH; ++h)
 #pragma unroll
                         for (int u = 0; u < 2; ++u) {
-                            const float p0 = ex2_approx(fmaf(sc[b][h][2 * u], E4M3 ? f[h][0] : p.qk, PBIAS - m[h][0]));
-                            const float p1 = ex2_approx(fmaf(sc[b][h][2 * u + 1], E4M3 ? f[h][1] : p.qk, PBIAS - m[h][1]));
+                            const float p0 = ex2_approx(fmaf(sc[b][h][2 * u], E4M3 ? f[h][0] : p.qk, base[h][0]));
+                            const float p1 = ex2_approx(fmaf(sc[b][h][2 * u + 1], E4M3 ? f[h][1] : p.qk, base[h][1]));
                             l[h][0] += p0;
                             l[h][1] += p1;
                             pb[h][u] = transpose8(E4M3 ? cvt_f16x2(p0, p1) : cvt_bf16x2(p0, p1));
@@ -529,6 +558,7 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
                 for (int w = 4; w <= 16; w <<= 1) l[h][u] += __shfl_xor_sync(0xffffffffu, l[h][u], w);
+                m[h][u] *= E4M3 ? f[h][u] : p.qk;
                 if (gq == 0) s_st[warp][h * 8 + 2 * cq + u] = make_float2(m[h][u], l[h][u]);
             }
         consumer_sync();   // also: every warp is done with this stage's keys and values
@@ -568,7 +598,7 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
                 const float2 x = s_st[w][h];
-                L += x.x == -INFINITY ? 0.f : x.y * ex2_approx(x.x - M);
+                L += x.y * (x.x == -INFINITY ? 0.f : ex2_approx(x.x - M));   // a NaN sum stays one
             }
             return bad ? make_float2(NAN, NAN) : make_float2(M, L);
         };
@@ -588,6 +618,13 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
                 const int h = i / half, d = (i - h * half) * 2;
                 write(h, d, value(h, d), row_stat(h));
             }
+            if (c.w.bad)   // all of its rows are NaN, not the first alone
+                for (int64_t row = c.w.row + 1, r1 = p.pos_off[c.b + 1]; row < r1; ++row)
+                    for (int i = tid; i < heads * half; i += PT_CONSUMERS) {
+                        const int64_t at = row * p.H + c.g * p.hq + c.m * HEADS + i / half;
+                        *reinterpret_cast<uint32_t*>(p.out + at * p.D + (i % half) * 2) = cvt_bf16x2(NAN, NAN);
+                        if (p.lse && i % half == 0) p.lse[at] = NAN;
+                    }
         } else {
             // a shared item: this piece to the workspace, joined by the last piece to arrive
             const int slot = (int)blockIdx.x * 2 + (kt_first == 0 ? 1 : 0);
@@ -700,7 +737,7 @@ wf_status launch_paged_token(const wf_paged_cache* c, const wf_paged_attn_args* 
         return true;
     }));
     uint8_t* w = static_cast<uint8_t*>(ws);
-    const PagedLayout L = paged_layout(c->B, a->H, c->G, c->D, a->max_rows);
+    const PagedLayout L = paged_layout(c->D, a->max_rows);
     const int64_t esize = e4m3 ? 1 : 2;
     const int64_t layer_bytes = (int64_t)c->num_pages * c->page_size * c->G * c->D * esize;
     TokenParams p = {};

@@ -539,7 +539,8 @@ class PagedCache:
 
 class PagedWorkspace(Workspace):
     """Workspace of the wf_paged_* / wf_pages_* calls on a cache of B sequences; H query heads and max_rows rows
-    a sequence as for wf_paged_attention (the other calls take any workspace of their B, G and D)."""
+    a sequence as for wf_paged_attention (the other calls take any workspace of their G and D).  Those calls take no
+    other workspace: elsewhere scratch may lie where they keep counters."""
 
     def __init__(self, B: int, H: int, G: int, D: int, max_rows: int = 1, device=None, stream=None):
         self.nbytes = int(lib().wf_paged_workspace_bytes(B, H, G, D, max_rows))
@@ -547,6 +548,12 @@ class PagedWorkspace(Workspace):
             raise ValueError("paged cache shapes outside the library's range")
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device or "cuda")
         _raise(lib().wf_workspace_init(self.buf.data_ptr(), self.nbytes, _stream(stream)), "wf_workspace_init")
+
+
+def _paged(ws):
+    if not isinstance(ws, PagedWorkspace):
+        raise ValueError("ws must be a PagedWorkspace")
+    return ws.buf.data_ptr(), ws.nbytes
 
 
 def _rows(t, name, heads, D):
@@ -572,7 +579,7 @@ def _lens(t, name, n, optional=False):
     return t.data_ptr() if n else _placeholder(t.device)
 
 
-def wf_paged_append(cache: PagedCache, k, v, pos_off, cache_len, ws: Workspace, layer: int = 0, stream=None):
+def wf_paged_append(cache: PagedCache, k, v, pos_off, cache_len, ws: PagedWorkspace, layer: int = 0, stream=None):
     """Store the round's keys and values (rows pos_off[b] + i of k, v [P, G, D] bf16, strided rows allowed) at
     positions cache_len[b] + i of each sequence."""
     a = cache.args
@@ -581,11 +588,11 @@ def wf_paged_append(cache: PagedCache, k, v, pos_off, cache_len, ws: Workspace, 
     if k.shape[0] != v.shape[0]:
         raise ValueError("k and v must have the same rows")
     _raise(lib().wf_paged_append(cache._ref, layer, kp, ks, vp, vs, k.shape[0], _lens(pos_off, "pos_off", a.B + 1),
-                                 _lens(cache_len, "cache_len", a.B), ws.ptr, ws.nbytes, _stream(stream)),
+                                 _lens(cache_len, "cache_len", a.B), *_paged(ws), _stream(stream)),
            "wf_paged_append")
 
 
-def wf_paged_attention(cache: PagedCache, q, pos_off, cache_len, ws: Workspace, node_off=None, kind=None, parent=None,
+def wf_paged_attention(cache: PagedCache, q, pos_off, cache_len, ws: PagedWorkspace, node_off=None, kind=None, parent=None,
                        max_rows: int = 1, layer: int = 0, scale=None, out=None, lse=None, with_lse: bool = False,
                        stream=None):
     """Attention of the round's rows over the paged cache -> (out [P, H, D] bf16, lse [P, H] fp32 or None).
@@ -617,12 +624,12 @@ def wf_paged_attention(cache: PagedCache, q, pos_off, cache_len, ws: Workspace, 
         raise ValueError("lse must be [P, H]")
     if lse is not None:
         a.lse = _check(lse, "lse", _F32)
-    _raise(lib().wf_paged_attention(cache._ref, ctypes.byref(a), ws.ptr, ws.nbytes, _stream(stream)),
+    _raise(lib().wf_paged_attention(cache._ref, ctypes.byref(a), *_paged(ws), _stream(stream)),
            "wf_paged_attention")
     return out, lse
 
 
-def wf_paged_compact(cache: PagedCache, n_accept, path, cache_len, ws: Workspace, new_len=None, stream=None):
+def wf_paged_compact(cache: PagedCache, n_accept, path, cache_len, ws: PagedWorkspace, new_len=None, stream=None):
     """Move the accepted path's keys and values up behind the round's first row, in every layer -> new_len [B]
     (pass cache_len as new_len to update it in place)."""
     B = cache.args.B
@@ -632,32 +639,32 @@ def wf_paged_compact(cache: PagedCache, n_accept, path, cache_len, ws: Workspace
         new_len = cache_len.new_empty(B)
     ps = path.shape[1] if path is not None else 0
     _raise(lib().wf_paged_compact(cache._ref, _lens(n_accept, "n_accept", B), _check(path, "path", _I32, True), ps,
-                                  _lens(cache_len, "cache_len", B), _lens(new_len, "new_len", B), ws.ptr, ws.nbytes,
+                                  _lens(cache_len, "cache_len", B), _lens(new_len, "new_len", B), *_paged(ws),
                                   _stream(stream)), "wf_paged_compact")
     return new_len
 
 
-def wf_pages_reserve(cache: PagedCache, pos_off, cache_len, ws: Workspace, added=None, stream=None):
+def wf_pages_reserve(cache: PagedCache, pos_off, cache_len, ws: PagedWorkspace, added=None, stream=None):
     """Pages for the round's rows, shared ones replaced by copies -> added [B] (pages taken, -1 = did not fit)."""
     B = cache.args.B
     if added is None:
         added = cache_len.new_empty(B)
     _raise(lib().wf_pages_reserve(cache._ref, _lens(pos_off, "pos_off", B + 1), _lens(cache_len, "cache_len", B),
-                                  _lens(added, "added", B), ws.ptr, ws.nbytes, _stream(stream)), "wf_pages_reserve")
+                                  _lens(added, "added", B), *_paged(ws), _stream(stream)), "wf_pages_reserve")
     return added
 
 
-def wf_pages_fork(cache: PagedCache, src, dst, cache_len, ws: Workspace, stream=None):
+def wf_pages_fork(cache: PagedCache, src, dst, cache_len, ws: PagedWorkspace, stream=None):
     """Sequences dst become copies of sequences src that share their pages; cache_len[dst] follows, in place."""
     n = src.numel()
     _raise(lib().wf_pages_fork(cache._ref, _check(src, "src", _I32), _lens(dst, "dst", n), n,
-                               _lens(cache_len, "cache_len", cache.args.B), ws.ptr, ws.nbytes, _stream(stream)),
+                               _lens(cache_len, "cache_len", cache.args.B), *_paged(ws), _stream(stream)),
            "wf_pages_fork")
 
 
-def wf_pages_trim(cache: PagedCache, cache_len, ws: Workspace, stream=None):
+def wf_pages_trim(cache: PagedCache, cache_len, ws: PagedWorkspace, stream=None):
     """Give back the pages past each sequence's length (0 frees the sequence)."""
-    _raise(lib().wf_pages_trim(cache._ref, _lens(cache_len, "cache_len", cache.args.B), ws.ptr, ws.nbytes,
+    _raise(lib().wf_pages_trim(cache._ref, _lens(cache_len, "cache_len", cache.args.B), *_paged(ws),
                                _stream(stream)), "wf_pages_trim")
 
 

@@ -1,6 +1,8 @@
 """The paged cache on the GPU against plain 64-bit references (paged_ref):
 attention of single tokens, chains and trees, appended and compacted rows, and
 the pages' bookkeeping.  Positions that no sequence owns hold NaN throughout."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -696,3 +698,139 @@ def test_binding_refuses_wrong_tensors():
     small = wf.PagedWorkspace(2, 4, 2, 32, 1)                # made for single tokens
     with pytest.raises(wf.WfError):
         wf.wf_paged_attention(cache, q, pos, ln, small, max_rows=3)
+
+
+def test_a_sequence_of_several_rows_among_single_tokens_is_nan():
+    c = ref.Case(60, (70, 9, 200), (1, 1, 1), 20, 2, 64, 16)
+    cache, ws = cache_of(c), wf.PagedWorkspace(3, 20, 2, 64)
+    good = run_attention(c, cache, ws=ws)
+    c.pos_off = np.array([0, 1, 4, 5], np.int32)             # the second sequence has three rows
+    c.P = 6
+    c.q = torch.cat([c.q[:1], c.q[1:2].expand(3, -1, -1), c.q[2:], c.q[:1]]).contiguous()
+    out, lse, _ = run_attention(c, cache, ws=ws, max_rows=1)
+    assert ws.device_error() == (BAD, 1)
+    assert np.isnan(out[1:4]).all() and np.isnan(lse[1:4]).all()
+    for new, old in ((0, 0), (4, 2)):
+        assert np.array_equal(out[new], good[0][old]) and np.array_equal(lse[new], good[1][old])
+    assert (out[5] == 7.0).all() and (lse[5] == 7.0).all()
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+def test_keys_of_minus_infinity_weigh_nothing(rows):
+    """Scores of -inf, over whole tiles and whole warps' shares of one, are weights of 0 and no NaN."""
+    c = ref.Case(61, (700,), (rows,), 4, 2, 64, 16)
+    c.q[:, :, 0] = c.q[:, :, 0].abs() + 0.125
+    outs = []
+    for low in (float("-inf"), -2.0 ** 100):
+        K = c.K.clone()
+        for t in [*range(0, 300), *range(320, 336), *range(400, 464), 500]:
+            c.K[0, c.table[0, t // 16], t % 16, :, 0] = low
+        outs.append(run_attention(c))
+        c.K = K
+    assert np.isfinite(outs[0][0]).all() and np.isfinite(outs[0][1]).all()
+    assert np.array_equal(outs[0][0], outs[1][0]) and np.array_equal(outs[0][1], outs[1][1])
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+def test_keys_that_are_nan_make_the_rows_nan(rows):
+    c = ref.Case(62, (700,), (rows,), 4, 2, 64, 16)
+    for t in range(320, 336):
+        c.K[0, c.table[0, t // 16], t % 16, 1, 3] = float("nan")
+    out, lse, ws = run_attention(c)
+    assert ws.device_error() == (0, 0)
+    assert np.isfinite(out[:, :2]).all() and np.isfinite(lse[:, :2]).all()
+    assert np.isnan(out[:, 2:]).all() and np.isnan(lse[:, 2:]).all()
+
+
+@pytest.mark.parametrize("rows", [1, 5])
+@pytest.mark.parametrize("power", [-120, 120])
+def test_queries_of_any_size_over_an_8_bit_cache(rows, power):
+    """Queries times 2^n against keys over 2^n: the same bits."""
+    c = ref.Case(63, (300,), (rows,), 8, 2, 64, 16, "e4m3")
+    c.q[0, 0] = 0                                            # a head without a direction: it weighs all alike
+    c.q = (c.q.float() * 2.0 ** power).to(torch.bfloat16)    # the least elements become subnormal and round
+    far_q = c.q.clone()
+    c.q = (far_q.double() * 2.0 ** -power).to(torch.bfloat16)   # exact: what the call far out is given
+    plain = run_attention(c)
+    c.q = far_q
+    c.k_scale = (np.asarray(c.k_scale) * 2.0 ** -power).astype(np.float32)
+    far = run_attention(c)
+    assert np.isfinite(far[0]).all()
+    assert np.array_equal(plain[0], far[0]) and np.array_equal(plain[1], far[1])
+
+
+def test_calls_of_other_shapes_share_a_workspace():
+    """A round's reserved pages for a few sequences, then a compaction of many, in one workspace."""
+    B, ps = 1500, 8
+    ws = wf.PagedWorkspace(B, 1, 1, 16)
+    K = torch.zeros((1, 8 * B, ps, 1, 16), dtype=torch.bfloat16, device=DEV)
+    few, pages = 600, 7
+    refs = torch.zeros(8 * B, dtype=torch.int32, device=DEV)
+    small = wf.PagedCache(K, K.clone(), torch.full((few, pages), -1, dtype=torch.int32, device=DEV), refs)
+    pos = torch.arange(few + 1, dtype=torch.int32, device=DEV) * (ps * pages)
+    added = wf.wf_pages_reserve(small, pos, torch.zeros(few, dtype=torch.int32, device=DEV), ws)
+    assert (added == pages).all().item()
+    table = torch.arange(B, dtype=torch.int32, device=DEV)[:, None]
+    big = wf.PagedCache(K, K.clone(), table.contiguous())
+    ln = torch.full((B,), 3, dtype=torch.int32, device=DEV)
+    n_acc = torch.arange(B, dtype=torch.int32, device=DEV) % 3
+    path = torch.arange(2, dtype=torch.int32, device=DEV).repeat(B, 1)
+    for _ in range(2):
+        new = torch.full((B,), -7, dtype=torch.int32, device=DEV)
+        wf.wf_paged_compact(big, n_acc, path, ln, ws, new_len=new)
+        assert torch.equal(new, ln + n_acc + 1)
+    assert ws.device_error() == (0, 0)
+
+
+def test_host_memory_is_refused():
+    """What the kernels copy with the tensor-memory accelerator must be this GPU's memory."""
+    c = ref.Case(64, (20, 20), (3, 1), 4, 2, 32, 16)
+    cache, ws = cache_of(c), wf.PagedWorkspace(2, 4, 2, 32, 3)
+    out = torch.full((c.P, 4, 32), 7.0, dtype=torch.bfloat16, device=DEV)
+    pos, ln, q = dev(c.pos_off), dev(np.array(c.lens, np.int32)), c.q.to(DEV)
+    a = wf.PagedAttnArgs(q=q.data_ptr(), q_stride=4 * 32, P=c.P, H=4, pos_off=pos.data_ptr(), cache_len=ln.data_ptr(),
+                         max_rows=3, layer=0, scale=0.25, out=out.data_ptr())
+    stream = torch.cuda.current_stream().cuda_stream
+    call = lambda cc, aa: wf.lib().wf_paged_attention(ctypes.byref(cc), ctypes.byref(aa), ws.ptr,  # noqa: E731
+                                                      ws.nbytes, stream)
+    pinned = torch.zeros(cache.K.numel() * 2, dtype=torch.uint8).pin_memory()
+    pageable = torch.zeros(cache.K.numel() * 2 + 64, dtype=torch.uint8)
+    for ptr in (pinned.data_ptr(), pageable.data_ptr() + (-pageable.data_ptr()) % 16):
+        for field in ("K", "V"):
+            other = wf.PagedCacheArgs.from_buffer_copy(cache.args)
+            setattr(other, field, ptr)
+            assert call(other, a) == 1, field
+        other = wf.PagedAttnArgs.from_buffer_copy(a)
+        other.q = ptr
+        assert call(cache.args, other) == 1
+    torch.cuda.synchronize()
+    assert (out == 7.0).all().item() and ws.device_error() == (0, 0)
+    assert call(cache.args, a) == 0
+    torch.cuda.synchronize()
+    assert ws.device_error() == (0, 0) and not (out == 7.0).all().item()
+
+
+def test_workspaces_of_other_calls_are_refused():
+    c = ref.Case(65, (20,), (1,), 4, 2, 32, 16)
+    with pytest.raises(ValueError):
+        wf.wf_paged_attention(cache_of(c), c.q.to(DEV), dev(c.pos_off), dev(np.array(c.lens, np.int32)),
+                              wf.Workspace(4096, 4))
+
+
+@pytest.mark.parametrize("rows", [1, 3])
+def test_keys_of_the_lowest_value_weigh_alike(rows):
+    """Every score the same, -3.4e38 / 64: the mean of the values, to its sums' and the output's rounding."""
+    c = ref.Case(66, (333,), (rows,), 4, 2, 64, 16)
+    low = torch.finfo(torch.bfloat16).min
+    c.K[:] = 0
+    c.K[..., 0] = low
+    c.q[:, :, 0] = 0.125
+    out, lse, ws = run_attention(c)
+    assert ws.device_error() == (0, 0)
+    for i in range(rows):
+        n = 333 + i + 1
+        for h in range(4):
+            v = c.dense(0, h // 2, "V")[:n]
+            tol = n * 2.0 ** -23 * np.abs(v).mean(0)
+            assert np.all(np.abs(out[i, h] - v.mean(0)) <= tol + 2.0 ** -8 * (np.abs(v.mean(0)) + tol))
+            assert abs(lse[i, h] - (low * 0.015625 + np.log(n))) <= 2.0 ** -22 * abs(low * 0.015625)
