@@ -612,7 +612,7 @@ def wf_paged_attention(cache: PagedCache, q, pos_off, cache_len, ws: PagedWorksp
     a.max_rows, a.layer = max_rows, layer
     a.scale = D ** -0.5 if scale is None else scale
     if out is None:
-        out = q.new_empty(q.shape)
+        out = torch.empty_like(q, memory_format=torch.contiguous_format)
         a.out = out.data_ptr() if a.P else _placeholder(q.device)
     elif out.numel() != q.numel():
         raise ValueError("out must be [P, H, D]")
@@ -636,7 +636,7 @@ def wf_paged_compact(cache: PagedCache, n_accept, path, cache_len, ws: PagedWork
     if path is not None and (path.dim() != 2 or path.shape[0] != B):
         raise ValueError("path must be [B, path_stride]")
     if new_len is None:
-        new_len = cache_len.new_empty(B)
+        new_len = torch.empty_like(cache_len)
     ps = path.shape[1] if path is not None else 0
     _raise(lib().wf_paged_compact(cache._ref, _lens(n_accept, "n_accept", B), _check(path, "path", _I32, True), ps,
                                   _lens(cache_len, "cache_len", B), _lens(new_len, "new_len", B), *_paged(ws),
@@ -648,7 +648,7 @@ def wf_pages_reserve(cache: PagedCache, pos_off, cache_len, ws: PagedWorkspace, 
     """Pages for the round's rows, shared ones replaced by copies -> added [B] (pages taken, -1 = did not fit)."""
     B = cache.args.B
     if added is None:
-        added = cache_len.new_empty(B)
+        added = torch.empty_like(cache_len)
     _raise(lib().wf_pages_reserve(cache._ref, _lens(pos_off, "pos_off", B + 1), _lens(cache_len, "cache_len", B),
                                   _lens(added, "added", B), *_paged(ws), _stream(stream)), "wf_pages_reserve")
     return added
