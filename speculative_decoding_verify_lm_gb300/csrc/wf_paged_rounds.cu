@@ -104,12 +104,15 @@ __device__ __forceinline__ RoundSeq round_seq(const RoundsParams& p, int b) {
 }
 
 // Weight of a tile of the query rows 2 rpt mp ..
+constexpr int PR_TWO = 4, PR_ONE = 3;
+// and of an item's beginning and end, where a CTA has three tiles or more on average
+constexpr int PR_ITEM = 12;
 __device__ __forceinline__ int tile_weight(const RoundsParams& p, const RoundSeq& w, int mp) {
-    return w.rows - mp * 2 * p.rpt > p.rpt ? 3 : 2;
+    return w.rows - mp * 2 * p.rpt > p.rpt ? PR_TWO : PR_ONE;
 }
-// Weight of a whole sequence: every tile of its products is weighed alike but the last rows'.
+// Weight of a whole sequence's tiles: those of its products are weighed alike but the last rows'.
 __device__ __forceinline__ int64_t seq_weight(const RoundsParams& p, const RoundSeq& w) {
-    return w.mp == 0 ? 0 : (int64_t)p.G * w.nt * (3 * (w.mp - 1) + tile_weight(p, w, w.mp - 1));
+    return w.mp == 0 ? 0 : (int64_t)p.G * w.nt * (PR_TWO * (w.mp - 1) + tile_weight(p, w, w.mp - 1));
 }
 
 // One piece of the CTA's stretch: tiles [kt, kt + tiles) of (sequence b, query rows 2 rpt mp .., KV head g).
@@ -271,7 +274,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
     __shared__ uint64_t q_ready[2];                        // queries brought to fp16, by stream
     __shared__ float2 s_xst[PR_ROWS];
     __shared__ float s_factor[PR_ROWS];                    // and their scores' factors, for the other stream
-    __shared__ int64_t s_plan, s_scan[THREADS / 32];
+    __shared__ int64_t s_plan, s_scan[2][THREADS / 32];
     volatile int* abort_flag = &abort_word;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -313,37 +316,43 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
 
     // ------------------------------------------------ this CTA's stretch (as in the single-token kernel)
     const int run = (p.B + THREADS - 1) / THREADS;
-    int64_t mine = 0;
-    bool heavy = false;   // a tile of weight 3
+    int64_t mine = 0, mine_items = 0;
+    bool heavy = false;   // a tile of weight PR_TWO
     for (int i = 0; i < run; ++i) {
         const int b = tid * run + i;
         if (b < p.B) {
             const RoundSeq w = round_seq(p, b);
             mine += seq_weight(p, w);
-            heavy |= w.mp > 0 && tile_weight(p, w, 0) == 3;
+            mine_items += (int64_t)p.G * w.mp;
+            heavy |= w.mp > 0 && tile_weight(p, w, 0) == PR_TWO;
             if (w.bad && blockIdx.x == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)b);
         }
     }
-    int64_t inc = mine;
+    int64_t inc = mine, inc_items = mine_items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += y;
+        const int64_t y = __shfl_up_sync(0xffffffffu, inc, o), z = __shfl_up_sync(0xffffffffu, inc_items, o);
+        if (lane >= o) inc += y, inc_items += z;
     }
-    if (lane == 31) s_scan[warp] = inc;
+    if (lane == 31) s_scan[0][warp] = inc, s_scan[1][warp] = inc_items;
     tc_fence_before();
     heavy = __syncthreads_or(heavy);
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    int64_t total = 0, before = inc - mine;
+    int64_t total = 0, items = 0, before = inc - mine, before_items = inc_items - mine_items;
 #pragma unroll
     for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += s_scan[w];
-        total += s_scan[w];
+        if (w < warp) before += s_scan[0][w], before_items += s_scan[1][w];
+        total += s_scan[0][w];
+        items += s_scan[1][w];
     }
+    const int ends = total >= (int64_t)PR_ITEM * gridDim.x ? PR_ITEM : 0;
+    total += ends * items;
+    before += ends * before_items;
+    mine += ends * mine_items;
     int64_t per = pg_quotient(total + gridDim.x - 1, gridDim.x);
     // every stretch between an item's first and its last holds one of its tiles
-    if (per < (heavy ? 3 : 2)) per = heavy ? 3 : 2;
+    if (per < (heavy ? PR_TWO : PR_ONE)) per = heavy ? PR_TWO : PR_ONE;
     const int64_t begin = (int64_t)blockIdx.x * per;
     const int64_t end = begin + per < total ? begin + per : total;
     if (begin < end && mine > 0 && before <= begin && begin < before + mine) {
@@ -351,7 +360,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
         int b = tid * run;
         for (;; ++b) {
             const RoundSeq w = round_seq(p, b);
-            const int64_t n = seq_weight(p, w);
+            const int64_t n = seq_weight(p, w) + (int64_t)ends * p.G * w.mp;
             if (begin < at + n) break;
             at += n;
         }
@@ -369,9 +378,9 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             // the first that starts in the stretch
             Piece x = {};
             int64_t start = begin;
-            int weight = 2;
+            int weight = PR_ONE;
             auto next_item = [&]() {
-                start += (int64_t)x.w.nt * weight;
+                start += (int64_t)x.w.nt * weight + ends;
                 x.kt = 0;
                 if (++x.g == p.G) {
                     x.g = 0;
@@ -391,16 +400,17 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             if (begin < end) {
                 x.b = s_pb;
                 x.w = round_seq(p, x.b);
-                const int64_t full = (int64_t)p.G * x.w.nt * 3;
+                const int64_t full = (int64_t)p.G * (x.w.nt * PR_TWO + ends);
                 x.mp = (int)pg_quotient(s_plan, full);
                 if (x.mp > x.w.mp - 1) x.mp = x.w.mp - 1;
                 weight = tile_weight(p, x.w, x.mp);
                 const int64_t in_rows = s_plan - x.mp * full;
-                x.g = (int)pg_quotient(in_rows, (int64_t)x.w.nt * weight);
-                const int64_t in_item = in_rows - (int64_t)x.g * x.w.nt * weight;
+                const int item = x.w.nt * weight + ends;
+                x.g = (int)pg_quotient(in_rows, item);
+                const int64_t in_item = in_rows - (int64_t)x.g * item;
                 start = begin - in_item;
                 x.kt = ((int)in_item + weight - 1) / weight;
-                if (x.kt == x.w.nt) next_item();
+                if (x.kt >= x.w.nt) next_item();
             }
             int sent = 0, k = 0;   // tiles of keys or values, pieces' queries copied or being copied
             for (int turn = 0;; ++turn) {
@@ -1097,78 +1107,132 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
 
 // ------------------------------------------------------------------ join
 // The pieces of a shared item, added in order: piece k is CTA c + k's, its
-// second slot for the item's first piece, else its first.  Block (c, y): pairs
-// 32 y .. of the item that begins in CTA c; lanes are pairs, warps share out the
-// dims' groups of four; results leave by way of shared memory in whole rows.
-constexpr int RJ_WARPS = 8;
-constexpr int RJ_BATCH = 8;   // pieces whose statistics and values are in flight together
+// second slot for the item's first piece, else its first.  A thread takes four
+// dims of a pair, a warp 128 bytes of a piece at a time and 32 of an output
+// row.  An item's pieces follow from how much longer it is than a stretch: of
+// many, sixteen are in flight for 8 pairs; of few, four for 32 pairs.  Few items
+// begin in their CTA and end elsewhere, so every block lists them for itself
+// and takes units of pairs in turn.
+constexpr int RJ_THREADS = 256;
+constexpr int RJ_FEW = 4;
+static_assert(PA_MAX_ROUND_CTAS <= RJ_THREADS, "a thread lists an item");
 
-__global__ void __launch_bounds__(RJ_WARPS * 32)
-    rounds_join_kernel(const int4* __restrict__ join, const float4* __restrict__ part, const float2* __restrict__ stat,
-                       uint16_t* out, float* lse, const float* v_scale, float bias, int H, int D, int hq) {
-    __shared__ uint2 s_row[32][128 / 4 + 1];
-    pdl_wait();
-    pdl_trigger();
-    const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int4 j = __ldcg(&join[c]);   // pieces, first row, pairs, KV head
-    const int first = blockIdx.y * 32;
-    if (first >= j.z) return;
-    const int pr = first + lane;
-    const bool in = pr < j.z;
-    const int quads = D / 4;
-    const float2* st = stat + (in ? pr : first);
-    const float4* src = part + (in ? pr : first);
-    constexpr int MQ = 128 / 4 / RJ_WARPS;   // groups of four dims a warp takes at most
-    float4 v[MQ];
-    float M = -INFINITY, L = 0.f;
+struct JoinParams {
+    const int4* join;
+    const float4* part;
+    const float2* stat;
+    uint16_t* out;
+    float* lse;
+    const float* v_scale;
+    float bias;
+    int ctas, H, D, hq;
+};
+
+__device__ __forceinline__ int join_pairs(int pieces) { return pieces <= RJ_FEW ? 32 : 8; }   // of a unit
+
+// W pairs a thread, 8 apart; BATCH pieces in flight
+template <int W, int BATCH>
+__device__ __forceinline__ void join_unit(const JoinParams& p, int4 j, int c, int pair0, int quad) {
+    const int quads = p.D / 4;
+    float4 v[W];
+    float M[W], L[W];
 #pragma unroll
-    for (int u = 0; u < MQ; ++u) v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k0 = 0; k0 < j.x; k0 += RJ_BATCH) {
-        float2 s2[RJ_BATCH];
-        float4 y[RJ_BATCH][MQ];
+    for (int q = 0; q < W; ++q) {
+        v[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+        M[q] = -INFINITY;
+        L[q] = 0.f;
+    }
+    for (int k0 = 0; k0 < j.x; k0 += BATCH) {
+        float2 s2[BATCH][W];
+        float4 y[BATCH][W];
 #pragma unroll
-        for (int k = 0; k < RJ_BATCH; ++k) {
-            const bool is = k0 + k < j.x;
+        for (int k = 0; k < BATCH; ++k) {
             const int64_t slot = (int64_t)(c + k0 + k) * 2 + (k0 + k == 0);
-            s2[k] = is ? __ldcg(st + slot * 2 * PR_ROWS) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int u = 0; u < MQ; ++u)
-                y[k][u] = is && warp + u * RJ_WARPS < quads
-                              ? __ldcg(src + (slot * quads + warp + u * RJ_WARPS) * 2 * PR_ROWS)
-                              : make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int q = 0; q < W; ++q) {
+                const int pr = pair0 + 8 * q;
+                const bool is = k0 + k < j.x && pr < j.z;
+                s2[k][q] = is ? __ldcg(p.stat + slot * 2 * PR_ROWS + pr) : make_float2(-INFINITY, 0.f);
+                y[k][q] = is ? __ldcg(p.part + (slot * quads + quad) * 2 * PR_ROWS + pr) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
         }
-        float top = M;
 #pragma unroll
-        for (int k = 0; k < RJ_BATCH; ++k) top = fmaxf(top, s2[k].x);
-        const float a = M == -INFINITY ? 0.f : ex2_approx(M - top);
-        M = top;
-        L *= a;
+        for (int q = 0; q < W; ++q) {
+            float top = M[q];
 #pragma unroll
-        for (int u = 0; u < MQ; ++u) v[u] = make_float4(v[u].x * a, v[u].y * a, v[u].z * a, v[u].w * a);
+            for (int k = 0; k < BATCH; ++k) top = fmaxf(top, s2[k][q].x);
+            const float a = M[q] == -INFINITY ? 0.f : ex2_approx(M[q] - top);
+            M[q] = top;
+            L[q] *= a;
+            v[q] = make_float4(v[q].x * a, v[q].y * a, v[q].z * a, v[q].w * a);
 #pragma unroll
-        for (int k = 0; k < RJ_BATCH; ++k) {
-            const float w = s2[k].x == -INFINITY ? 0.f : ex2_approx(s2[k].x - top);
-            L = fmaf(s2[k].y, w, L);
-#pragma unroll
-            for (int u = 0; u < MQ; ++u) {
-                v[u].x = fmaf(y[k][u].x, w, v[u].x);
-                v[u].y = fmaf(y[k][u].y, w, v[u].y);
-                v[u].z = fmaf(y[k][u].z, w, v[u].z);
-                v[u].w = fmaf(y[k][u].w, w, v[u].w);
+            for (int k = 0; k < BATCH; ++k) {
+                const float w = s2[k][q].x == -INFINITY ? 0.f : ex2_approx(s2[k][q].x - top);
+                L[q] = fmaf(s2[k][q].y, w, L[q]);
+                v[q].x = fmaf(y[k][q].x, w, v[q].x);
+                v[q].y = fmaf(y[k][q].y, w, v[q].y);
+                v[q].z = fmaf(y[k][q].z, w, v[q].z);
+                v[q].w = fmaf(y[k][q].w, w, v[q].w);
             }
         }
     }
-    const float inv = (v_scale ? __ldg(v_scale + j.w) : 1.f) / L;
+    const float vs = p.v_scale ? __ldg(p.v_scale + j.w) : 1.f;
 #pragma unroll
-    for (int u = 0; u < MQ; ++u)
-        if (warp + u * RJ_WARPS < quads)
-            s_row[lane][warp + u * RJ_WARPS] =
-                make_uint2(cvt_bf16x2(v[u].x * inv, v[u].y * inv), cvt_bf16x2(v[u].z * inv, v[u].w * inv));
-    auto pair_row = [&](int q) { return (int64_t)(j.y + q / hq) * H + j.w * hq + q % hq; };
-    if (warp == 0 && in && lse) lse[pair_row(pr)] = (M + __log2f(L) - bias) * LN2;
+    for (int q = 0; q < W; ++q) {
+        const int pr = pair0 + 8 * q;
+        if (pr >= j.z) break;
+        const float inv = vs / L[q];
+        const int row = pr / p.hq;
+        const int64_t at = (int64_t)(j.y + row) * p.H + j.w * p.hq + (pr - row * p.hq);
+        *reinterpret_cast<uint2*>(p.out + at * p.D + quad * 4) =
+            make_uint2(cvt_bf16x2(v[q].x * inv, v[q].y * inv), cvt_bf16x2(v[q].z * inv, v[q].w * inv));
+        if (p.lse && quad == 0) p.lse[at] = (M[q] + __log2f(L[q]) - p.bias) * LN2;
+    }
+}
+
+__global__ void __launch_bounds__(RJ_THREADS, 2) rounds_join_kernel(const JoinParams p) {
+    __shared__ int4 s_item[PA_MAX_ROUND_CTAS];
+    __shared__ int s_cta[PA_MAX_ROUND_CTAS], s_first[PA_MAX_ROUND_CTAS];   // its CTA, units before it
+    __shared__ int s_sum[2][RJ_THREADS / 32];
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int4 it = make_int4(0, 0, 0, 0);   // pieces, first row, pairs, KV head
+    if (tid < p.ctas) it = __ldcg(&p.join[tid]);
+    const int mine = it.x > 0 ? (it.z + join_pairs(it.x) - 1) / join_pairs(it.x) : 0;
+    int upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += y;
+    }
+    const unsigned some = __ballot_sync(0xffffffffu, mine > 0);
+    if (lane == 31) s_sum[0][warp] = upto, s_sum[1][warp] = __popc(some);
     __syncthreads();
-    for (int r = warp; r < 32 && first + r < j.z; r += RJ_WARPS)
-        if (lane < quads) reinterpret_cast<uint2*>(out + pair_row(first + r) * D)[lane] = s_row[r][lane];
+    int units = 0, items = 0, units0 = 0, items0 = 0;
+#pragma unroll
+    for (int w = 0; w < RJ_THREADS / 32; ++w) {
+        if (w == warp) units0 = units, items0 = items;
+        units += s_sum[0][w];
+        items += s_sum[1][w];
+    }
+    if (mine > 0) {
+        const int at = items0 + __popc(some & ((1u << lane) - 1u));
+        s_item[at] = it;
+        s_cta[at] = tid;
+        s_first[at] = units0 + upto - mine;
+    }
+    __syncthreads();
+    const int quad = warp * 4 + (lane >> 3);
+    if (quad >= p.D / 4) return;
+    int i = 0;
+    for (int u = blockIdx.x; u < units; u += gridDim.x) {
+        while (i + 1 < items && s_first[i + 1] <= u) ++i;
+        const int4 j = s_item[i];
+        const int pair0 = (u - s_first[i]) * join_pairs(j.x) + (lane & 7);
+        if (j.x <= RJ_FEW) join_unit<4, RJ_FEW>(p, j, s_cta[i], pair0, quad);
+        else join_unit<1, 16>(p, j, s_cta[i], pair0, quad);
+    }
 }
 
 // ------------------------------------------------------------------ host side
@@ -1300,10 +1364,22 @@ wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args*
     if (tiles < grid) grid = (int)tiles;
     const RoundsVariant v = rounds_variant((e4m3 ? 1 : 0) | (c->D > 64 ? 2 : 0));
     PR_TRY(launch(v.fn, dim3(grid), dim3(v.threads), (size_t)v.smem, s, tmQ, tmK, tmV, p));
+    JoinParams jp = {};
+    jp.join = p.join;
+    jp.part = p.part;
+    jp.stat = p.stat;
+    jp.out = a->out;
+    jp.lse = a->lse;
+    jp.v_scale = p.v_scale;
+    jp.bias = e4m3 ? RoundsShape<1, true>::BIAS : RoundsShape<1, false>::BIAS;
+    jp.ctas = grid;
+    jp.H = a->H;
+    jp.D = c->D;
+    jp.hq = p.hq;
+    // no more blocks than units that the bounds allow
     const int most = a->max_rows < 2 * p.rpt ? a->max_rows : 2 * p.rpt;   // query rows of an item
-    return launch(rounds_join_kernel, dim3(grid, cdiv(most * p.hq, 32)), dim3(RJ_WARPS * 32), 0, s, (const int4*)p.join,
-                  (const float4*)p.part, (const float2*)p.stat, a->out, a->lse, p.v_scale,
-                  e4m3 ? RoundsShape<1, true>::BIAS : RoundsShape<1, false>::BIAS, a->H, c->D, p.hq);
+    const int units = grid * cdiv(most * p.hq, 8), blocks = 2 * num_sms();
+    return launch(rounds_join_kernel, dim3(units < blocks ? units : blocks), dim3(RJ_THREADS), 0, s, jp);
 }
 
 }  // namespace wf
