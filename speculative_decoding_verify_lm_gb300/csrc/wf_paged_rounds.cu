@@ -1110,11 +1110,11 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
 // second slot for the item's first piece, else its first.  A thread takes four
 // dims of a pair, a warp 128 bytes of a piece at a time and 32 of an output
 // row.  An item's pieces follow from how much longer it is than a stretch: of
-// many, sixteen are in flight for 8 pairs; of few, four for 32 pairs.  Few items
+// many, ten are in flight for 8 pairs; of few, three for 32 pairs.  Few items
 // begin in their CTA and end elsewhere, so every block lists them for itself
 // and takes units of pairs in turn.
 constexpr int RJ_THREADS = 256;
-constexpr int RJ_FEW = 4;
+constexpr int RJ_FEW = 3;
 static_assert(PA_MAX_ROUND_CTAS <= RJ_THREADS, "a thread lists an item");
 
 struct JoinParams {
@@ -1231,7 +1231,7 @@ __global__ void __launch_bounds__(RJ_THREADS, 2) rounds_join_kernel(const JoinPa
         const int4 j = s_item[i];
         const int pair0 = (u - s_first[i]) * join_pairs(j.x) + (lane & 7);
         if (j.x <= RJ_FEW) join_unit<4, RJ_FEW>(p, j, s_cta[i], pair0, quad);
-        else join_unit<1, 16>(p, j, s_cta[i], pair0, quad);
+        else join_unit<1, 10>(p, j, s_cta[i], pair0, quad);
     }
 }
 
