@@ -50,8 +50,6 @@ namespace wf {
 
 constexpr int PR_KT = 128;         // positions of a tile
 constexpr int PR_ROWS = 128;       // pairs of a product
-constexpr int PR_XC = 32;          // dims that pass through shared memory together
-constexpr int PR_XBYTES = PR_ROWS * PR_XC * 4;
 
 struct RoundsParams {
     const int32_t* pos_off;
@@ -222,23 +220,36 @@ __device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* m
 }
 
 // Shared memory: queries [2][blocks][128 rows][128 B], a ring of tiles of keys or
-// values [blocks][128 positions][128 B], exchanged rows [128][32] fp32, and for an
-// 8-bit cache two raw tiles [128][D <= 64 blocks]; blocks = 64-dim blocks of a head.
+// values [blocks][128 positions][128 B], rows [128][32] fp32 that pass from one
+// stream to the other, two numbers of each thread, and for an 8-bit cache raw
+// tiles [128][D <= 64 blocks]; blocks = 64-dim blocks of a head.
 template <int BLK, bool E4M3>
 struct RoundsShape {
-    static constexpr int RING = E4M3 ? 3 : 4;        // tiles of keys or values ready or in flight
-    static constexpr int RAW = E4M3 ? 2 : 0;
-    // two streams of four softmax warps, the copying warp, an issuing warp a stream,
-    // and for an 8-bit cache the widening warps
+    // tiles of keys or values ready or in flight
+    static constexpr int RING = E4M3 ? (BLK == 2 ? 3 : 6) : (BLK == 2 ? 4 : 10);
+    static constexpr int RAW = E4M3 ? (BLK == 2 ? 2 : 4) : 0;
+    static constexpr int PLACES = E4M3 ? RAW : RING;   // that the copying warps fill
+    // a place belongs to the keys or to the values: else one copying warp, ahead of
+    // the other by a turn of the ring, would take an older release for its own
+    static_assert(E4M3 || RING % 2 == 0, "an even ring");
+    // two streams of four softmax warps, a copying warp, an issuing warp a stream, and
+    // a second copying warp for the values or for an 8-bit cache the widening warps
     static constexpr int WIDEN = E4M3 ? 5 : 0;
-    static constexpr int THREADS = (11 + WIDEN) * 32;
-    // registers: 512 threads start with 128 each (65,536); the softmax warps take 176,
-    // the other eight give down to 72 (63,488 in all)
+    static constexpr int COPIES = E4M3 ? 1 : 2;
+    // threads that share a row's scores of a tile
+    static constexpr int HALVES = E4M3 ? 1 : 2;
+    static constexpr int SOFT = 8 * HALVES;          // softmax warps
+    static constexpr int STREAM = 128 * HALVES;      // threads of a stream
+    static constexpr int THREADS = (SOFT + 2 + COPIES + WIDEN) * 32;
+    // 8-bit caches: 512 threads start with 128 registers each (65,536); the softmax
+    // warps take 168, the other eight give down to 80 (63,488 in all)
     static constexpr bool SPLIT_REGISTERS = E4M3;
     static constexpr int QTILE = BLK * PR_ROWS * 128;
     static constexpr int TILE = BLK * PR_KT * 128;
     static constexpr int RAW_TILE = BLK * PR_KT * 64;
-    static constexpr int SMEM = 1024 + 2 * QTILE + RING * TILE + PR_XBYTES + RAW * RAW_TILE;
+    static constexpr int XBYTES = PR_ROWS * 32 * 4;
+    static constexpr int XC = 32 / HALVES;           // dims that a thread takes from or to shared memory together
+    static constexpr int SMEM = 1024 + 2 * QTILE + RING * TILE + RAW * RAW_TILE + XBYTES + PR_ROWS * 8 + 2 * STREAM * 4;
     // the running maximum may lag by 2^LAG; fp16 probabilities use the range from 2^-24 up to 2^(BIAS + LAG)
     static constexpr float LAG = E4M3 ? 4.f : 8.f;
     static constexpr float BIAS = E4M3 ? 8.f : 0.f;
@@ -257,14 +268,18 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
     paged_rounds_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                         const __grid_constant__ CUtensorMap tmV, const RoundsParams p) {
     using S = RoundsShape<BLK, E4M3>;
-    constexpr int RING = S::RING, QTILE = S::QTILE, TILE = S::TILE, THREADS = S::THREADS, WIDEN = S::WIDEN;
+    constexpr int RING = S::RING, QTILE = S::QTILE, TILE = S::TILE, THREADS = S::THREADS, WIDEN = S::WIDEN, COPIES = S::COPIES;
+    constexpr int HALVES = S::HALVES, SOFT = S::SOFT, STREAM = S::STREAM, XC = S::XC;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint8_t* sQ = smem;
     uint8_t* sR = smem + 2 * QTILE;
-    uint8_t* sX = sR + RING * TILE;
-    uint8_t* sW = sX + PR_XBYTES;              // raw tiles
-    __shared__ uint64_t kv_full[RING], kv_empty[RING], raw_full[2], raw_empty[2], q_full, q_empty, told[8];
+    uint8_t* sW = sR + RING * TILE;            // raw tiles
+    uint8_t* sX = sW + S::RAW * S::RAW_TILE;
+    float2* s_xst = reinterpret_cast<float2*>(sX + S::XBYTES);                    // the second stream's rows'
+    float* s_own = reinterpret_cast<float*>(sX + S::XBYTES + PR_ROWS * 8);        // a number of each softmax thread
+    constexpr int PLACES = S::PLACES, RAW = E4M3 ? S::RAW : 1;
+    __shared__ uint64_t kv_full[RING], kv_empty[RING], raw_full[RAW], raw_empty[RAW], q_full, q_empty, told[8];
     __shared__ uint64_t piece_ready[8], piece_free[8];
     __shared__ Piece s_piece[8];   // the copying warp's next pieces, for the others
     __shared__ uint64_t s_full[2], p_full[2], o_full[2];   // by stream
@@ -272,7 +287,6 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
     __shared__ int abort_word, s_bad[8], s_odd[2][2], s_pb, s_turn;
     __shared__ uint8_t s_par[2][WF_MAX_SEQ_NODES + 1];   // row of each row's parent, by stream (a row's own copy)
     __shared__ uint64_t q_ready[2];                        // queries brought to fp16, by stream
-    __shared__ float2 s_xst[PR_ROWS];
     __shared__ float s_factor[PR_ROWS];                    // and their scores' factors, for the other stream
     __shared__ int64_t s_plan, s_scan[2][THREADS / 32];
     volatile int* abort_flag = &abort_word;
@@ -283,22 +297,23 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             mbar_init(&kv_full[i], E4M3 ? WIDEN : 1);
             mbar_init(&kv_empty[i], 2);   // both streams, or one twice
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < RAW; ++i) {
             mbar_init(&raw_full[i], 1);
             mbar_init(&raw_empty[i], E4M3 ? WIDEN : 1);
-            mbar_init(&q_ready[i], PR_ROWS);
         }
+        mbar_init(&q_ready[0], PR_ROWS);
+        mbar_init(&q_ready[1], PR_ROWS);
         mbar_init(&q_full, 1);
         mbar_init(&q_empty, 2);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_full[i], 1);
-            mbar_init(&p_full[i], PR_ROWS);
+            mbar_init(&p_full[i], STREAM);
             mbar_init(&o_full[i], 1);
         }
         for (int i = 0; i < 8; ++i) {
             mbar_init(&told[i], 1);
             mbar_init(&piece_ready[i], 1);
-            mbar_init(&piece_free[i], 4 + WIDEN);   // two streams, two issuing warps, the widening ones
+            mbar_init(&piece_free[i], 3 + COPIES + WIDEN);   // two streams, two issuing warps, the second copying, the widening ones
         }
         abort_word = s_turn = 0;
         s_odd[0][0] = s_odd[0][1] = s_odd[1][0] = s_odd[1][1] = 0;
@@ -307,7 +322,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
         tma_prefetch_desc(&tmK);
         tma_prefetch_desc(&tmV);
     }
-    if (warp == 8) {
+    if (warp == SOFT) {
         tmem_alloc(&tmem_slot, 512);
         tmem_relinquish();
     }
@@ -368,12 +383,44 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
         s_pb = b;
     }
     __syncthreads();
-    if (warp >= 8) {
-        if (S::SPLIT_REGISTERS) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (warp == 8) {
+    if (warp >= SOFT) {
+        if (S::SPLIT_REGISTERS) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+        const uint64_t pol = policy_evict_first();
+        const int per_tile = PR_KT / p.box_rows;   // boxes of a tile: at most 16
+        // lane i of a copying warp: the page of positions i box_rows .. of a tile (-2: none)
+        auto page_of = [&](const Piece& x, int kt) {
+            const int t = kt * PR_KT + lane * p.box_rows;
+            return lane < per_tile && t < x.w.T ? p.table[(int64_t)x.b * p.max_pages + (t >> p.page_shift)] : -2;
+        };
+        auto pool_row = [&](int kt, int page) {
+            return (page << p.page_shift) + ((kt * PR_KT + lane * p.box_rows) & ((1 << p.page_shift) - 1));
+        };
+        // a tile's keys or values to place `at`
+        auto load = [&](int kv, int at, const Piece& x, bool ok, int y, uint32_t boxes) {
+            const int place = at % PLACES;
+            uint64_t* full = E4M3 ? &raw_full[place] : &kv_full[place];
+            const int row_bytes = E4M3 ? p.D : BLK * 128;
+            if (lane == 0) mbar_arrive_expect_tx(full, boxes * p.box_rows * row_bytes);
+            __syncwarp();
+            if (ok && E4M3) {
+                tma_load_2d(sW + place * S::RAW_TILE + lane * p.box_rows * p.D, kv ? &tmV : &tmK, full, x.g * p.D, y,
+                            pol);
+            } else if (ok) {
+                uint8_t* dst = sR + place * TILE + lane * p.box_rows * 128;
+#pragma unroll
+                for (int blk = 0; blk < BLK; ++blk)
+                    tma_load_2d(dst + blk * PR_KT * 128, kv ? &tmV : &tmK, full, x.g * p.D + blk * 64, y, pol);
+            }
+        };
+        auto place_free = [&](int at) {
+            return at < PLACES || mbar_wait(E4M3 ? &raw_empty[at % PLACES] : &kv_empty[at % PLACES],
+                                            ((at / PLACES) & 1) ^ 1, p.timeout_ns, abort_flag);
+        };
+        auto landed = [&](int at) {
+            mbar_wait(E4M3 ? &raw_full[at % PLACES] : &kv_full[at % PLACES], (at / PLACES) & 1, p.timeout_ns, nullptr);
+        };
+        if (warp == SOFT) {
             // ---------------------------------------- copies: a tile's keys, then its values, to the ring's next places
-            const uint64_t pol = policy_evict_first();
-            const int per_tile = PR_KT / p.box_rows;   // boxes of a tile: at most 16
             // the stretch's first item: `start`, the weight before it; its tile kt is
             // the first that starts in the stretch
             Piece x = {};
@@ -412,7 +459,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                 x.kt = ((int)in_item + weight - 1) / weight;
                 if (x.kt >= x.w.nt) next_item();
             }
-            int sent = 0, k = 0;   // tiles of keys or values, pieces' queries copied or being copied
+            int sent = 0, last = -1, k = 0;   // places of the tiles before, the last place filled; pieces' queries
             for (int turn = 0;; ++turn) {
                 if (turn >= 8 && !mbar_wait(&piece_free[turn & 7], ((turn >> 3) & 1) ^ 1, p.timeout_ns, abort_flag)) {
                     *abort_flag = 1;
@@ -436,21 +483,13 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                 if (x.tiles == 0) break;
                 bool bad = false;
                 if (!x.w.bad) {
-                    int page = 0;
-                    auto look_up = [&](int kt) {
-                        const int t = kt * PR_KT + lane * p.box_rows;
-                        page = lane < per_tile && t < x.w.T
-                                   ? p.table[(int64_t)x.b * p.max_pages + (t >> p.page_shift)]
-                                   : -2;
-                    };
-                    look_up(x.kt);
+                    int page = page_of(x, x.kt);
                     for (int i = 0; i < x.tiles; ++i) {
-                        const int t = (x.kt + i) * PR_KT + lane * p.box_rows;
                         const bool ok = page >= 0 && page < p.num_pages;
                         bad |= page != -2 && !ok;
-                        const int y = ok ? (page << p.page_shift) + (t & ((1 << p.page_shift) - 1)) : 0;
+                        const int y = ok ? pool_row(x.kt + i, page) : 0;
                         const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xffffffffu, ok));
-                        if (i + 1 < x.tiles) look_up(x.kt + i + 1);
+                        if (i + 1 < x.tiles) page = page_of(x, x.kt + i + 1);
                         bool alive = true;
 #pragma unroll
                         for (int kv = 0; kv < 2; ++kv) {
@@ -468,30 +507,15 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                                 ++k;
                                 __syncwarp();
                             }
-                            const int at = sent;
                             // the raw tiles' turn for an 8-bit cache, else the ring's
-                            constexpr int PLACES = E4M3 ? 2 : RING;
-                            const int place = at % PLACES;
-                            uint64_t* full = E4M3 ? &raw_full[place] : &kv_full[place];
-                            uint64_t* empty = E4M3 ? &raw_empty[place] : &kv_empty[place];
-                            alive = alive && (at < PLACES || mbar_wait(empty, ((at / PLACES) & 1) ^ 1, p.timeout_ns,
-                                                                       abort_flag));
+                            const int at = sent + kv;
+                            if (kv == 1 && COPIES == 2) break;   // the other copying warp's
+                            alive = alive && place_free(at);
                             if (!alive) break;
-                            const int row_bytes = E4M3 ? p.D : BLK * 128;
-                            if (lane == 0) mbar_arrive_expect_tx(full, boxes * p.box_rows * row_bytes);
-                            ++sent;
-                            __syncwarp();
-                            if (ok && E4M3) {
-                                tma_load_2d(sW + place * S::RAW_TILE + lane * p.box_rows * p.D, kv ? &tmV : &tmK, full,
-                                            x.g * p.D, y, pol);
-                            } else if (ok) {
-                                uint8_t* dst = sR + place * TILE + lane * p.box_rows * 128;
-#pragma unroll
-                                for (int blk = 0; blk < BLK; ++blk)
-                                    tma_load_2d(dst + blk * PR_KT * 128, kv ? &tmV : &tmK, full, x.g * p.D + blk * 64, y,
-                                                pol);
-                            }
+                            load(kv, at, x, ok, y, boxes);
+                            last = at;
                         }
+                        sent += 2;
                         if (!alive) {
                             *abort_flag = 1;
                             if (lane == 0) record_error(p.ctrl, WF_ERR_TIMEOUT, 0x800u);
@@ -510,11 +534,41 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                 next_item();
             }
             // let every copy issued land before the shared memory goes
-            constexpr int PLACES = E4M3 ? 2 : RING;
-            for (int at = max(0, sent - PLACES); at < sent; ++at)
-                mbar_wait(E4M3 ? &raw_full[at % PLACES] : &kv_full[at % PLACES], (at / PLACES) & 1, p.timeout_ns, nullptr);
+            for (int at = max(0, last - PLACES + 1); at <= last; ++at)
+                if (COPIES == 1 || at % 2 == 0) landed(at);
             if (k > 0) mbar_wait(&q_full, (k & 1) ^ 1, p.timeout_ns, nullptr);
-        } else if (warp >= 11) {
+        } else if (COPIES == 2 && warp == SOFT + 3) {
+            // ---------------------------------------- copies of the values
+            int n = 0, last = -1;   // tiles before this piece, the last place filled
+            bool ok = true;
+            for (int turn = 0; ok; ++turn) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&piece_ready[turn & 7], (turn >> 3) & 1, p.timeout_ns, abort_flag));
+                if (!ok) break;
+                const Piece& x = s_piece[turn & 7];
+                if (x.tiles == 0) break;
+                const int tiles = x.w.bad ? 0 : x.tiles;
+                int page = tiles > 0 ? page_of(x, x.kt) : -2;
+                for (int i = 0; i < tiles && ok; ++i) {
+                    const bool in = page >= 0 && page < p.num_pages;
+                    const int y = in ? pool_row(x.kt + i, page) : 0;
+                    const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xffffffffu, in));
+                    if (i + 1 < tiles) page = page_of(x, x.kt + i + 1);
+                    const int at = 2 * (n + i) + 1;
+                    ok = __all_sync(0xffffffffu, place_free(at));
+                    if (!ok) break;
+                    load(1, at, x, in, y, boxes);
+                    last = at;
+                }
+                n += tiles;
+                __syncwarp();
+                if (ok && lane == 0) mbar_arrive(&piece_free[turn & 7]);
+            }
+            if (!ok) {
+                *abort_flag = 1;
+                if (lane == 0) record_error(p.ctrl, WF_ERR_TIMEOUT, 0x802u);
+            }
+            for (int at = max(1, last - PLACES + 1) | 1; at <= last; at += 2) landed(at);
+        } else if (warp >= SOFT + 3) {
             // ---------------------------------------- 8-bit rows widened to fp16 in the ring
             if (E4M3) {
                 int n = 0;
@@ -531,15 +585,15 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                     if (tiles == 0) break;
                     const int loads = s_piece[turn & 7].w.bad ? 0 : 2 * tiles;
                     for (int i = 0; i < loads && ok; ++i) {
-                        const int at = 2 * n + i, raw = at & 1, slot = at % RING;
-                        wait(&raw_full[raw], (at >> 1) & 1);
+                        const int at = 2 * n + i, raw = at % RAW, slot = at % RING;
+                        wait(&raw_full[raw], (at / RAW) & 1);
                         if (at >= RING) wait(&kv_empty[slot], ((at / RING) & 1) ^ 1);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         const uint8_t* src = sW + raw * S::RAW_TILE;
                         uint8_t* dst = sR + slot * TILE;
                         // 64 pieces a step, warp after warp
-                        for (int j = (warp - 11) * 64 + lane; j < PR_KT * per_row; j += WIDEN * 64) {
+                        for (int j = (warp - SOFT - 3) * 64 + lane; j < PR_KT * per_row; j += WIDEN * 64) {
                             uint4 v[2];
 #pragma unroll
                             for (int u = 0; u < 2; ++u)   // 128 rows of pieces: a multiple of 64
@@ -578,7 +632,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             // The whole warp runs this with the same values and one elected lane
             // issues: the operands' descriptors stay in uniform registers (issued
             // from a single thread's own, a product took 107 cycles instead of its 64).
-            const int w = __shfl_sync(0xffffffffu, warp - 9, 0);
+            const int w = __shfl_sync(0xffffffffu, warp - SOFT - 1, 0);
             const uint32_t tS = __shfl_sync(0xffffffffu, tmem, 0) + w * 128, tO = tS + 256;
             const uint32_t qdesc = __shfl_sync(0xffffffffu, desc_lo_rows(smem_u32(sQ)), 0);
             const uint32_t kdesc = __shfl_sync(0xffffffffu, desc_lo_rows(smem_u32(sR)), 0);
@@ -691,9 +745,10 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             }
         }
     } else {
-        // -------------------------------------------- softmax: stream w, thread = row of the product
-        if (S::SPLIT_REGISTERS) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
-        const int w = warp >> 2, row = tid & 127;
+        // -------------------------------------------- softmax: stream w, HALVES threads a row of the product
+        if (S::SPLIT_REGISTERS) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        const int w = warp / (4 * HALVES), half = (warp >> 2) & (HALVES - 1), row = tid & 127;
+        const int pair_id = 4 + w * 4 + (warp & 3);   // the named barrier of the warps that share rows
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tmem + lanes + w * 128, tO = tmem + lanes + 256 + w * 128;
         uint32_t sn = 0, on = 0;   // scores, outputs taken
@@ -712,7 +767,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             wait(&piece_ready[turn & 7], (turn >> 3) & 1);
             // all of both streams go on, or none (also: s_odd and the exchanged rows of
             // the piece before are read to their end)
-            if (!named_all(3, 256, ok)) break;
+            if (!named_all(3, 2 * STREAM, ok)) break;
             const Piece& x = s_piece[turn & 7];
             if (x.tiles == 0) break;
             const int first = (2 * x.mp + (x.solo ? 0 : w)) * p.rpt;   // first query row of this stream's product
@@ -738,7 +793,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                     bool off = n0 < 0 || nn != x.w.rows - 1;
                     if (off) tree = false;
                     else
-                        for (int a = row; a < nn; a += 128) {
+                        for (int a = half * 128 + row; a < nn; a += STREAM) {
                             const int pi = p.parent[n0 + a];
                             const bool wrong = pi < -1 || pi >= a;
                             s_par[w][1 + a] = (uint8_t)(wrong ? 0 : 1 + pi);
@@ -746,7 +801,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                         }
                     if (off) atomicOr(odd_word, 2);
                 }
-                named_sync(1 + w, 128);
+                named_sync(1 + w, STREAM);
             };
             float f = p.qk;   // the row's scores times this are base-2 exponents
             if (E4M3 && !x.w.bad) {
@@ -794,23 +849,24 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                     const bool masked = t0 + PR_KT > x.w.len;
                     wait(&s_full[w], sn++ & 1);
                     tc_fence_after();
-                    const bool go = warp_live && __all_sync(0xffffffffu, ok);
-                    uint32_t see[4];   // the positions that the row sees
+                    constexpr int WORDS = 4 / HALVES;   // of 32 positions that this thread takes
+                    const int u0 = t0 + half * 64;
+                    uint32_t see[WORDS];   // those that the row sees
                     if (masked) {
                         learn_tree();
                         // all below `upto`, then the row's ancestors
-                        const int upto = (tree ? x.w.len : x.w.len + r + 1) - t0;
+                        const int upto = (tree ? x.w.len : x.w.len + r + 1) - u0;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) {
+                        for (int c = 0; c < WORDS; ++c) {
                             const int u = upto - 32 * c;
                             see[c] = u <= 0 ? 0u : (u >= 32 ? 0xFFFFFFFFu : (1u << u) - 1u);
                         }
                         if (tree && live) {
                             int a = r;
                             while (true) {
-                                const int t = x.w.len + a - t0;
+                                const int t = x.w.len + a - u0;
 #pragma unroll
-                                for (int c = 0; c < 4; ++c)
+                                for (int c = 0; c < WORDS; ++c)
                                     if (t >= 32 * c && t < 32 * c + 32) see[c] |= 1u << (t & 31);
                                 if (a == 0) break;
                                 a = s_par[w][a];
@@ -818,15 +874,16 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                         }
                         __syncwarp();
                     }
-                    if (go) {
-                        uint32_t s[2][32];   // 64 scores at a time
+                    if (warp_live) {
+                        constexpr int STEP = 2 / HALVES;   // words of scores fetched together
+                        uint32_t s[STEP][32];
                         auto fetch = [&](int c0) {
-                            tmem_ld_32x32b_x32(tS + c0 * 32, s[0]);
-                            tmem_ld_32x32b_x32(tS + c0 * 32 + 32, s[1]);
+#pragma unroll
+                            for (int c = 0; c < STEP; ++c) tmem_ld_32x32b_x32(tS + half * 64 + (c0 + c) * 32, s[c]);
                             tmem_ld_wait();
                             if (masked) {
 #pragma unroll
-                                for (int c = 0; c < 2; ++c)
+                                for (int c = 0; c < STEP; ++c)
                                     if (!__all_sync(0xffffffffu, see[c0 + c] == 0xFFFFFFFFu))
 #pragma unroll
                                         for (int e = 0; e < 32; ++e)
@@ -837,28 +894,37 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                         auto largest = [&](float big) {
                             float top[4] = {big, big, big, big};
 #pragma unroll
-                            for (int c = 0; c < 2; ++c)
+                            for (int c = 0; c < STEP; ++c)
 #pragma unroll
                                 for (int e = 0; e < 32; e += 2) top[(e >> 1) & 3] = max3(top[(e >> 1) & 3], at(c, e), at(c, e + 1));
                             return fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
                         };
                         // The weights are taken against the running maximum as it is; only
                         // when a score has outgrown it by 2^LAG (or nothing has been seen
-                        // yet) is the tile's maximum taken first.
-                        uint32_t pk[4][16];
+                        // yet) is the tile's maximum taken first.  A row's threads hold the
+                        // same maximum and decide alike, whatever a wait has come to.
+                        uint32_t pk[WORDS][16];
                         float sum = 0.f;
                         bool again = !__all_sync(0xffffffffu, m > -INFINITY);
                         while (true) {
                             if (again) {
-                                fetch(0);
-                                const float low = largest(-INFINITY);
-                                fetch(2);
-                                const float mn = fmaxf(m, largest(low));
+                                float top = -INFINITY;
+#pragma unroll
+                                for (int c0 = 0; c0 < WORDS; c0 += STEP) {
+                                    fetch(c0);
+                                    top = largest(top);
+                                }
+                                if (HALVES == 2) {
+                                    s_own[(w * HALVES + half) * 128 + row] = top;
+                                    named_sync(pair_id, 64);
+                                    top = fmaxf(top, s_own[(w * HALVES + 1 - half) * 128 + row]);
+                                }
+                                const float mn = fmaxf(m, top);
                                 const float a = m == -INFINITY ? 0.f : ex2_approx((m - mn) * f);
                                 m = mn;
                                 l *= a;
                                 if (i > 0)   // every earlier product into O has completed before this tile's scores
-                                    for (int c = 0; c < p.D; c += 16) {
+                                    for (int c = half * 16; c < p.D; c += 16 * HALVES) {
                                         uint32_t y[16];
                                         tmem_ld_x16(tO + c, y);
                                         tmem_ld_wait();
@@ -876,18 +942,18 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                             uint64_t sum2[2] = {0, 0};
                             float big = -INFINITY;
 #pragma unroll
-                            for (int c0 = 0; c0 < 4; c0 += 2) {
+                            for (int c0 = 0; c0 < WORDS; c0 += STEP) {
                                 fetch(c0);
                                 if (far) {
 #pragma unroll
-                                    for (int c = 0; c < 2; ++c)
+                                    for (int c = 0; c < STEP; ++c)
 #pragma unroll
                                         for (int e = 0; e < 32; ++e)
                                             s[c][e] = __float_as_uint(at(c, e) - (m == -INFINITY ? 0.f : m));
                                 }
                                 if (!again) big = largest(big);
 #pragma unroll
-                                for (int c = 0; c < 2; ++c)
+                                for (int c = 0; c < STEP; ++c)
 #pragma unroll
                                     for (int e = 0; e < 16; ++e) {
                                         float z0, z1;
@@ -897,7 +963,9 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                                         pk[c0 + c][e] = E4M3 ? cvt_f16x2(p0, p1) : cvt_bf16x2(p0, p1);
                                     }
                             }
-                            if (again || !__any_sync(0xffffffffu, (far ? big : big - m) * f > S::LAG)) {
+                            // also: the row's other thread has read its scores, which these weights overwrite
+                            const bool stays = again || !((far ? big : big - m) * f > S::LAG);
+                            if (HALVES == 2 ? named_all(pair_id, 64, stays) : __all_sync(0xffffffffu, stays)) {
                                 float a0, a1;
                                 unpair(add2(sum2[0], sum2[1]), a0, a1);
                                 sum = a0 + a1;
@@ -907,10 +975,10 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                         }
                         l += sum;
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) tmem_st_x16(tS + c * 16, pk[c]);
+                        for (int c = 0; c < WORDS; ++c) tmem_st_x16(tS + (half * WORDS + c) * 16, pk[c]);
                     }
                     if (masked && t0 + row >= x.w.len) {
-                        // one position's values a thread: zero past the end, and where not
+                        // a position's values, by its threads: zero past the end, and where not
                         // finite (by both streams where both see the tile: the same bytes)
                         const int at = 2 * (n + j) + 1, slot = at % RING;
                         wait(&kv_full[slot], (at / RING) & 1);
@@ -919,10 +987,12 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
 #pragma unroll
                         for (int blk = 0; blk < BLK; ++blk) {
                             uint8_t* base = sR + slot * TILE + blk * PR_KT * 128 + row * 128;
+                            // 16-byte piece c of the row; a thread takes its share of the eight
                             auto piece = [&](int c) { return reinterpret_cast<uint4*>(base + ((c ^ (row & 7)) << 4)); };
+                            constexpr int SHARE = 8 / HALVES;
                             uint32_t probe[2] = {0, 0};
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
+                            for (int c = half * SHARE; c < (half + 1) * SHARE; ++c) {
                                 if (past) {
                                     *piece(c) = make_uint4(0, 0, 0, 0);
                                 } else {
@@ -939,7 +1009,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                             if (((probe[0] | probe[1]) & 0x7FFF7FFFu) == 0) continue;
                             odd = true;
 #pragma unroll 1
-                            for (int c = 0; c < 8; ++c) {
+                            for (int c = half * SHARE; c < (half + 1) * SHARE; ++c) {
                                 uint4 y = *piece(c);
                                 uint32_t* e = &y.x;
 #pragma unroll
@@ -972,9 +1042,11 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                 ++k;
             }
             const bool merge = x.solo && x.tiles > 1 && !x.w.bad;   // both streams hold parts of the same pairs
-            named_sync(3, 256);                                     // s_odd of both streams
+            if (HALVES == 2) s_own[(w * HALVES + half) * 128 + row] = l;
+            named_sync(3, 2 * STREAM);                              // s_odd of both streams, sums of both halves
+            if (HALVES == 2) l = s_own[w * HALVES * 128 + row] + s_own[(w * HALVES + 1) * 128 + row];
             const int learnt = s_odd[turn & 1][0] | s_odd[turn & 1][1];
-            if (row == 0) s_odd[(turn + 1) & 1][w] = 0;             // read last before the previous piece's end
+            if (row == 0 && half == 0) s_odd[(turn + 1) & 1][w] = 0;             // read last before the previous piece's end
             const bool odd = learnt & 1;
             bad |= (learnt & 2) != 0;
             const bool whole = x.tiles == x.w.nt;
@@ -984,8 +1056,8 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             m *= f;   // as exponents from here on
             float w0 = 1.f, w1 = 0.f, M = m, L = l;
             if (merge) {
-                if (w == 1) s_xst[row] = make_float2(m, l);
-                named_sync(3, 256);
+                if (w == 1 && half == 0) s_xst[row] = make_float2(m, l);
+                named_sync(3, 2 * STREAM);
                 if (w == 0) {
                     const float2 o1 = s_xst[row];
                     M = fmaxf(m, o1.x);
@@ -997,37 +1069,44 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             if (bad) M = L = NAN;
             const float inv = (E4M3 && p.v_scale ? __ldg(p.v_scale + x.g) : 1.f) / L;
             const int64_t out_pair = (int64_t)(x.w.r0 + r) * p.H + x.g * p.hq + (row - row / p.hq * p.hq);
-            float* xb = reinterpret_cast<float*>(sX);   // [128][32]: the second stream's rows, pieces of 16 bytes swizzled
-            for (int c0 = 0; c0 < p.D; c0 += PR_XC) {
+            // the second stream's rows, [128][XC] for each half, pieces of 16 bytes swizzled
+            float* xb = reinterpret_cast<float*>(sX) + (half * PR_ROWS + row) * XC;
+            constexpr int XP = XC / 4;   // 16-byte pieces
+            auto xpiece = [&](int e) { return xb + ((e ^ (row & (XP - 1))) << 2); };
+            auto fetch_out = [&](int c0, uint32_t (&y)[XC]) {
+                if constexpr (XC == 32) tmem_ld_32x32b_x32(tO + c0, y);
+                else tmem_ld_x16(tO + c0, y);
+                tmem_ld_wait();
+            };
+            // every thread makes the same number of rounds: they meet at barriers
+            for (int d0 = 0; d0 < p.D; d0 += XC * HALVES) {
+                const int c0 = d0 + half * XC;
                 if (merge) {
-                    if (c0 > 0) named_sync(3, 256);
+                    if (d0 > 0) named_sync(3, 2 * STREAM);
                     if (w == 1) {
-                        uint32_t y[32];
-                        tmem_ld_32x32b_x32(tO + c0, y);
-                        tmem_ld_wait();
+                        uint32_t y[XC];
+                        fetch_out(c0, y);
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            *reinterpret_cast<uint4*>(xb + row * PR_XC + ((e ^ (row & 7)) << 2)) =
-                                make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
+                        for (int e = 0; e < XP; ++e)
+                            *reinterpret_cast<uint4*>(xpiece(e)) = make_uint4(y[4 * e], y[4 * e + 1], y[4 * e + 2], y[4 * e + 3]);
                     }
-                    named_sync(3, 256);
+                    named_sync(3, 2 * STREAM);
                 }
-                float v[PR_XC];
+                float v[XC];
                 if (!x.w.bad && mine_tiles > 0) {   // warp-uniform
-                    uint32_t y[32];
-                    tmem_ld_32x32b_x32(tO + c0, y);
-                    tmem_ld_wait();
+                    uint32_t y[XC];
+                    fetch_out(c0, y);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = __uint_as_float(y[e]) * w0;
+                    for (int e = 0; e < XC; ++e) v[e] = __uint_as_float(y[e]) * w0;
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) v[e] = 0.f;
+                    for (int e = 0; e < XC; ++e) v[e] = 0.f;
                 }
                 if (writer) {
                     if (merge) {
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            const float4 y = *reinterpret_cast<const float4*>(xb + row * PR_XC + ((e ^ (row & 7)) << 2));
+                        for (int e = 0; e < XP; ++e) {
+                            const float4 y = *reinterpret_cast<const float4*>(xpiece(e));
                             v[4 * e] = fmaf(y.x, w1, v[4 * e]);
                             v[4 * e + 1] = fmaf(y.y, w1, v[4 * e + 1]);
                             v[4 * e + 2] = fmaf(y.z, w1, v[4 * e + 2]);
@@ -1038,7 +1117,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                     if (whole) {
                         uint4* dst = reinterpret_cast<uint4*>(p.out + out_pair * p.D + c0);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
+                        for (int e = 0; e < XC / 8; ++e)
                             if (c0 + (e >> 1) * 16 < p.D)
                                 dst[e] = make_uint4(cvt_bf16x2(v[8 * e] * inv, v[8 * e + 1] * inv),
                                                     cvt_bf16x2(v[8 * e + 2] * inv, v[8 * e + 3] * inv),
@@ -1047,7 +1126,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                     } else {
                         float4* dst = p.part + ((int64_t)slot * (p.D / 4) + c0 / 4) * 2 * PR_ROWS + prow;
 #pragma unroll
-                        for (int e = 0; e < 8; ++e)
+                        for (int e = 0; e < XP; ++e)
                             if (c0 + (e >> 2) * 16 < p.D)
                                 dst[e * 2 * PR_ROWS] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
                     }
@@ -1055,8 +1134,8 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                 __syncwarp();
             }
             if (bad && row == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)x.b);
-            if (writer && !whole) p.stat[slot * 2 * PR_ROWS + prow] = make_float2(M, L);
-            if (writer && whole && p.lse)
+            if (writer && half == 0 && !whole) p.stat[slot * 2 * PR_ROWS + prow] = make_float2(M, L);
+            if (writer && half == 0 && whole && p.lse)
                 p.lse[out_pair] = (M + __log2f(L) - S::BIAS) * LN2;
             if (tid == 0 && x.pieces > 0) {
                 p.join[blockIdx.x] = make_int4(x.pieces, x.w.r0 + 2 * x.mp * p.rpt, x.rows * p.hq, x.g);
@@ -1079,6 +1158,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                     const int64_t at = (((int64_t)page << p.page_shift) + (t & ((1 << p.page_shift) - 1))) * p.G + x.g;
 #pragma unroll 1
                     for (int d = 0; d < p.D; ++d) {
+                        if ((d / XC) % HALVES != half) continue;   // whoever wrote it above
                         const float y = E4M3 ? ((p.V[at * p.D + d] & 0x7F) == 0x7F ? NAN : 0.f)
                                              : pg_bf16_to_f32(reinterpret_cast<const uint16_t*>(p.V)[at * p.D + d]);
                         if (fabsf(y) < INFINITY) continue;
@@ -1094,15 +1174,15 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                 }
             }
             if (!x.w.bad) n += x.tiles;
-            named_sync(1 + w, 128);   // the stream has read the piece
-            if (row == 0) mbar_arrive(&piece_free[turn & 7]);
+            named_sync(1 + w, STREAM);   // the stream has read the piece
+            if (row == 0 && half == 0) mbar_arrive(&piece_free[turn & 7]);
         }
         if (tid == 0 && !shared_item) p.join[blockIdx.x] = make_int4(0, 0, 0, 0);
         tc_fence_before();
     }
     __syncthreads();
     tc_fence_after();
-    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (warp == SOFT) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------ join
