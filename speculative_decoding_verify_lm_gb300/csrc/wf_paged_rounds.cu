@@ -102,8 +102,8 @@ __device__ __forceinline__ RoundSeq round_seq(const RoundsParams& p, int b) {
 }
 
 // Weight of a tile of the query rows 2 rpt mp ..
-constexpr int PR_TWO = 4, PR_ONE = 3;
-// and of an item's beginning and end, where a CTA has three tiles or more on average
+constexpr int PR_TWO = 3, PR_ONE = 2;
+// and of an item's beginning and end, where a CTA has four tiles of weight 3 or more on average
 constexpr int PR_ITEM = 12;
 __device__ __forceinline__ int tile_weight(const RoundsParams& p, const RoundSeq& w, int mp) {
     return w.rows - mp * 2 * p.rpt > p.rpt ? PR_TWO : PR_ONE;
