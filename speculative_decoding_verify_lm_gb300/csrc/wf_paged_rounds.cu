@@ -284,11 +284,11 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
     __shared__ Piece s_piece[8];   // the copying warp's next pieces, for the others
     __shared__ uint64_t s_full[2], p_full[2], o_full[2];   // by stream
     __shared__ uint32_t tmem_slot;
-    __shared__ int abort_word, s_bad[8], s_odd[2][2], s_pb, s_turn;
+    __shared__ int abort_word, s_bad[8], s_odd[2][2], s_turn;
     __shared__ uint8_t s_par[2][WF_MAX_SEQ_NODES + 1];   // row of each row's parent, by stream (a row's own copy)
     __shared__ uint64_t q_ready[2];                        // queries brought to fp16, by stream
     __shared__ float s_factor[PR_ROWS];                    // and their scores' factors, for the other stream
-    __shared__ int64_t s_plan, s_scan[2][THREADS / 32];
+    __shared__ int64_t s_scan[2][THREADS / 32];   // weights and items of the sequences of each warp
     volatile int* abort_flag = &abort_word;
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -329,7 +329,8 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
     pdl_wait();
     pdl_trigger();
 
-    // ------------------------------------------------ this CTA's stretch (as in the single-token kernel)
+    // ------------------------------------------------ this CTA's stretch
+    // All threads weigh the sequences, the copying warp finds the stretch among them
     const int run = (p.B + THREADS - 1) / THREADS;
     int64_t mine = 0, mine_items = 0;
     bool heavy = false;   // a tile of weight PR_TWO
@@ -343,46 +344,16 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             if (w.bad && blockIdx.x == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)b);
         }
     }
-    int64_t inc = mine, inc_items = mine_items;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t y = __shfl_up_sync(0xffffffffu, inc, o), z = __shfl_up_sync(0xffffffffu, inc_items, o);
-        if (lane >= o) inc += y, inc_items += z;
+    for (int o = 16; o > 0; o >>= 1) {
+        mine += __shfl_xor_sync(0xffffffffu, mine, o);
+        mine_items += __shfl_xor_sync(0xffffffffu, mine_items, o);
     }
-    if (lane == 31) s_scan[0][warp] = inc, s_scan[1][warp] = inc_items;
+    if (lane == 0) s_scan[0][warp] = mine, s_scan[1][warp] = mine_items;
     tc_fence_before();
     heavy = __syncthreads_or(heavy);
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
-    int64_t total = 0, items = 0, before = inc - mine, before_items = inc_items - mine_items;
-#pragma unroll
-    for (int w = 0; w < THREADS / 32; ++w) {
-        if (w < warp) before += s_scan[0][w], before_items += s_scan[1][w];
-        total += s_scan[0][w];
-        items += s_scan[1][w];
-    }
-    const int ends = total >= (int64_t)PR_ITEM * gridDim.x ? PR_ITEM : 0;
-    total += ends * items;
-    before += ends * before_items;
-    mine += ends * mine_items;
-    int64_t per = pg_quotient(total + gridDim.x - 1, gridDim.x);
-    // every stretch between an item's first and its last holds one of its tiles
-    if (per < (heavy ? PR_TWO : PR_ONE)) per = heavy ? PR_TWO : PR_ONE;
-    const int64_t begin = (int64_t)blockIdx.x * per;
-    const int64_t end = begin + per < total ? begin + per : total;
-    if (begin < end && mine > 0 && before <= begin && begin < before + mine) {
-        int64_t at = before;
-        int b = tid * run;
-        for (;; ++b) {
-            const RoundSeq w = round_seq(p, b);
-            const int64_t n = seq_weight(p, w) + (int64_t)ends * p.G * w.mp;
-            if (begin < at + n) break;
-            at += n;
-        }
-        s_plan = begin - at;
-        s_pb = b;
-    }
-    __syncthreads();
     if (warp >= SOFT) {
         if (S::SPLIT_REGISTERS) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         const uint64_t pol = policy_evict_first();
@@ -421,6 +392,56 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
         };
         if (warp == SOFT) {
             // ---------------------------------------- copies: a tile's keys, then its values, to the ring's next places
+            auto inclusive = [&](int64_t v) {
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
+                    if (lane >= o) v += y;
+                }
+                return v;
+            };
+            const int64_t w_mine = lane < THREADS / 32 ? s_scan[0][lane] : 0;
+            const int64_t w_items = lane < THREADS / 32 ? s_scan[1][lane] : 0;
+            const int64_t w_upto = inclusive(w_mine), items_upto = inclusive(w_items);
+            int64_t total = __shfl_sync(0xffffffffu, w_upto, 31);
+            const int ends = total >= (int64_t)PR_ITEM * gridDim.x ? PR_ITEM : 0;
+            total += ends * __shfl_sync(0xffffffffu, items_upto, 31);
+            int64_t per = pg_quotient(total + gridDim.x - 1, gridDim.x);
+            // every stretch between an item's first and its last holds one of its tiles
+            if (per < (heavy ? PR_TWO : PR_ONE)) per = heavy ? PR_TWO : PR_ONE;
+            const int64_t begin = (int64_t)blockIdx.x * per;
+            const int64_t end = begin + per < total ? begin + per : total;
+            int64_t plan = 0;   // of the stretch's beginning, in its sequence
+            int pb = 0;         // which one
+            if (begin < end) {
+                // the warp that weighed it, the lane, then the sequence
+                auto holder = [&](int64_t upto, int64_t n) {
+                    return __ffs(__ballot_sync(0xffffffffu, n > 0 && upto - n <= begin && begin < upto)) - 1;
+                };
+                const int64_t w_all = w_mine + ends * w_items, all_upto = w_upto + ends * items_upto;
+                const int hw = holder(all_upto, w_all);
+                const int64_t before = __shfl_sync(0xffffffffu, all_upto - w_all, hw);
+                auto weight_of = [&](int b) {
+                    const RoundSeq w = round_seq(p, b);
+                    return seq_weight(p, w) + (int64_t)ends * p.G * w.mp;
+                };
+                const int b0 = (hw * 32 + lane) * run;
+                int64_t n = 0;
+                for (int i = 0; i < run; ++i)
+                    if (b0 + i < p.B) n += weight_of(b0 + i);
+                const int64_t upto = before + inclusive(n);
+                const int hl = holder(upto, n);
+                if (lane == hl) {
+                    plan = begin - (upto - n);
+                    for (pb = b0;; ++pb) {
+                        const int64_t one = run == 1 ? n : weight_of(pb);
+                        if (plan < one) break;
+                        plan -= one;
+                    }
+                }
+                plan = __shfl_sync(0xffffffffu, plan, hl);
+                pb = __shfl_sync(0xffffffffu, pb, hl);
+            }
             // the stretch's first item: `start`, the weight before it; its tile kt is
             // the first that starts in the stretch
             Piece x = {};
@@ -445,13 +466,13 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                 weight = tile_weight(p, x.w, x.mp);
             };
             if (begin < end) {
-                x.b = s_pb;
+                x.b = pb;
                 x.w = round_seq(p, x.b);
                 const int64_t full = (int64_t)p.G * (x.w.nt * PR_TWO + ends);
-                x.mp = (int)pg_quotient(s_plan, full);
+                x.mp = (int)pg_quotient(plan, full);
                 if (x.mp > x.w.mp - 1) x.mp = x.w.mp - 1;
                 weight = tile_weight(p, x.w, x.mp);
-                const int64_t in_rows = s_plan - x.mp * full;
+                const int64_t in_rows = plan - x.mp * full;
                 const int item = x.w.nt * weight + ends;
                 x.g = (int)pg_quotient(in_rows, item);
                 const int64_t in_item = in_rows - (int64_t)x.g * item;
