@@ -597,7 +597,10 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                 auto wait = [&](uint64_t* bar, uint32_t parity) {
                     ok = ok && mbar_wait(bar, parity, p.timeout_ns, abort_flag);
                 };
-                const int per_row = p.D / 16;   // 16-byte pieces of a raw row
+                // a lane keeps its 16-byte piece c of the rows r0, r0 + step ..
+                const int per_row = p.D / 16, rows = 32 / per_row, step = WIDEN * rows;
+                const int c = lane % per_row, r0 = lane < rows * per_row ? (warp - SOFT - 3) * rows + lane / per_row : PR_KT;
+                const bool swap = c & 4;
                 for (int turn = 0; ok; ++turn) {
                     wait(&piece_ready[turn & 7], (turn >> 3) & 1);
                     ok = __all_sync(0xffffffffu, ok);
@@ -613,22 +616,26 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                         if (!ok) break;
                         const uint8_t* src = sW + raw * S::RAW_TILE;
                         uint8_t* dst = sR + slot * TILE;
-                        // 64 pieces a step, warp after warp
-                        for (int j = (warp - SOFT - 3) * 64 + lane; j < PR_KT * per_row; j += WIDEN * 64) {
-                            uint4 v[2];
+                        for (int r = r0; r < PR_KT; r += 4 * step) {
+                            uint4 v[4];
 #pragma unroll
-                            for (int u = 0; u < 2; ++u)   // 128 rows of pieces: a multiple of 64
-                                v[u] = *reinterpret_cast<const uint4*>(src + (j + 32 * u) * 16);
+                            for (int u = 0; u < 4; ++u)
+                                if (r + u * step < PR_KT)
+                                    v[u] = *reinterpret_cast<const uint4*>(src + (r + u * step) * p.D + c * 16);
 #pragma unroll
-                            for (int u = 0; u < 2; ++u) {
-                                const int r = (j + 32 * u) / per_row, c = 2 * ((j + 32 * u) - r * per_row);
+                            for (int u = 0; u < 4; ++u) {
+                                const int ru = r + u * step;
+                                if (ru >= PR_KT) break;
                                 const uint4 lo = make_uint4(e4m3x2_f16x2(v[u].x), e4m3x2_f16x2(v[u].x >> 16),
                                                             e4m3x2_f16x2(v[u].y), e4m3x2_f16x2(v[u].y >> 16));
                                 const uint4 hi = make_uint4(e4m3x2_f16x2(v[u].z), e4m3x2_f16x2(v[u].z >> 16),
                                                             e4m3x2_f16x2(v[u].w), e4m3x2_f16x2(v[u].w >> 16));
-                                uint8_t* row = dst + (c >> 3) * PR_KT * 128 + r * 128;
-                                *reinterpret_cast<uint4*>(row + (((c & 7) ^ (r & 7)) << 4)) = lo;
-                                *reinterpret_cast<uint4*>(row + ((((c & 7) + 1) ^ (r & 7)) << 4)) = hi;
+                                uint8_t* row = dst + (c >> 2) * PR_KT * 128 + ru * 128;
+                                const int at_lo = ((2 * c & 7) ^ (ru & 7)) << 4;   // its neighbour: the other of two
+                                // half of a wide row's lanes store their second piece first: eight
+                                // lanes then meet eight different banks' groups
+                                *reinterpret_cast<uint4*>(row + (at_lo ^ (swap ? 16 : 0))) = swap ? hi : lo;
+                                *reinterpret_cast<uint4*>(row + (at_lo ^ (swap ? 0 : 16))) = swap ? lo : hi;
                             }
                         }
                         fence_async_smem();
