@@ -9,28 +9,40 @@
 // full batch: both have to run without a pause.
 //
 // The work is the flat sequence of 128-position tiles of every (sequence, up to
-// 256 pairs, KV head), a tile weighing 3 with two products of rows and 2 with
-// one (3,500 and 2,300 cycles), in equal stretches for one CTA an SM; the
-// pieces of an item that several CTAs share go to the workspace and a second,
-// small kernel joins them in order.
+// 256 pairs, KV head), in stretches of equal weight for one CTA an SM.  The
+// weights are fitted to the CTAs' cycles on a full batch: a tile 3 with two
+// products of rows and 2 with one (3,400 and 2,300 cycles), an item's beginning
+// and end 12 (about 13,000); with equal tiles the slowest CTA took a quarter
+// longer than the mean.  The pieces of an item that several CTAs share go to the
+// workspace and a second, small kernel joins them in order.
 //
-// Inside a CTA two streams of softmax warps (four each, a thread a row) work
-// in turn, so that the tensor cores compute one stream's products while the
-// other takes its exponentials:
+// Inside a CTA two streams of softmax warps work in turn, so that the tensor
+// cores compute one stream's products while the other takes its exponentials:
 //   two products of rows   each stream has one, both see every tile
 //   one                    both have it, stream w every second tile; their
 //                          results meet in shared memory
 // A product holds whole query rows: 128 / (heads a group) of them.
+// A stream's loop is scores -> exponentials -> both products, one after the
+// other, so its latency is what two products of rows are bound by: over a bf16
+// cache two threads share a row of scores (1,370 cycles a tile, one thread
+// 1,750; 120 -> 102 us for a batch of 32 rounds over 1,600 to 5,200 positions).
 // S and O live in tensor memory; P overwrites its S as the left operand of the
-// second product.  One warp copies queries and pages (tensor copies into the
-// 128-byte swizzle); each stream has a warp of its own that issues its products
-// (one for both spent most of its time on barriers: 139 us for the batch of 32).
+// second product.  Keys and values have a copying warp each (tensor copies into
+// the 128-byte swizzle, which one warp issues at 100 cycles a page: pages of 8
+// positions took 153 us with one warp, 115 with two), each stream a warp of its
+// own that issues its products (one for both spent most of its time on
+// barriers).
+//
+// What it reaches on that batch: 98 us, 4.3 TB/s, 63% of the copy rate.  A
+// product takes 91 cycles a 16-wide step instead of 64, since both operands of
+// the first and the tiles' arrival share the shared memory's bandwidth; an
+// item's end, the pieces' joining and the first tile's latency take the rest.
 //
 // An 8-bit cache goes through fp16 operands (the products take no mixed types):
-// its rows are copied raw and five more warps widen them into the ring, exactly
-// (one warp took 268 us for the batch of 32);
-// the queries are brought to fp16 in place, each row scaled by a power of two
-// that puts its largest element in [1, 2).
+// its rows are copied raw and five more warps widen them into the ring, exactly.
+// The widening bounds it (one warp 268 us for the batch of 32, five 153); the
+// queries are brought to fp16 in place, each row scaled by a power of two that
+// puts its largest element in [1, 2).
 //
 // Tiles that reach the round's own rows take a mask of 128 bits per row.  There
 // a stored value that is not finite is set to zero before the product (0 * inf

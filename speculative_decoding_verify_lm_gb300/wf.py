@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 import threading
 from typing import Optional
 
@@ -88,6 +89,9 @@ class PagedAttnArgs(ctypes.Structure):
     ]
 
 
+# the same bytes as PagedAttnArgs
+_PAGED_ATTN = struct.Struct("@PqiiPPPPPiifPP")
+
 _SIGS = {
     "wf_status_string": (ctypes.c_char_p, [_i32]),
     "wf_version": (_i32, []),
@@ -124,8 +128,7 @@ _SIGS = {
     "wf_paged_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
     "wf_paged_append": (_i32, [ctypes.POINTER(PagedCacheArgs), _i32, _c_void_p, ctypes.c_int64, _c_void_p,
                                ctypes.c_int64, _i32, _c_void_p, _c_void_p, _c_void_p, _sz, _c_void_p]),
-    "wf_paged_attention": (_i32, [ctypes.POINTER(PagedCacheArgs), ctypes.POINTER(PagedAttnArgs), _c_void_p, _sz,
-                                  _c_void_p]),
+    "wf_paged_attention": (_i32, [ctypes.POINTER(PagedCacheArgs), _c_void_p, _c_void_p, _sz, _c_void_p]),
     "wf_paged_compact": (_i32, [ctypes.POINTER(PagedCacheArgs), _c_void_p, _c_void_p, _i32, _c_void_p, _c_void_p,
                                 _c_void_p, _sz, _c_void_p]),
     "wf_pages_reserve": (_i32, [ctypes.POINTER(PagedCacheArgs), _c_void_p, _c_void_p, _c_void_p, _c_void_p, _sz,
@@ -529,12 +532,9 @@ class PagedCache:
         a.kv_type = WF_KV_E4M3 if e4m3 else WF_KV_BF16
         a.layers, a.num_pages, a.page_size, a.G, a.D = layers, num_pages, page_size, G, D
         a.B, a.max_pages = table.shape
+        self.B, self.G, self.D = a.B, a.G, a.D
         self.args = a
         self._ref = ctypes.byref(a)
-
-    @property
-    def B(self) -> int:
-        return self.args.B
 
 
 class PagedWorkspace(Workspace):
@@ -582,13 +582,13 @@ def _lens(t, name, n, optional=False):
 def wf_paged_append(cache: PagedCache, k, v, pos_off, cache_len, ws: PagedWorkspace, layer: int = 0, stream=None):
     """Store the round's keys and values (rows pos_off[b] + i of k, v [P, G, D] bf16, strided rows allowed) at
     positions cache_len[b] + i of each sequence."""
-    a = cache.args
-    kp, ks = _rows(k, "k", a.G, a.D)
-    vp, vs = _rows(v, "v", a.G, a.D)
+    B, G, D = cache.B, cache.G, cache.D
+    kp, ks = _rows(k, "k", G, D)
+    vp, vs = _rows(v, "v", G, D)
     if k.shape[0] != v.shape[0]:
         raise ValueError("k and v must have the same rows")
-    _raise(lib().wf_paged_append(cache._ref, layer, kp, ks, vp, vs, k.shape[0], _lens(pos_off, "pos_off", a.B + 1),
-                                 _lens(cache_len, "cache_len", a.B), *_paged(ws), _stream(stream)),
+    _raise((_lib or lib()).wf_paged_append(cache._ref, layer, kp, ks, vp, vs, k.shape[0], _lens(pos_off, "pos_off", B + 1),
+                                 _lens(cache_len, "cache_len", B), *_paged(ws), _stream(stream)),
            "wf_paged_append")
 
 
@@ -600,45 +600,43 @@ def wf_paged_attention(cache: PagedCache, q, pos_off, cache_len, ws: PagedWorksp
     q [P, H, D] bf16 (strided rows allowed), rows pos_off[b] .. pos_off[b+1]-1 of sequence b at positions
     cache_len[b] ..; single new tokens: one row each.  Chains unless parent (with node_off, and kind to mix) gives
     trees.  max_rows: most rows of a sequence.  scale: 1 / sqrt(D) if None."""
-    c = cache.args
-    a = PagedAttnArgs()
-    a.q, a.q_stride = _rows(q, "q", 0, c.D)
-    a.P, a.H, D = q.shape
-    a.pos_off = _lens(pos_off, "pos_off", c.B + 1)
-    a.cache_len = _lens(cache_len, "cache_len", c.B)
-    a.node_off = _lens(node_off, "node_off", c.B + 1, True)
-    a.kind = _lens(kind, "kind", c.B, True)
-    a.parent = _check(parent, "parent", _I32, True)
-    a.max_rows, a.layer = max_rows, layer
-    a.scale = D ** -0.5 if scale is None else scale
+    B, D = cache.B, cache.D
+    P, H = q.shape[0], q.shape[1]
+    qp, stride = _rows(q, "q", 0, D)
     if out is None:
         out = torch.empty_like(q, memory_format=torch.contiguous_format)
-        a.out = out.data_ptr() if a.P else _placeholder(q.device)
-    elif out.numel() != q.numel():
+        op = out.data_ptr() if P else _placeholder(q.device)
+    elif out.numel() != P * H * D:
         raise ValueError("out must be [P, H, D]")
     else:
-        a.out = _check(out, "out", _BF16)
-    if lse is None and with_lse:
-        lse = q.new_empty((a.P, a.H), dtype=torch.float32)
-    elif lse is not None and lse.numel() != a.P * a.H:
-        raise ValueError("lse must be [P, H]")
+        op = _check(out, "out", _BF16)
     if lse is not None:
-        a.lse = _check(lse, "lse", _F32)
-    _raise(lib().wf_paged_attention(cache._ref, ctypes.byref(a), *_paged(ws), _stream(stream)),
-           "wf_paged_attention")
+        if lse.numel() != P * H:
+            raise ValueError("lse must be [P, H]")
+    elif with_lse:
+        lse = torch.empty((P, H), dtype=torch.float32, device=q.device)
+    # packed at once: setting a structure's fields one by one takes four times as long
+    args = _PAGED_ATTN.pack(qp, stride, P, H, _lens(pos_off, "pos_off", B + 1), _lens(cache_len, "cache_len", B),
+                            _lens(node_off, "node_off", B + 1, True) or 0, _lens(kind, "kind", B, True) or 0,
+                            _check(parent, "parent", _I32, True) or 0, max_rows, layer,
+                            D ** -0.5 if scale is None else scale, op,
+                            0 if lse is None else _check(lse, "lse", _F32))
+    st = (_lib or lib()).wf_paged_attention(cache._ref, args, *_paged(ws), _stream(stream))
+    if st:
+        _raise(st, "wf_paged_attention")
     return out, lse
 
 
 def wf_paged_compact(cache: PagedCache, n_accept, path, cache_len, ws: PagedWorkspace, new_len=None, stream=None):
     """Move the accepted path's keys and values up behind the round's first row, in every layer -> new_len [B]
     (pass cache_len as new_len to update it in place)."""
-    B = cache.args.B
+    B = cache.B
     if path is not None and (path.dim() != 2 or path.shape[0] != B):
         raise ValueError("path must be [B, path_stride]")
     if new_len is None:
         new_len = torch.empty_like(cache_len)
     ps = path.shape[1] if path is not None else 0
-    _raise(lib().wf_paged_compact(cache._ref, _lens(n_accept, "n_accept", B), _check(path, "path", _I32, True), ps,
+    _raise((_lib or lib()).wf_paged_compact(cache._ref, _lens(n_accept, "n_accept", B), _check(path, "path", _I32, True), ps,
                                   _lens(cache_len, "cache_len", B), _lens(new_len, "new_len", B), *_paged(ws),
                                   _stream(stream)), "wf_paged_compact")
     return new_len
@@ -646,10 +644,10 @@ def wf_paged_compact(cache: PagedCache, n_accept, path, cache_len, ws: PagedWork
 
 def wf_pages_reserve(cache: PagedCache, pos_off, cache_len, ws: PagedWorkspace, added=None, stream=None):
     """Pages for the round's rows, shared ones replaced by copies -> added [B] (pages taken, -1 = did not fit)."""
-    B = cache.args.B
+    B = cache.B
     if added is None:
         added = torch.empty_like(cache_len)
-    _raise(lib().wf_pages_reserve(cache._ref, _lens(pos_off, "pos_off", B + 1), _lens(cache_len, "cache_len", B),
+    _raise((_lib or lib()).wf_pages_reserve(cache._ref, _lens(pos_off, "pos_off", B + 1), _lens(cache_len, "cache_len", B),
                                   _lens(added, "added", B), *_paged(ws), _stream(stream)), "wf_pages_reserve")
     return added
 
@@ -657,14 +655,14 @@ def wf_pages_reserve(cache: PagedCache, pos_off, cache_len, ws: PagedWorkspace, 
 def wf_pages_fork(cache: PagedCache, src, dst, cache_len, ws: PagedWorkspace, stream=None):
     """Sequences dst become copies of sequences src that share their pages; cache_len[dst] follows, in place."""
     n = src.numel()
-    _raise(lib().wf_pages_fork(cache._ref, _check(src, "src", _I32), _lens(dst, "dst", n), n,
-                               _lens(cache_len, "cache_len", cache.args.B), *_paged(ws), _stream(stream)),
+    _raise((_lib or lib()).wf_pages_fork(cache._ref, _check(src, "src", _I32), _lens(dst, "dst", n), n,
+                               _lens(cache_len, "cache_len", cache.B), *_paged(ws), _stream(stream)),
            "wf_pages_fork")
 
 
 def wf_pages_trim(cache: PagedCache, cache_len, ws: PagedWorkspace, stream=None):
     """Give back the pages past each sequence's length (0 frees the sequence)."""
-    _raise(lib().wf_pages_trim(cache._ref, _lens(cache_len, "cache_len", cache.args.B), *_paged(ws),
+    _raise((_lib or lib()).wf_pages_trim(cache._ref, _lens(cache_len, "cache_len", cache.B), *_paged(ws),
                                _stream(stream)), "wf_pages_trim")
 
 
