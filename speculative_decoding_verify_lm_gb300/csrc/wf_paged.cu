@@ -208,7 +208,9 @@ __global__ void __launch_bounds__(CP_THREADS) compact_kernel(const CompactParams
 
 // ------------------------------------------------------------------ reserve
 // One CTA decides.  A thread owns whole sequences; the free pages are found
-// 16,384 counts at a time, their numbers kept in shared memory.
+// 16,384 counts at a time, their numbers kept in shared memory.  A chain of
+// dependent loads bounds it, so the first counts are read while the sequences
+// are, and what a sequence needs stays in shared memory.
 //
 // Copy on write in sequence order without an ordered pass: every holder that
 // is about to write takes its reference away; a page whose count reaches 0 has
@@ -224,8 +226,6 @@ struct ReserveParams {
     const int32_t* pos_off;
     const int32_t* cache_len;
     int32_t* added;       // or null
-    int32_t* off;         // [B] first page of each sequence among those taken
-    int32_t* need;        // [B] pages it takes, -1 bad
     int32_t* copies;      // (from, to) of each page to copy
     uint32_t* n_copies;
     int B, page_shift, num_pages, max_pages;
@@ -274,20 +274,24 @@ __device__ __forceinline__ int block_scan(int v, int* s_warp, int* total) {
     return before + x - v;
 }
 
-// The free pages of [base, base + RS_CHUNK), lowest first, into `list`; returns their number.
-__device__ __forceinline__ int free_in_chunk(const int32_t* ref, int num_pages, int base, int32_t* list,
-                                             int* s_warp) {
-    constexpr int PER_WARP = RS_CHUNK / (RS_THREADS / 32);
-    constexpr int STEPS = PER_WARP / 32;
+// This thread's counts of the chunk [base, base + RS_CHUNK).
+constexpr int RS_PER_WARP = RS_CHUNK / (RS_THREADS / 32);
+constexpr int RS_STEPS = RS_PER_WARP / 32;
+__device__ __forceinline__ void chunk_counts(const int32_t* ref, int num_pages, int base, int (&r)[RS_STEPS]) {
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+#pragma unroll
+    for (int i = 0; i < RS_STEPS; ++i) {
+        const int page = base + w * RS_PER_WARP + i * 32 + lane;
+        r[i] = page < num_pages ? __ldcg(ref + page) : 1;
+    }
+}
+
+// The chunk's free pages, lowest first, into `list`; returns their number.
+__device__ __forceinline__ int free_in_chunk(const int (&r)[RS_STEPS], int base, int32_t* list, int* s_warp) {
+    constexpr int PER_WARP = RS_PER_WARP, STEPS = RS_STEPS;
     const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
     unsigned mask[STEPS];
     int n = 0;
-    int r[STEPS];
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const int page = base + w * PER_WARP + i * 32 + lane;
-        r[i] = page < num_pages ? __ldcg(ref + page) : 1;
-    }
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
         mask[i] = __ballot_sync(0xffffffffu, r[i] == 0);
@@ -306,13 +310,19 @@ __device__ __forceinline__ int free_in_chunk(const int32_t* ref, int num_pages, 
 }
 
 __global__ void __launch_bounds__(RS_THREADS) reserve_kernel(const ReserveParams p) {
-    extern __shared__ int32_t list[];   // [RS_CHUNK]
+    extern __shared__ int32_t list[];   // [RS_CHUNK] free pages
+    int32_t* off = list + RS_CHUNK;     // [B] first page of each sequence among those taken
+    int32_t* need = off + p.B;          // [B] pages it takes, -1 bad
     __shared__ int s_warp[32];
+    __shared__ unsigned s_copies;
     pdl_wait();
     pdl_trigger();   // the copies' CTAs may take their places and wait there
     const int tid = threadIdx.x;
     const int64_t cap = (int64_t)p.max_pages << p.page_shift;
-    if (tid == 0) *p.n_copies = 0;
+    if (tid == 0) s_copies = 0;
+    // which pages are free does not change below before they are handed out
+    int counts[RS_STEPS];
+    chunk_counts(p.ref, p.num_pages, 0, counts);
     // shared blocks that are about to be written are marked
     bool any_shared = false;
     for (int b = tid; b < p.B; b += RS_THREADS) {
@@ -333,13 +343,13 @@ __global__ void __launch_bounds__(RS_THREADS) reserve_kernel(const ReserveParams
                     }
                 }
         }
-        p.need[b] = ok ? 0 : -1;
+        need[b] = ok ? 0 : -1;
         if (!ok) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)b);
     }
     any_shared = __syncthreads_or(any_shared);
     auto each_marked = [&](auto&& f) {   // f(b, entry address, page)
         for (int b = tid; b < p.B; b += RS_THREADS) {
-            if (p.need[b] < 0) continue;
+            if (need[b] < 0) continue;
             const Blocks k = blocks_of(p, b);
             int32_t* row = p.table + (int64_t)b * p.max_pages;
             for (int j = k.j0; j < k.j1; ++j)
@@ -366,22 +376,23 @@ __global__ void __launch_bounds__(RS_THREADS) reserve_kernel(const ReserveParams
     for (int b0 = 0; b0 < p.B; b0 += RS_THREADS) {
         const int b = b0 + tid;
         int n = 0;
-        if (b < p.B && p.need[b] >= 0) {
+        if (b < p.B && need[b] >= 0) {
             const Blocks k = blocks_of(p, b);
             const int32_t* row = p.table + (int64_t)b * p.max_pages;
             for (int j = k.j0; j < k.j1; ++j) n += row[j] < 0;
-            p.need[b] = n;
+            need[b] = n;
         }
         int total;
         const int at = block_scan(n, s_warp, &total);
-        if (b < p.B) p.off[b] = carry + at;
+        if (b < p.B) off[b] = carry + at;
         carry += total;
     }
     const int wanted = carry;
     // how many of the wanted pages are there; a single chunk's list is kept
     int have = 0, base = 0, n_list = 0;
     while (have < wanted && base < p.num_pages) {
-        n_list = free_in_chunk(p.ref, p.num_pages, base, list, s_warp);
+        if (base > 0) chunk_counts(p.ref, p.num_pages, base, counts);
+        n_list = free_in_chunk(counts, base, list, s_warp);
         have += n_list;
         base += RS_CHUNK;
     }
@@ -389,12 +400,12 @@ __global__ void __launch_bounds__(RS_THREADS) reserve_kernel(const ReserveParams
     const bool kept = base <= RS_CHUNK;
     auto hand_out = [&](int first, int n) {   // list holds the pages of ranks [first, first + n)
         for (int b = tid; b < p.B; b += RS_THREADS) {
-            const int need = p.need[b], off = p.off[b];
-            if (need <= 0 || off + need > limit || off >= first + n || off + need <= first) continue;
+            const int taken = need[b], from = off[b];
+            if (taken <= 0 || from + taken > limit || from >= first + n || from + taken <= first) continue;
             const Blocks k = blocks_of(p, b);
             int32_t* row = p.table + (int64_t)b * p.max_pages;
-            int rank = off > first ? off : first;   // those below came from earlier chunks
-            for (int j = k.j0; j < k.j1 && rank < off + need && rank < first + n; ++j) {
+            int rank = from > first ? from : first;   // those below came from earlier chunks
+            for (int j = k.j0; j < k.j1 && rank < from + taken && rank < first + n; ++j) {
                 const int e = row[j];
                 if (e >= 0) continue;
                 const int page = list[rank - first];
@@ -402,7 +413,7 @@ __global__ void __launch_bounds__(RS_THREADS) reserve_kernel(const ReserveParams
                 row[j] = page;
                 __stcg(p.ref + page, 1);
                 if (e <= -2 && j == k.j0 && k.tail) {
-                    const uint32_t at = atomicAdd(p.n_copies, 1u);
+                    const uint32_t at = atomicAdd(&s_copies, 1u);
                     p.copies[2 * at] = -(e + 2);
                     p.copies[2 * at + 1] = page;
                 }
@@ -416,7 +427,8 @@ __global__ void __launch_bounds__(RS_THREADS) reserve_kernel(const ReserveParams
         } else {
             int first = 0;
             for (int c = 0; c < p.num_pages && first < limit; c += RS_CHUNK) {
-                const int n = free_in_chunk(p.ref, p.num_pages, c, list, s_warp);
+                chunk_counts(p.ref, p.num_pages, c, counts);
+                const int n = free_in_chunk(counts, c, list, s_warp);
                 hand_out(first, n);
                 first += n;
             }
@@ -424,9 +436,9 @@ __global__ void __launch_bounds__(RS_THREADS) reserve_kernel(const ReserveParams
     }
     // those that did not fit get their references back
     for (int b = tid; b < p.B; b += RS_THREADS) {
-        const int need = p.need[b];
-        const bool fits = need >= 0 && p.off[b] + need <= limit;
-        if (need > 0 && !fits) {
+        const int taken = need[b];
+        const bool fits = taken >= 0 && off[b] + taken <= limit;
+        if (taken > 0 && !fits) {
             const Blocks k = blocks_of(p, b);
             int32_t* row = p.table + (int64_t)b * p.max_pages;
             for (int j = k.j0; j < k.j1; ++j)
@@ -436,8 +448,9 @@ __global__ void __launch_bounds__(RS_THREADS) reserve_kernel(const ReserveParams
                     atomicAdd(p.ref + page, 1);
                 }
         }
-        if (p.added) p.added[b] = fits ? need : -1;
+        if (p.added) p.added[b] = fits ? taken : -1;
     }
+    if (tid == 0) *p.n_copies = s_copies;   // behind hand_out's barriers
 }
 
 // The pages that reserve_kernel listed, copied in every layer: 16 KB units
@@ -609,7 +622,8 @@ wf_status launch_pages_reserve(const wf_paged_cache* c, const int32_t* pos_off, 
     static std::mutex mu;
     static bool attr_set[64] = {false};
     PG_TRY(configure_once(mu, attr_set, [] {
-        return cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, RS_CHUNK * 4) ==
+        return cudaFuncSetAttribute(reserve_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    4 * (RS_CHUNK + 2 * WF_PAGED_MAX_SEQS)) ==
                cudaSuccess;
     }));
     uint8_t* w = static_cast<uint8_t*>(ws);
@@ -620,8 +634,6 @@ wf_status launch_pages_reserve(const wf_paged_cache* c, const int32_t* pos_off, 
     p.pos_off = pos_off;
     p.cache_len = cache_len;
     p.added = added;
-    p.off = reinterpret_cast<int32_t*>(w + L.off);
-    p.need = reinterpret_cast<int32_t*>(w + L.need);
     p.copies = reinterpret_cast<int32_t*>(w + L.copies);
     p.n_copies = &static_cast<Control*>(ws)->page_copies;
     p.B = c->B;
@@ -629,7 +641,7 @@ wf_status launch_pages_reserve(const wf_paged_cache* c, const int32_t* pos_off, 
     p.num_pages = c->num_pages;
     p.max_pages = c->max_pages;
     p.ctrl = static_cast<Control*>(ws);
-    PG_TRY(launch(reserve_kernel, dim3(1), dim3(RS_THREADS), (size_t)RS_CHUNK * 4, s, p));
+    PG_TRY(launch(reserve_kernel, dim3(1), dim3(RS_THREADS), 4 * ((size_t)RS_CHUNK + 2 * c->B), s, p));
     const int64_t page_bytes = (int64_t)c->page_size * c->G * c->D * kv_bytes(c);
     const int64_t layer_bytes = page_bytes * c->num_pages;
     // every unit that all sequences together can need, at most four CTAs an SM

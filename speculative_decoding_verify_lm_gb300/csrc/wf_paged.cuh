@@ -15,7 +15,7 @@ constexpr int PA_MAX_ROUND_CTAS = 160;   // and of a launch over drafted rows
 constexpr int PA_ROUND_M = 256;     // pairs of an item there
 
 struct PagedLayout {
-    size_t cnt, off, need, copies, join, stat, part, total;
+    size_t cnt, copies, join, stat, part, total;
 };
 
 // The counters have a fixed place, sized for the most sequences: calls of
@@ -29,10 +29,6 @@ inline PagedLayout paged_layout(int D, int max_rows) {
     PagedLayout L;
     size_t o = sizeof(Control);
     L.cnt = o;
-    o = align_up(o + 4 * SEQS, 256);
-    L.off = o;
-    o = align_up(o + 4 * SEQS, 256);
-    L.need = o;
     o = align_up(o + 4 * SEQS, 256);
     L.copies = o;
     o = align_up(o + 8 * SEQS, 256);
