@@ -25,8 +25,7 @@ struct Control {
     uint32_t router_done;     // CTAs finished in the current router launch
     uint32_t gemm_done;       // CTAs finished in the current LM-head launch
     uint32_t rope_tag[2];     // catch-up: (theta bits, D + 1) of the rotary table held in the workspace
-    uint32_t page_copies;     // pages listed by the current reserve launch
-    uint32_t pad[57];
+    uint32_t pad[58];
 };
 static_assert(sizeof(Control) == 256, "control block is 256 bytes");
 

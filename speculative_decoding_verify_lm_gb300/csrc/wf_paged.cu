@@ -637,7 +637,7 @@ wf_status launch_pages_reserve(const wf_paged_cache* c, const int32_t* pos_off, 
     p.cache_len = cache_len;
     p.added = added;
     p.copies = reinterpret_cast<int32_t*>(w + L.copies);
-    p.n_copies = &static_cast<Control*>(ws)->page_copies;
+    p.n_copies = reinterpret_cast<uint32_t*>(w + L.n_copies);
     p.B = c->B;
     p.page_shift = log2_of(c->page_size);
     p.num_pages = c->num_pages;

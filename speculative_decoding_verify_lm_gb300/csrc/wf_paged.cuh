@@ -7,15 +7,15 @@
 namespace wf {
 
 // ----------------------------------------------------------------- workspace
-// control block | arrival counters (zero at rest) | page bookkeeping of a
-// reserve call | shared items and partial results of the attention's splits
+// control block | arrival counters (zero at rest) | pages that a reserve call
+// copies | shared items and partial results of the attention's splits
 constexpr int PA_TILE_M = 16;       // query heads of a single-token item at most
 constexpr int PA_MAX_CTAS = 640;    // most CTAs of a single-token launch
 constexpr int PA_MAX_ROUND_CTAS = 160;   // and of a launch over drafted rows
 constexpr int PA_ROUND_M = 256;     // pairs of an item there
 
 struct PagedLayout {
-    size_t cnt, copies, join, stat, part, total;
+    size_t cnt, n_copies, copies, join, stat, part, total;
 };
 
 // The counters have a fixed place, sized for the most sequences: calls of
@@ -30,6 +30,8 @@ inline PagedLayout paged_layout(int D, int max_rows) {
     size_t o = sizeof(Control);
     L.cnt = o;
     o = align_up(o + 4 * SEQS, 256);
+    L.n_copies = o;   // pages listed by the current reserve launch
+    o += 256;
     L.copies = o;
     o = align_up(o + 8 * SEQS, 256);
     L.join = o;
