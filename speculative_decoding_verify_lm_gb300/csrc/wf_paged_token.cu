@@ -29,6 +29,11 @@
 // P^T reaches the second product by an 8 x 8 transpose between the lanes.  The
 // running maximum may lag by a factor of 2^LAG: no lane exchanges a maximum
 // unless one has outgrown it.
+//
+// What it reaches, in copy rates (6.8 TB/s): 91% on one sequence of 131,000
+// positions (87 us), 95% on 64 of 100 to 16,384 (157 us), 83% on 128 of 2,000 to
+// 6,000 over 8-bit (174 us), where the conversions and products fill the
+// computing warps' issue slots.  One user at 2,048 positions: 10.9 us of latency.
 #include "wf_paged.cuh"
 
 #define PT_TRY(x)                      \
@@ -705,7 +710,8 @@ static TokenVariant token_variant_of() {
     return {paged_token_kernel<DP, E4M3, NH>, TokenShape<DP, E4M3, NH>::SMEM, TokenShape<DP, E4M3, NH>::KT};
 }
 
-// bit 0: an 8-bit cache; bit 1: more than 8 query heads a KV head; bit 2: heads wider than 64
+// bit 0: an 8-bit cache; bit 1: items of 16 query heads; bit 2: heads wider than 64
+constexpr int TOKEN_VARIANTS = 7;
 static TokenVariant token_variant(int i) {
     switch (i) {
         case 0: return token_variant_of<64, false, 1>();
@@ -714,20 +720,19 @@ static TokenVariant token_variant(int i) {
         case 3: return token_variant_of<64, true, 2>();
         case 4: return token_variant_of<128, false, 1>();
         case 5: return token_variant_of<128, true, 1>();
-        case 6: return token_variant_of<128, false, 2>();
-        default: return token_variant_of<128, true, 2>();
+        default: return token_variant_of<128, false, 2>();
     }
 }
 
 wf_status launch_paged_token(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s) {
     static std::mutex mu;
     static bool attr_set[64] = {false};
-    static int ctas[64][8];   // CTAs an SM holds, per variant
+    static int ctas[64][TOKEN_VARIANTS];   // CTAs an SM holds
     const bool e4m3 = c->kv_type == WF_KV_E4M3;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev >= 64) return WF_ERR_CUDA;
     PT_TRY(configure_once(mu, attr_set, [dev] {
-        for (int i = 0; i < 8; ++i) {
+        for (int i = 0; i < TOKEN_VARIANTS; ++i) {
             const TokenVariant v = token_variant(i);
             if (cudaFuncSetAttribute(v.fn, cudaFuncAttributeMaxDynamicSharedMemorySize, v.smem) != cudaSuccess ||
                 cudaFuncSetAttribute(v.fn, cudaFuncAttributePreferredSharedMemoryCarveout, 100) != cudaSuccess ||
@@ -761,15 +766,22 @@ wf_status launch_paged_token(const wf_paged_cache* c, const wf_paged_attn_args* 
     p.G = c->G;
     p.D = c->D;
     p.hq = a->H / c->G;
-    p.mt = cdiv(p.hq, p.hq > 8 ? 16 : 8);
+    // Groups of more than 8 heads: items of 16 read the cache half as often (64
+    // sequences, 16 heads a group over 4 x 64: 61 us against 95 bf16, 52 against 62
+    // 8-bit; over 4 x 128 bf16 152 against 155).  Wide heads over an 8-bit cache are
+    // bound by instructions, and items of 8 let an SM hold two CTAs: 103 against 120.
+    const bool sixteen = p.hq > 8 && !(e4m3 && c->D > 64);
+    p.mt = cdiv(p.hq, sixteen ? 16 : 8);
     p.B = c->B;
     while ((1 << p.page_shift) < c->page_size) ++p.page_shift;
     p.num_pages = c->num_pages;
     p.max_pages = c->max_pages;
+    // shortest stretch, one user at 2,048 positions: 1 tile 10.85 us, 2 11.92, 3 10.87,
+    // 4 13.3, 6 14.9; of the equals the one that leaves fewer pieces
     p.min_tiles = 3;
     p.ctrl = static_cast<Control*>(ws);
     p.timeout_ns = wait_timeout_ns();
-    const int vi = (e4m3 ? 1 : 0) | (p.hq > 8 ? 2 : 0) | (c->D > 64 ? 4 : 0);
+    const int vi = (e4m3 ? 1 : 0) | (sixteen ? 2 : 0) | (c->D > 64 ? 4 : 0);
     const TokenVariant v = token_variant(vi);
     int grid = num_sms() * (ctas[dev][vi] > 0 ? ctas[dev][vi] : 1);
     if (grid > PA_MAX_CTAS) grid = PA_MAX_CTAS;
