@@ -82,6 +82,7 @@ struct RoundsParams {
     int P, H, G, D, hq, B, page_shift, num_pages, max_pages, max_rows;
     int rpt;                 // query rows of a product: 128 / hq
     int box_rows;            // rows of a copy: min(page_size, 128)
+    int per_tile;            // copies of a tile: 128 / box_rows, at most 16
     uint32_t idesc_s, idesc_o;
     Control* ctrl;
     uint64_t timeout_ns;
@@ -254,7 +255,7 @@ struct RoundsShape {
     static constexpr int STREAM = 128 * HALVES;      // threads of a stream
     static constexpr int THREADS = (SOFT + 2 + COPIES + WIDEN) * 32;
     // 8-bit caches: 512 threads start with 128 registers each (65,536); the softmax
-    // warps take 168, the other eight give down to 80 (63,488 in all)
+    // warps take 176, the other eight give down to 80 (the same 65,536)
     static constexpr bool SPLIT_REGISTERS = E4M3;
     static constexpr int QTILE = BLK * PR_ROWS * 128;
     static constexpr int TILE = BLK * PR_KT * 128;
@@ -342,26 +343,31 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
     pdl_trigger();
 
     // ------------------------------------------------ this CTA's stretch
-    // All threads weigh the sequences, the copying warp finds the stretch among them
+    // The copying warp finds it.  Up to 32 sequences it weighs by itself, a lane each,
+    // before the others are there; more are weighed by all threads.  (Code that is
+    // run once waits for its instructions: half a microsecond less than with the
+    // general way for all.)
+    const bool few = p.B <= 32;
     const int run = (p.B + THREADS - 1) / THREADS;
-    int64_t mine = 0, mine_items = 0;
     bool heavy = false;   // a tile of weight PR_TWO
-    for (int i = 0; i < run; ++i) {
-        const int b = tid * run + i;
-        if (b < p.B) {
-            const RoundSeq w = round_seq(p, b);
-            mine += seq_weight(p, w);
-            mine_items += (int64_t)p.G * w.mp;
-            heavy |= w.mp > 0 && tile_weight(p, w, 0) == PR_TWO;
-            if (w.bad && blockIdx.x == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)b);
-        }
+    int64_t mine = 0, mine_items = 0;   // weight and items of what this thread weighed
+    for (int i = 0; i < (few ? 1 : run); ++i) {
+        const int b = few ? (warp == SOFT ? lane : p.B) : tid * run + i;
+        if (b >= p.B) continue;
+        const RoundSeq w = round_seq(p, b);
+        mine += seq_weight(p, w);
+        mine_items += (int64_t)p.G * w.mp;
+        heavy |= w.mp > 0 && tile_weight(p, w, 0) == PR_TWO;
+        if (w.bad && blockIdx.x == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)b);
     }
+    if (!few) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        mine += __shfl_xor_sync(0xffffffffu, mine, o);
-        mine_items += __shfl_xor_sync(0xffffffffu, mine_items, o);
+        for (int o = 16; o > 0; o >>= 1) {
+            mine += __shfl_xor_sync(0xffffffffu, mine, o);
+            mine_items += __shfl_xor_sync(0xffffffffu, mine_items, o);
+        }
+        if (lane == 0) s_scan[0][warp] = mine, s_scan[1][warp] = mine_items;
     }
-    if (lane == 0) s_scan[0][warp] = mine, s_scan[1][warp] = mine_items;
     tc_fence_before();
     heavy = __syncthreads_or(heavy);
     tc_fence_after();
@@ -369,7 +375,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
     if (warp >= SOFT) {
         if (S::SPLIT_REGISTERS) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         const uint64_t pol = policy_evict_first();
-        const int per_tile = PR_KT / p.box_rows;   // boxes of a tile: at most 16
+        const int per_tile = p.per_tile;
         // lane i of a copying warp: the page of positions i box_rows .. of a tile (-2: none)
         auto page_of = [&](const Piece& x, int kt) {
             const int t = kt * PR_KT + lane * p.box_rows;
@@ -405,19 +411,28 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
         if (warp == SOFT) {
             // ---------------------------------------- copies: a tile's keys, then its values, to the ring's next places
             auto inclusive = [&](int64_t v) {
-#pragma unroll
+#pragma unroll 1
                 for (int o = 1; o < 32; o <<= 1) {
                     const int64_t y = __shfl_up_sync(0xffffffffu, v, o);
                     if (lane >= o) v += y;
                 }
                 return v;
             };
-            const int64_t w_mine = lane < THREADS / 32 ? s_scan[0][lane] : 0;
-            const int64_t w_items = lane < THREADS / 32 ? s_scan[1][lane] : 0;
-            const int64_t w_upto = inclusive(w_mine), items_upto = inclusive(w_items);
-            int64_t total = __shfl_sync(0xffffffffu, w_upto, 31);
+            // a lane's share: its sequence, or what a warp has weighed
+            int64_t n = mine, items = mine_items;
+            if (!few) {
+                n = lane < THREADS / 32 ? s_scan[0][lane] : 0;
+                items = lane < THREADS / 32 ? s_scan[1][lane] : 0;
+            }
+            int64_t total = n, all_items = items;
+#pragma unroll 1
+            for (int o = 16; o > 0; o >>= 1) {
+                total += __shfl_xor_sync(0xffffffffu, total, o);
+                all_items += __shfl_xor_sync(0xffffffffu, all_items, o);
+            }
             const int ends = total >= (int64_t)PR_ITEM * gridDim.x ? PR_ITEM : 0;
-            total += ends * __shfl_sync(0xffffffffu, items_upto, 31);
+            total += ends * all_items;
+            n += ends * items;
             int64_t per = pg_quotient(total + gridDim.x - 1, gridDim.x);
             // every stretch between an item's first and its last holds one of its tiles
             if (per < (heavy ? PR_TWO : PR_ONE)) per = heavy ? PR_TWO : PR_ONE;
@@ -426,33 +441,31 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             int64_t plan = 0;   // of the stretch's beginning, in its sequence
             int pb = 0;         // which one
             if (begin < end) {
-                // the warp that weighed it, the lane, then the sequence
-                auto holder = [&](int64_t upto, int64_t n) {
-                    return __ffs(__ballot_sync(0xffffffffu, n > 0 && upto - n <= begin && begin < upto)) - 1;
+                // the lane whose share holds the beginning; its place there
+                auto find = [&](int64_t from, int64_t share) {
+                    const int64_t upto = from + inclusive(share);
+                    const int l = __ffs(__ballot_sync(0xffffffffu, share > 0 && upto - share <= begin && begin < upto)) - 1;
+                    plan = begin - __shfl_sync(0xffffffffu, upto - share, l);
+                    return l;
                 };
-                const int64_t w_all = w_mine + ends * w_items, all_upto = w_upto + ends * items_upto;
-                const int hw = holder(all_upto, w_all);
-                const int64_t before = __shfl_sync(0xffffffffu, all_upto - w_all, hw);
-                auto weight_of = [&](int b) {
-                    const RoundSeq w = round_seq(p, b);
-                    return seq_weight(p, w) + (int64_t)ends * p.G * w.mp;
-                };
-                const int b0 = (hw * 32 + lane) * run;
-                int64_t n = 0;
-                for (int i = 0; i < run; ++i)
-                    if (b0 + i < p.B) n += weight_of(b0 + i);
-                const int64_t upto = before + inclusive(n);
-                const int hl = holder(upto, n);
-                if (lane == hl) {
-                    plan = begin - (upto - n);
-                    for (pb = b0;; ++pb) {
-                        const int64_t one = run == 1 ? n : weight_of(pb);
+                pb = find(0, n);
+                if (!few) {   // that was the warp: now the lane, then its sequence
+                    const int b0 = (pb * 32 + lane) * run;
+                    auto weight_of = [&](int b) {
+                        const RoundSeq w = round_seq(p, b);
+                        return seq_weight(p, w) + (int64_t)ends * p.G * w.mp;
+                    };
+                    int64_t share = 0;
+                    for (int i = 0; i < run; ++i)
+                        if (b0 + i < p.B) share += weight_of(b0 + i);
+                    const int l = find(begin - plan, share);
+                    pb = __shfl_sync(0xffffffffu, b0, l);
+                    for (;; ++pb) {
+                        const int64_t one = weight_of(pb);
                         if (plan < one) break;
                         plan -= one;
                     }
                 }
-                plan = __shfl_sync(0xffffffffu, plan, hl);
-                pb = __shfl_sync(0xffffffffu, pb, hl);
             }
             // the stretch's first item: `start`, the weight before it; its tile kt is
             // the first that starts in the stretch
@@ -480,11 +493,14 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             if (begin < end) {
                 x.b = pb;
                 x.w = round_seq(p, x.b);
-                const int64_t full = (int64_t)p.G * (x.w.nt * PR_TWO + ends);
-                x.mp = (int)pg_quotient(plan, full);
-                if (x.mp > x.w.mp - 1) x.mp = x.w.mp - 1;
+                int64_t in_rows = plan;
+                if (x.w.mp > 1) {
+                    const int64_t full = (int64_t)p.G * (x.w.nt * PR_TWO + ends);
+                    x.mp = (int)pg_quotient(plan, full);
+                    if (x.mp > x.w.mp - 1) x.mp = x.w.mp - 1;
+                    in_rows -= x.mp * full;
+                }
                 weight = tile_weight(p, x.w, x.mp);
-                const int64_t in_rows = plan - x.mp * full;
                 const int item = x.w.nt * weight + ends;
                 x.g = (int)pg_quotient(in_rows, item);
                 const int64_t in_item = in_rows - (int64_t)x.g * item;
@@ -786,7 +802,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
         }
     } else {
         // -------------------------------------------- softmax: stream w, HALVES threads a row of the product
-        if (S::SPLIT_REGISTERS) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        if (S::SPLIT_REGISTERS) asm volatile("setmaxnreg.inc.sync.aligned.u32 176;");
         const int w = warp / (4 * HALVES), half = (warp >> 2) & (HALVES - 1), row = tid & 127;
         const int pair_id = 4 + w * 4 + (warp & 3);   // the named barrier of the warps that share rows
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -1464,6 +1480,7 @@ wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args*
     p.max_rows = a->max_rows;
     p.rpt = PR_ROWS / p.hq;
     p.box_rows = c->page_size < PR_KT ? c->page_size : PR_KT;
+    p.per_tile = PR_KT / p.box_rows;
     // fp16 operands are format 0 where bf16 are 1; the values' contiguous dimension is N
     const uint32_t formats = e4m3 ? (1u << 7) | (1u << 10) : 0u;
     p.idesc_s = umma_idesc_bf16(PR_ROWS, PR_KT) & ~formats;

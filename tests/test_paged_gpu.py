@@ -834,3 +834,10 @@ def test_keys_of_the_lowest_value_weigh_alike(rows):
             tol = n * 2.0 ** -23 * np.abs(v).mean(0)
             assert np.all(np.abs(out[i, h] - v.mean(0)) <= tol + 2.0 ** -8 * (np.abs(v.mean(0)) + tol))
             assert abs(lse[i, h] - (low * 0.015625 + np.log(n))) <= 2.0 ** -22 * abs(low * 0.015625)
+
+
+def test_more_sequences_than_threads_in_a_round():
+    """1,500 short sequences of one to three rows, some without any."""
+    rows = tuple((1, 2, 3, 0, 2)[b % 5] for b in range(1500))
+    lens = tuple(7 * b % 90 for b in range(1500))
+    check(ref.Case(67, lens, rows, 2, 1, 16, 8, kinds=tuple(b % 2 for b in range(1500))))
