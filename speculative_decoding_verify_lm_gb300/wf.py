@@ -592,9 +592,9 @@ def wf_paged_append(cache: PagedCache, k, v, pos_off, cache_len, ws: PagedWorksp
            "wf_paged_append")
 
 
-def wf_paged_attention(cache: PagedCache, q, pos_off, cache_len, ws: PagedWorkspace, node_off=None, kind=None, parent=None,
-                       max_rows: int = 1, layer: int = 0, scale=None, out=None, lse=None, with_lse: bool = False,
-                       stream=None):
+def wf_paged_attention(cache: PagedCache, q, pos_off, cache_len, ws: PagedWorkspace, node_off=None, kind=None,
+                       parent=None, max_rows: int = 1, layer: int = 0, scale=None, out=None, lse=None,
+                       with_lse: bool = False, stream=None):
     """Attention of the round's rows over the paged cache -> (out [P, H, D] bf16, lse [P, H] fp32 or None).
 
     q [P, H, D] bf16 (strided rows allowed), rows pos_off[b] .. pos_off[b+1]-1 of sequence b at positions
