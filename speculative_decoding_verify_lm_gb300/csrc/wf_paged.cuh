@@ -121,7 +121,6 @@ __device__ __forceinline__ void pg_ldsm_x4_trans(uint32_t (&r)[4], uint32_t addr
 __device__ __forceinline__ void pg_cp16(uint32_t dst, const void* src, uint32_t bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
-__device__ __forceinline__ void pg_cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void pg_cp_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
