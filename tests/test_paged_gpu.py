@@ -841,3 +841,76 @@ def test_more_sequences_than_threads_in_a_round():
     rows = tuple((1, 2, 3, 0, 2)[b % 5] for b in range(1500))
     lens = tuple(7 * b % 90 for b in range(1500))
     check(ref.Case(67, lens, rows, 2, 1, 16, 8, kinds=tuple(b % 2 for b in range(1500))))
+
+
+@pytest.mark.parametrize("how", ["compact", "in place", "fork", "attention"])
+def test_catch_up_right_behind_a_call_that_writes_its_inputs(how):
+    """Compaction (into a fresh tensor and in place), forking and attention, each followed at once by a catch-up that
+    reads what they write: the bits of a run that waits in between."""
+    import pins
+    B, cap, G, D, H, ps, layers = 2, 512, 2, 64, 4, 16, 48
+    c = pins.catchup_case(70, din=H * D, H=H, G=G, D=D, n=(5, 9), L=(203, 402), cap=cap)
+    pages = B * cap // ps
+    g = torch.Generator(device=DEV).manual_seed(70)
+    K0 = torch.randn((layers, pages, ps, G, D), device=DEV, generator=g).to(torch.bfloat16)
+    V0 = torch.randn((layers, pages, ps, G, D), device=DEV, generator=g).to(torch.bfloat16)
+    K, V = K0.clone(), V0.clone()
+    table = torch.arange(pages, dtype=torch.int32, device=DEV).view(B, -1)   # the catch-up's [B, cap, G * D] view
+    if how == "fork":    # its lengths come from two sequences that the tables of this cache describe
+        table = torch.cat([table, torch.full_like(table, -1)])
+    ws = wf.PagedWorkspace(4, H, G, D, 9)
+    cache = wf.PagedCache(K, V, table, ref=torch.ones(pages, dtype=torch.int32, device=DEV))
+    before = {"fork": [203, 402, 0, 0]}.get(how, [200, 400])
+    ln = dev(np.array(before, np.int32))
+    lengths = ln if how in ("in place", "fork") else torch.empty_like(ln)
+    u = dev(c["u"])
+    cu = wf.Catchup(u, dev(c["bl_off"]), lengths[2:] if how == "fork" else lengths, dev(c["gamma"]), dev(c["Wk"]),
+                    dev(c["Wv"]), K[1].view(torch.int16).view(B, cap, G * D), V[1].view(torch.int16).view(B, cap, G * D),
+                    G, Wq=dev(c["Wq"]), Wo=dev(c["Wo"]), eps=c["eps"], theta=c["theta"])
+    n_acc, path = dev(np.array([2, 1], np.int32)), dev(np.array([[3, 5, -1], [4, -1, -1]], np.int32))
+    q = torch.randn((14, H, D), device=DEV, generator=g).to(torch.bfloat16)
+    pos = dev(np.array([0, 5, 14], np.int32))
+    copies, refs = cache.table.clone(), cache.ref.clone()
+
+    def reset():
+        K.copy_(K0), V.copy_(V0), ln.copy_(dev(np.array(before, np.int32)))
+        cache.table.copy_(copies), cache.ref.copy_(refs), u.copy_(dev(c["u"]))
+        if lengths is not ln:
+            lengths.fill_(-7 if how == "compact" else 203)
+
+    def first():
+        if how == "fork":
+            wf.wf_pages_fork(cache, dev_src, dev_dst, ln, ws)
+        elif how == "attention":
+            wf.wf_paged_attention(cache, q, pos, ln, ws, max_rows=9, layer=2, out=u.view(torch.bfloat16).view(14, H, D))
+        else:
+            wf.wf_paged_compact(cache, n_acc, path, ln, ws, new_len=lengths)
+
+    dev_src, dev_dst = dev(np.array([0, 1], np.int32)), dev(np.array([2, 3], np.int32))
+    seen = []
+    for wait in (True, False, False, False):
+        reset()
+        torch.cuda.synchronize()
+        first()
+        if wait:
+            torch.cuda.synchronize()
+        out, attn = cu()
+        torch.cuda.synchronize()
+        assert ws.device_error() == (0, 0) and cu.ws.device_error() == (0, 0)
+        seen.append([x.clone() for x in (out, attn, K, V, lengths)])
+    reset()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        first()
+        cu()
+    for _ in range(5):
+        reset()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert ws.device_error() == (0, 0) and cu.ws.device_error() == (0, 0)
+        seen.append([x.clone() for x in (cu.out, cu.attn, K, V, lengths)])
+    assert host(seen[0][4]).tolist() == {"fork": [203, 402, 203, 402], "attention": [203, 203]}.get(how, [203, 402])
+    for got in seen[1:]:
+        for a, b in zip(got, seen[0]):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
