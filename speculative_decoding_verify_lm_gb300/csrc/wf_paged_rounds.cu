@@ -379,10 +379,11 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
         if (S::SPLIT_REGISTERS) asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
         const uint64_t pol = policy_evict_first();
         const int per_tile = p.per_tile;
-        // lane i of a copying warp: the page of positions i box_rows .. of a tile (-2: none)
+        // lane i of a copying warp: the page of positions i box_rows .. of a tile; -2: the
+        // tile has no such positions, -1: they have no page, whatever negative entry says so
         auto page_of = [&](const Piece& x, int kt) {
             const int t = kt * PR_KT + lane * p.box_rows;
-            return lane < per_tile && t < x.w.T ? p.table[(int64_t)x.b * p.max_pages + (t >> p.page_shift)] : -2;
+            return lane < per_tile && t < x.w.T ? max(p.table[(int64_t)x.b * p.max_pages + (t >> p.page_shift)], -1) : -2;
         };
         auto pool_row = [&](int kt, int page) {
             return (page << p.page_shift) + ((kt * PR_KT + lane * p.box_rows) & ((1 << p.page_shift) - 1));

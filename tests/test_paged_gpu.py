@@ -914,3 +914,21 @@ def test_catch_up_right_behind_a_call_that_writes_its_inputs(how):
     for got in seen[1:]:
         for a, b in zip(got, seen[0]):
             assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("rows", [1, 9])
+@pytest.mark.parametrize("block", [2, 6])                    # cached positions; the round's own
+def test_any_table_entry_that_is_no_page_is_told(kv, rows, block):
+    c = ref.Case(71, (100, 64, 30), (rows,) * 3, 4, 2, 64, 16, kv, kinds=(1, 1, 1))
+    cache, ws = cache_of(c), wf.PagedWorkspace(3, 4, 2, 64, 9)
+    good = run_attention(c, cache, ws=ws)
+    assert ws.device_error() == (0, 0) and np.isfinite(good[0]).all()
+    for entry in (-1, -2, -3, -2 ** 31, c.num_pages, 2 ** 31 - 1):
+        t = c.table.copy()
+        t[0, block] = entry
+        other = wf.PagedCache(cache.K, cache.V, dev(t), k_scale=cache.k_scale, v_scale=cache.v_scale)
+        out, lse, _ = run_attention(c, other, ws=ws)
+        assert ws.device_error() == (BAD, 0), entry
+        assert np.isnan(out[:rows]).all() and np.isnan(lse[:rows]).all(), entry
+        assert np.array_equal(out[rows:], good[0][rows:]) and np.array_equal(lse[rows:], good[1][rows:])
