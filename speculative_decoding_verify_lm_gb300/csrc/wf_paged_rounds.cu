@@ -962,10 +962,12 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                         // The weights are taken against the running maximum as it is; only
                         // when a score has outgrown it by 2^LAG (or nothing has been seen
                         // yet) is the tile's maximum taken first.  A row's threads hold the
-                        // same maximum and decide alike, whatever a wait has come to.
+                        // same maximum and decide alike, whatever a wait has come to.  Rows that
+                        // are no query of the sequence (the next one's, or what the shared memory
+                        // held) have no say: a row's bits depend on its sequence alone.
                         uint32_t pk[WORDS][16];
                         float sum = 0.f;
-                        bool again = !__all_sync(0xffffffffu, m > -INFINITY);
+                        bool again = !__all_sync(0xffffffffu, !live || m > -INFINITY);
                         while (true) {
                             if (again) {
                                 float top = -INFINITY;
@@ -996,7 +998,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                             // exponents relative to the maximum's rounded product with f,
                             // or past PG_FAR to the maximum itself (as for single tokens)
                             float base = S::BIAS - (m == -INFINITY ? 0.f : m * f);
-                            const bool far = __any_sync(0xffffffffu, fabsf(base) > PG_FAR);
+                            const bool far = __any_sync(0xffffffffu, live && fabsf(base) > PG_FAR);
                             if (far) base = S::BIAS;
                             const uint64_t qk2 = pair_of(f, f), base2 = pair_of(base, base);
                             uint64_t sum2[2] = {0, 0};
@@ -1024,7 +1026,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                                     }
                             }
                             // also: the row's other thread has read its scores, which these weights overwrite
-                            const bool stays = again || !((far ? big : big - m) * f > S::LAG);
+                            const bool stays = again || !live || !((far ? big : big - m) * f > S::LAG);
                             if (HALVES == 2 ? named_all(pair_id, 64, stays) : __all_sync(0xffffffffu, stays)) {
                                 float a0, a1;
                                 unpair(add2(sum2[0], sum2[1]), a0, a1);

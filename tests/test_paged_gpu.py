@@ -932,3 +932,41 @@ def test_any_table_entry_that_is_no_page_is_told(kv, rows, block):
         assert ws.device_error() == (BAD, 0), entry
         assert np.isnan(out[:rows]).all() and np.isnan(lse[:rows]).all(), entry
         assert np.array_equal(out[rows:], good[0][rows:]) and np.array_equal(lse[rows:], good[1][rows:])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+@pytest.mark.parametrize("H,G,D", [(10, 2, 80), (12, 1, 64), (8, 2, 128)])
+def test_rows_do_not_depend_on_the_product_s_other_rows(kv, H, G, D):
+    """The same bits whatever the neighbour's queries are and whatever ran before: rows that are no query of the
+    sequence share its products and its warps."""
+    c = ref.Case(72, (900, 700), (3, 3), H, G, D, 16, kv)
+    cache, ws = cache_of(c), wf.PagedWorkspace(2, H, G, D, 3)
+    want = run_attention(c, cache, ws=ws)
+    q = c.q.clone()
+    # queries that fill every row of the products of another call, each as far out as it gets
+    full = ref.Case(73, (300,) * 8, (128,) * 8, 2, 2, D, 16, kv)
+    full_cache, full_ws = cache_of(full), wf.PagedWorkspace(8, 2, 2, D, 128)
+    for power, what in ((0, 1.0), (60, 1.0), (-60, 1.0), (0, float("nan")), (0, float("inf")), (0, 0.0)):
+        fill = torch.randn((8 * 128, 2, D), device=DEV).mul_(what).mul_(2.0 ** power).to(torch.bfloat16)
+        c.q = q.clone()
+        c.q[3:] = (q[3:].float() * what * 2.0 ** power).to(torch.bfloat16)
+        for _ in range(2):
+            run_attention(full, full_cache, ws=full_ws, q=fill)
+            got = run_attention(c, cache, ws=ws)
+            assert np.array_equal(got[0][:3], want[0][:3]) and np.array_equal(got[1][:3], want[1][:3]), (power, what)
+    assert ws.device_error() == (0, 0)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_repeated_rounds_give_the_same_bits(kv):
+    """Five heads a group (three rows of each product belong to nobody), pieces that are joined, other work between."""
+    c = ref.Case(74, (3000, 10, 1200, 2000), (61, 5, 130, 17), 10, 2, 64, 16, kv, kinds=(1, 1, 1, 0))
+    cache, ws = cache_of(c), wf.PagedWorkspace(4, 10, 2, 64, 130)
+    other = ref.Case(75, (400,) * 40, (40,) * 40, 8, 8, 64, 16, kv)
+    other_cache, other_ws = cache_of(other), wf.PagedWorkspace(40, 8, 8, 64, 40)
+    a = run_attention(c, cache, ws=ws)
+    for i in range(4):
+        fill = torch.randn((1600, 8, 64), device=DEV).mul_(float("nan") if i == 3 else 2.0 ** (20 * i)).to(torch.bfloat16)
+        run_attention(other, other_cache, ws=other_ws, q=fill)
+        b = run_attention(c, cache, ws=ws)
+        assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
