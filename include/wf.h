@@ -574,9 +574,9 @@ WF_API wf_status wf_paged_attention(const wf_paged_cache* cache, const wf_paged_
  * n_accept, path as returned by wf_verify_* / wf_round with the same
  * path_stride (0 .. WF_MAX_SEQ_NODES; an n_accept past it is taken as
  * path_stride; -1 keeps no row: new_len = cache_len).  new_len [B] device
- * int32 out, may be cache_len itself.  A path that does not increase or a
- * position without a page sets WF_ERR_BAD_DATA (info = b), moves nothing and
- * writes new_len[b] = -1.
+ * int32 out, may be cache_len itself.  A path that does not increase, or a
+ * first row or path row (read or written) without a page, sets WF_ERR_BAD_DATA
+ * (info = b), moves nothing and writes new_len[b] = -1.
  */
 WF_API wf_status wf_paged_compact(const wf_paged_cache* cache, const int32_t* n_accept, const int32_t* path,
                                   int path_stride, const int32_t* cache_len, int32_t* new_len, void* ws,

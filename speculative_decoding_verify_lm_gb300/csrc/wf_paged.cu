@@ -161,6 +161,8 @@ __global__ void __launch_bounds__(CP_THREADS) compact_kernel(const CompactParams
         return ((int64_t)page << p.page_shift) + (t & ((1 << p.page_shift) - 1));
     };
     bool bad = len < 0 || (!none && (int64_t)len + n + 1 > ((int64_t)p.max_pages << p.page_shift));
+    // the first row is kept whatever is accepted: by a thread without a path entry if there is one
+    if (tid == CP_THREADS - 1 && !bad && !none) bad = row_of(len) < 0;
     bool same = false;
     if (!bad && tid < n) {
         const int32_t* way = p.path + (int64_t)b * p.path_stride;

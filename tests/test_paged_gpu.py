@@ -970,3 +970,25 @@ def test_repeated_rounds_give_the_same_bits(kv):
         run_attention(other, other_cache, ws=other_ws, q=fill)
         b = run_attention(c, cache, ws=ws)
         assert np.array_equal(a[0], b[0]) and np.array_equal(a[1], b[1])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_compact_refuses_a_first_row_without_a_page(in_place):
+    """Nothing accepted, or a path that lies in the next page: the first row's own page has to be there."""
+    lens, rows = (16, 15, 7, 16), (2, 9, 2, 1)
+    c = ref.Case(76, lens, rows, 1, 1, 16, 8, layers=2)
+    t = c.table.copy()
+    t[0, 2] = -1                                             # position 16, nothing accepted
+    t[1, 1] = c.num_pages                                    # position 15, a path that stays in pages 2 and 3
+    path = np.array([[-1, -1], [1, 3], [0, -1], [-1, -1]], np.int32)
+    n = np.array([0, 2, 1, -1], np.int32)                    # the last keeps no row: its page does not matter
+    t[3, 2] = -1
+    cache = wf.PagedCache(c.K.to(DEV), c.V.to(DEV), dev(t))
+    ws = wf.PagedWorkspace(4, 1, 1, 16)
+    ln = dev(np.array(lens, np.int32))
+    new = wf.wf_paged_compact(cache, dev(n), dev(path), ln, ws, new_len=ln if in_place else None)
+    torch.cuda.synchronize()
+    code, info = ws.device_error()
+    assert code == BAD and info in (0, 1)
+    assert np.array_equal(host(new), [-1, -1, 9, 16])
+    assert torch.equal(cache.K.cpu().view(torch.int16), c.K.view(torch.int16))
