@@ -6,6 +6,10 @@
 // user's round, a launch and two or three dependent loads bound them.  Every
 // decision is taken in the order of the sequences, whatever order the threads
 // run in: results are the same from run to run.
+//
+// No pointer here is declared unaliased or read-only for the kernel's life: a
+// launch may begin while the kernel before it still writes the lengths, tables
+// and lists that it reads behind its wait.
 #include "wf_paged.cuh"
 
 #define PG_TRY(x)                      \
@@ -465,7 +469,7 @@ constexpr int PC_UNROLL = 8;
 constexpr int PC_UNIT = PC_THREADS * PC_UNROLL * 16;
 
 __global__ void __launch_bounds__(PC_THREADS)
-    page_copy_kernel(uint8_t* K, uint8_t* V, const int32_t* __restrict__ copies, const uint32_t* n_copies,
+    page_copy_kernel(uint8_t* K, uint8_t* V, const int32_t* copies, const uint32_t* n_copies,
                      int64_t layer_bytes, int64_t page_bytes, int layers) {
     pdl_wait();
     pdl_trigger();
@@ -500,7 +504,7 @@ __global__ void __launch_bounds__(PC_THREADS)
 constexpr int FK_THREADS = 256;
 
 __global__ void __launch_bounds__(FK_THREADS)
-    fork_kernel(int32_t* table, int32_t* ref, const int32_t* __restrict__ src, const int32_t* __restrict__ dst, int n,
+    fork_kernel(int32_t* table, int32_t* ref, const int32_t* src, const int32_t* dst, int n,
                 int32_t* cache_len, int B, int page_shift, int num_pages, int max_pages, Control* ctrl) {
     pdl_wait();
     pdl_trigger();
@@ -537,7 +541,7 @@ __global__ void __launch_bounds__(FK_THREADS)
 }
 
 __global__ void __launch_bounds__(FK_THREADS)
-    trim_kernel(int32_t* table, int32_t* ref, const int32_t* __restrict__ cache_len, int page_shift, int num_pages,
+    trim_kernel(int32_t* table, int32_t* ref, const int32_t* cache_len, int page_shift, int num_pages,
                 int max_pages, Control* ctrl) {
     pdl_wait();
     pdl_trigger();

@@ -38,3 +38,28 @@ def test_the_catch_up_reads_its_inputs_behind_the_wait():
         assert not re.search(r"\b%s\b" % name, early), f"norm_kernel reads {name} before its wait"
         # nor may the compiler take it for constant while the kernel before still writes it
         assert not re.search(r"__restrict__ %s\b" % name, params), name
+
+
+INPUTS = r"\b(p\.|c\.)?(q|k|v|pos_off|cache_len|table|ref|n_accept|path|node_off|kind|parent|src|dst|copies|n_copies)\b"
+
+
+@pytest.mark.parametrize("name,kernel_name", [
+    ("wf_paged.cu", "append_kernel"), ("wf_paged.cu", "compact_kernel"), ("wf_paged.cu", "reserve_kernel"),
+    ("wf_paged.cu", "page_copy_kernel"), ("wf_paged.cu", "fork_kernel"), ("wf_paged.cu", "trim_kernel"),
+    ("wf_paged_token.cu", "paged_token_kernel"), ("wf_paged_rounds.cu", "paged_rounds_kernel"),
+    ("wf_paged_rounds.cu", "rounds_join_kernel"),
+])
+def test_paged_kernels_read_and_promise_nothing_before_the_wait(name, kernel_name):
+    """Compaction in place, then trim: what one writes the next reads, and was launched meanwhile."""
+    params, early, whole = kernel(name, kernel_name)
+    assert not re.search(INPUTS, early), re.search(INPUTS, early)
+    assert "__restrict__" not in params
+
+
+@pytest.mark.parametrize("name", ["wf_paged.cu", "wf_paged_token.cu", "wf_paged_rounds.cu", "wf_paged.cuh"])
+def test_paged_kernels_take_only_scales_for_constant(name):
+    """Loads that assume that nobody writes meanwhile are left to the model's scales."""
+    text = re.sub(r"//[^\n]*", "", source(name))
+    assert "__restrict__" not in text
+    for arg in re.findall(r"__ldg\(([^)]*)\)", text):
+        assert re.match(r"(p\.[kv]_scale|sc) \+", arg), arg
