@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
     __shared__ uint64_t kv_full[RING], kv_empty[RING], raw_full[RAW], raw_empty[RAW], q_full, q_empty, told[8];
     __shared__ uint64_t piece_ready[8], piece_free[8];
     __shared__ Piece s_piece[8];   // the copying warp's next pieces, for the others
-    __shared__ uint64_t s_full[2], p_full[2], o_full[2];   // by stream
+    __shared__ uint64_t s_full[2], p_full[2], o_full[2], drained[2];   // by stream
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_word, s_bad[8], s_odd[2][2], s_turn;
     __shared__ uint8_t s_par[2][WF_MAX_SEQ_NODES + 1];   // row of each row's parent, by stream (a row's own copy)
@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             mbar_init(&s_full[i], 1);
             mbar_init(&p_full[i], STREAM);
             mbar_init(&o_full[i], 1);
+            mbar_init(&drained[i], 1);
         }
         for (int i = 0; i < 8; ++i) {
             mbar_init(&told[i], 1);
@@ -802,6 +803,9 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             if (!ok) {
                 *abort_flag = 1;
                 if (lane == 0) record_error(p.ctrl, WF_ERR_TIMEOUT, 0x810u);
+                // the products issued so far are complete before shared and tensor memory go
+                if (elect_one()) umma_commit(&drained[w]);
+                mbar_wait(&drained[w], 0, p.timeout_ns, nullptr);
             }
         }
     } else {

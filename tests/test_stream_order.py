@@ -1,5 +1,5 @@
-"""What a kernel may read before its dependency wait, checked in the sources
-(no GPU needed).
+"""What a kernel may read before its dependency wait and has to wait for before
+it leaves, checked in the sources (no GPU needed).
 
 Every kernel is launched while its predecessor on the stream may still be
 running.  A call's own inputs (rows, offsets, lengths, tables) can be what that
@@ -63,3 +63,14 @@ def test_paged_kernels_take_only_scales_for_constant(name):
     assert "__restrict__" not in text
     for arg in re.findall(r"__ldg\(([^)]*)\)", text):
         assert re.match(r"(p\.[kv]_scale|sc) \+", arg), arg
+
+
+@pytest.mark.parametrize("name", ["wf_gemm_select.cu", "wf_paged_rounds.cu"])
+def test_a_wait_that_gives_up_lets_its_products_complete(name):
+    """When a wait gives up the CTA frees its tensor memory and leaves.  Products of the tensor cores still in flight
+    would go on reading its shared memory: they are waited for on a barrier that they commit to, whatever the abort
+    flag says."""
+    text = re.sub(r"//[^\n]*", "", source(name))
+    commits = set(re.findall(r"umma_commit\(&?(\w+)", text))
+    drained = set(re.findall(r"mbar_wait\(&?(\w+)(?:\[\w+\])?, \w+, p\.timeout_ns, nullptr\)", text))
+    assert commits & drained, (commits, drained)
