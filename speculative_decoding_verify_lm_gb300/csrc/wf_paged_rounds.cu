@@ -803,10 +803,12 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             if (!ok) {
                 *abort_flag = 1;
                 if (lane == 0) record_error(p.ctrl, WF_ERR_TIMEOUT, 0x810u);
-                // the products issued so far are complete before shared and tensor memory go
-                if (elect_one()) umma_commit(&drained[w]);
-                mbar_wait(&drained[w], 0, p.timeout_ns, nullptr);
             }
+            // The products issued so far are complete before shared and tensor memory
+            // go, whichever warp's wait gave up (if none did, they are by now).
+            __syncwarp();
+            if (elect_one()) umma_commit(&drained[w]);
+            mbar_wait(&drained[w], 0, p.timeout_ns, nullptr);
         }
     } else {
         // -------------------------------------------- softmax: stream w, HALVES threads a row of the product
