@@ -571,6 +571,9 @@ __global__ void __launch_bounds__(PJ_THREADS)
                 umma_commit(&empty[s]);
             }
             umma_commit(tfull);   // arrives once every MMA issued above has completed
+            // nobody else may be left to wait for them, if a wait gave up: not before
+            // shared and tensor memory go
+            mbar_wait(tfull, 0, p.timeout_ns, nullptr);
         }
     } else {
         // ------------------------------------------------ epilogue warps: accumulator -> own partial tile

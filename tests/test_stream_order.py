@@ -65,7 +65,7 @@ def test_paged_kernels_take_only_scales_for_constant(name):
         assert re.match(r"(p\.[kv]_scale|sc) \+", arg), arg
 
 
-@pytest.mark.parametrize("name", ["wf_gemm_select.cu", "wf_paged_rounds.cu"])
+@pytest.mark.parametrize("name", ["wf_gemm_select.cu", "wf_catchup.cu", "wf_paged_rounds.cu"])
 def test_a_wait_that_gives_up_lets_its_products_complete(name):
     """When a wait gives up the CTA frees its tensor memory and leaves.  Products of the tensor cores still in flight
     would go on reading its shared memory: they are waited for on a barrier that they commit to, whatever the abort
