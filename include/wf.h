@@ -537,6 +537,8 @@ WF_API wf_status wf_paged_append(const wf_paged_cache* cache, int layer, const u
  *   s_t    = scale <q[row, h], key_t[g]>,  t the positions the row sees
  *   out[row, h] = sum_t softmax(s)_t value_t[g]                      (bf16)
  *   lse[row, h] = log sum_t e^(s_t)                                  (fp32, natural log)
+ * Scores, also times log2(e), have to lie in fp32's range; one of -inf is a
+ * weight of 0.
  * A masked position never reaches a row, whatever it holds; positions from
  * cache_len[b] + rows on are not read.  fp32 softmax statistics and sums; the
  * probabilities enter the product with V rounded to the 16-bit type of the
@@ -558,7 +560,7 @@ typedef struct wf_paged_attn_args {
     const int32_t* parent;     /* [N] sequence-local parents, or NULL: every sequence is a chain */
     int max_rows;              /* most rows of a sequence, 1 .. WF_MAX_SEQ_NODES + 1 */
     int layer;
-    float scale;               /* > 0 and finite, e.g. 1 / sqrt(D) */
+    float scale;               /* > 0, and finite times log2(e): at most 2.35e38; e.g. 1 / sqrt(D) */
     uint16_t* out;             /* [P, H, D] bf16 bits */
     float* lse;                /* [P, H] or NULL */
 } wf_paged_attn_args;

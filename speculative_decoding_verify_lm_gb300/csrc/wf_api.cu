@@ -523,7 +523,8 @@ wf_status wf_paged_attention(const wf_paged_cache* c, const wf_paged_attn_args* 
                              wf_stream_t stream) {
     if (!c || !a || a->layer < 0 || a->layer >= c->layers || a->P < 0) return WF_ERR_INVALID_ARG;
     if (!a->q || !a->out || !a->pos_off || !a->cache_len || (a->parent && !a->node_off)) return WF_ERR_INVALID_ARG;
-    if (!(a->scale > 0.f) || !(a->scale < INFINITY)) return WF_ERR_INVALID_ARG;
+    // the kernels take exponents to base 2: that factor has to be finite too
+    if (!(a->scale > 0.f) || !(a->scale * 1.44269504f < INFINITY)) return WF_ERR_INVALID_ARG;
     if (!aligned16(a->q) || !aligned16(a->out) || bad_paged_stride(a->q_stride, (int64_t)a->H * c->D))
         return WF_ERR_INVALID_ARG;
     WF_TRY(check_paged(c, a->H, a->max_rows, false, ws, ws_bytes));

@@ -122,3 +122,10 @@ def test_reference_e4m3_by_hand():
     x = np.array([0.0, 448.0, 1000.0, -17.0, -18.0, 2.0 ** -9, 2.0 ** -10, 1.5 * 2.0 ** -9, 0.0146484375, 1.0625, 1.1875])
     assert ref.nearest_e4m3(x).tolist() == [0.0, 448.0, 448.0, -16.0, -18.0, 2.0 ** -9, 0.0, 2.0 ** -8, 0.015625,
                                             1.0, 1.25]
+
+
+@pytest.mark.parametrize("scale,refused", [(2.3e38, False), (2.4e38, True), (3.4e38, True), (1e-38, False)])
+def test_scales_that_are_infinite_to_base_2_are_refused(scale, refused):
+    """The kernels' exponents are scores times scale times log2(e)."""
+    got = wf.lib().wf_paged_attention(ctypes.byref(cache()), ctypes.byref(attn(scale=scale)), 256, 256, None)
+    assert got == (INVALID if refused else WORKSPACE)
