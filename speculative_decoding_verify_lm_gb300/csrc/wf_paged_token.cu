@@ -46,6 +46,18 @@ namespace wf {
 
 constexpr int PT_CONSUMERS = 128;              // four computing warps
 constexpr int PT_THREADS = PT_CONSUMERS + 32;  // and the copying one
+constexpr int PT_JOIN = 16;                    // pieces of an item in flight together when they are joined
+// Shortest stretch in tiles: the longest item in no more pieces than are joined
+// together, up to 3 tiles (longer ones cost more than a second turn of joining).
+// One sequence over 8 heads of 128, stretches of 1, 2, 3, 4 tiles, us:
+//   bf16  300 positions 7.9 10.7 11.8 12.7,  1,250: 9.9 9.7 12.1 11.8,  2,048: 11.6 12.3 11.0 13.3,
+//         4,000: 12.8 12.8 12.3 14.3;  over one head 8.7 9.6 10.6 11.8, 11.4 10.0 11.0 12.3,
+//         13.4 11.9 11.2 12.4, 15.8 12.4 13.0 12.8
+//   8-bit 300 positions 8.5 11.9 8.7 14.3,  2,048: 10.1 12.3 13.6 14.5,  4,000: 11.6 11.0 14.4 13.3;
+//         over one head 9.4 10.4 9.2 9.2, 12.1 10.8 11.7 12.8, 12.6 11.0 12.0 13.0
+// Over 96 such batches (64 to 128 wide, 4 to 16 heads a group, 300 to 5,000
+// positions) this takes 1.04 of the best stretch's time, 3 tiles always 1.18, 1 always 1.07.
+constexpr int PT_MIN_TILES = 3;
 
 struct TokenParams {
     const uint16_t* q;
@@ -63,7 +75,7 @@ struct TokenParams {
     float2* stat;            // [CTA][2][16] (maximum, sum)
     uint32_t* cnt;           // [CTA] arrivals of the item that begins in it, zero at rest
     float qk;                // scale * log2(e)
-    int P, H, G, D, hq, mt, B, page_shift, num_pages, max_pages, min_tiles;
+    int P, H, G, D, hq, mt, B, page_shift, num_pages, max_pages;
     Control* ctrl;
     uint64_t timeout_ns;
 };
@@ -169,6 +181,7 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
     __shared__ float2 s_st[4][16];             // each warp's (maximum, sum)
     __shared__ int s_badpage[S::STAGES];       // the stage's tile has a position without a page
     __shared__ int64_t s_plan, s_scan[PT_THREADS / 32];
+    __shared__ int s_longest[PT_THREADS / 32];
     __shared__ int s_pb, s_last;
     __shared__ int s_abort_word;
     volatile int* abort_flag = &s_abort_word;
@@ -190,11 +203,13 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
     const int run = (p.B + PT_THREADS - 1) / PT_THREADS;
     const int items = p.G * p.mt;
     int64_t mine = 0;
+    int longest = 0;   // tiles of an item
     for (int i = 0; i < run; ++i) {
         const int b = tid * run + i;
         if (b < p.B) {
             const TokenSeq w = token_seq<KT>(p, b);
             mine += (int64_t)items * w.nt;
+            longest = max(longest, w.nt);
             if (w.bad && blockIdx.x == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)b);
         }
     }
@@ -204,16 +219,19 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
         const int64_t y = __shfl_up_sync(0xffffffffu, inc, o);
         if (lane >= o) inc += y;
     }
-    if (lane == 31) s_scan[warp] = inc;
+    longest = __reduce_max_sync(0xffffffffu, longest);
+    if (lane == 31) s_scan[warp] = inc, s_longest[warp] = longest;
     __syncthreads();
     int64_t total = 0, before = inc - mine;
 #pragma unroll
     for (int w = 0; w < PT_THREADS / 32; ++w) {
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
+        longest = max(longest, s_longest[w]);
     }
     int64_t per = pg_quotient(total + gridDim.x - 1, gridDim.x);
-    if (per < p.min_tiles) per = p.min_tiles;
+    const int least = min((longest + PT_JOIN - 1) / PT_JOIN, PT_MIN_TILES);
+    if (per < least) per = least;
     const int64_t begin = (int64_t)blockIdx.x * per;
     const int64_t end = begin + per < total ? begin + per : total;
     if (begin >= end) return;
@@ -647,7 +665,7 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
                 // piece k is CTA c0 + k's: its second slot for the item's first, else its
                 // first.  A thread takes four dims of a head; sixteen pieces' statistics
                 // and outputs are in flight together and added in order.
-                constexpr int BATCH = 16;
+                constexpr int BATCH = PT_JOIN;
                 const int quarter = p.D / 4;
                 for (int i = tid; i < heads * quarter; i += PT_CONSUMERS) {
                     const int h = i / quarter, d = (i - h * quarter) * 4;
@@ -776,9 +794,6 @@ wf_status launch_paged_token(const wf_paged_cache* c, const wf_paged_attn_args* 
     while ((1 << p.page_shift) < c->page_size) ++p.page_shift;
     p.num_pages = c->num_pages;
     p.max_pages = c->max_pages;
-    // shortest stretch, one user at 2,048 positions: 1 tile 10.85 us, 2 11.92, 3 10.87,
-    // 4 13.3, 6 14.9; of the equals the one that leaves fewer pieces
-    p.min_tiles = 3;
     p.ctrl = static_cast<Control*>(ws);
     p.timeout_ns = wait_timeout_ns();
     const int vi = (e4m3 ? 1 : 0) | (sixteen ? 2 : 0) | (c->D > 64 ? 4 : 0);
