@@ -541,8 +541,9 @@ WF_API wf_status wf_paged_append(const wf_paged_cache* cache, int layer, const u
  * weight of 0.
  * A masked position never reaches a row, whatever it holds; positions from
  * cache_len[b] + rows on are not read.  fp32 softmax statistics and sums; the
- * probabilities enter the product with V rounded to the 16-bit type of the
- * matrix instruction (bf16; fp16 for WF_KV_E4M3).  The result does not depend
+ * probabilities enter the product with V in the 16-bit type of the matrix
+ * instruction, fp16 for WF_KV_E4M3, else bf16: rounded to one such number, for
+ * max_rows = 1 over bf16 to the sum of two.  The result does not depend
  * on timing (splits of a long cache are joined in order).
  * A sequence with a parent outside [-1, i), more than max_rows rows, a
  * negative length, or a position without a page sets WF_ERR_BAD_DATA

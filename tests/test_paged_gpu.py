@@ -992,3 +992,46 @@ def test_compact_refuses_a_first_row_without_a_page(in_place):
     assert code == BAD and info in (0, 1)
     assert np.array_equal(host(new), [-1, -1, 9, 16])
     assert torch.equal(cache.K.cpu().view(torch.int16), c.K.view(torch.int16))
+
+
+@pytest.mark.parametrize("H,G,D,n", [(8, 2, 128, 700), (4, 4, 64, 90), (32, 2, 80, 3000), (12, 1, 128, 500)])
+def test_single_tokens_weigh_values_to_more_than_16_bits(H, G, D, n):
+    """Weights over a bf16 cache: 2^-14 of each off (a product of 2^-8 by the 2^-7 + 2^-9 that the first of its two
+    numbers leaves), beside the scores' and sums' fp32 and the output's one rounding."""
+    c = ref.Case(77, (n,), (1,), H, G, D, 16)
+    out, lse = check(c)
+    scale, hq = D ** -0.5, H // G
+    for h in range(H):
+        K, V, x = c.dense(0, h // hq, "K"), c.dense(0, h // hq, "V"), c.q[0, h].double().numpy()
+        s = scale * (K @ x)
+        w = np.exp(s - s.max())
+        w /= w.sum()
+        ds = scale * D * ref.FP32 * (np.abs(K) @ np.abs(x)).max() + 2.0 ** -22 * np.abs(s).max()
+        rel = 2.0 ** -14 + 2 * ds + 2.0 ** -20 + 2 * (n + 1) * ref.FP32
+        o, mass = w @ V, w @ np.abs(V)
+        assert np.all(np.abs(out[0, h] - o) <= rel * mass + ref.BF16 * (np.abs(o) + rel * mass)), h
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_infinite_values_that_a_single_token_sees(kv):
+    """An infinite value is the output's infinity in its dim, at any weight above zero, and in no other dim."""
+    c = ref.Case(78, (400, 30), (1, 1), 8, 2, 64, 16, kv)
+    clean = ref.attention(c, 0.125)
+    K = c.dense(0, 1, "K")
+    s = K @ c.q[0, 4].double().numpy()
+    for t in (int(s.argmax()), int(s.argmin()), 0, 400):     # the largest weight (1 before the sum), the least, the ends
+        V = c.V.clone()
+        spot = V[0, c.table[0, t // 16], t % 16, 1]
+        spot[3], spot[9] = (float("inf"), float("-inf")) if kv == "bf16" else (float("nan"),) * 2
+        was, c.V = c.V, V
+        out, lse, ws = run_attention(c)
+        c.V = was
+        assert ws.device_error() == (0, 0)
+        hit = np.zeros(out.shape, bool)
+        hit[0, 4:, [3, 9]] = True
+        assert np.all(np.abs(out - clean[0])[~hit] <= clean[2][~hit])
+        assert np.all(np.abs(lse - clean[1]) <= clean[3])
+        if kv == "bf16":
+            assert (out[0, 4:, 3] == np.inf).all() and (out[0, 4:, 9] == -np.inf).all()
+        else:
+            assert np.isnan(out[hit]).all()
