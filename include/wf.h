@@ -477,7 +477,10 @@ WF_API wf_status wf_catchup(const wf_catchup_args* args, void* ws, size_t ws_byt
  *
  * A page is free when its reference count is 0.  Pages are only written
  * through sequences that hold them alone: call wf_pages_reserve for a round's
- * rows before wf_paged_append writes them.
+ * rows before wf_paged_append writes them.  A sequence that it could not serve
+ * (added = -1) takes no part in the round: where the cache has reference
+ * counts, wf_paged_append and wf_paged_compact refuse to write to a page with a
+ * count above 1.
  */
 #define WF_KV_BF16 0
 #define WF_KV_E4M3 1   /* 8-bit values (4 exponent, 3 mantissa bits, largest 448) times an fp32 scale */
@@ -490,7 +493,8 @@ typedef struct wf_paged_cache {
     const float* k_scale;      /* [layers, G] fp32 > 0: key = stored value * scale (WF_KV_E4M3; NULL = 1) */
     const float* v_scale;      /* same, for the values */
     int32_t* table;            /* [B, max_pages] page of each block of positions, -1 = none */
-    int32_t* ref;              /* [num_pages] sequences that hold each page (wf_pages_*; else may be NULL) */
+    int32_t* ref;              /* [num_pages] sequences that hold each page (wf_pages_*; else may be NULL:
+                                  no page is shared) */
     int kv_type;               /* WF_KV_BF16 or WF_KV_E4M3 */
     int layers, num_pages;     /* num_pages * page_size < 2^31 - 4096 */
     int page_size;             /* a power of two, 8 .. 1024 */
@@ -518,7 +522,8 @@ WF_API size_t wf_paged_workspace_bytes(int B, int H, int G, int D, int max_rows)
  * stores x / scale, saturated to +-448 and rounded to the nearest value (ties
  * to even; NaN stays NaN).  Rows outside [pos_off[0], pos_off[B]) are not read
  * and no other position is written.  A position without a page (or past
- * max_pages) sets WF_ERR_BAD_DATA (info = b) and its row is dropped.
+ * max_pages), or in a page that another sequence holds too, sets
+ * WF_ERR_BAD_DATA (info = b) and its row is dropped.
  */
 WF_API wf_status wf_paged_append(const wf_paged_cache* cache, int layer, const uint16_t* k, int64_t k_stride,
                                  const uint16_t* v, int64_t v_stride, int P, const int32_t* pos_off,
@@ -578,8 +583,9 @@ WF_API wf_status wf_paged_attention(const wf_paged_cache* cache, const wf_paged_
  * path_stride (0 .. WF_MAX_SEQ_NODES; an n_accept past it is taken as
  * path_stride; -1 keeps no row: new_len = cache_len).  new_len [B] device
  * int32 out, may be cache_len itself.  A path that does not increase, or a
- * first row or path row (read or written) without a page, sets WF_ERR_BAD_DATA
- * (info = b), moves nothing and writes new_len[b] = -1.
+ * first row or path row (read or written) without a page, or a row to move into
+ * a page that another sequence holds too, sets WF_ERR_BAD_DATA (info = b),
+ * moves nothing and writes new_len[b] = -1.
  */
 WF_API wf_status wf_paged_compact(const wf_paged_cache* cache, const int32_t* n_accept, const int32_t* path,
                                   int path_stride, const int32_t* cache_len, int32_t* new_len, void* ws,

@@ -41,6 +41,7 @@ struct AppendParams {
     const int32_t* pos_off;
     const int32_t* cache_len;
     const int32_t* table;
+    const int32_t* ref;           // or null
     uint8_t* K;                   // this layer's rows
     uint8_t* V;
     const float* k_scale;         // this layer's [G] scales, or null
@@ -100,7 +101,10 @@ __global__ void __launch_bounds__(AP_WARPS * 32) append_kernel(const AppendParam
             int page = -1;
             if (len >= 0 && (t >> p.page_shift) < p.max_pages)
                 page = p.table[(int64_t)b * p.max_pages + (t >> p.page_shift)];
-            if (page < 0 || page >= p.num_pages) {
+            // A page that others hold too may have their rows where this one goes.  (The
+            // count is one more dependent load: 22.9 us against 22.1 for 256 trees, 4.1
+            // against 3.9 for a chain.)
+            if (page < 0 || page >= p.num_pages || (p.ref && p.ref[page] > 1)) {
                 if (lane == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)b);
                 return;
             }
@@ -138,6 +142,7 @@ struct CompactParams {
     uint8_t* K;
     uint8_t* V;
     const int32_t* table;
+    const int32_t* ref;           // or null
     const int32_t* n_accept;
     const int32_t* path;
     const int32_t* cache_len;
@@ -179,6 +184,8 @@ __global__ void __launch_bounds__(CP_THREADS) compact_kernel(const CompactParams
             same = s == tid;
             const int64_t from = row_of((int64_t)len + 1 + s), to = row_of((int64_t)len + 1 + tid);
             bad = from < 0 || to < 0;
+            // rows are moved within pages that the sequence holds alone
+            if (!bad && !same && p.ref) bad = p.ref[to >> p.page_shift] > 1;
             s_src[tid] = (int)from;
             s_dst[tid] = (int)to;
         }
@@ -586,6 +593,7 @@ wf_status launch_paged_append(const wf_paged_cache* c, int layer, const uint16_t
     p.pos_off = pos_off;
     p.cache_len = cache_len;
     p.table = c->table;
+    p.ref = c->ref;
     p.K = static_cast<uint8_t*>(c->K) + layer * layer_bytes;
     p.V = static_cast<uint8_t*>(c->V) + layer * layer_bytes;
     p.k_scale = c->k_scale ? c->k_scale + (int64_t)layer * c->G : nullptr;
@@ -609,6 +617,7 @@ wf_status launch_paged_compact(const wf_paged_cache* c, const int32_t* n_accept,
     p.K = static_cast<uint8_t*>(c->K);
     p.V = static_cast<uint8_t*>(c->V);
     p.table = c->table;
+    p.ref = c->ref;
     p.n_accept = n_accept;
     p.path = path;
     p.cache_len = cache_len;

@@ -1035,3 +1035,40 @@ def test_infinite_values_that_a_single_token_sees(kv):
             assert (out[0, 4:, 3] == np.inf).all() and (out[0, 4:, 9] == -np.inf).all()
         else:
             assert np.isnan(out[hit]).all()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "e4m3"])
+def test_shared_pages_are_not_written(kv):
+    """A reserve that finds no page leaves a sequence on shared pages; the round's append and compaction leave those
+    pages to the others, whose rows they hold."""
+    ps, G, D = 8, 1, 16
+    c = ref.Case(79, (13, 20), (6, 2), G, G, D, ps, kv, layers=2)
+    table = np.full((2, 5), -1, np.int32)
+    table[0, :2], table[1, :3] = [4, 1], [4, 1, 2]           # two pages in common; the first is shorter by 7 rows
+    refs = np.array([1, 2, 1, 1, 2], np.int32)               # none is free
+    cache = wf.PagedCache(c.K[:, :5].contiguous().to(DEV), c.V[:, :5].contiguous().to(DEV), dev(table), ref=dev(refs),
+                          k_scale=dev(c.k_scale) if kv == "e4m3" else None,
+                          v_scale=dev(c.v_scale) if kv == "e4m3" else None)
+    was = [x.clone().view(torch.uint8) for x in (cache.K, cache.V)]
+    ws = wf.PagedWorkspace(2, G, G, D)
+    pos, ln = dev(np.array([0, 3, 5], np.int32)), dev(np.array([13, 20], np.int32))
+    added = wf.wf_pages_reserve(cache, pos, ln, ws)
+    assert host(added).tolist() == [-1, -1] and ws.device_error() == (0, 0)
+    x = torch.randn((5, G, D), device=DEV).to(torch.bfloat16)
+    wf.wf_paged_append(cache, x, x, pos, ln, ws, layer=1)
+    torch.cuda.synchronize()
+    assert ws.device_error() == (BAD, 0)
+    # the first sequence's rows are dropped, the second's are in its own page
+    t1 = [int(table[1, t // ps]) * ps + t % ps for t in (20, 21)]
+    for pool, w in ((cache.K, was[0]), (cache.V, was[1])):
+        left = torch.ones(5 * ps, dtype=torch.bool)
+        left[t1] = False
+        got, want = pool.view(torch.uint8).view(2, 5 * ps, -1).cpu(), w.view(2, 5 * ps, -1).cpu()
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1][left], want[1][left])
+        assert not torch.equal(got[1][t1], want[1][t1])
+    was = [x_.clone().view(torch.uint8) for x_ in (cache.K, cache.V)]
+    n, path = dev(np.array([1, 1], np.int32)), dev(np.array([[1, -1], [0, -1]], np.int32))
+    new = wf.wf_paged_compact(cache, n, path, ln, ws)
+    assert host(new).tolist() == [-1, 22] and ws.device_error() == (BAD, 0)
+    for pool, w in zip((cache.K, cache.V), was):
+        assert torch.equal(pool.view(torch.uint8), w)
