@@ -522,8 +522,8 @@ WF_API size_t wf_paged_workspace_bytes(int B, int H, int G, int D, int max_rows)
  * stores x / scale, saturated to +-448 and rounded to the nearest value (ties
  * to even; NaN stays NaN).  Rows outside [pos_off[0], pos_off[B]) are not read
  * and no other position is written.  A position without a page (or past
- * max_pages), or in a page that another sequence holds too, sets
- * WF_ERR_BAD_DATA (info = b) and its row is dropped.
+ * max_pages), or in a page that another sequence holds too, a negative length
+ * or first row sets WF_ERR_BAD_DATA (info = b) and the row is dropped.
  */
 WF_API wf_status wf_paged_append(const wf_paged_cache* cache, int layer, const uint16_t* k, int64_t k_stride,
                                  const uint16_t* v, int64_t v_stride, int P, const int32_t* pos_off,

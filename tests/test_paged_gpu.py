@@ -1072,3 +1072,18 @@ def test_shared_pages_are_not_written(kv):
     assert host(new).tolist() == [-1, 22] and ws.device_error() == (BAD, 0)
     for pool, w in zip((cache.K, cache.V), was):
         assert torch.equal(pool.view(torch.uint8), w)
+
+
+@pytest.mark.parametrize("first", [-1, -5, -2 ** 31 + 40, -2 ** 31])
+def test_append_behind_a_negative_first_row(first):
+    """Offsets that no batch has: the rows are dropped and told of, at whatever distance from the first."""
+    c = ref.Case(80, (30, 9), (4, 4), 2, 2, 32, 16)
+    cache, ws = cache_of(c), wf.PagedWorkspace(2, 2, 2, 32)
+    x = torch.randn((8, 2, 32), device=DEV).to(torch.bfloat16)
+    wf.wf_paged_append(cache, x, x, dev(np.array([first, 4, 8], np.int64).astype(np.int32)),
+                       dev(np.array(c.lens, np.int32)), ws)
+    torch.cuda.synchronize()
+    assert ws.device_error() == (BAD, 0)
+    want = c.K.clone()
+    want[0, c.table[1, 0], 9:13] = x[4:].cpu()
+    assert torch.equal(cache.K.cpu().view(torch.int16), want.view(torch.int16))
