@@ -520,8 +520,9 @@ WF_API size_t wf_paged_workspace_bytes(int B, int H, int G, int D, int max_rows)
  * row to row (a multiple of 8, from G * D to 2^30: slices of one projection's
  * output are fine); pos_off [B+1], cache_len [B] device int32.  WF_KV_E4M3
  * stores x / scale, saturated to +-448 and rounded to the nearest value (ties
- * to even; NaN stays NaN).  Rows outside [pos_off[0], pos_off[B]) are not read
- * and no other position is written.  A position without a page (or past
+ * to even; NaN stays NaN).  Rows outside [pos_off[0], pos_off[B]) may be read
+ * (all P have to be readable memory) and change nothing; no other position is
+ * written.  A position without a page (or past
  * max_pages), or in a page that another sequence holds too, a negative length
  * or first row sets WF_ERR_BAD_DATA (info = b) and the row is dropped.
  */
@@ -544,8 +545,10 @@ WF_API wf_status wf_paged_append(const wf_paged_cache* cache, int layer, const u
  *   lse[row, h] = log sum_t e^(s_t)                                  (fp32, natural log)
  * Scores, also times log2(e), have to lie in fp32's range; one of -inf is a
  * weight of 0.
- * A masked position never reaches a row, whatever it holds; positions from
- * cache_len[b] + rows on are not read.  fp32 softmax statistics and sums; the
+ * A masked position never reaches a row, whatever it holds, nor does one from
+ * cache_len[b] + rows on (they may be read, to the end of their page).  A row's
+ * bits depend on its own sequence and on how the batch's lengths split it, not
+ * on other rows' queries or on what ran before.  fp32 softmax statistics and sums; the
  * probabilities enter the product with V in the 16-bit type of the matrix
  * instruction, fp16 for WF_KV_E4M3, else bf16: rounded to one such number, for
  * max_rows = 1 over bf16 to the sum of two.  The result does not depend

@@ -29,8 +29,8 @@ static int log2_of(int page_size) {
 // ------------------------------------------------------------------ append
 // One warp per row: the row's keys and values are loaded (eight 16-byte pieces
 // a lane in flight) before the lane knows where they go; the sequence search
-// and the page lookup run meanwhile.  256 trees of 61 rows of 8 x 128: 22 us, 85%
-// of the copy rate; 17 rows: 4 us, a launch.
+// and the page lookup run meanwhile.  256 trees of 61 rows of 8 x 128: 22.7 us,
+// 83% of the copy rate; 17 rows: 4.1 us, a launch.
 constexpr int AP_WARPS = 8;
 constexpr int AP_UNROLL = 8;
 
@@ -133,7 +133,7 @@ __global__ void __launch_bounds__(AP_WARPS * 32) append_kernel(const AppendParam
 // the path increases, a destination (row j) never lies past its own source
 // (row path[j] >= j) and so never on a later source: within a thread the moves
 // are safe in place, and threads share no byte.  48 trees' accepted rows in 32
-// layers: 19 us, 76% of the copy rate; one user's 2.9 us, a launch.
+// layers: 19 us, 76% of the copy rate; one user's 3.0 us, a launch.
 constexpr int CP_THREADS = 256;
 constexpr int CP_BATCH = 8;
 static_assert(WF_MAX_SEQ_NODES <= CP_THREADS, "one path entry a thread");

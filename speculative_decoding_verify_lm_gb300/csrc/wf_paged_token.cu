@@ -31,9 +31,9 @@
 // unless one has outgrown it.
 //
 // What it reaches, in copy rates (6.8 TB/s): 91% on one sequence of 131,000
-// positions (87 us), 95% on 64 of 100 to 16,384 (157 us), 83% on 128 of 2,000 to
-// 6,000 over 8-bit (174 us), where the conversions and products fill the
-// computing warps' issue slots.  One user at 2,048 positions: 10.9 us of latency.
+// positions (87 us), 93% on 64 of 100 to 16,384 (159 us), 83% on 128 of 2,000 to
+// 6,000 over 8-bit (175 us), where the conversions and products fill the
+// computing warps' issue slots.  One user at 2,048 positions: 11.1 us of latency.
 #include "wf_paged.cuh"
 
 #define PT_TRY(x)                      \
@@ -393,7 +393,9 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
                         // fp16 operands.  A position's four bytes cq * 4 .. + 3 of a 16-byte
                         // piece stand for the inner indices 2 cq, + 1, + 8, + 9, so the
                         // queries are taken in that order.  Each head is scaled by a power of
-                        // two that puts its largest element in [1, 2): exact, and undone in fp32.
+                        // two that puts its largest element in [1, 2), undone in fp32: exact down
+                        // to 2^-14 of that, off by at most 2^-25 of the largest below (fp16's
+                        // least step), the order of the fp32 sums' own rounding.
                         float big = 0.f;
                         auto lo = [](uint32_t w) { return pg_bf16_to_f32(w & 0xFFFFu); };
                         auto hi = [](uint32_t w) { return pg_bf16_to_f32(w >> 16); };
