@@ -225,7 +225,11 @@ __global__ void __launch_bounds__(CP_THREADS) compact_kernel(const CompactParams
 // One CTA decides.  A thread owns whole sequences; the free pages are found
 // 16,384 counts at a time, their numbers kept in shared memory.  A chain of
 // dependent loads bounds it, so the first counts are read while the sequences
-// are, and what a sequence needs stays in shared memory.
+// are, and what a sequence needs stays in shared memory.  Pools whose free pages
+// lie far up cost a look at every chunk below, and one more to hand them out if
+// several chunks hold them: 12.7 us (with the copies' launch) where the first
+// chunk has enough, whatever the pool, 25 where they are the last of 40,000 pages,
+// 60 of 150,000.
 //
 // Copy on write in sequence order without an ordered pass: every holder that
 // is about to write takes its reference away; a page whose count reaches 0 has
