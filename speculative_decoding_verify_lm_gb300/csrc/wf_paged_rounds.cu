@@ -401,8 +401,9 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             const int place = at % PLACES;
             uint64_t* full = E4M3 ? &raw_full[place] : &kv_full[place];
             const int row_bytes = E4M3 ? p.D : BLK * 128;
+            // a lane's copies may count before these bytes are expected: the phase waits for
+            // this arrival
             if (lane == 0) mbar_arrive_expect_tx(full, boxes * p.box_rows * row_bytes);
-            __syncwarp();
             if (ok && E4M3) {
                 tma_load_2d(sW + place * S::RAW_TILE + lane * p.box_rows * p.D, kv ? &tmV : &tmK, full, x.g * p.D, y,
                             pol);
@@ -420,6 +421,10 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
         auto landed = [&](int at) {
             mbar_wait(E4M3 ? &raw_full[at % PLACES] : &kv_full[at % PLACES], (at / PLACES) & 1, p.timeout_ns, nullptr);
         };
+        // A warp that goes on together gives up together, whatever each lane's last look
+        // at the barrier, the abort flag and the clock was: left to the lanes, some could
+        // leave while the others wait for them in the next shuffle.
+        auto whole_warp = [](bool got) { return __all_sync(0xffffffffu, got) != 0; };
         if (warp == SOFT) {
             // ---------------------------------------- copies: a tile's keys, then its values, to the ring's next places
             auto inclusive = [&](int64_t v) {
@@ -522,7 +527,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             }
             int sent = 0, last = -1, k = 0;   // places of the tiles before, the last place filled; pieces' queries
             for (int turn = 0;; ++turn) {
-                if (turn >= 8 && !mbar_wait(&piece_free[turn & 7], ((turn >> 3) & 1) ^ 1, p.timeout_ns, abort_flag)) {
+                if (!whole_warp(turn < 8 || mbar_wait(&piece_free[turn & 7], ((turn >> 3) & 1) ^ 1, p.timeout_ns, abort_flag))) {
                     *abort_flag = 1;
                     if (lane == 0) record_error(p.ctrl, WF_ERR_TIMEOUT, 0x801u);
                     break;
@@ -555,7 +560,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
 #pragma unroll
                         for (int kv = 0; kv < 2; ++kv) {
                             if (kv == 1 && i == 0) {   // the piece's queries, behind its first keys
-                                alive = alive && (k == 0 || mbar_wait(&q_empty, (k & 1) ^ 1, p.timeout_ns, abort_flag));
+                                alive = alive && whole_warp(k == 0 || mbar_wait(&q_empty, (k & 1) ^ 1, p.timeout_ns, abort_flag));
                                 if (!alive) break;
                                 const int nq = x.solo ? 1 : 2;
                                 if (lane == 0) {
@@ -571,7 +576,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                             // the raw tiles' turn for an 8-bit cache, else the ring's
                             const int at = sent + kv;
                             if (kv == 1 && COPIES == 2) break;   // the other copying warp's
-                            alive = alive && place_free(at);
+                            alive = alive && whole_warp(place_free(at));
                             if (!alive) break;
                             load(kv, at, x, ok, y, boxes);
                             last = at;
@@ -591,7 +596,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                         mbar_arrive(&told[(k - 1) & 7]);
                     }
                 }
-                if (*abort_flag) break;
+                if (!whole_warp(!*abort_flag)) break;
                 next_item();
             }
             // let every copy issued land before the shared memory goes
@@ -603,7 +608,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             int n = 0, last = -1;   // tiles before this piece, the last place filled
             bool ok = true;
             for (int turn = 0; ok; ++turn) {
-                ok = __all_sync(0xffffffffu, mbar_wait(&piece_ready[turn & 7], (turn >> 3) & 1, p.timeout_ns, abort_flag));
+                ok = whole_warp(mbar_wait(&piece_ready[turn & 7], (turn >> 3) & 1, p.timeout_ns, abort_flag));
                 if (!ok) break;
                 const Piece& x = s_piece[turn & 7];
                 if (x.tiles == 0) break;
@@ -615,7 +620,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                     const uint32_t boxes = (uint32_t)__popc(__ballot_sync(0xffffffffu, in));
                     if (i + 1 < tiles) page = page_of(x, x.kt + i + 1);
                     const int at = 2 * (n + i) + 1;
-                    ok = __all_sync(0xffffffffu, place_free(at));
+                    ok = whole_warp(place_free(at));
                     if (!ok) break;
                     load(1, at, x, in, y, boxes);
                     last = at;
@@ -643,7 +648,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                 const bool swap = c & 4;
                 for (int turn = 0; ok; ++turn) {
                     wait(&piece_ready[turn & 7], (turn >> 3) & 1);
-                    ok = __all_sync(0xffffffffu, ok);
+                    ok = whole_warp(ok);
                     if (!ok) break;
                     const int tiles = s_piece[turn & 7].tiles;
                     if (tiles == 0) break;
@@ -652,7 +657,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                         const int at = 2 * n + i, raw = at % RAW, slot = at % RING;
                         wait(&raw_full[raw], (at / RAW) & 1);
                         if (at >= RING) wait(&kv_empty[slot], ((at / RING) & 1) ^ 1);
-                        ok = __all_sync(0xffffffffu, ok);
+                        ok = whole_warp(ok);
                         if (!ok) break;
                         const uint8_t* src = sW + raw * S::RAW_TILE;
                         uint8_t* dst = sR + slot * TILE;
@@ -716,13 +721,13 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             // tensor cores finish one stream early and the streams fall out of step
             // (interleaved, both finish late and then both wait for exponentials).
             auto take_turn = [&]() {
-                ok = __all_sync(0xffffffffu, ok);
+                ok = whole_warp(ok);
                 if (ok && lane == 0 && atomicCAS(&s_turn, 0, 1) != 0) {
                     const uint64_t start = globaltimer_ns();
                     while (ok && atomicCAS(&s_turn, 0, 1) != 0)
                         ok = !*abort_flag && globaltimer_ns() - start <= p.timeout_ns;
                 }
-                ok = __all_sync(0xffffffffu, ok);
+                ok = whole_warp(ok);
             };
             auto give_turn = [&]() {
                 __syncwarp();
@@ -730,7 +735,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
             };
             for (int turn = 0; ok; ++turn) {
                 wait(&piece_ready[turn & 7], (turn >> 3) & 1);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = whole_warp(ok);
                 if (!ok) break;
                 const Piece& x = s_piece[turn & 7];
                 const int tiles = x.tiles;
@@ -760,6 +765,7 @@ __global__ void __launch_bounds__(RoundsShape<BLK, E4M3>::THREADS, 1)
                     };
                     wait(E4M3 ? &q_ready[w] : &q_full, qn++ & 1);
                     if (steps == 0) {
+                        ok = whole_warp(ok);
                         if (lane == 0) mbar_arrive(&q_empty);
                     } else {
                         arrived(place_of(0));

@@ -292,8 +292,9 @@ __global__ void __launch_bounds__(PT_THREADS, TokenShape<DP, E4M3, NH>::PER_SM) 
                 if (++c.kt == c.w.nt) token_next_item<KT>(p, c);
                 look_up();
             }
-            if (n >= S::STAGES &&
-                !mbar_wait(&s_empty[stage], ((n / S::STAGES) & 1) ^ 1, p.timeout_ns, abort_flag)) {
+            // the lanes give up together: the others would wait for those that left
+            if (!__all_sync(0xffffffffu, n < S::STAGES || mbar_wait(&s_empty[stage], ((n / S::STAGES) & 1) ^ 1,
+                                                                    p.timeout_ns, abort_flag))) {
                 *abort_flag = 1;
                 if (lane == 0) record_error(p.ctrl, WF_ERR_TIMEOUT, 0x700u);
                 break;

@@ -65,6 +65,21 @@ def test_paged_kernels_take_only_scales_for_constant(name):
         assert re.match(r"(p\.[kv]_scale|sc) \+", arg), arg
 
 
+def test_the_lanes_of_a_warp_give_up_together():
+    """The copying warps exchange values between their lanes: a wait that gives up has to end for all of them or for
+    none, or those that stay wait for those that left without a limit."""
+    for name in ("wf_paged_rounds.cu", "wf_paged_token.cu"):
+        text = re.sub(r"//[^\n]*", "", source(name))
+        text = text.replace("whole_warp(", "__all_sync(0xffffffffu, ")
+        for barrier in ("piece_free", "q_empty", "s_empty"):
+            for wait in re.finditer(r"mbar_wait\(&%s\b" % barrier, text):
+                before = text[:wait.start()]
+                assert "__all_sync" in before[before.rindex("\n", 0, before.rindex("\n")):] , (name, barrier)
+        calls = [m.start() for m in re.finditer(r"(?<!auto )\bplace_free\(at\)", text)]
+        for at in calls:
+            assert text[:at].endswith("__all_sync(0xffffffffu, "), name
+
+
 @pytest.mark.parametrize("name", ["wf_gemm_select.cu", "wf_catchup.cu", "wf_paged_rounds.cu"])
 def test_a_wait_that_gives_up_lets_its_products_complete(name):
     """When a wait gives up the CTA frees its tensor memory and leaves.  Products of the tensor cores still in flight
