@@ -533,7 +533,7 @@ wf_status wf_paged_attention(const wf_paged_cache* c, const wf_paged_attn_args* 
     // one row a sequence: the kernel for single tokens, bound by the cache's bytes;
     // drafted rows: the tensor-core one, which shares a read of the cache among them
     // (single tokens through it: 13.4 us against 11.1 for one user, 94 against 90 for
-    // one long sequence, 460 against 177 over an 8-bit cache)
+    // one long sequence, 460 against 171 over an 8-bit cache)
     return a->max_rows == 1 ? launch_paged_token(c, a, ws, stream) : launch_paged_rounds(c, a, ws, stream);
 }
 

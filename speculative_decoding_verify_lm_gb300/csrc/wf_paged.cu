@@ -29,8 +29,8 @@ static int log2_of(int page_size) {
 // ------------------------------------------------------------------ append
 // One warp per row: the row's keys and values are loaded (eight 16-byte pieces
 // a lane in flight) before the lane knows where they go; the sequence search
-// and the page lookup run meanwhile.  256 trees of 61 rows of 8 x 128: 22.7 us,
-// 83% of the copy rate; 17 rows: 4.1 us, a launch.
+// and the page lookup run meanwhile.  256 trees of 61 rows of 8 x 128: 22.9 us,
+// 82% of the copy rate; 17 rows: 4.2 us, a launch.
 constexpr int AP_WARPS = 8;
 constexpr int AP_UNROLL = 8;
 
@@ -102,8 +102,8 @@ __global__ void __launch_bounds__(AP_WARPS * 32) append_kernel(const AppendParam
             if (len >= 0 && first >= 0 && (t >> p.page_shift) < p.max_pages)
                 page = p.table[(int64_t)b * p.max_pages + (t >> p.page_shift)];
             // A page that others hold too may have their rows where this one goes.  (The
-            // count is one more dependent load: 22.9 us against 22.1 for 256 trees, 4.1
-            // against 3.9 for a chain.)
+            // count is one more dependent load: 22.9 us against 22.2 for 256 trees, 4.2
+            // against 4.0 for a chain.)
             if (page < 0 || page >= p.num_pages || (p.ref && p.ref[page] > 1)) {
                 if (lane == 0) record_error(p.ctrl, WF_ERR_BAD_DATA, (uint32_t)b);
                 return;

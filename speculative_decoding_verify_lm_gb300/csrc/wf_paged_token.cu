@@ -31,9 +31,9 @@
 // unless one has outgrown it.
 //
 // What it reaches, in copy rates (6.8 TB/s): 91% on one sequence of 131,000
-// positions (87 us), 93% on 64 of 100 to 16,384 (159 us), 83% on 128 of 2,000 to
-// 6,000 over 8-bit (175 us), where the conversions and products fill the
-// computing warps' issue slots.  One user at 2,048 positions: 11.1 us of latency.
+// positions (87 us), 94% on 64 of 100 to 16,384 (159 us), 85% on 128 of 2,000 to
+// 6,000 over 8-bit (171 us), where the conversions and products fill the
+// computing warps' issue slots.  One user at 2,048 positions: 11.0 us of latency.
 #include "wf_paged.cuh"
 
 #define PT_TRY(x)                      \
