@@ -15,6 +15,10 @@
  *   wf_router_mlp     neural router f_theta and the threshold decision
  *   wf_draft_topk     EAGLE-3 draft head, top-k, draft-to-target id map
  *   wf_lmhead_draft_topk  the target and draft heads in one weight sweep
+ *   wf_lmhead_logprobs  log-probabilities of given tokens under the target head,
+ *                     entropy, best alternatives
+ *   wf_draft_distill  the draft head's loss against a teacher's top logits
+ *                     (wf_draft_distill_grad: its gradients)
  *   wf_round          all of the above as one stream-ordered round
  *   wf_catchup        KV-only catch-up of the EAGLE-3 drafter after a switch
  *   wf_paged_*        a round's rows over a paged key-value cache: keys and
@@ -352,6 +356,98 @@ WF_API wf_status wf_lmhead_draft_topk(const uint16_t* hidden, const uint16_t* W,
                                const int32_t* d2t, int B, int Vd, int k, int32_t* draft_ids,
                                int32_t* tids, float* vals, float* lse, void* ws, size_t ws_bytes,
                                wf_stream_t stream);
+
+/* Longest list of given tokens, or of a teacher's alternatives, of one row. */
+#define WF_MAX_LISTED 64
+
+/*
+ * Log-probabilities under the target head: what the target gives to tokens that
+ * were drafted, sampled or read, how sure it is, and its best alternatives (the
+ * data that a drafter is distilled from).  The pages verify greedily and need
+ * none of this; no passage corresponds to the call.  Per row p, with
+ *   z_v = <hidden[p], W_v> / temperature
+ *   lse[p]        = log sum_v e^(z_v)
+ *   logp[p, s]    = z_(tok[p, s]) - lse[p]
+ *   H[p]          = entropy of softmax(z)                       (natural log)
+ *   top_ids[p, j] = the k ids of largest <hidden[p], W_v>, best first, the lower
+ *                   id on a tie;  top_logp[p, j] = their z - lse[p]
+ * Logits are accumulated in fp32 on the tensor cores and never stored; a given
+ * token's logit has the same bits as an alternative's.  Logits, also divided by
+ * the temperature and times log2(e), have to lie in fp32's range; a row with a
+ * NaN among them has NaN results, and a NaN is no alternative (top_ids -1).
+ * A tok of -1 is a place without a token: its logp is 0.  Any other id outside
+ * [0, V) sets WF_ERR_BAD_DATA (info = p) and its logp is NaN.
+ * Results do not depend on timing.
+ */
+typedef struct wf_logprobs_args {
+    const uint16_t* hidden;    /* [P, d] bf16 bits */
+    const uint16_t* W;         /* [V, d] bf16 bits */
+    int P, d, V;               /* 1 <= P, d % 8 == 0, 8 <= d <= 16384, 1 <= V < 2^31 - 256 */
+    float temperature;         /* > 0, its reciprocal finite and > 0 */
+    const int32_t* tok;        /* [P, S] or NULL */
+    int S;                     /* 1 .. WF_MAX_LISTED (0 if tok is NULL) */
+    int k;                     /* 0 .. WF_MAX_TOPK, at most V */
+    float* logp;               /* [P, S] (with tok) */
+    float* lse;                /* [P] or NULL */
+    float* H;                  /* [P] or NULL */
+    int32_t* top_ids;          /* [P, k] or NULL */
+    float* top_logp;           /* [P, k] or NULL; with k > 0 one of the two */
+} wf_logprobs_args;
+/* Workspace (bytes); 0 if the shapes are out of range.  These workspaces are for
+ * their own calls (with any shapes that they are large enough for). */
+WF_API size_t wf_logprobs_workspace_bytes(int P, int d, int V, int S, int k);
+WF_API wf_status wf_lmhead_logprobs(const wf_logprobs_args* args, void* ws, size_t ws_bytes, wf_stream_t stream);
+
+/*
+ * Distillation of the draft head (wf_draft_topk's Wd) from a teacher's top
+ * logits: how far the drafter's next-token distribution is from the target's
+ * decides how much of a draft is accepted.  The pages take trained drafters as
+ * given; no passage corresponds to these calls.  Row n, draft ids v < Vd:
+ *   z[n, v] = <x[n], Wd_v> / temperature,  q = softmax(z[n])
+ *   p_j     = softmax over the row's kept alternatives of tlogit[n, j] / temperature
+ *   loss[n] = sum_j p_j (log p_j - log q_(id_j))
+ *   lse[n]  = log sum_v e^(z[n, v])
+ * An alternative is kept if its id is not -1, has a draft id (t2d, where given)
+ * and its logit is not -inf; what else the places of the others hold has no say.
+ * Entries of one row that name the same id add up their p.  A row without a kept
+ * alternative has loss 0 and no gradient.  An id outside [0, V) (or, without t2d,
+ * [0, Vd)), or a t2d entry of Vd or more, sets WF_ERR_BAD_DATA (info = n): the
+ * row's loss is NaN and it has no gradient.  fp32 softmax statistics and sums;
+ * z has to lie in fp32's range, also times log2(e).
+ *
+ * wf_draft_distill writes loss and lse and, if z is given, the z[n, v] in fp32
+ * (columns from Vd, rounded up to 4, on are left as they are): 4 N Vd bytes that spare the
+ * gradients a second sweep of the head.  wf_draft_distill_grad takes that z and
+ * lse, the same x, Wd, teacher and temperature, and gloss[n] (the derivative of
+ * what is minimised by loss[n]; NULL = 1):
+ *   G[n, v] = gloss[n] / temperature (q_v - sum over j with id_j = v of p_j)
+ *   dx[n]   = sum_v G[n, v] Wd_v,   dWd_v = sum_n G[n, v] x[n]
+ * either output may be NULL, not both.  G is rounded to bf16 once, the sums are
+ * fp32 and rounded to bf16 at the end.  A row with gloss 0 adds nothing as long
+ * as its x is finite.  Results do not depend on timing.
+ */
+typedef struct wf_distill_args {
+    const uint16_t* x;         /* [N, d] bf16 bits, the drafter's hidden states */
+    const uint16_t* Wd;        /* [Vd, d] bf16 bits */
+    int N, d, Vd;              /* 1 <= N, d % 8 == 0, 8 <= d <= 16384, 1 <= Vd < 2^31 - 256 */
+    const int32_t* tid;        /* [N, k] ids of the teacher's alternatives, -1 = none: target ids if t2d is given */
+    const float* tlogit;       /* [N, k] their logits or log-probabilities */
+    int k;                     /* 1 .. WF_MAX_LISTED */
+    const int32_t* t2d;        /* [V] draft id of each target id, < 0 = none; or NULL: tid are draft ids */
+    int V;                     /* (0 if t2d is NULL) */
+    float temperature;         /* > 0, its reciprocal finite and > 0 */
+    float* z;                  /* [N, ldz] fp32, 16-byte aligned; wf_draft_distill: or NULL */
+    int64_t ldz;               /* a multiple of 4, from Vd to 2^34 */
+    float* lse;                /* [N]: out of wf_draft_distill, into wf_draft_distill_grad */
+    float* loss;               /* [N] (wf_draft_distill) */
+    const float* gloss;        /* [N] or NULL (wf_draft_distill_grad) */
+    uint16_t* dx;              /* [N, d] bf16 bits or NULL (wf_draft_distill_grad) */
+    uint16_t* dWd;             /* [Vd, d] bf16 bits or NULL (wf_draft_distill_grad) */
+} wf_distill_args;
+/* Workspace (bytes) of both calls, 2 N Vd and what the parts of split sums take; 0 if the shapes are out of range. */
+WF_API size_t wf_distill_workspace_bytes(int N, int d, int Vd, int k);
+WF_API wf_status wf_draft_distill(const wf_distill_args* args, void* ws, size_t ws_bytes, wf_stream_t stream);
+WF_API wf_status wf_draft_distill_grad(const wf_distill_args* args, void* ws, size_t ws_bytes, wf_stream_t stream);
 
 /*
  * One whole verify-and-route round (paper Sec. 3.2 - 3.3): LM-head argmax at

@@ -6,6 +6,7 @@
 #include <initializer_list>
 #include <mutex>
 
+#include "wf_heads.cuh"
 #include "wf_internal.cuh"
 #include "wf_merge.cuh"
 
@@ -62,6 +63,13 @@ wf_status launch_pages_fork(const wf_paged_cache* c, const int32_t* src, const i
 wf_status launch_pages_trim(const wf_paged_cache* c, const int32_t* cache_len, void* ws, cudaStream_t s);
 wf_status launch_paged_token(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s);
 wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s);
+
+size_t distill_grad_ldg(int Vd);
+size_t distill_part_bytes(int N, int d, int Vd);
+long distill_grad_units(int N, int d, int Vd);
+wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int N, int d, int Vd, int K, const float* z,
+                              int64_t ldz, const float* lse, const int32_t* ids, const float* p, const float* gs,
+                              uint16_t* dx, uint16_t* dWd, uint16_t* G, float* part, Control* ctrl, cudaStream_t s);
 
 static std::atomic<uint64_t> g_timeout_ns{2000000000ull};
 uint64_t wait_timeout_ns() { return g_timeout_ns.load(std::memory_order_relaxed); }
@@ -127,6 +135,76 @@ static wf_status check_ws(const void* ws, size_t ws_bytes, size_t need) {
 
 static bool bad_gemm_shape(int rows, int d, int n) {
     return rows < 1 || n < 1 || d < 8 || d % 8 != 0 || d > 16384;
+}
+
+// The heads' scoring and training: sizes that the tiles' arithmetic holds for.
+static bool bad_head_shape(int rows, int d, int n) {
+    return bad_gemm_shape(rows, d, n) || n >= 0x7fffffff - 256 || rows >= 0x7fffffff - 256;
+}
+static bool bad_temperature(float t) {
+    const float inv = 1.f / t;
+    return !(t > 0.f) || !(inv > 0.f) || isinf(inv) || isinf(inv * 1.4427f);
+}
+
+// Scratch of wf_lmhead_logprobs: the sorted lists and their logits, the states.
+struct ScoreLayout {
+    size_t ids, order, picked, states, total;
+};
+static ScoreLayout score_layout(int P, int d, int S, int k) {
+    ScoreLayout L;
+    const size_t list = align_up(4 * (size_t)P * (size_t)S, 256);
+    L.ids = sizeof(Control);
+    L.order = L.ids + (S > 1 ? list : 0);
+    L.picked = L.order + (S > 1 ? list : 0);
+    L.states = L.picked + list;
+    L.total = align_up(L.states + states_bytes(P, d, k), 256);
+    return L;
+}
+
+// Scratch of wf_draft_distill and its gradients: the teacher as lists, then
+// either the states of the sweep or G and the parts of dx.
+struct DistillLayout {
+    size_t ids, p, picked, stat, gs, states, G, part, total;
+};
+static DistillLayout distill_layout(int N, int d, int Vd, int k) {
+    DistillLayout L;
+    const size_t list = align_up(4 * (size_t)N * (size_t)k, 256), row = align_up(4 * (size_t)N, 256);
+    L.ids = sizeof(Control);
+    L.p = L.ids + list;
+    L.picked = L.p + list;
+    L.stat = L.picked + list;
+    L.gs = L.stat + row;
+    L.states = L.G = L.gs + row;
+    L.part = align_up(L.G + 2 * (size_t)N * distill_grad_ldg(Vd), 256);
+    const size_t a = L.part + distill_part_bytes(N, d, Vd), b = L.states + states_bytes(N, d, 0);
+    L.total = align_up(a > b ? a : b, 256);
+    return L;
+}
+
+static wf_status check_distill(const wf_distill_args* a) {
+    if (!a || !a->x || !a->Wd || !a->tid || !a->tlogit || !a->lse || bad_head_shape(a->N, a->d, a->Vd) || a->k < 1 ||
+        a->k > WF_MAX_LISTED || (a->t2d ? a->V < 1 : a->V != 0) || bad_temperature(a->temperature) ||
+        !aligned16(a->x) || !aligned16(a->Wd))
+        return WF_ERR_INVALID_ARG;
+    if (a->z && (!aligned16(a->z) || a->ldz % 4 != 0 || a->ldz < a->Vd || a->ldz > (1ll << 34)))
+        return WF_ERR_INVALID_ARG;
+    return WF_OK;
+}
+
+static TeacherCall teacher_of(const wf_distill_args* a, uint8_t* w, const DistillLayout& L) {
+    TeacherCall t{};
+    t.tid = a->tid;
+    t.tlogit = a->tlogit;
+    t.t2d = a->t2d;
+    t.N = a->N;
+    t.K = a->k;
+    t.V = a->V;
+    t.Vd = a->Vd;
+    t.inv_t = 1.f / a->temperature;
+    t.ids = reinterpret_cast<int32_t*>(w + L.ids);
+    t.p = reinterpret_cast<float*>(w + L.p);
+    t.ctrl = reinterpret_cast<Control*>(w);
+    return t;
 }
 
 #define WF_TRY(x)                        \
@@ -565,6 +643,144 @@ wf_status wf_pages_trim(const wf_paged_cache* c, const int32_t* cache_len, void*
     if (!c || !cache_len) return WF_ERR_INVALID_ARG;
     WF_TRY(check_paged(c, c->G, 1, true, ws, ws_bytes));
     return launch_pages_trim(c, cache_len, ws, stream);
+}
+
+size_t wf_logprobs_workspace_bytes(int P, int d, int V, int S, int k) {
+    if (bad_head_shape(P, d, V) || S < 0 || S > WF_MAX_LISTED || k < 0 || k > WF_MAX_TOPK || k > V) return 0;
+    return score_layout(P, d, S, k).total;
+}
+
+wf_status wf_lmhead_logprobs(const wf_logprobs_args* a, void* ws, size_t ws_bytes, wf_stream_t stream) {
+    if (!a || !a->hidden || !a->W || bad_head_shape(a->P, a->d, a->V) || bad_temperature(a->temperature) ||
+        !aligned16(a->hidden) || !aligned16(a->W) || a->k < 0 || a->k > WF_MAX_TOPK || a->k > a->V)
+        return WF_ERR_INVALID_ARG;
+    if (a->tok ? a->S < 1 || a->S > WF_MAX_LISTED || !a->logp : a->S != 0) return WF_ERR_INVALID_ARG;
+    if (a->k > 0 && !a->top_ids && !a->top_logp) return WF_ERR_INVALID_ARG;
+    if (!a->tok && a->k == 0 && !a->lse && !a->H) return WF_ERR_INVALID_ARG;
+    const ScoreLayout L = score_layout(a->P, a->d, a->S, a->k);
+    WF_TRY(check_ws(ws, ws_bytes, L.total));
+    WF_TRY(check_device());
+    WF_TRY(check_local({a->hidden, a->W}));
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    Control* ctrl = reinterpret_cast<Control*>(ws);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const int32_t* ids = a->tok;
+    const int32_t* order = nullptr;
+    if (a->S > 1) {
+        ids = reinterpret_cast<int32_t*>(w + L.ids);
+        order = reinterpret_cast<int32_t*>(w + L.order);
+        WF_TRY(launch_sort_tokens(a->tok, a->P, a->S, a->V, reinterpret_cast<int32_t*>(w + L.ids),
+                                  reinterpret_cast<int32_t*>(w + L.order), a->logp, ctrl, s));
+    }
+    const int chunk = sweep_chunk(a->P, a->d);
+    for (int r0 = 0; r0 < a->P; r0 += chunk) {
+        const size_t list = (size_t)r0 * a->S;
+        SweepCall c{};
+        c.act = a->hidden + (size_t)r0 * a->d;
+        c.W = a->W;
+        c.rows = a->P - r0 < chunk ? a->P - r0 : chunk;
+        c.d = a->d;
+        c.V = a->V;
+        c.inv_t = 1.f / a->temperature;
+        c.pick = ids ? ids + list : nullptr;
+        c.K = a->S;
+        c.picked = reinterpret_cast<float*>(w + L.picked) + list;
+        c.states = w + L.states;
+        c.k = a->k;
+        c.entropy = true;
+        c.ctrl = ctrl;
+        MergeCall m{};
+        WF_TRY(launch_sweep(c, &m.slots, s));
+        m.states = c.states;
+        m.rows = c.rows;
+        m.k = a->k;
+        m.K = a->S;
+        m.inv_t = c.inv_t;
+        m.lse = a->lse ? a->lse + r0 : nullptr;
+        m.H = a->H ? a->H + r0 : nullptr;
+        m.top_ids = a->top_ids ? a->top_ids + (size_t)r0 * a->k : nullptr;
+        m.top_logp = a->top_logp ? a->top_logp + (size_t)r0 * a->k : nullptr;
+        m.picked = c.picked;
+        m.ids = c.pick;
+        m.order = order ? order + list : nullptr;
+        m.logp = a->logp && a->tok ? a->logp + list : nullptr;
+        m.V = a->V;
+        m.ctrl = ctrl;
+        m.row0 = r0;
+        WF_TRY(launch_states_merge(m, s));
+    }
+    return WF_OK;
+}
+
+size_t wf_distill_workspace_bytes(int N, int d, int Vd, int k) {
+    if (bad_head_shape(N, d, Vd) || k < 1 || k > WF_MAX_LISTED) return 0;
+    return distill_layout(N, d, Vd, k).total;
+}
+
+wf_status wf_draft_distill(const wf_distill_args* a, void* ws, size_t ws_bytes, wf_stream_t stream) {
+    WF_TRY(check_distill(a));
+    if (!a->loss) return WF_ERR_INVALID_ARG;
+    const DistillLayout L = distill_layout(a->N, a->d, a->Vd, a->k);
+    WF_TRY(check_ws(ws, ws_bytes, L.total));
+    WF_TRY(check_device());
+    WF_TRY(check_local({a->x, a->Wd, a->z}));
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    TeacherCall t = teacher_of(a, w, L);
+    t.stat = reinterpret_cast<float*>(w + L.stat);
+    WF_TRY(launch_teacher(t, s));
+    const int chunk = sweep_chunk(a->N, a->d);
+    for (int r0 = 0; r0 < a->N; r0 += chunk) {
+        const size_t list = (size_t)r0 * a->k;
+        SweepCall c{};
+        c.act = a->x + (size_t)r0 * a->d;
+        c.W = a->Wd;
+        c.rows = a->N - r0 < chunk ? a->N - r0 : chunk;
+        c.d = a->d;
+        c.V = a->Vd;
+        c.inv_t = t.inv_t;
+        c.pick = t.ids + list;
+        c.K = a->k;
+        c.picked = reinterpret_cast<float*>(w + L.picked) + list;
+        c.states = w + L.states;
+        c.z = a->z ? a->z + (size_t)r0 * a->ldz : nullptr;
+        c.ldz = a->ldz;
+        c.ctrl = t.ctrl;
+        MergeCall m{};
+        WF_TRY(launch_sweep(c, &m.slots, s));
+        m.states = c.states;
+        m.rows = c.rows;
+        m.K = a->k;
+        m.inv_t = c.inv_t;
+        m.lse = a->lse + r0;
+        m.picked = c.picked;
+        m.ids = c.pick;
+        m.p = t.p + list;
+        m.stat = t.stat + r0;
+        m.loss = a->loss + r0;
+        m.ctrl = t.ctrl;
+        WF_TRY(launch_states_merge(m, s));
+    }
+    return WF_OK;
+}
+
+wf_status wf_draft_distill_grad(const wf_distill_args* a, void* ws, size_t ws_bytes, wf_stream_t stream) {
+    WF_TRY(check_distill(a));
+    if (!a->z || (!a->dx && !a->dWd) || !aligned16(a->dx) || !aligned16(a->dWd)) return WF_ERR_INVALID_ARG;
+    if (distill_grad_units(a->N, a->d, a->Vd) > 0x7fffffffL) return WF_ERR_INVALID_ARG;
+    const DistillLayout L = distill_layout(a->N, a->d, a->Vd, a->k);
+    WF_TRY(check_ws(ws, ws_bytes, L.total));
+    WF_TRY(check_device());
+    WF_TRY(check_local({a->x, a->Wd, a->z, a->dx, a->dWd, ws}));
+    uint8_t* w = static_cast<uint8_t*>(ws);
+    const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    TeacherCall t = teacher_of(a, w, L);
+    t.gloss = a->gloss;
+    t.gs = reinterpret_cast<float*>(w + L.gs);
+    WF_TRY(launch_teacher(t, s));
+    return launch_distill_grad(a->x, a->Wd, a->N, a->d, a->Vd, a->k, a->z, a->ldz, a->lse, t.ids, t.p, t.gs, a->dx,
+                               a->dWd, reinterpret_cast<uint16_t*>(w + L.G), reinterpret_cast<float*>(w + L.part),
+                               t.ctrl, s);
 }
 
 }  // extern "C"

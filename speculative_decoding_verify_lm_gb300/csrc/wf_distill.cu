@@ -1,0 +1,437 @@
+// The gradients of the draft head's distillation loss.  With z the kept logits
+// (over the temperature), q = softmax(z) and p the teacher's distribution,
+//   G[n, v] = gs_n (q[n, v] - p[n, v]),   gs_n = gloss_n / T (0 for a row without a teacher)
+//   dx[n, :] = sum_v G[n, v] Wd[v, :],    dWd[v, :] = sum_n G[n, v] x[n, :]
+// Two launches: G in bf16 (one pass over z), then both products as the tiles of
+// one persistent launch on the tensor cores.
+//
+// G is rounded to bf16 once (both products need operands of one type, and Wd
+// and x are bf16); the products sum in fp32 and are rounded to bf16 once more
+// on their way out.
+#include "wf_heads.cuh"
+
+namespace wf {
+
+namespace {
+
+// ------------------------------------------------------------------ G
+// Bound by the bytes of z (fp32, read) and G (bf16, written).  A thread takes 8
+// neighbouring ids at a time, GRAD_UNROLL such loads in flight; the few ids that
+// the teacher lists are put right behind a barrier, by the same CTA, from z.
+constexpr int GRAD_THREADS = 256;
+constexpr int GRAD_UNROLL = 4;
+constexpr int GRAD_COLS = GRAD_THREADS * 8 * GRAD_UNROLL;
+
+struct GradParams {
+    const float* z;
+    int64_t ldz;
+    int N, Vd, K;
+    const float* lse;
+    const float* gs;
+    const int32_t* ids;
+    const float* p;
+    uint16_t* G;
+    int64_t ldg;
+    int chunks;      // CTAs of a row
+};
+
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__global__ void __launch_bounds__(GRAD_THREADS) logit_grad_kernel(const GradParams a) {
+    pdl_wait();
+    pdl_trigger();
+    const int n = blockIdx.x / a.chunks, v0 = (blockIdx.x % a.chunks) * GRAD_COLS;
+    const float gs = a.gs[n], off = a.lse[n];
+    const float* z = a.z + (size_t)n * a.ldz;
+    uint16_t* G = a.G + (size_t)n * a.ldg;
+    float4 f[GRAD_UNROLL][2];
+#pragma unroll
+    for (int u = 0; u < GRAD_UNROLL; ++u) {
+        const int v = v0 + (u * GRAD_THREADS + (int)threadIdx.x) * 8;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            f[u][h] = gs != 0.f && v + 4 * h < a.Vd ? __ldcs(reinterpret_cast<const float4*>(z + v) + h)
+                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+#pragma unroll
+    for (int u = 0; u < GRAD_UNROLL; ++u) {
+        const int v = v0 + (u * GRAD_THREADS + (int)threadIdx.x) * 8;
+        if (v >= a.Vd) continue;
+        // ids from Vd on get 0: tensor copies look at a row's end in steps of 16 bytes
+        auto q = [&](float x, int j) {
+            return gs == 0.f || v + j >= a.Vd ? 0.f : gs * ex2_approx((x - off) * LOG2E);
+        };
+        uint4 o;
+        o.x = pack_bf16(q(f[u][0].x, 0), q(f[u][0].y, 1));
+        o.y = pack_bf16(q(f[u][0].z, 2), q(f[u][0].w, 3));
+        o.z = pack_bf16(q(f[u][1].x, 4), q(f[u][1].y, 5));
+        o.w = pack_bf16(q(f[u][1].z, 6), q(f[u][1].w, 7));
+        *reinterpret_cast<uint4*>(G + v) = o;
+    }
+    if (gs == 0.f) return;   // the same for the whole CTA
+    __syncthreads();
+    if ((int)threadIdx.x < a.K) {
+        const int32_t* ids = a.ids + (size_t)n * a.K;
+        const float* p = a.p + (size_t)n * a.K;
+        const int j = threadIdx.x, id = ids[j];
+        // the first of a run of equal ids takes all of their probability
+        if (id >= v0 && id < v0 + GRAD_COLS && id < a.Vd && (j == 0 || ids[j - 1] != id)) {
+            float pt = 0.f;
+            for (int i = j; i < a.K && ids[i] == id; ++i) pt += p[i];
+            const float q = ex2_approx((z[id] - off) * LOG2E);
+            G[id] = (uint16_t)pack_bf16(gs * (q - pt), 0.f);
+        }
+    }
+}
+
+// ------------------------------------------------------------------ dx and dWd
+// Tiles of 256 x 256 outputs by CTA pairs.  A tile of dx runs over Vd (G as it
+// lies, Wd with its contiguous dimension as the product's N), a tile of dWd over
+// the rows (G and x, both with their contiguous dimensions as M and N).  dx has
+// few and long tiles, dWd many and short ones: every pair first takes its share
+// of dx, the pairs with fewer of them begin dWd sooner, and all end together.
+// With too few rows for that dx is cut along Vd as well; its fp32 parts are
+// added up in order by a kernel of their own.
+constexpr int TM = 256, TN = 256;
+constexpr int OUT_STAGING = 4 * 2 * 4096;   // two boxes of 32 rows x 128 bytes a warp
+constexpr int PROD_STAGES = 6;
+constexpr int PROD_STAGE = 2 * BM * BK * 2;
+constexpr int PLAN_PAIRS = 76;              // pairs that the split is chosen for (152 SMs)
+constexpr int MAX_SPLIT = 16;
+constexpr int MAX_PARTS = 8 * PLAN_PAIRS;   // parts of all of dx's tiles: what a workspace holds
+
+struct ProdParams {
+    int N, Vd, d;
+    int x_m, x_n, w_m;        // row tiles of dx, column tiles of both, row tiles of dWd
+    int split, kb_x, kb_w;    // parts of dx's K; K blocks of a whole dx tile and of a dWd tile
+    int x_units, w_units;
+    int lead, late;           // pairs from `late` on have one dx unit less and begin dWd `lead` rounds sooner
+    int part_rows;            // rows of one part of dx (a multiple of 256)
+    Control* ctrl;
+    uint64_t timeout_ns;
+};
+
+struct Unit {
+    bool dx;
+    int row0, col0;     // of the output tile
+    int k0, kb;         // first K block, K blocks
+    int part;
+};
+__device__ __forceinline__ bool unit_at(const ProdParams& p, int slot, int slots, int i, Unit& u) {
+    const int mine = p.x_units > slot ? (p.x_units - slot + slots - 1) / slots : 0;
+    if (i < mine) {
+        const int v = slot + i * slots;
+        const int tile = v / p.split, part = v - tile * p.split;
+        u.dx = true;
+        u.part = part;
+        u.row0 = tile / p.x_n * TM;
+        u.col0 = tile % p.x_n * TN;
+        u.k0 = (int)((long)p.kb_x * part / p.split);
+        u.kb = (int)((long)p.kb_x * (part + 1) / p.split) - u.k0;
+        return true;
+    }
+    int j = i - mine, v;
+    const int ahead = p.lead * (slots - p.late);   // units that the early pairs take by themselves
+    if (slot >= p.late && j < p.lead) {
+        v = j * (slots - p.late) + slot - p.late;
+    } else {
+        if (slot >= p.late) j -= p.lead;
+        v = ahead + j * slots + slot;
+    }
+    if (v >= p.w_units) return false;
+    u.dx = false;
+    u.part = 0;
+    u.row0 = v / p.x_n * TM;
+    u.col0 = v % p.x_n * TN;
+    u.k0 = 0;
+    u.kb = p.kb_w;
+    return true;
+}
+
+// Descriptor of an operand whose contiguous dimension is the product's M or N:
+// blocks of 64 values x 64 K rows (128-byte rows, 128-byte swizzle) 8,192 bytes
+// apart, groups of 8 K rows 1,024 bytes apart.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | (uint64_t)(8192 >> 4) << 16 | (uint64_t)(1024 >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+constexpr uint32_t IDESC = umma_idesc_bf16(TM, TN);
+constexpr uint32_t A_MN = 1u << 15, B_MN = 1u << 16;   // the operand's M / N dimension is the contiguous one
+
+__global__ void __launch_bounds__(PIPE_THREADS, 1)
+    grad_products_kernel(const __grid_constant__ CUtensorMap tmGk, const __grid_constant__ CUtensorMap tmGm,
+                         const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
+                         const __grid_constant__ CUtensorMap tmDx, const __grid_constant__ CUtensorMap tmDw,
+                         const ProdParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    const Pipe g = pipe_at(smem_raw, PROD_STAGES, PROD_STAGE, BM * BK * 2, OUT_STAGING, p.ctrl, p.timeout_ns);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = (int)(cluster_ctarank() & 1u);
+    const bool first = rank == 0;
+    const int slot = (int)(blockIdx.x >> 1), slots = (int)(gridDim.x >> 1);
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmGk);
+        tma_prefetch_desc(&tmGm);
+        tma_prefetch_desc(&tmW);
+        tma_prefetch_desc(&tmX);
+        tma_prefetch_desc(&tmDx);
+        tma_prefetch_desc(&tmDw);
+    }
+    const uint32_t tmem_base = pipe_begin<true>(g);
+    pdl_wait();
+    pdl_trigger();
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol = policy_evict_normal();
+            Unit u{};
+            auto next = [&](int i) { return unit_at(p, slot, slots, i, u) ? u.kb : 0; };
+            auto tx = [&]() { return (uint32_t)(2 * PROD_STAGE); };
+            auto load = [&](int kc, int s, uint32_t bar) {
+                const int k = (u.k0 + kc) * BK;
+                if (u.dx) {
+                    pipe_load<true>(g.a(s), &tmGk, bar, k, u.row0 + rank * BM, pol);
+                } else {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        pipe_load<true>(g.a(s) + h * 8192, &tmGm, bar, u.row0 + rank * BM + 64 * h, k, pol);
+                }
+                const CUtensorMap* b = u.dx ? &tmW : &tmX;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    pipe_load<true>(g.b(s) + h * 8192, b, bar, u.col0 + rank * (TN / 2) + 64 * h, k, pol);
+            };
+            pipe_copy<true>(g, first, next, tx, load);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && first) {
+            Unit u{};
+            auto next = [&](int i) { return unit_at(p, slot, slots, i, u) ? u.kb : 0; };
+            auto issue = [&](int s, uint32_t d, int kc) {
+                const uint32_t as = smem_u32(g.a(s));
+                const uint64_t a = u.dx ? umma_desc_sw128(as) : desc_mn(as), b = desc_mn(smem_u32(g.b(s)));
+                const uint32_t a_step = u.dx ? 2 : 128;   // 16 values of K: 32 bytes of a row, or 16 rows of 128
+                const uint32_t idesc = IDESC | B_MN | (u.dx ? 0 : A_MN);
+#pragma unroll
+                for (int kk = 0; kk < BK / 16; ++kk)
+                    umma_bf16_pair(d, a + a_step * kk, b + 128 * kk, idesc, (kc | kk) != 0);
+            };
+            pipe_mma<true>(g, tmem_base, next, issue);
+        }
+    } else {
+        const int q = warp & 3;
+        const uint32_t tempty_first = first ? 0 : cluster_addr(&g.tempty[0], 0);
+        uint8_t* stage = pipe_extra(g) + q * 2 * 4096;
+        int box = 0;
+        Unit u{};
+        for (uint32_t i = 0; unit_at(p, slot, slots, (int)i, u); ++i) {
+            if (!pipe_acc_wait(g, i)) break;
+            const int row = u.row0 + rank * BM + q * 32;
+            const bool part = u.dx && p.split > 1;
+            if (row < (part ? p.part_rows : u.dx ? p.N : p.Vd)) {
+                const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (i & 1) * BN;
+                const int cols = min(TN, p.d - u.col0);
+                for (int c0 = 0; c0 < cols; c0 += part ? 32 : 64) {
+                    uint32_t r[2][32];
+                    tmem_ld_32x32b_x32(tbase + c0, r[0]);
+                    if (!part) tmem_ld_32x32b_x32(tbase + c0 + 32, r[1]);
+                    tmem_ld_wait();
+                    uint8_t* to = stage + box * 4096;
+                    if (lane == 0) tma_store_wait_read<1>();
+                    __syncwarp();
+                    if (part) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4*>(to + swizzled(lane, j)) =
+                                make_uint4(r[0][4 * j], r[0][4 * j + 1], r[0][4 * j + 2], r[0][4 * j + 3]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const uint32_t* v = r[j >> 2] + 8 * (j & 3);
+                            uint4 o;
+                            o.x = pack_bf16(__uint_as_float(v[0]), __uint_as_float(v[1]));
+                            o.y = pack_bf16(__uint_as_float(v[2]), __uint_as_float(v[3]));
+                            o.z = pack_bf16(__uint_as_float(v[4]), __uint_as_float(v[5]));
+                            o.w = pack_bf16(__uint_as_float(v[6]), __uint_as_float(v[7]));
+                            *reinterpret_cast<uint4*>(to + swizzled(lane, j)) = o;
+                        }
+                    }
+                    fence_async_store();
+                    __syncwarp();
+                    if (lane == 0)
+                        tma_store_2d(u.dx ? &tmDx : &tmDw, to, u.col0 + c0, u.part * (part ? p.part_rows : 0) + row);
+                    box ^= 1;
+                }
+            }
+            pipe_acc_release(g, i, tempty_first);
+        }
+        if (lane == 0) tma_store_wait_all();
+    }
+    pipe_end<true>(g, tmem_base);
+}
+
+// dx from the parts of a split product, added in order.
+__global__ void __launch_bounds__(256) dx_join_kernel(const float* part, int parts, int part_rows, int N, int d,
+                                                      uint16_t* dx) {
+    pdl_wait();
+    pdl_trigger();
+    const long units = (long)N * (d / 8);
+    for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < units; i += (long)gridDim.x * 256) {
+        const int n = (int)(i / (d / 8)), c = (int)(i % (d / 8)) * 8;
+        const float* at = part + (size_t)n * d + c;
+        const size_t step = (size_t)part_rows * d;
+        float s[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < parts; ++j) {
+            const float4 a = *reinterpret_cast<const float4*>(at + j * step);
+            const float4 b = *reinterpret_cast<const float4*>(at + j * step + 4);
+            s[0] += a.x;
+            s[1] += a.y;
+            s[2] += a.z;
+            s[3] += a.w;
+            s[4] += b.x;
+            s[5] += b.y;
+            s[6] += b.z;
+            s[7] += b.w;
+        }
+        uint4 o;
+        o.x = pack_bf16(s[0], s[1]);
+        o.y = pack_bf16(s[2], s[3]);
+        o.z = pack_bf16(s[4], s[5]);
+        o.w = pack_bf16(s[6], s[7]);
+        *reinterpret_cast<uint4*>(dx + (size_t)n * d + c) = o;
+    }
+}
+
+// ------------------------------------------------------------------ the plan
+// Costs in K blocks of a pair (64 of K, 256 x 256 outputs: 0.33 us at the bf16
+// rate).  A dWd tile writes 128 KB, a part of dx 256 KB, at the copy rate of
+// one pair (90 GB/s).
+constexpr double W_TILE_OUT = 4.4, X_PART_OUT = 9.0, TILE_FIXED = 1.0;
+
+struct Plan {
+    int x_m, x_n, w_m, kb_x, kb_w, split, part_rows;
+};
+double w_cost(int kb_w) { return (kb_w > W_TILE_OUT ? kb_w : W_TILE_OUT) + TILE_FIXED; }
+
+Plan plan_of(int N, int d, int Vd, bool dx, bool dw) {
+    Plan p{};
+    p.x_m = cdiv(N, TM);
+    p.x_n = cdiv(d, TN);
+    p.w_m = cdiv(Vd, TM);
+    p.kb_x = cdiv(Vd, BK);
+    p.kb_w = cdiv(N, BK);
+    p.split = 1;
+    p.part_rows = p.x_m * TM;
+    if (dx) {
+        const double w = dw ? (double)p.w_m * p.x_n * w_cost(p.kb_w) : 0.0;
+        double best = -1;
+        for (int s = 1; s <= MAX_SPLIT && s <= p.kb_x && (s == 1 || (long)s * p.x_m * p.x_n <= MAX_PARTS); ++s) {
+            const double unit = (double)p.kb_x / s + (s > 1 ? X_PART_OUT : TILE_FIXED);
+            const double units = (double)p.x_m * p.x_n * s;
+            const double longest = unit * cdiv((long)units, PLAN_PAIRS), mean = (units * unit + w) / PLAN_PAIRS;
+            // a split costs another launch and its bytes: about 8 K blocks
+            const double cost = (longest > mean ? longest : mean) + (s > 1 ? 8.0 : 0.0);
+            if (best < 0 || cost < best) {
+                best = cost;
+                p.split = s;
+            }
+        }
+    }
+    return p;
+}
+
+}  // namespace
+
+size_t distill_grad_ldg(int Vd) { return align_up((size_t)Vd, 64); }
+// The most blocks or tiles that a call counts.
+long distill_grad_units(int N, int d, int Vd) {
+    const long g = (long)N * cdiv(Vd, GRAD_COLS), x = (long)cdiv(N, TM) * cdiv(d, TN) * MAX_SPLIT,
+               w = (long)cdiv(Vd, TM) * cdiv(d, TN) * 2;
+    return g > x ? (g > w ? g : w) : (x > w ? x : w);
+}
+// Bytes of dx's parts: no fewer for more rows, so that a workspace for the most rows serves fewer.
+size_t distill_part_bytes(int N, int d, int Vd) {
+    const long most = (long)MAX_SPLIT * cdiv(N, TM) * cdiv(d, TN);
+    return (size_t)(most < MAX_PARTS ? most : MAX_PARTS) * TM * TN * 4;
+}
+
+// ids, p, gs: as launch_teacher left them.  G and part: scratch.
+wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int N, int d, int Vd, int K, const float* z,
+                              int64_t ldz, const float* lse, const int32_t* ids, const float* pr, const float* gs,
+                              uint16_t* dx, uint16_t* dWd, uint16_t* G, float* part, Control* ctrl, cudaStream_t s) {
+    GradParams a{};
+    a.z = z;
+    a.ldz = ldz;
+    a.N = N;
+    a.Vd = Vd;
+    a.K = K;
+    a.lse = lse;
+    a.gs = gs;
+    a.ids = ids;
+    a.p = pr;
+    a.G = G;
+    a.ldg = (int64_t)distill_grad_ldg(Vd);
+    a.chunks = cdiv(Vd, GRAD_COLS);
+    wf_status st = launch(logit_grad_kernel, dim3((unsigned)N * a.chunks), dim3(GRAD_THREADS), 0, s, a);
+    if (st != WF_OK) return st;
+
+    static std::mutex mu;
+    static bool attr_set[64] = {false};
+    static int pairs[64];
+    const int smem = pipe_smem(PROD_STAGES, PROD_STAGE, OUT_STAGING);
+    st = configure_once(mu, attr_set, [&] {
+        if (cudaFuncSetAttribute(grad_products_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess)
+            return false;
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return false;
+        if (dev < 64) pairs[dev] = resident_pairs(reinterpret_cast<const void*>(grad_products_kernel), PIPE_THREADS, smem);
+        return true;
+    });
+    if (st != WF_OK) return st;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return WF_ERR_CUDA;
+    int slots = dev < 64 ? pairs[dev] : num_sms() / 2;
+    const Plan pl = plan_of(N, d, Vd, dx != nullptr, dWd != nullptr);
+    ProdParams p{};
+    p.N = N;
+    p.Vd = Vd;
+    p.d = d;
+    p.x_m = pl.x_m;
+    p.x_n = pl.x_n;
+    p.w_m = pl.w_m;
+    p.split = pl.split;
+    p.kb_x = pl.kb_x;
+    p.kb_w = pl.kb_w;
+    p.x_units = dx ? pl.x_m * pl.x_n * pl.split : 0;
+    p.w_units = dWd ? pl.w_m * pl.x_n : 0;
+    p.part_rows = pl.part_rows;
+    if (slots > p.x_units + p.w_units) slots = p.x_units + p.w_units;
+    // pairs 0 .. late - 1 have one dx unit more than the others
+    p.late = p.x_units % slots;
+    const double ux = (double)pl.kb_x / pl.split + (pl.split > 1 ? X_PART_OUT : TILE_FIXED);
+    p.lead = p.late ? (int)(ux / w_cost(pl.kb_w) + 0.5) : 0;
+    p.ctrl = ctrl;
+    p.timeout_ns = wait_timeout_ns();
+    CUtensorMap gk, gm, tw, tx, tdx, tdw;
+    if (!make_tile_map(&gk, G, N, Vd, a.ldg, false, BK, BM) || !make_tile_map(&gm, G, N, Vd, a.ldg, false, 64, BK) ||
+        !make_tile_map(&tw, Wd, Vd, d, d, false, 64, BK) || !make_tile_map(&tx, x, N, d, d, false, 64, BK))
+        return WF_ERR_CUDA;
+    tdx = tdw = gk;
+    const bool parts = pl.split > 1;
+    if (dx && !(parts ? make_tile_map(&tdx, part, (uint64_t)pl.split * pl.part_rows, d, d, true, 32, 32)
+                      : make_tile_map(&tdx, dx, N, d, d, false, 64, 32)))
+        return WF_ERR_CUDA;
+    if (dWd && !make_tile_map(&tdw, dWd, Vd, d, d, false, 64, 32)) return WF_ERR_CUDA;
+    st = launch_cluster(grad_products_kernel, dim3(2 * slots), dim3(PIPE_THREADS), smem, s, 2u, gk, gm, tw, tx, tdx,
+                        tdw, p);
+    if (st != WF_OK || !dx || !parts) return st;
+    const long units = (long)N * (d / 8);
+    const int blocks = (int)(cdiv(units, 256) < 8 * num_sms() ? cdiv(units, 256) : 8 * num_sms());
+    return launch(dx_join_kernel, dim3(blocks), dim3(256), 0, s, (const float*)part, pl.split, pl.part_rows, N, d, dx);
+}
+
+}  // namespace wf

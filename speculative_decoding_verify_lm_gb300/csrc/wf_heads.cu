@@ -1,0 +1,297 @@
+// The small kernels around a sweep of a head's weights: the lists that it looks
+// for (given tokens, or a teacher's alternatives as probabilities over draft
+// ids), and the merge of a row's states into its log-sum-exp, entropy, best
+// alternatives, log-probabilities and loss.
+#include "wf_heads.cuh"
+
+namespace wf {
+
+namespace {
+
+constexpr int LIST_WARPS = 4;
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+// NaN wins
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const float o = __shfl_xor_sync(0xffffffffu, v, off);
+        v = v != v || o <= v ? v : o;
+    }
+    return v;
+}
+
+// The rank of each lane's two entries (places lane and lane + 32 of n <= 64)
+// among all, by id and then by place.
+__device__ __forceinline__ void ranks(const int (&id)[2], int n, int lane, int (&rank)[2]) {
+    rank[0] = rank[1] = 0;
+    for (int j = 0; j < n; ++j) {
+        const int o = __shfl_sync(0xffffffffu, j < 32 ? id[0] : id[1], j & 31);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) rank[h] += o < id[h] || (o == id[h] && j < lane + 32 * h);
+    }
+}
+
+// One warp a row.
+__global__ void __launch_bounds__(LIST_WARPS * 32) sort_tokens_kernel(const int32_t* tok, int rows, int S, int V,
+                                                                      int32_t* ids, int32_t* order, float* logp,
+                                                                      Control* ctrl) {
+    pdl_wait();
+    pdl_trigger();
+    const int row = blockIdx.x * LIST_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    const size_t base = (size_t)row * S;
+    int id[2], rank[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int j = lane + 32 * h;
+        id[h] = PICK_NONE;
+        if (j < S) {
+            const int t = tok[base + j];
+            if (t >= 0 && t < V) {
+                id[h] = t;
+            } else {
+                logp[base + j] = t == -1 ? 0.f : __int_as_float(0x7fc00000);
+                if (t != -1) record_error(ctrl, WF_ERR_BAD_DATA, (uint32_t)row);
+            }
+        }
+    }
+    ranks(id, S, lane, rank);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (lane + 32 * h < S) {
+            ids[base + rank[h]] = id[h];
+            order[base + rank[h]] = lane + 32 * h;
+        }
+}
+
+// One warp a row: p = softmax of the kept alternatives' logits / T, the others'
+// (no id, no draft id, or a logit of -inf) 0; entries of the same id stay apart,
+// their probabilities add up where they are used.  fp32 throughout.
+__global__ void __launch_bounds__(LIST_WARPS * 32) teacher_kernel(const TeacherCall t) {
+    pdl_wait();
+    pdl_trigger();
+    const int row = blockIdx.x * LIST_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    if (row >= t.N) return;
+    const size_t base = (size_t)row * t.K;
+    int id[2], rank[2];
+    float l[2], p[2];
+    bool bad = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int j = lane + 32 * h;
+        id[h] = PICK_NONE;
+        l[h] = -INFINITY;
+        if (j < t.K) {
+            int v = t.tid[base + j];
+            bool none = v == -1;
+            if (!none && t.t2d) {
+                if (v < 0 || v >= t.V) {
+                    bad = true;
+                    none = true;
+                } else {
+                    v = t.t2d[v];
+                    none = v < 0;   // no draft id for this target id
+                }
+            }
+            if (!none && (v < 0 || v >= t.Vd)) {
+                bad = true;
+                none = true;
+            }
+            if (!none) {
+                l[h] = t.tlogit[base + j];
+                if (l[h] != -INFINITY) id[h] = v;
+            }
+        }
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (bad) {   // the row takes no part
+        id[0] = id[1] = PICK_NONE;
+        l[0] = l[1] = -INFINITY;
+        if (lane == 0) record_error(t.ctrl, WF_ERR_BAD_DATA, (uint32_t)row);
+    }
+    const float top = warp_max(l[0] != l[0] || l[1] <= l[0] ? l[0] : l[1]);
+    const bool some = top != -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) p[h] = some && id[h] != PICK_NONE ? expf((l[h] - top) * t.inv_t) : 0.f;
+    const float total = warp_sum(p[0] + p[1]);
+    float plogp = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (some && id[h] != PICK_NONE) {
+            // log p from the logits: a p that rounds to 0 has a finite logarithm, times 0
+            const float logp = (l[h] - top) * t.inv_t - logf(total);
+            p[h] /= total;
+            plogp += p[h] == 0.f ? 0.f : p[h] * logp;
+        }
+    }
+    plogp = warp_sum(plogp);
+    ranks(id, t.K, lane, rank);
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (lane + 32 * h < t.K) {
+            t.ids[base + rank[h]] = id[h];
+            t.p[base + rank[h]] = p[h];
+        }
+    if (lane == 0) {
+        if (t.stat) t.stat[row] = bad ? __int_as_float(0x7fc00000) : plogp;
+        if (t.gs) t.gs[row] = some ? (t.gloss ? t.gloss[row] : 1.f) * t.inv_t : 0.f;
+    }
+}
+
+// One CTA a row: each thread takes the states of its slots, a fixed order of
+// merging makes the result the same in every run.
+constexpr int MERGE_WARPS = 4;
+
+template <int KT>
+__global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const MergeCall c) {
+    __shared__ float wm[MERGE_WARPS], wsum[MERGE_WARPS], wt[MERGE_WARPS];
+    __shared__ uint64_t wbest[MERGE_WARPS * 16];
+    pdl_wait();
+    pdl_trigger();
+    const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const float cc = LOG2E * c.inv_t;
+    float M = -INFINITY, S = 0.f, T = 0.f;
+    uint64_t loc[KT > 0 ? KT : 1];
+#pragma unroll
+    for (int j = 0; j < KT; ++j) loc[j] = 0;
+    for (int sl = threadIdx.x; sl < c.slots; sl += MERGE_WARPS * 32) {
+        const float4* at = reinterpret_cast<const float4*>(c.states + ((size_t)row * c.slots + sl) * state_bytes(KT));
+        const float4 h = at[0];
+        float4 e[KT > 0 ? KT / 2 : 1];
+#pragma unroll
+        for (int j = 0; j < KT / 2; ++j) e[j] = at[1 + j];
+        state_merge(cc, M, S, T, h.x, h.y, h.z);
+#pragma unroll
+        for (int j = 0; j < KT; ++j) {
+            const float4 f = e[j / 2];
+            const float v = j & 1 ? f.z : f.x;
+            const int id = __float_as_int(j & 1 ? f.w : f.y);
+            const uint64_t key = id < 0 ? 0ull : pack_key(v, (uint32_t)id);
+            if (key > loc[KT > 0 ? KT - 1 : 0]) {
+#pragma unroll
+                for (int s = KT - 1; s > 0; --s) {
+                    const bool shift = loc[s - 1] < key, land = !shift && loc[s] < key;
+                    loc[s] = shift ? loc[s - 1] : (land ? key : loc[s]);
+                }
+                if (loc[0] < key) loc[0] = key;
+            }
+        }
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const float m2 = __shfl_xor_sync(0xffffffffu, M, off), s2 = __shfl_xor_sync(0xffffffffu, S, off),
+                    t2 = __shfl_xor_sync(0xffffffffu, T, off);
+        // both lanes of a pair merge the lower lane's state first
+        if (lane & off) {
+            float m = m2, s = s2, t = t2;
+            state_merge(cc, m, s, t, M, S, T);
+            M = m;
+            S = s;
+            T = t;
+        } else {
+            state_merge(cc, M, S, T, m2, s2, t2);
+        }
+    }
+    if (lane == 0) {
+        wm[warp] = M;
+        wsum[warp] = S;
+        wt[warp] = T;
+    }
+    if constexpr (KT > 0) {
+        // the warp's k best, one after the other: keys are unique, so one lane owns each
+        for (int j = 0; j < c.k; ++j) {
+            const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(loc[0] >> 32));
+            const uint32_t lo =
+                __reduce_max_sync(0xffffffffu, (uint32_t)(loc[0] >> 32) == hi ? (uint32_t)loc[0] : 0u);
+            const uint64_t best = ((uint64_t)hi << 32) | lo;
+            if (lane == 0) wbest[warp * c.k + j] = best;
+            if (loc[0] == best) {
+#pragma unroll
+                for (int s = 0; s < KT - 1; ++s) loc[s] = loc[s + 1];
+                loc[KT - 1] = 0;
+            }
+        }
+    }
+    __syncthreads();
+    M = wm[0];
+    S = wsum[0];
+    T = wt[0];
+#pragma unroll
+    for (int w = 1; w < MERGE_WARPS; ++w) state_merge(cc, M, S, T, wm[w], wsum[w], wt[w]);
+    const float logs = logf(S), ref = state_ref(M, cc);
+    auto logq = [&](float v) { return fmaf(fmaf(v, cc, -ref), LN2, -logs); };
+    if (threadIdx.x == 0) {
+        if (c.lse) c.lse[row] = fmaf(ref, LN2, logs);
+        if (c.H) c.H[row] = logs - T * LN2 / S;
+    }
+    if constexpr (KT > 0) {
+        // each of the warps' winners finds its place among all of them
+        const int n = MERGE_WARPS * c.k;
+        if ((int)threadIdx.x < n) {
+            const uint64_t key = wbest[threadIdx.x];
+            int place = 0;
+            for (int j = 0; j < n; ++j) place += wbest[j] > key || (wbest[j] == key && j < (int)threadIdx.x);
+            if (place < c.k) {
+                const size_t o = (size_t)row * c.k + place;
+                if (c.top_ids) c.top_ids[o] = key ? (int32_t)key_id(key) : -1;
+                if (c.top_logp)
+                    c.top_logp[o] = key ? logq(key_val(key)) : __int_as_float(0x7fc00000);
+            }
+        }
+    }
+    if (c.logp) {
+        for (int j = threadIdx.x; j < c.K; j += MERGE_WARPS * 32) {
+            const size_t at = (size_t)row * c.K + j;
+            const int id = c.ids[at];
+            if (c.order) {
+                if (id != PICK_NONE)
+                    c.logp[(size_t)row * c.K + c.order[at]] = logq(c.picked[at]);
+            } else if (id >= 0 && id < c.V) {
+                c.logp[at] = logq(c.picked[at]);
+            } else {
+                c.logp[at] = id == -1 ? 0.f : __int_as_float(0x7fc00000);
+                if (id != -1) record_error(c.ctrl, WF_ERR_BAD_DATA, (uint32_t)(c.row0 + row));
+            }
+        }
+    }
+    if (c.loss && warp == 0) {
+        // sum p (log p - log q)
+        float part = 0.f;
+        for (int j = lane; j < c.K; j += 32) {
+            const size_t at = (size_t)row * c.K + j;
+            if (c.ids[at] != PICK_NONE) {
+                const float p = c.p[at];
+                if (p != 0.f) part = fmaf(p, logq(c.picked[at]), part);
+            }
+        }
+        part = warp_sum(part);
+        if (lane == 0) c.loss[row] = c.stat[row] - part;
+    }
+}
+
+}  // namespace
+
+wf_status launch_sort_tokens(const int32_t* tok, int rows, int S, int V, int32_t* ids, int32_t* order, float* logp,
+                             Control* ctrl, cudaStream_t s) {
+    return launch(sort_tokens_kernel, dim3(cdiv(rows, LIST_WARPS)), dim3(LIST_WARPS * 32), 0, s, tok, rows, S, V, ids,
+                  order, logp, ctrl);
+}
+
+wf_status launch_teacher(const TeacherCall& t, cudaStream_t s) {
+    return launch(teacher_kernel, dim3(cdiv(t.N, LIST_WARPS)), dim3(LIST_WARPS * 32), 0, s, t);
+}
+
+wf_status launch_states_merge(const MergeCall& c, cudaStream_t s) {
+    switch (state_width(c.k)) {
+        case 0: return launch(states_merge_kernel<0>, dim3(c.rows), dim3(MERGE_WARPS * 32), 0, s, c);
+        case 10: return launch(states_merge_kernel<10>, dim3(c.rows), dim3(MERGE_WARPS * 32), 0, s, c);
+        default: return launch(states_merge_kernel<16>, dim3(c.rows), dim3(MERGE_WARPS * 32), 0, s, c);
+    }
+}
+
+}  // namespace wf

@@ -1,0 +1,118 @@
+// What the target head's log-probabilities and the draft head's distillation
+// share: one sweep of a head's weights over the rows, whose logits are folded
+// as they leave the accumulator, and the merge of the sweep's partial states.
+#pragma once
+
+#include "wf_pipe.cuh"
+
+namespace wf {
+
+static_assert(WF_MAX_LISTED <= 64, "a warp's lanes sort two listed ids each");
+constexpr int PICK_NONE = 0x7fffffff;    // a list's place without an id: sorts last, matches nothing
+
+// Rows swept by one launch: what they read stays in L2 while the weights
+// stream past, and the states of a launch have a bounded size.
+constexpr long SWEEP_ACT_BYTES = 48L << 20;
+constexpr int SWEEP_MAX_ROWS = 16384;
+inline int sweep_chunk(int rows, int d) {
+    long c = SWEEP_ACT_BYTES / (2L * d) / (2 * BM) * (2 * BM);
+    if (c > SWEEP_MAX_ROWS) c = SWEEP_MAX_ROWS;
+    return rows < c ? rows : (int)c;   // d <= 16,384: at least 1,536 rows
+}
+
+// The state that one CTA (or pair) leaves for a row: (M, S, T, 0) as in
+// state_merge, then the k best as (logit, id) words.
+__host__ __device__ constexpr size_t state_bytes(int kt) { return 16 + 8 * (size_t)kt; }
+inline int state_width(int k) { return k == 0 ? 0 : k <= 10 ? 10 : 16; }
+constexpr int STATE_SLOTS = 160;         // CTAs of a sweep of one activation tile
+// (pairs of a sweep of several: REC_PAIRS)
+inline size_t states_bytes(int rows, int d, int k) {
+    // no fewer for more rows, so that a workspace for the most rows serves fewer
+    const size_t many = (size_t)sweep_chunk(rows, d) * REC_PAIRS, few = (size_t)(rows < BM ? rows : BM) * STATE_SLOTS;
+    return (many > few ? many : few) * state_bytes(state_width(k));
+}
+
+struct SweepCall {
+    const uint16_t *act, *W;
+    int rows, d, V;          // rows: of this launch, at most sweep_chunk()
+    float inv_t;
+    const int32_t* pick;     // [rows][K] ids, ascending (K > 1), or null
+    int K;
+    float* picked;           // [rows][K] their logits, where the id lies in [0, V)
+    uint8_t* states;
+    int k;                   // best logits kept
+    bool entropy;
+    float* z;                // [rows][ldz] logits times inv_t, or null
+    int64_t ldz;
+    Control* ctrl;
+};
+// Enqueues the sweep; *slots: states left for each row (row-major, in use all of them).
+wf_status launch_sweep(const SweepCall& c, int* slots, cudaStream_t s);
+
+// Lists of given tokens sorted by id, with the place that each came from; places
+// without a token (-1) get a log-probability of 0 and ids outside [0, V) NaN.
+wf_status launch_sort_tokens(const int32_t* tok, int rows, int S, int V, int32_t* ids, int32_t* order, float* logp,
+                             Control* ctrl, cudaStream_t s);
+
+// A teacher's alternatives as the draft head's: ids mapped, sorted, with their
+// probabilities.
+struct TeacherCall {
+    const int32_t* tid;      // [N][K]
+    const float* tlogit;     // [N][K]
+    const int32_t* t2d;      // [V] or null: tid are draft ids
+    int N, K, V, Vd;
+    float inv_t;
+    const float* gloss;      // [N] or null: 1
+    int32_t* ids;            // out [N][K] ascending draft ids, PICK_NONE last
+    float* p;                // out [N][K] their probabilities
+    float* stat;             // out [N] sum p log p; NaN: an id out of range; or null
+    float* gs;               // out [N] gloss / T, 0 for a row without a teacher; or null
+    Control* ctrl;
+};
+wf_status launch_teacher(const TeacherCall& t, cudaStream_t s);
+
+struct MergeCall {
+    const uint8_t* states;   // [rows][slots]
+    int rows, slots, k, K;
+    float inv_t;
+    float* lse;              // [rows] or null
+    float* H;                // [rows] or null
+    int32_t* top_ids;        // [rows][k] or null
+    float* top_logp;         // [rows][k] or null
+    const float* picked;     // [rows][K]
+    const int32_t* ids;      // [rows][K] as swept
+    const int32_t* order;    // [rows][K] or null: K = 1, ids are the tokens themselves
+    float* logp;             // [rows][K] or null
+    const float* p;          // [rows][K]: the loss is asked for
+    const float* stat;       // [rows]
+    float* loss;             // [rows]
+    int V;
+    int row0;                // first row's number in the call, for errors
+    Control* ctrl;
+};
+wf_status launch_states_merge(const MergeCall& c, cudaStream_t s);
+
+// A state's reference in base 2: the same rounded product wherever a state is
+// summed up, merged or read, so that its rounding cancels.
+__device__ __forceinline__ float state_ref(float M, float c) { return __fmul_rn(M, c); }
+
+// (M, S, T) of two states of one row: M the largest logit, S = sum 2^z, T = sum
+// z 2^z, z = c v - state_ref(M, c).  A state with S = 0 is empty; NaN stays NaN.
+__device__ __forceinline__ void state_merge(float c, float& M, float& S, float& T, float m2, float s2, float t2) {
+    if (s2 == 0.f) return;
+    if (S == 0.f) {
+        M = m2;
+        S = s2;
+        T = t2;
+        return;
+    }
+    const float mx = fmaxf(M, m2), ref = state_ref(mx, c);
+    const float d1 = state_ref(M, c) - ref, d2 = state_ref(m2, c) - ref;
+    const float a1 = ex2_approx(d1), a2 = ex2_approx(d2);
+    // a state far below the other: its weight is 0, and so is its part of T
+    T = (a1 == 0.f && S == S ? 0.f : (T + d1 * S) * a1) + (a2 == 0.f && s2 == s2 ? 0.f : (t2 + d2 * s2) * a2);
+    S = S * a1 + s2 * a2;
+    M = mx;
+}
+
+}  // namespace wf

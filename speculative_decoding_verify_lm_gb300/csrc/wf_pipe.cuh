@@ -1,0 +1,289 @@
+// The pipelined tcgen05 product that the heads' scoring and training kernels
+// share: a shared-memory ring filled by TMA, one elected thread issuing the
+// MMAs into two TMEM accumulators, and epilogue warps that read them.
+//
+//   warp 0     fills the ring: each stage holds an A tile and a B tile of one K
+//              block (64 values of K)
+//   warp 1     allocates TMEM and issues the MMAs of a stage; the stage is free
+//              again when they have completed
+//   warps 2-5  read a finished accumulator (thread = one row of the tile) while
+//              the next tile's MMAs run into the other one
+// PAIR: the two CTAs of a cluster compute one 256-row tile with paired MMAs;
+// each loads its own half of A's rows and of B's, the first CTA issues, and
+// both CTAs' barriers are committed to.
+// Every wait is bounded: one that runs out records WF_ERR_TIMEOUT, raises the
+// CTA's abort flag, waits (again bounded) for its own copies and MMAs in
+// flight, and the CTA frees TMEM and exits.
+#pragma once
+
+#include "wf_internal.cuh"
+
+namespace wf {
+
+constexpr int PIPE_THREADS = 192;
+constexpr int PIPE_MAX_STAGES = 8;
+constexpr int PIPE_TMEM_COLS = 2 * BN;     // two fp32 accumulators of up to BN columns
+constexpr int PIPE_BARRIER_BYTES = 256;    // barriers, TMEM address and abort flag behind the ring
+constexpr int PIPE_SMEM_MAX = 227 * 1024;
+constexpr int PIPE_STATIC_MAX = 512;       // of it, for a kernel's static shared memory
+// What a kernel records beside WF_ERR_TIMEOUT: which wait gave up.
+constexpr uint32_t PIPE_WHERE_COPY = 0x400, PIPE_WHERE_ACC = 0x500, PIPE_WHERE_STAGE = 0x510, PIPE_WHERE_TILE = 0x600;
+
+struct Pipe {
+    uint8_t* base;                 // the ring, 1,024-byte aligned
+    int stages, stage_bytes, a_bytes;
+    uint64_t *full, *empty, *tfull, *tempty, *drain;
+    uint32_t* tmem_slot;
+    volatile int* abort_flag;
+    Control* ctrl;
+    uint64_t timeout_ns;
+    __device__ __forceinline__ uint8_t* a(int s) const { return base + (size_t)s * stage_bytes; }
+    __device__ __forceinline__ uint8_t* b(int s) const { return base + (size_t)s * stage_bytes + a_bytes; }
+    __device__ __forceinline__ void fail(uint32_t where) const {
+        *abort_flag = 1;
+        record_error(ctrl, WF_ERR_TIMEOUT, where);
+    }
+};
+
+// Ring, `extra` bytes (a multiple of 1,024) behind it and the barriers, in dynamic shared memory from its start
+// rounded up to 1,024 bytes.
+__device__ __forceinline__ Pipe pipe_at(uint8_t* smem_raw, int stages, int stage_bytes, int a_bytes, int extra,
+                                        Control* ctrl, uint64_t timeout_ns) {
+    Pipe g;
+    g.base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    g.stages = stages;
+    g.stage_bytes = stage_bytes;
+    g.a_bytes = a_bytes;
+    g.full = reinterpret_cast<uint64_t*>(g.base + (size_t)stages * stage_bytes + extra);
+    g.empty = g.full + PIPE_MAX_STAGES;
+    g.tfull = g.empty + PIPE_MAX_STAGES;
+    g.tempty = g.tfull + 2;
+    g.drain = g.tempty + 2;
+    g.tmem_slot = reinterpret_cast<uint32_t*>(g.drain + 1);
+    g.abort_flag = reinterpret_cast<volatile int*>(g.tmem_slot + 1);
+    g.ctrl = ctrl;
+    g.timeout_ns = timeout_ns;
+    return g;
+}
+__device__ __forceinline__ uint8_t* pipe_extra(const Pipe& g) { return g.base + (size_t)g.stages * g.stage_bytes; }
+inline int pipe_smem(int stages, int stage_bytes, int extra) {
+    return stages * stage_bytes + PIPE_BARRIER_BYTES + extra + 1024;
+}
+
+// Barriers and TMEM; returns the TMEM base address.  All threads.
+template <bool PAIR>
+__device__ __forceinline__ uint32_t pipe_begin(const Pipe& g) {
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < g.stages; ++s) {
+            mbar_init(&g.full[s], 1);
+            mbar_init(&g.empty[s], 1);
+        }
+        for (int a = 0; a < 2; ++a) {
+            mbar_init(&g.tfull[a], 1);
+            mbar_init(&g.tempty[a], PAIR ? 256 : 128);   // PAIR: both CTAs' epilogue threads release
+        }
+        mbar_init(g.drain, 1);
+        *g.abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 1) {
+        if constexpr (PAIR) {
+            tmem_alloc_pair(g.tmem_slot, PIPE_TMEM_COLS);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(g.tmem_slot, PIPE_TMEM_COLS);
+            tmem_relinquish();
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();   // both CTAs' barriers and TMEM exist before either uses the other's
+    tc_fence_after();
+    return *g.tmem_slot;
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void pipe_end(const Pipe& g, uint32_t tmem_base) {
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();   // the first CTA's MMAs and the second's remote arrivals are done
+    tc_fence_after();
+    if ((threadIdx.x >> 5) == 1) {
+        if constexpr (PAIR)
+            tmem_dealloc_pair(tmem_base, PIPE_TMEM_COLS);
+        else
+            tmem_dealloc(tmem_base, PIPE_TMEM_COLS);
+    }
+}
+
+// The copying thread.  next(i) sets up the CTA's i-th tile and returns its K
+// blocks (0: no further tile); tx() is what a stage of it receives in bytes
+// (PAIR: both CTAs together); load(kc, s, bar) issues its copies into stage s,
+// counted on the barrier at shared address `bar` (PAIR: the first CTA's).
+template <bool PAIR, typename Next, typename Tx, typename Load>
+__device__ __forceinline__ void pipe_copy(const Pipe& g, bool first, Next next, Tx tx, Load load) {
+    const uint32_t full0 = PAIR ? cluster_addr(&g.full[0], 0) : smem_u32(&g.full[0]);
+    uint32_t it = 0;   // stages issued so far
+    int s = 0;         // = it % stages
+    uint32_t ph = 0;   // = (it / stages) & 1
+    bool ok = true;
+    for (int i = 0; ok; ++i) {
+        const int num_k = next(i);
+        if (num_k == 0) break;
+        const uint32_t bytes = tx();
+        for (int kc = 0; kc < num_k; ++kc, ++it) {
+            if (it > 0 && ++s == g.stages) {
+                s = 0;
+                ph ^= 1;
+            }
+            if (!mbar_wait(&g.empty[s], ph ^ 1, g.timeout_ns, g.abort_flag)) {
+                g.fail(PIPE_WHERE_COPY + s);
+                ok = false;
+                break;
+            }
+            if (!PAIR || first) mbar_arrive_expect_tx(&g.full[s], bytes);
+            load(kc, s, full0 + (uint32_t)(s * sizeof(uint64_t)));
+        }
+    }
+    if (!ok || *g.abort_flag) {
+        // let every copy this thread issued land before the CTA exits
+        if (!PAIR || first) {
+            for (uint32_t j = (it > (uint32_t)g.stages ? it - g.stages : 0); j < it; ++j)
+                mbar_wait(&g.full[j % g.stages], (j / g.stages) & 1, g.timeout_ns, nullptr);
+        } else {
+            // the second CTA's copies are counted on the first CTA's barriers,
+            // which it cannot wait on: give them a fixed 200 us (a copy from L2
+            // or HBM takes a few)
+            const uint64_t t0 = globaltimer_ns();
+            while (globaltimer_ns() - t0 < 200000ull) {
+            }
+        }
+    }
+}
+
+// The issuing thread (PAIR: of the first CTA).  next(i) as above; issue(s,
+// d_tmem, kc) issues stage s's MMAs into the accumulator at d_tmem (kc = 0
+// overwrites it).
+template <bool PAIR, typename Next, typename Issue>
+__device__ __forceinline__ void pipe_mma(const Pipe& g, uint32_t tmem_base, Next next, Issue issue) {
+    const uint32_t empty_peer = PAIR ? cluster_addr(&g.empty[0], 1) : 0;
+    const uint32_t tfull_peer = PAIR ? cluster_addr(&g.tfull[0], 1) : 0;
+    uint32_t it = 0;
+    int s = 0;
+    uint32_t ph = 0;
+    bool ok = true, issued = false;
+    for (uint32_t i = 0; ok; ++i) {
+        const int num_k = next((int)i);
+        if (num_k == 0) break;
+        const uint32_t acc = i & 1, acc_ph = (i >> 1) & 1;
+        // PAIR: released by both CTAs' epilogues (the second's arrivals are remote)
+        if (!(PAIR ? mbar_wait_cluster(&g.tempty[acc], acc_ph ^ 1, g.timeout_ns, g.abort_flag)
+                   : mbar_wait(&g.tempty[acc], acc_ph ^ 1, g.timeout_ns, g.abort_flag))) {
+            g.fail(PIPE_WHERE_ACC);
+            ok = false;
+            break;
+        }
+        tc_fence_after();
+        for (int kc = 0; kc < num_k; ++kc, ++it) {
+            if (it > 0 && ++s == g.stages) {
+                s = 0;
+                ph ^= 1;
+            }
+            if (!mbar_wait(&g.full[s], ph, g.timeout_ns, g.abort_flag)) {
+                g.fail(PIPE_WHERE_STAGE + s);
+                ok = false;
+                break;
+            }
+            tc_fence_after();
+            issue(s, tmem_base + acc * BN, kc);
+            if constexpr (PAIR) {
+                umma_commit_pair(smem_u32(&g.empty[s]));
+                umma_commit_pair(empty_peer + (uint32_t)(s * sizeof(uint64_t)));
+            } else {
+                umma_commit(&g.empty[s]);
+            }
+            issued = true;
+        }
+        if (ok) {
+            if constexpr (PAIR) {
+                umma_commit_pair(smem_u32(&g.tfull[acc]));
+                umma_commit_pair(tfull_peer + acc * (uint32_t)sizeof(uint64_t));
+            } else {
+                umma_commit(&g.tfull[acc]);
+            }
+        }
+    }
+    if (issued && (!ok || PAIR)) {
+        // every MMA issued above (PAIR: into both CTAs' TMEM) has completed before TMEM is freed
+        uint64_t* drain = g.drain;
+        if constexpr (PAIR)
+            umma_commit_pair(smem_u32(drain));
+        else
+            umma_commit(drain);
+        mbar_wait(drain, 0, g.timeout_ns, nullptr);
+    }
+}
+
+// Epilogue warps: wait for the i-th accumulator, and hand it back.
+__device__ __forceinline__ bool pipe_acc_wait(const Pipe& g, uint32_t i) {
+    if (!mbar_wait(&g.tfull[i & 1], (i >> 1) & 1, g.timeout_ns, g.abort_flag)) {
+        g.fail(PIPE_WHERE_TILE);
+        return false;
+    }
+    tc_fence_after();
+    return true;
+}
+// tempty_first: in a pair's second CTA the shared::cluster address of the first CTA's accumulator barriers, else 0.
+__device__ __forceinline__ void pipe_acc_release(const Pipe& g, uint32_t i, uint32_t tempty_first) {
+    tc_fence_before();
+    if (tempty_first)
+        mbar_arrive_remote(tempty_first + (i & 1) * (uint32_t)sizeof(uint64_t), 1u);
+    else
+        mbar_arrive(&g.tempty[i & 1]);
+}
+
+// One box into shared memory, its bytes counted on the barrier at `bar`.
+template <bool PAIR>
+__device__ __forceinline__ void pipe_load(uint8_t* dst, const CUtensorMap* map, uint32_t bar, int x, int y,
+                                          uint64_t policy) {
+    if constexpr (PAIR) {
+        tma_load_2d_pair(dst, map, bar, x, y, policy);
+    } else {
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+            " [%0], [%1, {%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+            "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(bar), "l"(policy)
+            : "memory");
+    }
+}
+
+// One box out of shared memory (clipped at the tensor's ends), by one thread:
+// the box has to have been made visible with fence_async_store first.
+__device__ __forceinline__ void fence_async_store() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap* map, const void* src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(smem_u32(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+}
+// All but the newest `N` stores of this thread have read their shared memory / all stores are done.
+template <int N>
+__device__ __forceinline__ void tma_store_wait_read() {
+    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void tma_store_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Byte of 16-byte unit u of row r in a 128-byte-row tile with the 128-byte swizzle.
+__device__ __forceinline__ uint32_t swizzled(int r, int u) { return (uint32_t)(r * 128 + ((u ^ (r & 7)) << 4)); }
+
+// Tensor map of [rows, cols] with row stride `stride` (elements), read or
+// written in boxes of box_cols (128 bytes) x box_rows, 128-byte swizzle.
+bool make_tile_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t stride, bool fp32,
+                   uint32_t box_cols, uint32_t box_rows);
+// Clusters of two CTAs of `kernel` that can be resident at once, at most REC_PAIRS.
+int resident_pairs(const void* kernel, int threads, int smem);
+constexpr int REC_PAIRS = 80;
+
+}  // namespace wf

@@ -1,0 +1,506 @@
+// One sweep of a head's weights over the rows (wf_lmhead_logprobs, the forward
+// part of wf_draft_distill):
+//   v = <act_row, W_id>   (bf16 products, fp32 sums, in TMEM only)
+// and per row, as the tiles of logits leave the accumulator,
+//   M = max v,  S = sum 2^z,  T = sum z 2^z,  z = c (v - M),  c = log2(e) / temperature
+// (lse and entropy follow from them), the k best (v, id), the logits of the
+// row's listed ids, and, where asked for, the logits themselves in fp32.
+//
+// A row's states stay with the CTA: its thread keeps M, S, T and the k best in
+// registers from tile to tile, and puts them aside in the workspace only when
+// the CTA's next tile is of other rows.  So a row ends with one state per CTA
+// that saw it, not one per tile (4,096 rows over 151,936 ids with 16 best: 76
+// states of 144 bytes a row instead of 594), and what a tile adds to the k best
+// is a few insertions.
+// One activation tile (up to 128 rows): bound by the weights' bytes; every CTA
+// its own tiles, ring slots as large as the rows.  More rows: pairs of CTAs on
+// tiles of 256 rows x 256 ids, bound by the tensor cores.
+#include <cudaTypedefs.h>
+
+#include "wf_heads.cuh"
+
+namespace wf {
+
+namespace {
+
+constexpr int STAGING = 4 * 2 * 4096;     // kept logits: two boxes of 32 rows x 128 bytes a warp
+
+struct SweepParams {
+    int rows, V;
+    int num_m, num_mt, num_n, num_k;      // 128-row tiles, row tiles of the schedule, weight tiles, K blocks
+    int bn, nbig, step;                   // nbig weight tiles of bn rows, then tiles of bn - step
+    uint32_t idesc, idesc_s;
+    int stages, stage_bytes, a_bytes;
+    float c, inv_t;
+    const int32_t* pick;
+    int K;
+    float* picked;
+    uint8_t* states;
+    int slots;                            // states per row
+    Control* ctrl;
+    uint64_t timeout_ns;
+};
+
+struct Span {
+    int row0, rows;
+    bool big;
+};
+__device__ __forceinline__ Span span(const SweepParams& p, int n) {
+    if (n < p.nbig) return {n * p.bn, p.bn, true};
+    const int h = p.bn - p.step;
+    return {p.nbig * p.bn + (n - p.nbig) * h, h, false};
+}
+
+// Insert (v, id) into a descending list; the earlier entry wins ties.
+template <int KT>
+__device__ __forceinline__ void insert(float (&tv)[KT], int (&ti)[KT], float v, int id) {
+#pragma unroll
+    for (int j = KT - 1; j > 0; --j) {
+        const bool shift = tv[j - 1] < v;
+        const bool land = !shift && tv[j] < v;
+        tv[j] = shift ? tv[j - 1] : (land ? v : tv[j]);
+        ti[j] = shift ? ti[j - 1] : (land ? id : ti[j]);
+    }
+    if (tv[0] < v) {
+        tv[0] = v;
+        ti[0] = id;
+    }
+}
+
+template <int KT>
+struct State {
+    float M, S, T;
+    float tv[KT > 0 ? KT : 1];
+    int ti[KT > 0 ? KT : 1];
+    __device__ __forceinline__ void clear() {
+        M = -INFINITY;
+        S = T = 0.f;
+        if constexpr (KT > 0) {
+#pragma unroll
+            for (int j = 0; j < KT; ++j) {
+                tv[j] = -INFINITY;
+                ti[j] = -1;
+            }
+        }
+    }
+    __device__ __forceinline__ void put(uint8_t* at) const {
+        float4* o = reinterpret_cast<float4*>(at);
+        o[0] = make_float4(M, S, T, 0.f);
+        if constexpr (KT > 0) {
+#pragma unroll
+            for (int j = 0; j < KT; j += 2)
+                o[1 + j / 2] = make_float4(tv[j], __int_as_float(ti[j]), tv[j + 1], __int_as_float(ti[j + 1]));
+        }
+    }
+    __device__ __forceinline__ void get(const uint8_t* at) {
+        const float4* o = reinterpret_cast<const float4*>(at);
+        const float4 h = o[0];
+        M = h.x;
+        S = h.y;
+        T = h.z;
+        if constexpr (KT > 0) {
+#pragma unroll
+            for (int j = 0; j < KT; j += 2) {
+                const float4 e = o[1 + j / 2];
+                tv[j] = e.x;
+                ti[j] = __float_as_int(e.y);
+                tv[j + 1] = e.z;
+                ti[j + 1] = __float_as_int(e.w);
+            }
+        }
+    }
+};
+
+// Fold 32 columns (the first lim of them) into a row's state.
+template <int KT, bool ENT, bool FULL>
+__device__ __forceinline__ void fold(const uint32_t (&r)[32], int lim, int col0, float c, State<KT>& st) {
+    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (FULL || j < lim) m4[j & 3] = fmaxf(m4[j & 3], __uint_as_float(r[j]));
+    const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+    if (mx > st.M) {   // a new largest logit: rescale what was summed so far
+        if (st.S != 0.f) {
+            const float dz = state_ref(st.M, c) - state_ref(mx, c);
+            const float sc = ex2_approx(dz);
+            if constexpr (ENT) st.T = sc == 0.f && st.S == st.S ? 0.f : (st.T + dz * st.S) * sc;
+            st.S *= sc;
+        }
+        st.M = mx;
+    }
+    const float off = state_ref(st.M, c);
+    float s4[4] = {0.f, 0.f, 0.f, 0.f}, t4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int j = 0; j < 32; ++j)
+        if (FULL || j < lim) {
+            const float z = fmaf(__uint_as_float(r[j]), c, -off);
+            const float e = ex2_approx(z);
+            s4[j & 3] += e;
+            if constexpr (ENT) t4[j & 3] = fmaf(z, e, t4[j & 3]);
+        }
+    st.S += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+    if constexpr (ENT) st.T += (t4[0] + t4[1]) + (t4[2] + t4[3]);
+    if constexpr (KT > 0) {
+        if (mx > st.tv[KT - 1]) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                if (FULL || j < lim) {
+                    const float v = __uint_as_float(r[j]);
+                    if (v > st.tv[KT - 1]) insert<KT>(st.tv, st.ti, v, col0 + j);
+                }
+        }
+    }
+}
+
+template <int KT, bool ENT, bool Z, bool PAIR>
+__global__ void __launch_bounds__(PIPE_THREADS, 1)
+    sweep_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+                 const __grid_constant__ CUtensorMap tmBs, const __grid_constant__ CUtensorMap tmZ,
+                 const SweepParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ uint32_t seen[4][SWEEP_MAX_ROWS / BM / 32];   // row tiles that a warp has a state of
+    const Pipe g = pipe_at(smem_raw, p.stages, p.stage_bytes, p.a_bytes, Z ? STAGING : 0, p.ctrl, p.timeout_ns);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PAIR ? (int)(cluster_ctarank() & 1u) : 0;
+    const bool first = rank == 0;
+    const int slot = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
+    const int nslots = PAIR ? (int)(gridDim.x >> 1) : (int)gridDim.x;
+    const int units = p.num_mt * p.num_n;   // unit u: row tile u % num_mt, weight tile u / num_mt
+    if (threadIdx.x == 0) {
+        tma_prefetch_desc(&tmA);
+        tma_prefetch_desc(&tmB);
+        if (p.nbig < p.num_n) tma_prefetch_desc(&tmBs);
+        if constexpr (Z) tma_prefetch_desc(&tmZ);
+    }
+    const uint32_t tmem_base = pipe_begin<PAIR>(g);
+    pdl_wait();
+    pdl_trigger();
+
+    if (warp == 0) {
+        if (lane == 0) {
+            const uint64_t pol_w = policy_evict_first(), pol_a = policy_evict_last();
+            int m = 0;
+            Span sp{};
+            auto next = [&](int i) {
+                const int u = slot + i * nslots;
+                if (u >= units) return 0;
+                m = PAIR ? 2 * (u % p.num_mt) + rank : u % p.num_mt;
+                sp = span(p, u / p.num_mt);
+                return p.num_k;
+            };
+            auto tx = [&]() { return (uint32_t)((PAIR ? 2 : 1) * p.a_bytes + sp.rows * BK * 2); };
+            auto load = [&](int kc, int s, uint32_t bar) {
+                const int half = PAIR ? sp.rows / 2 : 0;
+                pipe_load<PAIR>(g.a(s), &tmA, bar, kc * BK, m * BM, pol_a);
+                pipe_load<PAIR>(g.b(s), sp.big ? &tmB : &tmBs, bar, kc * BK, sp.row0 + rank * half, pol_w);
+            };
+            pipe_copy<PAIR>(g, first, next, tx, load);
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && first) {
+            uint32_t idesc = 0;
+            auto next = [&](int i) {
+                const int u = slot + i * nslots;
+                if (u >= units) return 0;
+                idesc = u / p.num_mt < p.nbig ? p.idesc : p.idesc_s;
+                return p.num_k;
+            };
+            auto issue = [&](int s, uint32_t d, int kc) {
+                const uint64_t a = umma_desc_sw128(smem_u32(g.a(s))), b = umma_desc_sw128(smem_u32(g.b(s)));
+#pragma unroll
+                for (int kk = 0; kk < BK / 16; ++kk) {   // 32 bytes of K a step
+                    if constexpr (PAIR)
+                        umma_bf16_pair(d, a + 2 * kk, b + 2 * kk, idesc, (kc | kk) != 0);
+                    else
+                        umma_bf16(d, a + 2 * kk, b + 2 * kk, idesc, (kc | kk) != 0);
+                }
+            };
+            pipe_mma<PAIR>(g, tmem_base, next, issue);
+        }
+    } else {
+        const int q = warp & 3;            // TMEM lane quadrant that this warp may access
+        const int rit = q * 32 + lane;
+        const uint32_t tempty_first = (PAIR && !first) ? cluster_addr(&g.tempty[0], 0) : 0;
+        uint8_t* stage = pipe_extra(g) + q * 2 * 4096;
+        for (int j = lane; j < (int)(sizeof(seen[0]) / 4); j += 32) seen[q][j] = 0;
+        __syncwarp();
+        State<KT> st;
+        st.clear();
+        int cur = -1;                      // the row tile whose states the registers hold
+        int box = 0;                       // Z: staging box in use
+        auto state_of = [&](int row) { return p.states + ((size_t)row * p.slots + slot) * state_bytes(KT); };
+        for (uint32_t i = 0;; ++i) {
+            const int u = slot + (int)i * nslots;
+            if (u >= units) break;
+            const int mt = u % p.num_mt, m = PAIR ? 2 * mt + rank : mt;
+            const Span sp = span(p, u / p.num_mt);
+            const int row = m * BM + rit;
+            const bool warp_live = m * BM + q * 32 < p.rows, live = row < p.rows;
+            if (mt != cur) {
+                if (cur >= 0) {
+                    const int was = (PAIR ? 2 * cur + rank : cur) * BM + rit;
+                    if (was < p.rows) st.put(state_of(was));
+                }
+                if ((seen[q][mt >> 5] >> (mt & 31)) & 1) {
+                    if (live) st.get(state_of(row));
+                } else {
+                    st.clear();
+                    __syncwarp();
+                    if (lane == 0) seen[q][mt >> 5] |= 1u << (mt & 31);
+                    __syncwarp();
+                }
+                cur = mt;
+                if constexpr (KT > 0) {
+                    if (!live) st.tv[KT - 1] = INFINITY;   // rows that are none insert nothing
+                }
+            }
+            // the row's listed ids from this tile's first on
+            const int32_t* list = p.K && live ? p.pick + (size_t)row * p.K : nullptr;
+            int at = 0, next_id = PICK_NONE;
+            if (list) {
+                if (p.K == 1) {
+                    const int id = list[0];
+                    next_id = id >= sp.row0 ? id : PICK_NONE;
+                } else {
+                    int hi = p.K;
+                    while (at < hi) {
+                        const int mid = (at + hi) >> 1;
+                        if (list[mid] < sp.row0)
+                            at = mid + 1;
+                        else
+                            hi = mid;
+                    }
+                    next_id = at < p.K ? list[at] : PICK_NONE;
+                }
+            }
+            if (!pipe_acc_wait(g, i)) break;
+            if (warp_live) {
+                const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (i & 1) * BN;
+                const int cols = min(sp.rows, p.V - sp.row0);
+                for (int c0 = 0; c0 < cols; c0 += 32) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tbase + c0, r);
+                    tmem_ld_wait();
+                    const int col0 = sp.row0 + c0, lim = min(32, cols - c0);
+                    if (lim == 32)
+                        fold<KT, ENT, true>(r, 32, col0, p.c, st);
+                    else
+                        fold<KT, ENT, false>(r, lim, col0, p.c, st);
+                    while (__any_sync(0xffffffffu, next_id < col0 + lim)) {
+                        if (next_id < col0 + lim) {
+                            const int j0 = next_id - col0;
+                            uint32_t v = r[0];
+#pragma unroll
+                            for (int j = 1; j < 32; ++j) v = j == j0 ? r[j] : v;
+                            p.picked[(size_t)row * p.K + at] = __uint_as_float(v);
+                            ++at;
+                            next_id = at < p.K ? list[at] : PICK_NONE;
+                        }
+                    }
+                    if constexpr (Z) {
+                        // 32 x 32 logits to the staging box, out by one tensor copy (clipped at the
+                        // last row, and the last id rounded up to 16 bytes)
+                        uint8_t* to = stage + box * 4096;
+                        if (lane == 0) tma_store_wait_read<1>();
+                        __syncwarp();
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4)
+                            *reinterpret_cast<float4*>(to + swizzled(lane, j >> 2)) =
+                                make_float4(__uint_as_float(r[j]) * p.inv_t, __uint_as_float(r[j + 1]) * p.inv_t,
+                                            __uint_as_float(r[j + 2]) * p.inv_t, __uint_as_float(r[j + 3]) * p.inv_t);
+                        fence_async_store();
+                        __syncwarp();
+                        if (lane == 0) tma_store_2d(&tmZ, to, col0, m * BM + q * 32);
+                        box ^= 1;
+                    }
+                }
+            }
+            pipe_acc_release(g, i, tempty_first);
+        }
+        if (cur >= 0) {
+            const int was = (PAIR ? 2 * cur + rank : cur) * BM + rit;
+            if (was < p.rows) st.put(state_of(was));
+        }
+        // rows that this CTA never saw get an empty state, so that the merge reads nothing stale
+        for (int mt = 0; mt < p.num_mt; ++mt) {
+            if ((seen[q][mt >> 5] >> (mt & 31)) & 1) continue;
+            const int row = (PAIR ? 2 * mt + rank : mt) * BM + rit;
+            if (row < p.rows) {
+                State<KT> none;
+                none.clear();
+                none.put(state_of(row));
+            }
+        }
+        if constexpr (Z) {
+            if (lane == 0) tma_store_wait_all();
+        }
+    }
+    pipe_end<PAIR>(g, tmem_base);
+}
+
+// Weight rows per tile: as few waves of as equal work as there are.  step 16
+// (two heights) for a sweep that keeps nothing; tiles whose logits leave in
+// boxes of 32 columns have one height, a multiple of 32.
+struct Tiles {
+    int num_n, bn, nbig, step;
+};
+Tiles tiles_of(int V, int slots, int num_mt, bool z) {
+    Tiles t{};
+    if (!z && V >= slots * BN_MIN && num_mt == 1) {
+        // the same number of tiles for every CTA, of two heights 16 apart
+        const int T = slots * cdiv(V, (long)slots * BN);
+        const int h = V / T / 16 * 16;
+        t.num_n = T;
+        t.step = 16;
+        t.bn = T * h == V ? h : h + 16;
+        t.nbig = T * h == V ? T : cdiv(V - (long)T * h, 16);
+        return t;
+    }
+    long best = -1;
+    const int by = z ? 32 : 16;
+    for (int bn = BN; bn >= BN_MIN; bn -= by) {
+        // a tile's fixed cost stands for 16 weight rows
+        const long cost = (long)cdiv((long)num_mt * cdiv(V, bn), slots) * (bn + 16);
+        if (best < 0 || cost < best) {
+            best = cost;
+            t.bn = bn;
+        }
+    }
+    t.num_n = t.nbig = cdiv(V, t.bn);
+    return t;
+}
+
+template <int KT, bool ENT, bool Z>
+wf_status launch_kt(const SweepCall& c, int* slots_out, cudaStream_t s) {
+    static std::mutex mu;
+    static bool attr_set[64] = {false};
+    const wf_status cst = configure_once(mu, attr_set, [] {
+        return cudaFuncSetAttribute(sweep_kernel<KT, ENT, Z, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    PIPE_SMEM_MAX - PIPE_STATIC_MAX) == cudaSuccess &&
+               cudaFuncSetAttribute(sweep_kernel<KT, ENT, Z, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    PIPE_SMEM_MAX - PIPE_STATIC_MAX) == cudaSuccess;
+    });
+    if (cst != WF_OK) return cst;
+    const bool pair = c.rows > BM;
+    SweepParams p{};
+    p.rows = c.rows;
+    p.V = c.V;
+    p.num_m = cdiv(c.rows, BM);
+    p.num_mt = pair ? cdiv(p.num_m, 2) : 1;
+    p.num_k = cdiv(c.d, BK);
+    const int a_rows = pair ? BM : (c.rows + 7) / 8 * 8;   // a short box reads no rows that are not there
+    p.a_bytes = a_rows * BK * 2;
+    const int b_bytes = (pair ? BN / 2 : BN) * BK * 2, extra = Z ? STAGING : 0;
+    p.stage_bytes = p.a_bytes + b_bytes;
+    p.stages = (PIPE_SMEM_MAX - PIPE_STATIC_MAX - PIPE_BARRIER_BYTES - 1024 - extra) / p.stage_bytes;
+    if (p.stages > PIPE_MAX_STAGES) p.stages = PIPE_MAX_STAGES;
+    const int smem = pipe_smem(p.stages, p.stage_bytes, extra);
+    int slots = 0;
+    if (pair) {
+        static std::mutex pmu;
+        static int pairs[64];
+        int dev = 0;
+        if (cudaGetDevice(&dev) != cudaSuccess) return WF_ERR_CUDA;
+        std::lock_guard<std::mutex> lock(pmu);
+        if (dev >= 64 || !pairs[dev]) {
+            slots = resident_pairs(reinterpret_cast<const void*>(sweep_kernel<KT, ENT, Z, true>), PIPE_THREADS, smem);
+            if (dev < 64) pairs[dev] = slots;
+        } else {
+            slots = pairs[dev];
+        }
+    } else {
+        slots = num_sms() < STATE_SLOTS ? num_sms() : STATE_SLOTS;
+    }
+    const Tiles t = tiles_of(c.V, slots, p.num_mt, Z);
+    p.num_n = t.num_n;
+    p.bn = t.bn;
+    p.nbig = t.nbig;
+    p.step = t.step;
+    const int units = p.num_mt * p.num_n;
+    if (units < slots) slots = units;
+    const int split = pair ? 2 : 1;
+    p.idesc = umma_idesc_bf16(split * BM, p.bn);
+    p.idesc_s = p.nbig < p.num_n ? umma_idesc_bf16(split * BM, p.bn - p.step) : p.idesc;
+    p.c = LOG2E * c.inv_t;
+    p.inv_t = c.inv_t;
+    p.pick = c.pick;
+    p.K = c.pick ? c.K : 0;
+    p.picked = c.picked;
+    p.states = c.states;
+    p.slots = slots;
+    p.ctrl = c.ctrl;
+    p.timeout_ns = wait_timeout_ns();
+    CUtensorMap ta, tb, tbs, tz;
+    if (!make_tile_map(&ta, c.act, c.rows, c.d, c.d, false, BK, a_rows) ||
+        !make_tile_map(&tb, c.W, c.V, c.d, c.d, false, BK, p.bn / split))
+        return WF_ERR_CUDA;
+    tbs = tb;
+    if (p.nbig < p.num_n && !make_tile_map(&tbs, c.W, c.V, c.d, c.d, false, BK, (p.bn - p.step) / split))
+        return WF_ERR_CUDA;
+    tz = ta;
+    if (Z && !make_tile_map(&tz, c.z, c.rows, c.V, c.ldz, true, 32, 32)) return WF_ERR_CUDA;
+    *slots_out = slots;
+    if (pair)
+        return launch_cluster(sweep_kernel<KT, ENT, Z, true>, dim3(2 * slots), dim3(PIPE_THREADS), smem, s, 2u, ta, tb,
+                              tbs, tz, p);
+    return launch(sweep_kernel<KT, ENT, Z, false>, dim3(slots), dim3(PIPE_THREADS), smem, s, ta, tb, tbs, tz, p);
+}
+
+}  // namespace
+
+wf_status launch_sweep(const SweepCall& c, int* slots, cudaStream_t s) {
+    if (c.z) return launch_kt<0, false, true>(c, slots, s);
+    if (!c.entropy) return launch_kt<0, false, false>(c, slots, s);
+    if (c.k == 0) return launch_kt<0, true, false>(c, slots, s);
+    if (c.k <= 10) return launch_kt<10, true, false>(c, slots, s);
+    return launch_kt<16, true, false>(c, slots, s);
+}
+
+static PFN_cuTensorMapEncodeTiled_v12000 tile_encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) !=
+                cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            f = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    }();
+    return fn;
+}
+
+bool make_tile_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t stride, bool fp32,
+                   uint32_t box_cols, uint32_t box_rows) {
+    auto enc = tile_encoder();
+    if (!enc) return false;
+    cuuint64_t dims[2] = {cols, rows};
+    cuuint64_t strides[1] = {stride * (fp32 ? 4 : 2)};
+    cuuint32_t box[2] = {box_cols, box_rows};
+    cuuint32_t estr[2] = {1, 1};
+    return enc(map, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2,
+               const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int resident_pairs(const void* kernel, int threads, int smem) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(2 * 64);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        cudaGetLastError();
+        n = num_sms() / 2;
+    }
+    return n < REC_PAIRS ? n : REC_PAIRS;
+}
+
+}  // namespace wf

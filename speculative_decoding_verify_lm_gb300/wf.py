@@ -12,7 +12,7 @@ import ctypes
 import os
 import struct
 import threading
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -25,6 +25,7 @@ WF_MAX_SEQ_NODES = 256
 WF_MAX_TOPK = 16
 WF_KV_BF16, WF_KV_E4M3 = 0, 1
 WF_PAGED_MAX_SEQS = 4096
+WF_MAX_LISTED = 64
 STATUS = {0: "WF_OK", 1: "WF_ERR_INVALID_ARG", 2: "WF_ERR_WORKSPACE", 3: "WF_ERR_CUDA", 4: "WF_ERR_UNSUPPORTED",
           5: "WF_ERR_BAD_DATA", 6: "WF_ERR_TIMEOUT"}
 
@@ -89,6 +90,25 @@ class PagedAttnArgs(ctypes.Structure):
     ]
 
 
+class LogprobsArgs(ctypes.Structure):
+    """Mirror of ``wf_logprobs_args``."""
+    _fields_ = [
+        ("hidden", _c_void_p), ("W", _c_void_p), ("P", _i32), ("d", _i32), ("V", _i32), ("temperature", _f32),
+        ("tok", _c_void_p), ("S", _i32), ("k", _i32), ("logp", _c_void_p), ("lse", _c_void_p), ("H", _c_void_p),
+        ("top_ids", _c_void_p), ("top_logp", _c_void_p),
+    ]
+
+
+class DistillArgs(ctypes.Structure):
+    """Mirror of ``wf_distill_args``."""
+    _fields_ = [
+        ("x", _c_void_p), ("Wd", _c_void_p), ("N", _i32), ("d", _i32), ("Vd", _i32), ("tid", _c_void_p),
+        ("tlogit", _c_void_p), ("k", _i32), ("t2d", _c_void_p), ("V", _i32), ("temperature", _f32), ("z", _c_void_p),
+        ("ldz", ctypes.c_int64), ("lse", _c_void_p), ("loss", _c_void_p), ("gloss", _c_void_p), ("dx", _c_void_p),
+        ("dWd", _c_void_p),
+    ]
+
+
 # the same bytes as PagedAttnArgs
 _PAGED_ATTN = struct.Struct("@PqiiPPPPPiifPP")
 
@@ -136,6 +156,11 @@ _SIGS = {
     "wf_pages_fork": (_i32, [ctypes.POINTER(PagedCacheArgs), _c_void_p, _c_void_p, _i32, _c_void_p, _c_void_p, _sz,
                              _c_void_p]),
     "wf_pages_trim": (_i32, [ctypes.POINTER(PagedCacheArgs), _c_void_p, _c_void_p, _sz, _c_void_p]),
+    "wf_logprobs_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
+    "wf_lmhead_logprobs": (_i32, [ctypes.POINTER(LogprobsArgs), _c_void_p, _sz, _c_void_p]),
+    "wf_distill_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
+    "wf_draft_distill": (_i32, [ctypes.POINTER(DistillArgs), _c_void_p, _sz, _c_void_p]),
+    "wf_draft_distill_grad": (_i32, [ctypes.POINTER(DistillArgs), _c_void_p, _sz, _c_void_p]),
 }
 
 
@@ -435,6 +460,157 @@ def wf_lmhead_draft_topk(hidden, W, x, Wd, d2t, k: int, ws: Workspace, ids=None,
                                     _stream(stream))
     _raise(st, "wf_lmhead_draft_topk")
     return ids, draft_ids, tids, vals
+
+
+class LogprobsWorkspace(Workspace):
+    """Workspace of wf_lmhead_logprobs for P rows of d, V ids, lists of S given tokens and k alternatives.  Those
+    calls take no other workspace, and other calls not this one."""
+
+    def __init__(self, P: int, d: int, V: int, S: int = 0, k: int = 0, device=None, stream=None):
+        self.nbytes = int(lib().wf_logprobs_workspace_bytes(P, d, V, S, k))
+        if self.nbytes == 0:
+            raise ValueError("log-probability shapes outside the library's range")
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device or "cuda")
+        # only its control block has to be zero
+        _raise(lib().wf_workspace_init(self.buf.data_ptr(), 256, _stream(stream)), "wf_workspace_init")
+
+
+class Logprobs(NamedTuple):
+    """What wf_lmhead_logprobs returns; None where it was not asked for."""
+    logp: Optional[torch.Tensor]
+    lse: torch.Tensor
+    H: Optional[torch.Tensor]
+    top_ids: Optional[torch.Tensor]
+    top_logp: Optional[torch.Tensor]
+
+
+def _own_ws(ws, kind):
+    if type(ws) is not kind:
+        raise ValueError(f"ws must be a {kind.__name__}")
+    return ws.buf.data_ptr(), ws.nbytes
+
+
+def _shaped(t, name, shape, dtypes, like):
+    """Address of a dense tensor of this shape on like's device."""
+    if t is None:
+        raise ValueError(f"{name} is required")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be on {like.device}")
+    return _check(t, name, dtypes)
+
+
+def _head(x, W, names):
+    if x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1]:
+        raise ValueError(f"{names[0]} must be [rows, d] and {names[1]} [ids, d]")
+    return _check(x, names[0], _BF16), _shaped(W, names[1], W.shape, _BF16, x)
+
+
+def wf_lmhead_logprobs(hidden, W, ws: LogprobsWorkspace, tok=None, k: int = 0, temperature: float = 1.0,
+                       with_entropy: bool = False, logp=None, lse=None, H=None, top_ids=None, top_logp=None,
+                       stream=None) -> Logprobs:
+    """Log-probabilities of given tokens tok [P] or [P, S] (-1: none) under softmax(hidden W^T / temperature), the
+    log-sum-exp, the entropy (with_entropy, or H given) and the k best alternatives of each row."""
+    hp, Wp = _head(hidden, W, ("hidden", "W"))
+    (P, d), V, dev = hidden.shape, W.shape[0], hidden.device
+    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
+    S, tp = 0, None
+    if tok is not None:
+        if tok.dim() not in (1, 2) or tok.shape[0] != P or (tok.dim() == 2 and not 1 <= tok.shape[1] <= WF_MAX_LISTED):
+            raise ValueError(f"tok must be [P] or [P, S], S up to {WF_MAX_LISTED}")
+        S = 1 if tok.dim() == 1 else tok.shape[1]
+        tp = _shaped(tok, "tok", tok.shape, _I32, hidden)
+        logp = new(tok.shape, torch.float32) if logp is None else logp
+    lse = new((P,), torch.float32) if lse is None else lse
+    if with_entropy and H is None:
+        H = new((P,), torch.float32)
+    if k:
+        top_ids = new((P, k), torch.int32) if top_ids is None else top_ids
+        top_logp = new((P, k), torch.float32) if top_logp is None else top_logp
+    args = LogprobsArgs(hp, Wp, P, d, V, float(temperature), tp, S, k,
+                        None if tok is None else _shaped(logp, "logp", tok.shape, _F32, hidden),
+                        _shaped(lse, "lse", (P,), _F32, hidden),
+                        None if H is None else _shaped(H, "H", (P,), _F32, hidden),
+                        _shaped(top_ids, "top_ids", (P, k), _I32, hidden) if k else None,
+                        _shaped(top_logp, "top_logp", (P, k), _F32, hidden) if k else None)
+    _raise((_lib or lib()).wf_lmhead_logprobs(ctypes.byref(args), *_own_ws(ws, LogprobsWorkspace), _stream(stream)),
+           "wf_lmhead_logprobs")
+    return Logprobs(logp if tok is not None else None, lse, H, top_ids if k else None, top_logp if k else None)
+
+
+class DistillWorkspace(Workspace):
+    """Workspace of wf_draft_distill and wf_draft_distill_grad for N rows of d, Vd draft ids and k alternatives of the
+    teacher.  Those calls take no other workspace, and other calls not this one."""
+
+    def __init__(self, N: int, d: int, Vd: int, k: int, device=None, stream=None):
+        self.nbytes = int(lib().wf_distill_workspace_bytes(N, d, Vd, k))
+        if self.nbytes == 0:
+            raise ValueError("distillation shapes outside the library's range")
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device or "cuda")
+        # only its control block has to be zero
+        _raise(lib().wf_workspace_init(self.buf.data_ptr(), 256, _stream(stream)), "wf_workspace_init")
+
+
+def distill_logits(N: int, Vd: int, device=None):
+    """A buffer for the logits that wf_draft_distill keeps for the gradients: [N, Vd rounded up to 4] fp32."""
+    return torch.empty((N, (Vd + 3) // 4 * 4), dtype=torch.float32, device=device or "cuda")
+
+
+def _distill(x, Wd, tid, tlogit, t2d, temperature, z, lse, **more):
+    xp, wp = _head(x, Wd, ("x", "Wd"))
+    (N, d), Vd = x.shape, Wd.shape[0]
+    if tid.dim() != 2 or tid.shape[0] != N or not 1 <= tid.shape[1] <= WF_MAX_LISTED:
+        raise ValueError(f"tid must be [N, k], k up to {WF_MAX_LISTED}")
+    if z is not None and (z.dim() != 2 or z.shape[0] != N or z.shape[1] < Vd or z.shape[1] % 4):
+        raise ValueError("z must be [N, ldz], ldz a multiple of 4 from Vd on")
+    if t2d is not None and (t2d.dim() != 1 or t2d.numel() == 0):
+        raise ValueError("t2d must be [V]")
+    return DistillArgs(xp, wp, N, d, Vd, _shaped(tid, "tid", tid.shape, _I32, x),
+                       _shaped(tlogit, "tlogit", tid.shape, _F32, x), tid.shape[1],
+                       None if t2d is None else _shaped(t2d, "t2d", t2d.shape, _I32, x),
+                       0 if t2d is None else t2d.numel(), float(temperature),
+                       None if z is None else _shaped(z, "z", z.shape, _F32, x), 0 if z is None else z.shape[1],
+                       _shaped(lse, "lse", (N,), _F32, x), **more)
+
+
+def wf_draft_distill(x, Wd, tid, tlogit, ws: DistillWorkspace, t2d=None, temperature: float = 1.0, z=None, loss=None,
+                     lse=None, stream=None):
+    """Distillation loss of the draft head against a teacher's top logits -> (loss [N], lse [N]).
+
+    x [N, d], Wd [Vd, d] bf16; tid, tlogit [N, k]: the teacher's alternatives (-1: none), target ids if t2d [V] is
+    given.  z (distill_logits) keeps the logits for wf_draft_distill_grad."""
+    N = x.shape[0]
+    loss = torch.empty(N, dtype=torch.float32, device=x.device) if loss is None else loss
+    lse = torch.empty(N, dtype=torch.float32, device=x.device) if lse is None else lse
+    args = _distill(x, Wd, tid, tlogit, t2d, temperature, z, lse, loss=_shaped(loss, "loss", (N,), _F32, x))
+    _raise((_lib or lib()).wf_draft_distill(ctypes.byref(args), *_own_ws(ws, DistillWorkspace), _stream(stream)),
+           "wf_draft_distill")
+    return loss, lse
+
+
+def wf_draft_distill_grad(x, Wd, tid, tlogit, z, lse, ws: DistillWorkspace, gloss=None, t2d=None,
+                          temperature: float = 1.0, dx=None, dWd=None, need_dx: bool = True, need_dWd: bool = True,
+                          stream=None):
+    """Gradients of the distillation loss -> (dx [N, d] or None, dWd [Vd, d] or None), bf16.
+
+    z and lse as wf_draft_distill left them; gloss [N]: the derivative of what is minimised by each row's loss (None:
+    1).  The other arguments as they were there."""
+    if z is None:
+        raise ValueError("z is required")
+    if not (need_dx or need_dWd):
+        raise ValueError("neither dx nor dWd is asked for")
+    if need_dx and dx is None:
+        dx = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+    if need_dWd and dWd is None:
+        dWd = torch.empty(Wd.shape, dtype=torch.bfloat16, device=x.device)
+    args = _distill(x, Wd, tid, tlogit, t2d, temperature, z, lse,
+                    gloss=None if gloss is None else _shaped(gloss, "gloss", (x.shape[0],), _F32, x),
+                    dx=_shaped(dx, "dx", x.shape, _BF16, x) if need_dx else None,
+                    dWd=_shaped(dWd, "dWd", Wd.shape, _BF16, x) if need_dWd else None)
+    _raise((_lib or lib()).wf_draft_distill_grad(ctypes.byref(args), *_own_ws(ws, DistillWorkspace), _stream(stream)),
+           "wf_draft_distill_grad")
+    return dx if need_dx else None, dWd if need_dWd else None
 
 
 class CatchupWorkspace(Workspace):
