@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1)
         tma_prefetch_desc(&tmDw);
     }
     const uint32_t tmem_base = pipe_begin<true>(g);
-    pdl_wait();
+    if (warp != 0) pdl_wait();   // warp 0: as it copies
     pdl_trigger();
     if (warp == 0) {
         if (lane == 0) {
@@ -190,7 +190,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1)
             Unit u{};
             auto next = [&](int i) { return unit_at(p, slot, slots, i, u) ? u.kb : 0; };
             auto tx = [&]() { return (uint32_t)(2 * PROD_STAGE); };
-            auto load = [&](int kc, int s, uint32_t bar) {
+            auto load_a = [&](int kc, int s, uint32_t bar) {
                 const int k = (u.k0 + kc) * BK;
                 if (u.dx) {
                     pipe_load<true>(g.a(s), &tmGk, bar, k, u.row0 + rank * BM, pol);
@@ -199,12 +199,15 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1)
                     for (int h = 0; h < 2; ++h)
                         pipe_load<true>(g.a(s) + h * 8192, &tmGm, bar, u.row0 + rank * BM + 64 * h, k, pol);
                 }
+            };
+            auto load_b = [&](int kc, int s, uint32_t bar) {
+                const int k = (u.k0 + kc) * BK;
                 const CUtensorMap* b = u.dx ? &tmW : &tmX;
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
                     pipe_load<true>(g.b(s) + h * 8192, b, bar, u.col0 + rank * (TN / 2) + 64 * h, k, pol);
             };
-            pipe_copy<true>(g, first, next, tx, load);
+            pipe_copy<true, false>(g, first, next, tx, load_a, load_b);
         }
     } else if (warp == 1) {
         if (lane == 0 && first) {

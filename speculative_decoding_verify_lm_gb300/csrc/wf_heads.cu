@@ -143,9 +143,10 @@ __global__ void __launch_bounds__(LIST_WARPS * 32) teacher_kernel(const TeacherC
     }
 }
 
-// One CTA a row: each thread takes the states of its slots, a fixed order of
-// merging makes the result the same in every run.
-constexpr int MERGE_WARPS = 4;
+// One CTA a row, one thread a state; a fixed order of merging makes the result
+// the same in every run.
+constexpr int MERGE_WARPS = STATE_SLOTS / 32;   // as many of them as the row has states
+static_assert(MERGE_WARPS * 32 >= STATE_SLOTS && MERGE_WARPS * 32 >= REC_PAIRS, "a thread for every state");
 
 template <int KT>
 __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const MergeCall c) {
@@ -153,33 +154,27 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const Me
     __shared__ uint64_t wbest[MERGE_WARPS * 16];
     pdl_wait();
     pdl_trigger();
-    const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const float cc = LOG2E * c.inv_t;
     float M = -INFINITY, S = 0.f, T = 0.f;
-    uint64_t loc[KT > 0 ? KT : 1];
+    uint64_t loc[KT > 0 ? KT : 1];   // the state's list, best first
 #pragma unroll
     for (int j = 0; j < KT; ++j) loc[j] = 0;
-    for (int sl = threadIdx.x; sl < c.slots; sl += MERGE_WARPS * 32) {
-        const float4* at = reinterpret_cast<const float4*>(c.states + ((size_t)row * c.slots + sl) * state_bytes(KT));
+    if ((int)threadIdx.x < c.slots) {
+        const float4* at =
+            reinterpret_cast<const float4*>(c.states + ((size_t)row * c.slots + threadIdx.x) * state_bytes(KT));
         const float4 h = at[0];
         float4 e[KT > 0 ? KT / 2 : 1];
 #pragma unroll
         for (int j = 0; j < KT / 2; ++j) e[j] = at[1 + j];
-        state_merge(cc, M, S, T, h.x, h.y, h.z);
+        M = h.x;
+        S = h.y;
+        T = h.z;
 #pragma unroll
         for (int j = 0; j < KT; ++j) {
             const float4 f = e[j / 2];
-            const float v = j & 1 ? f.z : f.x;
             const int id = __float_as_int(j & 1 ? f.w : f.y);
-            const uint64_t key = id < 0 ? 0ull : pack_key(v, (uint32_t)id);
-            if (key > loc[KT > 0 ? KT - 1 : 0]) {
-#pragma unroll
-                for (int s = KT - 1; s > 0; --s) {
-                    const bool shift = loc[s - 1] < key, land = !shift && loc[s] < key;
-                    loc[s] = shift ? loc[s - 1] : (land ? key : loc[s]);
-                }
-                if (loc[0] < key) loc[0] = key;
-            }
+            loc[j] = id < 0 ? 0ull : pack_key(j & 1 ? f.z : f.x, (uint32_t)id);
         }
     }
 #pragma unroll
@@ -221,8 +216,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const Me
     M = wm[0];
     S = wsum[0];
     T = wt[0];
-#pragma unroll
-    for (int w = 1; w < MERGE_WARPS; ++w) state_merge(cc, M, S, T, wm[w], wsum[w], wt[w]);
+    for (int w = 1; w < warps; ++w) state_merge(cc, M, S, T, wm[w], wsum[w], wt[w]);
     const float logs = logf(S), ref = state_ref(M, cc);
     auto logq = [&](float v) { return fmaf(fmaf(v, cc, -ref), LN2, -logs); };
     if (threadIdx.x == 0) {
@@ -231,8 +225,8 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const Me
     }
     if constexpr (KT > 0) {
         // each of the warps' winners finds its place among all of them
-        const int n = MERGE_WARPS * c.k;
-        if ((int)threadIdx.x < n) {
+        const int n = warps * c.k;
+        if ((int)threadIdx.x < n) {   // k <= 16 a warp: a thread for each
             const uint64_t key = wbest[threadIdx.x];
             int place = 0;
             for (int j = 0; j < n; ++j) place += wbest[j] > key || (wbest[j] == key && j < (int)threadIdx.x);
@@ -245,7 +239,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const Me
         }
     }
     if (c.logp) {
-        for (int j = threadIdx.x; j < c.K; j += MERGE_WARPS * 32) {
+        for (int j = threadIdx.x; j < c.K; j += blockDim.x) {
             const size_t at = (size_t)row * c.K + j;
             const int id = c.ids[at];
             if (c.order) {
@@ -287,10 +281,11 @@ wf_status launch_teacher(const TeacherCall& t, cudaStream_t s) {
 }
 
 wf_status launch_states_merge(const MergeCall& c, cudaStream_t s) {
+    const dim3 block(cdiv(c.slots, 32) * 32);
     switch (state_width(c.k)) {
-        case 0: return launch(states_merge_kernel<0>, dim3(c.rows), dim3(MERGE_WARPS * 32), 0, s, c);
-        case 10: return launch(states_merge_kernel<10>, dim3(c.rows), dim3(MERGE_WARPS * 32), 0, s, c);
-        default: return launch(states_merge_kernel<16>, dim3(c.rows), dim3(MERGE_WARPS * 32), 0, s, c);
+        case 0: return launch(states_merge_kernel<0>, dim3(c.rows), block, 0, s, c);
+        case 10: return launch(states_merge_kernel<10>, dim3(c.rows), block, 0, s, c);
+        default: return launch(states_merge_kernel<16>, dim3(c.rows), block, 0, s, c);
     }
 }
 

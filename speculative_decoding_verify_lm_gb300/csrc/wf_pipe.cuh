@@ -119,19 +119,31 @@ __device__ __forceinline__ void pipe_end(const Pipe& g, uint32_t tmem_base) {
 
 // The copying thread.  next(i) sets up the CTA's i-th tile and returns its K
 // blocks (0: no further tile); tx() is what a stage of it receives in bytes
-// (PAIR: both CTAs together); load(kc, s, bar) issues its copies into stage s,
-// counted on the barrier at shared address `bar` (PAIR: the first CTA's).
-template <bool PAIR, typename Next, typename Tx, typename Load>
-__device__ __forceinline__ void pipe_copy(const Pipe& g, bool first, Next next, Tx tx, Load load) {
+// (PAIR: both CTAs together); load_a(kc, s, bar) and load_b(kc, s, bar) issue
+// the copies of its operands into stage s, counted on the barrier at shared
+// address `bar` (PAIR: the first CTA's).
+// EARLY: B is a weight matrix, whose first stages are asked for while the kernel
+// before is still finishing; everything else waits for it.
+template <bool PAIR, bool EARLY, typename Next, typename Tx, typename LoadA, typename LoadB>
+__device__ __forceinline__ void pipe_copy(const Pipe& g, bool first, Next next, Tx tx, LoadA load_a, LoadB load_b) {
     const uint32_t full0 = PAIR ? cluster_addr(&g.full[0], 0) : smem_u32(&g.full[0]);
+    auto bar = [&](int s) { return full0 + (uint32_t)(s * sizeof(uint64_t)); };
+    int num_k = next(0);
+    uint32_t bytes = tx();
+    int early = 0;
+    if constexpr (EARLY) {
+        early = num_k < g.stages ? num_k : g.stages;
+        for (int s = 0; s < early; ++s) {
+            if (!PAIR || first) mbar_arrive_expect_tx(&g.full[s], bytes);
+            load_b(s, s, bar(s));
+        }
+    }
+    pdl_wait();
     uint32_t it = 0;   // stages issued so far
     int s = 0;         // = it % stages
     uint32_t ph = 0;   // = (it / stages) & 1
     bool ok = true;
-    for (int i = 0; ok; ++i) {
-        const int num_k = next(i);
-        if (num_k == 0) break;
-        const uint32_t bytes = tx();
+    for (int i = 0; ok && num_k > 0;) {
         for (int kc = 0; kc < num_k; ++kc, ++it) {
             if (it > 0 && ++s == g.stages) {
                 s = 0;
@@ -142,9 +154,14 @@ __device__ __forceinline__ void pipe_copy(const Pipe& g, bool first, Next next, 
                 ok = false;
                 break;
             }
-            if (!PAIR || first) mbar_arrive_expect_tx(&g.full[s], bytes);
-            load(kc, s, full0 + (uint32_t)(s * sizeof(uint64_t)));
+            if (!EARLY || it >= (uint32_t)early) {
+                if (!PAIR || first) mbar_arrive_expect_tx(&g.full[s], bytes);
+                load_b(kc, s, bar(s));
+            }
+            load_a(kc, s, bar(s));
         }
+        num_k = next(++i);
+        bytes = tx();
     }
     if (!ok || *g.abort_flag) {
         // let every copy this thread issued land before the CTA exits

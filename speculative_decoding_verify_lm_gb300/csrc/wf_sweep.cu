@@ -51,6 +51,18 @@ __device__ __forceinline__ Span span(const SweepParams& p, int n) {
     return {p.nbig * p.bn + (n - p.nbig) * h, h, false};
 }
 
+// r[j] for a j that is known only at run time: five levels of selects.
+__device__ __forceinline__ uint32_t column(const uint32_t (&r)[32], int j) {
+    uint32_t a[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) a[i] = j & 1 ? r[2 * i + 1] : r[2 * i];
+#pragma unroll
+    for (int w = 8, bit = 2; w >= 1; w >>= 1, bit <<= 1)
+#pragma unroll
+        for (int i = 0; i < w; ++i) a[i] = j & bit ? a[2 * i + 1] : a[2 * i];
+    return a[0];
+}
+
 // Insert (v, id) into a descending list; the earlier entry wins ties.
 template <int KT>
 __device__ __forceinline__ void insert(float (&tv)[KT], int (&ti)[KT], float v, int id) {
@@ -111,9 +123,44 @@ struct State {
     }
 };
 
-// Fold 32 columns (the first lim of them) into a row's state.
+// A bound that the KT-th best of a tile's columns reaches: the KT-th largest of
+// 32 maxima, each over the columns 32 apart, which are KT different columns.  An
+// empty list would take nearly every column of its first chunks; held to this
+// bound it takes about KT + 3 of 256.  A number just below the bound is returned,
+// to be exceeded.
+template <int KT>
+__device__ __forceinline__ float first_bound(uint32_t tbase, int cols) {
+    float top[32], best[KT];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) top[j] = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < KT; ++j) best[j] = -INFINITY;
+    for (int c0 = 0; c0 + 32 <= cols; c0 += 32) {
+        uint32_t r[32];
+        tmem_ld_32x32b_x32(tbase + c0, r);
+        tmem_ld_wait();
+#pragma unroll
+        for (int j = 0; j < 32; ++j) top[j] = fmaxf(top[j], __uint_as_float(r[j]));
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) {
+        float v = top[j];
+#pragma unroll
+        for (int i = 0; i < KT; ++i) {
+            const float hi = fmaxf(best[i], v);
+            v = fminf(best[i], v);
+            best[i] = hi;
+        }
+    }
+    const uint32_t order = f32_order(best[KT - 1]);
+    return best[KT - 1] == -INFINITY ? -INFINITY : f32_unorder(order - 1);
+}
+
+// Fold 32 columns (the first lim of them) into a row's state; only columns above
+// `bound` are candidates for its list.
 template <int KT, bool ENT, bool FULL>
-__device__ __forceinline__ void fold(const uint32_t (&r)[32], int lim, int col0, float c, State<KT>& st) {
+__device__ __forceinline__ void fold(const uint32_t (&r)[32], int lim, int col0, float c, float bound,
+                                     State<KT>& st) {
     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
     for (int j = 0; j < 32; ++j)
@@ -141,13 +188,25 @@ __device__ __forceinline__ void fold(const uint32_t (&r)[32], int lim, int col0,
     st.S += (s4[0] + s4[1]) + (s4[2] + s4[3]);
     if constexpr (ENT) st.T += (t4[0] + t4[1]) + (t4[2] + t4[3]);
     if constexpr (KT > 0) {
-        if (mx > st.tv[KT - 1]) {
+        // Columns above the row's k-th best as a mask; then every row of the warp
+        // takes its next one at the same time, so a chunk costs as many rounds as
+        // its busiest row has candidates (one or two once a few tiles are seen).
+        // Inserting column by column, which any of 32 rows can ask for, took 2.2
+        // times as long as the tile's products (1,248 rows: 1,065 us a call).
+        const float least = fmaxf(st.tv[KT - 1], bound);
+        uint32_t cand = 0;
+        if (__any_sync(0xffffffffu, mx > least)) {
 #pragma unroll
             for (int j = 0; j < 32; ++j)
-                if (FULL || j < lim) {
-                    const float v = __uint_as_float(r[j]);
-                    if (v > st.tv[KT - 1]) insert<KT>(st.tv, st.ti, v, col0 + j);
-                }
+                if (FULL || j < lim) cand |= __uint_as_float(r[j]) > least ? 1u << j : 0u;
+        }
+        while (__any_sync(0xffffffffu, cand != 0)) {
+            if (cand) {
+                const int j = __ffs((int)cand) - 1;
+                cand &= cand - 1;
+                const float v = __uint_as_float(column(r, j));
+                if (v > st.tv[KT - 1]) insert<KT>(st.tv, st.ti, v, col0 + j);
+            }
         }
     }
 }
@@ -173,7 +232,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1)
         if constexpr (Z) tma_prefetch_desc(&tmZ);
     }
     const uint32_t tmem_base = pipe_begin<PAIR>(g);
-    pdl_wait();
+    if (warp != 0) pdl_wait();   // warp 0: when it has asked for its first weights
     pdl_trigger();
 
     if (warp == 0) {
@@ -189,12 +248,14 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1)
                 return p.num_k;
             };
             auto tx = [&]() { return (uint32_t)((PAIR ? 2 : 1) * p.a_bytes + sp.rows * BK * 2); };
-            auto load = [&](int kc, int s, uint32_t bar) {
-                const int half = PAIR ? sp.rows / 2 : 0;
+            auto load_a = [&](int kc, int s, uint32_t bar) {
                 pipe_load<PAIR>(g.a(s), &tmA, bar, kc * BK, m * BM, pol_a);
+            };
+            auto load_b = [&](int kc, int s, uint32_t bar) {
+                const int half = PAIR ? sp.rows / 2 : 0;
                 pipe_load<PAIR>(g.b(s), sp.big ? &tmB : &tmBs, bar, kc * BK, sp.row0 + rank * half, pol_w);
             };
-            pipe_copy<PAIR>(g, first, next, tx, load);
+            pipe_copy<PAIR, true>(g, first, next, tx, load_a, load_b);
         }
     } else if (warp == 1) {
         if (lane == 0 && first) {
@@ -236,6 +297,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1)
             const Span sp = span(p, u / p.num_mt);
             const int row = m * BM + rit;
             const bool warp_live = m * BM + q * 32 < p.rows, live = row < p.rows;
+            bool fresh = false;   // the list is empty
             if (mt != cur) {
                 if (cur >= 0) {
                     const int was = (PAIR ? 2 * cur + rank : cur) * BM + rit;
@@ -244,6 +306,7 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1)
                 if ((seen[q][mt >> 5] >> (mt & 31)) & 1) {
                     if (live) st.get(state_of(row));
                 } else {
+                    fresh = true;
                     st.clear();
                     __syncwarp();
                     if (lane == 0) seen[q][mt >> 5] |= 1u << (mt & 31);
@@ -277,22 +340,22 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1)
             if (warp_live) {
                 const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (i & 1) * BN;
                 const int cols = min(sp.rows, p.V - sp.row0);
+                float bound = -INFINITY;
+                if constexpr (KT > 0) {
+                    if (fresh) bound = first_bound<KT>(tbase, cols);
+                }
                 for (int c0 = 0; c0 < cols; c0 += 32) {
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(tbase + c0, r);
                     tmem_ld_wait();
                     const int col0 = sp.row0 + c0, lim = min(32, cols - c0);
                     if (lim == 32)
-                        fold<KT, ENT, true>(r, 32, col0, p.c, st);
+                        fold<KT, ENT, true>(r, 32, col0, p.c, bound, st);
                     else
-                        fold<KT, ENT, false>(r, lim, col0, p.c, st);
+                        fold<KT, ENT, false>(r, lim, col0, p.c, bound, st);
                     while (__any_sync(0xffffffffu, next_id < col0 + lim)) {
                         if (next_id < col0 + lim) {
-                            const int j0 = next_id - col0;
-                            uint32_t v = r[0];
-#pragma unroll
-                            for (int j = 1; j < 32; ++j) v = j == j0 ? r[j] : v;
-                            p.picked[(size_t)row * p.K + at] = __uint_as_float(v);
+                            p.picked[(size_t)row * p.K + at] = __uint_as_float(column(r, next_id - col0));
                             ++at;
                             next_id = at < p.K ? list[at] : PICK_NONE;
                         }
@@ -338,35 +401,38 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1)
     pipe_end<PAIR>(g, tmem_base);
 }
 
-// Weight rows per tile: as few waves of as equal work as there are.  step 16
-// (two heights) for a sweep that keeps nothing; tiles whose logits leave in
-// boxes of 32 columns have one height, a multiple of 32.
+// Weight rows per tile: as many tiles as the CTAs (or pairs) take in the fewest
+// rounds, so that every CTA gets about the same rows in each.  Tiles have one of
+// two heights, `step` apart: 16, or 32 where logits leave in boxes of 32 columns.
+// (2,048 rows over 32,000 ids: 125 tiles of 256 are 13.2 rounds for 76 pairs; 133
+// of 240 or 256 are 14 full ones.  Tiles of one smaller height that fill the
+// rounds, 192 of them, took 236 us a call, since both operands cross to the SMs
+// once for each tile.)
 struct Tiles {
     int num_n, bn, nbig, step;
 };
+constexpr int MIN_TILE = 64;
 Tiles tiles_of(int V, int slots, int num_mt, bool z) {
     Tiles t{};
-    if (!z && V >= slots * BN_MIN && num_mt == 1) {
-        // the same number of tiles for every CTA, of two heights 16 apart
-        const int T = slots * cdiv(V, (long)slots * BN);
-        const int h = V / T / 16 * 16;
-        t.num_n = T;
-        t.step = 16;
-        t.bn = T * h == V ? h : h + 16;
-        t.nbig = T * h == V ? T : cdiv(V - (long)T * h, 16);
+    t.step = z ? 32 : 16;
+    const long rounds = cdiv((long)num_mt * cdiv(V, BN), slots);
+    long n = rounds * slots / num_mt;
+    if (n > V / MIN_TILE) n = V / MIN_TILE;
+    const int least = cdiv(V, BN);
+    if (n < least) n = least;
+    t.num_n = (int)n;
+    if (V < MIN_TILE) {
+        t.bn = MIN_TILE;
+        t.nbig = t.num_n;
         return t;
     }
-    long best = -1;
-    const int by = z ? 32 : 16;
-    for (int bn = BN; bn >= BN_MIN; bn -= by) {
-        // a tile's fixed cost stands for 16 weight rows
-        const long cost = (long)cdiv((long)num_mt * cdiv(V, bn), slots) * (bn + 16);
-        if (best < 0 || cost < best) {
-            best = cost;
-            t.bn = bn;
-        }
+    const int h = (int)(V / n) / t.step * t.step;   // at least MIN_TILE
+    t.bn = h + t.step;
+    t.nbig = cdiv(V - n * h, t.step);
+    if (t.nbig == 0) {
+        t.bn = h;
+        t.nbig = t.num_n;
     }
-    t.num_n = t.nbig = cdiv(V, t.bn);
     return t;
 }
 
