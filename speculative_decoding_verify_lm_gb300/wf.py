@@ -111,6 +111,9 @@ class DistillArgs(ctypes.Structure):
 
 # the same bytes as PagedAttnArgs
 _PAGED_ATTN = struct.Struct("@PqiiPPPPPiifPP")
+# ... as LogprobsArgs and as DistillArgs
+_LOGPROBS = struct.Struct("@PPiiifPiiPPPPP")
+_DISTILL = struct.Struct("@PPiiiPPiPifPqPPPPP")
 
 _SIGS = {
     "wf_status_string": (ctypes.c_char_p, [_i32]),
@@ -157,10 +160,10 @@ _SIGS = {
                              _c_void_p]),
     "wf_pages_trim": (_i32, [ctypes.POINTER(PagedCacheArgs), _c_void_p, _c_void_p, _sz, _c_void_p]),
     "wf_logprobs_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32, _i32]),
-    "wf_lmhead_logprobs": (_i32, [ctypes.POINTER(LogprobsArgs), _c_void_p, _sz, _c_void_p]),
+    "wf_lmhead_logprobs": (_i32, [_c_void_p, _c_void_p, _sz, _c_void_p]),
     "wf_distill_workspace_bytes": (_sz, [_i32, _i32, _i32, _i32]),
-    "wf_draft_distill": (_i32, [ctypes.POINTER(DistillArgs), _c_void_p, _sz, _c_void_p]),
-    "wf_draft_distill_grad": (_i32, [ctypes.POINTER(DistillArgs), _c_void_p, _sz, _c_void_p]),
+    "wf_draft_distill": (_i32, [_c_void_p, _c_void_p, _sz, _c_void_p]),
+    "wf_draft_distill_grad": (_i32, [_c_void_p, _c_void_p, _sz, _c_void_p]),
 }
 
 
@@ -491,14 +494,16 @@ def _own_ws(ws, kind):
 
 
 def _shaped(t, name, shape, dtypes, like):
-    """Address of a dense tensor of this shape on like's device."""
+    """Address of a dense tensor of this shape on like's device (like is a CUDA tensor)."""
     if t is None:
         raise ValueError(f"{name} is required")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
     if t.device != like.device:
         raise ValueError(f"{name} must be on {like.device}")
-    return _check(t, name, dtypes)
+    if t.dtype not in dtypes or not t.is_contiguous():
+        return _check(t, name, dtypes)
+    return t.data_ptr() or _check(t, name, dtypes)
 
 
 def _head(x, W, names):
@@ -511,32 +516,58 @@ def wf_lmhead_logprobs(hidden, W, ws: LogprobsWorkspace, tok=None, k: int = 0, t
                        with_entropy: bool = False, logp=None, lse=None, H=None, top_ids=None, top_logp=None,
                        stream=None) -> Logprobs:
     """Log-probabilities of given tokens tok [P] or [P, S] (-1: none) under softmax(hidden W^T / temperature), the
-    log-sum-exp, the entropy (with_entropy, or H given) and the k best alternatives of each row."""
+    log-sum-exp, the entropy (with_entropy, or H given) and the k best alternatives of each row.  Outputs not given
+    are allocated, in one piece."""
     hp, Wp = _head(hidden, W, ("hidden", "W"))
-    (P, d), V, dev = hidden.shape, W.shape[0], hidden.device
-    new = lambda shape, dt: torch.empty(shape, dtype=dt, device=dev)  # noqa: E731
-    S, tp = 0, None
+    (P, d), V = hidden.shape, W.shape[0]
+    S = tp = 0
     if tok is not None:
-        if tok.dim() not in (1, 2) or tok.shape[0] != P or (tok.dim() == 2 and not 1 <= tok.shape[1] <= WF_MAX_LISTED):
+        shape = tok.shape
+        S = 1 if len(shape) == 1 else shape[1] if len(shape) == 2 else 0
+        if not 1 <= S <= WF_MAX_LISTED or shape[0] != P:
             raise ValueError(f"tok must be [P] or [P, S], S up to {WF_MAX_LISTED}")
-        S = 1 if tok.dim() == 1 else tok.shape[1]
-        tp = _shaped(tok, "tok", tok.shape, _I32, hidden)
-        logp = new(tok.shape, torch.float32) if logp is None else logp
-    lse = new((P,), torch.float32) if lse is None else lse
-    if with_entropy and H is None:
-        H = new((P,), torch.float32)
-    if k:
-        top_ids = new((P, k), torch.int32) if top_ids is None else top_ids
-        top_logp = new((P, k), torch.float32) if top_logp is None else top_logp
-    args = LogprobsArgs(hp, Wp, P, d, V, float(temperature), tp, S, k,
-                        None if tok is None else _shaped(logp, "logp", tok.shape, _F32, hidden),
-                        _shaped(lse, "lse", (P,), _F32, hidden),
-                        None if H is None else _shaped(H, "H", (P,), _F32, hidden),
-                        _shaped(top_ids, "top_ids", (P, k), _I32, hidden) if k else None,
-                        _shaped(top_logp, "top_logp", (P, k), _F32, hidden) if k else None)
-    _raise((_lib or lib()).wf_lmhead_logprobs(ctypes.byref(args), *_own_ws(ws, LogprobsWorkspace), _stream(stream)),
-           "wf_lmhead_logprobs")
-    return Logprobs(logp if tok is not None else None, lse, H, top_ids if k else None, top_logp if k else None)
+        tp = _shaped(tok, "tok", shape, _I32, hidden)
+    # what is not given: pieces of one allocation, which takes as long as each of five would
+    want = P * ((S if tok is not None and logp is None else 0) + (lse is None) + (with_entropy and H is None) +
+                (k if k > 0 and top_ids is None else 0) + (k if k > 0 and top_logp is None else 0))
+    buf = torch.empty(want, dtype=torch.float32, device=hidden.device) if want > 0 else None
+    base = buf.data_ptr() if want > 0 else 0
+    at = 0
+    lp = lsep = Hp = idp = tlp = 0
+    if tok is None:
+        logp = None
+    elif logp is None:
+        logp, lp = torch.as_strided(buf, shape, (S, 1) if len(shape) == 2 else (1,), at), base + 4 * at
+        at += P * S
+    else:
+        lp = _shaped(logp, "logp", shape, _F32, hidden)
+    if lse is None:
+        lse, lsep = torch.as_strided(buf, (P,), (1,), at), base + 4 * at
+        at += P
+    else:
+        lsep = _shaped(lse, "lse", (P,), _F32, hidden)
+    if H is not None:
+        Hp = _shaped(H, "H", (P,), _F32, hidden)
+    elif with_entropy:
+        H, Hp = torch.as_strided(buf, (P,), (1,), at), base + 4 * at
+        at += P
+    if k <= 0:
+        top_ids = top_logp = None
+    else:
+        if top_logp is None:
+            top_logp, tlp = torch.as_strided(buf, (P, k), (k, 1), at), base + 4 * at
+            at += P * k
+        else:
+            tlp = _shaped(top_logp, "top_logp", (P, k), _F32, hidden)
+        if top_ids is None:
+            top_ids, idp = torch.as_strided(buf.view(torch.int32), (P, k), (k, 1), at), base + 4 * at
+        else:
+            idp = _shaped(top_ids, "top_ids", (P, k), _I32, hidden)
+    args = _LOGPROBS.pack(hp, Wp, P, d, V, temperature, tp, S, k, lp, lsep, Hp, idp, tlp)
+    st = (_lib or lib()).wf_lmhead_logprobs(args, *_own_ws(ws, LogprobsWorkspace), _stream(stream))
+    if st:
+        _raise(st, "wf_lmhead_logprobs")
+    return Logprobs(logp, lse, H, top_ids, top_logp)
 
 
 class DistillWorkspace(Workspace):
@@ -557,21 +588,31 @@ def distill_logits(N: int, Vd: int, device=None):
     return torch.empty((N, (Vd + 3) // 4 * 4), dtype=torch.float32, device=device or "cuda")
 
 
-def _distill(x, Wd, tid, tlogit, t2d, temperature, z, lse, **more):
+def _distill(fn, x, Wd, tid, tlogit, t2d, temperature, z, lse, loss, gloss, dx, dWd, ws, stream):
     xp, wp = _head(x, Wd, ("x", "Wd"))
     (N, d), Vd = x.shape, Wd.shape[0]
-    if tid.dim() != 2 or tid.shape[0] != N or not 1 <= tid.shape[1] <= WF_MAX_LISTED:
+    shape, V, ldz = tid.shape, 0, 0
+    if len(shape) != 2 or shape[0] != N or not 1 <= shape[1] <= WF_MAX_LISTED:
         raise ValueError(f"tid must be [N, k], k up to {WF_MAX_LISTED}")
-    if z is not None and (z.dim() != 2 or z.shape[0] != N or z.shape[1] < Vd or z.shape[1] % 4):
-        raise ValueError("z must be [N, ldz], ldz a multiple of 4 from Vd on")
-    if t2d is not None and (t2d.dim() != 1 or t2d.numel() == 0):
-        raise ValueError("t2d must be [V]")
-    return DistillArgs(xp, wp, N, d, Vd, _shaped(tid, "tid", tid.shape, _I32, x),
-                       _shaped(tlogit, "tlogit", tid.shape, _F32, x), tid.shape[1],
-                       None if t2d is None else _shaped(t2d, "t2d", t2d.shape, _I32, x),
-                       0 if t2d is None else t2d.numel(), float(temperature),
-                       None if z is None else _shaped(z, "z", z.shape, _F32, x), 0 if z is None else z.shape[1],
-                       _shaped(lse, "lse", (N,), _F32, x), **more)
+    if z is not None:
+        if z.dim() != 2 or z.shape[0] != N or z.shape[1] < Vd or z.shape[1] % 4:
+            raise ValueError("z must be [N, ldz], ldz a multiple of 4 from Vd on")
+        ldz = z.shape[1]
+    if t2d is not None:
+        V = t2d.numel()
+        if t2d.dim() != 1 or V == 0:
+            raise ValueError("t2d must be [V]")
+    args = _DISTILL.pack(xp, wp, N, d, Vd, _shaped(tid, "tid", shape, _I32, x),
+                         _shaped(tlogit, "tlogit", shape, _F32, x), shape[1],
+                         _shaped(t2d, "t2d", t2d.shape, _I32, x) if V else 0, V, temperature,
+                         _shaped(z, "z", z.shape, _F32, x) if ldz else 0, ldz, _shaped(lse, "lse", (N,), _F32, x),
+                         _shaped(loss, "loss", (N,), _F32, x) if loss is not None else 0,
+                         _shaped(gloss, "gloss", (N,), _F32, x) if gloss is not None else 0,
+                         _shaped(dx, "dx", x.shape, _BF16, x) if dx is not None else 0,
+                         _shaped(dWd, "dWd", Wd.shape, _BF16, x) if dWd is not None else 0)
+    st = getattr(_lib or lib(), fn)(args, *_own_ws(ws, DistillWorkspace), _stream(stream))
+    if st:
+        _raise(st, fn)
 
 
 def wf_draft_distill(x, Wd, tid, tlogit, ws: DistillWorkspace, t2d=None, temperature: float = 1.0, z=None, loss=None,
@@ -580,12 +621,11 @@ def wf_draft_distill(x, Wd, tid, tlogit, ws: DistillWorkspace, t2d=None, tempera
 
     x [N, d], Wd [Vd, d] bf16; tid, tlogit [N, k]: the teacher's alternatives (-1: none), target ids if t2d [V] is
     given.  z (distill_logits) keeps the logits for wf_draft_distill_grad."""
-    N = x.shape[0]
-    loss = torch.empty(N, dtype=torch.float32, device=x.device) if loss is None else loss
-    lse = torch.empty(N, dtype=torch.float32, device=x.device) if lse is None else lse
-    args = _distill(x, Wd, tid, tlogit, t2d, temperature, z, lse, loss=_shaped(loss, "loss", (N,), _F32, x))
-    _raise((_lib or lib()).wf_draft_distill(ctypes.byref(args), *_own_ws(ws, DistillWorkspace), _stream(stream)),
-           "wf_draft_distill")
+    if loss is None:
+        loss = torch.empty(x.shape[0], dtype=torch.float32, device=x.device)
+    if lse is None:
+        lse = torch.empty_like(loss)
+    _distill("wf_draft_distill", x, Wd, tid, tlogit, t2d, temperature, z, lse, loss, None, None, None, ws, stream)
     return loss, lse
 
 
@@ -600,17 +640,16 @@ def wf_draft_distill_grad(x, Wd, tid, tlogit, z, lse, ws: DistillWorkspace, glos
         raise ValueError("z is required")
     if not (need_dx or need_dWd):
         raise ValueError("neither dx nor dWd is asked for")
-    if need_dx and dx is None:
+    if not need_dx:
+        dx = None
+    elif dx is None:
         dx = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
-    if need_dWd and dWd is None:
+    if not need_dWd:
+        dWd = None
+    elif dWd is None:
         dWd = torch.empty(Wd.shape, dtype=torch.bfloat16, device=x.device)
-    args = _distill(x, Wd, tid, tlogit, t2d, temperature, z, lse,
-                    gloss=None if gloss is None else _shaped(gloss, "gloss", (x.shape[0],), _F32, x),
-                    dx=_shaped(dx, "dx", x.shape, _BF16, x) if need_dx else None,
-                    dWd=_shaped(dWd, "dWd", Wd.shape, _BF16, x) if need_dWd else None)
-    _raise((_lib or lib()).wf_draft_distill_grad(ctypes.byref(args), *_own_ws(ws, DistillWorkspace), _stream(stream)),
-           "wf_draft_distill_grad")
-    return dx if need_dx else None, dWd if need_dWd else None
+    _distill("wf_draft_distill_grad", x, Wd, tid, tlogit, t2d, temperature, z, lse, None, gloss, dx, dWd, ws, stream)
+    return dx, dWd
 
 
 class CatchupWorkspace(Workspace):

@@ -136,3 +136,14 @@ def test_distill_by_hand():
     G = [1 / 7 - .5, 2 / 7, 4 / 7 - .5]
     assert abs(float(dx[0, 0]) - (G[1] * math.log(2) + G[2] * math.log(4))) < 1e-7 and not bool(dx[1].any())
     assert torch.allclose(dW[:, 0], torch.tensor(G, dtype=torch.float64), atol=1e-7) and not bool(dW[:, 1:].any())
+
+
+def test_packed_arguments_are_the_structures_bytes():
+    """The binding packs what include/wf.h lays out: every field at its place."""
+    import struct
+    for fmt, cls in ((wf._LOGPROBS, wf.LogprobsArgs), (wf._DISTILL, wf.DistillArgs)):
+        values = [float(i + 2) if t is ctypes.c_float else i + 2 for i, (_, t) in enumerate(cls._fields_)]
+        a = cls(*values)
+        assert fmt.size == ctypes.sizeof(cls) and isinstance(fmt, struct.Struct)
+        got = cls.from_buffer_copy(fmt.pack(*values))
+        assert [getattr(got, n) for n, _ in cls._fields_] == [getattr(a, n) for n, _ in cls._fields_] == values
