@@ -96,8 +96,15 @@ __global__ void __launch_bounds__(GRAD_THREADS) logit_grad_kernel(const GradPara
 // of dx, the pairs with fewer of them begin dWd sooner, and all end together.
 // With too few rows for that dx is cut along Vd as well; its fp32 parts are
 // added up in order by a kernel of their own.
+// Up to 128 rows dx is computed as its transpose, Wd^T G^T: Wd's 256 columns are
+// the product's M and the rows its N, so that a K block costs what its rows need
+// and not 256 of them, and the tile is bound by Wd's bytes.
 constexpr int TM = 256, TN = 256;
-constexpr int OUT_STAGING = 4 * 2 * 4096;   // two boxes of 32 rows x 128 bytes a warp
+constexpr int OUT_BOX = 4096;               // 32 rows x 128 bytes on their way out
+// Eight epilogue warps, two on each 32 rows: a tile on its way out is a chain of
+// short steps (accumulator, rounding, shared memory, copy), 4,900 cycles for one
+// warp, where a short dWd tile (few rows) could leave in 2,800.
+constexpr int PROD_WARPS = 8, PROD_THREADS = pipe_threads(PROD_WARPS);
 constexpr int PROD_STAGES = 6;
 constexpr int PROD_STAGE = 2 * BM * BK * 2;
 constexpr int PLAN_PAIRS = 76;              // pairs that the split is chosen for (152 SMs)
@@ -110,7 +117,11 @@ struct ProdParams {
     int split, kb_x, kb_w;    // parts of dx's K; K blocks of a whole dx tile and of a dWd tile
     int x_units, w_units;
     int lead, late;           // pairs from `late` on have one dx unit less and begin dWd `lead` rounds sooner
-    int part_rows;            // rows of one part of dx (a multiple of 256)
+    int part_rows;            // rows of one part of dx
+    int flip;                 // dx is computed as its transpose, `flip` rows wide; 0: as it lies
+    int w_rows;               // rows of one K block of dWd (a multiple of 16)
+    uint16_t* dx;
+    float* part;
     Control* ctrl;
     uint64_t timeout_ns;
 };
@@ -121,36 +132,61 @@ struct Unit {
     int k0, kb;         // first K block, K blocks
     int part;
 };
-__device__ __forceinline__ bool unit_at(const ProdParams& p, int slot, int slots, int i, Unit& u) {
-    const int mine = p.x_units > slot ? (p.x_units - slot + slots - 1) / slots : 0;
-    if (i < mine) {
-        const int v = slot + i * slots;
-        const int tile = v / p.split, part = v - tile * p.split;
-        u.dx = true;
-        u.part = part;
-        u.row0 = tile / p.x_n * TM;
-        u.col0 = tile % p.x_n * TN;
-        u.k0 = (int)((long)p.kb_x * part / p.split);
-        u.kb = (int)((long)p.kb_x * (part + 1) / p.split) - u.k0;
+// The units of one pair, in its order: its share of dx, then of dWd.  A dWd tile
+// of few rows takes a microsecond, so the tiles' places are counted on from one
+// another instead of divided out.
+struct Units {
+    int x_left, x_next, slot, slots;
+    int lead_left, v, r, c, stride, dr, dc;
+    __device__ __forceinline__ void place(const ProdParams& p, int v0, int step) {
+        v = v0;
+        stride = step;
+        r = v0 / p.x_n;
+        c = v0 - r * p.x_n;
+        dr = step / p.x_n;
+        dc = step - dr * p.x_n;
+    }
+    __device__ __forceinline__ Units(const ProdParams& p, int slot_, int slots_) : slot(slot_), slots(slots_) {
+        x_left = p.x_units > slot ? (p.x_units - slot + slots - 1) / slots : 0;
+        x_next = slot;
+        lead_left = slot >= p.late ? p.lead : 0;
+        if (lead_left)
+            place(p, slot - p.late, slots - p.late);
+        else
+            place(p, p.lead * (slots - p.late) + slot, slots);
+    }
+    __device__ __forceinline__ bool next(const ProdParams& p, Unit& u) {
+        if (x_left > 0) {
+            const int tile = x_next / p.split, part = x_next - tile * p.split;
+            u.dx = true;
+            u.part = part;
+            u.row0 = tile / p.x_n * TM;
+            u.col0 = tile % p.x_n * TN;
+            u.k0 = (int)((long)p.kb_x * part / p.split);
+            u.kb = (int)((long)p.kb_x * (part + 1) / p.split) - u.k0;
+            x_next += slots;
+            --x_left;
+            return true;
+        }
+        if (v >= p.w_units) return false;
+        u.dx = false;
+        u.part = 0;
+        u.row0 = r * TM;
+        u.col0 = c * TN;
+        u.k0 = 0;
+        u.kb = p.kb_w;
+        v += stride;
+        r += dr;
+        c += dc;
+        if (c >= p.x_n) {
+            c -= p.x_n;
+            ++r;
+        }
+        // behind the units that the early pairs took by themselves, every pair takes its turn
+        if (lead_left && --lead_left == 0) place(p, p.lead * (slots - p.late) + slot, slots);
         return true;
     }
-    int j = i - mine, v;
-    const int ahead = p.lead * (slots - p.late);   // units that the early pairs take by themselves
-    if (slot >= p.late && j < p.lead) {
-        v = j * (slots - p.late) + slot - p.late;
-    } else {
-        if (slot >= p.late) j -= p.lead;
-        v = ahead + j * slots + slot;
-    }
-    if (v >= p.w_units) return false;
-    u.dx = false;
-    u.part = 0;
-    u.row0 = v / p.x_n * TM;
-    u.col0 = v % p.x_n * TN;
-    u.k0 = 0;
-    u.kb = p.kb_w;
-    return true;
-}
+};
 
 // Descriptor of an operand whose contiguous dimension is the product's M or N:
 // blocks of 64 values x 64 K rows (128-byte rows, 128-byte swizzle) 8,192 bytes
@@ -162,13 +198,13 @@ __device__ __forceinline__ uint64_t desc_mn(uint32_t addr) {
 constexpr uint32_t IDESC = umma_idesc_bf16(TM, TN);
 constexpr uint32_t A_MN = 1u << 15, B_MN = 1u << 16;   // the operand's M / N dimension is the contiguous one
 
-__global__ void __launch_bounds__(PIPE_THREADS, 1)
+__global__ void __launch_bounds__(PROD_THREADS, 1)
     grad_products_kernel(const __grid_constant__ CUtensorMap tmGk, const __grid_constant__ CUtensorMap tmGm,
                          const __grid_constant__ CUtensorMap tmW, const __grid_constant__ CUtensorMap tmX,
                          const __grid_constant__ CUtensorMap tmDx, const __grid_constant__ CUtensorMap tmDw,
                          const ProdParams p) {
     extern __shared__ uint8_t smem_raw[];
-    const Pipe g = pipe_at(smem_raw, PROD_STAGES, PROD_STAGE, BM * BK * 2, OUT_STAGING, p.ctrl, p.timeout_ns);
+    const Pipe g = pipe_at(smem_raw, PROD_STAGES, PROD_STAGE, BM * BK * 2, PROD_WARPS * OUT_BOX, p.ctrl, p.timeout_ns);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int rank = (int)(cluster_ctarank() & 1u);
     const bool first = rank == 0;
@@ -181,95 +217,141 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1)
         tma_prefetch_desc(&tmDx);
         tma_prefetch_desc(&tmDw);
     }
-    const uint32_t tmem_base = pipe_begin<true>(g);
+    const uint32_t tmem_base = pipe_begin<true, PROD_WARPS>(g);
     if (warp != 0) pdl_wait();   // warp 0: as it copies
     pdl_trigger();
     if (warp == 0) {
-        if (lane == 0) {
-            const uint64_t pol = policy_evict_normal();
-            Unit u{};
-            auto next = [&](int i) { return unit_at(p, slot, slots, i, u) ? u.kb : 0; };
-            auto tx = [&]() { return (uint32_t)(2 * PROD_STAGE); };
-            auto load_a = [&](int kc, int s, uint32_t bar) {
-                const int k = (u.k0 + kc) * BK;
-                if (u.dx) {
-                    pipe_load<true>(g.a(s), &tmGk, bar, k, u.row0 + rank * BM, pol);
-                } else {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        pipe_load<true>(g.a(s) + h * 8192, &tmGm, bar, u.row0 + rank * BM + 64 * h, k, pol);
-                }
-            };
-            auto load_b = [&](int kc, int s, uint32_t bar) {
-                const int k = (u.k0 + kc) * BK;
-                const CUtensorMap* b = u.dx ? &tmW : &tmX;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    pipe_load<true>(g.b(s) + h * 8192, b, bar, u.col0 + rank * (TN / 2) + 64 * h, k, pol);
-            };
-            pipe_copy<true, false>(g, first, next, tx, load_a, load_b);
-        }
+        const uint64_t pol = policy_evict_normal();
+        Unit u{};
+        Units units(p, slot, slots);
+        auto next = [&](int) { return units.next(p, u) ? u.kb : 0; };
+        auto tx = [&]() {
+            if (u.dx) return p.flip ? (uint32_t)(2 * BM * BK * 2 + p.flip * BK * 2) : (uint32_t)(2 * PROD_STAGE);
+            return (uint32_t)(2 * 4 * 128 * p.w_rows);
+        };
+        // lanes 0 and 1 copy the halves of A, lanes 2 and 3 those of B; where an operand lies with its K contiguous,
+        // it is one box, of the even lane
+        auto load = [&](int kc, int s, uint32_t bar, bool, bool) {
+            const int h = lane & 1, k = u.dx ? (u.k0 + kc) * BK : kc * p.w_rows;
+            const bool flip = u.dx && p.flip, rows_a = u.dx && !p.flip;
+            if (lane >= 4 || (lane == 1 && rows_a) || (lane == 3 && flip)) return;
+            const CUtensorMap* map;
+            int mn;   // the coordinate along M or N
+            if (lane < 2) {
+                map = rows_a ? &tmGk : flip ? &tmW : &tmGm;
+                mn = (flip ? u.col0 : u.row0) + rank * BM + (rows_a ? 0 : 64 * h);
+            } else {
+                map = flip ? &tmGk : u.dx ? &tmW : &tmX;
+                mn = flip ? rank * (p.flip / 2) : u.col0 + rank * (TN / 2) + 64 * h;
+            }
+            const bool k_inner = lane < 2 ? rows_a : flip;
+            pipe_load<true>((lane < 2 ? g.a(s) : g.b(s)) + h * 8192, map, bar, k_inner ? k : mn, k_inner ? mn : k, pol);
+        };
+        pipe_copy<true, false>(g, first, next, tx, load);
     } else if (warp == 1) {
         if (lane == 0 && first) {
             Unit u{};
-            auto next = [&](int i) { return unit_at(p, slot, slots, i, u) ? u.kb : 0; };
+            Units units(p, slot, slots);
+            auto next = [&](int) { return units.next(p, u) ? u.kb : 0; };
             auto issue = [&](int s, uint32_t d, int kc) {
-                const uint32_t as = smem_u32(g.a(s));
-                const uint64_t a = u.dx ? umma_desc_sw128(as) : desc_mn(as), b = desc_mn(smem_u32(g.b(s)));
-                const uint32_t a_step = u.dx ? 2 : 128;   // 16 values of K: 32 bytes of a row, or 16 rows of 128
-                const uint32_t idesc = IDESC | B_MN | (u.dx ? 0 : A_MN);
+                const uint32_t as = smem_u32(g.a(s)), bs = smem_u32(g.b(s));
+                const bool flip = u.dx && p.flip, a_rows = u.dx && !p.flip;
+                const uint64_t a = a_rows ? umma_desc_sw128(as) : desc_mn(as);
+                const uint64_t b = flip ? umma_desc_sw128(bs) : desc_mn(bs);
+                // 16 values of K: 32 bytes of a row, or 16 rows of 128
+                const uint32_t a_step = a_rows ? 2 : 128, b_step = flip ? 2 : 128;
+                const uint32_t idesc = flip ? umma_idesc_bf16(TM, p.flip) | A_MN : IDESC | B_MN | (u.dx ? 0 : A_MN);
+                if (u.dx || p.w_rows == BK) {
 #pragma unroll
-                for (int kk = 0; kk < BK / 16; ++kk)
-                    umma_bf16_pair(d, a + a_step * kk, b + 128 * kk, idesc, (kc | kk) != 0);
+                    for (int kk = 0; kk < BK / 16; ++kk)
+                        umma_bf16_pair(d, a + a_step * kk, b + b_step * kk, idesc, (kc | kk) != 0);
+                } else {
+                    for (int kk = 0; kk < p.w_rows / 16; ++kk)
+                        umma_bf16_pair(d, a + a_step * kk, b + b_step * kk, idesc, (kc | kk) != 0);
+                }
             };
             pipe_mma<true>(g, tmem_base, next, issue);
         }
     } else {
-        const int q = warp & 3;
+        const int q = warp & 3, half = (warp - 2) >> 2;   // accumulator rows 32 q.., columns of this half
         const uint32_t tempty_first = first ? 0 : cluster_addr(&g.tempty[0], 0);
-        uint8_t* stage = pipe_extra(g) + q * 2 * 4096;
-        int box = 0;
+        uint8_t* stage = pipe_extra(g) + (warp - 2) * OUT_BOX;
         Unit u{};
-        for (uint32_t i = 0; unit_at(p, slot, slots, (int)i, u); ++i) {
+        Units units(p, slot, slots);
+        for (uint32_t i = 0; units.next(p, u); ++i) {
             if (!pipe_acc_wait(g, i)) break;
             const int row = u.row0 + rank * BM + q * 32;
             const bool part = u.dx && p.split > 1;
-            if (row < (part ? p.part_rows : u.dx ? p.N : p.Vd)) {
-                const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (i & 1) * BN;
-                const int cols = min(TN, p.d - u.col0);
-                for (int c0 = 0; c0 < cols; c0 += part ? 32 : 64) {
-                    uint32_t r[2][32];
-                    tmem_ld_32x32b_x32(tbase + c0, r[0]);
-                    if (!part) tmem_ld_32x32b_x32(tbase + c0 + 32, r[1]);
+            const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (i & 1) * BN;
+            auto box_free = [&]() {   // the last store has read the box
+                if (lane == 0) tma_store_wait_read<0>();
+                __syncwarp();
+            };
+            auto box_out = [&](int col, int y) {
+                fence_async_store();
+                __syncwarp();
+                if (lane == 0) tma_store_2d(u.dx ? &tmDx : &tmDw, stage, col, y);
+            };
+            if (u.dx && p.flip) {
+                // thread = one column of dx, accumulator columns = its rows: a warp's stores are whole lines
+                const int c = u.col0 + rank * BM + q * 32 + lane;
+                for (int n0 = 32 * half; n0 < p.N; n0 += 64) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tbase + n0, r);
                     tmem_ld_wait();
-                    uint8_t* to = stage + box * 4096;
-                    if (lane == 0) tma_store_wait_read<1>();
-                    __syncwarp();
-                    if (part) {
 #pragma unroll
-                        for (int j = 0; j < 8; ++j)
-                            *reinterpret_cast<uint4*>(to + swizzled(lane, j)) =
-                                make_uint4(r[0][4 * j], r[0][4 * j + 1], r[0][4 * j + 2], r[0][4 * j + 3]);
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const uint32_t* v = r[j >> 2] + 8 * (j & 3);
-                            uint4 o;
-                            o.x = pack_bf16(__uint_as_float(v[0]), __uint_as_float(v[1]));
-                            o.y = pack_bf16(__uint_as_float(v[2]), __uint_as_float(v[3]));
-                            o.z = pack_bf16(__uint_as_float(v[4]), __uint_as_float(v[5]));
-                            o.w = pack_bf16(__uint_as_float(v[6]), __uint_as_float(v[7]));
-                            *reinterpret_cast<uint4*>(to + swizzled(lane, j)) = o;
+                    for (int j = 0; j < 32; ++j) {
+                        if (n0 + j < p.N && c < p.d) {
+                            if (part)
+                                p.part[((size_t)u.part * p.part_rows + n0 + j) * p.d + c] = __uint_as_float(r[j]);
+                            else
+                                p.dx[(size_t)(n0 + j) * p.d + c] = (uint16_t)pack_bf16(__uint_as_float(r[j]), 0.f);
                         }
                     }
-                    fence_async_store();
-                    __syncwarp();
-                    if (lane == 0)
-                        tma_store_2d(u.dx ? &tmDx : &tmDw, to, u.col0 + c0, u.part * (part ? p.part_rows : 0) + row);
-                    box ^= 1;
+                }
+                pipe_acc_release(g, i, tempty_first);
+            } else if (part) {
+                const int cols = min(TN / 2 * (half + 1), p.d - u.col0);
+                for (int c0 = TN / 2 * half; row < p.N && c0 < cols; c0 += 32) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tbase + c0, r);
+                    tmem_ld_wait();
+                    box_free();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        *reinterpret_cast<uint4*>(stage + swizzled(lane, j)) =
+                            make_uint4(r[4 * j], r[4 * j + 1], r[4 * j + 2], r[4 * j + 3]);
+                    box_out(u.col0 + c0, u.part * p.part_rows + row);
+                }
+                pipe_acc_release(g, i, tempty_first);
+            } else {
+                // all of the warp's columns leave the accumulator, rounded, before any leaves the SM: the
+                // next tile's products do not wait for the way out
+                uint32_t o[TN / 4];
+#pragma unroll
+                for (int c = 0; c < TN / 2; c += 32) {
+                    uint32_t r[32];
+                    tmem_ld_32x32b_x32(tbase + TN / 2 * half + c, r);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+                        o[c / 2 + j] = pack_bf16(__uint_as_float(r[2 * j]), __uint_as_float(r[2 * j + 1]));
+                }
+                pipe_acc_release(g, i, tempty_first);
+                if (row < (u.dx ? p.N : p.Vd)) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int col = u.col0 + TN / 2 * half + 64 * h;
+                        if (col >= p.d) break;
+                        box_free();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j)
+                            *reinterpret_cast<uint4*>(stage + swizzled(lane, j)) = make_uint4(
+                                o[32 * h + 4 * j], o[32 * h + 4 * j + 1], o[32 * h + 4 * j + 2], o[32 * h + 4 * j + 3]);
+                        box_out(col, row);
+                    }
                 }
             }
-            pipe_acc_release(g, i, tempty_first);
         }
         if (lane == 0) tma_store_wait_all();
     }
@@ -315,7 +397,7 @@ __global__ void __launch_bounds__(256) dx_join_kernel(const float* part, int par
 constexpr double W_TILE_OUT = 4.4, X_PART_OUT = 9.0, TILE_FIXED = 1.0;
 
 struct Plan {
-    int x_m, x_n, w_m, kb_x, kb_w, split, part_rows;
+    int x_m, x_n, w_m, kb_x, kb_w, split, part_rows, flip, w_rows;
 };
 double w_cost(int kb_w) { return (kb_w > W_TILE_OUT ? kb_w : W_TILE_OUT) + TILE_FIXED; }
 
@@ -325,9 +407,13 @@ Plan plan_of(int N, int d, int Vd, bool dx, bool dw) {
     p.x_n = cdiv(d, TN);
     p.w_m = cdiv(Vd, TM);
     p.kb_x = cdiv(Vd, BK);
+    // equal K blocks of dWd: rows that are not there cost a tensor copy more than
+    // others (one row in boxes of 64: 35 us without stores, 64 rows: 24)
     p.kb_w = cdiv(N, BK);
+    p.w_rows = cdiv(cdiv(N, p.kb_w), 16) * 16;
     p.split = 1;
-    p.part_rows = p.x_m * TM;
+    p.flip = N <= BM ? (N + 31) / 32 * 32 : 0;
+    p.part_rows = p.flip ? N : p.x_m * TM;
     if (dx) {
         const double w = dw ? (double)p.w_m * p.x_n * w_cost(p.kb_w) : 0.0;
         double best = -1;
@@ -384,14 +470,14 @@ wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int N, int 
     static std::mutex mu;
     static bool attr_set[64] = {false};
     static int pairs[64];
-    const int smem = pipe_smem(PROD_STAGES, PROD_STAGE, OUT_STAGING);
+    const int smem = pipe_smem(PROD_STAGES, PROD_STAGE, PROD_WARPS * OUT_BOX);
     st = configure_once(mu, attr_set, [&] {
         if (cudaFuncSetAttribute(grad_products_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
             cudaSuccess)
             return false;
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return false;
-        if (dev < 64) pairs[dev] = resident_pairs(reinterpret_cast<const void*>(grad_products_kernel), PIPE_THREADS, smem);
+        if (dev < 64) pairs[dev] = resident_pairs(reinterpret_cast<const void*>(grad_products_kernel), PROD_THREADS, smem);
         return true;
     });
     if (st != WF_OK) return st;
@@ -412,6 +498,10 @@ wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int N, int 
     p.x_units = dx ? pl.x_m * pl.x_n * pl.split : 0;
     p.w_units = dWd ? pl.w_m * pl.x_n : 0;
     p.part_rows = pl.part_rows;
+    p.flip = pl.flip;
+    p.w_rows = pl.w_rows;
+    p.dx = dx;
+    p.part = part;
     if (slots > p.x_units + p.w_units) slots = p.x_units + p.w_units;
     // pairs 0 .. late - 1 have one dx unit more than the others
     p.late = p.x_units % slots;
@@ -420,16 +510,16 @@ wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int N, int 
     p.ctrl = ctrl;
     p.timeout_ns = wait_timeout_ns();
     CUtensorMap gk, gm, tw, tx, tdx, tdw;
-    if (!make_tile_map(&gk, G, N, Vd, a.ldg, false, BK, BM) || !make_tile_map(&gm, G, N, Vd, a.ldg, false, 64, BK) ||
-        !make_tile_map(&tw, Wd, Vd, d, d, false, 64, BK) || !make_tile_map(&tx, x, N, d, d, false, 64, BK))
+    if (!make_tile_map(&gk, G, N, Vd, a.ldg, false, BK, pl.flip ? pl.flip / 2 : BM) || !make_tile_map(&gm, G, N, Vd, a.ldg, false, 64, pl.w_rows) ||
+        !make_tile_map(&tw, Wd, Vd, d, d, false, 64, BK) || !make_tile_map(&tx, x, N, d, d, false, 64, pl.w_rows))
         return WF_ERR_CUDA;
     tdx = tdw = gk;
     const bool parts = pl.split > 1;
-    if (dx && !(parts ? make_tile_map(&tdx, part, (uint64_t)pl.split * pl.part_rows, d, d, true, 32, 32)
+    if (dx && !pl.flip && !(parts ? make_tile_map(&tdx, part, (uint64_t)pl.split * pl.part_rows, d, d, true, 32, 32)
                       : make_tile_map(&tdx, dx, N, d, d, false, 64, 32)))
         return WF_ERR_CUDA;
     if (dWd && !make_tile_map(&tdw, dWd, Vd, d, d, false, 64, 32)) return WF_ERR_CUDA;
-    st = launch_cluster(grad_products_kernel, dim3(2 * slots), dim3(PIPE_THREADS), smem, s, 2u, gk, gm, tw, tx, tdx,
+    st = launch_cluster(grad_products_kernel, dim3(2 * slots), dim3(PROD_THREADS), smem, s, 2u, gk, gm, tw, tx, tdx,
                         tdw, p);
     if (st != WF_OK || !dx || !parts) return st;
     const long units = (long)N * (d / 8);

@@ -3,11 +3,12 @@
 // MMAs into two TMEM accumulators, and epilogue warps that read them.
 //
 //   warp 0     fills the ring: each stage holds an A tile and a B tile of one K
-//              block (64 values of K)
+//              block (64 values of K); each box is copied by a lane of its own
 //   warp 1     allocates TMEM and issues the MMAs of a stage; the stage is free
 //              again when they have completed
-//   warps 2-5  read a finished accumulator (thread = one row of the tile) while
-//              the next tile's MMAs run into the other one
+//   warps 2-   read a finished accumulator (thread = one row of the tile, or of
+//              one half of its columns) while the next tile's MMAs run into the
+//              other one
 // PAIR: the two CTAs of a cluster compute one 256-row tile with paired MMAs;
 // each loads its own half of A's rows and of B's, the first CTA issues, and
 // both CTAs' barriers are committed to.
@@ -20,7 +21,8 @@
 
 namespace wf {
 
-constexpr int PIPE_THREADS = 192;
+// Threads with `w` epilogue warps (4 or 8: a warp reads the 32 accumulator rows that its number mod 4 gives).
+constexpr int pipe_threads(int w) { return 64 + 32 * w; }
 constexpr int PIPE_MAX_STAGES = 8;
 constexpr int PIPE_TMEM_COLS = 2 * BN;     // two fp32 accumulators of up to BN columns
 constexpr int PIPE_BARRIER_BYTES = 256;    // barriers, TMEM address and abort flag behind the ring
@@ -71,7 +73,7 @@ inline int pipe_smem(int stages, int stage_bytes, int extra) {
 }
 
 // Barriers and TMEM; returns the TMEM base address.  All threads.
-template <bool PAIR>
+template <bool PAIR, int EPI_WARPS>
 __device__ __forceinline__ uint32_t pipe_begin(const Pipe& g) {
     const int warp = threadIdx.x >> 5;
     if (threadIdx.x == 0) {
@@ -81,7 +83,7 @@ __device__ __forceinline__ uint32_t pipe_begin(const Pipe& g) {
         }
         for (int a = 0; a < 2; ++a) {
             mbar_init(&g.tfull[a], 1);
-            mbar_init(&g.tempty[a], PAIR ? 256 : 128);   // PAIR: both CTAs' epilogue threads release
+            mbar_init(&g.tempty[a], (PAIR ? 2 : 1) * EPI_WARPS);   // PAIR: both CTAs' epilogue warps release
         }
         mbar_init(g.drain, 1);
         *g.abort_flag = 0;
@@ -117,25 +119,31 @@ __device__ __forceinline__ void pipe_end(const Pipe& g, uint32_t tmem_base) {
     }
 }
 
-// The copying thread.  next(i) sets up the CTA's i-th tile and returns its K
-// blocks (0: no further tile); tx() is what a stage of it receives in bytes
-// (PAIR: both CTAs together); load_a(kc, s, bar) and load_b(kc, s, bar) issue
-// the copies of its operands into stage s, counted on the barrier at shared
-// address `bar` (PAIR: the first CTA's).
+// The copying warp (all lanes).  next(i) sets up the CTA's i-th tile and returns
+// its K blocks (0: no further tile); tx() is what a stage of it receives in bytes
+// (PAIR: both CTAs together); load(kc, s, bar, a, b) issues the copies of operand
+// A (if a) and B (if b) into stage s, counted on the barrier at shared address
+// `bar` (PAIR: the first CTA's), each box by a lane of its own: one thread issuing
+// four boxes of 64 rows takes 900 cycles a stage, their products 512.
 // EARLY: B is a weight matrix, whose first stages are asked for while the kernel
 // before is still finishing; everything else waits for it.
-template <bool PAIR, bool EARLY, typename Next, typename Tx, typename LoadA, typename LoadB>
-__device__ __forceinline__ void pipe_copy(const Pipe& g, bool first, Next next, Tx tx, LoadA load_a, LoadB load_b) {
+template <bool PAIR, bool EARLY, typename Next, typename Tx, typename Load>
+__device__ __forceinline__ void pipe_copy(const Pipe& g, bool first, Next next, Tx tx, Load load) {
+    const int lane = threadIdx.x & 31;
     const uint32_t full0 = PAIR ? cluster_addr(&g.full[0], 0) : smem_u32(&g.full[0]);
     auto bar = [&](int s) { return full0 + (uint32_t)(s * sizeof(uint64_t)); };
+    auto expect = [&](int s, uint32_t bytes) {
+        if (lane == 0 && (!PAIR || first)) mbar_arrive_expect_tx(&g.full[s], bytes);
+        __syncwarp();
+    };
     int num_k = next(0);
     uint32_t bytes = tx();
     int early = 0;
     if constexpr (EARLY) {
         early = num_k < g.stages ? num_k : g.stages;
         for (int s = 0; s < early; ++s) {
-            if (!PAIR || first) mbar_arrive_expect_tx(&g.full[s], bytes);
-            load_b(s, s, bar(s));
+            expect(s, bytes);
+            load(s, s, bar(s), false, true);
         }
     }
     pdl_wait();
@@ -149,22 +157,21 @@ __device__ __forceinline__ void pipe_copy(const Pipe& g, bool first, Next next, 
                 s = 0;
                 ph ^= 1;
             }
-            if (!mbar_wait(&g.empty[s], ph ^ 1, g.timeout_ns, g.abort_flag)) {
+            // the lanes give up a wait together
+            if (!__all_sync(0xffffffffu, mbar_wait(&g.empty[s], ph ^ 1, g.timeout_ns, g.abort_flag))) {
                 g.fail(PIPE_WHERE_COPY + s);
                 ok = false;
                 break;
             }
-            if (!EARLY || it >= (uint32_t)early) {
-                if (!PAIR || first) mbar_arrive_expect_tx(&g.full[s], bytes);
-                load_b(kc, s, bar(s));
-            }
-            load_a(kc, s, bar(s));
+            const bool fresh = !EARLY || it >= (uint32_t)early;
+            if (fresh) expect(s, bytes);
+            load(kc, s, bar(s), true, fresh);
         }
         num_k = next(++i);
         bytes = tx();
     }
-    if (!ok || *g.abort_flag) {
-        // let every copy this thread issued land before the CTA exits
+    if (!ok || __any_sync(0xffffffffu, *g.abort_flag)) {
+        // let every copy this warp issued land before the CTA exits
         if (!PAIR || first) {
             for (uint32_t j = (it > (uint32_t)g.stages ? it - g.stages : 0); j < it; ++j)
                 mbar_wait(&g.full[j % g.stages], (j / g.stages) & 1, g.timeout_ns, nullptr);
@@ -195,8 +202,7 @@ __device__ __forceinline__ void pipe_mma(const Pipe& g, uint32_t tmem_base, Next
         if (num_k == 0) break;
         const uint32_t acc = i & 1, acc_ph = (i >> 1) & 1;
         // PAIR: released by both CTAs' epilogues (the second's arrivals are remote)
-        if (!(PAIR ? mbar_wait_cluster(&g.tempty[acc], acc_ph ^ 1, g.timeout_ns, g.abort_flag)
-                   : mbar_wait(&g.tempty[acc], acc_ph ^ 1, g.timeout_ns, g.abort_flag))) {
+        if (!mbar_wait(&g.tempty[acc], acc_ph ^ 1, g.timeout_ns, g.abort_flag)) {
             g.fail(PIPE_WHERE_ACC);
             ok = false;
             break;
@@ -252,12 +258,20 @@ __device__ __forceinline__ bool pipe_acc_wait(const Pipe& g, uint32_t i) {
     return true;
 }
 // tempty_first: in a pair's second CTA the shared::cluster address of the first CTA's accumulator barriers, else 0.
+// One arrival a warp, without a fence at cluster scope: nothing in memory is handed over, and the accumulator's reads
+// are ordered by tcgen05's own fences.  (A release at cluster scope waits for the warp's shared-memory writes on their
+// way out: 1,850 cycles a tile.)
 __device__ __forceinline__ void pipe_acc_release(const Pipe& g, uint32_t i, uint32_t tempty_first) {
     tc_fence_before();
-    if (tempty_first)
-        mbar_arrive_remote(tempty_first + (i & 1) * (uint32_t)sizeof(uint64_t), 1u);
-    else
-        mbar_arrive(&g.tempty[i & 1]);
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) {
+        if (tempty_first)
+            asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(
+                             tempty_first + (i & 1) * (uint32_t)sizeof(uint64_t))
+                         : "memory");
+        else
+            mbar_arrive(&g.tempty[i & 1]);
+    }
 }
 
 // One box into shared memory, its bytes counted on the barrier at `bar`.

@@ -23,6 +23,7 @@ namespace wf {
 
 namespace {
 
+constexpr int SWEEP_THREADS = pipe_threads(4);
 constexpr int STAGING = 4 * 2 * 4096;     // kept logits: two boxes of 32 rows x 128 bytes a warp
 
 struct SweepParams {
@@ -44,6 +45,22 @@ struct SweepParams {
 struct Span {
     int row0, rows;
     bool big;
+};
+// The tiles of one CTA (or pair): unit u = slot, slot + slots, ... is row tile u %
+// num_mt and weight tile u / num_mt, counted on without divisions.
+struct Walk {
+    int u, mt, n, step, dm, dn;
+    __device__ __forceinline__ Walk(const SweepParams& p, int slot, int slots)
+        : u(slot), mt(slot % p.num_mt), n(slot / p.num_mt), step(slots), dm(slots % p.num_mt), dn(slots / p.num_mt) {}
+    __device__ __forceinline__ void on(const SweepParams& p) {
+        u += step;
+        mt += dm;
+        n += dn;
+        if (mt >= p.num_mt) {
+            mt -= p.num_mt;
+            ++n;
+        }
+    }
 };
 __device__ __forceinline__ Span span(const SweepParams& p, int n) {
     if (n < p.nbig) return {n * p.bn, p.bn, true};
@@ -212,7 +229,7 @@ __device__ __forceinline__ void fold(const uint32_t (&r)[32], int lim, int col0,
 }
 
 template <int KT, bool ENT, bool Z, bool PAIR>
-__global__ void __launch_bounds__(PIPE_THREADS, 1)
+__global__ void __launch_bounds__(SWEEP_THREADS, 1)
     sweep_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
                  const __grid_constant__ CUtensorMap tmBs, const __grid_constant__ CUtensorMap tmZ,
                  const SweepParams p) {
@@ -231,39 +248,38 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1)
         if (p.nbig < p.num_n) tma_prefetch_desc(&tmBs);
         if constexpr (Z) tma_prefetch_desc(&tmZ);
     }
-    const uint32_t tmem_base = pipe_begin<PAIR>(g);
+    const uint32_t tmem_base = pipe_begin<PAIR, 4>(g);
     if (warp != 0) pdl_wait();   // warp 0: when it has asked for its first weights
     pdl_trigger();
 
     if (warp == 0) {
-        if (lane == 0) {
-            const uint64_t pol_w = policy_evict_first(), pol_a = policy_evict_last();
-            int m = 0;
-            Span sp{};
-            auto next = [&](int i) {
-                const int u = slot + i * nslots;
-                if (u >= units) return 0;
-                m = PAIR ? 2 * (u % p.num_mt) + rank : u % p.num_mt;
-                sp = span(p, u / p.num_mt);
-                return p.num_k;
-            };
-            auto tx = [&]() { return (uint32_t)((PAIR ? 2 : 1) * p.a_bytes + sp.rows * BK * 2); };
-            auto load_a = [&](int kc, int s, uint32_t bar) {
-                pipe_load<PAIR>(g.a(s), &tmA, bar, kc * BK, m * BM, pol_a);
-            };
-            auto load_b = [&](int kc, int s, uint32_t bar) {
-                const int half = PAIR ? sp.rows / 2 : 0;
-                pipe_load<PAIR>(g.b(s), sp.big ? &tmB : &tmBs, bar, kc * BK, sp.row0 + rank * half, pol_w);
-            };
-            pipe_copy<PAIR, true>(g, first, next, tx, load_a, load_b);
-        }
+        const uint64_t pol_w = policy_evict_first(), pol_a = policy_evict_last();
+        int m = 0;
+        Span sp{};
+        Walk w(p, slot, nslots);
+        auto next = [&](int) {
+            if (w.u >= units) return 0;
+            m = PAIR ? 2 * w.mt + rank : w.mt;
+            sp = span(p, w.n);
+            w.on(p);
+            return p.num_k;
+        };
+        auto tx = [&]() { return (uint32_t)((PAIR ? 2 : 1) * p.a_bytes + sp.rows * BK * 2); };
+        auto load = [&](int kc, int s, uint32_t bar, bool a, bool b) {
+            if (lane == 0 && a) pipe_load<PAIR>(g.a(s), &tmA, bar, kc * BK, m * BM, pol_a);
+            if (lane == 1 && b)
+                pipe_load<PAIR>(g.b(s), sp.big ? &tmB : &tmBs, bar, kc * BK,
+                                sp.row0 + (PAIR ? rank * (sp.rows / 2) : 0), pol_w);
+        };
+        pipe_copy<PAIR, true>(g, first, next, tx, load);
     } else if (warp == 1) {
         if (lane == 0 && first) {
             uint32_t idesc = 0;
-            auto next = [&](int i) {
-                const int u = slot + i * nslots;
-                if (u >= units) return 0;
-                idesc = u / p.num_mt < p.nbig ? p.idesc : p.idesc_s;
+            Walk w(p, slot, nslots);
+            auto next = [&](int) {
+                if (w.u >= units) return 0;
+                idesc = w.n < p.nbig ? p.idesc : p.idesc_s;
+                w.on(p);
                 return p.num_k;
             };
             auto issue = [&](int s, uint32_t d, int kc) {
@@ -290,11 +306,10 @@ __global__ void __launch_bounds__(PIPE_THREADS, 1)
         int cur = -1;                      // the row tile whose states the registers hold
         int box = 0;                       // Z: staging box in use
         auto state_of = [&](int row) { return p.states + ((size_t)row * p.slots + slot) * state_bytes(KT); };
-        for (uint32_t i = 0;; ++i) {
-            const int u = slot + (int)i * nslots;
-            if (u >= units) break;
-            const int mt = u % p.num_mt, m = PAIR ? 2 * mt + rank : mt;
-            const Span sp = span(p, u / p.num_mt);
+        Walk w(p, slot, nslots);
+        for (uint32_t i = 0; w.u < units; ++i, w.on(p)) {
+            const int mt = w.mt, m = PAIR ? 2 * mt + rank : mt;
+            const Span sp = span(p, w.n);
             const int row = m * BM + rit;
             const bool warp_live = m * BM + q * 32 < p.rows, live = row < p.rows;
             bool fresh = false;   // the list is empty
@@ -469,7 +484,7 @@ wf_status launch_kt(const SweepCall& c, int* slots_out, cudaStream_t s) {
         if (cudaGetDevice(&dev) != cudaSuccess) return WF_ERR_CUDA;
         std::lock_guard<std::mutex> lock(pmu);
         if (dev >= 64 || !pairs[dev]) {
-            slots = resident_pairs(reinterpret_cast<const void*>(sweep_kernel<KT, ENT, Z, true>), PIPE_THREADS, smem);
+            slots = resident_pairs(reinterpret_cast<const void*>(sweep_kernel<KT, ENT, Z, true>), SWEEP_THREADS, smem);
             if (dev < 64) pairs[dev] = slots;
         } else {
             slots = pairs[dev];
@@ -507,9 +522,9 @@ wf_status launch_kt(const SweepCall& c, int* slots_out, cudaStream_t s) {
     if (Z && !make_tile_map(&tz, c.z, c.rows, c.V, c.ldz, true, 32, 32)) return WF_ERR_CUDA;
     *slots_out = slots;
     if (pair)
-        return launch_cluster(sweep_kernel<KT, ENT, Z, true>, dim3(2 * slots), dim3(PIPE_THREADS), smem, s, 2u, ta, tb,
+        return launch_cluster(sweep_kernel<KT, ENT, Z, true>, dim3(2 * slots), dim3(SWEEP_THREADS), smem, s, 2u, ta, tb,
                               tbs, tz, p);
-    return launch(sweep_kernel<KT, ENT, Z, false>, dim3(slots), dim3(PIPE_THREADS), smem, s, ta, tb, tbs, tz, p);
+    return launch(sweep_kernel<KT, ENT, Z, false>, dim3(slots), dim3(SWEEP_THREADS), smem, s, ta, tb, tbs, tz, p);
 }
 
 }  // namespace
