@@ -67,9 +67,9 @@ wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args*
 size_t distill_grad_ldg(int Vd);
 size_t distill_part_bytes(int N, int d, int Vd);
 long distill_grad_units(int N, int d, int Vd);
-wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int N, int d, int Vd, int K, const float* z,
-                              int64_t ldz, const float* lse, const int32_t* ids, const float* p, const float* gs,
-                              uint16_t* dx, uint16_t* dWd, uint16_t* G, float* part, Control* ctrl, cudaStream_t s);
+wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int d, const Teacher& t, const float* z,
+                              int64_t ldz, const float* lse, const float* gloss, uint16_t* dx, uint16_t* dWd,
+                              uint16_t* G, float* part, cudaStream_t s);
 
 static std::atomic<uint64_t> g_timeout_ns{2000000000ull};
 uint64_t wait_timeout_ns() { return g_timeout_ns.load(std::memory_order_relaxed); }
@@ -164,7 +164,7 @@ static ScoreLayout score_layout(int P, int d, int S, int k) {
 // Scratch of wf_draft_distill and its gradients: the teacher as lists, then
 // either the states of the sweep or G and the parts of dx.
 struct DistillLayout {
-    size_t ids, p, picked, stat, gs, states, G, part, total;
+    size_t ids, p, picked, stat, states, G, part, total;
 };
 static DistillLayout distill_layout(int N, int d, int Vd, int k) {
     DistillLayout L;
@@ -173,8 +173,7 @@ static DistillLayout distill_layout(int N, int d, int Vd, int k) {
     L.p = L.ids + list;
     L.picked = L.p + list;
     L.stat = L.picked + list;
-    L.gs = L.stat + row;
-    L.states = L.G = L.gs + row;
+    L.states = L.G = L.stat + row;
     L.part = align_up(L.G + 2 * (size_t)N * distill_grad_ldg(Vd), 256);
     const size_t a = L.part + distill_part_bytes(N, d, Vd), b = L.states + states_bytes(N, d, 0);
     L.total = align_up(a > b ? a : b, 256);
@@ -191,8 +190,8 @@ static wf_status check_distill(const wf_distill_args* a) {
     return WF_OK;
 }
 
-static TeacherCall teacher_of(const wf_distill_args* a, uint8_t* w, const DistillLayout& L) {
-    TeacherCall t{};
+static Teacher teacher_of(const wf_distill_args* a, void* ws) {
+    Teacher t{};
     t.tid = a->tid;
     t.tlogit = a->tlogit;
     t.t2d = a->t2d;
@@ -201,9 +200,7 @@ static TeacherCall teacher_of(const wf_distill_args* a, uint8_t* w, const Distil
     t.V = a->V;
     t.Vd = a->Vd;
     t.inv_t = 1.f / a->temperature;
-    t.ids = reinterpret_cast<int32_t*>(w + L.ids);
-    t.p = reinterpret_cast<float*>(w + L.p);
-    t.ctrl = reinterpret_cast<Control*>(w);
+    t.ctrl = reinterpret_cast<Control*>(ws);
     return t;
 }
 
@@ -726,9 +723,11 @@ wf_status wf_draft_distill(const wf_distill_args* a, void* ws, size_t ws_bytes, 
     WF_TRY(check_local({a->x, a->Wd, a->z}));
     uint8_t* w = static_cast<uint8_t*>(ws);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    TeacherCall t = teacher_of(a, w, L);
-    t.stat = reinterpret_cast<float*>(w + L.stat);
-    WF_TRY(launch_teacher(t, s));
+    const Teacher t = teacher_of(a, ws);
+    int32_t* ids = reinterpret_cast<int32_t*>(w + L.ids);
+    float* p = reinterpret_cast<float*>(w + L.p);
+    float* stat = reinterpret_cast<float*>(w + L.stat);
+    WF_TRY(launch_teacher(t, ids, p, stat, s));
     const int chunk = sweep_chunk(a->N, a->d);
     for (int r0 = 0; r0 < a->N; r0 += chunk) {
         const size_t list = (size_t)r0 * a->k;
@@ -739,7 +738,7 @@ wf_status wf_draft_distill(const wf_distill_args* a, void* ws, size_t ws_bytes, 
         c.d = a->d;
         c.V = a->Vd;
         c.inv_t = t.inv_t;
-        c.pick = t.ids + list;
+        c.pick = ids + list;
         c.K = a->k;
         c.picked = reinterpret_cast<float*>(w + L.picked) + list;
         c.states = w + L.states;
@@ -755,8 +754,8 @@ wf_status wf_draft_distill(const wf_distill_args* a, void* ws, size_t ws_bytes, 
         m.lse = a->lse + r0;
         m.picked = c.picked;
         m.ids = c.pick;
-        m.p = t.p + list;
-        m.stat = t.stat + r0;
+        m.p = p + list;
+        m.stat = stat + r0;
         m.loss = a->loss + r0;
         m.ctrl = t.ctrl;
         WF_TRY(launch_states_merge(m, s));
@@ -774,13 +773,8 @@ wf_status wf_draft_distill_grad(const wf_distill_args* a, void* ws, size_t ws_by
     WF_TRY(check_local({a->x, a->Wd, a->z, a->dx, a->dWd, ws}));
     uint8_t* w = static_cast<uint8_t*>(ws);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    TeacherCall t = teacher_of(a, w, L);
-    t.gloss = a->gloss;
-    t.gs = reinterpret_cast<float*>(w + L.gs);
-    WF_TRY(launch_teacher(t, s));
-    return launch_distill_grad(a->x, a->Wd, a->N, a->d, a->Vd, a->k, a->z, a->ldz, a->lse, t.ids, t.p, t.gs, a->dx,
-                               a->dWd, reinterpret_cast<uint16_t*>(w + L.G), reinterpret_cast<float*>(w + L.part),
-                               t.ctrl, s);
+    return launch_distill_grad(a->x, a->Wd, a->d, teacher_of(a, ws), a->z, a->ldz, a->lse, a->gloss, a->dx, a->dWd,
+                               reinterpret_cast<uint16_t*>(w + L.G), reinterpret_cast<float*>(w + L.part), s);
 }
 
 }  // extern "C"

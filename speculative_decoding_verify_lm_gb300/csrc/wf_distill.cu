@@ -16,8 +16,9 @@ namespace {
 
 // ------------------------------------------------------------------ G
 // Bound by the bytes of z (fp32, read) and G (bf16, written).  A thread takes 8
-// neighbouring ids at a time, GRAD_UNROLL such loads in flight; the few ids that
-// the teacher lists are put right behind a barrier, by the same CTA, from z.
+// neighbouring ids at a time, GRAD_UNROLL such loads in flight; meanwhile the
+// first warp works out the row's teacher, and behind a barrier puts the few ids
+// that it lists right, from z.
 constexpr int GRAD_THREADS = 256;
 constexpr int GRAD_UNROLL = 4;
 constexpr int GRAD_COLS = GRAD_THREADS * 8 * GRAD_UNROLL;
@@ -25,11 +26,9 @@ constexpr int GRAD_COLS = GRAD_THREADS * 8 * GRAD_UNROLL;
 struct GradParams {
     const float* z;
     int64_t ldz;
-    int N, Vd, K;
     const float* lse;
-    const float* gs;
-    const int32_t* ids;
-    const float* p;
+    const float* gloss;   // [N] or null: 1
+    Teacher t;
     uint16_t* G;
     int64_t ldg;
     int chunks;      // CTAs of a row
@@ -42,10 +41,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 }
 
 __global__ void __launch_bounds__(GRAD_THREADS) logit_grad_kernel(const GradParams a) {
+    __shared__ float row_gs;
     pdl_wait();
     pdl_trigger();
     const int n = blockIdx.x / a.chunks, v0 = (blockIdx.x % a.chunks) * GRAD_COLS;
-    const float gs = a.gs[n], off = a.lse[n];
+    const int Vd = a.t.Vd, lane = threadIdx.x & 31;
+    const float off = a.lse[n];
     const float* z = a.z + (size_t)n * a.ldz;
     uint16_t* G = a.G + (size_t)n * a.ldg;
     float4 f[GRAD_UNROLL][2];
@@ -54,16 +55,23 @@ __global__ void __launch_bounds__(GRAD_THREADS) logit_grad_kernel(const GradPara
         const int v = v0 + (u * GRAD_THREADS + (int)threadIdx.x) * 8;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
-            f[u][h] = gs != 0.f && v + 4 * h < a.Vd ? __ldcs(reinterpret_cast<const float4*>(z + v) + h)
-                                                    : make_float4(0.f, 0.f, 0.f, 0.f);
+            f[u][h] = v + 4 * h < Vd ? __ldcs(reinterpret_cast<const float4*>(z + v) + h)
+                                     : make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    TeacherRow r;
+    if (threadIdx.x < 32) {
+        r = teacher_row(a.t, n, lane);
+        if (lane == 0) row_gs = r.some ? (a.gloss ? a.gloss[n] : 1.f) * a.t.inv_t : 0.f;
+    }
+    __syncthreads();
+    const float gs = row_gs;
 #pragma unroll
     for (int u = 0; u < GRAD_UNROLL; ++u) {
         const int v = v0 + (u * GRAD_THREADS + (int)threadIdx.x) * 8;
-        if (v >= a.Vd) continue;
+        if (v >= Vd) continue;
         // ids from Vd on get 0: tensor copies look at a row's end in steps of 16 bytes
         auto q = [&](float x, int j) {
-            return gs == 0.f || v + j >= a.Vd ? 0.f : gs * ex2_approx((x - off) * LOG2E);
+            return gs == 0.f || v + j >= Vd ? 0.f : gs * ex2_approx((x - off) * LOG2E);
         };
         uint4 o;
         o.x = pack_bf16(q(f[u][0].x, 0), q(f[u][0].y, 1));
@@ -74,16 +82,25 @@ __global__ void __launch_bounds__(GRAD_THREADS) logit_grad_kernel(const GradPara
     }
     if (gs == 0.f) return;   // the same for the whole CTA
     __syncthreads();
-    if ((int)threadIdx.x < a.K) {
-        const int32_t* ids = a.ids + (size_t)n * a.K;
-        const float* p = a.p + (size_t)n * a.K;
-        const int j = threadIdx.x, id = ids[j];
-        // the first of a run of equal ids takes all of their probability
-        if (id >= v0 && id < v0 + GRAD_COLS && id < a.Vd && (j == 0 || ids[j - 1] != id)) {
-            float pt = 0.f;
-            for (int i = j; i < a.K && ids[i] == id; ++i) pt += p[i];
-            const float q = ex2_approx((z[id] - off) * LOG2E);
-            G[id] = (uint16_t)pack_bf16(gs * (q - pt), 0.f);
+    if (threadIdx.x < 32) {
+        // the first place that names an id takes the probability of all that do
+        float pt[2] = {0.f, 0.f};
+        bool again[2] = {false, false};
+        for (int j = 0; j < a.t.K; ++j) {
+            const int id = __shfl_sync(0xffffffffu, j < 32 ? r.id[0] : r.id[1], j & 31);
+            const float p = __shfl_sync(0xffffffffu, j < 32 ? r.p[0] : r.p[1], j & 31);
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (id == r.id[h]) {
+                    pt[h] += p;
+                    again[h] |= j < lane + 32 * h;
+                }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int id = r.id[h];
+            if (lane + 32 * h < a.t.K && !again[h] && id >= v0 && id < v0 + GRAD_COLS && id < Vd)
+                G[id] = (uint16_t)pack_bf16(gs * (ex2_approx((z[id] - off) * LOG2E) - pt[h]), 0.f);
         }
     }
 }
@@ -447,39 +464,34 @@ size_t distill_part_bytes(int N, int d, int Vd) {
     return (size_t)(most < MAX_PARTS ? most : MAX_PARTS) * TM * TN * 4;
 }
 
-// ids, p, gs: as launch_teacher left them.  G and part: scratch.
-wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int N, int d, int Vd, int K, const float* z,
-                              int64_t ldz, const float* lse, const int32_t* ids, const float* pr, const float* gs,
-                              uint16_t* dx, uint16_t* dWd, uint16_t* G, float* part, Control* ctrl, cudaStream_t s) {
+// G and part: scratch.
+wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int d, const Teacher& t, const float* z,
+                              int64_t ldz, const float* lse, const float* gloss, uint16_t* dx, uint16_t* dWd,
+                              uint16_t* G, float* part, cudaStream_t s) {
+    const int N = t.N, Vd = t.Vd;
     GradParams a{};
     a.z = z;
     a.ldz = ldz;
-    a.N = N;
-    a.Vd = Vd;
-    a.K = K;
     a.lse = lse;
-    a.gs = gs;
-    a.ids = ids;
-    a.p = pr;
+    a.gloss = gloss;
+    a.t = t;
     a.G = G;
     a.ldg = (int64_t)distill_grad_ldg(Vd);
     a.chunks = cdiv(Vd, GRAD_COLS);
-    wf_status st = launch(logit_grad_kernel, dim3((unsigned)N * a.chunks), dim3(GRAD_THREADS), 0, s, a);
-    if (st != WF_OK) return st;
-
     static std::mutex mu;
     static bool attr_set[64] = {false};
     static int pairs[64];
     const int smem = pipe_smem(PROD_STAGES, PROD_STAGE, PROD_WARPS * OUT_BOX);
-    st = configure_once(mu, attr_set, [&] {
-        if (cudaFuncSetAttribute(grad_products_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
-            cudaSuccess)
+    wf_status st = configure_once(mu, attr_set, [&] {
+        if (!set_smem(grad_products_kernel, smem) || !set_smem(logit_grad_kernel, 0) || !set_smem(dx_join_kernel, 0))
             return false;
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return false;
         if (dev < 64) pairs[dev] = resident_pairs(reinterpret_cast<const void*>(grad_products_kernel), PROD_THREADS, smem);
         return true;
     });
+    if (st != WF_OK) return st;
+    st = launch(logit_grad_kernel, dim3((unsigned)N * a.chunks), dim3(GRAD_THREADS), 0, s, a);
     if (st != WF_OK) return st;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return WF_ERR_CUDA;
@@ -507,7 +519,7 @@ wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int N, int 
     p.late = p.x_units % slots;
     const double ux = (double)pl.kb_x / pl.split + (pl.split > 1 ? X_PART_OUT : TILE_FIXED);
     p.lead = p.late ? (int)(ux / w_cost(pl.kb_w) + 0.5) : 0;
-    p.ctrl = ctrl;
+    p.ctrl = t.ctrl;
     p.timeout_ns = wait_timeout_ns();
     CUtensorMap gk, gm, tw, tx, tdx, tdw;
     if (!make_tile_map(&gk, G, N, Vd, a.ldg, false, BK, pl.flip ? pl.flip / 2 : BM) || !make_tile_map(&gm, G, N, Vd, a.ldg, false, 64, pl.w_rows) ||

@@ -10,21 +10,6 @@ namespace {
 
 constexpr int LIST_WARPS = 4;
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-    return v;
-}
-// NaN wins
-__device__ __forceinline__ float warp_max(float v) {
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1) {
-        const float o = __shfl_xor_sync(0xffffffffu, v, off);
-        v = v != v || o <= v ? v : o;
-    }
-    return v;
-}
-
 // The rank of each lane's two entries (places lane and lane + 32 of n <= 64)
 // among all, by id and then by place.
 __device__ __forceinline__ void ranks(const int (&id)[2], int n, int lane, int (&rank)[2]) {
@@ -69,78 +54,24 @@ __global__ void __launch_bounds__(LIST_WARPS * 32) sort_tokens_kernel(const int3
         }
 }
 
-// One warp a row: p = softmax of the kept alternatives' logits / T, the others'
-// (no id, no draft id, or a logit of -inf) 0; entries of the same id stay apart,
-// their probabilities add up where they are used.  fp32 throughout.
-__global__ void __launch_bounds__(LIST_WARPS * 32) teacher_kernel(const TeacherCall t) {
+// One warp a row.
+__global__ void __launch_bounds__(LIST_WARPS * 32) teacher_kernel(const Teacher t, int32_t* ids, float* p,
+                                                                  float* stat) {
     pdl_wait();
     pdl_trigger();
     const int row = blockIdx.x * LIST_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (row >= t.N) return;
+    const TeacherRow r = teacher_row(t, row, lane);
+    int rank[2];
+    ranks(r.id, t.K, lane, rank);
     const size_t base = (size_t)row * t.K;
-    int id[2], rank[2];
-    float l[2], p[2];
-    bool bad = false;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int j = lane + 32 * h;
-        id[h] = PICK_NONE;
-        l[h] = -INFINITY;
-        if (j < t.K) {
-            int v = t.tid[base + j];
-            bool none = v == -1;
-            if (!none && t.t2d) {
-                if (v < 0 || v >= t.V) {
-                    bad = true;
-                    none = true;
-                } else {
-                    v = t.t2d[v];
-                    none = v < 0;   // no draft id for this target id
-                }
-            }
-            if (!none && (v < 0 || v >= t.Vd)) {
-                bad = true;
-                none = true;
-            }
-            if (!none) {
-                l[h] = t.tlogit[base + j];
-                if (l[h] != -INFINITY) id[h] = v;
-            }
-        }
-    }
-    bad = __any_sync(0xffffffffu, bad);
-    if (bad) {   // the row takes no part
-        id[0] = id[1] = PICK_NONE;
-        l[0] = l[1] = -INFINITY;
-        if (lane == 0) record_error(t.ctrl, WF_ERR_BAD_DATA, (uint32_t)row);
-    }
-    const float top = warp_max(l[0] != l[0] || l[1] <= l[0] ? l[0] : l[1]);
-    const bool some = top != -INFINITY;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) p[h] = some && id[h] != PICK_NONE ? expf((l[h] - top) * t.inv_t) : 0.f;
-    const float total = warp_sum(p[0] + p[1]);
-    float plogp = 0.f;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        if (some && id[h] != PICK_NONE) {
-            // log p from the logits: a p that rounds to 0 has a finite logarithm, times 0
-            const float logp = (l[h] - top) * t.inv_t - logf(total);
-            p[h] /= total;
-            plogp += p[h] == 0.f ? 0.f : p[h] * logp;
-        }
-    }
-    plogp = warp_sum(plogp);
-    ranks(id, t.K, lane, rank);
 #pragma unroll
     for (int h = 0; h < 2; ++h)
         if (lane + 32 * h < t.K) {
-            t.ids[base + rank[h]] = id[h];
-            t.p[base + rank[h]] = p[h];
+            ids[base + rank[h]] = r.id[h];
+            p[base + rank[h]] = r.p[h];
         }
-    if (lane == 0) {
-        if (t.stat) t.stat[row] = bad ? __int_as_float(0x7fc00000) : plogp;
-        if (t.gs) t.gs[row] = some ? (t.gloss ? t.gloss[row] : 1.f) * t.inv_t : 0.f;
-    }
+    if (lane == 0) stat[row] = r.plogp;
 }
 
 // One CTA a row, one thread a state; a fixed order of merging makes the result
@@ -270,17 +201,32 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const Me
 
 }  // namespace
 
+static wf_status configure() {
+    static std::mutex mu;
+    static bool attr_set[64] = {false};
+    return configure_once(mu, attr_set, [] {
+        return set_smem(sort_tokens_kernel, 0) && set_smem(teacher_kernel, 0) && set_smem(states_merge_kernel<0>, 0) &&
+               set_smem(states_merge_kernel<10>, 0) && set_smem(states_merge_kernel<16>, 0);
+    });
+}
+
 wf_status launch_sort_tokens(const int32_t* tok, int rows, int S, int V, int32_t* ids, int32_t* order, float* logp,
                              Control* ctrl, cudaStream_t s) {
+    const wf_status st = configure();
+    if (st != WF_OK) return st;
     return launch(sort_tokens_kernel, dim3(cdiv(rows, LIST_WARPS)), dim3(LIST_WARPS * 32), 0, s, tok, rows, S, V, ids,
                   order, logp, ctrl);
 }
 
-wf_status launch_teacher(const TeacherCall& t, cudaStream_t s) {
-    return launch(teacher_kernel, dim3(cdiv(t.N, LIST_WARPS)), dim3(LIST_WARPS * 32), 0, s, t);
+wf_status launch_teacher(const Teacher& t, int32_t* ids, float* p, float* stat, cudaStream_t s) {
+    const wf_status st = configure();
+    if (st != WF_OK) return st;
+    return launch(teacher_kernel, dim3(cdiv(t.N, LIST_WARPS)), dim3(LIST_WARPS * 32), 0, s, t, ids, p, stat);
 }
 
 wf_status launch_states_merge(const MergeCall& c, cudaStream_t s) {
+    const wf_status st = configure();
+    if (st != WF_OK) return st;
     const dim3 block(cdiv(c.slots, 32) * 32);
     switch (state_width(c.k)) {
         case 0: return launch(states_merge_kernel<0>, dim3(c.rows), block, 0, s, c);

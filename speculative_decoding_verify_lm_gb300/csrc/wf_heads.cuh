@@ -54,22 +54,18 @@ wf_status launch_sweep(const SweepCall& c, int* slots, cudaStream_t s);
 wf_status launch_sort_tokens(const int32_t* tok, int rows, int S, int V, int32_t* ids, int32_t* order, float* logp,
                              Control* ctrl, cudaStream_t s);
 
-// A teacher's alternatives as the draft head's: ids mapped, sorted, with their
-// probabilities.
-struct TeacherCall {
+// A teacher's alternatives.
+struct Teacher {
     const int32_t* tid;      // [N][K]
     const float* tlogit;     // [N][K]
     const int32_t* t2d;      // [V] or null: tid are draft ids
     int N, K, V, Vd;
     float inv_t;
-    const float* gloss;      // [N] or null: 1
-    int32_t* ids;            // out [N][K] ascending draft ids, PICK_NONE last
-    float* p;                // out [N][K] their probabilities
-    float* stat;             // out [N] sum p log p; NaN: an id out of range; or null
-    float* gs;               // out [N] gloss / T, 0 for a row without a teacher; or null
     Control* ctrl;
 };
-wf_status launch_teacher(const TeacherCall& t, cudaStream_t s);
+// ... as sorted lists: ids [N][K] ascending draft ids, PICK_NONE last, p their probabilities, stat [N] sum p log p (NaN: an id
+// out of range).
+wf_status launch_teacher(const Teacher& t, int32_t* ids, float* p, float* stat, cudaStream_t s);
 
 struct MergeCall {
     const uint8_t* states;   // [rows][slots]
@@ -113,6 +109,86 @@ __device__ __forceinline__ void state_merge(float c, float& M, float& S, float& 
     T = (a1 == 0.f && S == S ? 0.f : (T + d1 * S) * a1) + (a2 == 0.f && s2 == s2 ? 0.f : (t2 + d2 * s2) * a2);
     S = S * a1 + s2 * a2;
     M = mx;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+    return v;
+}
+// NaN wins
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        const float o = __shfl_xor_sync(0xffffffffu, v, off);
+        v = v != v || o <= v ? v : o;
+    }
+    return v;
+}
+
+// One row's alternatives by one warp: lane l has places l and l + 32.
+struct TeacherRow {
+    int id[2];      // draft id, PICK_NONE for a place that is not kept
+    float p[2];     // softmax of the kept logits / T; entries of one id stay apart
+    float plogp;    // sum p log p; NaN if an id is out of range
+    bool some;      // whether the row has a kept alternative
+};
+__device__ __forceinline__ TeacherRow teacher_row(const Teacher& t, int row, int lane) {
+    const size_t base = (size_t)row * t.K;
+    TeacherRow r;
+    float l[2];
+    bool bad = false;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int j = lane + 32 * h;
+        r.id[h] = PICK_NONE;
+        l[h] = -INFINITY;
+        if (j < t.K) {
+            int v = t.tid[base + j];
+            const float logit = t.tlogit[base + j];
+            bool none = v == -1;
+            if (!none && t.t2d) {
+                if (v < 0 || v >= t.V) {
+                    bad = true;
+                    none = true;
+                } else {
+                    v = t.t2d[v];
+                    none = v < 0;   // no draft id for this target id
+                }
+            }
+            if (!none && (v < 0 || v >= t.Vd)) {
+                bad = true;
+                none = true;
+            }
+            if (!none && logit != -INFINITY) {
+                l[h] = logit;
+                r.id[h] = v;
+            }
+        }
+    }
+    bad = __any_sync(0xffffffffu, bad);
+    if (bad) {   // the row takes no part
+        r.id[0] = r.id[1] = PICK_NONE;
+        l[0] = l[1] = -INFINITY;
+        if (lane == 0) record_error(t.ctrl, WF_ERR_BAD_DATA, (uint32_t)row);
+    }
+    const float top = warp_max(l[0] != l[0] || l[1] <= l[0] ? l[0] : l[1]);
+    r.some = top != -INFINITY;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) r.p[h] = r.some && r.id[h] != PICK_NONE ? expf((l[h] - top) * t.inv_t) : 0.f;
+    const float total = warp_sum(r.p[0] + r.p[1]);
+    float plogp = 0.f;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        if (r.some && r.id[h] != PICK_NONE) {
+            // log p from the logits: a p that rounds to 0 has a finite logarithm, times 0
+            const float logp = (l[h] - top) * t.inv_t - logf(total);
+            r.p[h] /= total;
+            plogp += r.p[h] == 0.f ? 0.f : r.p[h] * logp;
+        }
+    }
+    r.plogp = bad ? __int_as_float(0x7fc00000) : warp_sum(plogp);
+    return r;
 }
 
 }  // namespace wf

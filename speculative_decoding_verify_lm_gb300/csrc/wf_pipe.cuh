@@ -23,9 +23,9 @@ namespace wf {
 
 // Threads with `w` epilogue warps (4 or 8: a warp reads the 32 accumulator rows that its number mod 4 gives).
 constexpr int pipe_threads(int w) { return 64 + 32 * w; }
-constexpr int PIPE_MAX_STAGES = 8;
+constexpr int PIPE_MAX_STAGES = 12;
 constexpr int PIPE_TMEM_COLS = 2 * BN;     // two fp32 accumulators of up to BN columns
-constexpr int PIPE_BARRIER_BYTES = 256;    // barriers, TMEM address and abort flag behind the ring
+constexpr int PIPE_BARRIER_BYTES = 512;    // barriers, TMEM address and abort flag behind the ring
 constexpr int PIPE_SMEM_MAX = 227 * 1024;
 constexpr int PIPE_STATIC_MAX = 512;       // of it, for a kernel's static shared memory
 // What a kernel records beside WF_ERR_TIMEOUT: which wait gave up.
@@ -313,6 +313,15 @@ __device__ __forceinline__ uint32_t swizzled(int r, int u) { return (uint32_t)(r
 // written in boxes of box_cols (128 bytes) x box_rows, 128-byte swizzle.
 bool make_tile_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t stride, bool fp32,
                    uint32_t box_cols, uint32_t box_rows);
+// Dynamic shared memory that a kernel may ask for, and an SM set up for as much shared memory as there is: what runs
+// before and after a sweep then fits beside it (its prologue is over when the sweep ends) and no SM is set up anew in
+// between.  Where a merge did not fit, a call took 3 to 15 us longer.
+template <typename K>
+inline bool set_smem(K kernel, int bytes) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess &&
+           cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                cudaSharedmemCarveoutMaxShared) == cudaSuccess;
+}
 // Clusters of two CTAs of `kernel` that can be resident at once, at most REC_PAIRS.
 int resident_pairs(const void* kernel, int threads, int smem);
 constexpr int REC_PAIRS = 80;

@@ -24,6 +24,7 @@ namespace wf {
 namespace {
 
 constexpr int SWEEP_THREADS = pipe_threads(4);
+constexpr int SWEEP_SMEM = 220 * 1024;   // leaves room on the SM for the merge's and the lists' CTAs
 constexpr int STAGING = 4 * 2 * 4096;     // kept logits: two boxes of 32 rows x 128 bytes a warp
 
 struct SweepParams {
@@ -456,10 +457,8 @@ wf_status launch_kt(const SweepCall& c, int* slots_out, cudaStream_t s) {
     static std::mutex mu;
     static bool attr_set[64] = {false};
     const wf_status cst = configure_once(mu, attr_set, [] {
-        return cudaFuncSetAttribute(sweep_kernel<KT, ENT, Z, false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    PIPE_SMEM_MAX - PIPE_STATIC_MAX) == cudaSuccess &&
-               cudaFuncSetAttribute(sweep_kernel<KT, ENT, Z, true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    PIPE_SMEM_MAX - PIPE_STATIC_MAX) == cudaSuccess;
+        return set_smem(sweep_kernel<KT, ENT, Z, false>, SWEEP_SMEM) &&
+               set_smem(sweep_kernel<KT, ENT, Z, true>, SWEEP_SMEM);
     });
     if (cst != WF_OK) return cst;
     const bool pair = c.rows > BM;
@@ -471,11 +470,6 @@ wf_status launch_kt(const SweepCall& c, int* slots_out, cudaStream_t s) {
     p.num_k = cdiv(c.d, BK);
     const int a_rows = pair ? BM : (c.rows + 7) / 8 * 8;   // a short box reads no rows that are not there
     p.a_bytes = a_rows * BK * 2;
-    const int b_bytes = (pair ? BN / 2 : BN) * BK * 2, extra = Z ? STAGING : 0;
-    p.stage_bytes = p.a_bytes + b_bytes;
-    p.stages = (PIPE_SMEM_MAX - PIPE_STATIC_MAX - PIPE_BARRIER_BYTES - 1024 - extra) / p.stage_bytes;
-    if (p.stages > PIPE_MAX_STAGES) p.stages = PIPE_MAX_STAGES;
-    const int smem = pipe_smem(p.stages, p.stage_bytes, extra);
     int slots = 0;
     if (pair) {
         static std::mutex pmu;
@@ -484,7 +478,8 @@ wf_status launch_kt(const SweepCall& c, int* slots_out, cudaStream_t s) {
         if (cudaGetDevice(&dev) != cudaSuccess) return WF_ERR_CUDA;
         std::lock_guard<std::mutex> lock(pmu);
         if (dev >= 64 || !pairs[dev]) {
-            slots = resident_pairs(reinterpret_cast<const void*>(sweep_kernel<KT, ENT, Z, true>), SWEEP_THREADS, smem);
+            slots = resident_pairs(reinterpret_cast<const void*>(sweep_kernel<KT, ENT, Z, true>), SWEEP_THREADS,
+                                   SWEEP_SMEM);
             if (dev < 64) pairs[dev] = slots;
         } else {
             slots = pairs[dev];
@@ -493,6 +488,13 @@ wf_status launch_kt(const SweepCall& c, int* slots_out, cudaStream_t s) {
         slots = num_sms() < STATE_SLOTS ? num_sms() : STATE_SLOTS;
     }
     const Tiles t = tiles_of(c.V, slots, p.num_mt, Z);
+    const int b_bytes = (pair ? t.bn / 2 : t.bn) * BK * 2, extra = Z ? STAGING : 0;
+    p.stage_bytes = p.a_bytes + b_bytes;
+    // an MMA reads BM rows of A whatever the box holds: the last stage's may reach past a stage that is shorter
+    const int reach = BM * BK * 2 > p.stage_bytes ? BM * BK * 2 - p.stage_bytes : 0;
+    p.stages = (SWEEP_SMEM - PIPE_BARRIER_BYTES - 1024 - extra - reach) / p.stage_bytes;
+    if (p.stages > PIPE_MAX_STAGES) p.stages = PIPE_MAX_STAGES;
+    const int smem = pipe_smem(p.stages, p.stage_bytes, extra) + reach;
     p.num_n = t.num_n;
     p.bn = t.bn;
     p.nbig = t.nbig;

@@ -517,7 +517,7 @@ def wf_lmhead_logprobs(hidden, W, ws: LogprobsWorkspace, tok=None, k: int = 0, t
                        stream=None) -> Logprobs:
     """Log-probabilities of given tokens tok [P] or [P, S] (-1: none) under softmax(hidden W^T / temperature), the
     log-sum-exp, the entropy (with_entropy, or H given) and the k best alternatives of each row.  Outputs not given
-    are allocated, in one piece."""
+    are allocated."""
     hp, Wp = _head(hidden, W, ("hidden", "W"))
     (P, d), V = hidden.shape, W.shape[0]
     S = tp = 0
@@ -527,42 +527,39 @@ def wf_lmhead_logprobs(hidden, W, ws: LogprobsWorkspace, tok=None, k: int = 0, t
         if not 1 <= S <= WF_MAX_LISTED or shape[0] != P:
             raise ValueError(f"tok must be [P] or [P, S], S up to {WF_MAX_LISTED}")
         tp = _shaped(tok, "tok", shape, _I32, hidden)
-    # what is not given: pieces of one allocation, which takes as long as each of five would
-    want = P * ((S if tok is not None and logp is None else 0) + (lse is None) + (with_entropy and H is None) +
-                (k if k > 0 and top_ids is None else 0) + (k if k > 0 and top_logp is None else 0))
-    buf = torch.empty(want, dtype=torch.float32, device=hidden.device) if want > 0 else None
-    base = buf.data_ptr() if want > 0 else 0
-    at = 0
-    lp = lsep = Hp = idp = tlp = 0
+    # (pieces of one allocation would take longer: a view costs most of what an allocation does)
+    new, dev = torch.empty, hidden.device
+    lp = Hp = idp = tlp = 0
     if tok is None:
         logp = None
     elif logp is None:
-        logp, lp = torch.as_strided(buf, shape, (S, 1) if len(shape) == 2 else (1,), at), base + 4 * at
-        at += P * S
+        logp = new(shape, dtype=torch.float32, device=dev)
+        lp = logp.data_ptr()
     else:
         lp = _shaped(logp, "logp", shape, _F32, hidden)
     if lse is None:
-        lse, lsep = torch.as_strided(buf, (P,), (1,), at), base + 4 * at
-        at += P
+        lse = new(P, dtype=torch.float32, device=dev)
+        lsep = lse.data_ptr()
     else:
         lsep = _shaped(lse, "lse", (P,), _F32, hidden)
     if H is not None:
         Hp = _shaped(H, "H", (P,), _F32, hidden)
     elif with_entropy:
-        H, Hp = torch.as_strided(buf, (P,), (1,), at), base + 4 * at
-        at += P
+        H = torch.empty_like(lse)
+        Hp = H.data_ptr()
     if k <= 0:
         top_ids = top_logp = None
     else:
-        if top_logp is None:
-            top_logp, tlp = torch.as_strided(buf, (P, k), (k, 1), at), base + 4 * at
-            at += P * k
-        else:
-            tlp = _shaped(top_logp, "top_logp", (P, k), _F32, hidden)
         if top_ids is None:
-            top_ids, idp = torch.as_strided(buf.view(torch.int32), (P, k), (k, 1), at), base + 4 * at
+            top_ids = new((P, k), dtype=torch.int32, device=dev)
+            idp = top_ids.data_ptr()
         else:
             idp = _shaped(top_ids, "top_ids", (P, k), _I32, hidden)
+        if top_logp is None:
+            top_logp = new((P, k), dtype=torch.float32, device=dev)
+            tlp = top_logp.data_ptr()
+        else:
+            tlp = _shaped(top_logp, "top_logp", (P, k), _F32, hidden)
     args = _LOGPROBS.pack(hp, Wp, P, d, V, temperature, tp, S, k, lp, lsep, Hp, idp, tlp)
     st = (_lib or lib()).wf_lmhead_logprobs(args, *_own_ws(ws, LogprobsWorkspace), _stream(stream))
     if st:
