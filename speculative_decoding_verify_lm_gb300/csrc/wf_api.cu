@@ -685,6 +685,7 @@ wf_status wf_lmhead_logprobs(const wf_logprobs_args* a, void* ws, size_t ws_byte
         c.states = w + L.states;
         c.k = a->k;
         c.entropy = true;
+        c.after_lists = r0 == 0 && a->S > 1;
         c.ctrl = ctrl;
         MergeCall m{};
         WF_TRY(launch_sweep(c, &m.slots, s));
@@ -744,6 +745,7 @@ wf_status wf_draft_distill(const wf_distill_args* a, void* ws, size_t ws_bytes, 
         c.states = w + L.states;
         c.z = a->z ? a->z + (size_t)r0 * a->ldz : nullptr;
         c.ldz = a->ldz;
+        c.after_lists = r0 == 0;
         c.ctrl = t.ctrl;
         MergeCall m{};
         WF_TRY(launch_sweep(c, &m.slots, s));

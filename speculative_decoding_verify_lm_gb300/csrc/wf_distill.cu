@@ -42,8 +42,7 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 __global__ void __launch_bounds__(GRAD_THREADS) logit_grad_kernel(const GradParams a) {
     __shared__ float row_gs;
-    pdl_wait();
-    pdl_trigger();
+    pdl_trigger();   // the products may start
     const int n = blockIdx.x / a.chunks, v0 = (blockIdx.x % a.chunks) * GRAD_COLS;
     const int Vd = a.t.Vd, lane = threadIdx.x & 31;
     const float off = a.lse[n];
@@ -235,8 +234,7 @@ __global__ void __launch_bounds__(PROD_THREADS, 1)
         tma_prefetch_desc(&tmDw);
     }
     const uint32_t tmem_base = pipe_begin<true, PROD_WARPS>(g);
-    if (warp != 0) pdl_wait();   // warp 0: as it copies
-    pdl_trigger();
+    if (warp != 0) pdl_wait();   // warp 0: before it copies
     if (warp == 0) {
         const uint64_t pol = policy_evict_normal();
         Unit u{};
@@ -308,6 +306,7 @@ __global__ void __launch_bounds__(PROD_THREADS, 1)
                 fence_async_store();
                 __syncwarp();
                 if (lane == 0) tma_store_2d(u.dx ? &tmDx : &tmDw, stage, col, y);
+                __syncwarp();
             };
             if (u.dx && p.flip) {
                 // thread = one column of dx, accumulator columns = its rows: a warp's stores are whole lines
@@ -378,8 +377,6 @@ __global__ void __launch_bounds__(PROD_THREADS, 1)
 // dx from the parts of a split product, added in order.
 __global__ void __launch_bounds__(256) dx_join_kernel(const float* part, int parts, int part_rows, int N, int d,
                                                       uint16_t* dx) {
-    pdl_wait();
-    pdl_trigger();
     const long units = (long)N * (d / 8);
     for (long i = (long)blockIdx.x * 256 + threadIdx.x; i < units; i += (long)gridDim.x * 256) {
         const int n = (int)(i / (d / 8)), c = (int)(i % (d / 8)) * 8;
@@ -491,7 +488,7 @@ wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int d, cons
         return true;
     });
     if (st != WF_OK) return st;
-    st = launch(logit_grad_kernel, dim3((unsigned)N * a.chunks), dim3(GRAD_THREADS), 0, s, a);
+    st = launch_plain(logit_grad_kernel, dim3((unsigned)N * a.chunks), dim3(GRAD_THREADS), 0, s, 1u, a);
     if (st != WF_OK) return st;
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return WF_ERR_CUDA;
@@ -536,7 +533,7 @@ wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int d, cons
     if (st != WF_OK || !dx || !parts) return st;
     const long units = (long)N * (d / 8);
     const int blocks = (int)(cdiv(units, 256) < 8 * num_sms() ? cdiv(units, 256) : 8 * num_sms());
-    return launch(dx_join_kernel, dim3(blocks), dim3(256), 0, s, (const float*)part, pl.split, pl.part_rows, N, d, dx);
+    return launch_plain(dx_join_kernel, dim3(blocks), dim3(256), 0, s, 1u, (const float*)part, pl.split, pl.part_rows, N, d, dx);
 }
 
 }  // namespace wf

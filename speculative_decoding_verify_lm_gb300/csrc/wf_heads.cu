@@ -25,8 +25,7 @@ __device__ __forceinline__ void ranks(const int (&id)[2], int n, int lane, int (
 __global__ void __launch_bounds__(LIST_WARPS * 32) sort_tokens_kernel(const int32_t* tok, int rows, int S, int V,
                                                                       int32_t* ids, int32_t* order, float* logp,
                                                                       Control* ctrl) {
-    pdl_wait();
-    pdl_trigger();
+    pdl_trigger();   // the sweep may start and ask for its first weights
     const int row = blockIdx.x * LIST_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (row >= rows) return;
     const size_t base = (size_t)row * S;
@@ -57,8 +56,7 @@ __global__ void __launch_bounds__(LIST_WARPS * 32) sort_tokens_kernel(const int3
 // One warp a row.
 __global__ void __launch_bounds__(LIST_WARPS * 32) teacher_kernel(const Teacher t, int32_t* ids, float* p,
                                                                   float* stat) {
-    pdl_wait();
-    pdl_trigger();
+    pdl_trigger();   // the sweep may start and ask for its first weights
     const int row = blockIdx.x * LIST_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (row >= t.N) return;
     const TeacherRow r = teacher_row(t, row, lane);
@@ -83,8 +81,6 @@ template <int KT>
 __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const MergeCall c) {
     __shared__ float wm[MERGE_WARPS], wsum[MERGE_WARPS], wt[MERGE_WARPS];
     __shared__ uint64_t wbest[MERGE_WARPS * 16];
-    pdl_wait();
-    pdl_trigger();
     const int row = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
     const float cc = LOG2E * c.inv_t;
     float M = -INFINITY, S = 0.f, T = 0.f;
@@ -214,14 +210,14 @@ wf_status launch_sort_tokens(const int32_t* tok, int rows, int S, int V, int32_t
                              Control* ctrl, cudaStream_t s) {
     const wf_status st = configure();
     if (st != WF_OK) return st;
-    return launch(sort_tokens_kernel, dim3(cdiv(rows, LIST_WARPS)), dim3(LIST_WARPS * 32), 0, s, tok, rows, S, V, ids,
+    return launch_plain(sort_tokens_kernel, dim3(cdiv(rows, LIST_WARPS)), dim3(LIST_WARPS * 32), 0, s, 1u, tok, rows, S, V, ids,
                   order, logp, ctrl);
 }
 
 wf_status launch_teacher(const Teacher& t, int32_t* ids, float* p, float* stat, cudaStream_t s) {
     const wf_status st = configure();
     if (st != WF_OK) return st;
-    return launch(teacher_kernel, dim3(cdiv(t.N, LIST_WARPS)), dim3(LIST_WARPS * 32), 0, s, t, ids, p, stat);
+    return launch_plain(teacher_kernel, dim3(cdiv(t.N, LIST_WARPS)), dim3(LIST_WARPS * 32), 0, s, 1u, t, ids, p, stat);
 }
 
 wf_status launch_states_merge(const MergeCall& c, cudaStream_t s) {
@@ -229,9 +225,9 @@ wf_status launch_states_merge(const MergeCall& c, cudaStream_t s) {
     if (st != WF_OK) return st;
     const dim3 block(cdiv(c.slots, 32) * 32);
     switch (state_width(c.k)) {
-        case 0: return launch(states_merge_kernel<0>, dim3(c.rows), block, 0, s, c);
-        case 10: return launch(states_merge_kernel<10>, dim3(c.rows), block, 0, s, c);
-        default: return launch(states_merge_kernel<16>, dim3(c.rows), block, 0, s, c);
+        case 0: return launch_plain(states_merge_kernel<0>, dim3(c.rows), block, 0, s, 1u, c);
+        case 10: return launch_plain(states_merge_kernel<10>, dim3(c.rows), block, 0, s, 1u, c);
+        default: return launch_plain(states_merge_kernel<16>, dim3(c.rows), block, 0, s, 1u, c);
     }
 }
 

@@ -44,6 +44,7 @@ struct SweepCall {
     bool entropy;
     float* z;                // [rows][ldz] logits times inv_t, or null
     int64_t ldz;
+    bool after_lists;        // the kernel before on the stream is this call's that made the lists
     Control* ctrl;
 };
 // Enqueues the sweep; *slots: states left for each row (row-major, in use all of them).

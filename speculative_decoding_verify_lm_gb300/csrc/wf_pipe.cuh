@@ -107,6 +107,7 @@ __device__ __forceinline__ uint32_t pipe_begin(const Pipe& g) {
 
 template <bool PAIR>
 __device__ __forceinline__ void pipe_end(const Pipe& g, uint32_t tmem_base) {
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     if constexpr (PAIR) cluster_sync();   // the first CTA's MMAs and the second's remote arrivals are done
@@ -126,7 +127,8 @@ __device__ __forceinline__ void pipe_end(const Pipe& g, uint32_t tmem_base) {
 // `bar` (PAIR: the first CTA's), each box by a lane of its own: one thread issuing
 // four boxes of 64 rows takes 900 cycles a stage, their products 512.
 // EARLY: B is a weight matrix, whose first stages are asked for while the kernel
-// before is still finishing; everything else waits for it.
+// before (of the same call, which has itself waited for what came before it) is
+// still running; everything else waits for it.
 template <bool PAIR, bool EARLY, typename Next, typename Tx, typename Load>
 __device__ __forceinline__ void pipe_copy(const Pipe& g, bool first, Next next, Tx tx, Load load) {
     const int lane = threadIdx.x & 31;
@@ -170,6 +172,9 @@ __device__ __forceinline__ void pipe_copy(const Pipe& g, bool first, Next next, 
         num_k = next(++i);
         bytes = tx();
     }
+    // the last stages' releases have arrived too before the CTA's shared memory is another's
+    for (uint32_t j = (it > (uint32_t)g.stages ? it - g.stages : 0); ok && j < it; ++j)
+        ok = __all_sync(0xffffffffu, mbar_wait(&g.empty[j % g.stages], (j / g.stages) & 1, g.timeout_ns, g.abort_flag));
     if (!ok || __any_sync(0xffffffffu, *g.abort_flag)) {
         // let every copy this warp issued land before the CTA exits
         if (!PAIR || first) {
@@ -248,13 +253,18 @@ __device__ __forceinline__ void pipe_mma(const Pipe& g, uint32_t tmem_base, Next
     }
 }
 
-// Epilogue warps: wait for the i-th accumulator, and hand it back.
+// Epilogue warps (all lanes): wait for the i-th accumulator, and hand it back.
+// The lanes leave the wait, or give it up, together: what follows (accumulator
+// reads, votes) is for whole warps.
 __device__ __forceinline__ bool pipe_acc_wait(const Pipe& g, uint32_t i) {
-    if (!mbar_wait(&g.tfull[i & 1], (i >> 1) & 1, g.timeout_ns, g.abort_flag)) {
+    __syncwarp();
+    const bool there = mbar_wait(&g.tfull[i & 1], (i >> 1) & 1, g.timeout_ns, g.abort_flag);
+    if (!__all_sync(0xffffffffu, there)) {
         g.fail(PIPE_WHERE_TILE);
         return false;
     }
     tc_fence_after();
+    __syncwarp();
     return true;
 }
 // tempty_first: in a pair's second CTA the shared::cluster address of the first CTA's accumulator barriers, else 0.
@@ -313,6 +323,31 @@ __device__ __forceinline__ uint32_t swizzled(int r, int u) { return (uint32_t)(r
 // written in boxes of box_cols (128 bytes) x box_rows, 128-byte swizzle.
 bool make_tile_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols, uint64_t stride, bool fp32,
                    uint32_t box_cols, uint32_t box_rows);
+// Stream order of these kernels.  A sweep or a product takes every SM nearly whole
+// (all tensor memory, up to 226 KB of shared memory, CTA pairs that need both SMs of
+// a pair free at once), so nothing may sit waiting beside one that is not yet
+// running everywhere: what follows it, and what begins a call, is launched in
+// plain stream order.  Only the kernel straight before it in the same call (the
+// lists, the pass that makes G) lets it start early; their CTAs are small enough
+// to fit beside it in any order.
+template <typename... KArgs, typename... Args>
+inline wf_status launch_plain(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
+                              unsigned cluster, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) == cudaSuccess ? WF_OK : WF_ERR_CUDA;
+}
+
 // Dynamic shared memory that a kernel may ask for, and an SM set up for as much shared memory as there is: what runs
 // before and after a sweep then fits beside it (its prologue is over when the sweep ends) and no SM is set up anew in
 // between.  Where a merge did not fit, a call took 3 to 15 us longer.

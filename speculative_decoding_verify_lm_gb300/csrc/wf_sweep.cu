@@ -251,7 +251,6 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
     }
     const uint32_t tmem_base = pipe_begin<PAIR, 4>(g);
     if (warp != 0) pdl_wait();   // warp 0: when it has asked for its first weights
-    pdl_trigger();
 
     if (warp == 0) {
         const uint64_t pol_w = policy_evict_first(), pol_a = policy_evict_last();
@@ -341,14 +340,9 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
                     const int id = list[0];
                     next_id = id >= sp.row0 ? id : PICK_NONE;
                 } else {
-                    int hi = p.K;
-                    while (at < hi) {
-                        const int mid = (at + hi) >> 1;
-                        if (list[mid] < sp.row0)
-                            at = mid + 1;
-                        else
-                            hi = mid;
-                    }
+                    // the first place whose id is not below the tile's: the same steps for every row
+                    for (int step = 64; step > 0; step >>= 1)
+                        if (at + step <= p.K && list[at + step - 1] < sp.row0) at += step;
                     next_id = at < p.K ? list[at] : PICK_NONE;
                 }
             }
@@ -390,6 +384,7 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
                         fence_async_store();
                         __syncwarp();
                         if (lane == 0) tma_store_2d(&tmZ, to, col0, m * BM + q * 32);
+                        __syncwarp();
                         box ^= 1;
                     }
                 }
@@ -501,7 +496,7 @@ wf_status launch_kt(const SweepCall& c, int* slots_out, cudaStream_t s) {
     p.step = t.step;
     const int units = p.num_mt * p.num_n;
     if (units < slots) slots = units;
-    const int split = pair ? 2 : 1;
+    const unsigned split = pair ? 2 : 1;
     p.idesc = umma_idesc_bf16(split * BM, p.bn);
     p.idesc_s = p.nbig < p.num_n ? umma_idesc_bf16(split * BM, p.bn - p.step) : p.idesc;
     p.c = LOG2E * c.inv_t;
@@ -523,10 +518,10 @@ wf_status launch_kt(const SweepCall& c, int* slots_out, cudaStream_t s) {
     tz = ta;
     if (Z && !make_tile_map(&tz, c.z, c.rows, c.V, c.ldz, true, 32, 32)) return WF_ERR_CUDA;
     *slots_out = slots;
-    if (pair)
-        return launch_cluster(sweep_kernel<KT, ENT, Z, true>, dim3(2 * slots), dim3(SWEEP_THREADS), smem, s, 2u, ta, tb,
-                              tbs, tz, p);
-    return launch(sweep_kernel<KT, ENT, Z, false>, dim3(slots), dim3(SWEEP_THREADS), smem, s, ta, tb, tbs, tz, p);
+    const dim3 grid(pair ? 2 * slots : slots);
+    auto kernel = pair ? sweep_kernel<KT, ENT, Z, true> : sweep_kernel<KT, ENT, Z, false>;
+    return c.after_lists ? launch_cluster(kernel, grid, dim3(SWEEP_THREADS), smem, s, split, ta, tb, tbs, tz, p)
+                         : launch_plain(kernel, grid, dim3(SWEEP_THREADS), smem, s, split, ta, tb, tbs, tz, p);
 }
 
 }  // namespace

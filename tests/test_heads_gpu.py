@@ -517,3 +517,22 @@ def test_host_memory_is_refused():
         wf.wf_lmhead_logprobs(h, W, wf.LogprobsWorkspace(8, 256, 9001), k=17)
     with pytest.raises(wf.WfError):   # a workspace of fewer rows
         wf.wf_lmhead_logprobs(ref.states(3000, 256, g), W, ws)
+
+
+def test_a_long_queue_of_steps_ends():
+    """Hundreds of steps enqueued at once, no wait on the host between them: each kernel that takes whole SMs starts
+    with nothing waiting beside it."""
+    g = gen(35)
+    h, W, x, Wd, d2t, t2d = _batch(g, N=300, Vd=9000, V=12001)
+    (N, d), V, Vd, k = x.shape, W.shape[0], Wd.shape[0], 10
+    lws, dws, z = wf.LogprobsWorkspace(N, d, V, k=k), wf.DistillWorkspace(N, d, Vd, k), wf.distill_logits(N, Vd)
+    first = None
+    for _ in range(400):
+        best = wf.wf_lmhead_logprobs(h, W, lws, k=k)
+        loss, lse = wf.wf_draft_distill(x, Wd, best.top_ids, best.top_logp, dws, t2d=t2d, z=z)
+        got = (best.top_ids, loss, lse, *wf.wf_draft_distill_grad(x, Wd, best.top_ids, best.top_logp, z, lse, dws,
+                                                                  t2d=t2d))
+        first = first or [t.clone() for t in got]
+    torch.cuda.synchronize()
+    assert lws.device_error() == dws.device_error() == (0, 0)
+    assert all(torch.equal(a, b) for a, b in zip(got, first))
