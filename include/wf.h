@@ -422,8 +422,8 @@ WF_API wf_status wf_lmhead_logprobs(const wf_logprobs_args* args, void* ws, size
  * what is minimised by loss[n]; NULL = 1):
  *   G[n, v] = gloss[n] / temperature (q_v - sum over j with id_j = v of p_j)
  *   dx[n]   = sum_v G[n, v] Wd_v,   dWd_v = sum_n G[n, v] x[n]
- * either output may be NULL, not both.  G is rounded to bf16 once, the sums are
- * fp32 and rounded to bf16 at the end.  A row with gloss 0 adds nothing as long
+ * either output may be NULL, not both.  G is rounded to bf16 (up to 128 rows: to
+ * the sum of two bf16 numbers), the sums are fp32 and rounded to bf16 at the end.  A row with gloss 0 adds nothing as long
  * as its x is finite.  Results do not depend on timing.
  */
 typedef struct wf_distill_args {

@@ -64,7 +64,7 @@ wf_status launch_pages_trim(const wf_paged_cache* c, const int32_t* cache_len, v
 wf_status launch_paged_token(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s);
 wf_status launch_paged_rounds(const wf_paged_cache* c, const wf_paged_attn_args* a, void* ws, cudaStream_t s);
 
-size_t distill_grad_ldg(int Vd);
+size_t distill_grad_bytes(int N, int Vd);
 size_t distill_part_bytes(int N, int d, int Vd);
 long distill_grad_units(int N, int d, int Vd);
 wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int d, const Teacher& t, const float* z,
@@ -174,7 +174,7 @@ static DistillLayout distill_layout(int N, int d, int Vd, int k) {
     L.picked = L.p + list;
     L.stat = L.picked + list;
     L.states = L.G = L.stat + row;
-    L.part = align_up(L.G + 2 * (size_t)N * distill_grad_ldg(Vd), 256);
+    L.part = align_up(L.G + distill_grad_bytes(N, Vd), 256);
     const size_t a = L.part + distill_part_bytes(N, d, Vd), b = L.states + states_bytes(N, d, 0);
     L.total = align_up(a > b ? a : b, 256);
     return L;

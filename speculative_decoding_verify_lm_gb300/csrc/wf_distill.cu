@@ -5,14 +5,20 @@
 // Two launches: G in bf16 (one pass over z), then both products as the tiles of
 // one persistent launch on the tensor cores.
 //
-// G is rounded to bf16 once (both products need operands of one type, and Wd
-// and x are bf16); the products sum in fp32 and are rounded to bf16 once more
-// on their way out.
+// G is rounded to bf16 (both products need operands of one type, and Wd and x
+// are bf16); the products sum in fp32 and are rounded to bf16 once more on their
+// way out.  A gradient is then off by 1.4 times what its own rounding makes; the
+// few entries that the teacher lists hold nearly all of G, so with few rows it
+// can as well be 1.7 times.  Up to TWO_PART_ROWS rows, where the weights' bytes
+// bound both products, G goes in as the sum of two bf16 numbers, of which nothing
+// is seen in the result (64 rows over 32,000 ids: error 0.0025 -> 0.0017).
 #include "wf_heads.cuh"
 
 namespace wf {
 
 namespace {
+
+constexpr int TWO_PART_ROWS = BM;
 
 // ------------------------------------------------------------------ G
 // Bound by the bytes of z (fp32, read) and G (bf16, written).  A thread takes 8
@@ -31,6 +37,7 @@ struct GradParams {
     Teacher t;
     uint16_t* G;
     int64_t ldg;
+    int64_t lo;      // elements from G's first part to its second, 0 = one part
     int chunks;      // CTAs of a row
 };
 
@@ -38,6 +45,11 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+// What bf16 leaves of a number.
+__device__ __forceinline__ float bf16_rest(float v) {
+    return v - __uint_as_float(pack_bf16(v, 0.f) << 16);
 }
 
 __global__ void __launch_bounds__(GRAD_THREADS) logit_grad_kernel(const GradParams a) {
@@ -72,12 +84,21 @@ __global__ void __launch_bounds__(GRAD_THREADS) logit_grad_kernel(const GradPara
         auto q = [&](float x, int j) {
             return gs == 0.f || v + j >= Vd ? 0.f : gs * ex2_approx((x - off) * LOG2E);
         };
+        const float g[8] = {q(f[u][0].x, 0), q(f[u][0].y, 1), q(f[u][0].z, 2), q(f[u][0].w, 3),
+                            q(f[u][1].x, 4), q(f[u][1].y, 5), q(f[u][1].z, 6), q(f[u][1].w, 7)};
         uint4 o;
-        o.x = pack_bf16(q(f[u][0].x, 0), q(f[u][0].y, 1));
-        o.y = pack_bf16(q(f[u][0].z, 2), q(f[u][0].w, 3));
-        o.z = pack_bf16(q(f[u][1].x, 4), q(f[u][1].y, 5));
-        o.w = pack_bf16(q(f[u][1].z, 6), q(f[u][1].w, 7));
+        o.x = pack_bf16(g[0], g[1]);
+        o.y = pack_bf16(g[2], g[3]);
+        o.z = pack_bf16(g[4], g[5]);
+        o.w = pack_bf16(g[6], g[7]);
         *reinterpret_cast<uint4*>(G + v) = o;
+        if (a.lo) {
+            o.x = pack_bf16(bf16_rest(g[0]), bf16_rest(g[1]));
+            o.y = pack_bf16(bf16_rest(g[2]), bf16_rest(g[3]));
+            o.z = pack_bf16(bf16_rest(g[4]), bf16_rest(g[5]));
+            o.w = pack_bf16(bf16_rest(g[6]), bf16_rest(g[7]));
+            *reinterpret_cast<uint4*>(G + a.lo + v) = o;
+        }
     }
     if (gs == 0.f) return;   // the same for the whole CTA
     __syncthreads();
@@ -98,8 +119,11 @@ __global__ void __launch_bounds__(GRAD_THREADS) logit_grad_kernel(const GradPara
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int id = r.id[h];
-            if (lane + 32 * h < a.t.K && !again[h] && id >= v0 && id < v0 + GRAD_COLS && id < Vd)
-                G[id] = (uint16_t)pack_bf16(gs * (ex2_approx((z[id] - off) * LOG2E) - pt[h]), 0.f);
+            if (lane + 32 * h < a.t.K && !again[h] && id >= v0 && id < v0 + GRAD_COLS && id < Vd) {
+                const float g = gs * (ex2_approx((z[id] - off) * LOG2E) - pt[h]);
+                G[id] = (uint16_t)pack_bf16(g, 0.f);
+                if (a.lo) G[a.lo + id] = (uint16_t)pack_bf16(bf16_rest(g), 0.f);
+            }
         }
     }
 }
@@ -136,6 +160,7 @@ struct ProdParams {
     int part_rows;            // rows of one part of dx
     int flip;                 // dx is computed as its transpose, `flip` rows wide; 0: as it lies
     int w_rows;               // rows of one K block of dWd (a multiple of 16)
+    int parts;                // G's parts, rows N apart (2: only with flip)
     uint16_t* dx;
     float* part;
     Control* ctrl;
@@ -190,7 +215,7 @@ struct Units {
         u.row0 = r * TM;
         u.col0 = c * TN;
         u.k0 = 0;
-        u.kb = p.kb_w;
+            u.kb = p.kb_w * p.parts;
         v += stride;
         r += dr;
         c += dc;
@@ -241,23 +266,26 @@ __global__ void __launch_bounds__(PROD_THREADS, 1)
         Units units(p, slot, slots);
         auto next = [&](int) { return units.next(p, u) ? u.kb : 0; };
         auto tx = [&]() {
-            if (u.dx) return p.flip ? (uint32_t)(2 * BM * BK * 2 + p.flip * BK * 2) : (uint32_t)(2 * PROD_STAGE);
+            if (u.dx)
+                return p.flip ? (uint32_t)(2 * BM * BK * 2 + p.parts * p.flip * BK * 2) : (uint32_t)(2 * PROD_STAGE);
             return (uint32_t)(2 * 4 * 128 * p.w_rows);
         };
         // lanes 0 and 1 copy the halves of A, lanes 2 and 3 those of B; where an operand lies with its K contiguous,
         // it is one box, of the even lane
         auto load = [&](int kc, int s, uint32_t bar, bool, bool) {
-            const int h = lane & 1, k = u.dx ? (u.k0 + kc) * BK : kc * p.w_rows;
+            const int h = lane & 1, lo = !u.dx && kc >= p.kb_w;   // dWd: G's first part, then its second
+            int k = u.dx ? (u.k0 + kc) * BK : (kc - (lo ? p.kb_w : 0)) * p.w_rows;
             const bool flip = u.dx && p.flip, rows_a = u.dx && !p.flip;
-            if (lane >= 4 || (lane == 1 && rows_a) || (lane == 3 && flip)) return;
+            if (lane >= 4 || (lane == 1 && rows_a) || (lane == 3 && flip && p.parts == 1)) return;
             const CUtensorMap* map;
             int mn;   // the coordinate along M or N
             if (lane < 2) {
                 map = rows_a ? &tmGk : flip ? &tmW : &tmGm;
                 mn = (flip ? u.col0 : u.row0) + rank * BM + (rows_a ? 0 : 64 * h);
+                if (lo) k += p.N;
             } else {
                 map = flip ? &tmGk : u.dx ? &tmW : &tmX;
-                mn = flip ? rank * (p.flip / 2) : u.col0 + rank * (TN / 2) + 64 * h;
+                mn = flip ? rank * (p.flip / 2) + h * p.N : u.col0 + rank * (TN / 2) + 64 * h;
             }
             const bool k_inner = lane < 2 ? rows_a : flip;
             pipe_load<true>((lane < 2 ? g.a(s) : g.b(s)) + h * 8192, map, bar, k_inner ? k : mn, k_inner ? mn : k, pol);
@@ -276,7 +304,13 @@ __global__ void __launch_bounds__(PROD_THREADS, 1)
                 // 16 values of K: 32 bytes of a row, or 16 rows of 128
                 const uint32_t a_step = a_rows ? 2 : 128, b_step = flip ? 2 : 128;
                 const uint32_t idesc = flip ? umma_idesc_bf16(TM, p.flip) | A_MN : IDESC | B_MN | (u.dx ? 0 : A_MN);
-                if (u.dx || p.w_rows == BK) {
+                if (flip && p.parts == 2) {   // both parts of G against the same weights
+#pragma unroll
+                    for (int kk = 0; kk < BK / 16; ++kk) {
+                        umma_bf16_pair(d, a + a_step * kk, b + b_step * kk, idesc, (kc | kk) != 0);
+                        umma_bf16_pair(d, a + a_step * kk, b + (8192 >> 4) + b_step * kk, idesc, 1);
+                    }
+                } else if (u.dx || p.w_rows == BK) {
 #pragma unroll
                     for (int kk = 0; kk < BK / 16; ++kk)
                         umma_bf16_pair(d, a + a_step * kk, b + b_step * kk, idesc, (kc | kk) != 0);
@@ -411,7 +445,7 @@ __global__ void __launch_bounds__(256) dx_join_kernel(const float* part, int par
 constexpr double W_TILE_OUT = 4.4, X_PART_OUT = 9.0, TILE_FIXED = 1.0;
 
 struct Plan {
-    int x_m, x_n, w_m, kb_x, kb_w, split, part_rows, flip, w_rows;
+    int x_m, x_n, w_m, kb_x, kb_w, split, part_rows, flip, w_rows, parts;
 };
 double w_cost(int kb_w) { return (kb_w > W_TILE_OUT ? kb_w : W_TILE_OUT) + TILE_FIXED; }
 
@@ -428,8 +462,9 @@ Plan plan_of(int N, int d, int Vd, bool dx, bool dw) {
     p.split = 1;
     p.flip = N <= BM ? (N + 31) / 32 * 32 : 0;
     p.part_rows = p.flip ? N : p.x_m * TM;
+    p.parts = N <= TWO_PART_ROWS ? 2 : 1;
     if (dx) {
-        const double w = dw ? (double)p.w_m * p.x_n * w_cost(p.kb_w) : 0.0;
+        const double w = dw ? (double)p.w_m * p.x_n * w_cost(p.kb_w * p.parts) : 0.0;
         double best = -1;
         for (int s = 1; s <= MAX_SPLIT && s <= p.kb_x && (s == 1 || (long)s * p.x_m * p.x_n <= MAX_PARTS); ++s) {
             const double unit = (double)p.kb_x / s + (s > 1 ? X_PART_OUT : TILE_FIXED);
@@ -449,6 +484,12 @@ Plan plan_of(int N, int d, int Vd, bool dx, bool dw) {
 }  // namespace
 
 size_t distill_grad_ldg(int Vd) { return align_up((size_t)Vd, 64); }
+// Rows of G's buffer: two parts, and what the transposed product's boxes reach to; no fewer for more rows.
+static int grad_rows(int N) {
+    const int two = 2 * (((N < TWO_PART_ROWS ? N : TWO_PART_ROWS) + 31) / 32 * 32);
+    return N > two ? N : two;
+}
+size_t distill_grad_bytes(int N, int Vd) { return 2 * (size_t)grad_rows(N) * distill_grad_ldg(Vd); }
 // The most blocks or tiles that a call counts.
 long distill_grad_units(int N, int d, int Vd) {
     const long g = (long)N * cdiv(Vd, GRAD_COLS), x = (long)cdiv(N, TM) * cdiv(d, TN) * MAX_SPLIT,
@@ -474,6 +515,7 @@ wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int d, cons
     a.t = t;
     a.G = G;
     a.ldg = (int64_t)distill_grad_ldg(Vd);
+    a.lo = N <= TWO_PART_ROWS ? N * a.ldg : 0;
     a.chunks = cdiv(Vd, GRAD_COLS);
     static std::mutex mu;
     static bool attr_set[64] = {false};
@@ -509,17 +551,22 @@ wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int d, cons
     p.part_rows = pl.part_rows;
     p.flip = pl.flip;
     p.w_rows = pl.w_rows;
+    p.parts = pl.parts;
     p.dx = dx;
     p.part = part;
     if (slots > p.x_units + p.w_units) slots = p.x_units + p.w_units;
     // pairs 0 .. late - 1 have one dx unit more than the others
     p.late = p.x_units % slots;
     const double ux = (double)pl.kb_x / pl.split + (pl.split > 1 ? X_PART_OUT : TILE_FIXED);
-    p.lead = p.late ? (int)(ux / w_cost(pl.kb_w) + 0.5) : 0;
+    p.lead = p.late ? (int)(ux / w_cost(pl.kb_w * pl.parts) + 0.5) : 0;
     p.ctrl = t.ctrl;
     p.timeout_ns = wait_timeout_ns();
     CUtensorMap gk, gm, tw, tx, tdx, tdw;
-    if (!make_tile_map(&gk, G, N, Vd, a.ldg, false, BK, pl.flip ? pl.flip / 2 : BM) || !make_tile_map(&gm, G, N, Vd, a.ldg, false, 64, pl.w_rows) ||
+    const int g_rows = N * pl.parts;
+    // The transposed product may read any rows behind the last (they are columns that nobody keeps), and a box
+    // of rows that are not there takes longer (one row: dx 53 us).
+    if (!make_tile_map(&gk, G, pl.flip ? N + pl.flip : g_rows, Vd, a.ldg, false, BK, pl.flip ? pl.flip / 2 : BM) ||
+        !make_tile_map(&gm, G, g_rows, Vd, a.ldg, false, 64, pl.w_rows) ||
         !make_tile_map(&tw, Wd, Vd, d, d, false, 64, BK) || !make_tile_map(&tx, x, N, d, d, false, 64, pl.w_rows))
         return WF_ERR_CUDA;
     tdx = tdw = gk;

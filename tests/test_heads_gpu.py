@@ -382,7 +382,7 @@ def test_distill_past_32_bit_offsets():
     xs, ts, ls = x[some].contiguous(), tid[some].contiguous(), tl[some].contiguous()
     want = ref.distill(xs, Wd, ts, ls, None, 1.0)
     check_loss(loss[some], lse[some], want, 1.0, Vd)
-    gx, gW, tx, tW = ref.grads(xs, Wd, want, None, 1.0)
+    gx, gW, tx, tW = ref.grads(xs, Wd, want, None, 1.0, rows=N)
     within(dx[some], gx, tx, "dx")
     within(dW, gW, tW, "dWd")
     rest = torch.ones(N, dtype=torch.bool, device=DEV)
