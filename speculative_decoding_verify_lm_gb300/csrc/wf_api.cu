@@ -146,17 +146,14 @@ static bool bad_temperature(float t) {
     return !(t > 0.f) || !(inv > 0.f) || isinf(inv) || isinf(inv * 1.4427f);
 }
 
-// Scratch of wf_lmhead_logprobs: the sorted lists and their logits, the states.
+// Scratch of wf_lmhead_logprobs: the given tokens' logits, the states.
 struct ScoreLayout {
-    size_t ids, order, picked, states, total;
+    size_t picked, states, total;
 };
 static ScoreLayout score_layout(int P, int d, int S, int k) {
     ScoreLayout L;
-    const size_t list = align_up(4 * (size_t)P * (size_t)S, 256);
-    L.ids = sizeof(Control);
-    L.order = L.ids + (S > 1 ? list : 0);
-    L.picked = L.order + (S > 1 ? list : 0);
-    L.states = L.picked + list;
+    L.picked = sizeof(Control);
+    L.states = align_up(L.picked + 4 * (size_t)P * (size_t)S, 256);
     L.total = align_up(L.states + states_bytes(P, d, k), 256);
     return L;
 }
@@ -661,14 +658,6 @@ wf_status wf_lmhead_logprobs(const wf_logprobs_args* a, void* ws, size_t ws_byte
     uint8_t* w = static_cast<uint8_t*>(ws);
     Control* ctrl = reinterpret_cast<Control*>(ws);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    const int32_t* ids = a->tok;
-    const int32_t* order = nullptr;
-    if (a->S > 1) {
-        ids = reinterpret_cast<int32_t*>(w + L.ids);
-        order = reinterpret_cast<int32_t*>(w + L.order);
-        WF_TRY(launch_sort_tokens(a->tok, a->P, a->S, a->V, reinterpret_cast<int32_t*>(w + L.ids),
-                                  reinterpret_cast<int32_t*>(w + L.order), a->logp, ctrl, s));
-    }
     const int chunk = sweep_chunk(a->P, a->d);
     for (int r0 = 0; r0 < a->P; r0 += chunk) {
         const size_t list = (size_t)r0 * a->S;
@@ -679,13 +668,12 @@ wf_status wf_lmhead_logprobs(const wf_logprobs_args* a, void* ws, size_t ws_byte
         c.d = a->d;
         c.V = a->V;
         c.inv_t = 1.f / a->temperature;
-        c.pick = ids ? ids + list : nullptr;
+        c.pick = a->tok ? a->tok + list : nullptr;
         c.K = a->S;
         c.picked = reinterpret_cast<float*>(w + L.picked) + list;
         c.states = w + L.states;
         c.k = a->k;
         c.entropy = true;
-        c.after_lists = r0 == 0 && a->S > 1;
         c.ctrl = ctrl;
         MergeCall m{};
         WF_TRY(launch_sweep(c, &m.slots, s));
@@ -700,7 +688,6 @@ wf_status wf_lmhead_logprobs(const wf_logprobs_args* a, void* ws, size_t ws_byte
         m.top_logp = a->top_logp ? a->top_logp + (size_t)r0 * a->k : nullptr;
         m.picked = c.picked;
         m.ids = c.pick;
-        m.order = order ? order + list : nullptr;
         m.logp = a->logp && a->tok ? a->logp + list : nullptr;
         m.V = a->V;
         m.ctrl = ctrl;
@@ -728,7 +715,8 @@ wf_status wf_draft_distill(const wf_distill_args* a, void* ws, size_t ws_bytes, 
     int32_t* ids = reinterpret_cast<int32_t*>(w + L.ids);
     float* p = reinterpret_cast<float*>(w + L.p);
     float* stat = reinterpret_cast<float*>(w + L.stat);
-    WF_TRY(launch_teacher(t, ids, p, stat, s));
+    // where the logits are kept the loss is read off them; else the sweep looks out for the teacher's ids
+    if (!a->z) WF_TRY(launch_teacher(t, ids, p, stat, s));
     const int chunk = sweep_chunk(a->N, a->d);
     for (int r0 = 0; r0 < a->N; r0 += chunk) {
         const size_t list = (size_t)r0 * a->k;
@@ -739,27 +727,33 @@ wf_status wf_draft_distill(const wf_distill_args* a, void* ws, size_t ws_bytes, 
         c.d = a->d;
         c.V = a->Vd;
         c.inv_t = t.inv_t;
-        c.pick = ids + list;
-        c.K = a->k;
-        c.picked = reinterpret_cast<float*>(w + L.picked) + list;
         c.states = w + L.states;
-        c.z = a->z ? a->z + (size_t)r0 * a->ldz : nullptr;
-        c.ldz = a->ldz;
-        c.after_lists = r0 == 0;
         c.ctrl = t.ctrl;
         MergeCall m{};
+        if (a->z) {
+            c.z = a->z + (size_t)r0 * a->ldz;
+            c.ldz = a->ldz;
+            m.z = c.z;
+            m.ldz = c.ldz;
+            m.t = t;
+        } else {
+            c.pick = ids + list;
+            c.K = a->k;
+            c.picked = reinterpret_cast<float*>(w + L.picked) + list;
+            c.after_lists = r0 == 0;
+            m.picked = c.picked;
+            m.p = p + list;
+            m.stat = stat + r0;
+        }
         WF_TRY(launch_sweep(c, &m.slots, s));
         m.states = c.states;
         m.rows = c.rows;
         m.K = a->k;
         m.inv_t = c.inv_t;
         m.lse = a->lse + r0;
-        m.picked = c.picked;
-        m.ids = c.pick;
-        m.p = p + list;
-        m.stat = stat + r0;
         m.loss = a->loss + r0;
         m.ctrl = t.ctrl;
+        m.row0 = r0;
         WF_TRY(launch_states_merge(m, s));
     }
     return WF_OK;

@@ -1,6 +1,5 @@
-// The small kernels around a sweep of a head's weights: the lists that it looks
-// for (given tokens, or a teacher's alternatives as probabilities over draft
-// ids), and the merge of a row's states into its log-sum-exp, entropy, best
+// The small kernels around a sweep of a head's weights: a teacher's alternatives
+// as probabilities over draft ids, for the sweep to look for, and the merge of a row's states into its log-sum-exp, entropy, best
 // alternatives, log-probabilities and loss.
 #include "wf_heads.cuh"
 
@@ -10,49 +9,6 @@ namespace {
 
 constexpr int LIST_WARPS = 4;
 
-// The rank of each lane's two entries (places lane and lane + 32 of n <= 64)
-// among all, by id and then by place.
-__device__ __forceinline__ void ranks(const int (&id)[2], int n, int lane, int (&rank)[2]) {
-    rank[0] = rank[1] = 0;
-    for (int j = 0; j < n; ++j) {
-        const int o = __shfl_sync(0xffffffffu, j < 32 ? id[0] : id[1], j & 31);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) rank[h] += o < id[h] || (o == id[h] && j < lane + 32 * h);
-    }
-}
-
-// One warp a row.
-__global__ void __launch_bounds__(LIST_WARPS * 32) sort_tokens_kernel(const int32_t* tok, int rows, int S, int V,
-                                                                      int32_t* ids, int32_t* order, float* logp,
-                                                                      Control* ctrl) {
-    pdl_trigger();   // the sweep may start and ask for its first weights
-    const int row = blockIdx.x * LIST_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    if (row >= rows) return;
-    const size_t base = (size_t)row * S;
-    int id[2], rank[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int j = lane + 32 * h;
-        id[h] = PICK_NONE;
-        if (j < S) {
-            const int t = tok[base + j];
-            if (t >= 0 && t < V) {
-                id[h] = t;
-            } else {
-                logp[base + j] = t == -1 ? 0.f : __int_as_float(0x7fc00000);
-                if (t != -1) record_error(ctrl, WF_ERR_BAD_DATA, (uint32_t)row);
-            }
-        }
-    }
-    ranks(id, S, lane, rank);
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-        if (lane + 32 * h < S) {
-            ids[base + rank[h]] = id[h];
-            order[base + rank[h]] = lane + 32 * h;
-        }
-}
-
 // One warp a row.
 __global__ void __launch_bounds__(LIST_WARPS * 32) teacher_kernel(const Teacher t, int32_t* ids, float* p,
                                                                   float* stat) {
@@ -60,14 +16,12 @@ __global__ void __launch_bounds__(LIST_WARPS * 32) teacher_kernel(const Teacher 
     const int row = blockIdx.x * LIST_WARPS + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     if (row >= t.N) return;
     const TeacherRow r = teacher_row(t, row, lane);
-    int rank[2];
-    ranks(r.id, t.K, lane, rank);
     const size_t base = (size_t)row * t.K;
 #pragma unroll
     for (int h = 0; h < 2; ++h)
         if (lane + 32 * h < t.K) {
-            ids[base + rank[h]] = r.id[h];
-            p[base + rank[h]] = r.p[h];
+            ids[base + lane + 32 * h] = r.id[h];
+            p[base + lane + 32 * h] = r.p[h];
         }
     if (lane == 0) stat[row] = r.plogp;
 }
@@ -169,10 +123,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const Me
         for (int j = threadIdx.x; j < c.K; j += blockDim.x) {
             const size_t at = (size_t)row * c.K + j;
             const int id = c.ids[at];
-            if (c.order) {
-                if (id != PICK_NONE)
-                    c.logp[(size_t)row * c.K + c.order[at]] = logq(c.picked[at]);
-            } else if (id >= 0 && id < c.V) {
+            if (id >= 0 && id < c.V) {
                 c.logp[at] = logq(c.picked[at]);
             } else {
                 c.logp[at] = id == -1 ? 0.f : __int_as_float(0x7fc00000);
@@ -182,16 +133,24 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const Me
     }
     if (c.loss && warp == 0) {
         // sum p (log p - log q)
-        float part = 0.f;
-        for (int j = lane; j < c.K; j += 32) {
-            const size_t at = (size_t)row * c.K + j;
-            if (c.ids[at] != PICK_NONE) {
+        float part = 0.f, stat;
+        if (c.z) {
+            const TeacherRow r = teacher_row(c.t, c.row0 + row, lane);
+            stat = r.plogp;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                if (r.p[h] != 0.f)
+                    part = fmaf(r.p[h], fmaf(fmaf(c.z[(size_t)row * c.ldz + r.id[h]], LOG2E, -ref), LN2, -logs), part);
+        } else {
+            stat = c.stat[row];
+            for (int j = lane; j < c.K; j += 32) {
+                const size_t at = (size_t)row * c.K + j;
                 const float p = c.p[at];
                 if (p != 0.f) part = fmaf(p, logq(c.picked[at]), part);
             }
         }
         part = warp_sum(part);
-        if (lane == 0) c.loss[row] = c.stat[row] - part;
+        if (lane == 0) c.loss[row] = stat - part;
     }
 }
 
@@ -201,17 +160,9 @@ static wf_status configure() {
     static std::mutex mu;
     static bool attr_set[64] = {false};
     return configure_once(mu, attr_set, [] {
-        return set_smem(sort_tokens_kernel, 0) && set_smem(teacher_kernel, 0) && set_smem(states_merge_kernel<0>, 0) &&
+        return set_smem(teacher_kernel, 0) && set_smem(states_merge_kernel<0>, 0) &&
                set_smem(states_merge_kernel<10>, 0) && set_smem(states_merge_kernel<16>, 0);
     });
-}
-
-wf_status launch_sort_tokens(const int32_t* tok, int rows, int S, int V, int32_t* ids, int32_t* order, float* logp,
-                             Control* ctrl, cudaStream_t s) {
-    const wf_status st = configure();
-    if (st != WF_OK) return st;
-    return launch_plain(sort_tokens_kernel, dim3(cdiv(rows, LIST_WARPS)), dim3(LIST_WARPS * 32), 0, s, 1u, tok, rows, S, V, ids,
-                  order, logp, ctrl);
 }
 
 wf_status launch_teacher(const Teacher& t, int32_t* ids, float* p, float* stat, cudaStream_t s) {

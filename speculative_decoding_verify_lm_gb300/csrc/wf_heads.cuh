@@ -7,8 +7,8 @@
 
 namespace wf {
 
-static_assert(WF_MAX_LISTED <= 64, "a warp's lanes sort two listed ids each");
-constexpr int PICK_NONE = 0x7fffffff;    // a list's place without an id: sorts last, matches nothing
+static_assert(WF_MAX_LISTED <= 64, "a warp's lanes take two listed ids each");
+constexpr int PICK_NONE = 0x7fffffff;    // a list's place without an id: matches nothing
 
 // Rows swept by one launch: what they read stays in L2 while the weights
 // stream past, and the states of a launch have a bounded size.
@@ -36,7 +36,7 @@ struct SweepCall {
     const uint16_t *act, *W;
     int rows, d, V;          // rows: of this launch, at most sweep_chunk()
     float inv_t;
-    const int32_t* pick;     // [rows][K] ids, ascending (K > 1), or null
+    const int32_t* pick;     // [rows][K] ids in any order, or null
     int K;
     float* picked;           // [rows][K] their logits, where the id lies in [0, V)
     uint8_t* states;
@@ -50,11 +50,6 @@ struct SweepCall {
 // Enqueues the sweep; *slots: states left for each row (row-major, in use all of them).
 wf_status launch_sweep(const SweepCall& c, int* slots, cudaStream_t s);
 
-// Lists of given tokens sorted by id, with the place that each came from; places
-// without a token (-1) get a log-probability of 0 and ids outside [0, V) NaN.
-wf_status launch_sort_tokens(const int32_t* tok, int rows, int S, int V, int32_t* ids, int32_t* order, float* logp,
-                             Control* ctrl, cudaStream_t s);
-
 // A teacher's alternatives.
 struct Teacher {
     const int32_t* tid;      // [N][K]
@@ -64,8 +59,8 @@ struct Teacher {
     float inv_t;
     Control* ctrl;
 };
-// ... as sorted lists: ids [N][K] ascending draft ids, PICK_NONE last, p their probabilities, stat [N] sum p log p (NaN: an id
-// out of range).
+// ... as lists for a sweep: ids [N][K] draft ids (PICK_NONE: not kept), p their probabilities, stat [N] sum p log p (NaN: an
+// id out of range).
 wf_status launch_teacher(const Teacher& t, int32_t* ids, float* p, float* stat, cudaStream_t s);
 
 struct MergeCall {
@@ -78,11 +73,13 @@ struct MergeCall {
     float* top_logp;         // [rows][k] or null
     const float* picked;     // [rows][K]
     const int32_t* ids;      // [rows][K] as swept
-    const int32_t* order;    // [rows][K] or null: K = 1, ids are the tokens themselves
     float* logp;             // [rows][K] or null
-    const float* p;          // [rows][K]: the loss is asked for
+    float* loss;             // [rows] or null; then either the lists as launch_teacher made them
+    const float* p;          // [rows][K]
     const float* stat;       // [rows]
-    float* loss;             // [rows]
+    const float* z;          // or [rows][ldz], the logits that the sweep kept, and the teacher
+    int64_t ldz;
+    Teacher t;
     int V;
     int row0;                // first row's number in the call, for errors
     Control* ctrl;

@@ -34,7 +34,7 @@ struct SweepParams {
     uint32_t idesc, idesc_s;
     int stages, stage_bytes, a_bytes;
     float c, inv_t;
-    const int32_t* pick;
+    const int32_t* pick;                  // [rows][K] ids in any order
     int K;
     float* picked;
     uint8_t* states;
@@ -332,20 +332,14 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
                     if (!live) st.tv[KT - 1] = INFINITY;   // rows that are none insert nothing
                 }
             }
-            // the row's listed ids from this tile's first on
-            const int32_t* list = p.K && live ? p.pick + (size_t)row * p.K : nullptr;
-            int at = 0, next_id = PICK_NONE;
-            if (list) {
-                if (p.K == 1) {
-                    const int id = list[0];
-                    next_id = id >= sp.row0 ? id : PICK_NONE;
-                } else {
-                    // the first place whose id is not below the tile's: the same steps for every row
-                    for (int step = 64; step > 0; step >>= 1)
-                        if (at + step <= p.K && list[at + step - 1] < sp.row0) at += step;
-                    next_id = at < p.K ? list[at] : PICK_NONE;
+            // the row's listed ids in this tile, the lowest first
+            const size_t list = (size_t)row * p.K;
+            int next_id = PICK_NONE;
+            if (live)
+                for (int j = 0; j < p.K; ++j) {
+                    const int id = p.pick[list + j];
+                    next_id = id >= sp.row0 && id < next_id ? id : next_id;
                 }
-            }
             if (!pipe_acc_wait(g, i)) break;
             if (warp_live) {
                 const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (i & 1) * BN;
@@ -365,9 +359,14 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
                         fold<KT, ENT, false>(r, lim, col0, p.c, bound, st);
                     while (__any_sync(0xffffffffu, next_id < col0 + lim)) {
                         if (next_id < col0 + lim) {
-                            p.picked[(size_t)row * p.K + at] = __uint_as_float(column(r, next_id - col0));
-                            ++at;
-                            next_id = at < p.K ? list[at] : PICK_NONE;
+                            const float v = __uint_as_float(column(r, next_id - col0));
+                            int after = PICK_NONE;
+                            for (int j = 0; j < p.K; ++j) {   // the list is short, in any order, an id may be there twice
+                                const int id = p.pick[list + j];
+                                if (id == next_id) p.picked[list + j] = v;
+                                after = id > next_id && id < after ? id : after;
+                            }
+                            next_id = after;
                         }
                     }
                     if constexpr (Z) {
