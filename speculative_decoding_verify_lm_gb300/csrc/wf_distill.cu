@@ -147,6 +147,7 @@ constexpr int OUT_BOX = 4096;               // 32 rows x 128 bytes on their way 
 constexpr int PROD_WARPS = 8, PROD_THREADS = pipe_threads(PROD_WARPS);
 constexpr int PROD_STAGES = 6;
 constexpr int PROD_STAGE = 2 * BM * BK * 2;
+constexpr int SPREAD_ROWS = 64;             // rows up to which every pair gets a part of dx
 constexpr int PLAN_PAIRS = 76;              // pairs that the split is chosen for (152 SMs)
 constexpr int MAX_SPLIT = 16;
 constexpr int MAX_PARTS = 8 * PLAN_PAIRS;   // parts of all of dx's tiles: what a workspace holds
@@ -463,7 +464,14 @@ Plan plan_of(int N, int d, int Vd, bool dx, bool dw) {
     p.flip = N <= BM ? (N + 31) / 32 * 32 : 0;
     p.part_rows = p.flip ? N : p.x_m * TM;
     p.parts = N <= TWO_PART_ROWS ? 2 : 1;
-    if (dx) {
+    if (dx && p.x_m * p.x_n <= PLAN_PAIRS && N <= SPREAD_ROWS) {
+        // few rows: both products are bound by the weights' bytes, and dx's half of them comes soonest with a part
+        // for every pair (16 rows over 32,000 ids: 7 parts of each of 10 tiles 68.8 us, 4 of each 74.0; 30 rows over
+        // 47,330: 142.9 and 154.8; with 128 rows 89.1 and 84.1, so there the costs below decide)
+        p.split = PLAN_PAIRS / p.x_n;
+        if (p.split > MAX_SPLIT) p.split = MAX_SPLIT;
+        if (p.split > p.kb_x) p.split = p.kb_x;
+    } else if (dx) {
         const double w = dw ? (double)p.w_m * p.x_n * w_cost(p.kb_w * p.parts) : 0.0;
         double best = -1;
         for (int s = 1; s <= MAX_SPLIT && s <= p.kb_x && (s == 1 || (long)s * p.x_m * p.x_n <= MAX_PARTS); ++s) {
