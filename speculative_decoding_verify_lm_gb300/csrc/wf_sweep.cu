@@ -336,6 +336,7 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
             const size_t list = (size_t)row * p.K;
             int next_id = PICK_NONE;
             if (live)
+#pragma unroll 4
                 for (int j = 0; j < p.K; ++j) {
                     const int id = p.pick[list + j];
                     next_id = id >= sp.row0 && id < next_id ? id : next_id;
@@ -357,14 +358,18 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
                         fold<KT, ENT, true>(r, 32, col0, p.c, bound, st);
                     else
                         fold<KT, ENT, false>(r, lim, col0, p.c, bound, st);
-                    while (__any_sync(0xffffffffu, next_id < col0 + lim)) {
+                    if (__any_sync(0xffffffffu, next_id < col0 + lim)) {
+                        // the list is in any order and an id may be there twice: one look through it takes all of
+                        // the chunk's, however close they lie (one look for each took 80 us for 64 neighbours)
+                        int after = PICK_NONE;
                         if (next_id < col0 + lim) {
-                            const float v = __uint_as_float(column(r, next_id - col0));
-                            int after = PICK_NONE;
-                            for (int j = 0; j < p.K; ++j) {   // the list is short, in any order, an id may be there twice
+#pragma unroll 4
+                            for (int j = 0; j < p.K; ++j) {
                                 const int id = p.pick[list + j];
-                                if (id == next_id) p.picked[list + j] = v;
-                                after = id > next_id && id < after ? id : after;
+                                if (id >= col0 && id < col0 + lim)
+                                    p.picked[list + j] = __uint_as_float(column(r, id - col0));
+                                else if (id >= col0 + lim && id < after)
+                                    after = id;
                             }
                             next_id = after;
                         }
