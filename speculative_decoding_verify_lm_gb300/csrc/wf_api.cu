@@ -148,12 +148,13 @@ static bool bad_temperature(float t) {
 
 // Scratch of wf_lmhead_logprobs: the given tokens' logits, the states.
 struct ScoreLayout {
-    size_t picked, states, total;
+    size_t picked, reached, states, total;
 };
 static ScoreLayout score_layout(int P, int d, int S, int k) {
     ScoreLayout L;
     L.picked = sizeof(Control);
-    L.states = align_up(L.picked + 4 * (size_t)P * (size_t)S, 256);
+    L.reached = align_up(L.picked + 4 * (size_t)P * (size_t)S, 256);
+    L.states = align_up(L.reached + 4 * (size_t)sweep_chunk(P, d), 256);
     L.total = align_up(L.states + states_bytes(P, d, k), 256);
     return L;
 }
@@ -673,6 +674,7 @@ wf_status wf_lmhead_logprobs(const wf_logprobs_args* a, void* ws, size_t ws_byte
         c.picked = reinterpret_cast<float*>(w + L.picked) + list;
         c.states = w + L.states;
         c.k = a->k;
+        c.reached = reinterpret_cast<uint32_t*>(w + L.reached);
         c.entropy = true;
         c.ctrl = ctrl;
         MergeCall m{};

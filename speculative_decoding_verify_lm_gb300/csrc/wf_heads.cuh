@@ -41,6 +41,7 @@ struct SweepCall {
     float* picked;           // [rows][K] their logits, where the id lies in [0, V)
     uint8_t* states;
     int k;                   // best logits kept
+    uint32_t* reached;       // scratch [rows] (k > 0)
     bool entropy;
     float* z;                // [rows][ldz] logits times inv_t, or null
     int64_t ldz;

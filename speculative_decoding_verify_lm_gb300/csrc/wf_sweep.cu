@@ -12,6 +12,10 @@
 // that saw it, not one per tile (4,096 rows over 151,936 ids with 16 best: 76
 // states of 144 bytes a row instead of 594), and what a tile adds to the k best
 // is a few insertions.
+// With several row tiles the pairs that see the same rows tell each other the
+// KT-th best that they have reached, so that late columns are candidates for few
+// lists (1,215 rows of 512 over 123,478 ids with 10 best: 270 us a call alone, 236
+// so): the sets differ with timing, the k best among them do not.
 // One activation tile (up to 128 rows): bound by the weights' bytes; every CTA
 // its own tiles, ring slots as large as the rows.  More rows: pairs of CTAs on
 // tiles of 256 rows x 256 ids, bound by the tensor cores.
@@ -39,6 +43,7 @@ struct SweepParams {
     float* picked;
     uint8_t* states;
     int slots;                            // states per row
+    uint32_t* reached;                    // [rows] what the KT-th best of some pair's list has reached (f32_order), or null
     Control* ctrl;
     uint64_t timeout_ns;
 };
@@ -313,6 +318,10 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
             const int row = m * BM + rit;
             const bool warp_live = m * BM + q * 32 < p.rows, live = row < p.rows;
             bool fresh = false;   // the list is empty
+            uint32_t shared = 0;  // the highest KT-th best that any pair has put down for this row
+            if constexpr (KT > 0) {
+                if (p.reached && live) shared = __ldcg(p.reached + row);
+            }
             if (mt != cur) {
                 if (cur >= 0) {
                     const int was = (PAIR ? 2 * cur + rank : cur) * BM + rit;
@@ -347,7 +356,9 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
                 const int cols = min(sp.rows, p.V - sp.row0);
                 float bound = -INFINITY;
                 if constexpr (KT > 0) {
-                    if (fresh) bound = first_bound<KT>(tbase, cols);
+                    if (shared) bound = f32_unorder(shared - 1);   // as good as it is still a candidate
+                    if (fresh && __any_sync(0xffffffffu, live && !shared))
+                        bound = fmaxf(bound, first_bound<KT>(tbase, cols));
                 }
                 for (int c0 = 0; c0 < cols; c0 += 32) {
                     uint32_t r[32];
@@ -394,6 +405,13 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
                 }
             }
             pipe_acc_release(g, i, tempty_first);
+            if constexpr (KT > 0) {
+                // what a full list has reached holds for the row's other pairs too
+                if (p.reached && live && st.ti[KT - 1] >= 0) {
+                    const uint32_t mine = f32_order(st.tv[KT - 1]);
+                    if (mine > shared) atomicMax(p.reached + row, mine);
+                }
+            }
         }
         if (cur >= 0) {
             const int was = (PAIR ? 2 * cur + rank : cur) * BM + rit;
@@ -510,6 +528,10 @@ wf_status launch_kt(const SweepCall& c, int* slots_out, cudaStream_t s) {
     p.picked = c.picked;
     p.states = c.states;
     p.slots = slots;
+    if (p.num_mt > 1 && KT > 0) {
+        p.reached = c.reached;
+        if (cudaMemsetAsync(c.reached, 0, 4 * (size_t)c.rows, s) != cudaSuccess) return WF_ERR_CUDA;
+    }
     p.ctrl = c.ctrl;
     p.timeout_ns = wait_timeout_ns();
     CUtensorMap ta, tb, tbs, tz;
