@@ -216,7 +216,7 @@ struct Units {
         u.row0 = r * TM;
         u.col0 = c * TN;
         u.k0 = 0;
-            u.kb = p.kb_w * p.parts;
+        u.kb = p.kb_w * p.parts;
         v += stride;
         r += dr;
         c += dc;

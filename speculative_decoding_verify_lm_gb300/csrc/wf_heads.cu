@@ -55,7 +55,8 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const Me
         for (int j = 0; j < KT; ++j) {
             const float4 f = e[j / 2];
             const int id = __float_as_int(j & 1 ? f.w : f.y);
-            loc[j] = id < 0 ? 0ull : pack_key(j & 1 ? f.z : f.x, (uint32_t)id);
+            // + 0: zeros of both signs are one value, and rank by id
+            loc[j] = id < 0 ? 0ull : pack_key((j & 1 ? f.z : f.x) + 0.f, (uint32_t)id);
         }
     }
 #pragma unroll

@@ -21,6 +21,8 @@
 // tiles of 256 rows x 256 ids, bound by the tensor cores.
 #include <cudaTypedefs.h>
 
+#include <cfloat>
+
 #include "wf_heads.cuh"
 
 namespace wf {
@@ -146,6 +148,12 @@ struct State {
     }
 };
 
+// A number below v that nothing lies between (for a zero, of either sign, the
+// first that arithmetic without denormals tells from it).
+__device__ __forceinline__ float just_below(float v) {
+    return v == 0.f ? -FLT_MIN : f32_unorder(f32_order(v) - 1);
+}
+
 // A bound that the KT-th best of a tile's columns reaches: the KT-th largest of
 // 32 maxima, each over the columns 32 apart, which are KT different columns.  An
 // empty list would take nearly every column of its first chunks; held to this
@@ -175,8 +183,7 @@ __device__ __forceinline__ float first_bound(uint32_t tbase, int cols) {
             best[i] = hi;
         }
     }
-    const uint32_t order = f32_order(best[KT - 1]);
-    return best[KT - 1] == -INFINITY ? -INFINITY : f32_unorder(order - 1);
+    return best[KT - 1] == -INFINITY ? -INFINITY : just_below(best[KT - 1]);
 }
 
 // Fold 32 columns (the first lim of them) into a row's state; only columns above
@@ -356,7 +363,7 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
                 const int cols = min(sp.rows, p.V - sp.row0);
                 float bound = -INFINITY;
                 if constexpr (KT > 0) {
-                    if (shared) bound = f32_unorder(shared - 1);   // as good as it is still a candidate
+                    if (shared) bound = just_below(f32_unorder(shared));   // as good as it is still a candidate
                     if (fresh && __any_sync(0xffffffffu, live && !shared))
                         bound = fmaxf(bound, first_bound<KT>(tbase, cols));
                 }

@@ -1,0 +1,43 @@
+"""Best alternatives of rows whose k-th best logit is exactly zero: a padded batch's rows of zeros, and rows for which
+few ids have a logit above zero."""
+import pytest
+import torch
+
+import heads_ref as ref
+from speculative_decoding_verify_lm_gb300 import wf
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+
+
+def check(h, W, k):
+    P, V = h.shape[0], W.shape[0]
+    tok = torch.arange(P, device=DEV).int() % V
+    r = wf.wf_lmhead_logprobs(h, W, wf.LogprobsWorkspace(P, h.shape[1], V, S=1, k=k), tok=tok, k=k, with_entropy=True)
+    want, tol = ref.logprobs(h, W, 1.0, tok, k)
+    assert torch.equal(r.top_ids, want["top_ids"])
+    assert bool(((r.top_logp.double() - want["top_logp"]).abs() <= tol["logp"][:, None]).all())
+    assert bool(((r.logp.double() - want["logp"]).abs() <= tol["logp"]).all())
+
+
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+@pytest.mark.parametrize("P,V,k", [(5, 1, 1), (5, 300, 4), (60, 41000, 10), (300, 700, 16), (700, 50021, 10),
+                                   (2100, 9001, 3)])
+def test_rows_of_zeros(P, V, k, sign):
+    """Every logit is zero, of either sign: the k lowest ids."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(P + V)
+    W, h = ref.head(V, 64, g, std=0.1), ref.states(P, 64, g)
+    h[P // 3:] = sign * 0.0
+    check(h, W, k)
+
+
+@pytest.mark.parametrize("P,V,k", [(40, 41000, 10), (300, 50021, 16), (1030, 9001, 4)])
+def test_few_ids_above_zero(P, V, k):
+    """A few ids' logits are not zero, and about half of those lie below it."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(P)
+    W, h = torch.zeros((V, 64), dtype=torch.bfloat16, device=DEV), ref.states(P, 64, g)
+    some = torch.arange(V // 2, V, 5000, device=DEV)
+    W[some] = ref.head(some.numel(), 64, g, std=0.1)
+    check(h, W, k)
