@@ -416,15 +416,16 @@ WF_API wf_status wf_lmhead_logprobs(const wf_logprobs_args* args, void* ws, size
  * z has to lie in fp32's range, also times log2(e).
  *
  * wf_draft_distill writes loss and lse and, if z is given, the z[n, v] in fp32
- * (columns from Vd, rounded up to 4, on are left as they are): 4 N Vd bytes that spare the
- * gradients a second sweep of the head.  wf_draft_distill_grad takes that z and
- * lse, the same x, Wd, teacher and temperature, and gloss[n] (the derivative of
- * what is minimised by loss[n]; NULL = 1):
+ * (columns from Vd, rounded up to 4, on are left as they are): 4 N Vd bytes that
+ * spare the gradients a second sweep of the head.  wf_draft_distill_grad takes
+ * that z and lse, the same x, Wd, teacher and temperature, and gloss[n] (the
+ * derivative of what is minimised by loss[n]; NULL = 1):
  *   G[n, v] = gloss[n] / temperature (q_v - sum over j with id_j = v of p_j)
  *   dx[n]   = sum_v G[n, v] Wd_v,   dWd_v = sum_n G[n, v] x[n]
- * either output may be NULL, not both.  G is rounded to bf16 (up to 128 rows: to
- * the sum of two bf16 numbers), the sums are fp32 and rounded to bf16 at the end.  A row with gloss 0 adds nothing as long
- * as its x is finite.  Results do not depend on timing.
+ * either output may be NULL, not both; they overlap no input.  G is rounded to
+ * bf16 (up to 128 rows: to the sum of two bf16 numbers), the sums are fp32 and
+ * rounded to bf16 at the end.  A row with gloss 0 adds nothing as long as its x
+ * is finite.  Results do not depend on timing.
  */
 typedef struct wf_distill_args {
     const uint16_t* x;         /* [N, d] bf16 bits, the drafter's hidden states */
@@ -444,7 +445,8 @@ typedef struct wf_distill_args {
     uint16_t* dx;              /* [N, d] bf16 bits or NULL (wf_draft_distill_grad) */
     uint16_t* dWd;             /* [Vd, d] bf16 bits or NULL (wf_draft_distill_grad) */
 } wf_distill_args;
-/* Workspace (bytes) of both calls, 2 N Vd and what the parts of split sums take; 0 if the shapes are out of range. */
+/* Workspace (bytes) of both calls: 2 N Vd, and what the parts of split sums and
+ * the sweep's states take; 0 if the shapes are out of range. */
 WF_API size_t wf_distill_workspace_bytes(int N, int d, int Vd, int k);
 WF_API wf_status wf_draft_distill(const wf_distill_args* args, void* ws, size_t ws_bytes, wf_stream_t stream);
 WF_API wf_status wf_draft_distill_grad(const wf_distill_args* args, void* ws, size_t ws_bytes, wf_stream_t stream);

@@ -1,6 +1,9 @@
 // The small kernels around a sweep of a head's weights: a teacher's alternatives
-// as probabilities over draft ids, for the sweep to look for, and the merge of a row's states into its log-sum-exp, entropy, best
-// alternatives, log-probabilities and loss.
+// as probabilities over draft ids, for the sweep to look for, and the merge of a
+// row's states into its log-sum-exp, entropy, best alternatives,
+// log-probabilities and loss.  Both are bound by latency, one row's chain of
+// loads and votes: a merge takes 6 to 7.5 us at 17 to 1,024 rows (a full head's
+// sweep of few rows 118).
 #include "wf_heads.cuh"
 
 namespace wf {
@@ -27,7 +30,8 @@ __global__ void __launch_bounds__(LIST_WARPS * 32) teacher_kernel(const Teacher 
 }
 
 // One CTA a row, one thread a state; a fixed order of merging makes the result
-// the same in every run.
+// the same in every run.  The states come out of L2 (17 rows: 152 of 16 to 144
+// bytes a row).
 constexpr int MERGE_WARPS = STATE_SLOTS / 32;   // as many of them as the row has states
 static_assert(MERGE_WARPS * 32 >= STATE_SLOTS && MERGE_WARPS * 32 >= REC_PAIRS, "a thread for every state");
 

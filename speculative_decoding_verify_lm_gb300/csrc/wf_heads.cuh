@@ -60,8 +60,8 @@ struct Teacher {
     float inv_t;
     Control* ctrl;
 };
-// ... as lists for a sweep: ids [N][K] draft ids (PICK_NONE: not kept), p their probabilities, stat [N] sum p log p (NaN: an
-// id out of range).
+// ... as lists for a sweep: ids [N][K] draft ids (PICK_NONE: not kept), p their
+// probabilities, stat [N] sum p log p (NaN: an id out of range).
 wf_status launch_teacher(const Teacher& t, int32_t* ids, float* p, float* stat, cudaStream_t s);
 
 struct MergeCall {
