@@ -350,15 +350,23 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
                     if (!live) st.tv[KT - 1] = INFINITY;   // rows that are none insert nothing
                 }
             }
-            // the row's listed ids in this tile, the lowest first
+            // the row's listed ids in this tile: their places, and the lowest of them
             const size_t list = (size_t)row * p.K;
             int next_id = PICK_NONE;
-            if (live)
-#pragma unroll 4
-                for (int j = 0; j < p.K; ++j) {
-                    const int id = p.pick[list + j];
-                    next_id = id >= sp.row0 && id < next_id ? id : next_id;
-                }
+            uint32_t here[2] = {0u, 0u};
+            if (live) {
+                const int end = sp.row0 + min(sp.rows, p.V - sp.row0);
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll 16
+                    for (int j = 32 * h; j < min(p.K, 32 * h + 32); ++j) {
+                        const int id = p.pick[list + j];
+                        if (id >= sp.row0 && id < end) {
+                            here[h] |= 1u << (j & 31);
+                            next_id = min(next_id, id);
+                        }
+                    }
+            }
             if (!pipe_acc_wait(g, i)) break;
             if (warp_live) {
                 const uint32_t tbase = tmem_base + ((uint32_t)(q * 32) << 16) + (i & 1) * BN;
@@ -379,19 +387,21 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
                     else
                         fold<KT, ENT, false>(r, lim, col0, p.c, bound, st);
                     if (__any_sync(0xffffffffu, next_id < col0 + lim)) {
-                        // the list is in any order and an id may be there twice: one look through it takes all of
-                        // the chunk's, however close they lie (one look for each took 80 us for 64 neighbours)
-                        int after = PICK_NONE;
+                        // the list is in any order and an id may be there twice: one look through the tile's places
+                        // takes all of the chunk's, however close they lie
                         if (next_id < col0 + lim) {
-#pragma unroll 4
-                            for (int j = 0; j < p.K; ++j) {
-                                const int id = p.pick[list + j];
-                                if (id >= col0 && id < col0 + lim)
-                                    p.picked[list + j] = __uint_as_float(column(r, id - col0));
-                                else if (id >= col0 + lim && id < after)
-                                    after = id;
-                            }
-                            next_id = after;
+                            next_id = PICK_NONE;
+#pragma unroll
+                            for (int h = 0; h < 2; ++h)
+                                for (uint32_t left = here[h]; left; left &= left - 1) {
+                                    const int j = __ffs((int)left) - 1, id = p.pick[list + 32 * h + j];
+                                    if (id < col0 + lim) {
+                                        p.picked[list + 32 * h + j] = __uint_as_float(column(r, id - col0));
+                                        here[h] &= ~(1u << j);
+                                    } else {
+                                        next_id = min(next_id, id);
+                                    }
+                                }
                         }
                     }
                     if constexpr (Z) {
