@@ -493,14 +493,14 @@ def _own_ws(ws, kind):
     return ws.buf.data_ptr(), ws.nbytes
 
 
-def _shaped(t, name, shape, dtypes, like):
-    """Address of a dense tensor of this shape on like's device (like is a CUDA tensor)."""
+def _shaped(t, name, shape, dtypes, dev):
+    """Address of a dense tensor of this shape on CUDA device number dev."""
     if t is None:
         raise ValueError(f"{name} is required")
     if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, not {list(t.shape)}")
-    if t.device != like.device:
-        raise ValueError(f"{name} must be on {like.device}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on cuda:{dev}")
     if t.dtype not in dtypes or not t.is_contiguous():
         return _check(t, name, dtypes)
     return t.data_ptr() or _check(t, name, dtypes)
@@ -509,7 +509,8 @@ def _shaped(t, name, shape, dtypes, like):
 def _head(x, W, names):
     if x.dim() != 2 or W.dim() != 2 or x.shape[1] != W.shape[1]:
         raise ValueError(f"{names[0]} must be [rows, d] and {names[1]} [ids, d]")
-    return _check(x, names[0], _BF16), _shaped(W, names[1], W.shape, _BF16, x)
+    xp, dev = _check(x, names[0], _BF16), x.get_device()
+    return xp, _shaped(W, names[1], W.shape, _BF16, dev), dev
 
 
 def wf_lmhead_logprobs(hidden, W, ws: LogprobsWorkspace, tok=None, k: int = 0, temperature: float = 1.0,
@@ -518,7 +519,7 @@ def wf_lmhead_logprobs(hidden, W, ws: LogprobsWorkspace, tok=None, k: int = 0, t
     """Log-probabilities of given tokens tok [P] or [P, S] (-1: none) under softmax(hidden W^T / temperature), the
     log-sum-exp, the entropy (with_entropy, or H given) and the k best alternatives of each row.  Outputs not given
     are allocated."""
-    hp, Wp = _head(hidden, W, ("hidden", "W"))
+    hp, Wp, dev = _head(hidden, W, ("hidden", "W"))
     (P, d), V = hidden.shape, W.shape[0]
     S = tp = 0
     if tok is not None:
@@ -526,40 +527,41 @@ def wf_lmhead_logprobs(hidden, W, ws: LogprobsWorkspace, tok=None, k: int = 0, t
         S = 1 if len(shape) == 1 else shape[1] if len(shape) == 2 else 0
         if not 1 <= S <= WF_MAX_LISTED or shape[0] != P:
             raise ValueError(f"tok must be [P] or [P, S], S up to {WF_MAX_LISTED}")
-        tp = _shaped(tok, "tok", shape, _I32, hidden)
-    # (pieces of one allocation would take longer: a view costs most of what an allocation does)
-    new, dev = torch.empty, hidden.device
+        tp = _shaped(tok, "tok", shape, _I32, dev)
+    # (pieces of one allocation would take longer: a view costs most of what an allocation does, and one of a given
+    # shape twice what one like another tensor does)
+    new, like, fp32, on = torch.empty, torch.empty_like, torch.float32, hidden.device
     lp = Hp = idp = tlp = 0
     if tok is None:
         logp = None
     elif logp is None:
-        logp = new(shape, dtype=torch.float32, device=dev)
+        logp = like(tok, dtype=fp32)
         lp = logp.data_ptr()
     else:
-        lp = _shaped(logp, "logp", shape, _F32, hidden)
+        lp = _shaped(logp, "logp", shape, _F32, dev)
     if lse is None:
-        lse = new(P, dtype=torch.float32, device=dev)
+        lse = new(P, dtype=fp32, device=on)
         lsep = lse.data_ptr()
     else:
-        lsep = _shaped(lse, "lse", (P,), _F32, hidden)
+        lsep = _shaped(lse, "lse", (P,), _F32, dev)
     if H is not None:
-        Hp = _shaped(H, "H", (P,), _F32, hidden)
+        Hp = _shaped(H, "H", (P,), _F32, dev)
     elif with_entropy:
-        H = torch.empty_like(lse)
+        H = like(lse)
         Hp = H.data_ptr()
     if k <= 0:
         top_ids = top_logp = None
     else:
         if top_ids is None:
-            top_ids = new((P, k), dtype=torch.int32, device=dev)
+            top_ids = new(P, k, dtype=torch.int32, device=on)
             idp = top_ids.data_ptr()
         else:
-            idp = _shaped(top_ids, "top_ids", (P, k), _I32, hidden)
+            idp = _shaped(top_ids, "top_ids", (P, k), _I32, dev)
         if top_logp is None:
-            top_logp = new((P, k), dtype=torch.float32, device=dev)
+            top_logp = like(top_ids, dtype=fp32)
             tlp = top_logp.data_ptr()
         else:
-            tlp = _shaped(top_logp, "top_logp", (P, k), _F32, hidden)
+            tlp = _shaped(top_logp, "top_logp", (P, k), _F32, dev)
     args = _LOGPROBS.pack(hp, Wp, P, d, V, temperature, tp, S, k, lp, lsep, Hp, idp, tlp)
     st = (_lib or lib()).wf_lmhead_logprobs(args, *_own_ws(ws, LogprobsWorkspace), _stream(stream))
     if st:
@@ -586,7 +588,7 @@ def distill_logits(N: int, Vd: int, device=None):
 
 
 def _distill(fn, x, Wd, tid, tlogit, t2d, temperature, z, lse, loss, gloss, dx, dWd, ws, stream):
-    xp, wp = _head(x, Wd, ("x", "Wd"))
+    xp, wp, dev = _head(x, Wd, ("x", "Wd"))
     (N, d), Vd = x.shape, Wd.shape[0]
     shape, V, ldz = tid.shape, 0, 0
     if len(shape) != 2 or shape[0] != N or not 1 <= shape[1] <= WF_MAX_LISTED:
@@ -599,14 +601,14 @@ def _distill(fn, x, Wd, tid, tlogit, t2d, temperature, z, lse, loss, gloss, dx, 
         V = t2d.numel()
         if t2d.dim() != 1 or V == 0:
             raise ValueError("t2d must be [V]")
-    args = _DISTILL.pack(xp, wp, N, d, Vd, _shaped(tid, "tid", shape, _I32, x),
-                         _shaped(tlogit, "tlogit", shape, _F32, x), shape[1],
-                         _shaped(t2d, "t2d", t2d.shape, _I32, x) if V else 0, V, temperature,
-                         _shaped(z, "z", z.shape, _F32, x) if ldz else 0, ldz, _shaped(lse, "lse", (N,), _F32, x),
-                         _shaped(loss, "loss", (N,), _F32, x) if loss is not None else 0,
-                         _shaped(gloss, "gloss", (N,), _F32, x) if gloss is not None else 0,
-                         _shaped(dx, "dx", x.shape, _BF16, x) if dx is not None else 0,
-                         _shaped(dWd, "dWd", Wd.shape, _BF16, x) if dWd is not None else 0)
+    args = _DISTILL.pack(xp, wp, N, d, Vd, _shaped(tid, "tid", shape, _I32, dev),
+                         _shaped(tlogit, "tlogit", shape, _F32, dev), shape[1],
+                         _shaped(t2d, "t2d", t2d.shape, _I32, dev) if V else 0, V, temperature,
+                         _shaped(z, "z", z.shape, _F32, dev) if ldz else 0, ldz, _shaped(lse, "lse", (N,), _F32, dev),
+                         _shaped(loss, "loss", (N,), _F32, dev) if loss is not None else 0,
+                         _shaped(gloss, "gloss", (N,), _F32, dev) if gloss is not None else 0,
+                         _shaped(dx, "dx", x.shape, _BF16, dev) if dx is not None else 0,
+                         _shaped(dWd, "dWd", Wd.shape, _BF16, dev) if dWd is not None else 0)
     st = getattr(_lib or lib(), fn)(args, *_own_ws(ws, DistillWorkspace), _stream(stream))
     if st:
         _raise(st, fn)
@@ -640,11 +642,11 @@ def wf_draft_distill_grad(x, Wd, tid, tlogit, z, lse, ws: DistillWorkspace, glos
     if not need_dx:
         dx = None
     elif dx is None:
-        dx = torch.empty(x.shape, dtype=torch.bfloat16, device=x.device)
+        dx = torch.empty_like(x)
     if not need_dWd:
         dWd = None
     elif dWd is None:
-        dWd = torch.empty(Wd.shape, dtype=torch.bfloat16, device=x.device)
+        dWd = torch.empty_like(Wd)
     _distill("wf_draft_distill_grad", x, Wd, tid, tlogit, t2d, temperature, z, lse, None, gloss, dx, dWd, ws, stream)
     return dx, dWd
 
