@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(PROD_THREADS, 1)
                          const ProdParams p) {
     extern __shared__ uint8_t smem_raw[];
     const Pipe g = pipe_at(smem_raw, PROD_STAGES, PROD_STAGE, BM * BK * 2, PROD_WARPS * OUT_BOX, p.ctrl, p.timeout_ns);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
     const int rank = (int)(cluster_ctarank() & 1u);
     const bool first = rank == 0;
     const int slot = (int)(blockIdx.x >> 1), slots = (int)(gridDim.x >> 1);
@@ -298,7 +298,7 @@ __global__ void __launch_bounds__(PROD_THREADS, 1)
         };
         pipe_copy<true, false>(g, first, next, tx, load);
     } else if (warp == 1) {
-        if (lane == 0 && first) {
+        if (first) {
             Unit u{};
             Units units(p, slot, slots);
             auto next = [&](int) { return units.next(p, u) ? u.kb : 0; };

@@ -4,8 +4,8 @@
 //
 //   warp 0     fills the ring: each stage holds an A tile and a B tile of one K
 //              block (64 values of K); each box is copied by a lane of its own
-//   warp 1     allocates TMEM and issues the MMAs of a stage; the stage is free
-//              again when they have completed
+//   warp 1     allocates TMEM and issues the MMAs of a stage (one elected
+//              thread); the stage is free again when they have completed
 //   warps 2-   read a finished accumulator (thread = one row of the tile, or of
 //              one half of its columns) while the next tile's MMAs run into the
 //              other one
@@ -72,6 +72,9 @@ inline int pipe_smem(int stages, int stage_bytes, int extra) {
     return stages * stage_bytes + PIPE_BARRIER_BYTES + extra + 1024;
 }
 
+// The thread's warp, the same in all of its lanes also to the compiler.
+__device__ __forceinline__ int warp_number() { return __shfl_sync(0xffffffffu, (int)(threadIdx.x >> 5), 0); }
+
 // Barriers and TMEM; returns the TMEM base address.  All threads.
 template <bool PAIR, int EPI_WARPS>
 __device__ __forceinline__ uint32_t pipe_begin(const Pipe& g) {
@@ -102,7 +105,7 @@ __device__ __forceinline__ uint32_t pipe_begin(const Pipe& g) {
     __syncthreads();
     if constexpr (PAIR) cluster_sync();   // both CTAs' barriers and TMEM exist before either uses the other's
     tc_fence_after();
-    return *g.tmem_slot;
+    return __shfl_sync(0xffffffffu, *g.tmem_slot, 0);
 }
 
 template <bool PAIR>
@@ -191,9 +194,20 @@ __device__ __forceinline__ void pipe_copy(const Pipe& g, bool first, Next next, 
     }
 }
 
-// The issuing thread (PAIR: of the first CTA).  next(i) as above; issue(s,
-// d_tmem, kc) issues stage s's MMAs into the accumulator at d_tmem (kc = 0
-// overwrites it).
+// One thread of the warp, the same one every time (all lanes).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
+// The issuing warp (all lanes; PAIR: of the first CTA).  next(i) as above;
+// issue(s, d_tmem, kc) issues stage s's MMAs into the accumulator at d_tmem (kc =
+// 0 overwrites it), by one elected thread.  The warp walks the loop together and
+// only the issue itself is one thread's: the compiler then knows the operands to be
+// the warp's, where a lane in a branch of its own took 70 cycles for each MMA (645
+// a stage whose products take 512: 1,248 rows of 2,560 over 151,936 ids 558 us a
+// call, 500 so).
 template <bool PAIR, typename Next, typename Issue>
 __device__ __forceinline__ void pipe_mma(const Pipe& g, uint32_t tmem_base, Next next, Issue issue) {
     const uint32_t empty_peer = PAIR ? cluster_addr(&g.empty[0], 1) : 0;
@@ -202,12 +216,15 @@ __device__ __forceinline__ void pipe_mma(const Pipe& g, uint32_t tmem_base, Next
     int s = 0;
     uint32_t ph = 0;
     bool ok = true, issued = false;
+    auto wait = [&](uint64_t* bar, uint32_t parity) {
+        return __all_sync(0xffffffffu, mbar_wait(bar, parity, g.timeout_ns, g.abort_flag)) != 0;
+    };
     for (uint32_t i = 0; ok; ++i) {
         const int num_k = next((int)i);
         if (num_k == 0) break;
         const uint32_t acc = i & 1, acc_ph = (i >> 1) & 1;
         // PAIR: released by both CTAs' epilogues (the second's arrivals are remote)
-        if (!mbar_wait(&g.tempty[acc], acc_ph ^ 1, g.timeout_ns, g.abort_flag)) {
+        if (!wait(&g.tempty[acc], acc_ph ^ 1)) {
             g.fail(PIPE_WHERE_ACC);
             ok = false;
             break;
@@ -218,22 +235,25 @@ __device__ __forceinline__ void pipe_mma(const Pipe& g, uint32_t tmem_base, Next
                 s = 0;
                 ph ^= 1;
             }
-            if (!mbar_wait(&g.full[s], ph, g.timeout_ns, g.abort_flag)) {
+            if (!wait(&g.full[s], ph)) {
                 g.fail(PIPE_WHERE_STAGE + s);
                 ok = false;
                 break;
             }
             tc_fence_after();
-            issue(s, tmem_base + acc * BN, kc);
-            if constexpr (PAIR) {
-                umma_commit_pair(smem_u32(&g.empty[s]));
-                umma_commit_pair(empty_peer + (uint32_t)(s * sizeof(uint64_t)));
-            } else {
-                umma_commit(&g.empty[s]);
+            if (elect_one()) {
+                issue(s, tmem_base + acc * BN, kc);
+                if constexpr (PAIR) {
+                    umma_commit_pair(smem_u32(&g.empty[s]));
+                    umma_commit_pair(empty_peer + (uint32_t)(s * sizeof(uint64_t)));
+                } else {
+                    umma_commit(&g.empty[s]);
+                }
             }
+            __syncwarp();
             issued = true;
         }
-        if (ok) {
+        if (ok && elect_one()) {
             if constexpr (PAIR) {
                 umma_commit_pair(smem_u32(&g.tfull[acc]));
                 umma_commit_pair(tfull_peer + acc * (uint32_t)sizeof(uint64_t));
@@ -245,10 +265,13 @@ __device__ __forceinline__ void pipe_mma(const Pipe& g, uint32_t tmem_base, Next
     if (issued && (!ok || PAIR)) {
         // every MMA issued above (PAIR: into both CTAs' TMEM) has completed before TMEM is freed
         uint64_t* drain = g.drain;
-        if constexpr (PAIR)
-            umma_commit_pair(smem_u32(drain));
-        else
-            umma_commit(drain);
+        if (elect_one()) {
+            if constexpr (PAIR)
+                umma_commit_pair(smem_u32(drain));
+            else
+                umma_commit(drain);
+        }
+        __syncwarp();
         mbar_wait(drain, 0, g.timeout_ns, nullptr);
     }
 }

@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t seen[4][SWEEP_MAX_ROWS / BM / 32];   // row tiles that a warp has a state of
     const Pipe g = pipe_at(smem_raw, p.stages, p.stage_bytes, p.a_bytes, Z ? STAGING : 0, p.ctrl, p.timeout_ns);
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_number(), lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)(cluster_ctarank() & 1u) : 0;
     const bool first = rank == 0;
     const int slot = PAIR ? (int)(blockIdx.x >> 1) : (int)blockIdx.x;
@@ -287,7 +287,7 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
         };
         pipe_copy<PAIR, true>(g, first, next, tx, load);
     } else if (warp == 1) {
-        if (lane == 0 && first) {
+        if (first) {
             uint32_t idesc = 0;
             Walk w(p, slot, nslots);
             auto next = [&](int) {
