@@ -276,25 +276,29 @@ __global__ void __launch_bounds__(PROD_THREADS, 1)
                 return p.flip ? (uint32_t)(2 * BM * BK * 2 + p.parts * p.flip * BK * 2) : (uint32_t)(2 * PROD_STAGE);
             return (uint32_t)(2 * 4 * 128 * p.w_rows);
         };
-        // lanes 0 and 1 copy the halves of A, lanes 2 and 3 those of B; where an operand lies with its K contiguous,
-        // it is one box, of the even lane
+        // two boxes of A and two of B; where an operand lies with its K contiguous, it is one box
         auto load = [&](int kc, int s, uint32_t bar, bool, bool) {
-            const int h = lane & 1, lo = !u.dx && kc >= p.kb_w;   // dWd: G's first part, then its second
-            int k = u.dx ? (u.k0 + kc) * BK : (kc - (lo ? p.kb_w : 0)) * p.w_rows;
-            const bool flip = u.dx && p.flip, rows_a = u.dx && !p.flip;
-            if (lane >= 4 || (lane == 1 && rows_a) || (lane == 3 && flip && p.parts == 1)) return;
-            const CUtensorMap* map;
-            int mn;   // the coordinate along M or N
-            if (lane < 2) {
-                map = rows_a ? &tmGk : flip ? &tmW : &tmGm;
-                mn = (flip ? u.col0 : u.row0) + rank * BM + (rows_a ? 0 : 64 * h);
-                if (lo) k += p.N;
+            uint8_t *a = g.a(s), *b = g.b(s);
+            const int col = u.col0 + rank * (TN / 2);
+            if (!u.dx) {
+                const bool lo = kc >= p.kb_w;   // G's first part, then its second
+                const int k = (kc - (lo ? p.kb_w : 0)) * p.w_rows, row = u.row0 + rank * BM;
+                pipe_load<true>(a, &tmGm, bar, row, k + (lo ? p.N : 0), pol);
+                pipe_load<true>(a + 8192, &tmGm, bar, row + 64, k + (lo ? p.N : 0), pol);
+                pipe_load<true>(b, &tmX, bar, col, k, pol);
+                pipe_load<true>(b + 8192, &tmX, bar, col + 64, k, pol);
+            } else if (p.flip) {
+                const int k = (u.k0 + kc) * BK, row = rank * (p.flip / 2);
+                pipe_load<true>(a, &tmW, bar, u.col0 + rank * BM, k, pol);
+                pipe_load<true>(a + 8192, &tmW, bar, u.col0 + rank * BM + 64, k, pol);
+                pipe_load<true>(b, &tmGk, bar, k, row, pol);
+                if (p.parts == 2) pipe_load<true>(b + 8192, &tmGk, bar, k, row + p.N, pol);
             } else {
-                map = flip ? &tmGk : u.dx ? &tmW : &tmX;
-                mn = flip ? rank * (p.flip / 2) + h * p.N : u.col0 + rank * (TN / 2) + 64 * h;
+                const int k = (u.k0 + kc) * BK;
+                pipe_load<true>(a, &tmGk, bar, k, u.row0 + rank * BM, pol);
+                pipe_load<true>(b, &tmW, bar, col, k, pol);
+                pipe_load<true>(b + 8192, &tmW, bar, col + 64, k, pol);
             }
-            const bool k_inner = lane < 2 ? rows_a : flip;
-            pipe_load<true>((lane < 2 ? g.a(s) : g.b(s)) + h * 8192, map, bar, k_inner ? k : mn, k_inner ? mn : k, pol);
         };
         pipe_copy<true, false>(g, first, next, tx, load);
     } else if (warp == 1) {

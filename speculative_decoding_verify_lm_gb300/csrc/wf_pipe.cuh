@@ -3,7 +3,7 @@
 // MMAs into two TMEM accumulators, and epilogue warps that read them.
 //
 //   warp 0     fills the ring: each stage holds an A tile and a B tile of one K
-//              block (64 values of K); each box is copied by a lane of its own
+//              block (64 values of K), copied by one elected thread
 //   warp 1     allocates TMEM and issues the MMAs of a stage (one elected
 //              thread); the stage is free again when they have completed
 //   warps 2-   read a finished accumulator (thread = one row of the tile, or of
@@ -123,22 +123,31 @@ __device__ __forceinline__ void pipe_end(const Pipe& g, uint32_t tmem_base) {
     }
 }
 
+// One thread of the warp, the same one every time (all lanes).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t one;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
+    return one != 0;
+}
+
 // The copying warp (all lanes).  next(i) sets up the CTA's i-th tile and returns
 // its K blocks (0: no further tile); tx() is what a stage of it receives in bytes
 // (PAIR: both CTAs together); load(kc, s, bar, a, b) issues the copies of operand
 // A (if a) and B (if b) into stage s, counted on the barrier at shared address
-// `bar` (PAIR: the first CTA's), each box by a lane of its own: one thread issuing
-// four boxes of 64 rows takes 900 cycles a stage, their products 512.
+// `bar` (PAIR: the first CTA's), by one elected thread, the warp walking the loop
+// together as in pipe_mma.
 // EARLY: B is a weight matrix, whose first stages are asked for while the kernel
 // before (of the same call, which has itself waited for what came before it) is
 // still running; everything else waits for it.
 template <bool PAIR, bool EARLY, typename Next, typename Tx, typename Load>
 __device__ __forceinline__ void pipe_copy(const Pipe& g, bool first, Next next, Tx tx, Load load) {
-    const int lane = threadIdx.x & 31;
     const uint32_t full0 = PAIR ? cluster_addr(&g.full[0], 0) : smem_u32(&g.full[0]);
     auto bar = [&](int s) { return full0 + (uint32_t)(s * sizeof(uint64_t)); };
-    auto expect = [&](int s, uint32_t bytes) {
-        if (lane == 0 && (!PAIR || first)) mbar_arrive_expect_tx(&g.full[s], bytes);
+    auto fill = [&](int kc, int s, uint32_t bytes, bool fresh, bool a, bool b) {
+        if (elect_one()) {
+            if (fresh && (!PAIR || first)) mbar_arrive_expect_tx(&g.full[s], bytes);
+            load(kc, s, bar(s), a, b);
+        }
         __syncwarp();
     };
     int num_k = next(0);
@@ -147,8 +156,7 @@ __device__ __forceinline__ void pipe_copy(const Pipe& g, bool first, Next next, 
     if constexpr (EARLY) {
         early = num_k < g.stages ? num_k : g.stages;
         for (int s = 0; s < early; ++s) {
-            expect(s, bytes);
-            load(s, s, bar(s), false, true);
+            fill(s, s, bytes, true, false, true);
         }
     }
     pdl_wait();
@@ -169,8 +177,7 @@ __device__ __forceinline__ void pipe_copy(const Pipe& g, bool first, Next next, 
                 break;
             }
             const bool fresh = !EARLY || it >= (uint32_t)early;
-            if (fresh) expect(s, bytes);
-            load(kc, s, bar(s), true, fresh);
+            fill(kc, s, bytes, fresh, true, fresh);
         }
         num_k = next(++i);
         bytes = tx();
@@ -192,13 +199,6 @@ __device__ __forceinline__ void pipe_copy(const Pipe& g, bool first, Next next, 
             }
         }
     }
-}
-
-// One thread of the warp, the same one every time (all lanes).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t one;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(one));
-    return one != 0;
 }
 
 // The issuing warp (all lanes; PAIR: of the first CTA).  next(i) as above;

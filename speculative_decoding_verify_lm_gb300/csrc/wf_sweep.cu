@@ -280,8 +280,8 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
         };
         auto tx = [&]() { return (uint32_t)((PAIR ? 2 : 1) * p.a_bytes + sp.rows * BK * 2); };
         auto load = [&](int kc, int s, uint32_t bar, bool a, bool b) {
-            if (lane == 0 && a) pipe_load<PAIR>(g.a(s), &tmA, bar, kc * BK, m * BM, pol_a);
-            if (lane == 1 && b)
+            if (a) pipe_load<PAIR>(g.a(s), &tmA, bar, kc * BK, m * BM, pol_a);
+            if (b)
                 pipe_load<PAIR>(g.b(s), sp.big ? &tmB : &tmBs, bar, kc * BK,
                                 sp.row0 + (PAIR ? rank * (sp.rows / 2) : 0), pol_w);
         };
