@@ -154,7 +154,7 @@ static ScoreLayout score_layout(int P, int d, int S, int k) {
     ScoreLayout L;
     L.picked = sizeof(Control);
     L.reached = align_up(L.picked + 4 * (size_t)P * (size_t)S, 256);
-    L.states = align_up(L.reached + 4 * (size_t)sweep_chunk(P, d), 256);
+    L.states = align_up(L.reached + 4 * (size_t)sweep_chunk(P, d) * REACHED, 256);
     L.total = align_up(L.states + states_bytes(P, d, k), 256);
     return L;
 }

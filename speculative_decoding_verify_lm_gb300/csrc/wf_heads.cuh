@@ -24,6 +24,7 @@ inline int sweep_chunk(int rows, int d) {
 // state_merge, then the k best as (logit, id) words.
 __host__ __device__ constexpr size_t state_bytes(int kt) { return 16 + 8 * (size_t)kt; }
 inline int state_width(int k) { return k == 0 ? 0 : k <= 10 ? 10 : 16; }
+constexpr int REACHED = 16;              // words for the maxima of a row that the pairs of a sweep share
 constexpr int STATE_SLOTS = 160;         // CTAs of a sweep of one activation tile
 // (pairs of a sweep of several: REC_PAIRS)
 inline size_t states_bytes(int rows, int d, int k) {
@@ -41,7 +42,7 @@ struct SweepCall {
     float* picked;           // [rows][K] their logits, where the id lies in [0, V)
     uint8_t* states;
     int k;                   // best logits kept
-    uint32_t* reached;       // scratch [rows] (k > 0)
+    uint32_t* reached;       // scratch [rows][REACHED], 16-byte aligned (k > 0)
     bool entropy;
     float* z;                // [rows][ldz] logits times inv_t, or null
     int64_t ldz;

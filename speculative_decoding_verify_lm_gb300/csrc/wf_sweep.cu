@@ -12,10 +12,11 @@
 // that saw it, not one per tile (4,096 rows over 151,936 ids with 16 best: 76
 // states of 144 bytes a row instead of 594), and what a tile adds to the k best
 // is a few insertions.
-// With several row tiles the pairs that see the same rows tell each other the
-// KT-th best that they have reached, so that late columns are candidates for few
-// lists (1,215 rows of 512 over 123,478 ids with 10 best: 270 us a call alone, 236
-// so): the sets differ with timing, the k best among them do not.
+// With several row tiles the pairs that see the same rows tell each other their
+// tiles' maxima, which bound the row's KT-th best from below, so that late columns
+// are candidates for few lists (1,215 rows of 512 over 123,478 ids with 10 best: 270
+// us a call without, 199 so): what is a candidate differs with timing, the k best
+// among them do not.
 // One activation tile (up to 128 rows): bound by the weights' bytes; every CTA
 // its own tiles, ring slots as large as the rows (17 rows of 2,560 over 151,936
 // ids: 118 us, 6.6 TB/s).  More rows: pairs of CTAs on tiles of 256 rows x 256
@@ -47,7 +48,7 @@ struct SweepParams {
     float* picked;
     uint8_t* states;
     int slots;                            // states per row
-    uint32_t* reached;                    // [rows] the highest KT-th best of any pair (f32_order, 0 = none yet), or null
+    uint32_t* reached;                    // [rows][REACHED] maxima of classes of tiles (f32_order, 0 = none yet), or null
     Control* ctrl;
     uint64_t timeout_ns;
 };
@@ -188,10 +189,55 @@ __device__ __forceinline__ float first_bound(uint32_t tbase, int cols) {
     return best[KT - 1] == -INFINITY ? -INFINITY : just_below(best[KT - 1]);
 }
 
+// The weight tiles n of a row fall into 16 classes n mod 16, whose maxima all pairs
+// put down as they see them.  The KT-th largest of these is reached by KT different
+// columns, and lies not far below the row's KT-th best so far: 10 of 16 have about
+// 16 columns above it.  (The least of 10 classes needs no sorting and has about 30:
+// 208 us where this takes 199, 1,215 rows of 512 over 123,478 ids; 16 of 32 classes
+// for 16 best, in two sorted halves, cost more than they spared: 3,000 rows of 1,000
+// over 60,000 ids 408 us, the least of 16 classes 380.)
+// Descending order of 16 numbers (bitonic).
+__device__ __forceinline__ void sort16(uint32_t (&v)[16]) {
+#pragma unroll
+    for (int s = 1; s <= 4; ++s)
+#pragma unroll
+        for (int t = s - 1; t >= 0; --t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const int o = i ^ (1 << t);
+                if (o > i) {
+                    const uint32_t a = v[i], b = v[o];
+                    const bool down = (i >> s & 1) == 0;
+                    v[i] = down ? max(a, b) : min(a, b);
+                    v[o] = down ? min(a, b) : max(a, b);
+                }
+            }
+}
+template <int KT>
+__device__ __forceinline__ uint32_t reached_by(const uint32_t* at) {
+    uint32_t v[REACHED];
+#pragma unroll
+    for (int j = 0; j < REACHED; j += 4) {
+        const uint4 q = __ldcg(reinterpret_cast<const uint4*>(at + j));
+        v[j] = q.x;
+        v[j + 1] = q.y;
+        v[j + 2] = q.z;
+        v[j + 3] = q.w;
+    }
+    if constexpr (KT < REACHED) {
+        sort16(v);
+        return v[KT - 1];
+    }
+    uint32_t least = v[0];
+#pragma unroll
+    for (int j = 1; j < REACHED; ++j) least = min(least, v[j]);
+    return least;
+}
+
 // Fold 32 columns (the first lim of them) into a row's state; only columns above
-// `bound` are candidates for its list.
+// `bound` are candidates for its list.  Returns their maximum.
 template <int KT, bool ENT, bool FULL>
-__device__ __forceinline__ void fold(const uint32_t (&r)[32], int lim, int col0, float c, float bound,
+__device__ __forceinline__ float fold(const uint32_t (&r)[32], int lim, int col0, float c, float bound,
                                      State<KT>& st) {
     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -241,6 +287,7 @@ __device__ __forceinline__ void fold(const uint32_t (&r)[32], int lim, int col0,
             }
         }
     }
+    return mx;
 }
 
 template <int KT, bool ENT, bool Z, bool PAIR>
@@ -327,9 +374,9 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
             const int row = m * BM + rit;
             const bool warp_live = m * BM + q * 32 < p.rows, live = row < p.rows;
             bool fresh = false;   // the list is empty
-            uint32_t shared = 0;  // the highest KT-th best that any pair has put down for this row
+            uint32_t shared = 0;  // what the row's KT-th best has reached in what all pairs put down
             if constexpr (KT > 0) {
-                if (p.reached && live) shared = __ldcg(p.reached + row);
+                if (p.reached && live) shared = reached_by<KT>(p.reached + (size_t)row * REACHED);
             }
             if (mt != cur) {
                 if (cur >= 0) {
@@ -379,15 +426,14 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
                     if (fresh && __any_sync(0xffffffffu, live && !shared))
                         bound = fmaxf(bound, first_bound<KT>(tbase, cols));
                 }
+                float top = -INFINITY;   // of the tile's columns
                 for (int c0 = 0; c0 < cols; c0 += 32) {
                     uint32_t r[32];
                     tmem_ld_32x32b_x32(tbase + c0, r);
                     tmem_ld_wait();
                     const int col0 = sp.row0 + c0, lim = min(32, cols - c0);
-                    if (lim == 32)
-                        fold<KT, ENT, true>(r, 32, col0, p.c, bound, st);
-                    else
-                        fold<KT, ENT, false>(r, lim, col0, p.c, bound, st);
+                    top = fmaxf(top, lim == 32 ? fold<KT, ENT, true>(r, 32, col0, p.c, bound, st)
+                                               : fold<KT, ENT, false>(r, lim, col0, p.c, bound, st));
                     if (__any_sync(0xffffffffu, next_id < col0 + lim)) {
                         // an id may be there twice; one look through the tile's places takes all of the chunk's
                         if (next_id < col0 + lim) {
@@ -423,15 +469,13 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
                         box ^= 1;
                     }
                 }
-            }
-            pipe_acc_release(g, i, tempty_first);
-            if constexpr (KT > 0) {
-                // what a full list has reached holds for the row's other pairs too
-                if (p.reached && live && st.ti[KT - 1] >= 0) {
-                    const uint32_t mine = f32_order(st.tv[KT - 1]);
-                    if (mine > shared) atomicMax(p.reached + row, mine);
+                if constexpr (KT > 0) {
+                    // a class's maximum below what is reached has no say in it
+                    if (p.reached && live && top > -INFINITY && f32_order(top) > shared)
+                        atomicMax(p.reached + (size_t)row * REACHED + w.n % REACHED, f32_order(top));
                 }
             }
+            pipe_acc_release(g, i, tempty_first);
         }
         if (cur >= 0) {
             const int was = (PAIR ? 2 * cur + rank : cur) * BM + rit;
@@ -548,9 +592,11 @@ wf_status launch_kt(const SweepCall& c, int* slots_out, cudaStream_t s) {
     p.picked = c.picked;
     p.states = c.states;
     p.slots = slots;
-    if (p.num_mt > 1 && KT > 0) {
+    // worth its memory traffic (and a launch that clears it) from about four tiles a pair on: with 6 of them 800 rows
+    // of 2,048 over 30,000 ids take 84 us and 85 without, with 2 of them 300 rows of 256 over 20,000 40 and 38
+    if (KT > 0 && p.num_mt > 1 && units >= 4 * slots) {
         p.reached = c.reached;
-        if (cudaMemsetAsync(c.reached, 0, 4 * (size_t)c.rows, s) != cudaSuccess) return WF_ERR_CUDA;
+        if (cudaMemsetAsync(c.reached, 0, 4 * (size_t)c.rows * REACHED, s) != cudaSuccess) return WF_ERR_CUDA;
     }
     p.ctrl = c.ctrl;
     p.timeout_ns = wait_timeout_ns();

@@ -1,5 +1,5 @@
-"""Best alternatives of rows whose k-th best logit is exactly zero: a padded batch's rows of zeros, and rows for which
-few ids have a logit above zero."""
+"""Best alternatives of rows whose k-th best logit is exactly zero (a padded batch's rows of zeros, rows for which few
+ids have a logit above zero), and of rows that many pairs of CTAs see tile after tile, whose best bound each other."""
 import pytest
 import torch
 
@@ -41,3 +41,30 @@ def test_few_ids_above_zero(P, V, k):
     some = torch.arange(V // 2, V, 5000, device=DEV)
     W[some] = ref.head(some.numel(), 64, g, std=0.1)
     check(h, W, k)
+
+
+@pytest.mark.parametrize("P,V,k", [(700, 50021, 10), (1500, 30011, 16), (400, 60001, 1)])
+def test_many_tiles_of_the_same_rows(P, V, k):
+    """Eager, captured and replayed on new inputs, with logits that rise with the id, fall with it or lie anyhow."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(V)
+    W, h = ref.head(V, 64, g, std=0.05), ref.states(P, 64, g)
+    W[:, 0] = (torch.arange(V, device=DEV) // 512 * 2.0 ** -5).to(torch.bfloat16)   # 2 to 8 bits, exact
+    h[:, 0] = torch.tensor([0.0, 2.0, -2.0], device=DEV).repeat(P)[:P].to(torch.bfloat16)
+    ws = wf.LogprobsWorkspace(P, 64, V, k=k)
+    buf = h.clone()
+    wf.wf_lmhead_logprobs(buf, W, ws, k=k)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = wf.wf_lmhead_logprobs(buf, W, ws, k=k, with_entropy=True)
+    for shift in (0, 1, 2):
+        new = h.roll(shift, 0).contiguous()
+        eager = wf.wf_lmhead_logprobs(new, W, ws, k=k, with_entropy=True)
+        buf.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        want, tol = ref.logprobs(new, W, 1.0, None, k)
+        for r in (eager, out):
+            assert torch.equal(r.top_ids, want["top_ids"])
+            assert bool(((r.top_logp.double() - want["top_logp"]).abs() <= tol["logp"][:, None]).all())
+        assert torch.equal(eager.lse, out.lse) and torch.equal(eager.H, out.H)
