@@ -40,6 +40,7 @@ struct GradParams {
     int64_t ldg;
     int64_t lo;      // elements from G's first part to its second, 0 = one part
     int chunks;      // CTAs of a row
+    int turns;       // times GRAD_COLS ids that a CTA takes
 };
 
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
@@ -56,49 +57,54 @@ __device__ __forceinline__ float bf16_rest(float v) {
 __global__ void __launch_bounds__(GRAD_THREADS) logit_grad_kernel(const GradParams a) {
     __shared__ float row_gs;
     pdl_trigger();   // the products may start
-    const int n = blockIdx.x / a.chunks, v0 = (blockIdx.x % a.chunks) * GRAD_COLS;
-    const int Vd = a.t.Vd, lane = threadIdx.x & 31;
+    const int n = blockIdx.x / a.chunks, v0 = (blockIdx.x % a.chunks) * a.turns * GRAD_COLS;
+    const int Vd = a.t.Vd, v1 = min(Vd, v0 + a.turns * GRAD_COLS), lane = threadIdx.x & 31;
     const float off = a.lse[n];
     const float* z = a.z + (size_t)n * a.ldz;
     uint16_t* G = a.G + (size_t)n * a.ldg;
-    float4 f[GRAD_UNROLL][2];
-#pragma unroll
-    for (int u = 0; u < GRAD_UNROLL; ++u) {
-        const int v = v0 + (u * GRAD_THREADS + (int)threadIdx.x) * 8;
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-            f[u][h] = v + 4 * h < Vd ? __ldcs(reinterpret_cast<const float4*>(z + v) + h)
-                                     : make_float4(0.f, 0.f, 0.f, 0.f);
-    }
     TeacherRow r;
-    if (threadIdx.x < 32) {
-        r = teacher_row(a.t, n, lane);
-        if (lane == 0) row_gs = r.some ? (a.gloss ? a.gloss[n] : 1.f) * a.t.inv_t : 0.f;
-    }
-    __syncthreads();
-    const float gs = row_gs;
+    float gs = 0.f;
+    for (int base = v0; base < v1; base += GRAD_COLS) {
+        float4 f[GRAD_UNROLL][2];
 #pragma unroll
-    for (int u = 0; u < GRAD_UNROLL; ++u) {
-        const int v = v0 + (u * GRAD_THREADS + (int)threadIdx.x) * 8;
-        if (v >= Vd) continue;
-        // ids from Vd on get 0: tensor copies look at a row's end in steps of 16 bytes
-        auto q = [&](float x, int j) {
-            return gs == 0.f || v + j >= Vd ? 0.f : gs * ex2_approx((x - off) * LOG2E);
-        };
-        const float g[8] = {q(f[u][0].x, 0), q(f[u][0].y, 1), q(f[u][0].z, 2), q(f[u][0].w, 3),
-                            q(f[u][1].x, 4), q(f[u][1].y, 5), q(f[u][1].z, 6), q(f[u][1].w, 7)};
-        uint4 o;
-        o.x = pack_bf16(g[0], g[1]);
-        o.y = pack_bf16(g[2], g[3]);
-        o.z = pack_bf16(g[4], g[5]);
-        o.w = pack_bf16(g[6], g[7]);
-        *reinterpret_cast<uint4*>(G + v) = o;
-        if (a.lo) {
-            o.x = pack_bf16(bf16_rest(g[0]), bf16_rest(g[1]));
-            o.y = pack_bf16(bf16_rest(g[2]), bf16_rest(g[3]));
-            o.z = pack_bf16(bf16_rest(g[4]), bf16_rest(g[5]));
-            o.w = pack_bf16(bf16_rest(g[6]), bf16_rest(g[7]));
-            *reinterpret_cast<uint4*>(G + a.lo + v) = o;
+        for (int u = 0; u < GRAD_UNROLL; ++u) {
+            const int v = base + (u * GRAD_THREADS + (int)threadIdx.x) * 8;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                f[u][h] = v + 4 * h < Vd ? __ldcs(reinterpret_cast<const float4*>(z + v) + h)
+                                         : make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        if (base == v0) {
+            if (threadIdx.x < 32) {
+                r = teacher_row(a.t, n, lane);
+                if (lane == 0) row_gs = r.some ? (a.gloss ? a.gloss[n] : 1.f) * a.t.inv_t : 0.f;
+            }
+            __syncthreads();
+            gs = row_gs;
+        }
+#pragma unroll
+        for (int u = 0; u < GRAD_UNROLL; ++u) {
+            const int v = base + (u * GRAD_THREADS + (int)threadIdx.x) * 8;
+            if (v >= Vd) continue;
+            // ids from Vd on get 0: tensor copies look at a row's end in steps of 16 bytes
+            auto q = [&](float x, int j) {
+                return gs == 0.f || v + j >= Vd ? 0.f : gs * ex2_approx((x - off) * LOG2E);
+            };
+            const float g[8] = {q(f[u][0].x, 0), q(f[u][0].y, 1), q(f[u][0].z, 2), q(f[u][0].w, 3),
+                                q(f[u][1].x, 4), q(f[u][1].y, 5), q(f[u][1].z, 6), q(f[u][1].w, 7)};
+            uint4 o;
+            o.x = pack_bf16(g[0], g[1]);
+            o.y = pack_bf16(g[2], g[3]);
+            o.z = pack_bf16(g[4], g[5]);
+            o.w = pack_bf16(g[6], g[7]);
+            *reinterpret_cast<uint4*>(G + v) = o;
+            if (a.lo) {
+                o.x = pack_bf16(bf16_rest(g[0]), bf16_rest(g[1]));
+                o.y = pack_bf16(bf16_rest(g[2]), bf16_rest(g[3]));
+                o.z = pack_bf16(bf16_rest(g[4]), bf16_rest(g[5]));
+                o.w = pack_bf16(bf16_rest(g[6]), bf16_rest(g[7]));
+                *reinterpret_cast<uint4*>(G + a.lo + v) = o;
+            }
         }
     }
     if (gs == 0.f) return;   // the same for the whole CTA
@@ -120,7 +126,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) logit_grad_kernel(const GradPara
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int id = r.id[h];
-            if (lane + 32 * h < a.t.K && !again[h] && id >= v0 && id < v0 + GRAD_COLS && id < Vd) {
+            if (lane + 32 * h < a.t.K && !again[h] && id >= v0 && id < v1) {
                 const float g = gs * (ex2_approx((z[id] - off) * LOG2E) - pt[h]);
                 G[id] = (uint16_t)pack_bf16(g, 0.f);
                 if (a.lo) G[a.lo + id] = (uint16_t)pack_bf16(bf16_rest(g), 0.f);
@@ -533,7 +539,12 @@ wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int d, cons
     a.G = G;
     a.ldg = (int64_t)distill_grad_ldg(Vd);
     a.lo = N <= TWO_PART_ROWS ? N * a.ldg : 0;
-    a.chunks = cdiv(Vd, GRAD_COLS);
+    // a row's teacher is worked out by each of its CTAs: as few as leave eight for an SM (a CTA for each GRAD_COLS ids
+    // takes as long with few rows, and with 64 listed 1,500 rows' gradients over 32,000 ids of 256 130 us in place of 115)
+    const int pieces = cdiv(Vd, GRAD_COLS);
+    const long most = (long)N * pieces / (8 * num_sms());
+    a.turns = most < 1 ? 1 : most < pieces ? (int)most : pieces;
+    a.chunks = cdiv(pieces, a.turns);
     static std::mutex mu;
     static bool attr_set[64] = {false};
     static int pairs[64];
