@@ -143,10 +143,9 @@ __global__ void __launch_bounds__(GRAD_THREADS) logit_grad_kernel(const GradPara
 // of dx, the pairs with fewer of them begin dWd sooner, and all end together.
 // With too few rows for that dx is cut along Vd as well; its fp32 parts are
 // added up in order by a kernel of their own.
-// Measured over 32,000 ids of 2,560: 4,096 rows 1.79 PFLOP/s (0.93 of a library
-// product's burst rate, at the power cap), 1,024 rows 203 us with the tensor
-// pipe active for 72 % of the cycles (256 x 256 tiles of a pair take about all
-// that shared memory delivers), 64 rows 66 us: Wd's bytes twice, dWd's once.
+// Measured over 32,000 ids of 2,560: 4,096 rows 653 us (2.05 PFLOP/s before the
+// power cap), 1,024 rows 184 us with the tensor pipe active for 87 % of the
+// cycles, 64 rows 59 us: Wd's bytes once, dWd's once (5.5 TB/s).
 // Up to 128 rows dx is computed as its transpose, Wd^T G^T: Wd's 256 columns are
 // the product's M and the rows its N, so that a K block costs what its rows need
 // and not 256 of them, and the tile is bound by Wd's bytes.

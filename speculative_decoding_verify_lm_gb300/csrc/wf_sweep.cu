@@ -20,8 +20,9 @@
 // One activation tile (up to 128 rows): bound by the weights' bytes; every CTA
 // its own tiles, ring slots as large as the rows (17 rows of 2,560 over 151,936
 // ids: 118 us, 6.6 TB/s).  More rows: pairs of CTAs on tiles of 256 rows x 256
-// ids, bound by the tensor cores (3,967 rows with 16 best: 1.74 PFLOP/s; with
-// d below about 1,000 by what the four epilogue warps do with a tile).
+// ids, bound by the tensor cores (1,248 rows with 10 best: 484 us, 2.0 PFLOP/s;
+// 3,967 rows with 16 at the power cap 1.9; with d below about 1,000 by what the
+// four epilogue warps do with a tile).
 #include <cudaTypedefs.h>
 
 #include <cfloat>
