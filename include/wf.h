@@ -430,7 +430,7 @@ WF_API wf_status wf_lmhead_logprobs(const wf_logprobs_args* args, void* ws, size
 typedef struct wf_distill_args {
     const uint16_t* x;         /* [N, d] bf16 bits, the drafter's hidden states */
     const uint16_t* Wd;        /* [Vd, d] bf16 bits */
-    int N, d, Vd;              /* 1 <= N, d % 8 == 0, 8 <= d <= 16384, 1 <= Vd < 2^31 - 256 */
+    int N, d, Vd;              /* 1 <= N, d % 8 == 0, 8 <= d <= 16384, 1 <= Vd < 2^30 */
     const int32_t* tid;        /* [N, k] ids of the teacher's alternatives, -1 = none: target ids if t2d is given */
     const float* tlogit;       /* [N, k] their logits or log-probabilities */
     int k;                     /* 1 .. WF_MAX_LISTED */

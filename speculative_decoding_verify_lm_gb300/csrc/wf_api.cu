@@ -141,6 +141,8 @@ static bool bad_gemm_shape(int rows, int d, int n) {
 static bool bad_head_shape(int rows, int d, int n) {
     return bad_gemm_shape(rows, d, n) || n >= 0x7fffffff - 256 || rows >= 0x7fffffff - 256;
 }
+// Distillation: the pass that makes G counts a row's ids in steps of thousands.
+static bool bad_distill_shape(int N, int d, int Vd) { return bad_head_shape(N, d, Vd) || Vd >= 1 << 30; }
 static bool bad_temperature(float t) {
     const float inv = 1.f / t;
     return !(t > 0.f) || !(inv > 0.f) || isinf(inv) || isinf(inv * 1.4427f);
@@ -179,7 +181,7 @@ static DistillLayout distill_layout(int N, int d, int Vd, int k) {
 }
 
 static wf_status check_distill(const wf_distill_args* a) {
-    if (!a || !a->x || !a->Wd || !a->tid || !a->tlogit || !a->lse || bad_head_shape(a->N, a->d, a->Vd) || a->k < 1 ||
+    if (!a || !a->x || !a->Wd || !a->tid || !a->tlogit || !a->lse || bad_distill_shape(a->N, a->d, a->Vd) || a->k < 1 ||
         a->k > WF_MAX_LISTED || (a->t2d ? a->V < 1 : a->V != 0) || bad_temperature(a->temperature) ||
         !aligned16(a->x) || !aligned16(a->Wd))
         return WF_ERR_INVALID_ARG;
@@ -700,7 +702,7 @@ wf_status wf_lmhead_logprobs(const wf_logprobs_args* a, void* ws, size_t ws_byte
 }
 
 size_t wf_distill_workspace_bytes(int N, int d, int Vd, int k) {
-    if (bad_head_shape(N, d, Vd) || k < 1 || k > WF_MAX_LISTED) return 0;
+    if (bad_distill_shape(N, d, Vd) || k < 1 || k > WF_MAX_LISTED) return 0;
     return distill_layout(N, d, Vd, k).total;
 }
 

@@ -58,7 +58,7 @@ __global__ void __launch_bounds__(GRAD_THREADS) logit_grad_kernel(const GradPara
     __shared__ float row_gs;
     pdl_trigger();   // the products may start
     const int n = blockIdx.x / a.chunks, v0 = (blockIdx.x % a.chunks) * a.turns * GRAD_COLS;
-    const int Vd = a.t.Vd, v1 = min(Vd, v0 + a.turns * GRAD_COLS), lane = threadIdx.x & 31;
+    const int Vd = a.t.Vd, v1 = v0 + min(Vd - v0, a.turns * GRAD_COLS), lane = threadIdx.x & 31;
     const float off = a.lse[n];
     const float* z = a.z + (size_t)n * a.ldz;
     uint16_t* G = a.G + (size_t)n * a.ldg;

@@ -93,6 +93,14 @@ def test_workspace_sizes():
             N + 1, 2560, 32000, 1, 10)
 
 
+def test_ids_that_an_int_does_not_count_in_steps():
+    """Draft vocabularies from 2^30 on: the pass over a row's logits would step past 2^31."""
+    for fn in ("wf_draft_distill", "wf_draft_distill_grad"):
+        assert distill(fn, Vd=2 ** 30, ldz=2 ** 30) == INVALID
+    size = wf.lib().wf_distill_workspace_bytes
+    assert size(1, 8, 2 ** 30, 1) == 0 and size(1, 8, 2 ** 30 - 1, 1) >= 2 ** 31
+
+
 def test_the_binding_refuses_before_the_library():
     x, W = torch.zeros(4, 64, dtype=torch.bfloat16), torch.zeros(10, 64, dtype=torch.bfloat16)
     with pytest.raises(ValueError, match="CUDA"):
