@@ -63,6 +63,15 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const Me
             loc[j] = id < 0 ? 0ull : pack_key((j & 1 ? f.z : f.x) + 0.f, (uint32_t)id);
         }
     }
+    // the teacher's chain of loads (ids, their draft ids, those logits) while the states are on their way
+    TeacherRow r{};
+    float zt[2] = {0.f, 0.f};
+    if (c.z && warp == 0) {
+        r = teacher_row(c.t, c.row0 + row, lane);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (r.p[h] != 0.f) zt[h] = c.z[(size_t)row * c.ldz + r.id[h]];
+    }
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         const float m2 = __shfl_xor_sync(0xffffffffu, M, off), s2 = __shfl_xor_sync(0xffffffffu, S, off),
@@ -140,12 +149,10 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const Me
         // sum p (log p - log q)
         float part = 0.f, stat;
         if (c.z) {
-            const TeacherRow r = teacher_row(c.t, c.row0 + row, lane);
             stat = r.plogp;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (r.p[h] != 0.f)
-                    part = fmaf(r.p[h], fmaf(fmaf(c.z[(size_t)row * c.ldz + r.id[h]], LOG2E, -ref), LN2, -logs), part);
+                if (r.p[h] != 0.f) part = fmaf(r.p[h], fmaf(fmaf(zt[h], LOG2E, -ref), LN2, -logs), part);
         } else {
             stat = c.stat[row];
             for (int j = lane; j < c.K; j += 32) {
