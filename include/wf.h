@@ -372,9 +372,11 @@ WF_API wf_status wf_lmhead_draft_topk(const uint16_t* hidden, const uint16_t* W,
  *   top_ids[p, j] = the k ids of largest <hidden[p], W_v>, best first, the lower
  *                   id on a tie;  top_logp[p, j] = their z - lse[p]
  * Logits are accumulated in fp32 on the tensor cores and never stored; a given
- * token's logit has the same bits as an alternative's.  Logits, also divided by
- * the temperature and times log2(e), have to lie in fp32's range; a row with a
- * NaN among them has NaN results, and a NaN is no alternative (top_ids -1).
+ * token's logit has the same bits as an alternative's.  Logits and their
+ * differences within a row, also divided by the temperature and times log2(e),
+ * have to lie in fp32's range; what the temperature makes of them costs no digits
+ * but lse's own (differences are taken first).  A row with a NaN among its logits
+ * has NaN results, and a NaN is no alternative (top_ids -1).
  * A tok of -1 is a place without a token: its logp is 0.  Any other id outside
  * [0, V) sets WF_ERR_BAD_DATA (info = p) and its logp is NaN.
  * Results do not depend on timing.
@@ -413,7 +415,8 @@ WF_API wf_status wf_lmhead_logprobs(const wf_logprobs_args* args, void* ws, size
  * alternative has loss 0 and no gradient.  An id outside [0, V) (or, without t2d,
  * [0, Vd)), or a t2d entry of Vd or more, sets WF_ERR_BAD_DATA (info = n): the
  * row's loss is NaN and it has no gradient.  fp32 softmax statistics and sums;
- * z has to lie in fp32's range, also times log2(e).
+ * z and its differences within a row have to lie in fp32's range, also times
+ * log2(e).
  *
  * wf_draft_distill writes loss and lse and, if z is given, the z[n, v] in fp32
  * (columns from Vd, rounded up to 4, on are left as they are): 4 N Vd bytes that

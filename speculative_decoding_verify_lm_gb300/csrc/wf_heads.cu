@@ -112,10 +112,10 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const Me
     S = wsum[0];
     T = wt[0];
     for (int w = 1; w < warps; ++w) state_merge(cc, M, S, T, wm[w], wsum[w], wt[w]);
-    const float logs = logf(S), ref = state_ref(M, cc);
-    auto logq = [&](float v) { return fmaf(fmaf(v, cc, -ref), LN2, -logs); };
+    const float logs = logf(S), lse = fmaf(M, c.inv_t, logs);
+    auto logq = [&](float v) { return fmaf(v - M, c.inv_t, -logs); };
     if (threadIdx.x == 0) {
-        if (c.lse) c.lse[row] = fmaf(ref, LN2, logs);
+        if (c.lse) c.lse[row] = lse;
         if (c.H) c.H[row] = logs - T * LN2 / S;
     }
     if constexpr (KT > 0) {
@@ -152,7 +152,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const Me
             stat = r.plogp;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (r.p[h] != 0.f) part = fmaf(r.p[h], fmaf(fmaf(zt[h], LOG2E, -ref), LN2, -logs), part);
+                if (r.p[h] != 0.f) part = fmaf(r.p[h], zt[h] - lse, part);
         } else {
             stat = c.stat[row];
             for (int j = lane; j < c.K; j += 32) {

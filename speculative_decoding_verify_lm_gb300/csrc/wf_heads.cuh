@@ -88,12 +88,11 @@ struct MergeCall {
 };
 wf_status launch_states_merge(const MergeCall& c, cudaStream_t s);
 
-// A state's reference in base 2: the same rounded product wherever a state is
-// summed up, merged or read, so that its rounding cancels.
-__device__ __forceinline__ float state_ref(float M, float c) { return __fmul_rn(M, c); }
-
 // (M, S, T) of two states of one row: M the largest logit, S = sum 2^z, T = sum
-// z 2^z, z = c v - state_ref(M, c).  A state with S = 0 is empty; NaN stays NaN.
+// z 2^z, z = c (v - M).  The difference comes first: the largest logit has z = 0
+// and S >= 1 whatever c M's size is (a rounded c M in place of it is off by more
+// than 2^z can take once c M passes 2^31, a small temperature's).  A state with
+// S = 0 is empty; NaN stays NaN.
 __device__ __forceinline__ void state_merge(float c, float& M, float& S, float& T, float m2, float s2, float t2) {
     if (s2 == 0.f) return;
     if (S == 0.f) {
@@ -102,8 +101,8 @@ __device__ __forceinline__ void state_merge(float c, float& M, float& S, float& 
         T = t2;
         return;
     }
-    const float mx = fmaxf(M, m2), ref = state_ref(mx, c);
-    const float d1 = state_ref(M, c) - ref, d2 = state_ref(m2, c) - ref;
+    const float mx = fmaxf(M, m2);
+    const float d1 = (M - mx) * c, d2 = (m2 - mx) * c;
     const float a1 = ex2_approx(d1), a2 = ex2_approx(d2);
     // a state far below the other: its weight is 0, and so is its part of T
     T = (a1 == 0.f && S == S ? 0.f : (T + d1 * S) * a1) + (a2 == 0.f && s2 == s2 ? 0.f : (t2 + d2 * s2) * a2);

@@ -235,6 +235,22 @@ __device__ __forceinline__ uint32_t reached_by(const uint32_t* at) {
     return least;
 }
 
+// Two numbers in one 64-bit register, and (a + add) * mul of two at a time, each
+// step rounded.  (A fused product with a rounded c M would be one step, and off by
+// c M 2^-24.  Where the fold bounds, 1,215 rows of 512 over 123,478 ids without
+// alternatives, that is 133 us and this 140; 1,248 rows of 2,560 take 526 either way.)
+__device__ __forceinline__ uint64_t pair_f32(float lo, float hi) {
+    uint64_t p;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(lo), "f"(hi));
+    return p;
+}
+__device__ __forceinline__ void sum_times(float (&z)[2], float a, float b, uint64_t add, uint64_t mul) {
+    asm("{\n\t.reg .b64 v;\n\tmov.b64 v, {%2, %3};\n\tadd.rn.f32x2 v, v, %4;\n\tmul.rn.f32x2 v, v, %5;\n\t"
+        "mov.b64 {%0, %1}, v;\n\t}"
+        : "=f"(z[0]), "=f"(z[1])
+        : "f"(a), "f"(b), "l"(add), "l"(mul));
+}
+
 // Fold 32 columns (the first lim of them) into a row's state; only columns above
 // `bound` are candidates for its list.  Returns their maximum.
 template <int KT, bool ENT, bool FULL>
@@ -247,23 +263,27 @@ __device__ __forceinline__ float fold(const uint32_t (&r)[32], int lim, int col0
     const float mx = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
     if (mx > st.M) {   // a new largest logit: rescale what was summed so far
         if (st.S != 0.f) {
-            const float dz = state_ref(st.M, c) - state_ref(mx, c);
+            const float dz = (st.M - mx) * c;
             const float sc = ex2_approx(dz);
             if constexpr (ENT) st.T = sc == 0.f && st.S == st.S ? 0.f : (st.T + dz * st.S) * sc;
             st.S *= sc;
         }
         st.M = mx;
     }
-    const float off = state_ref(st.M, c);
+    const uint64_t below = pair_f32(-st.M, -st.M), c2 = pair_f32(c, c);
     float s4[4] = {0.f, 0.f, 0.f, 0.f}, t4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < 32; ++j)
-        if (FULL || j < lim) {
-            const float z = fmaf(__uint_as_float(r[j]), c, -off);
-            const float e = ex2_approx(z);
-            s4[j & 3] += e;
-            if constexpr (ENT) t4[j & 3] = fmaf(z, e, t4[j & 3]);
-        }
+    for (int j = 0; j < 32; j += 2) {
+        float z[2];
+        sum_times(z, __uint_as_float(r[j]), __uint_as_float(r[j + 1]), below, c2);
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+            if (FULL || j + h < lim) {
+                const float e = ex2_approx(z[h]);
+                s4[(j + h) & 3] += e;
+                if constexpr (ENT) t4[(j + h) & 3] = fmaf(z[h], e, t4[(j + h) & 3]);
+            }
+    }
     st.S += (s4[0] + s4[1]) + (s4[2] + s4[3]);
     if constexpr (ENT) st.T += (t4[0] + t4[1]) + (t4[2] + t4[3]);
     if constexpr (KT > 0) {
