@@ -416,7 +416,9 @@ WF_API wf_status wf_lmhead_logprobs(const wf_logprobs_args* args, void* ws, size
  * [0, Vd)), or a t2d entry of Vd or more, sets WF_ERR_BAD_DATA (info = n): the
  * row's loss is NaN and it has no gradient.  fp32 softmax statistics and sums;
  * z and its differences within a row have to lie in fp32's range, also times
- * log2(e).
+ * log2(e).  Kept logits are rounded to fp32 one by one, and so is lse: beside the
+ * row's largest, the loss read off them is off by up to |z| 2^-23 a unit of p, and q
+ * in the gradients by a factor of up to e^(|z| 2^-22) (|z| 10^4: 0.2 %).
  *
  * wf_draft_distill writes loss and lse and, if z is given, the z[n, v] in fp32
  * (columns from Vd, rounded up to 4, on are left as they are): 4 N Vd bytes that

@@ -112,10 +112,12 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const Me
     S = wsum[0];
     T = wt[0];
     for (int w = 1; w < warps; ++w) state_merge(cc, M, S, T, wm[w], wsum[w], wt[w]);
-    const float logs = logf(S), lse = fmaf(M, c.inv_t, logs);
+    // The largest logit over the temperature is rounded as a kept one is, so that it cancels against it: in the loss
+    // below, and where log S is lost in lse also in the gradients, which have z and lse alone.
+    const float logs = logf(S), zmax = __fmul_rn(M, c.inv_t);
     auto logq = [&](float v) { return fmaf(v - M, c.inv_t, -logs); };
     if (threadIdx.x == 0) {
-        if (c.lse) c.lse[row] = lse;
+        if (c.lse) c.lse[row] = __fadd_rn(zmax, logs);
         if (c.H) c.H[row] = logs - T * LN2 / S;
     }
     if constexpr (KT > 0) {
@@ -152,7 +154,7 @@ __global__ void __launch_bounds__(MERGE_WARPS * 32) states_merge_kernel(const Me
             stat = r.plogp;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
-                if (r.p[h] != 0.f) part = fmaf(r.p[h], zt[h] - lse, part);
+                if (r.p[h] != 0.f) part = fmaf(r.p[h], (zt[h] - zmax) - logs, part);
         } else {
             stat = c.stat[row];
             for (int j = lane; j < c.K; j += 32) {

@@ -129,3 +129,45 @@ def test_loss(T, N):
     within(lse, r.lse, r.tol_lse, "lse")
     within(loss, want, tol, "loss")
     assert float(loss[5]) == 0
+
+
+@pytest.mark.parametrize("N", [41, 300])
+@pytest.mark.parametrize("T", TEMPERATURES)
+def test_kept_logits(T, N):
+    """The loss read off kept logits, and the gradients."""
+    T = f32(T)
+    x, W, g = inputs(N, N)
+    r = Row(x, W, T)
+    tid, tl = teacher(r, N, g)
+    want, tol, ids, p, some = loss_of(r, tid, tl, T)
+    # gradients of the size of one whatever the temperature
+    gloss = (torch.rand(N, device=DEV, generator=g) + 0.5) * min(T, 1e6)
+    ws, z = wf.DistillWorkspace(N, 64, V, 4), wf.distill_logits(N, V)
+    loss, lse = wf.wf_draft_distill(x, W, tid.int(), tl, ws, temperature=T, z=z)
+    dx, dW = wf.wf_draft_distill_grad(x, W, tid.int(), tl, z, lse, ws, gloss=gloss, temperature=T)
+    within(z[:, :V], r.raw / T, 2 * U * (r.raw / T).abs(), "z")
+    within(lse, r.lse, r.tol_lse, "lse")
+    # kept logits are rounded one by one; the largest's own rounding cancels
+    other = torch.gather(r.zz, 1, ids) < 0
+    big = (torch.gather(r.raw, 1, ids).abs() + r.top.abs()) / T
+    within(loss, want, tol + (p * torch.where(other, U * big, 0.0)).sum(1), "loss")
+    assert float(loss[5]) == 0
+
+    gs = torch.where(some, gloss.double() / T, 0.0)[:, None]
+    pt = torch.zeros_like(r.q).scatter_add_(1, ids, p)
+    G = gs * (r.q - pt)
+    # q = e^(z - lse): kept logits' roundings but the largest's; lse's own, half a step of it and no more than log S, by
+    # which it lies beside a number of fp32, the largest kept logit; their difference's
+    ez = torch.where(r.zz < 0, U * (r.raw.abs() + r.top.abs()) / T, 0.0) + torch.minimum(r.logs, U * r.lse[:, None].abs())
+    ez = ez + 3 * U * r.zz.abs() + r.el[:, None] + 4 * U * r.lq.abs() + 4 * U
+    eq = (r.lq + ez).clamp(max=30).exp() - r.q
+    eG = (BF if N > 128 else BF * BF) * G.abs() + gs * (eq + pt * 250 * U) * (1 + 4 * U)
+    # below 2^-126 there are no normal numbers: the exponential gives 0 there (a q of up to 2^-126, times gs), and a part
+    # of G that small, or the second part of a larger one, may count as 0 (2^-126 each)
+    eG = eG + (gs + 2) * 2.0 ** -126
+    Wd, X = W.double(), x.double()
+    gx, gW = G @ Wd, G.T @ X
+    tx = (1 + BF) * (eG @ Wd.abs() + 4 * V * U * (G.abs() @ Wd.abs())) + BF * gx.abs() + 1e-38
+    tW = (1 + BF) * (eG.T @ X.abs() + 4 * N * U * (G.abs().T @ X.abs())) + BF * gW.abs() + 1e-38
+    within(dx, gx, tx, "dx")
+    within(dW, gW, tW, "dWd")
