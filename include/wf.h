@@ -411,14 +411,18 @@ WF_API wf_status wf_lmhead_logprobs(const wf_logprobs_args* args, void* ws, size
  *   lse[n]  = log sum_v e^(z[n, v])
  * An alternative is kept if its id is not -1, has a draft id (t2d, where given)
  * and its logit is not -inf; what else the places of the others hold has no say.
- * Entries of one row that name the same id add up their p.  A row without a kept
- * alternative has loss 0 and no gradient.  An id outside [0, V) (or, without t2d,
- * [0, Vd)), or a t2d entry of Vd or more, sets WF_ERR_BAD_DATA (info = n): the
- * row's loss is NaN and it has no gradient.  fp32 softmax statistics and sums;
- * z and its differences within a row have to lie in fp32's range, also times
- * log2(e).  Kept logits are rounded to fp32 one by one, and so is lse: beside the
- * row's largest, the loss read off them is off by up to |z| 2^-23 a unit of p, and q
- * in the gradients by a factor of up to e^(|z| 2^-22) (|z| 10^4: 0.2 %).
+ * The loss takes a row's places apart.  Where several name one draft id (as a t2d
+ * that maps two target ids to it makes them) it is below KL(p || q) by what tells
+ * these places apart, a constant of the teacher: the gradient is the divergence's,
+ * in which their p add up.  A row without a kept alternative has loss 0 and no
+ * gradient.  An id outside [0, V) (or, without t2d, [0, Vd)), or a t2d entry of Vd
+ * or more, sets WF_ERR_BAD_DATA (info = n): the row's loss is NaN and it has no
+ * gradient.
+ * Softmax statistics and sums are fp32; z and its differences within a row have to
+ * lie in fp32's range, also times log2(e).  Kept logits are rounded to fp32 one by
+ * one, and so is lse: beside the row's largest, the loss read off them is off by up
+ * to |z| 2^-23 a unit of p, and q in the gradients by a factor of up to
+ * e^(|z| 2^-22) (|z| 10^4: 0.2 %).
  *
  * wf_draft_distill writes loss and lse and, if z is given, the z[n, v] in fp32
  * (columns from Vd, rounded up to 4, on are left as they are): 4 N Vd bytes that
