@@ -657,7 +657,7 @@ wf_status wf_lmhead_logprobs(const wf_logprobs_args* a, void* ws, size_t ws_byte
     const ScoreLayout L = score_layout(a->P, a->d, a->S, a->k);
     WF_TRY(check_ws(ws, ws_bytes, L.total));
     WF_TRY(check_device());
-    WF_TRY(check_local({a->hidden, a->W}));
+    WF_TRY(check_local({a->hidden, a->W, ws}));
     uint8_t* w = static_cast<uint8_t*>(ws);
     Control* ctrl = reinterpret_cast<Control*>(ws);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
@@ -712,7 +712,7 @@ wf_status wf_draft_distill(const wf_distill_args* a, void* ws, size_t ws_bytes, 
     const DistillLayout L = distill_layout(a->N, a->d, a->Vd, a->k);
     WF_TRY(check_ws(ws, ws_bytes, L.total));
     WF_TRY(check_device());
-    WF_TRY(check_local({a->x, a->Wd, a->z}));
+    WF_TRY(check_local({a->x, a->Wd, a->z, ws}));
     uint8_t* w = static_cast<uint8_t*>(ws);
     const cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const Teacher t = teacher_of(a, ws);

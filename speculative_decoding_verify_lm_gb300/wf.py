@@ -487,9 +487,11 @@ class Logprobs(NamedTuple):
     top_logp: Optional[torch.Tensor]
 
 
-def _own_ws(ws, kind):
+def _own_ws(ws, kind, dev):
     if type(ws) is not kind:
         raise ValueError(f"ws must be a {kind.__name__}")
+    if ws.buf.get_device() != dev:
+        raise ValueError(f"ws must be on cuda:{dev}")
     return ws.buf.data_ptr(), ws.nbytes
 
 
@@ -563,7 +565,7 @@ def wf_lmhead_logprobs(hidden, W, ws: LogprobsWorkspace, tok=None, k: int = 0, t
         else:
             tlp = _shaped(top_logp, "top_logp", (P, k), _F32, dev)
     args = _LOGPROBS.pack(hp, Wp, P, d, V, temperature, tp, S, k, lp, lsep, Hp, idp, tlp)
-    st = (_lib or lib()).wf_lmhead_logprobs(args, *_own_ws(ws, LogprobsWorkspace), _stream(stream))
+    st = (_lib or lib()).wf_lmhead_logprobs(args, *_own_ws(ws, LogprobsWorkspace, dev), _stream(stream))
     if st:
         _raise(st, "wf_lmhead_logprobs")
     return Logprobs(logp, lse, H, top_ids, top_logp)
@@ -609,7 +611,7 @@ def _distill(fn, x, Wd, tid, tlogit, t2d, temperature, z, lse, loss, gloss, dx, 
                          _shaped(gloss, "gloss", (N,), _F32, dev) if gloss is not None else 0,
                          _shaped(dx, "dx", x.shape, _BF16, dev) if dx is not None else 0,
                          _shaped(dWd, "dWd", Wd.shape, _BF16, dev) if dWd is not None else 0)
-    st = getattr(_lib or lib(), fn)(args, *_own_ws(ws, DistillWorkspace), _stream(stream))
+    st = getattr(_lib or lib(), fn)(args, *_own_ws(ws, DistillWorkspace, dev), _stream(stream))
     if st:
         _raise(st, fn)
 
