@@ -28,6 +28,7 @@
 #include <cfloat>
 
 #include "wf_heads.cuh"
+#include "wf_tiles.cuh"
 
 namespace wf {
 
@@ -519,41 +520,6 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
     pipe_end<PAIR>(g, tmem_base);
 }
 
-// Weight rows per tile: as many tiles as the CTAs (or pairs) take in the fewest
-// rounds, so that every CTA gets about the same rows in each.  Tiles have one of
-// two heights, `step` apart: 16, or 32 where logits leave in boxes of 32 columns.
-// (2,048 rows over 32,000 ids: 125 tiles of 256 are 13.2 rounds for 76 pairs; 133
-// of 240 or 256 are 14 full ones.  Tiles of one smaller height that fill the
-// rounds, 192 of them, took 236 us a call, since both operands cross to the SMs
-// once for each tile.)
-struct Tiles {
-    int num_n, bn, nbig, step;
-};
-constexpr int MIN_TILE = 64;
-Tiles tiles_of(int V, int slots, int num_mt, bool z) {
-    Tiles t{};
-    t.step = z ? 32 : 16;
-    const long rounds = cdiv((long)num_mt * cdiv(V, BN), slots);
-    long n = rounds * slots / num_mt;
-    if (n > V / MIN_TILE) n = V / MIN_TILE;
-    const int least = cdiv(V, BN);
-    if (n < least) n = least;
-    t.num_n = (int)n;
-    if (V < MIN_TILE) {
-        t.bn = MIN_TILE;
-        t.nbig = t.num_n;
-        return t;
-    }
-    const int h = (int)(V / n) / t.step * t.step;   // at least MIN_TILE
-    t.bn = h + t.step;
-    t.nbig = cdiv(V - n * h, t.step);
-    if (t.nbig == 0) {
-        t.bn = h;
-        t.nbig = t.num_n;
-    }
-    return t;
-}
-
 template <int KT, bool ENT, bool Z>
 wf_status launch_kt(const SweepCall& c, int* slots_out, cudaStream_t s) {
     static std::mutex mu;
@@ -589,7 +555,7 @@ wf_status launch_kt(const SweepCall& c, int* slots_out, cudaStream_t s) {
     } else {
         slots = num_sms() < STATE_SLOTS ? num_sms() : STATE_SLOTS;
     }
-    const Tiles t = tiles_of(c.V, slots, p.num_mt, Z);
+    const Tiles t = tiles_of(c.V, slots, p.num_mt, tile_step(pair, Z));
     const int b_bytes = (pair ? t.bn / 2 : t.bn) * BK * 2, extra = Z ? STAGING : 0;
     p.stage_bytes = p.a_bytes + b_bytes;
     // an MMA reads BM rows of A whatever the box holds: the last stage's may reach past a stage that is shorter
