@@ -157,6 +157,9 @@ constexpr int OUT_BOX = 4096;               // 32 rows x 128 bytes on their way 
 constexpr int PROD_WARPS = 8, PROD_THREADS = pipe_threads(PROD_WARPS);
 constexpr int PROD_STAGES = 6;
 constexpr int PROD_STAGE = 2 * BM * BK * 2;
+constexpr int PROD_SMEM = pipe_smem(PROD_STAGES, PROD_STAGE, PROD_WARPS * OUT_BOX);
+static_assert(PROD_SMEM + PIPE_STATIC_MAX <= PIPE_SMEM_MAX, "a CTA's shared memory");
+static_assert(pipe_alone(PROD_SMEM), "no SM holds CTAs of two pairs");
 constexpr int SPREAD_ROWS = 64;             // rows up to which every pair gets a part of dx
 constexpr int PLAN_PAIRS = 76;              // pairs that the split is chosen for (152 SMs)
 constexpr int MAX_SPLIT = 16;
@@ -547,14 +550,13 @@ wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int d, cons
     static std::mutex mu;
     static bool attr_set[64] = {false};
     static int pairs[64];
-    const int smem = pipe_smem(PROD_STAGES, PROD_STAGE, PROD_WARPS * OUT_BOX);
-    wf_status st = configure_once(mu, attr_set, [&] {
-        if (!set_smem(grad_products_kernel, smem) || !set_smem(logit_grad_kernel, 0) || !set_smem(dx_join_kernel, 0))
+    wf_status st = configure_once(mu, attr_set, [] {
+        if (!set_smem(grad_products_kernel, PROD_SMEM) || !set_smem(logit_grad_kernel, 0) || !set_smem(dx_join_kernel, 0))
             return false;
         int dev = 0;
         if (cudaGetDevice(&dev) != cudaSuccess) return false;
         if (dev < 64)
-            pairs[dev] = resident_pairs(reinterpret_cast<const void*>(grad_products_kernel), PROD_THREADS, smem);
+            pairs[dev] = resident_pairs(reinterpret_cast<const void*>(grad_products_kernel), PROD_THREADS, PROD_SMEM);
         return true;
     });
     if (st != WF_OK) return st;
@@ -603,7 +605,7 @@ wf_status launch_distill_grad(const uint16_t* x, const uint16_t* Wd, int d, cons
                       : make_tile_map(&tdx, dx, N, d, d, false, 64, 32)))
         return WF_ERR_CUDA;
     if (dWd && !make_tile_map(&tdw, dWd, Vd, d, d, false, 64, 32)) return WF_ERR_CUDA;
-    st = launch_cluster(grad_products_kernel, dim3(2 * slots), dim3(PROD_THREADS), smem, s, 2u, gk, gm, tw, tx, tdx,
+    st = launch_cluster(grad_products_kernel, dim3(2 * slots), dim3(PROD_THREADS), PROD_SMEM, s, 2u, gk, gm, tw, tx, tdx,
                         tdw, p);
     if (st != WF_OK || !dx || !parts) return st;
     const long units = (long)N * (d / 8);

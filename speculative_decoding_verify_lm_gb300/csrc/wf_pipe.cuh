@@ -12,9 +12,23 @@
 // PAIR: the two CTAs of a cluster compute one 256-row tile with paired MMAs;
 // each loads its own half of A's rows and of B's, the first CTA issues, and
 // both CTAs' barriers are committed to.
-// Every wait is bounded: one that runs out records WF_ERR_TIMEOUT, raises the
-// CTA's abort flag, waits (again bounded) for its own copies and MMAs in
+// Every mbarrier wait is bounded: one that runs out records WF_ERR_TIMEOUT, raises
+// the CTA's abort flag, waits (again bounded) for its own copies and MMAs in
 // flight, and the CTA frees TMEM and exits.
+// The other waits have no limit of their own; what each waits for does not wait
+// for it:
+//   TMEM (pipe_begin)   CTAs that hold some on this SM, of whatever kernel or
+//                       stream, give it back when their own work is done.  The
+//                       CTAs of a pair allocate one by one, so two pairs that had
+//                       one SM of the same two each would wait for one another:
+//                       a pair's CTA takes more than half of an SM's shared
+//                       memory (asserted beside each kernel, as the LM head's
+//                       pairs do), so no SM ever holds CTAs of two pairs.
+//   cluster barriers    both CTAs of a pair are started together, and every thread
+//                       reaches both barriers, also behind a wait that gave up
+//   pdl_wait            the kernel before, which waits for nothing (stream order,
+//                       below)
+//   bulk-store groups   copies out of this CTA's own shared memory
 #pragma once
 
 #include "wf_internal.cuh"
@@ -26,8 +40,10 @@ constexpr int pipe_threads(int w) { return 64 + 32 * w; }
 constexpr int PIPE_MAX_STAGES = 12;
 constexpr int PIPE_TMEM_COLS = 2 * BN;     // two fp32 accumulators of up to BN columns
 constexpr int PIPE_BARRIER_BYTES = 512;    // barriers, TMEM address and abort flag behind the ring
-constexpr int PIPE_SMEM_MAX = 227 * 1024;
+constexpr int PIPE_SMEM_MAX = 227 * 1024;  // a CTA's shared memory
 constexpr int PIPE_STATIC_MAX = 512;       // of it, for a kernel's static shared memory
+// Whether no SM (228 KB, 1 KB of it reserved for each CTA) holds two CTAs of this much dynamic shared memory.
+constexpr bool pipe_alone(int smem) { return 2 * (smem + 1024) > 228 * 1024; }
 // What a kernel records beside WF_ERR_TIMEOUT: which wait gave up.
 constexpr uint32_t PIPE_WHERE_COPY = 0x400, PIPE_WHERE_ACC = 0x500, PIPE_WHERE_STAGE = 0x510, PIPE_WHERE_TILE = 0x600;
 
@@ -68,7 +84,7 @@ __device__ __forceinline__ Pipe pipe_at(uint8_t* smem_raw, int stages, int stage
     return g;
 }
 __device__ __forceinline__ uint8_t* pipe_extra(const Pipe& g) { return g.base + (size_t)g.stages * g.stage_bytes; }
-inline int pipe_smem(int stages, int stage_bytes, int extra) {
+constexpr int pipe_smem(int stages, int stage_bytes, int extra) {
     return stages * stage_bytes + PIPE_BARRIER_BYTES + extra + 1024;
 }
 
@@ -348,11 +364,17 @@ bool make_tile_map(CUtensorMap* map, const void* base, uint64_t rows, uint64_t c
                    uint32_t box_cols, uint32_t box_rows);
 // Stream order of these kernels.  A sweep or a product takes every SM nearly whole
 // (all tensor memory, up to 226 KB of shared memory, CTA pairs that need both SMs of
-// a pair free at once), so nothing may sit waiting beside one that is not yet
-// running everywhere: what follows it, and what begins a call, is launched in
+// a pair free at once), so what follows one, and what begins a call, is launched in
 // plain stream order.  Only the kernel straight before it in the same call (the
-// lists, the pass that makes G) lets it start early; their CTAs are small enough
-// to fit beside it in any order.
+// lists, the pass that makes G) lets it start early.  That one was itself launched
+// in plain order, so it is all that is unfinished on the stream; it waits for
+// nothing; and it lets go in its first instruction, which takes effect when every
+// one of its blocks has started, so that blocks which wait beside them keep none of
+// it from running.
+// (Where every kernel let the next one start early, long queues of steps stopped
+// about once in 10,000 passes, with no bounded wait giving up.  Why is not
+// established; in this order more than three million passes ran clean, in the same
+// time.)
 template <typename... KArgs, typename... Args>
 inline wf_status launch_plain(void (*kernel)(KArgs...), dim3 grid, dim3 block, size_t smem, cudaStream_t s,
                               unsigned cluster, Args&&... args) {
@@ -371,9 +393,8 @@ inline wf_status launch_plain(void (*kernel)(KArgs...), dim3 grid, dim3 block, s
     return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...) == cudaSuccess ? WF_OK : WF_ERR_CUDA;
 }
 
-// Dynamic shared memory that a kernel may ask for, and an SM set up for as much shared memory as there is: what runs
-// before and after a sweep then fits beside it (its prologue is over when the sweep ends) and no SM is set up anew in
-// between.  Where a merge did not fit, a call took 3 to 15 us longer.
+// Dynamic shared memory that a kernel may ask for, and SMs set up for as much shared memory as there is by every kernel
+// of these calls, so that none is set up anew between them (where one was, a call took 3 to 15 us longer).
 template <typename K>
 inline bool set_smem(K kernel, int bytes) {
     return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess &&

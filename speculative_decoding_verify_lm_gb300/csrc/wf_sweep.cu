@@ -35,8 +35,13 @@ namespace wf {
 namespace {
 
 constexpr int SWEEP_THREADS = pipe_threads(4);
-constexpr int SWEEP_SMEM = 220 * 1024;   // leaves room on the SM for the merge's and the lists' CTAs
+constexpr int SWEEP_SMEM = 220 * 1024;   // leaves room on the SM for CTAs of the lists
 constexpr int STAGING = 4 * 2 * 4096;     // kept logits: two boxes of 32 rows x 128 bytes a warp
+static_assert(SWEEP_SMEM + PIPE_STATIC_MAX <= PIPE_SMEM_MAX, "a CTA's shared memory");
+// a pair's ring fills SWEEP_SMEM but for less than a stage, the largest of them 128 rows of A and half a tile of B
+constexpr int PAIR_STAGE_MAX = (BM + MAX_TILE / 2) * BK * 2;
+static_assert((SWEEP_SMEM - STAGING) / ((BM + MIN_TILE / 2) * BK * 2) <= PIPE_MAX_STAGES, "... whatever the tile");
+static_assert(pipe_alone(SWEEP_SMEM - PAIR_STAGE_MAX), "no SM holds CTAs of two pairs");
 
 struct SweepParams {
     int rows, V;
@@ -319,6 +324,7 @@ __global__ void __launch_bounds__(SWEEP_THREADS, 1)
                  const SweepParams p) {
     extern __shared__ uint8_t smem_raw[];
     __shared__ uint32_t seen[4][SWEEP_MAX_ROWS / BM / 32];   // row tiles that a warp has a state of
+    static_assert(sizeof(seen) <= PIPE_STATIC_MAX, "static shared memory");
     const Pipe g = pipe_at(smem_raw, p.stages, p.stage_bytes, p.a_bytes, Z ? STAGING : 0, p.ctrl, p.timeout_ns);
     const int warp = warp_number(), lane = threadIdx.x & 31;
     const int rank = PAIR ? (int)(cluster_ctarank() & 1u) : 0;
