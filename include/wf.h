@@ -433,8 +433,9 @@ WF_API wf_status wf_lmhead_logprobs(const wf_logprobs_args* args, void* ws, size
  *   dx[n]   = sum_v G[n, v] Wd_v,   dWd_v = sum_n G[n, v] x[n]
  * either output may be NULL, not both; they overlap no input.  G is rounded to
  * bf16 (up to 128 rows: to the sum of two bf16 numbers), the sums are fp32 and
- * rounded to bf16 at the end.  A row with gloss 0 adds nothing as long as its x
- * is finite.  Results do not depend on timing.
+ * rounded to bf16 at the end.  A row with gloss 0, or without a gradient (no kept
+ * alternative, an id out of range), adds nothing as long as its x is finite.
+ * Results do not depend on timing.
  */
 typedef struct wf_distill_args {
     const uint16_t* x;         /* [N, d] bf16 bits, the drafter's hidden states */

@@ -161,7 +161,8 @@ constexpr int PROD_SMEM = pipe_smem(PROD_STAGES, PROD_STAGE, PROD_WARPS * OUT_BO
 static_assert(PROD_SMEM + PIPE_STATIC_MAX <= PIPE_SMEM_MAX, "a CTA's shared memory");
 static_assert(pipe_alone(PROD_SMEM), "no SM holds CTAs of two pairs");
 constexpr int SPREAD_ROWS = 64;             // rows up to which every pair gets a part of dx
-constexpr int PLAN_PAIRS = 76;              // pairs that the split is chosen for (152 SMs)
+// Pairs that the split is chosen for (152 SMs), also where fewer are resident: the order of dx's sums is the sizes' alone.
+constexpr int PLAN_PAIRS = 76;
 constexpr int MAX_SPLIT = 16;
 constexpr int MAX_PARTS = 8 * PLAN_PAIRS;   // parts of all of dx's tiles: what a workspace holds
 
@@ -483,8 +484,10 @@ Plan plan_of(int N, int d, int Vd, bool dx, bool dw) {
     p.parts = N <= TWO_PART_ROWS ? 2 : 1;
     if (dx && p.x_m * p.x_n <= PLAN_PAIRS && N <= SPREAD_ROWS) {
         // few rows: both products are bound by the weights' bytes, and dx's half of them comes soonest with a part
-        // for every pair (16 rows over 32,000 ids: 7 parts of each of 10 tiles 68.8 us, 4 of each 74.0; 30 rows over
-        // 47,330: 142.9 and 154.8; with 128 rows 89.1 and 84.1, so there the costs below decide)
+        // for every pair, where the costs below would take fewer (us, a part for every pair / by the costs):
+        //   d 4,096 over 32,000 ids   16 rows 95.0 / 101.6,  64 rows 101.9 / 106.6,  80 rows 111.9 / 110.4
+        //   d 2,560 over 32,000 ids   16 rows 66.7 / 67.3,   64 rows 72.8 / 71.8,    80 rows 80.3 / 75.3
+        //   d 1,024 over 10,007 ids   16 rows 20.8 / 19.2,   64 rows 21.9 / 19.8 (16 parts of few K blocks)
         p.split = PLAN_PAIRS / p.x_n;
         if (p.split > MAX_SPLIT) p.split = MAX_SPLIT;
         if (p.split > p.kb_x) p.split = p.kb_x;

@@ -15,14 +15,15 @@
 // With several row tiles the pairs that see the same rows tell each other their
 // tiles' maxima, which bound the row's KT-th best from below, so that late columns
 // are candidates for few lists (1,215 rows of 512 over 123,478 ids with 10 best: 270
-// us a call without, 199 so): what is a candidate differs with timing, the k best
+// us a call without, 188 so): what is a candidate differs with timing, the k best
 // among them do not.
 // One activation tile (up to 128 rows): bound by the weights' bytes; every CTA
 // its own tiles, ring slots as large as the rows (17 rows of 2,560 over 151,936
 // ids: 118 us, 6.6 TB/s).  More rows: pairs of CTAs on tiles of 256 rows x 256
-// ids, bound by the tensor cores (1,248 rows with 10 best: 484 us, 2.0 PFLOP/s;
-// 3,967 rows with 16 at the power cap 1.9; with d below about 1,000 by what the
-// four epilogue warps do with a tile).
+// ids, bound by the tensor cores (1,248 rows with 10 best: 482 to 494 us, 2.0
+// PFLOP/s, and 550 to 560 in a long run at the power cap; 3,967 rows with 16: 1.48
+// ms rested, 1.6 to 1.7 at the cap; with d below about 1,000 by what the four
+// epilogue warps do with a tile).
 #include <cudaTypedefs.h>
 
 #include <cfloat>
